@@ -74,6 +74,7 @@ typedef enum { MLA_DT_F32 = 0, MLA_DT_BF16 = 1 } mla_dtype;
 #define MLA_DEV_SEQ_TOO_LONG 0x2 /* seq_lens[b] > max_blocks * 64 or > max_seq_len */
 #define MLA_DEV_WAIT_TIMEOUT 0x4 /* a bounded pipeline wait expired; outputs are invalid */
 #define MLA_DEV_BAD_SLOT 0x8     /* mla_cache_write: a slot at or beyond num_blocks * 64 (skipped) */
+#define MLA_DEV_BAD_PAGE 0x10    /* mla_decode_sparse: a selected page out of order or out of range (skipped) */
 
 /* Human-readable name of a status. Never NULL. */
 const char* mla_status_string(mla_status s);
@@ -331,6 +332,106 @@ mla_status mla_decode_noalloc(const void* q, const void* kv_cache, mla_kv_dtype 
                               int max_seq_len, int B, int Sq, int H, float scale, int num_splits,
                               void* o_latent, mla_dtype o_dtype, float* lse, int32_t* dev_status,
                               mla_stream_t stream);
+
+/*
+ * Decode of a batch whose requests share their first prefix_len cached tokens (a common system
+ * prompt or document): the same result as mla_decode, with the prefix pages read once for the
+ * whole batch. The first prefix_len / 64 entries of every block_table row name the same pages;
+ * only row 0's are used for the prefix, so the others may hold anything there. All prefix_len
+ * tokens must have been written. A request with seq_lens[b] < prefix_len (an empty slot of a padded
+ * batch, say) attends to its seq_lens[b] first prefix tokens only, 0 giving o = 0, lse = -inf.
+ *   prefix_len   a multiple of 64, 0 <= prefix_len <= max_blocks * 64; seq_lens counts it
+ *   num_splits   as mla_decode, for the part of each request behind the prefix; how the prefix
+ *                itself is divided over the device is the library's choice
+ *   workspace    >= mla_decode_shared_prefix_workspace_bytes for the same arguments, 256-byte
+ *                aligned, contents undefined before and after
+ * All other arguments, limits and errors as mla_decode. Row 0 of block_table is read whatever
+ * seq_lens[0] is.
+ */
+size_t mla_decode_shared_prefix_workspace_bytes(mla_kv_dtype kv_dtype, int B, int Sq, int H, int prefix_len,
+                                                int num_splits, int max_seq_len);
+mla_status mla_decode_shared_prefix(const void* q, const void* kv_cache, mla_kv_dtype kv_dtype, int64_t num_blocks,
+                                    const int32_t* block_table, int max_blocks, const int32_t* seq_lens,
+                                    int max_seq_len, int prefix_len, int B, int Sq, int H, float scale,
+                                    int num_splits, void* workspace, size_t workspace_bytes, void* o_latent,
+                                    mla_dtype o_dtype, float* lse, int32_t* dev_status, mla_stream_t stream);
+
+/*
+ * Decode over selected pages, in four calls: mla_page_keys keeps one mean key per cache page,
+ * mla_page_scores scores every page of a request for its query rows, mla_select_pages picks each
+ * row's pages, and mla_decode_sparse attends to them. All heads of a row share its pages, since
+ * they all read the same latent rows.
+ *
+ * mla_page_keys: for every page of request b that holds any of the tokens start_lens[b] ..
+ * seq_lens[b] - 1,
+ *     page_keys[block, d] = mean of K[block, i, d] over the page's valid tokens i     (576 values)
+ * where block = block_table[b, page] and a page's valid tokens are those below seq_lens[b]. Call it
+ * after the tokens were written (mla_cache_write), with the lengths before and after; keys of other
+ * pages are left as they are. K as in mla_decode (e4m3 * k_scale for the FP8 format); fp32 sums,
+ * rounded once to bf16. A page of two requests must be equally full in both.
+ *   kv_cache     [num_blocks, 64, mla_kv_row_bytes(kv_dtype)] bytes (16-byte aligned)
+ *   block_table  int32 [B, max_blocks]
+ *   start_lens   int32 [B] in device memory, or NULL: 0 for every request (all pages)
+ *   seq_lens     int32 [B] in device memory; a request with seq_lens[b] <= start_lens[b] is skipped
+ *   max_new_len  host upper bound of seq_lens[b] - start_lens[b] (exceeding it sets
+ *                MLA_DEV_SEQ_TOO_LONG and leaves pages out), <= max_blocks * 64
+ *   page_keys    bf16 [num_blocks, 576], 16-byte aligned
+ * A bad block id sets MLA_DEV_BAD_BLOCK_ID and its page is skipped.
+ */
+mla_status mla_page_keys(const void* kv_cache, mla_kv_dtype kv_dtype, int64_t num_blocks, const int32_t* block_table,
+                         int max_blocks, const int32_t* start_lens, const int32_t* seq_lens, int max_new_len, int B,
+                         void* page_keys, int32_t* dev_status, mla_stream_t stream);
+
+/*
+ * mla_page_scores: for query row t of request b, which sees n = max(0, seq_lens[b] - (Sq - 1 - t))
+ * tokens, and each of its ceil(n / 64) pages j,
+ *     scores[b, t, j] = max_h scale * < q[b, t, h, 0:576], page_keys[block_table[b, j]] >
+ * (fp32 sums of exact products; NaN if any head's is). The row's other entries, up to
+ * ceil(max_seq_len / 64), are set to -inf, and so is a page with a bad block id
+ * (MLA_DEV_BAD_BLOCK_ID).
+ *   q            bf16 [B, Sq, H, 576] contiguous, the absorbed query of mla_decode (16-byte aligned)
+ *   page_keys    bf16 [num_blocks, 576] (16-byte aligned)
+ *   max_seq_len  host upper bound of seq_lens (exceeding it sets MLA_DEV_SEQ_TOO_LONG; the row is
+ *                scored as if it had max_seq_len tokens), <= max_blocks * 64
+ *   scores       fp32 [B, Sq, ceil(max_seq_len / 64)]
+ * 1 <= H <= 128, scale > 0.
+ */
+mla_status mla_page_scores(const void* q, const void* page_keys, int64_t num_blocks, const int32_t* block_table,
+                           int max_blocks, const int32_t* seq_lens, int max_seq_len, int B, int Sq, int H, float scale,
+                           float* scores, int32_t* dev_status, mla_stream_t stream);
+
+/*
+ * mla_select_pages: the pages of each query row. A row with np = ceil(n / 64) pages (n as above)
+ * gets all of them if np <= max_sel; else its first sink_pages, its last local_pages, and of the
+ * others the max_sel - sink_pages - local_pages with the highest scores (of equal scores the lower
+ * page; -0 equals 0; NaN is below everything). Scores of the first and last pages are not read.
+ *   scores        fp32, row r = b * Sq + t at scores + r * scores_stride, num_pages entries
+ *                 (num_pages <= 49152; a longer seq_lens[b] sets MLA_DEV_SEQ_TOO_LONG and is cut)
+ *   max_sel       >= 1; sink_pages + local_pages <= max_sel
+ *   pages         int32 [B, Sq, max_sel]: ascending page numbers, -1 behind the last
+ */
+mla_status mla_select_pages(const float* scores, int64_t scores_stride, int num_pages, const int32_t* seq_lens, int B,
+                            int Sq, int max_sel, int sink_pages, int local_pages, int32_t* pages, int32_t* dev_status,
+                            mla_stream_t stream);
+
+/*
+ * mla_decode_sparse: mla_decode with each query row's attention limited to its selected pages:
+ * row (b, t) attends to the tokens j < n (n as above) with j / 64 in pages[b, t, :].
+ *   pages        int32 [B, Sq, max_sel]: ascending page numbers; -1 is skipped, so shorter lists
+ *                are padded with it. An entry that is not above every entry before it, or not one
+ *                of the row's ceil(n / 64) pages, sets MLA_DEV_BAD_PAGE and is skipped.
+ *   max_sel      1 <= max_sel <= (2^31 - 1) / 64; a row without pages gets o = 0, lse = -inf
+ *   num_splits   as mla_decode, over each row's selected tokens
+ *   workspace    >= mla_decode_sparse_workspace_bytes(...) bytes for the same arguments, 256-byte
+ *                aligned (the rows' page tables and split-KV partials), contents undefined
+ * All other arguments, results and errors as mla_decode.
+ */
+size_t mla_decode_sparse_workspace_bytes(mla_kv_dtype kv_dtype, int B, int Sq, int H, int max_sel, int num_splits);
+mla_status mla_decode_sparse(const void* q, const void* kv_cache, mla_kv_dtype kv_dtype, int64_t num_blocks,
+                             const int32_t* block_table, int max_blocks, const int32_t* seq_lens, const int32_t* pages,
+                             int max_sel, int B, int Sq, int H, float scale, int num_splits, void* workspace,
+                             size_t workspace_bytes, void* o_latent, mla_dtype o_dtype, float* lse,
+                             int32_t* dev_status, mla_stream_t stream);
 
 #ifdef __cplusplus
 }

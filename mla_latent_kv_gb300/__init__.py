@@ -19,7 +19,7 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "mla_latent_kv.h")
 KV_BF16, KV_FP8 = 0, 1
 DT_F32, DT_BF16 = 0, 1
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE_TOO_SMALL, ERR_CUDA = range(5)
-DEV_BAD_BLOCK_ID, DEV_SEQ_TOO_LONG, DEV_WAIT_TIMEOUT = 0x1, 0x2, 0x4
+DEV_BAD_BLOCK_ID, DEV_SEQ_TOO_LONG, DEV_WAIT_TIMEOUT, DEV_BAD_SLOT, DEV_BAD_PAGE = 0x1, 0x2, 0x4, 0x8, 0x10
 L, R, D, P, V, PAGE, MAX_HEADS = 512, 64, 576, 128, 128, 64, 128
 
 _lock = threading.Lock()
@@ -86,6 +86,22 @@ def lib() -> ctypes.CDLL:
         l.mla_prefill_chunk_plan.argtypes = [vp, i32, i64, vp, i64]
         l.mla_prefill.argtypes = [vp, vp, i64, vp, i64, vp, i32, i64, vp, i32, vp, vp, vp, vp, i32, i32, vp, vp,
                                   f32, i64, vp, sz, vp, vp, vp, vp]
+        l.mla_decode_shared_prefix_workspace_bytes.restype = sz
+        l.mla_decode_shared_prefix_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+        l.mla_decode_shared_prefix.restype = i32
+        l.mla_decode_shared_prefix.argtypes = [vp, vp, i32, i64, vp, i32, vp, i32, i32, i32, i32, i32, f32, i32, vp,
+                                               sz, vp, i32, vp, vp, vp]
+        l.mla_page_keys.restype = i32
+        l.mla_page_keys.argtypes = [vp, i32, i64, vp, i32, vp, vp, i32, i32, vp, vp, vp]
+        l.mla_page_scores.restype = i32
+        l.mla_page_scores.argtypes = [vp, vp, i64, vp, i32, vp, i32, i32, i32, i32, f32, vp, vp, vp]
+        l.mla_select_pages.restype = i32
+        l.mla_select_pages.argtypes = [vp, i64, i32, vp, i32, i32, i32, i32, i32, vp, vp, vp]
+        l.mla_decode_sparse_workspace_bytes.restype = sz
+        l.mla_decode_sparse_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
+        l.mla_decode_sparse.restype = i32
+        l.mla_decode_sparse.argtypes = [vp, vp, i32, i64, vp, i32, vp, vp, i32, i32, i32, i32, f32, i32, vp, sz, vp,
+                                        i32, vp, vp, vp]
         _lib = l
         return l
 
@@ -344,3 +360,163 @@ def prefill(q, kv_c, k_pe, kv_cache, block_table, ctx_lens, query_start_loc, w_u
                              _p(w_uk_t), _p(w_uv), float(scale), int(chunk_rows), _p(workspace), ws_bytes, _p(o),
                              _p(lse), _p(dev_status), _stream(stream)))
     return o, lse
+
+
+# ------------------------------------------------------------------ shared prefix, selected pages
+def _tensor(name, t, dtype, shape):
+    """`t` as an argument the kernels read through its pointer: contiguous, of the dtype and shape
+    (None = any size)."""
+    if t.dtype != dtype or t.dim() != len(shape) or not t.is_contiguous() or \
+            any(want is not None and want != got for want, got in zip(shape, t.shape)):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape "
+                         f"{tuple('*' if d is None else d for d in shape)}, got {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+def _here(t):
+    """`t`'s device, which must be the current one: the calls launch on the current device's stream."""
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current CUDA device, got {t.device}")
+    return t.device
+
+
+def _cache_blocks(kv_cache, kv_dtype, num_blocks):
+    """Blocks of the cache, checked against its size when given."""
+    rb = row_bytes(kv_dtype)
+    if rb < 0:
+        raise MlaError(ERR_INVALID_ARG, f"unknown kv_dtype {kv_dtype}")
+    have = kv_cache.numel() * kv_cache.element_size() // (PAGE * rb)
+    if not kv_cache.is_contiguous() or (num_blocks is not None and num_blocks > have):
+        raise ValueError(f"kv_cache must be contiguous and hold num_blocks={num_blocks} pages (it holds {have})")
+    return have if num_blocks is None else int(num_blocks)
+
+
+def _work_buf(workspace, need, device):
+    """A workspace of at least `need` bytes and its size."""
+    import torch
+    if workspace is None:
+        return (torch.empty(need, dtype=torch.uint8, device=device), need) if need else (None, 0)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def decode_shared_prefix_workspace_bytes(B: int, Sq: int, H: int, prefix_len: int, max_seq_len: int,
+                                         kv_dtype: int = KV_BF16, num_splits: int = -1) -> int:
+    return int(lib().mla_decode_shared_prefix_workspace_bytes(kv_dtype, B, Sq, H, int(prefix_len), num_splits,
+                                                              int(max_seq_len)))
+
+
+def decode_shared_prefix(q, kv_cache, block_table, seq_lens, max_seq_len, prefix_len, scale, kv_dtype=KV_BF16,
+                         num_splits=-1, workspace=None, o_latent=None, o_dtype=None, lse=None, dev_status=None,
+                         stream=None, num_blocks=None):
+    """decode() of a batch whose requests share their first prefix_len tokens (a multiple of 64): the
+    first prefix_len / 64 entries of block_table's rows name the same pages, read once for all
+    -> (o_latent [B,Sq,H,512], lse [B,Sq,H])."""
+    import torch
+    B, Sq, H = q.shape[0], q.shape[1], q.shape[2]
+    _tensor("q", q, torch.bfloat16, (B, Sq, H, D))
+    _tensor("block_table", block_table, torch.int32, (B, None))
+    _tensor("seq_lens", seq_lens, torch.int32, (B,))
+    nb = _cache_blocks(kv_cache, kv_dtype, num_blocks)
+    _here(q)
+    need = decode_shared_prefix_workspace_bytes(B, Sq, H, prefix_len, max_seq_len, kv_dtype, num_splits)
+    workspace, ws_bytes = _work_buf(workspace, need, q.device)
+    o_dtype = _dt_code(o_latent, o_dtype)
+    o_latent = _out_buf(o_latent, (B, Sq, H, L), o_dtype, q.device)
+    lse = _out_buf(lse, (B, Sq, H), DT_F32, q.device)
+    _check(lib().mla_decode_shared_prefix(_p(q), _p(kv_cache), kv_dtype, nb, _p(block_table), block_table.shape[1],
+                                          _p(seq_lens), int(max_seq_len), int(prefix_len), B, Sq, H, float(scale),
+                                          int(num_splits), _p(workspace), ws_bytes, _p(o_latent), o_dtype, _p(lse),
+                                          _p(dev_status), _stream(stream)))
+    return o_latent, lse
+
+
+def page_keys(kv_cache, block_table, seq_lens, max_new_len, kv_dtype=KV_BF16, start_lens=None, page_keys=None,
+              dev_status=None, stream=None, num_blocks=None):
+    """Mean key of every page that holds any of each request's tokens start_lens[b] .. seq_lens[b] - 1
+    (start_lens None: all of them) -> page_keys bf16 [num_blocks, 576], written in place when given
+    (other pages' keys stay)."""
+    import torch
+    B = block_table.shape[0]
+    _tensor("block_table", block_table, torch.int32, (B, None))
+    _tensor("seq_lens", seq_lens, torch.int32, (B,))
+    if start_lens is not None:
+        _tensor("start_lens", start_lens, torch.int32, (B,))
+    nb = _cache_blocks(kv_cache, kv_dtype, num_blocks)
+    _here(kv_cache)
+    if page_keys is None:
+        page_keys = torch.zeros((nb, D), dtype=torch.bfloat16, device=kv_cache.device)
+    _tensor("page_keys", page_keys, torch.bfloat16, (nb, D))
+    _check(lib().mla_page_keys(_p(kv_cache), kv_dtype, nb, _p(block_table), block_table.shape[1], _p(start_lens),
+                               _p(seq_lens), int(max_new_len), B, _p(page_keys), _p(dev_status), _stream(stream)))
+    return page_keys
+
+
+def page_scores(q, page_keys, block_table, seq_lens, max_seq_len, scale, scores=None, dev_status=None, stream=None):
+    """Score of every page for every query row, max over heads of scale * <q, page key>
+    -> fp32 [B, Sq, ceil(max_seq_len / 64)], -inf past a row's pages."""
+    import torch
+    B, Sq, H = q.shape[0], q.shape[1], q.shape[2]
+    _tensor("q", q, torch.bfloat16, (B, Sq, H, D))
+    _tensor("page_keys", page_keys, torch.bfloat16, (None, D))
+    _tensor("block_table", block_table, torch.int32, (B, None))
+    _tensor("seq_lens", seq_lens, torch.int32, (B,))
+    _here(q)
+    width = -(-int(max_seq_len) // PAGE)
+    if scores is None:
+        scores = torch.empty((B, Sq, width), dtype=torch.float32, device=q.device)
+    _tensor("scores", scores, torch.float32, (B, Sq, width))
+    _check(lib().mla_page_scores(_p(q), _p(page_keys), page_keys.shape[0], _p(block_table), block_table.shape[1],
+                                 _p(seq_lens), int(max_seq_len), B, Sq, H, float(scale), _p(scores), _p(dev_status),
+                                 _stream(stream)))
+    return scores
+
+
+def select_pages(scores, seq_lens, max_sel, sink_pages=1, local_pages=1, pages=None, dev_status=None, stream=None):
+    """The pages of each query row from scores [B, Sq, num_pages] (rows may be strided): the first
+    sink_pages, the last local_pages, and the best others -> int32 [B, Sq, max_sel], ascending, -1
+    behind the last."""
+    import torch
+    B, Sq, width = scores.shape
+    if scores.dtype != torch.float32 or (width > 1 and scores.stride(2) != 1) or \
+            (B > 1 and Sq > 1 and scores.stride(0) != Sq * scores.stride(1)):
+        raise ValueError("scores must be fp32 [B, Sq, num_pages] with unit inner stride and evenly spaced rows")
+    # dimensions of one element have strides of no meaning
+    stride = scores.stride(1) if Sq > 1 else (scores.stride(0) if B > 1 else width)
+    _tensor("seq_lens", seq_lens, torch.int32, (B,))
+    _here(scores)
+    if pages is None:
+        pages = torch.empty((B, Sq, max_sel), dtype=torch.int32, device=scores.device)
+    _tensor("pages", pages, torch.int32, (B, Sq, max_sel))
+    _check(lib().mla_select_pages(_p(scores), int(stride), width, _p(seq_lens), B, Sq, int(max_sel), int(sink_pages),
+                                  int(local_pages), _p(pages), _p(dev_status), _stream(stream)))
+    return pages
+
+
+def decode_sparse_workspace_bytes(B: int, Sq: int, H: int, max_sel: int, kv_dtype: int = KV_BF16,
+                                  num_splits: int = -1) -> int:
+    return int(lib().mla_decode_sparse_workspace_bytes(kv_dtype, B, Sq, H, int(max_sel), num_splits))
+
+
+def decode_sparse(q, kv_cache, block_table, seq_lens, pages, scale, kv_dtype=KV_BF16, num_splits=-1, workspace=None,
+                  o_latent=None, o_dtype=None, lse=None, dev_status=None, stream=None, num_blocks=None):
+    """decode() with each query row's attention limited to its selected pages [B, Sq, max_sel] int32
+    (ascending, -1 skipped) -> (o_latent [B,Sq,H,512], lse [B,Sq,H])."""
+    import torch
+    B, Sq, H = q.shape[0], q.shape[1], q.shape[2]
+    _tensor("q", q, torch.bfloat16, (B, Sq, H, D))
+    _tensor("block_table", block_table, torch.int32, (B, None))
+    _tensor("seq_lens", seq_lens, torch.int32, (B,))
+    _tensor("pages", pages, torch.int32, (B, Sq, None))
+    nb = _cache_blocks(kv_cache, kv_dtype, num_blocks)
+    _here(q)
+    K = pages.shape[2]
+    workspace, ws_bytes = _work_buf(workspace, decode_sparse_workspace_bytes(B, Sq, H, K, kv_dtype, num_splits),
+                                    q.device)
+    o_dtype = _dt_code(o_latent, o_dtype)
+    o_latent = _out_buf(o_latent, (B, Sq, H, L), o_dtype, q.device)
+    lse = _out_buf(lse, (B, Sq, H), DT_F32, q.device)
+    _check(lib().mla_decode_sparse(_p(q), _p(kv_cache), kv_dtype, nb, _p(block_table), block_table.shape[1],
+                                   _p(seq_lens), _p(pages), K, B, Sq, H, float(scale), int(num_splits), _p(workspace),
+                                   ws_bytes, _p(o_latent), o_dtype, _p(lse), _p(dev_status), _stream(stream)))
+    return o_latent, lse

@@ -28,7 +28,7 @@ __device__ __forceinline__ RowGeom row_geometry(const DecodeArgs& p, int unit, b
         const int S = p.num_splits;
         g.r = unit / S;
         split_range(visible_tokens(p, g.r, report), S, unit % S, &g.j0, &g.j1);
-        g.slot = S > 1 ? unit : -1;
+        g.slot = S > 1 || p.all_partial ? unit : -1;
     }
     int q_len;
     row_request(p, g.r, &g.b, &g.t, &q_len);
@@ -37,10 +37,10 @@ __device__ __forceinline__ RowGeom row_geometry(const DecodeArgs& p, int unit, b
     return g;
 }
 
-// Physical block of page `pg` of request b, or -1 (reported as MLA_DEV_BAD_BLOCK_ID) if the
+// Physical block of page `pg` (counted from the base) of request b, or -1 (reported as MLA_DEV_BAD_BLOCK_ID) if the
 // block-table entry is outside the cache.
 __device__ __forceinline__ int page_block(const DecodeArgs& p, int b, int pg) {
-    const int32_t blk = p.block_table[(size_t)b * p.max_blocks + pg];
+    const int32_t blk = *table_entry(p, b, pg);
     if (blk < 0 || (int64_t)blk >= p.num_blocks) {
         if (p.dev_status) atomicOr(p.dev_status, MLA_DEV_BAD_BLOCK_ID);
         return -1;

@@ -173,7 +173,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     const int unit = (int)(blockIdx.x >> 1);
     RowGeom g{};
-    if (!p.plan_units) g = row_geometry(p, unit, tid == 0 && rank == 0);  // its loads overlap the set-up
+    if (!p.plan_units && !p.wait_first)
+        g = row_geometry(p, unit, tid == 0 && rank == 0);  // its loads overlap the set-up
     volatile int* abort = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
     int32_t* ds = p.dev_status;
     auto bar = [&](int i) -> uint32_t { return sbase + OFF_CTRL + 8u * (uint32_t)i; };
@@ -204,11 +205,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();  // both CTAs' barriers exist before any remote arrive or store
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM);
     if (tid == 0) griddep_launch_dependents();
-    if (p.plan_units) {
-        // The schedule is the preceding kernel's output: the set-up above overlapped it.
-        // Clusters past its unit count leave together (both CTAs read the same count).
+    if (p.plan_units || p.wait_first) {
+        // The schedule (or the lengths and block table) is the preceding kernel's output: the
+        // set-up above overlapped it. Clusters past the schedule's unit count leave together
+        // (both CTAs read the same count).
         griddep_wait();
-        if (unit >= *p.plan_count) {
+        if (p.plan_units && unit >= *p.plan_count) {
             if (warp == 0) tmem_dealloc(tmem, kTmemCols);
             cluster_sync();
             return;

@@ -170,15 +170,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // fetches the first group's block-table entries while the length is still on its way
     // (validated once the page count is known).
     int blk_early[kPPG] = {-1, -1, -1, -1};
-    const bool early_blocks = p.plan_units == nullptr && p.qsl == nullptr && unit % p.num_splits == 0;
+    const bool early_blocks =
+        p.plan_units == nullptr && p.qsl == nullptr && !p.wait_first && unit % p.num_splits == 0;
     if (early_blocks && tid == 0 && rank == 0) {
-        const int32_t* row = p.block_table + (size_t)(unit / p.num_splits / p.Sq) * p.max_blocks;
 #pragma unroll
         for (int q = 0; q < kPPG; ++q)
-            if (q < p.max_blocks) blk_early[q] = ld_nc_s32(row + q);
+            if (p.base / kPage + q < p.max_blocks) blk_early[q] = ld_nc_s32(table_entry(p, unit / p.num_splits / p.Sq, q));
     }
     RowGeom g{};
-    if (!p.plan_units) g = row_geometry(p, unit, tid == 0 && rank == 0);  // its loads overlap the set-up
+    if (!p.plan_units && !p.wait_first)
+        g = row_geometry(p, unit, tid == 0 && rank == 0);  // its loads overlap the set-up
     volatile int* abort = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
     int32_t* ds = p.dev_status;
     auto bar = [&](int i) -> uint32_t { return sbase + 8u * (uint32_t)i; };
@@ -206,11 +207,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();  // both CTAs' barriers exist before any remote arrive or copy
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM);
     if (tid == 0) griddep_launch_dependents();
-    if (p.plan_units) {
-        // The schedule is the preceding kernel's output: the set-up above overlapped it.
-        // Clusters past its unit count leave together (both CTAs read the same count).
+    if (p.plan_units || p.wait_first) {
+        // The schedule (or the lengths and block table) is the preceding kernel's output: the
+        // set-up above overlapped it. Clusters past the schedule's unit count leave together
+        // (both CTAs read the same count).
         griddep_wait();
-        if (unit >= *p.plan_count) {
+        if (p.plan_units && unit >= *p.plan_count) {
             if (warp == 0) tmem_dealloc(tmem, kTmemCols);
             cluster_sync();
             return;
@@ -620,7 +622,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // Only a hint: the loop gives up quietly if it falls behind or the unit aborts.
                 const int ptid = tid - 192;
                 const volatile int* prog = reinterpret_cast<const volatile int*>(smem + OFF_PROG);
-                const int32_t* brow = p.block_table + (size_t)g.b * p.max_blocks + g.page0;
                 int spins = 0;
                 for (int t = kPPG; t < npages; ++t) {
                     bool go = true;
@@ -632,7 +633,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         __nanosleep(128);
                     }
                     if (!go) break;
-                    const int32_t blk = brow[t];
+                    const int32_t blk = *table_entry(p, g.b, g.page0 + t);
                     if (blk < 0 || (int64_t)blk >= p.num_blocks) continue;
                     const uint8_t* page = p.cache + (size_t)blk * (kPage * kBf16RowBytes);
                     for (int l = ptid; l < kPage * kBf16RowBytes / 128; l += 128) prefetch_l2(page + 128 * l);

@@ -32,6 +32,13 @@ struct DecodeArgs {
     const int32_t* qsl;         // packed rows: request b owns rows [qsl[b], qsl[b + 1]); else null
     float scale;
     int num_splits;             // resolved, >= 1
+    int shared_pages;           // the first pages of every request are those of block_table's row 0
+    int base;                   // tokens (whole pages) at the front of every request that are left out
+    int all_partial;            // every unit writes a partial state, also the only one of its row
+    int wait_first;             // lengths and block table are the preceding kernel's output
+    const float* pre_o;         // partial states of every row over the base tokens, merged with the
+    const float* pre_lse;       // row's own: [pre_splits, rows, H, 512] and [pre_splits, rows, H]
+    int pre_splits;             // (0: none)
     float* part_o;              // [B*Sq, S, H, 512] fp32 (num_splits > 1)
     float* part_lse;            // [B*Sq, S, H]     fp32 (num_splits > 1)
     void* o_latent;             // [B, Sq, H, 512]
@@ -70,7 +77,7 @@ __device__ __forceinline__ void row_request(const DecodeArgs& p, int r, int* b, 
     *q_len = p.qsl[lo + 1] - p.qsl[lo];
 }
 
-// Visible tokens of query row r: seq_len - (q_len - 1 - t), clamped at 0, with seq_len clamped
+// Visible tokens of query row r past the base: seq_len - (q_len - 1 - t) - base, clamped at 0, with seq_len clamped
 // to what the block table can hold; an out-of-range seq_len sets
 // MLA_DEV_SEQ_TOO_LONG when `report`.
 __device__ __forceinline__ int visible_tokens(const DecodeArgs& p, int r, bool report) {
@@ -82,8 +89,14 @@ __device__ __forceinline__ int visible_tokens(const DecodeArgs& p, int r, bool r
         if (report && p.dev_status) atomicOr(p.dev_status, MLA_DEV_SEQ_TOO_LONG);
         seq = seq < 0 ? 0 : (seq > cap ? cap : seq);
     }
-    const int n = seq - (q_len - 1 - t);
+    const int n = seq - (q_len - 1 - t) - p.base;
     return n < 0 ? 0 : n;
+}
+
+// The block-table entry of page `pg` (counted from the base) of request b.
+__device__ __forceinline__ const int32_t* table_entry(const DecodeArgs& p, int b, int pg) {
+    const int page = p.base / MLA_PAGE_SIZE + pg;
+    return p.block_table + (page < p.shared_pages ? (size_t)page : (size_t)b * p.max_blocks + page);
 }
 
 // Upper bound of planned units (num_splits == -2) for B * Sq query rows on `pairs` SM pairs.
@@ -96,7 +109,9 @@ struct WorkspaceLayout {
     int64_t partial_slots;  // rows of part_o / part_lse
 };
 // `rows` query rows (split partials per row); B, kv_dtype and max_seq_len do not change it.
-WorkspaceLayout workspace_layout(int kv_dtype, int B, int64_t rows, int H, int num_splits, int max_seq_len);
+// `all_partial`: one uniform split has its partial state too.
+WorkspaceLayout workspace_layout(int kv_dtype, int B, int64_t rows, int H, int num_splits, int max_seq_len,
+                                 bool all_partial = false);
 
 // Token range [j0, j1) of split s of a row with n visible tokens: the row is cut into
 // num_splits page-aligned chunks of round_up(ceil(n / S), 64) tokens; trailing splits may be
@@ -128,6 +143,77 @@ cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, size_t 
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
+
+// ---- page keys, page scores, page choice and sparse decode ----------------------------------
+struct PageKeysArgs {
+    const uint8_t* cache;       // [num_blocks, 64, row_bytes]
+    int64_t num_blocks;
+    const int32_t* block_table; // [B, max_blocks]
+    int max_blocks;
+    const int32_t* start_lens;  // [B] or null (0): tokens whose pages have their keys
+    const int32_t* seq_lens;    // [B]
+    int max_new_len, pages_per_req, B;
+    uint16_t* page_keys;        // bf16 [num_blocks, 576]
+    int32_t* dev_status;        // or null
+};
+struct PageScoresArgs {
+    const uint16_t* q;          // bf16 [B, Sq, H, 576]
+    const uint16_t* page_keys;  // bf16 [num_blocks, 576]
+    int64_t num_blocks;
+    const int32_t* block_table; // [B, max_blocks]
+    int max_blocks;
+    const int32_t* seq_lens;    // [B]
+    int max_seq_len, B, Sq, H;
+    float scale;
+    float* scores;              // fp32 [B * Sq, width]
+    int width;                  // ceil(max_seq_len / 64)
+    int32_t* dev_status;        // or null
+};
+struct SelectArgs {
+    const float* scores;        // row r at scores + r * stride, `width` entries
+    int64_t stride;
+    int width;
+    const int32_t* seq_lens;    // [B]
+    int B, Sq, K, sink, local;
+    int32_t* pages;             // [B * Sq, K]
+    int32_t* dev_status;        // or null
+};
+struct SparseTableArgs {
+    const int32_t* pages;       // [B * Sq, K] ascending page numbers, -1 behind
+    int K;
+    const int32_t* block_table; // [B, max_blocks]
+    int max_blocks;
+    const int32_t* seq_lens;    // [B]
+    int B, Sq;
+    int32_t* table;             // [B * Sq, K] blocks of the selected pages
+    int32_t* lens;              // [B * Sq] their tokens
+    int32_t* dev_status;        // or null
+};
+constexpr int kMaxSelectWidth = 49152;  // pages of a row whose keys fit the shared memory of a CTA
+cudaError_t launch_page_keys(const PageKeysArgs& a, bool fp8, cudaStream_t s);
+cudaError_t launch_page_scores(const PageScoresArgs& a, cudaStream_t s);
+cudaError_t launch_select_pages(const SelectArgs& a, cudaStream_t s);
+cudaError_t launch_sparse_table(const SparseTableArgs& a, cudaStream_t s);
+
+// What the body of a decode call does beyond mla_decode (its own call by default).
+struct DecodeExtra {
+    const char* who = "mla_decode";  // the entry point, for messages
+    int shared_pages = 0;            // see DecodeArgs
+    int base = 0;
+    bool all_partial = false;
+    bool wait_first = false;
+    const float* pre_o = nullptr;
+    const float* pre_lse = nullptr;
+    int pre_splits = 0;
+};
+mla_status decode_impl(const void* q, const void* kv_cache, mla_kv_dtype kv_dtype, int64_t num_blocks,
+                       const int32_t* block_table, int max_blocks, const int32_t* seq_lens, const int32_t* qsl,
+                       int max_seq_len, int B, int Sq, int64_t rows, int H, float scale, int num_splits,
+                       void* workspace, size_t workspace_bytes, void* o_latent, mla_dtype o_dtype, float* lse,
+                       int32_t* dev_status, mla_stream_t stream, const DecodeExtra& x);
+
+// Clear the detail string and return MLA_OK.
+mla_status set_ok();
 
 // Record an error for mla_last_error_detail() and return `st` (printf-style message).
 mla_status set_error(mla_status st, const char* fmt, ...);

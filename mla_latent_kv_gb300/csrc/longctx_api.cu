@@ -1,0 +1,257 @@
+// longctx_api.cu -- the entry points for long contexts: decode of a batch that shares a prefix, and
+// the steps of decode over selected pages (mean page keys, page scores, page choice, attention).
+// Host-side validation and launches, by the rules of mla_api.cu: nothing is allocated, freed or
+// synchronised, and every argument is checked before the first launch.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "internal.h"
+
+namespace {
+
+using mla::set_error;
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+bool known_kv(mla_kv_dtype d) { return d == MLA_KV_BF16 || d == MLA_KV_FP8_E4M3_SCALED; }
+
+mla_status cuda_error(cudaError_t e, const char* who) {
+    return set_error(MLA_ERR_CUDA, "%s launch: %s (%s)", who, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
+// Checks that the calls share. B == 0 is allowed.
+mla_status check_shape(const char* who, int B, int Sq, int64_t num_blocks, int max_blocks, int max_seq_len) {
+    if (B < 0 || Sq < 1) return set_error(MLA_ERR_INVALID_ARG, "%s: B=%d, Sq=%d", who, B, Sq);
+    if (max_seq_len < 0 || max_blocks < 0 || num_blocks < 0)
+        return set_error(MLA_ERR_INVALID_ARG, "%s: negative length, max_blocks or num_blocks", who);
+    if ((int64_t)max_seq_len > (int64_t)max_blocks * mla::kPage)
+        return set_error(MLA_ERR_INVALID_ARG, "%s: max_seq_len=%d exceeds max_blocks*64=%lld", who, max_seq_len,
+                         (long long)max_blocks * mla::kPage);
+    if (num_blocks > (int64_t)(INT32_MAX / mla::kPage))
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: num_blocks=%lld too large (max %d)", who, (long long)num_blocks,
+                         INT32_MAX / mla::kPage);
+    if ((int64_t)B * Sq > INT32_MAX / MLA_MAX_HEADS)
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: %lld query rows too many", who, (long long)B * Sq);
+    return MLA_OK;
+}
+
+// Workspace of a sparse decode: the rows' tables and lengths, then that of their decode.
+struct SparseLayout {
+    size_t table, lens, decode, total;
+};
+SparseLayout sparse_layout(mla_kv_dtype kv, int64_t rows, int H, int K, int S) {
+    SparseLayout w{};
+    w.table = 0;
+    w.lens = up256((size_t)rows * K * sizeof(int32_t));
+    w.decode = w.lens + up256((size_t)rows * sizeof(int32_t));
+    w.total = w.decode + mla::workspace_layout(kv, (int)rows, rows, H, S, K * mla::kPage).total;
+    return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+mla_status mla_page_keys(const void* kv_cache, mla_kv_dtype kv_dtype, int64_t num_blocks, const int32_t* block_table,
+                         int max_blocks, const int32_t* start_lens, const int32_t* seq_lens, int max_new_len, int B,
+                         void* page_keys, int32_t* dev_status, mla_stream_t stream) {
+    const char* who = "mla_page_keys";
+    if (!known_kv(kv_dtype)) return set_error(MLA_ERR_INVALID_ARG, "%s: unknown kv_dtype %d", who, (int)kv_dtype);
+    const mla_status st = check_shape(who, B, 1, num_blocks, max_blocks, max_new_len);
+    if (st != MLA_OK) return st;
+    if (B == 0 || max_new_len == 0) return mla::set_ok();
+    if (!kv_cache || !block_table || !seq_lens || !page_keys)
+        return set_error(MLA_ERR_INVALID_ARG, "%s: null pointer", who);
+    if (!aligned16(kv_cache) || !aligned16(page_keys))
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: kv_cache and page_keys must be 16-byte aligned", who);
+    mla::PageKeysArgs a{};
+    a.cache = (const uint8_t*)kv_cache;
+    a.num_blocks = num_blocks;
+    a.block_table = block_table;
+    a.max_blocks = max_blocks;
+    a.start_lens = start_lens;
+    a.seq_lens = seq_lens;
+    a.max_new_len = max_new_len;
+    // new tokens that start inside a page touch one page more than their number fills
+    const int full = (max_new_len + mla::kPage - 1) / mla::kPage;
+    a.pages_per_req = std::min(start_lens ? full + 1 : full, max_blocks);
+    a.B = B;
+    a.page_keys = (uint16_t*)page_keys;
+    a.dev_status = dev_status;
+    if ((int64_t)B * a.pages_per_req > INT32_MAX)
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: %lld pages too many", who, (long long)B * a.pages_per_req);
+    const cudaError_t e = mla::launch_page_keys(a, kv_dtype == MLA_KV_FP8_E4M3_SCALED, (cudaStream_t)stream);
+    return e == cudaSuccess ? mla::set_ok() : cuda_error(e, who);
+}
+
+mla_status mla_page_scores(const void* q, const void* page_keys, int64_t num_blocks, const int32_t* block_table,
+                           int max_blocks, const int32_t* seq_lens, int max_seq_len, int B, int Sq, int H, float scale,
+                           float* scores, int32_t* dev_status, mla_stream_t stream) {
+    const char* who = "mla_page_scores";
+    if (H < 1 || H > MLA_MAX_HEADS)
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: H=%d outside [1, %d]", who, H, MLA_MAX_HEADS);
+    const mla_status st = check_shape(who, B, Sq, num_blocks, max_blocks, max_seq_len);
+    if (st != MLA_OK) return st;
+    if (!std::isfinite(scale) || scale <= 0.f)
+        return set_error(MLA_ERR_INVALID_ARG, "%s: scale must be finite and > 0", who);
+    if (B == 0 || max_seq_len == 0) return mla::set_ok();
+    if (!q || !page_keys || !block_table || !seq_lens || !scores)
+        return set_error(MLA_ERR_INVALID_ARG, "%s: null pointer", who);
+    if (!aligned16(q) || !aligned16(page_keys))
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: q and page_keys must be 16-byte aligned", who);
+    mla::PageScoresArgs a{};
+    a.q = (const uint16_t*)q;
+    a.page_keys = (const uint16_t*)page_keys;
+    a.num_blocks = num_blocks;
+    a.block_table = block_table;
+    a.max_blocks = max_blocks;
+    a.seq_lens = seq_lens;
+    a.max_seq_len = max_seq_len;
+    a.B = B;
+    a.Sq = Sq;
+    a.H = H;
+    a.scale = scale;
+    a.scores = scores;
+    a.width = (max_seq_len + mla::kPage - 1) / mla::kPage;
+    a.dev_status = dev_status;
+    if ((int64_t)B * Sq * ((a.width + 127) / 128) > INT32_MAX)
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: B*Sq*max_seq_len too large", who);
+    const cudaError_t e = mla::launch_page_scores(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? mla::set_ok() : cuda_error(e, who);
+}
+
+mla_status mla_select_pages(const float* scores, int64_t scores_stride, int num_pages, const int32_t* seq_lens, int B,
+                            int Sq, int max_sel, int sink_pages, int local_pages, int32_t* pages, int32_t* dev_status,
+                            mla_stream_t stream) {
+    const char* who = "mla_select_pages";
+    if (B < 0 || Sq < 1 || num_pages < 0 || max_sel < 1)
+        return set_error(MLA_ERR_INVALID_ARG, "%s: B=%d, Sq=%d, num_pages=%d, max_sel=%d", who, B, Sq, num_pages,
+                         max_sel);
+    if (sink_pages < 0 || local_pages < 0 || (int64_t)sink_pages + local_pages > max_sel)
+        return set_error(MLA_ERR_INVALID_ARG, "%s: sink_pages=%d and local_pages=%d do not fit max_sel=%d", who,
+                         sink_pages, local_pages, max_sel);
+    if (scores_stride < num_pages)
+        return set_error(MLA_ERR_INVALID_ARG, "%s: scores_stride=%lld < num_pages=%d", who, (long long)scores_stride,
+                         num_pages);
+    if (num_pages > mla::kMaxSelectWidth)
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: num_pages=%d above %d", who, num_pages, mla::kMaxSelectWidth);
+    if ((int64_t)B * Sq > INT32_MAX)
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: %lld query rows too many", who, (long long)B * Sq);
+    if (B == 0) return mla::set_ok();
+    if (!seq_lens || !pages || (num_pages > 0 && !scores))
+        return set_error(MLA_ERR_INVALID_ARG, "%s: null pointer", who);
+    mla::SelectArgs a{};
+    a.scores = scores;
+    a.stride = scores_stride;
+    a.width = num_pages;
+    a.seq_lens = seq_lens;
+    a.B = B;
+    a.Sq = Sq;
+    a.K = max_sel;
+    a.sink = sink_pages;
+    a.local = local_pages;
+    a.pages = pages;
+    a.dev_status = dev_status;
+    const cudaError_t e = mla::launch_select_pages(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? mla::set_ok() : cuda_error(e, who);
+}
+
+size_t mla_decode_sparse_workspace_bytes(mla_kv_dtype kv_dtype, int B, int Sq, int H, int max_sel, int num_splits) {
+    if (!known_kv(kv_dtype) || B < 1 || Sq < 1 || H < 1 || H > MLA_MAX_HEADS || max_sel < 1 ||
+        max_sel > INT32_MAX / mla::kPage || (int64_t)B * Sq > INT32_MAX / MLA_MAX_HEADS)
+        return 0;
+    const int rows = B * Sq;
+    const int S = mla_resolve_num_splits(num_splits, rows, 1, H, max_sel * mla::kPage);
+    if (S < 1 && S != -2) return 0;
+    return sparse_layout(kv_dtype, rows, H, max_sel, S).total;
+}
+
+mla_status mla_decode_sparse(const void* q, const void* kv_cache, mla_kv_dtype kv_dtype, int64_t num_blocks,
+                             const int32_t* block_table, int max_blocks, const int32_t* seq_lens, const int32_t* pages,
+                             int max_sel, int B, int Sq, int H, float scale, int num_splits, void* workspace,
+                             size_t workspace_bytes, void* o_latent, mla_dtype o_dtype, float* lse,
+                             int32_t* dev_status, mla_stream_t stream) {
+    const char* who = "mla_decode_sparse";
+    if (!known_kv(kv_dtype)) return set_error(MLA_ERR_INVALID_ARG, "%s: unknown kv_dtype %d", who, (int)kv_dtype);
+    if (H < 1 || H > MLA_MAX_HEADS)
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: H=%d outside [1, %d]", who, H, MLA_MAX_HEADS);
+    const mla_status st = check_shape(who, B, Sq, num_blocks, max_blocks, 0);
+    if (st != MLA_OK) return st;
+    if ((int64_t)max_blocks * mla::kPage > INT32_MAX)
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: max_blocks=%d too large", who, max_blocks);
+    if (max_sel < 1 || max_sel > INT32_MAX / mla::kPage)
+        return set_error(MLA_ERR_INVALID_ARG, "%s: max_sel=%d outside [1, %d]", who, max_sel, INT32_MAX / mla::kPage);
+    if (num_splits < -2) return set_error(MLA_ERR_INVALID_ARG, "%s: num_splits=%d < -2", who, num_splits);
+    if (o_dtype != MLA_DT_F32 && o_dtype != MLA_DT_BF16)
+        return set_error(MLA_ERR_INVALID_ARG, "%s: unknown o_dtype %d", who, (int)o_dtype);
+    if (!std::isfinite(scale) || scale <= 0.f)
+        return set_error(MLA_ERR_INVALID_ARG, "%s: scale must be finite and > 0", who);
+    if (B == 0) return mla::set_ok();
+    if (!q || !o_latent || !seq_lens || !pages || !kv_cache || !block_table)
+        return set_error(MLA_ERR_INVALID_ARG, "%s: null pointer", who);
+    if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(o_latent))
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: q, kv_cache and o_latent must be 16-byte aligned", who);
+    const int rows = B * Sq;
+    const int S = mla_resolve_num_splits(num_splits, rows, 1, H, max_sel * mla::kPage);
+    if (S < 1 && S != -2) return set_error(MLA_ERR_CUDA, "%s: could not resolve num_splits (no CUDA device?)", who);
+    const SparseLayout w = sparse_layout(kv_dtype, rows, H, max_sel, S);
+    if (!workspace || workspace_bytes < w.total)
+        return set_error(MLA_ERR_WORKSPACE_TOO_SMALL, "%s: workspace %zu bytes < %zu needed", who,
+                         workspace ? workspace_bytes : (size_t)0, w.total);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: workspace must be 256-byte aligned", who);
+    mla::SparseTableArgs t{};
+    t.pages = pages;
+    t.K = max_sel;
+    t.block_table = block_table;
+    t.max_blocks = max_blocks;
+    t.seq_lens = seq_lens;
+    t.B = B;
+    t.Sq = Sq;
+    t.table = (int32_t*)((char*)workspace + w.table);
+    t.lens = (int32_t*)((char*)workspace + w.lens);
+    t.dev_status = dev_status;
+    const cudaError_t e = mla::launch_sparse_table(t, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_error(e, who);
+    mla::DecodeExtra x;
+    x.who = who;
+    x.wait_first = true;
+    return mla::decode_impl(q, kv_cache, kv_dtype, num_blocks, t.table, max_sel, t.lens, nullptr, max_sel * mla::kPage,
+                            rows, 1, rows, H, scale, S, (char*)workspace + w.decode, w.total - w.decode, o_latent,
+                            o_dtype, lse, dev_status, stream, x);
+}
+
+size_t mla_decode_shared_prefix_workspace_bytes(mla_kv_dtype kv_dtype, int B, int Sq, int H, int prefix_len,
+                                                int num_splits, int max_seq_len) {
+    if (!known_kv(kv_dtype) || B < 1 || Sq < 1 || H < 1 || H > MLA_MAX_HEADS || prefix_len < 0 ||
+        prefix_len % mla::kPage || max_seq_len < 0 || (int64_t)B * Sq > INT32_MAX / MLA_MAX_HEADS)
+        return 0;
+    const int S = mla_resolve_num_splits(num_splits, B, Sq, H, max_seq_len);
+    if (S < 1 && S != -2) return 0;
+    return mla::workspace_layout(kv_dtype, B, (int64_t)B * Sq, H, S, max_seq_len).total;
+}
+
+mla_status mla_decode_shared_prefix(const void* q, const void* kv_cache, mla_kv_dtype kv_dtype, int64_t num_blocks,
+                                    const int32_t* block_table, int max_blocks, const int32_t* seq_lens,
+                                    int max_seq_len, int prefix_len, int B, int Sq, int H, float scale,
+                                    int num_splits, void* workspace, size_t workspace_bytes, void* o_latent,
+                                    mla_dtype o_dtype, float* lse, int32_t* dev_status, mla_stream_t stream) {
+    const char* who = "mla_decode_shared_prefix";
+    const mla_status st = check_shape(who, B, Sq, num_blocks, max_blocks, max_seq_len);
+    if (st != MLA_OK) return st;
+    if (prefix_len < 0 || prefix_len % mla::kPage)
+        return set_error(MLA_ERR_INVALID_ARG, "%s: prefix_len=%d is not a multiple of 64", who, prefix_len);
+    if ((int64_t)prefix_len > (int64_t)max_blocks * mla::kPage)
+        return set_error(MLA_ERR_INVALID_ARG, "%s: prefix_len=%d exceeds max_blocks*64=%lld", who, prefix_len,
+                         (long long)max_blocks * mla::kPage);
+    mla::DecodeExtra x;
+    x.who = who;
+    x.shared_pages = prefix_len / mla::kPage;
+    return mla::decode_impl(q, kv_cache, kv_dtype, num_blocks, block_table, max_blocks, seq_lens, nullptr, max_seq_len,
+                            B, Sq, (int64_t)B * Sq, H, scale, num_splits, workspace, workspace_bytes, o_latent, o_dtype,
+                            lse, dev_status, stream, x);
+}
+
+}  // extern "C"

@@ -20,8 +20,11 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kBatch = 4;  // splits whose partials are loaded together
 
+template <bool kPre>
 __device__ __forceinline__ void merge_item(const DecodeArgs& p, int64_t r, int h, int half, int lane);
 
+// kPre: the row's states over the base tokens (pre_o, pre_lse) come before its own.
+template <bool kPre>
 __global__ void __launch_bounds__(kWarps * 32) merge_kernel(DecodeArgs p) {
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();  // the partials are the preceding kernel's output
@@ -34,10 +37,11 @@ __global__ void __launch_bounds__(kWarps * 32) merge_kernel(DecodeArgs p) {
         const int64_t item = t >> 1;
         const int64_t i = item / p.H;
         const int64_t r = p.plan_rows ? (int64_t)p.plan_split_rows[i] : i;
-        merge_item(p, r, (int)(item % p.H), (int)(t & 1), lane);
+        merge_item<kPre>(p, r, (int)(item % p.H), (int)(t & 1), lane);
     }
 }
 
+template <bool kPre>
 __device__ __forceinline__ void merge_item(const DecodeArgs& p, int64_t r, int h, int half, int lane) {
     // the row's partials are slots [slot0, slot0 + S): uniform splits put row r at r * S; a
     // device-built schedule lists them per row (a row with one unit already wrote its output)
@@ -46,7 +50,7 @@ __device__ __forceinline__ void merge_item(const DecodeArgs& p, int64_t r, int h
         const int2 ri = p.plan_rows[r];
         S = ri.y;
         slot0 = ri.x;
-        if (S <= 1) return;
+        if (!kPre && S <= 1) return;
     } else {
         S = p.num_splits;
         slot0 = (int)(r * S);
@@ -55,6 +59,9 @@ __device__ __forceinline__ void merge_item(const DecodeArgs& p, int64_t r, int h
 
     float M = -CUDART_INF_F;
     for (int s = lane; s < S; s += 32) M = fmaxf(M, lse_p[(size_t)s * p.H]);
+    const size_t heads = (size_t)p.rows * p.H, rh = (size_t)r * p.H + h;
+    if constexpr (kPre)
+        for (int s = lane; s < p.pre_splits; s += 32) M = fmaxf(M, p.pre_lse[(size_t)s * heads + rh]);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
 
@@ -62,10 +69,9 @@ __device__ __forceinline__ void merge_item(const DecodeArgs& p, int64_t r, int h
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
     float wsum = 0.f;
-    if (M != -CUDART_INF_F) {
-        const size_t split_stride = (size_t)p.H * kL;
-        const float* src0 = p.part_o + ((size_t)slot0 * p.H + h) * kL + half * (kL / 2) + lane * 8;
-        for (int s0 = 0; s0 < S; s0 += kBatch) {
+    // the states at src0 + s * stride and lses + s * lse_stride, s < count
+    auto add = [&](const float* src0, size_t stride, const float* lses, size_t lse_stride, int count) {
+        for (int s0 = 0; s0 < count; s0 += kBatch) {
             // all loads of the batch first, then the arithmetic in split order
             float ls[kBatch];
             float4 v[kBatch][2];
@@ -73,9 +79,9 @@ __device__ __forceinline__ void merge_item(const DecodeArgs& p, int64_t r, int h
             for (int u = 0; u < kBatch; ++u) {
                 ls[u] = -CUDART_INF_F;
                 v[u][0] = v[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (s0 + u < S) {
-                    ls[u] = lse_p[(size_t)(s0 + u) * p.H];
-                    const float4* src = reinterpret_cast<const float4*>(src0 + (size_t)(s0 + u) * split_stride);
+                if (s0 + u < count) {
+                    ls[u] = lses[(size_t)(s0 + u) * lse_stride];
+                    const float4* src = reinterpret_cast<const float4*>(src0 + (size_t)(s0 + u) * stride);
                     v[u][0] = src[0];
                     v[u][1] = src[1];
                 }
@@ -94,6 +100,11 @@ __device__ __forceinline__ void merge_item(const DecodeArgs& p, int64_t r, int h
                 }
             }
         }
+    };
+    if (M != -CUDART_INF_F) {
+        const int dim = half * (kL / 2) + lane * 8;
+        if constexpr (kPre) add(p.pre_o + rh * kL + dim, heads * kL, p.pre_lse + rh, heads, p.pre_splits);
+        add(p.part_o + ((size_t)slot0 * p.H + h) * kL + dim, (size_t)p.H * kL, lse_p, p.H, S);
     }
     const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
     const size_t base = ((size_t)r * p.H + h) * kL + half * (kL / 2) + lane * 8;
@@ -118,7 +129,7 @@ cudaError_t launch_merge(const DecodeArgs& a, cudaStream_t s) {
     // grid-stride over the split rows: enough warps that each takes about one (row, head, half),
     // since a task is a chain of dependent loads; with no split row every block ends at once
     if (a.plan_rows && blocks > 1216) blocks = 1216;
-    return launch_pdl(merge_kernel, dim3((unsigned)blocks), dim3(kWarps * 32), 0, s, a);
+    return launch_pdl(a.pre_splits > 0 ? merge_kernel<true> : merge_kernel<false>, dim3((unsigned)blocks), dim3(kWarps * 32), 0, s, a);
 }
 
 }  // namespace mla

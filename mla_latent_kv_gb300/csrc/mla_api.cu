@@ -36,6 +36,10 @@ mla_status cuda_fail(cudaError_t e, const char* what) {
     return fail(MLA_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
+mla_status cuda_fail(cudaError_t e, const char* who, const char* what) {
+    return fail(MLA_ERR_CUDA, "%s %s: %s (%s)", who, what, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int device_sm_count() {
@@ -49,12 +53,13 @@ int device_sm_count() {
 }  // namespace
 
 namespace mla {
-WorkspaceLayout workspace_layout(int kv_dtype, int B, int64_t rows, int H, int num_splits, int max_seq_len) {
+WorkspaceLayout workspace_layout(int kv_dtype, int B, int64_t rows, int H, int num_splits, int max_seq_len,
+                                 bool all_partial) {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     WorkspaceLayout w{};
     if (B <= 0 || rows <= 0 || H <= 0) return w;
     size_t off = 0;
-    int64_t slots = num_splits > 1 ? rows * num_splits : 0;
+    int64_t slots = num_splits > 1 || (num_splits == 1 && all_partial) ? rows * num_splits : 0;
     if (num_splits == -2) {  // device-built schedule: header, unit list, per-row slots
         const int sms = device_sm_count();
         if (sms < 1) return w;
@@ -80,6 +85,8 @@ mla_status set_error(mla_status st, const char* fmt, ...) {
     va_end(ap);
     return st;
 }
+
+mla_status set_ok() { return ok(); }
 }  // namespace mla
 
 extern "C" {
@@ -194,55 +201,56 @@ mla_status mla_absorb_q(const void* q_nope, int64_t snt, int64_t snh, const void
 
 }  // extern "C"
 
-namespace {
+namespace mla {
 
-// Shared body of mla_decode (uniform Sq rows per request, qsl == nullptr) and mla_decode_varlen
-// (packed rows, qsl = query_start_loc, Sq == 1): `rows` query rows of q / o_latent / lse.
+// Shared body of mla_decode (uniform Sq rows per request, qsl == nullptr), mla_decode_varlen
+// (packed rows, qsl = query_start_loc, Sq == 1) and the calls that decode a part of the cache:
+// `rows` query rows of q / o_latent / lse.
 mla_status decode_impl(const void* q, const void* kv_cache, mla_kv_dtype kv_dtype, int64_t num_blocks,
                        const int32_t* block_table, int max_blocks, const int32_t* seq_lens, const int32_t* qsl,
                        int max_seq_len, int B, int Sq, int64_t rows, int H, float scale, int num_splits,
                        void* workspace, size_t workspace_bytes, void* o_latent, mla_dtype o_dtype, float* lse,
-                       int32_t* dev_status, mla_stream_t stream) {
+                       int32_t* dev_status, mla_stream_t stream, const DecodeExtra& x) {
     if (H < 1 || H > MLA_MAX_HEADS)
-        return fail(MLA_ERR_UNSUPPORTED, "mla_decode: H=%d outside [1, %d]", H, MLA_MAX_HEADS);
+        return fail(MLA_ERR_UNSUPPORTED, "%s: H=%d outside [1, %d]", x.who, H, MLA_MAX_HEADS);
     if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_FP8_E4M3_SCALED)
-        return fail(MLA_ERR_INVALID_ARG, "mla_decode: unknown kv_dtype %d", (int)kv_dtype);
+        return fail(MLA_ERR_INVALID_ARG, "%s: unknown kv_dtype %d", x.who, (int)kv_dtype);
     if (o_dtype != MLA_DT_F32 && o_dtype != MLA_DT_BF16)
-        return fail(MLA_ERR_INVALID_ARG, "mla_decode: unknown o_dtype %d", (int)o_dtype);
+        return fail(MLA_ERR_INVALID_ARG, "%s: unknown o_dtype %d", x.who, (int)o_dtype);
     if (max_seq_len < 0 || max_blocks < 0 || num_blocks < 0)
-        return fail(MLA_ERR_INVALID_ARG, "mla_decode: negative max_seq_len/max_blocks/num_blocks");
+        return fail(MLA_ERR_INVALID_ARG, "%s: negative max_seq_len/max_blocks/num_blocks", x.who);
     if ((int64_t)max_seq_len > (int64_t)max_blocks * mla::kPage)
-        return fail(MLA_ERR_INVALID_ARG, "mla_decode: max_seq_len=%d exceeds max_blocks*64=%lld", max_seq_len,
+        return fail(MLA_ERR_INVALID_ARG, "%s: max_seq_len=%d exceeds max_blocks*64=%lld", x.who, max_seq_len,
                     (long long)max_blocks * mla::kPage);
     if (!(std::isfinite(scale)) || scale <= 0.f)
-        return fail(MLA_ERR_INVALID_ARG, "mla_decode: scale must be finite and > 0");
-    if (num_splits < -2) return fail(MLA_ERR_INVALID_ARG, "mla_decode: num_splits=%d < -2", num_splits);
+        return fail(MLA_ERR_INVALID_ARG, "%s: scale must be finite and > 0", x.who);
+    if (num_splits < -2) return fail(MLA_ERR_INVALID_ARG, "%s: num_splits=%d < -2", x.who, num_splits);
     if (B == 0 || rows == 0) return ok();
     if (!q || !o_latent || !seq_lens || (max_seq_len > 0 && (!kv_cache || !block_table)))
-        return fail(MLA_ERR_INVALID_ARG, "mla_decode: null pointer");
-    if (rows > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "mla_decode: %lld query rows too many", (long long)rows);
+        return fail(MLA_ERR_INVALID_ARG, "%s: null pointer", x.who);
+    if (rows > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "%s: %lld query rows too many", x.who, (long long)rows);
     if (!aligned16(q) || (kv_cache && !aligned16(kv_cache)) || !aligned16(o_latent))
-        return fail(MLA_ERR_UNSUPPORTED, "mla_decode: q, kv_cache and o_latent must be 16-byte aligned");
+        return fail(MLA_ERR_UNSUPPORTED, "%s: q, kv_cache and o_latent must be 16-byte aligned", x.who);
     if (num_blocks > (int64_t)(INT32_MAX / mla::kPage))
-        return fail(MLA_ERR_UNSUPPORTED, "mla_decode: num_blocks=%lld too large (max %d)", (long long)num_blocks,
+        return fail(MLA_ERR_UNSUPPORTED, "%s: num_blocks=%lld too large (max %d)", x.who, (long long)num_blocks,
                     INT32_MAX / mla::kPage);
-    int S = mla_resolve_num_splits(num_splits, (int)rows, 1, H, max_seq_len);
+    int S = mla_resolve_num_splits(num_splits, (int)rows, 1, H, std::max(0, max_seq_len - x.base));
     const bool planned = S == -2;
-    if (S < 1 && !planned) return fail(MLA_ERR_CUDA, "mla_decode: could not resolve num_splits (no CUDA device?)");
+    if (S < 1 && !planned) return fail(MLA_ERR_CUDA, "%s: could not resolve num_splits (no CUDA device?)", x.who);
     if (rows * H > (int64_t)INT32_MAX)
-        return fail(MLA_ERR_UNSUPPORTED, "mla_decode: rows*H=%lld too large", (long long)(rows * H));
+        return fail(MLA_ERR_UNSUPPORTED, "%s: rows*H=%lld too large", x.who, (long long)(rows * H));
     const int pairs = planned ? std::max(1, device_sm_count() / 2) : 1;
     const int64_t max_units = planned ? mla::plan_max_units(rows, pairs) : rows * S;
     if (max_units > (int64_t)1 << 30)
-        return fail(MLA_ERR_UNSUPPORTED, "mla_decode: %lld work units too many", (long long)max_units);
-    const mla::WorkspaceLayout wl = mla::workspace_layout(kv_dtype, B, rows, H, S, max_seq_len);
+        return fail(MLA_ERR_UNSUPPORTED, "%s: %lld work units too many", x.who, (long long)max_units);
+    const mla::WorkspaceLayout wl = mla::workspace_layout(kv_dtype, B, rows, H, S, max_seq_len, x.all_partial);
     const size_t need = wl.total;
     if (need > 0 && (workspace == nullptr || workspace_bytes < need))
         return fail(MLA_ERR_WORKSPACE_TOO_SMALL,
-                    "mla_decode: workspace %zu bytes < %zu needed (%d splits)",
+                    "%s: workspace %zu bytes < %zu needed (%d splits)", x.who,
                     workspace ? workspace_bytes : (size_t)0, need, S);
     if (need > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u))
-        return fail(MLA_ERR_UNSUPPORTED, "mla_decode: workspace must be 256-byte aligned");
+        return fail(MLA_ERR_UNSUPPORTED, "%s: workspace must be 256-byte aligned", x.who);
 
     mla::DecodeArgs a{};
     a.q = (const uint16_t*)q;
@@ -260,6 +268,13 @@ mla_status decode_impl(const void* q, const void* kv_cache, mla_kv_dtype kv_dtyp
     a.H = H;
     a.scale = scale;
     a.num_splits = planned ? 1 : S;
+    a.shared_pages = x.shared_pages;
+    a.base = x.base;
+    a.all_partial = x.all_partial ? 1 : 0;
+    a.wait_first = x.wait_first ? 1 : 0;
+    a.pre_o = x.pre_o;
+    a.pre_lse = x.pre_lse;
+    a.pre_splits = x.pre_splits;
     if (wl.partial_slots > 0) {
         a.part_o = (float*)((char*)workspace + wl.part_o);
         a.part_lse = (float*)((char*)workspace + wl.part_lse);
@@ -282,18 +297,18 @@ mla_status decode_impl(const void* q, const void* kv_cache, mla_kv_dtype kv_dtyp
     cudaError_t e = cudaSuccess;
     if (planned) {
         e = mla::launch_plan(a, pairs, st);
-        if (e != cudaSuccess) return cuda_fail(e, "mla_decode schedule launch");
+        if (e != cudaSuccess) return cuda_fail(e, x.who, "schedule launch");
     }
     e = fp8 ? mla::launch_decode_fp8_sm103(a, st) : mla::launch_decode_sm103(a, st);
-    if (e != cudaSuccess) return cuda_fail(e, "mla_decode launch");
-    if (planned || S > 1) {
+    if (e != cudaSuccess) return cuda_fail(e, x.who, "decode launch");
+    if (planned || S > 1 || x.all_partial) {
         e = mla::launch_merge(a, st);
-        if (e != cudaSuccess) return cuda_fail(e, "mla_decode merge launch");
+        if (e != cudaSuccess) return cuda_fail(e, x.who, "merge launch");
     }
     return ok();
 }
 
-}  // namespace
+}  // namespace mla
 
 extern "C" {
 
@@ -304,9 +319,9 @@ mla_status mla_decode(const void* q, const void* kv_cache, mla_kv_dtype kv_dtype
                       int32_t* dev_status, mla_stream_t stream) {
     if (B < 0) return fail(MLA_ERR_INVALID_ARG, "mla_decode: B=%d < 0", B);
     if (Sq < 1) return fail(MLA_ERR_INVALID_ARG, "mla_decode: Sq=%d < 1", Sq);
-    return decode_impl(q, kv_cache, kv_dtype, num_blocks, block_table, max_blocks, seq_lens, nullptr, max_seq_len,
-                       B, Sq, (int64_t)B * Sq, H, scale, num_splits, workspace, workspace_bytes, o_latent, o_dtype,
-                       lse, dev_status, stream);
+    return mla::decode_impl(q, kv_cache, kv_dtype, num_blocks, block_table, max_blocks, seq_lens, nullptr, max_seq_len,
+                            B, Sq, (int64_t)B * Sq, H, scale, num_splits, workspace, workspace_bytes, o_latent,
+                            o_dtype, lse, dev_status, stream, mla::DecodeExtra{});
 }
 
 mla_status mla_decode_varlen(const void* q, const void* kv_cache, mla_kv_dtype kv_dtype, int64_t num_blocks,
@@ -316,9 +331,9 @@ mla_status mla_decode_varlen(const void* q, const void* kv_cache, mla_kv_dtype k
                              mla_dtype o_dtype, float* lse, int32_t* dev_status, mla_stream_t stream) {
     if (B < 0 || total_q < 0) return fail(MLA_ERR_INVALID_ARG, "mla_decode_varlen: B=%d, total_q=%d", B, total_q);
     if (total_q > 0 && !query_start_loc) return fail(MLA_ERR_INVALID_ARG, "mla_decode_varlen: null query_start_loc");
-    return decode_impl(q, kv_cache, kv_dtype, num_blocks, block_table, max_blocks, seq_lens, query_start_loc,
-                       max_seq_len, B, 1, total_q, H, scale, num_splits, workspace, workspace_bytes, o_latent,
-                       o_dtype, lse, dev_status, stream);
+    return mla::decode_impl(q, kv_cache, kv_dtype, num_blocks, block_table, max_blocks, seq_lens, query_start_loc,
+                            max_seq_len, B, 1, total_q, H, scale, num_splits, workspace, workspace_bytes, o_latent,
+                            o_dtype, lse, dev_status, stream, mla::DecodeExtra{});
 }
 
 mla_status mla_cache_write(const void* kv_c, int64_t kv_c_stride_t, const void* k_pe, int64_t k_pe_stride_t,

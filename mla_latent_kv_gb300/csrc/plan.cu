@@ -177,6 +177,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(DecodeArgs p, int pairs)
         const int S = units_of(pg, c);
         if (S == 1) {
             cnt[bucket_of(pg, c)] += 1;
+            cnt[kBuckets] += p.all_partial;
+            cnt[kBuckets + 1] += p.all_partial;
         } else {
             cnt[0] += rem ? S - 1 : S;  // full-size units
             if (rem) cnt[bucket_of(pg - (S - 1) * c, c)] += 1;
@@ -227,6 +229,13 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(DecodeArgs p, int pairs)
         const int n = tokens(r);
         const int pg = pages_of(n);
         const int S = units_of(pg, c);
+        if (S == 1 && p.all_partial) {  // its one unit writes a partial state like the others
+            const int slot = base[kBuckets + 1]++;
+            units[base[bucket_of(pg, c)]++] = make_int4(r, 0, n, slot);
+            rows[r] = make_int2(slot, 1);
+            split_rows[base[kBuckets]++] = r;
+            continue;
+        }
         if (S == 1) {
             units[base[bucket_of(pg, c)]++] = make_int4(r, 0, n, -1);
             rows[r] = make_int2(-1, 1);

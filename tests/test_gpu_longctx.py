@@ -1,0 +1,446 @@
+"""Decode over a shared prefix and over selected pages, on the GPU, against their definitions in 64 bits."""
+import math
+
+import numpy as np
+import pytest
+
+import mla_inputs as mi
+from longctx_util import D, L, PAGE, attend, bf16, check_attention, dev, keys_values, paged_case, select_rule
+
+pytestmark = pytest.mark.gpu
+BF, F8 = mi.KV_BF16, mi.KV_FP8
+
+
+def _status():
+    import torch
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+# -------------------------------------------------------------------------------- shared prefix
+def _prefix(c, num_splits=-1, status=None, **kw):
+    import mla_latent_kv_gb300 as mla
+    return mla.decode_shared_prefix(c["q"], c["cache"], c["table"], c["seq_lens"], c["max_len"], c["prefix"], c["scale"],
+                                    kv_dtype=c["kv"], num_splits=num_splits, dev_status=status,
+                                    num_blocks=c["num_blocks"], **kw)
+
+
+@pytest.mark.parametrize("kv", [BF, F8])
+@pytest.mark.parametrize("B,Sq,H,prefix,suffix", [
+    (1, 1, 1, 64, [1]),                      # one row of one head, one page
+    (2, 1, 16, 128, [172, 3]),
+    (3, 1, 20, 192, [1, 64, 65]),            # odd number of prefix pages, heads not a tile
+    (5, 2, 128, 640, [2, 63, 130, 64, 7]),   # ten row tiles
+    (9, 3, 37, 320, [3, 5, 64, 66, 200, 4, 9, 128, 129]),
+    (2, 1, 128, 4096, [1, 100]),             # a long prefix, few rows: divided over the device
+    (130, 1, 8, 1024, [1 + b % 90 for b in range(130)]),  # more rows than SM pairs
+])
+def test_shared_prefix(kv, B, Sq, H, prefix, suffix):
+    c = paged_case([prefix + s for s in suffix], Sq, H, kv, seed=B * 100 + H, prefix=prefix,
+                   scale_v=0.5 if kv == F8 else None)
+    st = _status()
+    o, lse = _prefix(c, status=st)
+    assert int(st.item()) == 0
+    check_attention(o, lse, attend(c))
+
+
+@pytest.mark.parametrize("kv", [BF, F8])
+@pytest.mark.parametrize("num_splits", [1, 3, 0, -1, -2])
+def test_shared_prefix_suffix_splits_and_bf16_output(kv, num_splits):
+    import mla_latent_kv_gb300 as mla
+    c = paged_case([576 + s for s in (1, 700, 64, 129)], 1, 32, kv, seed=7, prefix=576)
+    o, lse = _prefix(c, num_splits, o_dtype=mla.DT_BF16)
+    check_attention(o, lse, attend(c), bf16_out=True)
+
+
+@pytest.mark.parametrize("kv", [BF, F8])
+def test_shared_prefix_rows_inside_the_prefix(kv):
+    """Requests shorter than the prefix see their own tokens only; empty slots give o = 0, lse = -inf."""
+    lens = [256 + 70, 0, 1, 2, 64, 100, 255, 256, 257, 0]
+    c = paged_case(lens, 2, 40, kv, seed=11, prefix=256)
+    o, lse = _prefix(c)
+    check_attention(o, lse, attend(c))
+
+
+@pytest.mark.parametrize("kv", [BF, F8])
+def test_shared_prefix_every_slot_empty_and_no_prefix(kv):
+    c = paged_case([0, 0, 0], 1, 16, kv, seed=12, prefix=128)
+    o, lse = _prefix(c)
+    check_attention(o, lse, attend(c))
+    c = paged_case([300, 5], 1, 16, kv, seed=13, prefix=0)
+    o, lse = _prefix(c)
+    check_attention(o, lse, attend(c))
+
+
+def test_shared_prefix_moving_maximum():
+    """Keys that grow along the prefix: the running maximum moves past the rescale threshold often."""
+    import torch
+    c = paged_case([1024 + 40, 1024 + 3], 1, 64, BF, seed=14, prefix=1024)
+    rows = c["cache"].view(torch.bfloat16).view(c["num_blocks"], PAGE, D)
+    for i, blk in enumerate(c["full_table"][0, :16]):
+        rows[int(blk)] *= 1.0 + i
+    o, lse = _prefix(c)
+    check_attention(o, lse, attend(c))
+
+
+def test_shared_prefix_equals_decode_at_scale():
+    """2048 rows of 16 heads over 16384 shared tokens: against the same call without sharing."""
+    import torch
+    import mla_latent_kv_gb300 as mla
+    B, H, prefix = 128, 16, 16384
+    c = paged_case([prefix + 1 + 7 * b for b in range(B)], 1, H, BF, seed=15, prefix=prefix)
+    st = _status()
+    o, lse = _prefix(c, status=st)
+    o2, lse2 = mla.decode(c["q"], c["cache"], dev(c["full_table"]), c["seq_lens"], c["max_len"], c["scale"],
+                          num_splits=-1, num_blocks=c["num_blocks"])
+    assert int(st.item()) == 0
+    # each side rounds its weights to bf16 (2^-8); over thousands of tokens of N(0, 1) values the
+    # sums |p| |v| + |o| stay below 2
+    assert (o - o2).abs().max().item() <= 2 * 2 * 2.0 ** -8
+    assert (lse - lse2).abs().max().item() <= 2 * (576 * 2.0 ** -24 * 40 + 2.0 ** -18 * 20)
+    assert torch.isfinite(o).all()
+
+
+def test_shared_prefix_bad_prefix_block_is_reported():
+    c = paged_case([200, 210], 1, 16, BF, seed=16, prefix=128)
+    c["table"][0, 1] = c["num_blocks"] + 3
+    st = _status()
+    _prefix(c, status=st)
+    assert int(st.item()) & 0x1
+
+
+def test_shared_prefix_workspace_is_checked():
+    import torch
+    import mla_latent_kv_gb300 as mla
+    c = paged_case([600, 610], 1, 128, BF, seed=17, prefix=512)
+    need = mla.decode_shared_prefix_workspace_bytes(2, 1, 128, 512, c["max_len"])
+    if need:
+        with pytest.raises(mla.MlaError) as e:
+            _prefix(c, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+        assert e.value.status == mla.ERR_WORKSPACE_TOO_SMALL
+    ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")  # NaN bytes
+    o, lse = _prefix(c, workspace=ws[:need])
+    check_attention(o, lse, attend(c))
+    assert bool((ws[need:] == 0xFF).all())
+
+
+# ------------------------------------------------------------------------------------ page keys
+@pytest.mark.parametrize("kv", [BF, F8])
+@pytest.mark.parametrize("lens,starts", [
+    ([1, 63, 64, 65, 0, 1000], None),
+    ([1, 64, 130, 700, 5, 0, 640], [0, 63, 129, 128, 5, 0, 639]),  # nothing new in the fifth
+    ([129, 200], [64, 250]),                                       # start past the length
+])
+def test_page_keys(kv, lens, starts):
+    import torch
+    import mla_latent_kv_gb300 as mla
+    c = paged_case(lens, 1, 1, kv, seed=30, extra_cols=2)
+    k, _ = keys_values(c)
+    start = [0] * len(lens) if starts is None else starts
+    max_new = max(0, max(n - s for n, s in zip(lens, start)))
+    keys = torch.full((c["num_blocks"], D), 7.0, dtype=torch.bfloat16, device="cuda")
+    st = _status()
+    out = mla.page_keys(c["cache"], c["table"], c["seq_lens"], max_new, kv_dtype=kv, page_keys=keys, dev_status=st,
+                        start_lens=None if starts is None else dev(np.asarray(starts, np.int32)),
+                        num_blocks=c["num_blocks"])
+    assert out is keys and int(st.item()) == 0
+    left = torch.ones(c["num_blocks"], dtype=torch.bool)
+    for b, n in enumerate(lens):
+        for p in range(start[b] // PAGE, -(-n // PAGE)) if n > start[b] else []:
+            blk = int(c["full_table"][b, p])
+            rows = k[blk, :min(PAGE, n - p * PAGE)]
+            want = rows.mean(0)
+            # 64 fp32 additions (and the FP8 format's product), one rounding to bf16
+            tol = 2.0 ** -8 * want.abs() + 66 * 2.0 ** -24 * rows.abs().mean(0)
+            assert bool(((keys[blk].double() - want).abs() <= tol).all()), (b, p)
+            left[blk] = False
+    assert bool((keys[left.cuda()] == 7.0).all())  # pages without new tokens keep their keys
+
+
+def test_page_keys_reports_bad_blocks_and_lengths():
+    import torch
+    import mla_latent_kv_gb300 as mla
+    c = paged_case([200, 100], 1, 1, BF, seed=31)
+    c["table"][1, 0] = -1
+    st = _status()
+    keys = mla.page_keys(c["cache"], c["table"], c["seq_lens"], 200, dev_status=st, num_blocks=c["num_blocks"])
+    assert int(st.item()) == mla.DEV_BAD_BLOCK_ID and torch.isfinite(keys).all()
+    st.zero_()
+    c = paged_case([200, 100], 1, 1, BF, seed=31)
+    mla.page_keys(c["cache"], c["table"], c["seq_lens"], 150, dev_status=st, num_blocks=c["num_blocks"])
+    assert int(st.item()) == mla.DEV_SEQ_TOO_LONG
+
+
+# ---------------------------------------------------------------------------------- page scores
+def _scores_ref(c, keys, b, t):
+    n = max(0, int(c["lens"][b]) - (c["Sq"] - 1 - t))
+    ids = [int(x) for x in c["full_table"][b, :-(-n // PAGE)]]
+    if not ids:
+        return None, None
+    k, q = keys[ids].double(), c["q"][b, t].double()
+    s = (q @ k.t() * c["scale"]).amax(0)
+    tol = 577 * 2.0 ** -24 * c["scale"] * (q.abs() @ k.abs().t()).amax(0) + 2.0 ** -24 * s.abs()
+    return s, tol
+
+
+@pytest.mark.parametrize("H", [1, 7, 16, 33, 100, 128])
+@pytest.mark.parametrize("Sq,lens", [(1, [0, 1, 64, 65, 5000]), (2, [1, 2, 8192, 8193, 128, 129])])
+def test_page_scores(H, Sq, lens):
+    import torch
+    import mla_latent_kv_gb300 as mla
+    c = paged_case(lens, Sq, H, BF, seed=50 + H)
+    rng = np.random.default_rng(51)
+    keys = bf16(mi.normal_bf16(rng, (c["num_blocks"], D), std=0.125))
+    st = _status()
+    s = mla.page_scores(c["q"], keys, c["table"], c["seq_lens"], c["max_len"], c["scale"], dev_status=st)
+    assert int(st.item()) == 0 and s.shape[2] == -(-c["max_len"] // PAGE)
+    for b in range(c["B"]):
+        for t in range(Sq):
+            want, tol = _scores_ref(c, keys, b, t)
+            m = 0 if want is None else want.numel()
+            if m:
+                assert bool(((s[b, t, :m].double() - want).abs() <= tol).all()), (b, t)
+            assert bool((s[b, t, m:] == -math.inf).all())
+
+
+def test_page_scores_nan_and_bad_blocks():
+    import torch
+    import mla_latent_kv_gb300 as mla
+    c = paged_case([640], 1, 20, BF, seed=60)
+    keys = bf16(mi.normal_bf16(np.random.default_rng(61), (c["num_blocks"], D)))
+    ids = c["full_table"][0]
+    keys[int(ids[3]), 100] = math.nan
+    keys[int(ids[4]), 5] = math.inf
+    c["table"][0, 7] = -5
+    st = _status()
+    s = mla.page_scores(c["q"], keys, c["table"], c["seq_lens"], c["max_len"], c["scale"], dev_status=st)[0, 0].cpu()
+    assert int(st.item()) == mla.DEV_BAD_BLOCK_ID
+    assert math.isnan(s[3]) and s[4] == math.inf and s[7] == -math.inf
+    assert torch.isfinite(s[[0, 1, 2, 5, 6, 8, 9]]).all()
+
+
+# --------------------------------------------------------------------------------------- select
+@pytest.mark.parametrize("K,sink,local", [(1, 0, 0), (1, 1, 0), (1, 0, 1), (4, 0, 0), (16, 1, 1), (16, 8, 8), (64, 2, 3)])
+@pytest.mark.parametrize("width", [1, 31, 64, 300, 2049, 5001])
+def test_select_pages(K, sink, local, width):
+    import torch
+    import mla_latent_kv_gb300 as mla
+    rng = np.random.default_rng(width * 100 + K)
+    Sq, B = 2, 7
+    lens = rng.integers(0, width * PAGE + 1, size=B)
+    lens[:3] = [width * PAGE, 0, 1]
+    s = rng.standard_normal((B, Sq, width)).astype(np.float32)
+    s[3] = np.round(s[3] * 2) / 2                       # many ties
+    s[4] = -1.5                                         # nothing but ties
+    s[5, :, ::3] = np.nan
+    s[5, :, 1::5] = -np.inf
+    s[6, :, ::4] = np.inf
+    s[6, :, 1::4] = 0.0
+    s[6, :, 2::4] = -0.0
+    st = _status()
+    pages = mla.select_pages(dev(s), dev(lens.astype(np.int32)), K, sink, local, dev_status=st).cpu().numpy()
+    assert int(st.item()) == 0
+    for b in range(B):
+        for t in range(Sq):
+            want = select_rule(s[b, t], max(0, int(lens[b]) - (Sq - 1 - t)), K, sink, local)
+            assert list(pages[b, t]) == want + [-1] * (K - len(want)), (b, t)
+
+
+def test_select_pages_widest_strided_and_too_long():
+    import torch
+    import mla_latent_kv_gb300 as mla
+    rng = np.random.default_rng(5)
+    wide = rng.standard_normal((1, 1, 49152)).astype(np.float32)
+    lens = dev(np.array([49152 * PAGE], np.int32))
+    got = mla.select_pages(dev(wide), lens, 100, 1, 1).cpu().numpy()[0, 0]
+    assert list(got) == select_rule(wide[0, 0], 49152 * PAGE, 100, 1, 1)
+    s = dev(rng.standard_normal((3, 1, 40)).astype(np.float32))[:, :, :20]  # rows 40 apart
+    st = _status()
+    lens = np.array([1000, 20 * PAGE, 20 * PAGE + 1], np.int32)
+    got = mla.select_pages(s, dev(lens), 5, 1, 1, dev_status=st).cpu().numpy()
+    assert int(st.item()) == mla.DEV_SEQ_TOO_LONG  # the third: cut at the scores' width
+    for b, n in enumerate([1000, 20 * PAGE, 20 * PAGE]):
+        assert list(got[b, 0]) == select_rule(s[b, 0].cpu().numpy(), n, 5, 1, 1)
+
+
+# --------------------------------------------------------------------------------- sparse decode
+def _pick(c, K, seed, gaps=False):
+    """Random ascending pages [B, Sq, K] and the lists they stand for; gaps: -1 between entries too."""
+    rng = np.random.default_rng(seed)
+    pages = np.full((c["B"], c["Sq"], K), -1, np.int32)
+    lists = []
+    for b in range(c["B"]):
+        lists.append([])
+        for t in range(c["Sq"]):
+            total = -(-max(0, int(c["lens"][b]) - (c["Sq"] - 1 - t)) // PAGE)
+            m = int(rng.integers(0, min(total, K) + 1)) if gaps else min(total, K)
+            ids = np.sort(rng.choice(total, m, replace=False)) if m else np.zeros(0, np.int64)
+            at = np.sort(rng.choice(K, m, replace=False)) if gaps else np.arange(m)
+            pages[b, t, at] = ids
+            lists[-1].append([int(x) for x in ids])
+    return pages, lists
+
+
+def _sparse(c, pages, num_splits=-1, status=None, **kw):
+    import mla_latent_kv_gb300 as mla
+    return mla.decode_sparse(c["q"], c["cache"], c["table"], c["seq_lens"], dev(pages), c["scale"], kv_dtype=c["kv"],
+                             num_splits=num_splits, dev_status=status, num_blocks=c["num_blocks"], **kw)
+
+
+@pytest.mark.parametrize("kv", [BF, F8])
+@pytest.mark.parametrize("num_splits", [1, 4, -1, -2])
+@pytest.mark.parametrize("Sq,H,K,lens", [
+    (1, 128, 6, [0, 1, 63, 64, 65, 700, 1000, 384]),
+    (2, 20, 1, [1, 2, 64, 65, 66, 300]),
+    (3, 16, 70, [5000, 200, 4]),       # more entries than a warp, more than one per row's pages
+])
+def test_sparse_decode(kv, num_splits, Sq, H, K, lens):
+    c = paged_case(lens, Sq, H, kv, seed=80 + K)
+    for gaps in (False, True):
+        pages, lists = _pick(c, K, 81, gaps)
+        st = _status()
+        o, lse = _sparse(c, pages, num_splits, st)
+        assert int(st.item()) == 0
+        check_attention(o, lse, attend(c, lists))
+
+
+def test_sparse_decode_many_rows_bf16_output():
+    import mla_latent_kv_gb300 as mla
+    lens = [1 + (37 * b) % 900 for b in range(100)]
+    c = paged_case(lens, 1, 16, BF, seed=90)
+    pages, lists = _pick(c, 5, 91, gaps=True)
+    o, lse = _sparse(c, pages, o_dtype=mla.DT_BF16)
+    check_attention(o, lse, attend(c, lists), bf16_out=True)
+
+
+def test_sparse_decode_of_all_pages_is_decode():
+    import torch
+    import mla_latent_kv_gb300 as mla
+    c = paged_case([700, 64, 1, 1000], 1, 64, BF, seed=92)
+    pages = np.full((4, 1, 16), -1, np.int32)
+    for b, n in enumerate(c["lens"]):
+        pages[b, 0, :-(-int(n) // PAGE)] = np.arange(-(-int(n) // PAGE))
+    o, lse = _sparse(c, pages, 1)
+    o2, lse2 = mla.decode(c["q"], c["cache"], c["table"], c["seq_lens"], c["max_len"], c["scale"], num_splits=1,
+                          num_blocks=c["num_blocks"])
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_sparse_decode_skips_and_reports_bad_entries():
+    """Out of order, twice, out of range, below -1: skipped and reported, the rest is attended to."""
+    import mla_latent_kv_gb300 as mla
+    c = paged_case([640] * 6, 1, 16, BF, seed=93)
+    rows = [([3, 3, 5, -1], [3, 5]), ([5, 2, 6, -1], [5, 6]), ([1, 10, 4, 9], [1, 4, 9]), ([-2, 0, 1, 2], [0, 1, 2]),
+            ([2147483647, 0, 9, 9], [0, 9]), ([4, 5, 6, 7], [4, 5, 6, 7])]
+    pages = np.array([[r[0]] for r in rows], np.int32)
+    st = _status()
+    o, lse = _sparse(c, pages, 2, st)
+    assert int(st.item()) == mla.DEV_BAD_PAGE
+    check_attention(o, lse, attend(c, [[r[1]] for r in rows]))
+
+
+# ------------------------------------------------------------------------------------- together
+@pytest.mark.parametrize("kv", [BF, F8])
+@pytest.mark.parametrize("stream", [False, True])
+def test_write_score_select_attend(kv, stream):
+    """A decode step over selected pages: write the new rows, refresh their pages' keys, score,
+    select, attend; eager, then captured in a graph and replayed after new inputs."""
+    import torch
+    import mla_latent_kv_gb300 as mla
+    lens = [3000, 64, 65, 1, 900, 2049]
+    B, H, K = len(lens), 32, 6
+    c = paged_case(lens, 1, H, kv, seed=95)
+    rng = np.random.default_rng(96)
+    slots = dev(np.array([int(c["full_table"][b, (n - 1) // PAGE]) * PAGE + (n - 1) % PAGE for b, n in enumerate(lens)],
+                         np.int64))
+    new_c, new_pe = bf16(mi.normal_bf16(rng, (B, 512))), bf16(mi.normal_bf16(rng, (B, 64)))
+    start = c["seq_lens"] - 1
+    keys = mla.page_keys(c["cache"], c["table"], c["seq_lens"], c["max_len"], kv_dtype=kv, num_blocks=c["num_blocks"])
+    scores = torch.empty((B, 1, -(-c["max_len"] // PAGE)), device="cuda")
+    pages = torch.empty((B, 1, K), dtype=torch.int32, device="cuda")
+    ws = torch.empty(mla.decode_sparse_workspace_bytes(B, 1, H, K, kv), dtype=torch.uint8, device="cuda")
+    o = torch.empty((B, 1, H, L), device="cuda")
+    lse = torch.empty((B, 1, H), device="cuda")
+    st = _status()
+
+    def step():
+        mla.cache_write(new_c, new_pe, slots, c["cache"], kv_dtype=kv, num_blocks=c["num_blocks"], dev_status=st)
+        mla.page_keys(c["cache"], c["table"], c["seq_lens"], 1, kv_dtype=kv, start_lens=start, page_keys=keys,
+                      num_blocks=c["num_blocks"], dev_status=st)
+        mla.page_scores(c["q"], keys, c["table"], c["seq_lens"], c["max_len"], c["scale"], scores=scores, dev_status=st)
+        mla.select_pages(scores, c["seq_lens"], K, pages=pages, dev_status=st)
+        mla.decode_sparse(c["q"], c["cache"], c["table"], c["seq_lens"], pages, c["scale"], kv_dtype=kv, workspace=ws,
+                          o_latent=o, lse=lse, num_blocks=c["num_blocks"], dev_status=st)
+
+    def check():
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0
+        sc = scores.cpu().numpy()
+        lists = [[select_rule(sc[b, 0], n, K, 1, 1)] for b, n in enumerate(lens)]
+        got = pages.cpu().numpy()
+        for b in range(B):
+            assert list(got[b, 0][got[b, 0] >= 0]) == lists[b][0]
+        k64, _ = keys_values(c)
+        for b, n in enumerate(lens):  # the refreshed page's key and its score
+            blk = int(c["full_table"][b, (n - 1) // PAGE])
+            rows = k64[blk, :(n - 1) % PAGE + 1]
+            tol = 2.0 ** -8 * rows.mean(0).abs() + 66 * 2.0 ** -24 * rows.abs().mean(0)
+            assert bool(((keys[blk].double() - rows.mean(0)).abs() <= tol).all())
+        check_attention(o, lse, attend(c, lists))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side if stream else torch.cuda.current_stream()):
+        step()
+        check()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        c["q"].copy_(bf16(mi.normal_bf16(rng, (B, 1, H, D))))
+        new_c.copy_(bf16(mi.normal_bf16(rng, (B, 512))))
+        o.zero_()
+        g.replay()
+        check()
+
+
+@pytest.mark.parametrize("kv", [BF, F8])
+def test_shared_prefix_step_in_a_graph(kv):
+    """absorb -> decode over the shared prefix -> out_proj captured, replayed after new queries, and
+    two captured calls that take turns on one workspace."""
+    import torch
+    import mla_latent_kv_gb300 as mla
+    B, H, prefix = 6, 64, 512
+    c = paged_case([prefix + s for s in (1, 70, 300, 64, 5, 129)], 1, H, kv, seed=97, prefix=prefix)
+    rng = np.random.default_rng(98)
+    e = mi.e2e_case(B, 1, H, [64] * B, seed=99)
+    qn, qp = bf16(e["q_nope"]).view(B, H, 128), bf16(e["q_pe"]).view(B, H, 64)
+    wk, wv = bf16(e["w_uk_t"]), bf16(e["w_uv"])
+    q2 = c["q"].view(B, H, D)
+    need = max(1, mla.decode_shared_prefix_workspace_bytes(B, 1, H, prefix, c["max_len"], kv))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    ol, lse = torch.empty((B, 1, H, L), device="cuda"), torch.empty((B, 1, H), device="cuda")
+    out = torch.empty((B, H, 128), device="cuda")
+
+    def step():
+        mla.absorb_q(qn, qp, wk, out=q2)
+        _prefix(c, workspace=ws, o_latent=ol, lse=lse)
+        mla.out_proj(ol.view(B, H, L), wv, out=out)
+
+    step()
+    torch.cuda.synchronize()
+    check_attention(ol, lse, attend(c))
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        step()
+    with torch.cuda.graph(g2):
+        step()
+    first = out.clone()
+    for g in (g1, g2, g1):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+    qn.copy_(bf16(mi.normal_bf16(rng, (B, H, 128))))
+    g2.replay()
+    torch.cuda.synchronize()
+    check_attention(ol, lse, attend(c))
+    assert not torch.equal(out, first)
