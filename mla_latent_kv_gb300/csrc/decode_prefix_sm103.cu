@@ -1,0 +1,730 @@
+// decode_prefix_sm103.cu -- the shared part of mla_decode_shared_prefix: every query row and head of
+// the batch against the prefix pages, which all requests have in common.
+//
+// For a flat row f = (request, query position, head) of the batch's R*H rows and a range of the
+// prefix tokens:  S = scale * q[f] K^T,  P = softmax(S),  o[f] = P V,  written as a partial state
+// (o, lse) that the merge combines with the other ranges and with the row's own tokens.
+//
+// What bounds it. With the keys common to all rows the work is a plain matrix product: 2 * 256 * 64 *
+// (576 + 512) flops per page and 256 rows, against 74 KB of keys that stay in L2. mla_decode's kernel
+// takes 128 rows at a time; every key byte is then written to shared memory once and read by the
+// tensor core once, and that traffic, not the tensor core, sets its pace (128 B/clk for full-rate
+// MMAs of M = 128). Here two SMs work as a pair on 256 rows (tcgen05 cta_group::2, M = 256): each SM
+// loads half of the keys and the tensor cores of both read both halves, which halves the
+// shared-memory traffic per flop.
+//
+// One cluster of four CTAs per (256 flat rows, range of pages); CTA i of a pair holds rows
+// [128 i, 128 i + 128):
+//   CTAs 0, 1 ("scores")  Q: 512 latent dims in tensor memory (256 columns), 64 rope dims in shared
+//       memory. Pages go two at a time ("groups" of 128 tokens): CTA i loads page 2 g + i, three
+//       64-dim panels (24 KB) per ring slot and TMA copy. S = Q K^T per group: 36 pair MMAs of
+//       M = 256 x N = 128 x K = 16 into one of two 128-column buffers, so that the next group's
+//       run while this one's softmax reads. Softmax: eight warps, two per TMEM lane quarter, one page
+//       of the group each; fp32 online softmax whose running maximum moves only when it grows by
+//       more than 2^8. One barrier a group tells whether any row's does; only then are the maxima
+//       of the two halves exchanged. P (bf16, swizzled) and the rows' rescale factors are staged
+//       and sent to the output CTA of the same rows with one bulk copy per page.
+//   CTAs 2, 3 ("output")  hold the 256 x 512 fp32 output accumulators (all of both SMs' tensor
+//       memory). CTA i loads dims [128 i, 128 i + 128) and [256 + 128 i, ...) of each page; per page
+//       8 pair MMAs of M = 256 x N = 256 x K = 16, V read as an MN-major operand from the TMA tile.
+//       Helper warps rescale O when a group's maximum moved. Epilogue: fp32 O / l by TMA stores.
+//
+// Rounding: P to bf16 (the MMA's operand), 2^-8 relative per weight at most; the sums l that normalise
+// O and give the LSE are of the unrounded fp32 weights.
+//
+// FP8 cache: the prefix is widened once per call to bf16 (exactly: e4m3 codes are bf16 values) into the
+// workspace; k_scale multiplies the fp32 scores and v_scale the weights before their rounding.
+//
+// All waits are bounded (see sm103_ptx.cuh); on a timeout the kernel winds down and reports
+// MLA_DEV_WAIT_TIMEOUT instead of hanging.
+#include <cuda.h>
+#include <math_constants.h>
+
+#include <cstring>
+
+#include "decode_common.cuh"
+#include "internal.h"
+#include "sm103_ptx.cuh"
+
+namespace mla {
+
+cudaError_t encode_tmap(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const void* base,
+                        const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box, bool swizzle128);
+
+namespace {
+
+using namespace ptx;
+using dec::warp_wait;
+
+constexpr int kThreads = 320;  // warp 0 TMA, warp 1 MMA, warps 2-9 softmax / 2-5 helpers, 2-9 epilogue
+constexpr int kTileRows = 256;
+constexpr int kPPG = 2;                      // pages per group, one per scores CTA
+constexpr int kPageBox = kPage * 128;        // one page's rows of one 64-dim panel (8 KB)
+constexpr int kSlotPanels = 3;
+constexpr int kSlotBytes = kSlotPanels * kPageBox;  // 24 KB
+constexpr int kSlots = 7;                    // K ring of a scores CTA
+constexpr int kQPanelBytes = 128 * 128;      // 128 rows x 64 dims of Q (16 KB)
+constexpr int kPBufs = 5;                    // P buffers of an output CTA (one page each)
+constexpr int kVStages = 4;                  // V ring of an output CTA: a page's 4 panels each
+constexpr int kVStageBytes = 4 * kPageBox;   // 32 KB
+constexpr int kPBytes = 128 * 128;           // P page: 128 rows x 64 tokens bf16
+constexpr int kPMsgBytes = (kPBytes + 512 + 4 + 15) / 16 * 16;  // P + alpha[128] + flag
+constexpr int kPBufStride = 17 * 1024;
+constexpr int kCtrlBytes = 4096;
+// scores CTA
+constexpr int OFF_QROPE = kCtrlBytes;
+constexpr int OFF_RING = OFF_QROPE + kQPanelBytes;
+constexpr int OFF_STAGE = OFF_RING + kSlots * kSlotBytes;  // two P staging buffers, one per half
+constexpr int kSmem0 = OFF_STAGE + 2 * kPBufStride;
+// output CTA
+constexpr int OFF_V = kCtrlBytes;
+constexpr int OFF_PB = OFF_V + kVStages * kVStageBytes;
+constexpr int kSmem1 = OFF_PB + kPBufs * kPBufStride;
+constexpr int kSmemBytes = kSmem0 > kSmem1 ? kSmem0 : kSmem1;
+static_assert(kSmemBytes <= 232448, "over the per-CTA shared memory limit");
+static_assert(kPMsgBytes <= kPBufStride, "P message");
+static_assert(OFF_RING % 1024 == 0 && OFF_STAGE % 1024 == 0 && OFF_PB % 1024 == 0 && kPBufStride % 1024 == 0 &&
+                  kSlotBytes % 1024 == 0,
+              "128-byte swizzled tiles need 1024-byte alignment");
+static_assert(8 * 128 * 128 <= kSmem1 - OFF_V, "epilogue tiles");
+// Q's latent panels land in the two staging buffers (panels 0, 1) and ring slots 3-6 (panels 2-7),
+// so that the first page's keys can load into slots 0-2 at once.
+static_assert(kSlots == 7 && 6 * kQPanelBytes == 4 * kSlotBytes, "Q panel homes");
+__device__ __forceinline__ uint32_t q_panel_off(int pn) {
+    return pn < 2 ? OFF_STAGE + pn * kPBufStride : OFF_RING + 3 * kSlotBytes + (pn - 2) * kQPanelBytes;
+}
+
+// Barrier slots, one layout for all four CTAs (multicast commits land at the same offset in each).
+enum : int {
+    B_SLOTFULL = 0,                     // [kSlots] CTA 0: slot landed in both scores CTAs (TMA tx)
+    B_SLOTEMPTY = B_SLOTFULL + kSlots,  // [kSlots] CTAs 0, 1: slot's QK MMAs completed
+    B_SFULL = B_SLOTEMPTY + kSlots,     // [2] CTAs 0, 1: S buffer ready
+    B_SEMPTY = B_SFULL + 2,             // [2] CTA 0: S buffer read by the 16 softmax warps of the pair
+    B_QFULL = B_SEMPTY + 2,             // CTAs 0, 1: Q landed in shared memory
+    B_QREADY,                           // CTAs 0, 1: Q latent dims moved to TMEM (256 threads)
+    B_QPEER,                            // CTA 0: CTA 1's Q moved
+    B_STAGEFREE,                        // [2] CTAs 0, 1: staging buffer's copy has landed
+    B_PEMPTY = B_STAGEFREE + 2,         // [kPBufs] all: PV MMAs of the page in P buffer b completed
+    B_VFULL = B_PEMPTY + kPBufs,        // [kVStages] CTA 2: V stage landed in both output CTAs
+    B_VEMPTY = B_VFULL + kVStages,      // [kVStages] CTAs 2, 3: V stage consumed
+    B_PFULL = B_VEMPTY + kVStages,      // [kPBufs] CTAs 2, 3: P message landed
+    B_READY = B_PFULL + kPBufs,         // [kPBufs] CTA 2: the 8 helper warps of the pair are done with the page
+    B_STATS = B_READY + kPBufs,         // CTAs 2, 3: final row statistics written
+    B_COUNT
+};
+static_assert(8 * B_COUNT <= 512, "barrier slots");
+constexpr int OFF_TMEM = 512;
+constexpr int OFF_ABORT = 516;
+constexpr int OFF_MX = 1024;      // scores: f32 [2][128] exchange between the two halves
+constexpr int OFF_STAT_M = 2048;  // output: f32 [128] final running max (log2 units)
+constexpr int OFF_STAT_L = 2560;  // output: f32 [128] row sum
+
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kSCol = 256;  // scores: Q latent in columns [0, 256), S buffers at 256 and 384
+constexpr uint32_t kIdescQK = idesc_bf16_f32(256, 128, false, false);
+constexpr uint32_t kIdescPV = idesc_bf16_f32(256, 256, false, true);
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr uint32_t kBarMax = 1, kBarOr = 2, kBarHalf0 = 3, kBarEpi = 4, kBarStage0 = 5;
+constexpr int kEpiPanelBytes = 128 * 128;
+
+template <bool kScaled>
+__global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
+    decode_prefix_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                         const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap o_map,
+                         const PrefixArgs p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = smem_addr(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int side = (int)(rank & 1);  // which half of the tile's rows
+    const bool scores = rank < 2;
+    if (sbase & 1023u) {  // the swizzled layouts need 1024-byte aligned tiles; never expected
+        if (tid == 0 && p.dev_status) atomicOr(p.dev_status, MLA_DEV_WAIT_TIMEOUT);
+        return;  // all CTAs of the cluster see the same alignment and leave together
+    }
+    const int unit = (int)(blockIdx.x >> 2);
+    const int tile = unit / p.splits, split = unit % p.splits;
+    const int page0 = min(p.prefix_pages, split * p.pages_per_split);
+    const int npages = min(p.prefix_pages, page0 + p.pages_per_split) - page0;
+    const int ngroups = (npages + kPPG - 1) / kPPG;
+    const int rows0 = tile * kTileRows + 128 * side;  // first flat row of this CTA
+    volatile int* abort = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
+    int32_t* ds = p.dev_status;
+    auto bar = [&](int i) -> uint32_t { return sbase + 8u * (uint32_t)i; };
+
+    if (tid == 0) {
+        *abort = 0;
+        for (int i = 0; i < B_COUNT; ++i) {
+            uint32_t cnt = 1;
+            if (i >= B_SEMPTY && i < B_SEMPTY + 2) cnt = 16;
+            if (i == B_QREADY) cnt = 256;
+            if (i >= B_READY && i < B_READY + kPBufs) cnt = 8;
+            bar_init(bar(i), cnt);
+        }
+        if (!scores)  // P buffers armed for their first message before a scores CTA can send one
+            for (int b = 0; b < kPBufs; ++b) bar_arrive_expect_tx(bar(B_PFULL + b), kPMsgBytes);
+        fence_barrier_init();
+    }
+    if (warp == 0) {
+        tmem_alloc_pair(sbase + OFF_TMEM, kTmemCols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    cluster_sync();  // every CTA's barriers exist before any remote arrive or copy
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM);
+    griddep_wait();  // q, the cache and the lengths may be earlier kernels' outputs
+    if (tid == 0) griddep_launch_dependents();
+
+    // First cache row of the unit's page i (out of range: TMA fills zeros).
+    auto page_row = [&](int i) -> int {
+        if (i >= npages) return p.key_rows;
+        if (!p.block_table) return (page0 + i) * kPage;  // widened prefix: its pages in order
+        const int32_t blk = p.block_table[page0 + i];
+        if (blk < 0 || (int64_t)blk >= p.num_blocks) {
+            if (ds) atomicOr(ds, MLA_DEV_BAD_BLOCK_ID);
+            return p.key_rows;
+        }
+        return blk * kPage;
+    };
+
+    if (scores) {
+        if (warp == 0) {
+            if (lane == 0 && npages > 0) {
+                tma_prefetch_desc(&k_map);
+                tma_prefetch_desc(&q_map);
+                bar_arrive_expect_tx(bar(B_QFULL), 9 * kQPanelBytes);
+                for (int qn = 0; qn < 8; ++qn)
+                    tma_load_2d(sbase + q_panel_off(qn), &q_map, bar(B_QFULL), qn * 64, rows0);
+                tma_load_2d(sbase + OFF_QROPE, &q_map, bar(B_QFULL), 8 * 64, rows0);
+                int issued = 0;
+                bool ok = true;
+                for (int gi = 0; gi < ngroups && ok; ++gi) {
+                    const int y = page_row(kPPG * gi + side);
+                    for (int t = 0; t < 3; ++t) {
+                        const int m = 3 * gi + t, slot = m % kSlots, k = m / kSlots;
+                        // first use of slots 3-6: Q's panels have been moved out to TMEM
+                        ok = k > 0       ? wait_bar<true>(bar(B_SLOTEMPTY + slot), (k - 1) & 1, abort, ds)
+                             : slot >= 3 ? wait_bar(bar(B_QREADY), 0, abort, ds)
+                                         : true;
+                        if (!ok) break;
+                        // both CTAs' bytes are counted on CTA 0's barrier
+                        if (side == 0) bar_arrive_expect_tx(bar(B_SLOTFULL + slot), 2 * kSlotBytes);
+                        tma_load_3d_pair(sbase + OFF_RING + slot * kSlotBytes, &k_map,
+                                         map_to_rank(bar(B_SLOTFULL + slot), 0), 0, y, kSlotPanels * t);
+                        ++issued;
+                    }
+                }
+                // Teardown: the MMAs have consumed the last slots, so every copy has landed and no
+                // commit is still on its way here.
+                for (int m = (issued > kSlots ? issued - kSlots : 0); m < issued; ++m) {
+                    volatile int dummy = 0;
+                    wait_bar<true>(bar(B_SLOTEMPTY + m % kSlots), (m / kSlots) & 1, *abort ? &dummy : abort, ds);
+                }
+            }
+        } else if (warp == 1) {
+            if (lane == 0 && npages > 0 && side == 1) {
+                // tell the issuing CTA that this CTA's half of Q is in place
+                wait_bar(bar(B_QREADY), 0, abort, ds);
+                tc_fence_after();
+                tc_fence_before();
+                bar_arrive_remote(bar(B_QPEER), 0);
+            }
+            if (lane == 0 && npages > 0 && side == 0) {
+                bool ok = wait_bar(bar(B_QREADY), 0, abort, ds) && wait_bar<true>(bar(B_QPEER), 0, abort, ds);
+                if (ok) tc_fence_after();
+                for (int gi = 0; gi < ngroups && ok; ++gi) {
+                    const int buf = gi & 1, use = gi >> 1;
+                    if (use > 0) {  // both CTAs' softmax warps have read the buffer's previous S
+                        if (!(ok = wait_bar<true>(bar(B_SEMPTY + buf), (use - 1) & 1, abort, ds))) break;
+                        tc_fence_after();
+                    }
+                    const uint32_t d = tmem + kSCol + 128u * buf;
+                    for (int t = 0; t < 3; ++t) {
+                        const int m = 3 * gi + t, slot = m % kSlots, k = m / kSlots;
+                        if (!(ok = wait_bar<true>(bar(B_SLOTFULL + slot), k & 1, abort, ds))) break;
+                        const uint32_t kb = sbase + OFF_RING + slot * kSlotBytes;
+#pragma unroll
+                        for (int q = 0; q < kSlotPanels; ++q) {
+                            const int pn = kSlotPanels * t + q;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint64_t bd = smem_desc_sw128(kb + q * kPageBox + 32 * j, 16, 1024);
+                                if (pn < 8) {
+                                    mma_pair_ts(d, tmem + 8u * (4 * pn + j), bd, kIdescQK, (pn | j) ? 1u : 0u);
+                                } else {
+                                    const uint64_t ad = smem_desc_sw128(sbase + OFF_QROPE + 32 * j, 16, 1024);
+                                    mma_pair_ss(d, ad, bd, kIdescQK, 1u);
+                                }
+                            }
+                        }
+                        mma_pair_commit(bar(B_SLOTEMPTY + slot), 0x3);
+                    }
+                    if (ok) mma_pair_commit(bar(B_SFULL + buf), 0x3);
+                }
+            }
+        } else {
+            // ------------------------- softmax warps (256 threads) -------------------------
+            const int half = (warp - 2) >> 2;  // page `half` of each group
+            const int row = 32 * (warp & 3) + lane;
+            const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+            float* mx = reinterpret_cast<float*>(smem + OFF_MX);
+            // Tokens of this unit that the row may see (rows past the batch see all: never stored).
+            int lim = INT32_MAX;
+            const int64_t flat = (int64_t)rows0 + row;
+            if (flat < p.flat_rows) {
+                const int r = (int)(flat / p.H), b = r / p.Sq, t = r % p.Sq;
+                const int seq = min(max(p.seq_lens[b], 0), p.max_seq_len);
+                lim = max(0, seq - (p.Sq - 1 - t)) - page0 * kPage;
+            }
+            const int warp_lim = __reduce_min_sync(0xffffffffu, lim);
+            if (npages > 0) {
+                // Q latent dims: this half moves panels 4 half .. 4 half + 3 into TMEM
+                const bool okq = warp_wait(bar(B_QFULL), 0, abort, ds);
+#pragma unroll 1
+                for (int pn = 4 * half; pn < 4 * half + 4; ++pn) {
+                    uint32_t v[32];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        uint4 x = make_uint4(0, 0, 0, 0);
+                        if (okq)
+                            x = *reinterpret_cast<const uint4*>(smem + q_panel_off(pn) + row * 128 +
+                                                                ((c ^ (row & 7)) << 4));
+                        v[4 * c] = x.x;
+                        v[4 * c + 1] = x.y;
+                        v[4 * c + 2] = x.z;
+                        v[4 * c + 3] = x.w;
+                    }
+                    tmem_st32(tmem + lane_base + 32u * pn, v);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                bar_arrive(bar(B_QREADY));
+            }
+            const float sl2 = p.scale * 1.4426950408889634f;  // exp2 domain
+            float m_run = -CUDART_INF_F, l_run = 0.f;          // each half keeps its own sum
+            const uint32_t out_rank = 2u + (uint32_t)side;
+            const uint32_t pbuf_remote = map_to_rank(sbase + OFF_PB, out_rank);
+            const uint32_t pfull_remote = map_to_rank(bar(B_PFULL), out_rank);
+            uint8_t* stage = smem + OFF_STAGE + half * kPBufStride;
+            const int htid = tid - 64 - 128 * half;
+            for (int gi = 0; gi < ngroups; ++gi) {
+                // No early exit from this loop: all 256 threads must pass the same named barriers
+                // (which cannot time out); after an abort the waits return at once.
+                const int page = kPPG * gi + half, buf = gi & 1;
+                const bool okS = warp_wait<true>(bar(B_SFULL + buf), (gi >> 1) & 1, abort, ds);
+                uint32_t s[2][32];
+                if (okS) {
+                    tc_fence_after();
+                    const uint32_t scol = tmem + lane_base + kSCol + 128u * buf + 64u * half;
+                    tmem_ld32(scol, s[0]);
+                    tmem_ld32(scol + 32u, s[1]);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive_remote(bar(B_SEMPTY + buf), 0);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) s[c][j] = __float_as_uint(-CUDART_INF_F);
+                }
+                const float4* sc = nullptr;  // (k_scale, v_scale) of two tokens each
+                if constexpr (kScaled) {
+                    sc = reinterpret_cast<const float4*>(p.scales + (size_t)(page0 + min(page, npages - 1)) * kPage);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float4 x = __ldg(sc + 16 * c + j);
+                            s[c][2 * j] = __float_as_uint(__uint_as_float(s[c][2 * j]) * x.x);
+                            s[c][2 * j + 1] = __float_as_uint(__uint_as_float(s[c][2 * j + 1]) * x.z);
+                        }
+                }
+                if (page >= npages || warp_lim < (page + 1) * kPage) {  // some row does not see all of the page
+                    const int v = page >= npages ? 0 : lim - page * kPage;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (32 * c + j >= v) s[c][j] = __float_as_uint(-CUDART_INF_F);
+                }
+                float lm4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) lm4[j & 3] = fmaxf(lm4[j & 3], __uint_as_float(s[c][j]));
+                const float lm = fmaxf(fmaxf(lm4[0], lm4[1]), fmaxf(lm4[2], lm4[3]));
+                // Does any of the 256 rows x halves pass the threshold? The barrier also keeps the
+                // next exchange's writes of mx behind this one's reads.
+                const bool any = named_bar_or(kBarOr, 256, lm * sl2 > m_run + kRescaleThreshold);
+                float alpha = 1.f;
+                if (any) {
+                    mx[half * 128 + row] = lm;
+                    named_bar(kBarMax, 256);
+                    const float mt = fmaxf(lm, mx[(1 - half) * 128 + row]) * sl2;  // scale > 0
+                    if (mt > m_run + kRescaleThreshold) {
+                        alpha = fast_exp2(m_run - mt);  // 0 while m_run = -inf
+                        m_run = mt;
+                    }
+                    l_run *= alpha;
+                }
+                const float mref = m_run == -CUDART_INF_F ? 0.f : m_run;  // nothing seen yet: weights 0
+                uint32_t pk[32];
+                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float a0 = fast_exp2(fmaf(__uint_as_float(s[c][2 * j]), sl2, -mref));
+                        float a1 = fast_exp2(fmaf(__uint_as_float(s[c][2 * j + 1]), sl2, -mref));
+                        l4[2 * (j & 1)] += a0;
+                        l4[2 * (j & 1) + 1] += a1;
+                        if constexpr (kScaled) {
+                            const float4 x = __ldg(sc + 16 * c + j);
+                            a0 *= x.y;
+                            a1 *= x.w;
+                        }
+                        pk[16 * c + j] = pack_bf16x2(a0, a1);
+                    }
+                l_run += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                if (page < npages) {  // a page past the end sends nothing
+                    // the staging buffer is free once the previous group's copy has landed
+                    if (gi > 0) warp_wait<true>(bar(B_STAGEFREE + half), (gi - 1) & 1, abort, ds);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        *reinterpret_cast<uint4*>(stage + row * 128 + ((c ^ (row & 7)) << 4)) =
+                            make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+                    // the group's first page carries the rescale that O needs before it
+                    reinterpret_cast<float*>(stage + kPBytes)[row] = alpha;
+                    if (row == 0)
+                        *reinterpret_cast<uint32_t*>(stage + kPBytes + 512) = (half == 0 && any && gi > 0) ? 1u : 0u;
+                    fence_proxy_async_cta();  // generic writes before the bulk copy reads them
+                }
+                named_bar(kBarStage0 + half, 128);
+                if (htid == 0 && page < npages && okS) {
+                    const int pb = page % kPBufs, up = page / kPBufs;
+                    if (up == 0 || wait_bar<true>(bar(B_PEMPTY + pb), (up - 1) & 1, abort, ds))
+                        bulk_copy_to_peer(pbuf_remote + pb * kPBufStride, sbase + OFF_STAGE + half * kPBufStride,
+                                          kPMsgBytes, pfull_remote + 8u * pb);
+                }
+            }
+            // combine the two halves' sums, ship the final statistics
+            named_bar(kBarMax, 256);
+            if (half == 1) mx[row] = l_run;
+            named_bar(kBarMax, 256);
+            if (half == 0) {
+                l_run += mx[row];
+                st_cluster_u32(map_to_rank(sbase + OFF_STAT_M, out_rank) + 4u * row, __float_as_uint(m_run));
+                st_cluster_u32(map_to_rank(sbase + OFF_STAT_L, out_rank) + 4u * row, __float_as_uint(l_run));
+                named_bar(kBarHalf0, 128);
+                if (tid == 64) {
+                    bar_arrive_remote(bar(B_STATS), out_rank);
+                    // nothing may still be on its way to this CTA when it exits: the last
+                    // multicast commits of the output pair
+                    for (int pg = (npages > kPBufs ? npages - kPBufs : 0); pg < npages; ++pg) {
+                        volatile int dummy = 0;
+                        wait_bar<true>(bar(B_PEMPTY + pg % kPBufs), (pg / kPBufs) & 1, *abort ? &dummy : abort, ds);
+                    }
+                }
+            }
+        }
+    } else {
+        // ============================== output CTAs ==============================
+        if (warp == 0) {
+            if (lane == 0 && npages > 0) {
+                tma_prefetch_desc(&v_map);
+                int issued = 0;
+                for (int i = 0; i < npages; ++i) {
+                    const int y = page_row(i);
+                    const int st = i % kVStages, k = i / kVStages;
+                    if (k > 0 && !wait_bar<true>(bar(B_VEMPTY + st), (k - 1) & 1, abort, ds)) break;
+                    if (side == 0) bar_arrive_expect_tx(bar(B_VFULL + st), 2 * kVStageBytes);
+                    const uint32_t full = map_to_rank(bar(B_VFULL + st), 2);
+                    const uint32_t dst = sbase + OFF_V + st * kVStageBytes;
+                    tma_load_3d_pair(dst, &v_map, full, 0, y, 2 * side);
+                    tma_load_3d_pair(dst + 2 * kPageBox, &v_map, full, 0, y, 4 + 2 * side);
+                    issued = i + 1;
+                }
+                for (int i = (issued > kVStages ? issued - kVStages : 0); i < issued; ++i) {  // teardown, as above
+                    volatile int dummy = 0;
+                    wait_bar<true>(bar(B_VEMPTY + i % kVStages), (i / kVStages) & 1, *abort ? &dummy : abort, ds);
+                }
+            }
+        } else if (warp == 1) {
+            if (lane == 0) {
+                if (side == 0) {
+                    bool ok = true;
+                    for (int i = 0; i < npages && ok; ++i) {
+                        const int pb = i % kPBufs, st = i % kVStages;
+                        if (!(ok = wait_bar<true>(bar(B_READY + pb), (i / kPBufs) & 1, abort, ds))) break;
+                        if (!(ok = wait_bar<true>(bar(B_VFULL + st), (i / kVStages) & 1, abort, ds))) break;
+                        tc_fence_after();  // after a rescale by the helper warps' tcgen05.st
+                        const uint32_t pbuf = sbase + OFF_PB + pb * kPBufStride;
+                        const uint32_t vb = sbase + OFF_V + st * kVStageBytes;
+#pragma unroll
+                        for (int kk = 0; kk < kPage / 16; ++kk) {
+                            const uint64_t ad = smem_desc_sw128(pbuf + kk * 32, 16, 1024);
+#pragma unroll
+                            for (int nh = 0; nh < 2; ++nh) {
+                                const uint64_t bd =
+                                    smem_desc_sw128(vb + nh * 2 * kPageBox + kk * 2048, kPageBox, 1024);
+                                mma_pair_ss(tmem + 256u * nh, ad, bd, kIdescPV, (i > 0 || kk > 0) ? 1u : 0u);
+                            }
+                        }
+                        mma_pair_commit(bar(B_VEMPTY + st), 0xC);
+                        mma_pair_commit(bar(B_PEMPTY + pb), 0xF);
+                    }
+                }
+                // teardown: the last commits have landed in this CTA
+                for (int pg = (npages > kPBufs ? npages - kPBufs : 0); pg < npages; ++pg) {
+                    volatile int dummy = 0;
+                    wait_bar<true>(bar(B_PEMPTY + pg % kPBufs), (pg / kPBufs) & 1, *abort ? &dummy : abort, ds);
+                }
+            }
+        } else {
+            // ------------- helper warps 2-5: P arrival, rescale; warps 2-9: the epilogue -------------
+            const int row = 32 * (warp & 3) + lane;
+            const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+            const int ctid = tid - 64;  // 0..255; 0..127 are the helper warps
+            const int eset = warp >= 6 ? 1 : 0;
+            int pages_ready = warp >= 6 ? npages : 0;
+            for (int i = 0; i < npages && warp < 6; ++i) {
+                const int pb = i % kPBufs;
+                if (!warp_wait<true>(bar(B_PFULL + pb), (i / kPBufs) & 1, abort, ds)) break;
+                if (ctid == 0) {
+                    bar_arrive_expect_tx(bar(B_PFULL + pb), kPMsgBytes);           // re-arm for the next message
+                    bar_arrive_remote(bar(B_STAGEFREE + (i & 1)), (uint32_t)side);  // the sender's staging buffer
+                }
+                const uint8_t* pmsg = smem + OFF_PB + pb * kPBufStride;
+                const bool fix = i > 0 && *reinterpret_cast<const volatile uint32_t*>(pmsg + kPBytes + 512) != 0;
+                if (fix) {  // O must hold every earlier PV product before it is rescaled
+                    if (!warp_wait<true>(bar(B_PEMPTY + (i - 1) % kPBufs), ((i - 1) / kPBufs) & 1, abort, ds)) break;
+                    tc_fence_after();
+                    const float a = reinterpret_cast<const volatile float*>(pmsg + kPBytes)[row];
+#pragma unroll 1
+                    for (int c = 0; c < kL / 32; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32(tmem + lane_base + 32u * c, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * a);
+                        tmem_st32(tmem + lane_base + 32u * c, v);
+                    }
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                // P came through the async proxy into this CTA and is read by MMAs that CTA 2
+                // issues: it is made visible along this warp's arrival
+                fence_proxy_async_cta();
+                __syncwarp();
+                if (lane == 0) bar_arrive_remote(bar(B_READY + pb), 2);
+                pages_ready = i + 1;
+            }
+            const bool has_o = npages > 0 && pages_ready == npages && !*abort;
+            wait_bar<true>(bar(B_STATS), 0, abort, ds);
+            const bool o_ok = has_o && wait_bar<true>(bar(B_PEMPTY + (npages - 1) % kPBufs),
+                                                      ((npages - 1) / kPBufs) & 1, abort, ds);
+            tc_fence_after();
+            const float m = reinterpret_cast<volatile float*>(smem + OFF_STAT_M)[row];
+            const float l = reinterpret_cast<volatile float*>(smem + OFF_STAT_L)[row];
+            const bool use_o = __all_sync(0xffffffffu, o_ok);
+            const bool empty = !use_o || !(l > 0.f);
+            const float inv = empty ? 0.f : 1.f / l;
+            const int64_t flat = (int64_t)rows0 + row;
+            if (eset == 0 && flat < p.flat_rows)
+                p.part_lse[(size_t)split * p.flat_rows + flat] =
+                    empty ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
+            // O / l leaves through TMA stores, as in the decode kernel: two rounds of eight
+            // 32-column panels over the V ring, rows past the batch cut off by the tensor map
+            for (int rd = 0; rd < 2; ++rd) {
+                if (rd > 0) {  // the previous round's stores have read their tiles
+                    if (ctid == 0) bulk_wait_group_read<0>();
+                    named_bar(kBarEpi, 256);
+                }
+                uint32_t v[4][32];
+                if (use_o) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        tmem_ld32(tmem + lane_base + (uint32_t)(rd * 256 + (4 * eset + q) * 32), v[q]);
+                    tmem_wait_ld();
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint8_t* out = smem + OFF_V + (4 * eset + q) * kEpiPanelBytes;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);  // an empty row: also where O holds garbage
+                        if (!empty)
+                            x = make_float4(__uint_as_float(v[q][4 * c]) * inv, __uint_as_float(v[q][4 * c + 1]) * inv,
+                                            __uint_as_float(v[q][4 * c + 2]) * inv,
+                                            __uint_as_float(v[q][4 * c + 3]) * inv);
+                        *reinterpret_cast<float4*>(out + row * 128 + ((c ^ (row & 7)) << 4)) = x;
+                    }
+                }
+                fence_proxy_async_cta();
+                named_bar(kBarEpi, 256);
+                if (ctid == 0 && rows0 < p.flat_rows) {
+                    for (int pl = 0; pl < 8; ++pl)
+                        tma_store_3d(&o_map, sbase + OFF_V + pl * kEpiPanelBytes, rd * 256 + pl * 32, rows0, split);
+                    bulk_commit_group();
+                }
+            }
+            if (ctid == 0) bulk_wait_group<0>();  // the stores are complete before the CTA exits
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 0) tmem_dealloc_pair(tmem, kTmemCols);
+    cluster_sync();
+}
+
+// ------------------------------------------------------------------------------------------
+// FP8 prefix -> bf16 rows (exact) and scales, once per call. One warp per token: lanes take
+// 8-byte chunks of the 576 codes.
+// ------------------------------------------------------------------------------------------
+__global__ void __launch_bounds__(256) prefix_widen_kernel(PrefixArgs p, const uint8_t* cache, uint16_t* x,
+                                                           float2* scales) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int token = (int)blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (token >= p.prefix_pages * kPage) return;
+    const int32_t blk = p.block_table[token / kPage];
+    const bool bad = blk < 0 || (int64_t)blk >= p.num_blocks;
+    if (bad && lane == 0 && p.dev_status) atomicOr(p.dev_status, MLA_DEV_BAD_BLOCK_ID);
+    const uint8_t* src = cache + ((size_t)(bad ? 0 : blk) * kPage + token % kPage) * kFp8RowBytes;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const int c = lane + 32 * i;
+        if (c >= kD / 8) continue;
+        uint2 v = make_uint2(0u, 0u);
+        if (!bad) v = *reinterpret_cast<const uint2*>(src + 8 * c);
+        *reinterpret_cast<uint4*>(x + (size_t)token * kD + 8 * c) =
+            make_uint4(e4m3x2_to_bf16x2(v.x & 0xffffu), e4m3x2_to_bf16x2(v.x >> 16), e4m3x2_to_bf16x2(v.y & 0xffffu),
+                       e4m3x2_to_bf16x2(v.y >> 16));
+    }
+    if (lane == 0) scales[token] = bad ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2*>(src + kD);
+}
+
+int g_attr_done[2][64] = {};
+int g_clusters[64] = {};
+
+cudaError_t set_attr(int dev, bool scaled) {
+    if (dev < 64 && g_attr_done[scaled][dev]) return cudaSuccess;
+    const cudaError_t e =
+        scaled ? cudaFuncSetAttribute(decode_prefix_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes)
+               : cudaFuncSetAttribute(decode_prefix_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e == cudaSuccess && dev < 64) g_attr_done[scaled][dev] = 1;
+    return e;
+}
+
+}  // namespace
+
+int prefix_clusters() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+    if (dev < 64 && g_clusters[dev] > 0) return g_clusters[dev];
+    if (set_attr(dev, false) != cudaSuccess) return -1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(4);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 4;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, decode_prefix_kernel<false>, &cfg) != cudaSuccess || n < 1) return -1;
+    if (dev < 64) g_clusters[dev] = n;
+    return n;
+}
+
+// The split of a prefix of `pages` pages over `flat_rows` rows: S ranges of an even number of pages.
+void prefix_split(int64_t flat_rows, int pages, int clusters, int* splits, int* pages_per_split) {
+    // Time of S splits: waves of clusters, each a range of pages and a fixed part, and the partial
+    // states written and read back. In page-times of one cluster (about 0.9 us).
+    constexpr double kUnitPages = 14.0;
+    const int64_t tiles = (flat_rows + kTileRows - 1) / kTileRows;
+    const double partial = (double)flat_rows * (kL + 1) * 8.0 / 5.0e6 / 0.9;  // bytes / (bytes per page-time)
+    double best = 1e300;
+    *splits = 1;
+    *pages_per_split = (pages + 1) / 2 * 2;
+    for (int S = 1; S <= (pages + 1) / 2 && S <= 4096; ++S) {
+        const int per = ((pages + S - 1) / S + 1) / 2 * 2;
+        const int used = (pages + per - 1) / per;  // ranges that hold pages
+        if (used < S && S > 1) continue;
+        const int64_t waves = (tiles * S + clusters - 1) / clusters;
+        const double t = (double)waves * (per + kUnitPages) + S * partial;
+        if (t < best * 0.999) {
+            best = t;
+            *splits = S;
+            *pages_per_split = per;
+        }
+    }
+}
+
+cudaError_t launch_decode_prefix(const PrefixArgs& in, const uint8_t* cache, bool fp8, uint16_t* widened,
+                                 float2* scales, cudaStream_t s) {
+    PrefixArgs a = in;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    e = set_attr(dev, fp8);
+    if (e != cudaSuccess) return e;
+    const void* base = cache;
+    uint64_t rows = (uint64_t)a.num_blocks * kPage;
+    if (fp8) {
+        e = launch_pdl(prefix_widen_kernel, dim3((unsigned)(a.prefix_pages * kPage / 8)), dim3(256), 0, s, a, cache,
+                       widened, scales);
+        if (e != cudaSuccess) return e;
+        a.block_table = nullptr;
+        a.scales = scales;
+        base = widened;
+        rows = (uint64_t)a.prefix_pages * kPage;
+    }
+    a.key_rows = (int)rows;
+    CUtensorMap k_map, v_map, q_map, o_map;
+    memset(&k_map, 0, sizeof k_map);
+    memset(&v_map, 0, sizeof v_map);
+    memset(&q_map, 0, sizeof q_map);
+    memset(&o_map, 0, sizeof o_map);
+    {
+        // the rows as [panel of 64 dims][row][64]: one box is several panels of a page
+        const uint64_t dims[3] = {64, rows, (uint64_t)(kD / 64)};
+        const uint64_t strides[2] = {(uint64_t)kBf16RowBytes, 128};
+        const uint32_t kbox[3] = {64, (uint32_t)kPage, (uint32_t)kSlotPanels};
+        e = encode_tmap(&k_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, kbox, true);
+        if (e != cudaSuccess) return e;
+        const uint32_t vbox[3] = {64, (uint32_t)kPage, 2};
+        e = encode_tmap(&v_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, vbox, true);
+        if (e != cudaSuccess) return e;
+    }
+    {
+        const uint64_t dims[2] = {(uint64_t)kD, (uint64_t)a.flat_rows};
+        const uint64_t strides[1] = {(uint64_t)kD * 2};
+        const uint32_t box[2] = {64, 128};
+        e = encode_tmap(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.q, dims, strides, box, true);
+        if (e != cudaSuccess) return e;
+    }
+    {
+        const uint64_t dims[3] = {(uint64_t)kL, (uint64_t)a.flat_rows, (uint64_t)a.splits};
+        const uint64_t strides[2] = {(uint64_t)kL * 4, (uint64_t)a.flat_rows * kL * 4};
+        const uint32_t box[3] = {32, 128, 1};
+        e = encode_tmap(&o_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, a.part_o, dims, strides, box, true);
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t tiles = ((int64_t)a.flat_rows + kTileRows - 1) / kTileRows;
+    const dim3 grid((unsigned)(4 * tiles * a.splits));
+    return fp8 ? launch_pdl(decode_prefix_kernel<true>, grid, dim3(kThreads), kSmemBytes, s, k_map, v_map, q_map,
+                            o_map, a)
+               : launch_pdl(decode_prefix_kernel<false>, grid, dim3(kThreads), kSmemBytes, s, k_map, v_map, q_map,
+                            o_map, a);
+}
+
+}  // namespace mla

@@ -198,6 +198,7 @@ cudaError_t launch_sparse_table(const SparseTableArgs& a, cudaStream_t s);
 // What the body of a decode call does beyond mla_decode (its own call by default).
 struct DecodeExtra {
     const char* who = "mla_decode";  // the entry point, for messages
+    bool check_only = false;         // return after the argument checks that need no device
     int shared_pages = 0;            // see DecodeArgs
     int base = 0;
     bool all_partial = false;
@@ -214,6 +215,28 @@ mla_status decode_impl(const void* q, const void* kv_cache, mla_kv_dtype kv_dtyp
 
 // Clear the detail string and return MLA_OK.
 mla_status set_ok();
+
+// ---- decode over a prefix that the batch shares ------------------------------------------------
+struct PrefixArgs {
+    const uint16_t* q;          // bf16 [flat_rows, 576]: (request, query position, head)
+    int flat_rows;              // B * Sq * H
+    const int32_t* block_table; // the prefix pages' blocks (row 0 of the table); null: rows in order
+    int64_t num_blocks;
+    int key_rows;               // rows behind the keys' tensor map
+    int prefix_pages, splits, pages_per_split;
+    const float2* scales;       // FP8: per prefix token (k_scale, v_scale)
+    const int32_t* seq_lens;    // [B]
+    int max_seq_len, Sq, H;
+    float scale;
+    float* part_o;              // fp32 [splits, flat_rows, 512]
+    float* part_lse;            // fp32 [splits, flat_rows]
+    int32_t* dev_status;        // or null
+};
+int prefix_clusters();  // clusters of the prefix kernel that run at once on the current device, or -1
+void prefix_split(int64_t flat_rows, int pages, int clusters, int* splits, int* pages_per_split);
+// FP8: the prefix's rows are widened into `widened` [prefix tokens, 576] and `scales` first.
+cudaError_t launch_decode_prefix(const PrefixArgs& a, const uint8_t* cache, bool fp8, uint16_t* widened,
+                                 float2* scales, cudaStream_t s);
 
 // Record an error for mla_last_error_detail() and return `st` (printf-style message).
 mla_status set_error(mla_status st, const char* fmt, ...);

@@ -50,6 +50,42 @@ SparseLayout sparse_layout(mla_kv_dtype kv, int64_t rows, int H, int K, int S) {
     return w;
 }
 
+// How a shared-prefix call runs, and its workspace: the widened prefix (FP8), the prefix's partial
+// states, then what the decode of the requests' own tokens needs.
+struct PrefixPlan {
+    int pages, splits, pages_per_split;  // of the prefix kernel; splits == 0: the decode kernels do it all
+    int own_splits;                      // resolved, of the requests' own tokens
+    size_t widened, scales, part_o, part_lse, decode, total;
+};
+bool plan_prefix(mla_kv_dtype kv, int rows, int H, int prefix_len, int num_splits, int max_seq_len, PrefixPlan* w) {
+    // tokens past max_seq_len are no request's
+    const int pages = std::min(prefix_len, (max_seq_len + mla::kPage - 1) / mla::kPage * mla::kPage) / mla::kPage;
+    w->pages = pages;
+    const int64_t flat = (int64_t)rows * H;
+    if (pages > 0) {
+        const int clusters = mla::prefix_clusters();
+        if (clusters < 1) return false;
+        mla::prefix_split(flat, pages, clusters, &w->splits, &w->pages_per_split);
+        size_t off = 0;
+        if (kv == MLA_KV_FP8_E4M3_SCALED) {
+            w->widened = off;
+            off += up256((size_t)pages * mla::kPage * mla::kBf16RowBytes);
+            w->scales = off;
+            off += up256((size_t)pages * mla::kPage * sizeof(float2));
+        }
+        w->part_o = off;
+        off += up256((size_t)w->splits * flat * mla::kL * sizeof(float));
+        w->part_lse = off;
+        off += up256((size_t)w->splits * flat * sizeof(float));
+        w->decode = off;
+    }
+    const int own_len = std::max(0, max_seq_len - pages * mla::kPage);
+    w->own_splits = mla_resolve_num_splits(num_splits, rows, 1, H, own_len);
+    if (w->own_splits < 1 && w->own_splits != -2) return false;
+    w->total = w->decode + mla::workspace_layout(kv, rows, rows, H, w->own_splits, own_len, w->splits > 0).total;
+    return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -228,9 +264,8 @@ size_t mla_decode_shared_prefix_workspace_bytes(mla_kv_dtype kv_dtype, int B, in
     if (!known_kv(kv_dtype) || B < 1 || Sq < 1 || H < 1 || H > MLA_MAX_HEADS || prefix_len < 0 ||
         prefix_len % mla::kPage || max_seq_len < 0 || (int64_t)B * Sq > INT32_MAX / MLA_MAX_HEADS)
         return 0;
-    const int S = mla_resolve_num_splits(num_splits, B, Sq, H, max_seq_len);
-    if (S < 1 && S != -2) return 0;
-    return mla::workspace_layout(kv_dtype, B, (int64_t)B * Sq, H, S, max_seq_len).total;
+    PrefixPlan w{};
+    return plan_prefix(kv_dtype, B * Sq, H, prefix_len, num_splits, max_seq_len, &w) ? w.total : 0;
 }
 
 mla_status mla_decode_shared_prefix(const void* q, const void* kv_cache, mla_kv_dtype kv_dtype, int64_t num_blocks,
@@ -249,9 +284,56 @@ mla_status mla_decode_shared_prefix(const void* q, const void* kv_cache, mla_kv_
     mla::DecodeExtra x;
     x.who = who;
     x.shared_pages = prefix_len / mla::kPage;
-    return mla::decode_impl(q, kv_cache, kv_dtype, num_blocks, block_table, max_blocks, seq_lens, nullptr, max_seq_len,
-                            B, Sq, (int64_t)B * Sq, H, scale, num_splits, workspace, workspace_bytes, o_latent, o_dtype,
-                            lse, dev_status, stream, x);
+    auto decode = [&](int splits, void* ws, size_t bytes) {
+        return mla::decode_impl(q, kv_cache, kv_dtype, num_blocks, block_table, max_blocks, seq_lens, nullptr,
+                                max_seq_len, B, Sq, (int64_t)B * Sq, H, scale, splits, ws, bytes, o_latent, o_dtype,
+                                lse, dev_status, stream, x);
+    };
+    // What mla_decode refuses is refused by the same checks before anything is launched (and a
+    // batch that launches nothing ends there).
+    x.check_only = true;
+    const mla_status checked = decode(1, nullptr, 0);
+    if (checked != MLA_OK || B == 0) return checked;
+    x.check_only = false;
+    if (num_splits < -2) return set_error(MLA_ERR_INVALID_ARG, "%s: num_splits=%d < -2", who, num_splits);
+    PrefixPlan w{};
+    if (!plan_prefix(kv_dtype, B * Sq, H, prefix_len, num_splits, max_seq_len, &w))
+        return set_error(MLA_ERR_CUDA, "%s: could not plan the call (no CUDA device?)", who);
+    if (w.total > 0 && (!workspace || workspace_bytes < w.total))
+        return set_error(MLA_ERR_WORKSPACE_TOO_SMALL, "%s: workspace %zu bytes < %zu needed", who,
+                         workspace ? workspace_bytes : (size_t)0, w.total);
+    if (w.total > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: workspace must be 256-byte aligned", who);
+    char* ws = (char*)workspace;
+    if (w.splits > 0) {
+        mla::PrefixArgs a{};
+        a.q = (const uint16_t*)q;
+        a.flat_rows = B * Sq * H;
+        a.block_table = block_table;
+        a.num_blocks = num_blocks;
+        a.prefix_pages = w.pages;
+        a.splits = w.splits;
+        a.pages_per_split = w.pages_per_split;
+        a.seq_lens = seq_lens;
+        a.max_seq_len = max_seq_len;
+        a.Sq = Sq;
+        a.H = H;
+        a.scale = scale;
+        a.part_o = (float*)(ws + w.part_o);
+        a.part_lse = (float*)(ws + w.part_lse);
+        a.dev_status = dev_status;
+        const cudaError_t e = mla::launch_decode_prefix(
+            a, (const uint8_t*)kv_cache, kv_dtype == MLA_KV_FP8_E4M3_SCALED, (uint16_t*)(ws + w.widened),
+            (float2*)(ws + w.scales), (cudaStream_t)stream);
+        if (e != cudaSuccess) return cuda_error(e, who);
+        x.base = w.pages * mla::kPage;
+        x.all_partial = true;
+        x.wait_first = true;  // no cached row is read before the kernels ahead of this call have ended
+        x.pre_o = a.part_o;
+        x.pre_lse = a.part_lse;
+        x.pre_splits = w.splits;
+    }
+    return decode(w.own_splits, ws ? ws + w.decode : nullptr, w.total - w.decode);
 }
 
 }  // extern "C"

@@ -234,11 +234,12 @@ mla_status decode_impl(const void* q, const void* kv_cache, mla_kv_dtype kv_dtyp
     if (num_blocks > (int64_t)(INT32_MAX / mla::kPage))
         return fail(MLA_ERR_UNSUPPORTED, "%s: num_blocks=%lld too large (max %d)", x.who, (long long)num_blocks,
                     INT32_MAX / mla::kPage);
+    if (rows * H > (int64_t)INT32_MAX)
+        return fail(MLA_ERR_UNSUPPORTED, "%s: rows*H=%lld too large", x.who, (long long)(rows * H));
+    if (x.check_only) return ok();
     int S = mla_resolve_num_splits(num_splits, (int)rows, 1, H, std::max(0, max_seq_len - x.base));
     const bool planned = S == -2;
     if (S < 1 && !planned) return fail(MLA_ERR_CUDA, "%s: could not resolve num_splits (no CUDA device?)", x.who);
-    if (rows * H > (int64_t)INT32_MAX)
-        return fail(MLA_ERR_UNSUPPORTED, "%s: rows*H=%lld too large", x.who, (long long)(rows * H));
     const int pairs = planned ? std::max(1, device_sm_count() / 2) : 1;
     const int64_t max_units = planned ? mla::plan_max_units(rows, pairs) : rows * S;
     if (max_units > (int64_t)1 << 30)
