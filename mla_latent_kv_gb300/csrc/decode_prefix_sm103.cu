@@ -56,13 +56,14 @@ namespace {
 using namespace ptx;
 using dec::warp_wait;
 
-constexpr int kThreads = 320;  // warp 0 TMA, warp 1 MMA, warps 2-9 softmax / 2-5 helpers, 2-9 epilogue
+constexpr int kThreads = 576;  // warp 0 TMA, warp 1 MMA, warps 2-17 softmax / 2-5 helpers, 2-17 epilogue
+constexpr int kSoftThreads = kThreads - 64;
 constexpr int kTileRows = 256;
 constexpr int kPPG = 2;                      // pages per group, one per scores CTA
 constexpr int kPageBox = kPage * 128;        // one page's rows of one 64-dim panel (8 KB)
 constexpr int kSlotPanels = 3;
 constexpr int kSlotBytes = kSlotPanels * kPageBox;  // 24 KB
-constexpr int kSlots = 7;                    // K ring of a scores CTA
+constexpr int kSlots = 5;                    // K ring of a scores CTA
 constexpr int kQPanelBytes = 128 * 128;      // 128 rows x 64 dims of Q (16 KB)
 constexpr int kPBufs = 5;                    // P buffers of an output CTA (one page each)
 constexpr int kVStages = 4;                  // V ring of an output CTA: a page's 4 panels each
@@ -74,8 +75,9 @@ constexpr int kCtrlBytes = 4096;
 // scores CTA
 constexpr int OFF_QROPE = kCtrlBytes;
 constexpr int OFF_RING = OFF_QROPE + kQPanelBytes;
-constexpr int OFF_STAGE = OFF_RING + kSlots * kSlotBytes;  // two P staging buffers, one per half
-constexpr int kSmem0 = OFF_STAGE + 2 * kPBufStride;
+constexpr int kStages = 4;                   // P staging buffers: each of a group's pages has two
+constexpr int OFF_STAGE = OFF_RING + kSlots * kSlotBytes;
+constexpr int kSmem0 = OFF_STAGE + kStages * kPBufStride;
 // output CTA
 constexpr int OFF_V = kCtrlBytes;
 constexpr int OFF_PB = OFF_V + kVStages * kVStageBytes;
@@ -87,11 +89,13 @@ static_assert(OFF_RING % 1024 == 0 && OFF_STAGE % 1024 == 0 && OFF_PB % 1024 == 
                   kSlotBytes % 1024 == 0,
               "128-byte swizzled tiles need 1024-byte alignment");
 static_assert(8 * 128 * 128 <= kSmem1 - OFF_V, "epilogue tiles");
-// Q's latent panels land in the two staging buffers (panels 0, 1) and ring slots 3-6 (panels 2-7),
-// so that the first page's keys can load into slots 0-2 at once.
-static_assert(kSlots == 7 && 6 * kQPanelBytes == 4 * kSlotBytes, "Q panel homes");
+// Q's latent panels land in the four staging buffers (panels 0-3) and at the end of the ring
+// (panels 4-7, over slots 2-4), so that the first keys can load into slots 0 and 1 at once.
+static_assert(kSlots == 5 && kStages == 4 && 4 * kQPanelBytes <= 3 * kSlotBytes, "Q panel homes");
+constexpr int OFF_Q47 = OFF_RING + kSlots * kSlotBytes - 4 * kQPanelBytes;
+static_assert(OFF_Q47 % 1024 == 0 && OFF_Q47 >= OFF_RING + 2 * kSlotBytes, "Q panel homes");
 __device__ __forceinline__ uint32_t q_panel_off(int pn) {
-    return pn < 2 ? OFF_STAGE + pn * kPBufStride : OFF_RING + 3 * kSlotBytes + (pn - 2) * kQPanelBytes;
+    return pn < 4 ? OFF_STAGE + pn * kPBufStride : OFF_Q47 + (pn - 4) * kQPanelBytes;
 }
 
 // Barrier slots, one layout for all four CTAs (multicast commits land at the same offset in each).
@@ -99,12 +103,12 @@ enum : int {
     B_SLOTFULL = 0,                     // [kSlots] CTA 0: slot landed in both scores CTAs (TMA tx)
     B_SLOTEMPTY = B_SLOTFULL + kSlots,  // [kSlots] CTAs 0, 1: slot's QK MMAs completed
     B_SFULL = B_SLOTEMPTY + kSlots,     // [2] CTAs 0, 1: S buffer ready
-    B_SEMPTY = B_SFULL + 2,             // [2] CTA 0: S buffer read by the 16 softmax warps of the pair
+    B_SEMPTY = B_SFULL + 2,             // [2] CTA 0: S buffer read by the 32 softmax warps of the pair
     B_QFULL = B_SEMPTY + 2,             // CTAs 0, 1: Q landed in shared memory
-    B_QREADY,                           // CTAs 0, 1: Q latent dims moved to TMEM (256 threads)
+    B_QREADY,                           // CTAs 0, 1: Q latent dims moved to TMEM (512 threads)
     B_QPEER,                            // CTA 0: CTA 1's Q moved
-    B_STAGEFREE,                        // [2] CTAs 0, 1: staging buffer's copy has landed
-    B_PEMPTY = B_STAGEFREE + 2,         // [kPBufs] all: PV MMAs of the page in P buffer b completed
+    B_STAGEFREE,                        // [4] CTAs 0, 1: staging buffer's copy has landed
+    B_PEMPTY = B_STAGEFREE + kStages,         // [kPBufs] all: PV MMAs of the page in P buffer b completed
     B_VFULL = B_PEMPTY + kPBufs,        // [kVStages] CTA 2: V stage landed in both output CTAs
     B_VEMPTY = B_VFULL + kVStages,      // [kVStages] CTAs 2, 3: V stage consumed
     B_PFULL = B_VEMPTY + kVStages,      // [kPBufs] CTAs 2, 3: P message landed
@@ -115,7 +119,7 @@ enum : int {
 static_assert(8 * B_COUNT <= 512, "barrier slots");
 constexpr int OFF_TMEM = 512;
 constexpr int OFF_ABORT = 516;
-constexpr int OFF_MX = 1024;      // scores: f32 [2][128] exchange between the two halves
+constexpr int OFF_MX = 1024;      // scores: f32 [4][128] exchange between the column quarters
 constexpr int OFF_STAT_M = 2048;  // output: f32 [128] final running max (log2 units)
 constexpr int OFF_STAT_L = 2560;  // output: f32 [128] row sum
 
@@ -124,7 +128,7 @@ constexpr uint32_t kSCol = 256;  // scores: Q latent in columns [0, 256), S buff
 constexpr uint32_t kIdescQK = idesc_bf16_f32(256, 128, false, false);
 constexpr uint32_t kIdescPV = idesc_bf16_f32(256, 256, false, true);
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr uint32_t kBarMax = 1, kBarOr = 2, kBarHalf0 = 3, kBarEpi = 4, kBarStage0 = 5;
+constexpr uint32_t kBarMax = 1, kBarOr = 2, kBarQuarter0 = 3, kBarEpi = 4, kBarStage0 = 5;
 constexpr int kEpiPanelBytes = 128 * 128;
 
 template <bool kScaled>
@@ -134,7 +138,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                          const PrefixArgs p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_addr(smem);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // warp-uniform, also to the compiler
     const uint32_t rank = cluster_ctarank();
     const int side = (int)(rank & 1);  // which half of the tile's rows
     const bool scores = rank < 2;
@@ -156,8 +161,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         *abort = 0;
         for (int i = 0; i < B_COUNT; ++i) {
             uint32_t cnt = 1;
-            if (i >= B_SEMPTY && i < B_SEMPTY + 2) cnt = 16;
-            if (i == B_QREADY) cnt = 256;
+            if (i >= B_SEMPTY && i < B_SEMPTY + 2) cnt = 32;
+            if (i == B_QREADY) cnt = kSoftThreads;
             if (i >= B_READY && i < B_READY + kPBufs) cnt = 8;
             bar_init(bar(i), cnt);
         }
@@ -173,7 +178,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     cluster_sync();  // every CTA's barriers exist before any remote arrive or copy
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM), 0);
     griddep_wait();  // q, the cache and the lengths may be earlier kernels' outputs
     if (tid == 0) griddep_launch_dependents();
 
@@ -204,9 +209,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     const int y = page_row(kPPG * gi + side);
                     for (int t = 0; t < 3; ++t) {
                         const int m = 3 * gi + t, slot = m % kSlots, k = m / kSlots;
-                        // first use of slots 3-6: Q's panels have been moved out to TMEM
+                        // first use of slots 2-4: Q's panels have been moved out to TMEM
                         ok = k > 0       ? wait_bar<true>(bar(B_SLOTEMPTY + slot), (k - 1) & 1, abort, ds)
-                             : slot >= 3 ? wait_bar(bar(B_QREADY), 0, abort, ds)
+                             : slot >= 2 ? wait_bar(bar(B_QREADY), 0, abort, ds)
                                          : true;
                         if (!ok) break;
                         // both CTAs' bytes are counted on CTA 0's barrier
@@ -231,42 +236,53 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 bar_arrive_remote(bar(B_QPEER), 0);
             }
-            if (lane == 0 && npages > 0 && side == 0) {
-                bool ok = wait_bar(bar(B_QREADY), 0, abort, ds) && wait_bar<true>(bar(B_QPEER), 0, abort, ds);
+            if (npages > 0 && side == 0) {
+                // The whole warp runs the loop and one elected lane issues: descriptors and addresses
+                // then live in uniform registers. Issued from a lane-0 branch, an MMA took 140 cycles
+                // instead of the 64 that the tensor core needs.
+                const bool leader = elect_one();
+                bool ok = warp_wait(bar(B_QREADY), 0, abort, ds) && warp_wait<true>(bar(B_QPEER), 0, abort, ds);
                 if (ok) tc_fence_after();
+                const uint64_t rope0 = smem_desc_sw128(sbase + OFF_QROPE, 16, 1024);
+                int slot = 0, phase = 0;
                 for (int gi = 0; gi < ngroups && ok; ++gi) {
                     const int buf = gi & 1, use = gi >> 1;
                     if (use > 0) {  // both CTAs' softmax warps have read the buffer's previous S
-                        if (!(ok = wait_bar<true>(bar(B_SEMPTY + buf), (use - 1) & 1, abort, ds))) break;
+                        if (!(ok = warp_wait<true>(bar(B_SEMPTY + buf), (use - 1) & 1, abort, ds))) break;
                         tc_fence_after();
                     }
                     const uint32_t d = tmem + kSCol + 128u * buf;
-                    for (int t = 0; t < 3; ++t) {
-                        const int m = 3 * gi + t, slot = m % kSlots, k = m / kSlots;
-                        if (!(ok = wait_bar<true>(bar(B_SLOTFULL + slot), k & 1, abort, ds))) break;
-                        const uint32_t kb = sbase + OFF_RING + slot * kSlotBytes;
+#pragma unroll
+                    for (int t = 0; t < 3; ++t) {  // unrolled: every TMEM address and flag an immediate offset
+                        if (!(ok = warp_wait<true>(bar(B_SLOTFULL + slot), phase, abort, ds))) break;
+                        const uint64_t bd0 = smem_desc_sw128(sbase + OFF_RING + slot * kSlotBytes, 16, 1024);
 #pragma unroll
                         for (int q = 0; q < kSlotPanels; ++q) {
                             const int pn = kSlotPanels * t + q;
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                const uint64_t bd = smem_desc_sw128(kb + q * kPageBox + 32 * j, 16, 1024);
-                                if (pn < 8) {
-                                    mma_pair_ts(d, tmem + 8u * (4 * pn + j), bd, kIdescQK, (pn | j) ? 1u : 0u);
-                                } else {
-                                    const uint64_t ad = smem_desc_sw128(sbase + OFF_QROPE + 32 * j, 16, 1024);
-                                    mma_pair_ss(d, ad, bd, kIdescQK, 1u);
+                                const uint64_t bd = bd0 + (uint64_t)((q * kPageBox + 32 * j) >> 4);
+                                if (leader) {
+                                    if (pn < 8)
+                                        mma_pair_ts(d, tmem + 8u * (4 * pn + j), bd, kIdescQK, (pn | j) ? 1u : 0u);
+                                    else
+                                        mma_pair_ss(d, rope0 + (uint64_t)(2 * j), bd, kIdescQK, 1u);
                                 }
                             }
                         }
-                        mma_pair_commit(bar(B_SLOTEMPTY + slot), 0x3);
+                        if (leader) mma_pair_commit(bar(B_SLOTEMPTY + slot), 0x3);
+                        if (++slot == kSlots) {
+                            slot = 0;
+                            phase ^= 1;
+                        }
                     }
-                    if (ok) mma_pair_commit(bar(B_SFULL + buf), 0x3);
+                    if (ok && leader) mma_pair_commit(bar(B_SFULL + buf), 0x3);
                 }
             }
         } else {
-            // ------------------------- softmax warps (256 threads) -------------------------
-            const int half = (warp - 2) >> 2;  // page `half` of each group
+            // ------------------------- softmax warps (512 threads) -------------------------
+            // Quarter `quarter` of the warps owns 32 columns of each group's S: half of page `pg2`.
+            const int quarter = (warp - 2) >> 2, pg2 = quarter >> 1, sub = quarter & 1;
             const int row = 32 * (warp & 3) + lane;
             const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
             float* mx = reinterpret_cast<float*>(smem + OFF_MX);
@@ -280,10 +296,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             }
             const int warp_lim = __reduce_min_sync(0xffffffffu, lim);
             if (npages > 0) {
-                // Q latent dims: this half moves panels 4 half .. 4 half + 3 into TMEM
+                // Q latent dims: this quarter moves panels 2 quarter and 2 quarter + 1 into TMEM
                 const bool okq = warp_wait(bar(B_QFULL), 0, abort, ds);
 #pragma unroll 1
-                for (int pn = 4 * half; pn < 4 * half + 4; ++pn) {
+                for (int pn = 2 * quarter; pn < 2 * quarter + 2; ++pn) {
                     uint32_t v[32];
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
@@ -303,67 +319,56 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 bar_arrive(bar(B_QREADY));
             }
             const float sl2 = p.scale * 1.4426950408889634f;  // exp2 domain
-            float m_run = -CUDART_INF_F, l_run = 0.f;          // each half keeps its own sum
+            float m_run = -CUDART_INF_F, l_run = 0.f;          // each quarter keeps its own sum
             const uint32_t out_rank = 2u + (uint32_t)side;
             const uint32_t pbuf_remote = map_to_rank(sbase + OFF_PB, out_rank);
             const uint32_t pfull_remote = map_to_rank(bar(B_PFULL), out_rank);
-            uint8_t* stage = smem + OFF_STAGE + half * kPBufStride;
-            const int htid = tid - 64 - 128 * half;
             for (int gi = 0; gi < ngroups; ++gi) {
-                // No early exit from this loop: all 256 threads must pass the same named barriers
+                // No early exit from this loop: all 512 threads must pass the same named barriers
                 // (which cannot time out); after an abort the waits return at once.
-                const int page = kPPG * gi + half, buf = gi & 1;
+                const int page = kPPG * gi + pg2, buf = gi & 1;
                 const bool okS = warp_wait<true>(bar(B_SFULL + buf), (gi >> 1) & 1, abort, ds);
-                uint32_t s[2][32];
+                uint32_t s[32];
                 if (okS) {
                     tc_fence_after();
-                    const uint32_t scol = tmem + lane_base + kSCol + 128u * buf + 64u * half;
-                    tmem_ld32(scol, s[0]);
-                    tmem_ld32(scol + 32u, s[1]);
+                    tmem_ld32(tmem + lane_base + kSCol + 128u * buf + 32u * quarter, s);
                     tmem_wait_ld();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) bar_arrive_remote(bar(B_SEMPTY + buf), 0);
+                    if (lane == 0) bar_arrive_remote_relaxed(bar(B_SEMPTY + buf), 0);
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) s[c][j] = __float_as_uint(-CUDART_INF_F);
+                    for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(-CUDART_INF_F);
                 }
                 const float4* sc = nullptr;  // (k_scale, v_scale) of two tokens each
                 if constexpr (kScaled) {
-                    sc = reinterpret_cast<const float4*>(p.scales + (size_t)(page0 + min(page, npages - 1)) * kPage);
+                    sc = reinterpret_cast<const float4*>(p.scales + (size_t)(page0 + min(page, npages - 1)) * kPage +
+                                                         32 * sub);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float4 x = __ldg(sc + 16 * c + j);
-                            s[c][2 * j] = __float_as_uint(__uint_as_float(s[c][2 * j]) * x.x);
-                            s[c][2 * j + 1] = __float_as_uint(__uint_as_float(s[c][2 * j + 1]) * x.z);
-                        }
+                    for (int j = 0; j < 16; ++j) {
+                        const float4 x = __ldg(sc + j);
+                        s[2 * j] = __float_as_uint(__uint_as_float(s[2 * j]) * x.x);
+                        s[2 * j + 1] = __float_as_uint(__uint_as_float(s[2 * j + 1]) * x.z);
+                    }
                 }
                 if (page >= npages || warp_lim < (page + 1) * kPage) {  // some row does not see all of the page
-                    const int v = page >= npages ? 0 : lim - page * kPage;
+                    const int v = page >= npages ? 0 : lim - page * kPage - 32 * sub;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (32 * c + j >= v) s[c][j] = __float_as_uint(-CUDART_INF_F);
+                    for (int j = 0; j < 32; ++j)
+                        if (j >= v) s[j] = __float_as_uint(-CUDART_INF_F);
                 }
                 float lm4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) lm4[j & 3] = fmaxf(lm4[j & 3], __uint_as_float(s[c][j]));
+                for (int j = 0; j < 32; ++j) lm4[j & 3] = fmaxf(lm4[j & 3], __uint_as_float(s[j]));
                 const float lm = fmaxf(fmaxf(lm4[0], lm4[1]), fmaxf(lm4[2], lm4[3]));
-                // Does any of the 256 rows x halves pass the threshold? The barrier also keeps the
-                // next exchange's writes of mx behind this one's reads.
-                const bool any = named_bar_or(kBarOr, 256, lm * sl2 > m_run + kRescaleThreshold);
+                // Does any row's part pass the threshold? The barrier also keeps the next exchange's
+                // writes of mx behind this one's reads.
+                const bool any = named_bar_or(kBarOr, kSoftThreads, lm * sl2 > m_run + kRescaleThreshold);
                 float alpha = 1.f;
                 if (any) {
-                    mx[half * 128 + row] = lm;
-                    named_bar(kBarMax, 256);
-                    const float mt = fmaxf(lm, mx[(1 - half) * 128 + row]) * sl2;  // scale > 0
+                    mx[quarter * 128 + row] = lm;
+                    named_bar(kBarMax, kSoftThreads);
+                    const float mt = fmaxf(fmaxf(mx[row], mx[128 + row]), fmaxf(mx[256 + row], mx[384 + row])) * sl2;
                     if (mt > m_run + kRescaleThreshold) {
                         alpha = fast_exp2(m_run - mt);  // 0 while m_run = -inf
                         m_run = mt;
@@ -371,54 +376,55 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     l_run *= alpha;
                 }
                 const float mref = m_run == -CUDART_INF_F ? 0.f : m_run;  // nothing seen yet: weights 0
-                uint32_t pk[32];
+                uint32_t pk[16];
                 float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float a0 = fast_exp2(fmaf(__uint_as_float(s[c][2 * j]), sl2, -mref));
-                        float a1 = fast_exp2(fmaf(__uint_as_float(s[c][2 * j + 1]), sl2, -mref));
-                        l4[2 * (j & 1)] += a0;
-                        l4[2 * (j & 1) + 1] += a1;
-                        if constexpr (kScaled) {
-                            const float4 x = __ldg(sc + 16 * c + j);
-                            a0 *= x.y;
-                            a1 *= x.w;
-                        }
-                        pk[16 * c + j] = pack_bf16x2(a0, a1);
+                for (int j = 0; j < 16; ++j) {
+                    float a0 = fast_exp2(fmaf(__uint_as_float(s[2 * j]), sl2, -mref));
+                    float a1 = fast_exp2(fmaf(__uint_as_float(s[2 * j + 1]), sl2, -mref));
+                    l4[2 * (j & 1)] += a0;
+                    l4[2 * (j & 1) + 1] += a1;
+                    if constexpr (kScaled) {
+                        const float4 x = __ldg(sc + j);
+                        a0 *= x.y;
+                        a1 *= x.w;
                     }
+                    pk[j] = pack_bf16x2(a0, a1);
+                }
                 l_run += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                // the page's staging buffers take turns: this one is free once the copy of two groups
+                // ago has landed
+                const int sbi = 2 * (gi & 1) + pg2;
+                uint8_t* stage = smem + OFF_STAGE + sbi * kPBufStride;
                 if (page < npages) {  // a page past the end sends nothing
-                    // the staging buffer is free once the previous group's copy has landed
-                    if (gi > 0) warp_wait<true>(bar(B_STAGEFREE + half), (gi - 1) & 1, abort, ds);
+                    if (gi > 1) warp_wait<true>(bar(B_STAGEFREE + sbi), ((gi >> 1) - 1) & 1, abort, ds);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        *reinterpret_cast<uint4*>(stage + row * 128 + ((c ^ (row & 7)) << 4)) =
+                    for (int c = 0; c < 4; ++c)
+                        *reinterpret_cast<uint4*>(stage + row * 128 + (((4 * sub + c) ^ (row & 7)) << 4)) =
                             make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
                     // the group's first page carries the rescale that O needs before it
-                    reinterpret_cast<float*>(stage + kPBytes)[row] = alpha;
-                    if (row == 0)
-                        *reinterpret_cast<uint32_t*>(stage + kPBytes + 512) = (half == 0 && any && gi > 0) ? 1u : 0u;
+                    if (sub == 0) reinterpret_cast<float*>(stage + kPBytes)[row] = alpha;
+                    if (sub == 0 && row == 0)
+                        *reinterpret_cast<uint32_t*>(stage + kPBytes + 512) = (pg2 == 0 && any && gi > 0) ? 1u : 0u;
                     fence_proxy_async_cta();  // generic writes before the bulk copy reads them
                 }
-                named_bar(kBarStage0 + half, 128);
-                if (htid == 0 && page < npages && okS) {
+                named_bar(kBarStage0 + pg2, kSoftThreads / 2);
+                if (sub == 0 && row == 0 && page < npages && okS) {
                     const int pb = page % kPBufs, up = page / kPBufs;
                     if (up == 0 || wait_bar<true>(bar(B_PEMPTY + pb), (up - 1) & 1, abort, ds))
-                        bulk_copy_to_peer(pbuf_remote + pb * kPBufStride, sbase + OFF_STAGE + half * kPBufStride,
+                        bulk_copy_to_peer(pbuf_remote + pb * kPBufStride, sbase + OFF_STAGE + sbi * kPBufStride,
                                           kPMsgBytes, pfull_remote + 8u * pb);
                 }
             }
-            // combine the two halves' sums, ship the final statistics
-            named_bar(kBarMax, 256);
-            if (half == 1) mx[row] = l_run;
-            named_bar(kBarMax, 256);
-            if (half == 0) {
-                l_run += mx[row];
+            // combine the quarters' sums, ship the final statistics
+            named_bar(kBarMax, kSoftThreads);
+            mx[quarter * 128 + row] = l_run;
+            named_bar(kBarMax, kSoftThreads);
+            if (quarter == 0) {
+                l_run = (mx[row] + mx[128 + row]) + (mx[256 + row] + mx[384 + row]);
                 st_cluster_u32(map_to_rank(sbase + OFF_STAT_M, out_rank) + 4u * row, __float_as_uint(m_run));
                 st_cluster_u32(map_to_rank(sbase + OFF_STAT_L, out_rank) + 4u * row, __float_as_uint(l_run));
-                named_bar(kBarHalf0, 128);
+                named_bar(kBarQuarter0, 128);
                 if (tid == 64) {
                     bar_arrive_remote(bar(B_STATS), out_rank);
                     // nothing may still be on its way to this CTA when it exits: the last
@@ -453,49 +459,48 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         } else if (warp == 1) {
-            if (lane == 0) {
-                if (side == 0) {
-                    bool ok = true;
-                    for (int i = 0; i < npages && ok; ++i) {
-                        const int pb = i % kPBufs, st = i % kVStages;
-                        if (!(ok = wait_bar<true>(bar(B_READY + pb), (i / kPBufs) & 1, abort, ds))) break;
-                        if (!(ok = wait_bar<true>(bar(B_VFULL + st), (i / kVStages) & 1, abort, ds))) break;
-                        tc_fence_after();  // after a rescale by the helper warps' tcgen05.st
-                        const uint32_t pbuf = sbase + OFF_PB + pb * kPBufStride;
-                        const uint32_t vb = sbase + OFF_V + st * kVStageBytes;
+            if (side == 0) {
+                const bool leader = elect_one();  // as for the scores
+                bool ok = true;
+                for (int i = 0; i < npages && ok; ++i) {
+                    const int pb = i % kPBufs, st = i % kVStages;
+                    if (!(ok = warp_wait<true>(bar(B_READY + pb), (i / kPBufs) & 1, abort, ds))) break;
+                    if (!(ok = warp_wait<true>(bar(B_VFULL + st), (i / kVStages) & 1, abort, ds))) break;
+                    tc_fence_after();  // after a rescale by the helper warps' tcgen05.st
+                    const uint64_t ad0 = smem_desc_sw128(sbase + OFF_PB + pb * kPBufStride, 16, 1024);
+                    const uint64_t bd0 = smem_desc_sw128(sbase + OFF_V + st * kVStageBytes, kPageBox, 1024);
 #pragma unroll
-                        for (int kk = 0; kk < kPage / 16; ++kk) {
-                            const uint64_t ad = smem_desc_sw128(pbuf + kk * 32, 16, 1024);
+                    for (int kk = 0; kk < kPage / 16; ++kk)
 #pragma unroll
-                            for (int nh = 0; nh < 2; ++nh) {
-                                const uint64_t bd =
-                                    smem_desc_sw128(vb + nh * 2 * kPageBox + kk * 2048, kPageBox, 1024);
-                                mma_pair_ss(tmem + 256u * nh, ad, bd, kIdescPV, (i > 0 || kk > 0) ? 1u : 0u);
-                            }
-                        }
+                        for (int nh = 0; nh < 2; ++nh)
+                            if (leader)
+                                mma_pair_ss(tmem + 256u * nh, ad0 + (uint64_t)((kk * 32) >> 4),
+                                            bd0 + (uint64_t)((nh * 2 * kPageBox + kk * 2048) >> 4), kIdescPV,
+                                            kk > 0 ? 1u : (i > 0 ? 1u : 0u));
+                    if (leader) {
                         mma_pair_commit(bar(B_VEMPTY + st), 0xC);
                         mma_pair_commit(bar(B_PEMPTY + pb), 0xF);
                     }
                 }
-                // teardown: the last commits have landed in this CTA
-                for (int pg = (npages > kPBufs ? npages - kPBufs : 0); pg < npages; ++pg) {
-                    volatile int dummy = 0;
-                    wait_bar<true>(bar(B_PEMPTY + pg % kPBufs), (pg / kPBufs) & 1, *abort ? &dummy : abort, ds);
-                }
+            }
+            // teardown: the last commits have landed in this CTA
+            for (int pg = (npages > kPBufs ? npages - kPBufs : 0); pg < npages; ++pg) {
+                volatile int dummy = 0;
+                wait_bar<true>(bar(B_PEMPTY + pg % kPBufs), (pg / kPBufs) & 1, *abort ? &dummy : abort, ds);
             }
         } else {
-            // ------------- helper warps 2-5: P arrival, rescale; warps 2-9: the epilogue -------------
+            // ------------- helper warps 2-5: P arrival, rescale; warps 2-17: the epilogue -------------
             const int row = 32 * (warp & 3) + lane;
             const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-            const int ctid = tid - 64;  // 0..255; 0..127 are the helper warps
-            const int eset = warp >= 6 ? 1 : 0;
+            const int ctid = tid - 64;  // 0..511; 0..127 are the helper warps
+            const int eset = (warp - 2) >> 2;
             int pages_ready = warp >= 6 ? npages : 0;
             for (int i = 0; i < npages && warp < 6; ++i) {
                 const int pb = i % kPBufs;
                 if (!warp_wait<true>(bar(B_PFULL + pb), (i / kPBufs) & 1, abort, ds)) break;
                 if (ctid == 0) {
                     bar_arrive_expect_tx(bar(B_PFULL + pb), kPMsgBytes);           // re-arm for the next message
-                    bar_arrive_remote(bar(B_STAGEFREE + (i & 1)), (uint32_t)side);  // the sender's staging buffer
+                    bar_arrive_remote_relaxed(bar(B_STAGEFREE + (i & 3)), (uint32_t)side);  // the sender's staging buffer
                 }
                 const uint8_t* pmsg = smem + OFF_PB + pb * kPBufStride;
                 const bool fix = i > 0 && *reinterpret_cast<const volatile uint32_t*>(pmsg + kPBytes + 512) != 0;
@@ -519,7 +524,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 // issues: it is made visible along this warp's arrival
                 fence_proxy_async_cta();
                 __syncwarp();
-                if (lane == 0) bar_arrive_remote(bar(B_READY + pb), 2);
+                if (lane == 0) bar_arrive_remote_relaxed(bar(B_READY + pb), 2);
                 pages_ready = i + 1;
             }
             const bool has_o = npages > 0 && pages_ready == npages && !*abort;
@@ -541,18 +546,18 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             for (int rd = 0; rd < 2; ++rd) {
                 if (rd > 0) {  // the previous round's stores have read their tiles
                     if (ctid == 0) bulk_wait_group_read<0>();
-                    named_bar(kBarEpi, 256);
+                    named_bar(kBarEpi, kSoftThreads);
                 }
-                uint32_t v[4][32];
+                uint32_t v[2][32];  // this warp set's two panels
                 if (use_o) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        tmem_ld32(tmem + lane_base + (uint32_t)(rd * 256 + (4 * eset + q) * 32), v[q]);
+                    for (int q = 0; q < 2; ++q)
+                        tmem_ld32(tmem + lane_base + (uint32_t)(rd * 256 + (2 * eset + q) * 32), v[q]);
                     tmem_wait_ld();
                 }
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint8_t* out = smem + OFF_V + (4 * eset + q) * kEpiPanelBytes;
+                for (int q = 0; q < 2; ++q) {
+                    uint8_t* out = smem + OFF_V + (2 * eset + q) * kEpiPanelBytes;
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);  // an empty row: also where O holds garbage
@@ -564,7 +569,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
                 fence_proxy_async_cta();
-                named_bar(kBarEpi, 256);
+                named_bar(kBarEpi, kSoftThreads);
                 if (ctid == 0 && rows0 < p.flat_rows) {
                     for (int pl = 0; pl < 8; ++pl)
                         tma_store_3d(&o_map, sbase + OFF_V + pl * kEpiPanelBytes, rd * 256 + pl * 32, rows0, split);

@@ -47,6 +47,14 @@ __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+// True in one lane of a converged warp. Code around it that all lanes run (waits, descriptor
+// arithmetic) stays warp-uniform, which a branch on the lane number would not be.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // ------------------------------------------------------------------------------------------
 // mbarrier
 // ------------------------------------------------------------------------------------------
@@ -71,6 +79,14 @@ __device__ __forceinline__ void bar_arrive_expect_tx(uint32_t bar, uint32_t byte
 __device__ __forceinline__ void bar_arrive_remote(uint32_t bar, uint32_t rank) {
     uint32_t ra = map_to_rank(bar, rank);
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(ra) : "memory");
+}
+
+// The same without the release: for an arrival that only says "I am done reading" and publishes no
+// write of this thread. A release at cluster scope first waits for the thread's own writes to be
+// visible to the cluster, which takes most of a microsecond.
+__device__ __forceinline__ void bar_arrive_remote_relaxed(uint32_t bar, uint32_t rank) {
+    uint32_t ra = map_to_rank(bar, rank);
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(ra) : "memory");
 }
 
 __device__ __forceinline__ bool bar_try_wait(uint32_t bar, uint32_t parity) {
