@@ -165,7 +165,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                       const DecodeArgs p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_addr(smem);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // warp-uniform, also to the compiler
     const uint32_t rank = cluster_ctarank();
     if (sbase & 1023u) {  // the swizzled layouts need 1024-byte aligned tiles; never expected
         if (tid == 0 && p.dev_status) atomicOr(p.dev_status, MLA_DEV_WAIT_TIMEOUT);
@@ -203,7 +204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     cluster_sync();  // both CTAs' barriers exist before any remote arrive or store
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM), 0);
     if (tid == 0) griddep_launch_dependents();
     if (p.plan_units || p.wait_first) {
         // The schedule (or the lengths and block table) is the preceding kernel's output: the
@@ -271,41 +272,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         } else if (warp == 1) {
-            if (lane == 0 && npages > 0) {
+            if (npages > 0) {
+                // the whole warp runs the loop and one elected lane issues (as in the bf16 kernel)
+                const bool leader = elect_one();
+                const uint64_t rope0 = smem_desc_sw128(sbase + OFF_QROPE, 16, 1024);
                 int done = 0;  // triples whose MMAs were issued
-                bool ok = wait_bar(bar(B_QREADY), 0, abort, ds);
+                bool ok = warp_wait(bar(B_QREADY), 0, abort, ds);
                 if (ok) tc_fence_after();
                 for (int gi = 0; gi < ngroups && ok; ++gi) {
                     const int sb = gi & 1;
                     if (gi >= 2) {  // the softmax warps have read this S buffer's previous group
-                        if (!(ok = wait_bar(bar(B_SEMPTY + sb), ((gi >> 1) - 1) & 1, abort, ds))) break;
+                        if (!(ok = warp_wait(bar(B_SEMPTY + sb), ((gi >> 1) - 1) & 1, abort, ds))) break;
                         tc_fence_after();
                     }
                     const uint32_t d = tmem + kSCol + 128u * sb;
+#pragma unroll
                     for (int t = 0; t < 3; ++t) {
                         const int m = 3 * gi + t, ks = m % kKSlots;
                         // written by the converter warps (generic stores + proxy fence + arrive)
-                        if (!(ok = wait_bar(bar(B_KFULL + ks), (m / kKSlots) & 1, abort, ds))) break;
+                        if (!(ok = warp_wait(bar(B_KFULL + ks), (m / kKSlots) & 1, abort, ds))) break;
                         tc_fence_after();
-                        const uint32_t kb = sbase + OFF_KRING + ks * kKSlotBytes;
+                        const uint64_t bd0 = smem_desc_sw128(sbase + OFF_KRING + ks * kKSlotBytes, 16, 1024);
 #pragma unroll
                         for (int i = 0; i < 3; ++i) {
                             const int pn = 3 * t + i;
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                const uint64_t bd = smem_desc_sw128(kb + i * kKPanelBytes + 32 * j, 16, 1024);
-                                if (pn < 8) {
-                                    mma_ts(d, tmem + 8u * (4 * pn + j), bd, kIdescQK, (pn | j) ? 1u : 0u);
-                                } else {
-                                    const uint64_t ad = smem_desc_sw128(sbase + OFF_QROPE + 32 * j, 16, 1024);
-                                    mma_ss(d, ad, bd, kIdescQK, 1u);
+                                const uint64_t bd = bd0 + (uint64_t)((i * kKPanelBytes + 32 * j) >> 4);
+                                if (leader) {
+                                    if (pn < 8)
+                                        mma_ts(d, tmem + 8u * (4 * pn + j), bd, kIdescQK, (pn | j) ? 1u : 0u);
+                                    else
+                                        mma_ss(d, rope0 + (uint64_t)(2 * j), bd, kIdescQK, 1u);
                                 }
                             }
                         }
-                        mma_commit(bar(B_KEMPTY + ks));
+                        if (leader) mma_commit(bar(B_KEMPTY + ks));
                         ++done;
                     }
-                    if (ok) mma_commit(bar(B_SFULL + sb));
+                    if (ok && leader) mma_commit(bar(B_SFULL + sb));
                 }
                 volatile int dummy = 0;  // drain: the last commits have landed before teardown
                 for (int m = (done > kKSlots ? done - kKSlots : 0); m < done; ++m) {
@@ -589,20 +594,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         } else if (warp == 1) {
-            // MMA thread: per page one wait for P (PFULL) and the helpers (READY), then for each of
+            // MMA warp: per page one wait for P (PFULL) and the helpers (READY), then for each of
             // its two V stages the stage's wait and its MMAs of N = 256 (K steps x 2 column halves)
-            if (lane == 0) {
+            {
+                const bool leader = elect_one();
                 int done = 0;  // V stages whose MMAs were issued
                 bool ok = true;
                 for (int i = 0; i < npages && ok; ++i) {
                     const int pb = i % kPBufs;
-                    if (!(ok = wait_bar(bar(B_PFULL + pb), (i / kPBufs) & 1, abort, ds))) break;
-                    if (!(ok = wait_bar(bar(B_READY + pb), (i / kPBufs) & 1, abort, ds))) break;
+                    if (!(ok = warp_wait(bar(B_PFULL + pb), (i / kPBufs) & 1, abort, ds))) break;
+                    if (!(ok = warp_wait(bar(B_READY + pb), (i / kPBufs) & 1, abort, ds))) break;
                     tc_fence_after();  // after a rescale by the helper warps' tcgen05.st
                     const uint32_t pbuf = sbase + OFF_PB + pb * kPBufStride;
                     for (int hf = 0; hf < 2 && ok; ++hf) {
                         const int hs = 2 * i + hf, st = hs % kVStages;
-                        if (!(ok = wait_bar(bar(B_VFULL + st), (hs / kVStages) & 1, abort, ds))) break;
+                        if (!(ok = warp_wait(bar(B_VFULL + st), (hs / kVStages) & 1, abort, ds))) break;
                         tc_fence_after();  // V was written by the converter warps
                         const uint32_t vb = sbase + OFF_V + st * kVStageBytes;
 #pragma unroll
@@ -612,15 +618,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int nh = 0; nh < 2; ++nh) {
                                 const uint64_t bd = smem_desc_sw128(vb + nh * 4 * kVBox + k * 2048, kVBox, 1024);
-                                mma_ss(tmem + 256u * nh, ad, bd, kIdescPV, (i > 0 || kk > 0) ? 1u : 0u);
+                                if (leader) mma_ss(tmem + 256u * nh, ad, bd, kIdescPV, (i > 0 || kk > 0) ? 1u : 0u);
                             }
                         }
-                        mma_commit(bar(B_VEMPTY + st));
+                        if (leader) mma_commit(bar(B_VEMPTY + st));
                         done = hs + 1;
                     }
                     if (!ok) break;
                     // P buffer pb is free again (CTA 0) and O holds page i (helper warps, CTA 1)
-                    mma_commit_multicast(bar(B_PEMPTY + pb), (uint16_t)0x3);
+                    if (leader) mma_commit_multicast(bar(B_PEMPTY + pb), (uint16_t)0x3);
                 }
                 volatile int dummy = 0;  // drain the V-ring commits before teardown
                 for (int i = (done > kVStages ? done - kVStages : 0); i < done; ++i) {
@@ -640,7 +646,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (!warp_wait(bar(B_PFULL + pb), up & 1, abort, ds)) break;
                     if (ctid == 0) {
                         bar_arrive_expect_tx(bar(B_PFULL + pb), kPMsgBytes);  // the next message
-                        bar_arrive_remote(bar(B_STAGEFREE + (i & 1)), 0);   // CTA 0 may restage
+                        bar_arrive_remote_relaxed(bar(B_STAGEFREE + (i & 1)), 0);  // CTA 0 may restage
                     }
                     const uint8_t* pmsg = smem + OFF_PB + pb * kPBufStride;
                     const bool fix = i > 0 && *reinterpret_cast<const volatile uint32_t*>(pmsg + kPBytes + 512) != 0;

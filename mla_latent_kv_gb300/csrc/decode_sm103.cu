@@ -159,7 +159,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const DecodeArgs p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_addr(smem);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // warp-uniform, also to the compiler
     const uint32_t rank = cluster_ctarank();
     if (sbase & 1023u) {  // the swizzled layouts need 1024-byte aligned tiles; never expected
         if (tid == 0 && p.dev_status) atomicOr(p.dev_status, MLA_DEV_WAIT_TIMEOUT);
@@ -205,7 +206,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     cluster_sync();  // both CTAs' barriers exist before any remote arrive or copy
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM), 0);
     if (tid == 0) griddep_launch_dependents();
     if (p.plan_units || p.wait_first) {
         // The schedule (or the lengths and block table) is the preceding kernel's output: the
@@ -283,34 +284,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int qn = 0; qn < 8; ++qn)
                     tma_load_2d(sbase + q_panel_off(qn), &q_map, bar(B_QFULL), qn * 64, g.r * p.H);
                 tma_load_2d(sbase + OFF_QROPE, &q_map, bar(B_QFULL), 8 * 64, g.r * p.H);
+            }
+            __syncwarp();
+            if (npages > 0) {
+                // The whole warp runs the loop and one elected lane issues: addresses and
+                // descriptors then live in uniform registers, and an MMA costs the issuing warp a
+                // few instructions (from a lane-0 branch it took over 100 cycles).
+                const bool leader = elect_one();
+                const uint64_t rope0 = smem_desc_sw128(sbase + OFF_QROPE, 16, 1024);
                 int done = 0;
-                bool ok = wait_bar(bar(B_QREADY), 0, abort, ds);
+                bool ok = warp_wait(bar(B_QREADY), 0, abort, ds);
                 if (ok) tc_fence_after();
                 for (int gi = 0; gi < ngroups && ok; ++gi) {
                     if (gi > 0) {  // the softmax warps have read the previous S out of TMEM
-                        if (!(ok = wait_bar(bar(B_SEMPTY), (gi - 1) & 1, abort, ds))) break;
+                        if (!(ok = warp_wait(bar(B_SEMPTY), (gi - 1) & 1, abort, ds))) break;
                         tc_fence_after();
                     }
                     const uint32_t d = tmem + kSCol;
-                    for (int pn = 0; pn < 9; ++pn) {
+#pragma unroll
+                    for (int pn = 0; pn < 9; ++pn) {  // unrolled: TMEM addresses are immediate offsets
                         const int m = 9 * gi + pn, slot = m % kSlots, k = m / kSlots;
                         // TMA-written operands are ordered by the barrier itself: no tcgen05 fence
-                        if (!(ok = wait_bar(bar(B_SLOTFULL + slot), k & 1, abort, ds))) break;
-                        const uint32_t kb = sbase + OFF_RING + slot * kSlotBytes;
+                        if (!(ok = warp_wait(bar(B_SLOTFULL + slot), k & 1, abort, ds))) break;
+                        const uint64_t bd0 = smem_desc_sw128(sbase + OFF_RING + slot * kSlotBytes, 16, 1024);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const uint64_t bd = smem_desc_sw128(kb + 32 * j, 16, 1024);
-                            if (pn < 8) {
-                                mma_ts(d, tmem + 8u * (4 * pn + j), bd, kIdescQK, (pn | j) ? 1u : 0u);
-                            } else {
-                                const uint64_t ad = smem_desc_sw128(sbase + OFF_QROPE + 32 * j, 16, 1024);
-                                mma_ss(d, ad, bd, kIdescQK, 1u);
+                            const uint64_t bd = bd0 + (uint64_t)(2 * j);
+                            if (leader) {
+                                if (pn < 8)
+                                    mma_ts(d, tmem + 8u * (4 * pn + j), bd, kIdescQK, (pn | j) ? 1u : 0u);
+                                else
+                                    mma_ss(d, rope0 + (uint64_t)(2 * j), bd, kIdescQK, 1u);
                             }
                         }
-                        mma_commit(bar(B_SLOTEMPTY + slot));
+                        if (leader) mma_commit(bar(B_SLOTEMPTY + slot));
                         ++done;
                     }
-                    if (ok) mma_commit(bar(B_SFULL));
+                    if (ok && leader) mma_commit(bar(B_SFULL));
                 }
                 volatile int dummy = 0;  // drain: the last commits have landed before teardown
                 for (int m = (done > kSlots ? done - kSlots : 0); m < done; ++m) {
@@ -516,22 +526,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         } else if (warp == 1) {
-            // MMA thread: per page one wait for P (PFULL) and the helpers (READY), then for each of
+            // MMA warp: per page one wait for P (PFULL) and the helpers (READY), then for each of
             // its V stages the stage's wait and its MMAs of N = 256 (K steps x 2 column halves)
-            if (lane == 0) {
+            {
+                const bool leader = elect_one();  // as for the scores
                 int done = 0;  // V stages whose MMAs were issued
                 bool ok = true;
                 for (int i = 0; i < npages && ok; ++i) {
                     const int pb = i % kPBufs;
                     // V and P were written by the async proxy (TMA / bulk copy): the MMA thread
                     // observes their barriers itself; READY adds the helpers' rescale / zeroing.
-                    if (!(ok = wait_bar(bar(B_PFULL + pb), (i / kPBufs) & 1, abort, ds))) break;
-                    if (!(ok = wait_bar(bar(B_READY + pb), (i / kPBufs) & 1, abort, ds))) break;
+                    if (!(ok = warp_wait(bar(B_PFULL + pb), (i / kPBufs) & 1, abort, ds))) break;
+                    if (!(ok = warp_wait(bar(B_READY + pb), (i / kPBufs) & 1, abort, ds))) break;
                     tc_fence_after();  // after a rescale by the helper warps' tcgen05.st
                     const uint32_t pbuf = sbase + OFF_PB + pb * kPBufStride;
                     for (int hf = 0; hf < kVPerPage && ok; ++hf) {
                         const int hs = kVPerPage * i + hf, st = hs % kVStages;
-                        if (!(ok = wait_bar(bar(B_VFULL + st), (hs / kVStages) & 1, abort, ds))) break;
+                        if (!(ok = warp_wait(bar(B_VFULL + st), (hs / kVStages) & 1, abort, ds))) break;
                         const uint32_t vb = sbase + OFF_V + st * kVStageBytes;
 #pragma unroll
                         for (int k = 0; k < kVRows / 16; ++k) {
@@ -540,17 +551,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int nh = 0; nh < 2; ++nh) {
                                 const uint64_t bd = smem_desc_sw128(vb + nh * 4 * kVBox + k * 2048, kVBox, 1024);
-                                mma_ss(tmem + 256u * nh, ad, bd, kIdescPV, (i > 0 || kk > 0) ? 1u : 0u);
+                                if (leader) mma_ss(tmem + 256u * nh, ad, bd, kIdescPV, (i > 0 || kk > 0) ? 1u : 0u);
                             }
                         }
-                        mma_commit(bar(B_VEMPTY + st));
+                        if (leader) mma_commit(bar(B_VEMPTY + st));
                         done = hs + 1;
                     }
                     if (!ok) break;
                     // P buffer pb is free again (CTA 0) and O holds page i (helper warps, CTA 1).
                     // One barrier per P buffer keeps every waiter within one phase of it: a
                     // page's P only arrives after the PV of the page kPBufs earlier completed.
-                    mma_commit_multicast(bar(B_PEMPTY + pb), (uint16_t)0x3);
+                    if (leader) mma_commit_multicast(bar(B_PEMPTY + pb), (uint16_t)0x3);
                 }
                 volatile int dummy = 0;  // drain the V-ring commits before teardown
                 for (int i = (done > kVStages ? done - kVStages : 0); i < done; ++i) {
@@ -571,7 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!warp_wait(bar(B_PFULL + pb), up & 1, abort, ds)) break;
                 if (ctid == 0) {
                     bar_arrive_expect_tx(bar(B_PFULL + pb), kPMsgBytes);  // re-arm for the next message
-                    bar_arrive_remote(bar(B_STAGEFREE + (i & 3)), 0);     // CTA 0's staging buffer is free
+                    bar_arrive_remote_relaxed(bar(B_STAGEFREE + (i & 3)), 0);  // CTA 0's staging buffer is free
                 }
                 const uint8_t* pmsg = smem + OFF_PB + pb * kPBufStride;
                 const bool fix = i > 0 && *reinterpret_cast<const volatile uint32_t*>(pmsg + kPBytes + 512) != 0;
