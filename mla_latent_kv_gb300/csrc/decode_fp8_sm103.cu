@@ -400,13 +400,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int u = 0; u < 4; ++u) {
                             const int j = 4 * j4 + u;
-                            float x = __uint_as_float(s[c][j]) * kk[u];
-                            if (32 * c + j >= valid) x = -CUDART_INF_F;
-                            s[c][j] = __float_as_uint(x);
-                            lm = fmaxf(lm, x);
+                            s[c][j] = __float_as_uint(__uint_as_float(s[c][j]) * kk[u]);
                         }
                     }
                 }
+                if (valid < kPage) {  // a whole page needs no mask
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (32 * c + j >= valid) s[c][j] = __float_as_uint(-CUDART_INF_F);
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) lm = fmaxf(lm, __uint_as_float(s[c][j]));
                 mx[half * 128 + row] = lm;
                 named_bar(kBarMax, 256);
                 const float mt = fmaxf(lm, mx[(1 - half) * 128 + row]) * sl2;  // scale > 0
@@ -513,26 +521,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         const uint32_t raw = sbase + OFF_RAW + rs * kRawSlotBytes;
                         const uint32_t kb = sbase + OFF_KRING + ks * kKSlotBytes;
-                        // eight loads, then eight widen-and-store: the compiler cannot move a load
-                        // above an earlier store to shared memory, so batching keeps loads in flight
-#pragma unroll 1
-                        for (int k0 = 0; k0 < 24; k0 += 8) {
+                        // Panel i, rows R = rr + 16 u of the two pages: page u / 4, row pair
+                        // (rr >> 1) + 8 (u % 4), parity rr & 1 (odd rows start 8 bytes in), so that
+                        // every address is the thread's base plus a constant: these warps share
+                        // their schedulers with the softmax and pay for each instruction. Eight
+                        // loads, then eight widen-and-store: the compiler cannot move a load above
+                        // an earlier store to shared memory, so batching keeps loads in flight.
+                        const int c = ctid & 7, rr = ctid >> 3, e = rr & 1;
+                        const uint32_t src = raw + e * (kBoxBytes + 8) + (rr >> 1) * kBoxW + 8 * c;
+                        const uint32_t dst = kb + rr * 128 + ((c ^ (rr & 7)) << 4);
+                        const bool two = np == kPPG;
+#pragma unroll
+                        for (int i = 0; i < 3; ++i) {
                             uint2 v[8];
 #pragma unroll
-                            for (int u = 0; u < 8; ++u) {
-                                const int item = ctid + 128 * (k0 + u);
-                                const int c = item & 7, R = (item >> 3) & 127, i = item >> 10;
-                                const int q = R >> 6, r = R & 63, e = r & 1, j = r >> 1;
-                                // even rows start at the box's first byte, odd rows 8 bytes in
-                                v[u] = q < np ? lds_u2(raw + (2 * q + e) * kBoxBytes + j * kBoxW + 8 * e + 64 * i + 8 * c)
-                                              : make_uint2(0u, 0u);
-                            }
+                            for (int u = 0; u < 8; ++u)
+                                v[u] = u < 4 || two ? lds_u2(src + (u >> 2) * 2 * kBoxBytes + (u & 3) * 8 * kBoxW + 64 * i)
+                                                    : make_uint2(0u, 0u);
 #pragma unroll
-                            for (int u = 0; u < 8; ++u) {
-                                const int item = ctid + 128 * (k0 + u);
-                                const int c = item & 7, R = (item >> 3) & 127, i = item >> 10;
-                                if ((R >> 6) < np) sts_u4(kb + i * kKPanelBytes + R * 128 + ((c ^ (R & 7)) << 4), widen8(v[u]));
-                            }
+                            for (int u = 0; u < 8; ++u)
+                                if (u < 4 || two) sts_u4(dst + i * kKPanelBytes + u * 16 * 128, widen8(v[u]));
                         }
                         if (t == 2) {
                             // the group's scales, for the softmax warps: (k_scale, v_scale) sit in the

@@ -398,15 +398,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int pg0 = kPPG * gi + 2 * half;  // first of this half's two pages
                 const int valid0 = valid_rows(g, pg0), valid1 = valid_rows(g, pg0 + 1);
                 float lm = -CUDART_INF_F;
+                if (valid0 < kPage || valid1 < kPage) {  // whole pages need no mask
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int v = c < 2 ? valid0 - 32 * c : valid1 - 32 * (c - 2);
+                    for (int c = 0; c < 4; ++c) {
+                        const int v = c < 2 ? valid0 - 32 * c : valid1 - 32 * (c - 2);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        if (j >= v) s[c][j] = __float_as_uint(-CUDART_INF_F);
-                        lm = fmaxf(lm, __uint_as_float(s[c][j]));
+                        for (int j = 0; j < 32; ++j)
+                            if (j >= v) s[c][j] = __float_as_uint(-CUDART_INF_F);
                     }
                 }
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) lm = fmaxf(lm, __uint_as_float(s[c][j]));
                 mx[half * 128 + row] = lm;
                 named_bar(kBarMax, 256);
                 const float mt = fmaxf(lm, mx[(1 - half) * 128 + row]) * sl2;  // scale > 0
