@@ -46,9 +46,9 @@ namespace {
 using namespace ptx;
 using namespace dec;
 
-// warps: 0 producer, 1 MMA; CTA 0: 2-9 softmax, 10-13 K converters;
+// warps: 0 producer, 1 MMA; CTA 0: 2-9 softmax, 10-17 K converters;
 // CTA 1: 2-5 helpers, 6-13 V converters, 2-9 epilogue
-constexpr int kThreads = 448;
+constexpr int kThreads = 576;
 constexpr int kPPG = 2;                           // pages per group
 constexpr int kPairBytes = 2 * kFp8RowBytes;      // 1168: one row pair of the cache
 constexpr int kBoxW = 208;                        // raw box width (bytes): 192 dims + 16
@@ -109,12 +109,12 @@ __device__ __forceinline__ uint32_t q_panel_off(int pn) {
 // lands on CTA 0's B_PEMPTY slots.
 enum : int {
     B_RAWFULL = 0,                       // [kRawSlots] CTA0: raw triple landed (TMA tx)
-    B_RAWEMPTY = B_RAWFULL + kRawSlots,  // [kRawSlots] CTA0: raw triple widened (128 converter threads)
-    B_KFULL = B_RAWEMPTY + kRawSlots,    // [kKSlots] CTA0: bf16 triple written (128 converter threads)
+    B_RAWEMPTY = B_RAWFULL + kRawSlots,  // [kRawSlots] CTA0: raw triple widened (256 converter threads)
+    B_KFULL = B_RAWEMPTY + kRawSlots,    // [kKSlots] CTA0: bf16 triple written (256 converter threads)
     B_KEMPTY = B_KFULL + kKSlots,        // [kKSlots] CTA0: bf16 triple consumed by the QK MMAs
     B_SFULL = B_KEMPTY + kKSlots,        // [2] CTA0: S buffer ready
     B_SEMPTY = B_SFULL + 2,              // [2] CTA0: S buffer read by the softmax warps (256)
-    B_SCFULL = B_SEMPTY + 2,             // [2] CTA0: a group's scales written (128 converter threads)
+    B_SCFULL = B_SEMPTY + 2,             // [2] CTA0: a group's scales written (256 converter threads)
     B_SCEMPTY = B_SCFULL + 2,            // [2] CTA0: a group's scales read (256 softmax threads)
     B_QFULL = B_SCEMPTY + 2,             // CTA0: Q landed in shared memory (TMA tx)
     B_QREADY,                            // CTA0: Q latent dims moved to TMEM (256)
@@ -184,10 +184,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         *abort = 0;
         for (int i = 0; i < B_COUNT; ++i) {
             uint32_t cnt = 1;
+            if (i >= B_READY && i < B_READY + kPBufs) cnt = 128;
             if ((i >= B_RAWEMPTY && i < B_RAWEMPTY + kRawSlots) || (i >= B_KFULL && i < B_KFULL + kKSlots) ||
-                (i >= B_SCFULL && i < B_SCFULL + 2) || (i >= B_READY && i < B_READY + kPBufs))
-                cnt = 128;
-            if ((i >= B_SEMPTY && i < B_SEMPTY + 2) || (i >= B_SCEMPTY && i < B_SCEMPTY + 2) || i == B_QREADY ||
+                (i >= B_SCFULL && i < B_SCFULL + 2) || (i >= B_SEMPTY && i < B_SEMPTY + 2) || (i >= B_SCEMPTY && i < B_SCEMPTY + 2) || i == B_QREADY ||
                 (i >= B_VRAWEMPTY && i < B_VRAWEMPTY + kVRawSlots) || (i >= B_VFULL && i < B_VFULL + kVStages))
                 cnt = 256;
             bar_init(bar(i), cnt);
@@ -502,7 +501,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         } else {
-            // ---------------- K converter warps 10-13 (128 threads) ----------------
+            // ---------------- K converter warps 10-17 (256 threads) ----------------
             // Triple m = 3 gi + t of group gi: raw slot m % kRawSlots -> bf16 slot m % kKSlots,
             // three 64-dim panels x 128 rows (two pages) x 8 chunks of 8 dims. Rows of a page past
             // the unit's last page stay stale: their scores are masked by index.
@@ -521,27 +520,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         const uint32_t raw = sbase + OFF_RAW + rs * kRawSlotBytes;
                         const uint32_t kb = sbase + OFF_KRING + ks * kKSlotBytes;
-                        // Panel i, rows R = rr + 16 u of the two pages: page u / 4, row pair
-                        // (rr >> 1) + 8 (u % 4), parity rr & 1 (odd rows start 8 bytes in), so that
+                        // Panel i, rows R = rr + 32 u of the two pages: page u / 2, row pair
+                        // (rr >> 1) + 16 (u % 2), parity rr & 1 (odd rows start 8 bytes in), so that
                         // every address is the thread's base plus a constant: these warps share
-                        // their schedulers with the softmax and pay for each instruction. Eight
-                        // loads, then eight widen-and-store: the compiler cannot move a load above
-                        // an earlier store to shared memory, so batching keeps loads in flight.
+                        // their schedulers with the softmax and pay for each instruction. All loads,
+                        // then the widen-and-stores: the compiler cannot move a load above an
+                        // earlier store to shared memory, so batching keeps loads in flight.
                         const int c = ctid & 7, rr = ctid >> 3, e = rr & 1;
                         const uint32_t src = raw + e * (kBoxBytes + 8) + (rr >> 1) * kBoxW + 8 * c;
                         const uint32_t dst = kb + rr * 128 + ((c ^ (rr & 7)) << 4);
                         const bool two = np == kPPG;
+                        uint2 v[3][4];
 #pragma unroll
-                        for (int i = 0; i < 3; ++i) {
-                            uint2 v[8];
+                        for (int i = 0; i < 3; ++i)
 #pragma unroll
-                            for (int u = 0; u < 8; ++u)
-                                v[u] = u < 4 || two ? lds_u2(src + (u >> 2) * 2 * kBoxBytes + (u & 3) * 8 * kBoxW + 64 * i)
-                                                    : make_uint2(0u, 0u);
+                            for (int u = 0; u < 4; ++u)
+                                v[i][u] = u < 2 || two ? lds_u2(src + (u >> 1) * 2 * kBoxBytes + (u & 1) * 16 * kBoxW + 64 * i)
+                                                       : make_uint2(0u, 0u);
 #pragma unroll
-                            for (int u = 0; u < 8; ++u)
-                                if (u < 4 || two) sts_u4(dst + i * kKPanelBytes + u * 16 * 128, widen8(v[u]));
-                        }
+                        for (int i = 0; i < 3; ++i)
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                if (u < 2 || two) sts_u4(dst + i * kKPanelBytes + u * 32 * 128, widen8(v[i][u]));
                         if (t == 2) {
                             // the group's scales, for the softmax warps: (k_scale, v_scale) sit in the
                             // 8 bytes after the row's 576 codes. Rows past the last visible token get
@@ -549,14 +549,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             const int sb = gi & 1;
                             if (gi >= 2 && !(ok = warp_wait(bar(B_SCEMPTY + sb), ((gi >> 1) - 1) & 1, abort, ds)))
                                 break;
-                            const int q = ctid >> 6, r = ctid & 63, e = r & 1, j = r >> 1;
+                            const int q = ctid >> 6, r = ctid & 63, e = r & 1, j = r >> 1;  // q 0, 1: 128 tokens
                             float2 sc = make_float2(0.f, 0.f);
                             if (q < np && r < valid_rows(g, kPPG * gi + q)) {
                                 const uint2 w = lds_u2(raw + (2 * q + e) * kBoxBytes + j * kBoxW + 8 * e + 192);
                                 sc = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
                             }
-                            reinterpret_cast<float*>(smem + OFF_KSC)[128 * sb + ctid] = sc.x;
-                            reinterpret_cast<float*>(smem + OFF_VSC)[128 * sb + ctid] = sc.y;
+                            if (ctid < 128) {
+                                reinterpret_cast<float*>(smem + OFF_KSC)[128 * sb + ctid] = sc.x;
+                                reinterpret_cast<float*>(smem + OFF_VSC)[128 * sb + ctid] = sc.y;
+                            }
                             bar_arrive(bar(B_SCFULL + sb));
                         }
                         fence_proxy_async_cta();  // generic-proxy writes before the MMAs read them
@@ -677,7 +679,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     bar_arrive(bar(B_READY + pb));
                     pages_ready = i + 1;
                 }
-            } else {
+            } else if (warp < 14) {
                 // ------------- V converter warps 6-13 (256 threads) -------------
                 // half page hs: raw slot hs % kVRawSlots -> V stage hs % kVStages, 32 rows x 8
                 // panels x 8 chunks; rows past the last visible token (or of a page that was not
