@@ -513,11 +513,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int t = 0; t < 3 && ok; ++t) {
                         const int m = 3 * gi + t, rs = m % kRawSlots, ks = m % kKSlots;
                         if (!(ok = warp_wait(bar(B_RAWFULL + rs), (m / kRawSlots) & 1, abort, ds))) break;
-                        // the bf16 slot: its previous triple's MMAs have completed (the first two
-                        // uses: Q's panels have been moved out to TMEM)
-                        ok = m >= kKSlots ? warp_wait(bar(B_KEMPTY + ks), ((m / kKSlots) - 1) & 1, abort, ds)
-                                          : warp_wait(bar(B_QREADY), 0, abort, ds);
-                        if (!ok) break;
                         const uint32_t raw = sbase + OFF_RAW + rs * kRawSlotBytes;
                         const uint32_t kb = sbase + OFF_KRING + ks * kKSlotBytes;
                         // Panel i, rows R = rr + 32 u of the two pages: page u / 2, row pair
@@ -537,6 +532,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             for (int u = 0; u < 4; ++u)
                                 v[i][u] = u < 2 || two ? lds_u2(src + (u >> 1) * 2 * kBoxBytes + (u & 1) * 16 * kBoxW + 64 * i)
                                                        : make_uint2(0u, 0u);
+                        // the bf16 slot: its previous triple's MMAs have completed (the first two
+                        // uses: Q's panels have been moved out to TMEM)
+                        ok = m >= kKSlots ? warp_wait(bar(B_KEMPTY + ks), ((m / kKSlots) - 1) & 1, abort, ds)
+                                          : warp_wait(bar(B_QREADY), 0, abort, ds);
+                        if (!ok) break;
 #pragma unroll
                         for (int i = 0; i < 3; ++i)
 #pragma unroll
@@ -692,27 +692,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int hf = 0; hf < 2; ++hf) {
                         const int hs = 2 * i + hf, rs = hs % kVRawSlots, st = hs % kVStages;
                         if (!(ok = warp_wait(bar(B_VRAWFULL + rs), (hs / kVRawSlots) & 1, abort, ds))) break;
-                        if (hs >= kVStages &&
-                            !(ok = warp_wait(bar(B_VEMPTY + st), ((hs / kVStages) - 1) & 1, abort, ds)))
-                            break;
                         const bool copied = *reinterpret_cast<const volatile int*>(raw_ok + rs) != 0;
                         const uint32_t raw = sbase + OFF_VRAW + rs * kHalfPageBytes;
                         const uint32_t vb = sbase + OFF_V + st * kVStageBytes;
-                        // all eight loads first (see the K converters)
+                        // Chunk c of panel pn, rows r0 + 4 k: constant offsets, and all eight loads
+                        // first, before the wait for the stage (see the K converters)
+                        const int c = ctid & 7, pn = (ctid >> 3) & 7, r0 = ctid >> 6;  // r0 < 4
+                        const uint32_t src = raw + r0 * kFp8RowBytes + 64 * pn + 8 * c;
+                        const int left = copied ? valid - kVRows * hf - r0 : 0;  // rows k with 4 k < left are read
                         uint2 v[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int item = ctid + 256 * k;
-                            const int c = item & 7, pn = (item >> 3) & 7, r = item >> 6;
-                            v[k] = copied && kVRows * hf + r < valid ? lds_u2(raw + r * kFp8RowBytes + 64 * pn + 8 * c)
-                                                                     : make_uint2(0u, 0u);
-                        }
+                        for (int k = 0; k < 8; ++k)
+                            v[k] = 4 * k < left ? lds_u2(src + k * 4 * kFp8RowBytes) : make_uint2(0u, 0u);
+                        if (hs >= kVStages &&
+                            !(ok = warp_wait(bar(B_VEMPTY + st), ((hs / kVStages) - 1) & 1, abort, ds)))
+                            break;
+                        // rows r0 + 4 k are r0 (k even) or r0 + 4 (k odd) within the swizzle's eight
+                        const uint32_t dst0 = vb + pn * kVBox + r0 * 128 + ((c ^ r0) << 4);
+                        const uint32_t dst1 = vb + pn * kVBox + (r0 + 4) * 128 + ((c ^ (r0 + 4)) << 4);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int item = ctid + 256 * k;
-                            const int c = item & 7, pn = (item >> 3) & 7, r = item >> 6;
-                            sts_u4(vb + pn * kVBox + r * 128 + ((c ^ (r & 7)) << 4), widen8(v[k]));
-                        }
+                        for (int k = 0; k < 8; ++k) sts_u4((k & 1 ? dst1 : dst0) + (k >> 1) * 1024, widen8(v[k]));
                         fence_proxy_async_cta();  // generic-proxy writes before the MMAs read them
                         bar_arrive(bar(B_VFULL + st));
                         bar_arrive(bar(B_VRAWEMPTY + rs));
