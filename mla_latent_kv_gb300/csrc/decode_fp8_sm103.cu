@@ -174,7 +174,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     const int unit = (int)(blockIdx.x >> 1);
     RowGeom g{};
-    if (!p.plan_units && !p.wait_first)
+    if (!p.plan_units && p.order != kOrderWaitFirst)
         g = row_geometry(p, unit, tid == 0 && rank == 0);  // its loads overlap the set-up
     volatile int* abort = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
     int32_t* ds = p.dev_status;
@@ -205,11 +205,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();  // both CTAs' barriers exist before any remote arrive or store
     const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM), 0);
     if (tid == 0) griddep_launch_dependents();
-    if (p.plan_units || p.wait_first) {
+    if (p.plan_units || p.order == kOrderWaitFirst) {
         // The schedule (or the lengths and block table) is the preceding kernel's output: the
         // set-up above overlapped it. Clusters past the schedule's unit count leave together
         // (both CTAs read the same count).
-        griddep_wait();
+        if (p.order != kOrderFree) griddep_wait();
         if (p.plan_units && unit >= *p.plan_count) {
             if (warp == 0) tmem_dealloc(tmem, kTmemCols);
             cluster_sync();
@@ -243,7 +243,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int t = 0; t < 3; ++t) {
                         const int m = 3 * gi + t, slot = m % kRawSlots, k = m / kRawSlots;
                         if (!q_issued && m == 2) {
-                            griddep_wait();
+                            if (p.order != kOrderFree) griddep_wait();
                             bar_arrive_expect_tx(bar(B_QFULL), 9 * kQPanelBytes);
                             for (int qn = 0; qn < 8; ++qn)
                                 tma_load_2d(sbase + q_panel_off(qn), &q_map, bar(B_QFULL), qn * 64, g.r * p.H);

@@ -327,6 +327,14 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 // No early exit from this loop: all 512 threads must pass the same named barriers
                 // (which cannot time out); after an abort the waits return at once.
                 const int page = kPPG * gi + pg2, buf = gi & 1;
+                size_t sc = 0;               // the quarter's first token of the page, in float4 units
+                float4 ks[kScaled ? 8 : 1];  // k_scale of its 32 tokens, loaded while S is on its way
+                if constexpr (kScaled) {
+                    sc = ((size_t)(page0 + min(page, npages - 1)) * kPage + 32 * sub) / 4;
+                    const float4* src = reinterpret_cast<const float4*>(p.k_scales) + sc;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) ks[j] = __ldg(src + j);
+                }
                 const bool okS = warp_wait<true>(bar(B_SFULL + buf), (gi >> 1) & 1, abort, ds);
                 uint32_t s[32];
                 if (okS) {
@@ -340,16 +348,18 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(-CUDART_INF_F);
                 }
-                const float4* sc = nullptr;  // (k_scale, v_scale) of two tokens each
+                float4 vs[kScaled ? 8 : 1];  // v_scale of this quarter's 32 tokens, on their way early
                 if constexpr (kScaled) {
-                    sc = reinterpret_cast<const float4*>(p.scales + (size_t)(page0 + min(page, npages - 1)) * kPage +
-                                                         32 * sub);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float4 x = __ldg(sc + j);
-                        s[2 * j] = __float_as_uint(__uint_as_float(s[2 * j]) * x.x);
-                        s[2 * j + 1] = __float_as_uint(__uint_as_float(s[2 * j + 1]) * x.z);
+                    for (int j = 0; j < 8; ++j) {
+                        s[4 * j] = __float_as_uint(__uint_as_float(s[4 * j]) * ks[j].x);
+                        s[4 * j + 1] = __float_as_uint(__uint_as_float(s[4 * j + 1]) * ks[j].y);
+                        s[4 * j + 2] = __float_as_uint(__uint_as_float(s[4 * j + 2]) * ks[j].z);
+                        s[4 * j + 3] = __float_as_uint(__uint_as_float(s[4 * j + 3]) * ks[j].w);
                     }
+                    const float4* src = reinterpret_cast<const float4*>(p.v_scales) + sc;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) vs[j] = __ldg(src + j);
                 }
                 if (page >= npages || warp_lim < (page + 1) * kPage) {  // some row does not see all of the page
                     const int v = page >= npages ? 0 : lim - page * kPage - 32 * sub;
@@ -385,9 +395,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     l4[2 * (j & 1)] += a0;
                     l4[2 * (j & 1) + 1] += a1;
                     if constexpr (kScaled) {
-                        const float4 x = __ldg(sc + j);
-                        a0 *= x.y;
-                        a1 *= x.w;
+                        a0 *= j & 1 ? vs[j >> 1].z : vs[j >> 1].x;
+                        a1 *= j & 1 ? vs[j >> 1].w : vs[j >> 1].y;
                     }
                     pk[j] = pack_bf16x2(a0, a1);
                 }
@@ -592,7 +601,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
 // 8-byte chunks of the 576 codes.
 // ------------------------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) prefix_widen_kernel(PrefixArgs p, const uint8_t* cache, uint16_t* x,
-                                                           float2* scales) {
+                                                           float* k_scales, float* v_scales) {
     griddep_wait();
     griddep_launch_dependents();
     const int token = (int)blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -611,7 +620,11 @@ __global__ void __launch_bounds__(256) prefix_widen_kernel(PrefixArgs p, const u
             make_uint4(e4m3x2_to_bf16x2(v.x & 0xffffu), e4m3x2_to_bf16x2(v.x >> 16), e4m3x2_to_bf16x2(v.y & 0xffffu),
                        e4m3x2_to_bf16x2(v.y >> 16));
     }
-    if (lane == 0) scales[token] = bad ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2*>(src + kD);
+    if (lane == 0) {
+        const float2 sc = bad ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2*>(src + kD);
+        k_scales[token] = sc.x;
+        v_scales[token] = sc.y;
+    }
 }
 
 int g_attr_done[2][64] = {};
@@ -675,7 +688,7 @@ void prefix_split(int64_t flat_rows, int pages, int clusters, int* splits, int* 
 }
 
 cudaError_t launch_decode_prefix(const PrefixArgs& in, const uint8_t* cache, bool fp8, uint16_t* widened,
-                                 float2* scales, cudaStream_t s) {
+                                 float* scales, cudaStream_t s) {
     PrefixArgs a = in;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -685,11 +698,13 @@ cudaError_t launch_decode_prefix(const PrefixArgs& in, const uint8_t* cache, boo
     const void* base = cache;
     uint64_t rows = (uint64_t)a.num_blocks * kPage;
     if (fp8) {
+        float* v_scales = scales + (size_t)a.prefix_pages * kPage;
         e = launch_pdl(prefix_widen_kernel, dim3((unsigned)(a.prefix_pages * kPage / 8)), dim3(256), 0, s, a, cache,
-                       widened, scales);
+                       widened, scales, v_scales);
         if (e != cudaSuccess) return e;
         a.block_table = nullptr;
-        a.scales = scales;
+        a.k_scales = scales;
+        a.v_scales = v_scales;
         base = widened;
         rows = (uint64_t)a.prefix_pages * kPage;
     }

@@ -172,14 +172,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // (validated once the page count is known).
     int blk_early[kPPG] = {-1, -1, -1, -1};
     const bool early_blocks =
-        p.plan_units == nullptr && p.qsl == nullptr && !p.wait_first && unit % p.num_splits == 0;
+        p.plan_units == nullptr && p.qsl == nullptr && p.order != kOrderWaitFirst && unit % p.num_splits == 0;
     if (early_blocks && tid == 0 && rank == 0) {
 #pragma unroll
         for (int q = 0; q < kPPG; ++q)
             if (p.base / kPage + q < p.max_blocks) blk_early[q] = ld_nc_s32(table_entry(p, unit / p.num_splits / p.Sq, q));
     }
     RowGeom g{};
-    if (!p.plan_units && !p.wait_first)
+    if (!p.plan_units && p.order != kOrderWaitFirst)
         g = row_geometry(p, unit, tid == 0 && rank == 0);  // its loads overlap the set-up
     volatile int* abort = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
     int32_t* ds = p.dev_status;
@@ -208,11 +208,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();  // both CTAs' barriers exist before any remote arrive or copy
     const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM), 0);
     if (tid == 0) griddep_launch_dependents();
-    if (p.plan_units || p.wait_first) {
+    if (p.plan_units || p.order == kOrderWaitFirst) {
         // The schedule (or the lengths and block table) is the preceding kernel's output: the
         // set-up above overlapped it. Clusters past the schedule's unit count leave together
         // (both CTAs read the same count).
-        griddep_wait();
+        if (p.order != kOrderFree) griddep_wait();
         if (p.plan_units && unit >= *p.plan_count) {
             if (warp == 0) tmem_dealloc(tmem, kTmemCols);
             cluster_sync();
@@ -279,7 +279,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // Q, the preceding kernel's output, is loaded from here so that it goes out at
                 // once, in parallel with the producer's block-table reads and first K panels.
                 tma_prefetch_desc(&q_map);
-                griddep_wait();
+                if (p.order != kOrderFree) griddep_wait();
                 bar_arrive_expect_tx(bar(B_QFULL), 9 * kQPanelBytes);
                 for (int qn = 0; qn < 8; ++qn)
                     tma_load_2d(sbase + q_panel_off(qn), &q_map, bar(B_QFULL), qn * 64, g.r * p.H);

@@ -17,6 +17,12 @@ constexpr int kPage = MLA_PAGE_SIZE;  // 64 tokens per page
 constexpr int kBf16RowBytes = 2 * kD; // 1152
 constexpr int kFp8RowBytes = kD + 8;  // 584
 
+// What a decode kernel may read before the kernel ahead of it in the stream has ended: weights, cache
+// and block table (the default: kernels of the library write none of them; q and a device-built
+// schedule wait), nothing (the one ahead writes the lengths and the block table), or everything
+// (the one ahead began only after all before it had ended, and writes nothing that is read here).
+enum { kOrderDefault = 0, kOrderWaitFirst = 1, kOrderFree = 2 };
+
 // Everything a decode launch needs, resolved and validated on the host.
 struct DecodeArgs {
     const uint16_t* q;          // bf16 [B, Sq, H, 576]
@@ -35,7 +41,7 @@ struct DecodeArgs {
     int shared_pages;           // the first pages of every request are those of block_table's row 0
     int base;                   // tokens (whole pages) at the front of every request that are left out
     int all_partial;            // every unit writes a partial state, also the only one of its row
-    int wait_first;             // lengths and block table are the preceding kernel's output
+    int order;                  // kOrder*: what the kernel may read before the preceding one ends
     const float* pre_o;         // partial states of every row over the base tokens, merged with the
     const float* pre_lse;       // row's own: [pre_splits, rows, H, 512] and [pre_splits, rows, H]
     int pre_splits;             // (0: none)
@@ -202,7 +208,10 @@ struct DecodeExtra {
     int shared_pages = 0;            // see DecodeArgs
     int base = 0;
     bool all_partial = false;
-    bool wait_first = false;
+    int order = kOrderDefault;
+    // launched between the schedule and the decode (null: nothing); its error ends the call
+    cudaError_t (*between)(void*) = nullptr;
+    void* between_arg = nullptr;
     const float* pre_o = nullptr;
     const float* pre_lse = nullptr;
     int pre_splits = 0;
@@ -224,7 +233,8 @@ struct PrefixArgs {
     int64_t num_blocks;
     int key_rows;               // rows behind the keys' tensor map
     int prefix_pages, splits, pages_per_split;
-    const float2* scales;       // FP8: per prefix token (k_scale, v_scale)
+    const float* k_scales;      // FP8: per prefix token
+    const float* v_scales;
     const int32_t* seq_lens;    // [B]
     int max_seq_len, Sq, H;
     float scale;
@@ -234,9 +244,10 @@ struct PrefixArgs {
 };
 int prefix_clusters();  // clusters of the prefix kernel that run at once on the current device, or -1
 void prefix_split(int64_t flat_rows, int pages, int clusters, int* splits, int* pages_per_split);
-// FP8: the prefix's rows are widened into `widened` [prefix tokens, 576] and `scales` first.
+// FP8: the prefix's rows are widened into `widened` [prefix tokens, 576] and `scales` [2, prefix
+// tokens] first.
 cudaError_t launch_decode_prefix(const PrefixArgs& a, const uint8_t* cache, bool fp8, uint16_t* widened,
-                                 float2* scales, cudaStream_t s);
+                                 float* scales, cudaStream_t s);
 
 // Record an error for mla_last_error_detail() and return `st` (printf-style message).
 mla_status set_error(mla_status st, const char* fmt, ...);

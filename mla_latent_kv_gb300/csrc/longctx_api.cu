@@ -57,6 +57,19 @@ struct PrefixPlan {
     int own_splits;                      // resolved, of the requests' own tokens
     size_t widened, scales, part_o, part_lse, decode, total;
 };
+// The prefix kernel's launch, as a step of the decode that follows it.
+struct PrefixLaunch {
+    mla::PrefixArgs a;
+    const uint8_t* cache;
+    bool fp8;
+    uint16_t* widened;
+    float* scales;
+    cudaStream_t stream;
+    static cudaError_t run(void* self) {
+        const PrefixLaunch& l = *static_cast<const PrefixLaunch*>(self);
+        return mla::launch_decode_prefix(l.a, l.cache, l.fp8, l.widened, l.scales, l.stream);
+    }
+};
 bool plan_prefix(mla_kv_dtype kv, int rows, int H, int prefix_len, int num_splits, int max_seq_len, PrefixPlan* w) {
     // tokens past max_seq_len are no request's
     const int pages = std::min(prefix_len, (max_seq_len + mla::kPage - 1) / mla::kPage * mla::kPage) / mla::kPage;
@@ -71,7 +84,7 @@ bool plan_prefix(mla_kv_dtype kv, int rows, int H, int prefix_len, int num_split
             w->widened = off;
             off += up256((size_t)pages * mla::kPage * mla::kBf16RowBytes);
             w->scales = off;
-            off += up256((size_t)pages * mla::kPage * sizeof(float2));
+            off += up256((size_t)pages * mla::kPage * 2 * sizeof(float));
         }
         w->part_o = off;
         off += up256((size_t)w->splits * flat * mla::kL * sizeof(float));
@@ -253,7 +266,7 @@ mla_status mla_decode_sparse(const void* q, const void* kv_cache, mla_kv_dtype k
     if (e != cudaSuccess) return cuda_error(e, who);
     mla::DecodeExtra x;
     x.who = who;
-    x.wait_first = true;
+    x.order = mla::kOrderWaitFirst;
     return mla::decode_impl(q, kv_cache, kv_dtype, num_blocks, t.table, max_sel, t.lens, nullptr, max_sel * mla::kPage,
                             rows, 1, rows, H, scale, S, (char*)workspace + w.decode, w.total - w.decode, o_latent,
                             o_dtype, lse, dev_status, stream, x);
@@ -305,8 +318,9 @@ mla_status mla_decode_shared_prefix(const void* q, const void* kv_cache, mla_kv_
     if (w.total > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return set_error(MLA_ERR_UNSUPPORTED, "%s: workspace must be 256-byte aligned", who);
     char* ws = (char*)workspace;
+    PrefixLaunch launch{};
     if (w.splits > 0) {
-        mla::PrefixArgs a{};
+        mla::PrefixArgs& a = launch.a;
         a.q = (const uint16_t*)q;
         a.flat_rows = B * Sq * H;
         a.block_table = block_table;
@@ -322,13 +336,19 @@ mla_status mla_decode_shared_prefix(const void* q, const void* kv_cache, mla_kv_
         a.part_o = (float*)(ws + w.part_o);
         a.part_lse = (float*)(ws + w.part_lse);
         a.dev_status = dev_status;
-        const cudaError_t e = mla::launch_decode_prefix(
-            a, (const uint8_t*)kv_cache, kv_dtype == MLA_KV_FP8_E4M3_SCALED, (uint16_t*)(ws + w.widened),
-            (float2*)(ws + w.scales), (cudaStream_t)stream);
-        if (e != cudaSuccess) return cuda_error(e, who);
         x.base = w.pages * mla::kPage;
         x.all_partial = true;
-        x.wait_first = true;  // no cached row is read before the kernels ahead of this call have ended
+        // The prefix kernel goes between the schedule and the decode of the requests' own tokens. It
+        // lets that one start once all of its clusters run, which is after everything ahead of this
+        // call has ended: the decode takes the SMs that the prefix leaves and reads what it likes.
+        launch.cache = (const uint8_t*)kv_cache;
+        launch.fp8 = kv_dtype == MLA_KV_FP8_E4M3_SCALED;
+        launch.widened = (uint16_t*)(ws + w.widened);
+        launch.scales = (float*)(ws + w.scales);
+        launch.stream = (cudaStream_t)stream;
+        x.between = &PrefixLaunch::run;
+        x.between_arg = &launch;
+        x.order = mla::kOrderFree;
         x.pre_o = a.part_o;
         x.pre_lse = a.part_lse;
         x.pre_splits = w.splits;

@@ -272,7 +272,7 @@ mla_status decode_impl(const void* q, const void* kv_cache, mla_kv_dtype kv_dtyp
     a.shared_pages = x.shared_pages;
     a.base = x.base;
     a.all_partial = x.all_partial ? 1 : 0;
-    a.wait_first = x.wait_first ? 1 : 0;
+    a.order = x.order;
     a.pre_o = x.pre_o;
     a.pre_lse = x.pre_lse;
     a.pre_splits = x.pre_splits;
@@ -299,6 +299,10 @@ mla_status decode_impl(const void* q, const void* kv_cache, mla_kv_dtype kv_dtyp
     if (planned) {
         e = mla::launch_plan(a, pairs, st);
         if (e != cudaSuccess) return cuda_fail(e, x.who, "schedule launch");
+    }
+    if (x.between) {
+        e = x.between(x.between_arg);
+        if (e != cudaSuccess) return cuda_fail(e, x.who, "launch");
     }
     e = fp8 ? mla::launch_decode_fp8_sm103(a, st) : mla::launch_decode_sm103(a, st);
     if (e != cudaSuccess) return cuda_fail(e, x.who, "decode launch");
