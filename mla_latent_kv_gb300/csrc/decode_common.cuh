@@ -48,6 +48,18 @@ __device__ __forceinline__ int page_block(const DecodeArgs& p, int b, int pg) {
     return blk;
 }
 
+// Before a unit's output is written. By default the kernel ahead in the stream may still read the
+// buffers, so its end is awaited. With kOrderFree nothing in flight touches them, and only the last
+// unit waits: the grid must not end before the kernel ahead does, since the kernel behind waits for
+// this grid alone and reads the other's output too.
+__device__ __forceinline__ void output_wait(const DecodeArgs& p, int unit) {
+    if (p.order == kOrderFree) {
+        const int last = p.plan_units ? *p.plan_count - 1 : p.rows * p.num_splits - 1;
+        if (unit != last) return;
+    }
+    ptx::griddep_wait();
+}
+
 // A bounded mbarrier wait taken by a whole warp: true only if every lane's wait succeeded.
 template <bool kCluster = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* ds) {

@@ -722,8 +722,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // ------------- epilogue, warps 2-9 (each warp set stages half of the panels) -------------
                 const int etid = tid - 64;  // 0..255
                 const int eset = warp >= 6 ? 1 : 0;
-                // outputs may still be read by the preceding kernel until it completes
-                griddep_wait();
+                output_wait(p, unit);
                 const bool has_o = npages > 0 && pages_ready == npages && !*abort;
                 wait_bar<true>(bar(B_STATS), 0, abort, ds);
                 const bool o_ok =

@@ -654,8 +654,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int l = ptid; l < kPage * kBf16RowBytes / 128; l += 128) prefetch_l2(page + 128 * l);
                 }
             }
-            // epilogue (outputs may still be read by the preceding kernel until it completes)
-            griddep_wait();
+            // epilogue
+            output_wait(p, unit);
             const bool has_o = npages > 0 && pages_ready == npages && !*abort;
             wait_bar<true>(bar(B_STATS), 0, abort, ds);
             const bool o_ok =
