@@ -100,7 +100,7 @@ static_assert(kBoxBytes % 128 == 0, "TMA boxes start on 128-byte boundaries");
 // the softmax warps move them to TMEM.
 static_assert(6 * kQPanelBytes == kKSlots * kKSlotBytes && 2 * kQPanelBytes <= 2 * kPMsgBytes, "Q panel homes");
 // the epilogue stages its output tiles over the V ring, the raw ring and the P buffers
-static_assert(OFF_V + 8 * 128 * 128 <= kSmem1, "epilogue tiles");
+static_assert(OFF_V + 12 * kTileBytes <= kSmem1, "epilogue tiles");
 __device__ __forceinline__ uint32_t q_panel_off(int pn) {
     return pn < 6 ? OFF_KRING + pn * kQPanelBytes : OFF_STAGE + (pn - 6) * kQPanelBytes;
 }
@@ -148,8 +148,7 @@ constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 256, false, true);
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr uint32_t kBarMax = 1, kBarOr = 2, kBarHalf0 = 3;  // named barriers of the softmax warps
 constexpr uint32_t kBarStage0 = 5;                          // + half: one half's P staging
-constexpr uint32_t kBarEpi = 4;                             // named barrier of CTA 1's epilogue warps
-constexpr int kEpiPanelBytes = 128 * 128;
+constexpr uint32_t kBarEpi = 4;                             // [2] named barriers of CTA 1's epilogue sets
 
 // Eight e4m3 codes -> eight bf16 (exact), as one 16-byte chunk of a bf16 row.
 __device__ __forceinline__ uint4 widen8(uint2 v) {
@@ -742,88 +741,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     else if (p.lse)
                         p.lse[(size_t)g.r * p.H + row] = lse_v;
                 }
-                // O / l leaves through TMA stores: each 128-byte-wide column panel of the 128 x 512
-                // result is written to a swizzled shared tile (the rings are idle now) and stored as
-                // one box of H rows. fp32 output: two rounds of eight 32-column panels; bf16: one
-                // round of eight 64-column panels.
-                const bool out_f32 = g.slot >= 0 || p.o_dtype == MLA_DT_F32;
-                const int rounds = out_f32 ? 2 : 1;
+                // O / l leaves through TMA stores over the rings, which are idle now
                 const int zc = g.slot >= 0 ? g.slot : g.r;
                 const CUtensorMap* omap = g.slot >= 0 ? &p_map : &o_map;
-                for (int rd = 0; rd < rounds; ++rd) {
-                    if (rd > 0) {  // the previous round's stores have read their tiles
-                        if (etid == 0) bulk_wait_group_read<0>();
-                        named_bar(kBarEpi, 256);
-                    }
-                    if (out_f32) {
-                        // this warp set's four 32-column panels, two at a time (register budget)
-#pragma unroll 1
-                        for (int q0 = 0; q0 < 4; q0 += 2) {
-                            uint32_t v[2][32];
-                            if (use_o) {
-#pragma unroll
-                                for (int q = 0; q < 2; ++q)
-                                    tmem_ld32(tmem + lane_base + (uint32_t)(rd * 256 + (4 * eset + q0 + q) * 32), v[q]);
-                                tmem_wait_ld();
-                            } else {
-#pragma unroll
-                                for (int q = 0; q < 2; ++q)
-#pragma unroll
-                                    for (int j = 0; j < 32; ++j) v[q][j] = 0u;
-                            }
-                            if (live) {
-#pragma unroll
-                                for (int q = 0; q < 2; ++q) {
-                                    uint8_t* tile = smem + OFF_V + (4 * eset + q0 + q) * kEpiPanelBytes;
-#pragma unroll
-                                    for (int c = 0; c < 8; ++c)
-                                        *reinterpret_cast<uint4*>(tile + row * 128 + ((c ^ (row & 7)) << 4)) =
-                                            make_uint4(__float_as_uint(__uint_as_float(v[q][4 * c]) * inv),
-                                                       __float_as_uint(__uint_as_float(v[q][4 * c + 1]) * inv),
-                                                       __float_as_uint(__uint_as_float(v[q][4 * c + 2]) * inv),
-                                                       __float_as_uint(__uint_as_float(v[q][4 * c + 3]) * inv));
-                                }
-                            }
-                        }
-                    } else {
-#pragma unroll 1
-                        for (int pl = 4 * eset; pl < 4 * eset + 4; ++pl) {
-                            uint8_t* tile = smem + OFF_V + pl * kEpiPanelBytes;
-                            const int col0 = pl * 64;
-                            uint32_t v[2][32];
-#pragma unroll
-                            for (int h2 = 0; h2 < 2; ++h2) {
-                                if (use_o) {
-                                    tmem_ld32(tmem + lane_base + (uint32_t)(col0 + 32 * h2), v[h2]);
-                                } else {
-#pragma unroll
-                                    for (int j = 0; j < 32; ++j) v[h2][j] = 0u;
-                                }
-                            }
-                            if (use_o) tmem_wait_ld();
-                            if (live) {
-#pragma unroll
-                                for (int c = 0; c < 8; ++c) {
-                                    const uint32_t* w = &v[c >> 2][8 * (c & 3)];
-                                    *reinterpret_cast<uint4*>(tile + row * 128 + ((c ^ (row & 7)) << 4)) = make_uint4(
-                                        pack_bf16x2(__uint_as_float(w[0]) * inv, __uint_as_float(w[1]) * inv),
-                                        pack_bf16x2(__uint_as_float(w[2]) * inv, __uint_as_float(w[3]) * inv),
-                                        pack_bf16x2(__uint_as_float(w[4]) * inv, __uint_as_float(w[5]) * inv),
-                                        pack_bf16x2(__uint_as_float(w[6]) * inv, __uint_as_float(w[7]) * inv));
-                                }
-                            }
-                        }
-                    }
-                    fence_proxy_async_cta();
-                    named_bar(kBarEpi, 256);
-                    if (etid == 0) {
-                        const int cpp = out_f32 ? 32 : 64;  // columns per panel
-                        for (int pl = 0; pl < 8; ++pl)
-                            tma_store_3d(omap, sbase + OFF_V + pl * kEpiPanelBytes, rd * 256 + pl * cpp, 0, zc);
-                        bulk_commit_group();
-                    }
-                }
-                if (etid == 0) bulk_wait_group<0>();  // the stores are complete before the CTA exits
+                const bool issuer = (etid & 127) == 0;
+                if (g.slot >= 0 || p.o_dtype == MLA_DT_F32)
+                    store_rows<true, 2, 6, kBarEpi>(smem, sbase, OFF_V, tmem + lane_base, row, eset, issuer, live,
+                                                    empty, inv, omap, 0, zc, true);
+                else
+                    store_rows<false, 2, 6, kBarEpi>(smem, sbase, OFF_V, tmem + lane_base, row, eset, issuer, live,
+                                                     empty, inv, omap, 0, zc, true);
             }
         }
     }

@@ -54,6 +54,7 @@ cudaError_t encode_tmap(CUtensorMap* map, CUtensorMapDataType dtype, int rank, c
 namespace {
 
 using namespace ptx;
+using dec::store_rows;
 using dec::warp_wait;
 
 constexpr int kThreads = 576;  // warp 0 TMA, warp 1 MMA, warps 2-17 softmax / 2-5 helpers, 2-17 epilogue
@@ -88,7 +89,7 @@ static_assert(kPMsgBytes <= kPBufStride, "P message");
 static_assert(OFF_RING % 1024 == 0 && OFF_STAGE % 1024 == 0 && OFF_PB % 1024 == 0 && kPBufStride % 1024 == 0 &&
                   kSlotBytes % 1024 == 0,
               "128-byte swizzled tiles need 1024-byte alignment");
-static_assert(8 * 128 * 128 <= kSmem1 - OFF_V, "epilogue tiles");
+static_assert(OFF_V + 12 * dec::kTileBytes <= kSmem1, "epilogue tiles");
 // Q's latent panels land in the four staging buffers (panels 0-3) and at the end of the ring
 // (panels 4-7, over slots 2-4), so that the first keys can load into slots 0 and 1 at once.
 static_assert(kSlots == 5 && kStages == 4 && 4 * kQPanelBytes <= 3 * kSlotBytes, "Q panel homes");
@@ -128,8 +129,8 @@ constexpr uint32_t kSCol = 256;  // scores: Q latent in columns [0, 256), S buff
 constexpr uint32_t kIdescQK = idesc_bf16_f32(256, 128, false, false);
 constexpr uint32_t kIdescPV = idesc_bf16_f32(256, 256, false, true);
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr uint32_t kBarMax = 1, kBarOr = 2, kBarQuarter0 = 3, kBarEpi = 4, kBarStage0 = 5;
-constexpr int kEpiPanelBytes = 128 * 128;
+constexpr uint32_t kBarMax = 1, kBarOr = 2, kBarQuarter0 = 3, kBarStage0 = 5;
+constexpr uint32_t kBarEpi = 1;  // [4] the epilogue's warp sets (output CTAs)
 
 template <bool kScaled>
 __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
@@ -550,42 +551,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             if (eset == 0 && flat < p.flat_rows)
                 p.part_lse[(size_t)split * p.flat_rows + flat] =
                     empty ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
-            // O / l leaves through TMA stores, as in the decode kernel: two rounds of eight
-            // 32-column panels over the V ring, rows past the batch cut off by the tensor map
-            for (int rd = 0; rd < 2; ++rd) {
-                if (rd > 0) {  // the previous round's stores have read their tiles
-                    if (ctid == 0) bulk_wait_group_read<0>();
-                    named_bar(kBarEpi, kSoftThreads);
-                }
-                uint32_t v[2][32];  // this warp set's two panels
-                if (use_o) {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        tmem_ld32(tmem + lane_base + (uint32_t)(rd * 256 + (2 * eset + q) * 32), v[q]);
-                    tmem_wait_ld();
-                }
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint8_t* out = smem + OFF_V + (2 * eset + q) * kEpiPanelBytes;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);  // an empty row: also where O holds garbage
-                        if (!empty)
-                            x = make_float4(__uint_as_float(v[q][4 * c]) * inv, __uint_as_float(v[q][4 * c + 1]) * inv,
-                                            __uint_as_float(v[q][4 * c + 2]) * inv,
-                                            __uint_as_float(v[q][4 * c + 3]) * inv);
-                        *reinterpret_cast<float4*>(out + row * 128 + ((c ^ (row & 7)) << 4)) = x;
-                    }
-                }
-                fence_proxy_async_cta();
-                named_bar(kBarEpi, kSoftThreads);
-                if (ctid == 0 && rows0 < p.flat_rows) {
-                    for (int pl = 0; pl < 8; ++pl)
-                        tma_store_3d(&o_map, sbase + OFF_V + pl * kEpiPanelBytes, rd * 256 + pl * 32, rows0, split);
-                    bulk_commit_group();
-                }
-            }
-            if (ctid == 0) bulk_wait_group<0>();  // the stores are complete before the CTA exits
+            // O / l leaves through TMA stores over the V ring and the P buffers; rows past the batch
+            // are cut off by the tensor map
+            store_rows<true, 4, 3, kBarEpi>(smem, sbase, OFF_V, tmem + lane_base, row, eset, (ctid & 127) == 0, true,
+                                            empty, inv, &o_map, rows0, split, rows0 < p.flat_rows);
         }
     }
 

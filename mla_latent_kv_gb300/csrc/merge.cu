@@ -55,56 +55,69 @@ __device__ __forceinline__ void merge_item(const DecodeArgs& p, int64_t r, int h
         S = p.num_splits;
         slot0 = (int)(r * S);
     }
-    const float* lse_p = p.part_lse + (size_t)slot0 * p.H + h;  // stride H between splits
-
-    float M = -CUDART_INF_F;
-    for (int s = lane; s < S; s += 32) M = fmaxf(M, lse_p[(size_t)s * p.H]);
+    // The row's states in order: those over the base tokens (kPre), then its own.
     const size_t heads = (size_t)p.rows * p.H, rh = (size_t)r * p.H + h;
-    if constexpr (kPre)
-        for (int s = lane; s < p.pre_splits; s += 32) M = fmaxf(M, p.pre_lse[(size_t)s * heads + rh]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    const int npre = kPre ? p.pre_splits : 0, total = npre + S;
+    const int dim = half * (kL / 2) + lane * 8;
+    auto state_lse = [&](int s) -> float {
+        return kPre && s < npre ? p.pre_lse[(size_t)s * heads + rh]
+                                : p.part_lse[((size_t)slot0 + (s - npre)) * p.H + h];
+    };
+    auto state_o = [&](int s) -> const float4* {
+        return reinterpret_cast<const float4*>(kPre && s < npre
+                                                   ? p.pre_o + ((size_t)s * heads + rh) * kL + dim
+                                                   : p.part_o + (((size_t)slot0 + (s - npre)) * p.H + h) * kL + dim);
+    };
 
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-    float wsum = 0.f;
-    // the states at src0 + s * stride and lses + s * lse_stride, s < count
-    auto add = [&](const float* src0, size_t stride, const float* lses, size_t lse_stride, int count) {
-        for (int s0 = 0; s0 < count; s0 += kBatch) {
-            // all loads of the batch first, then the arithmetic in split order
-            float ls[kBatch];
-            float4 v[kBatch][2];
+    float wsum = 0.f, M = -CUDART_INF_F;
+    float ls[kBatch];
+    float4 v[kBatch][2];
+    auto load = [&](int s0) {
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                ls[u] = -CUDART_INF_F;
-                v[u][0] = v[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (s0 + u < count) {
-                    ls[u] = lses[(size_t)(s0 + u) * lse_stride];
-                    const float4* src = reinterpret_cast<const float4*>(src0 + (size_t)(s0 + u) * stride);
-                    v[u][0] = src[0];
-                    v[u][1] = src[1];
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                if (ls[u] == -CUDART_INF_F) continue;  // an empty split has no weight
-                const float w = __expf(ls[u] - M);
-                wsum += w;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    acc[4 * i + 0] = fmaf(w, v[u][i].x, acc[4 * i + 0]);
-                    acc[4 * i + 1] = fmaf(w, v[u][i].y, acc[4 * i + 1]);
-                    acc[4 * i + 2] = fmaf(w, v[u][i].z, acc[4 * i + 2]);
-                    acc[4 * i + 3] = fmaf(w, v[u][i].w, acc[4 * i + 3]);
-                }
+        for (int u = 0; u < kBatch; ++u) {
+            ls[u] = -CUDART_INF_F;
+            v[u][0] = v[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (s0 + u < total) {
+                ls[u] = state_lse(s0 + u);
+                const float4* src = state_o(s0 + u);
+                v[u][0] = src[0];
+                v[u][1] = src[1];
             }
         }
     };
-    if (M != -CUDART_INF_F) {
-        const int dim = half * (kL / 2) + lane * 8;
-        if constexpr (kPre) add(p.pre_o + rh * kL + dim, heads * kL, p.pre_lse + rh, heads, p.pre_splits);
-        add(p.part_o + ((size_t)slot0 * p.H + h) * kL + dim, (size_t)p.H * kL, lse_p, p.H, S);
+    auto add = [&]() {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (ls[u] == -CUDART_INF_F) continue;  // an empty split has no weight
+            const float w = __expf(ls[u] - M);
+            wsum += w;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                acc[4 * i + 0] = fmaf(w, v[u][i].x, acc[4 * i + 0]);
+                acc[4 * i + 1] = fmaf(w, v[u][i].y, acc[4 * i + 1]);
+                acc[4 * i + 2] = fmaf(w, v[u][i].z, acc[4 * i + 2]);
+                acc[4 * i + 3] = fmaf(w, v[u][i].w, acc[4 * i + 3]);
+            }
+        }
+    };
+    if (total <= kBatch) {  // one batch: the maximum comes from the loads that are on their way anyway
+        load(0);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) M = fmaxf(M, ls[u]);
+        add();
+    } else {
+        for (int s = lane; s < total; s += 32) M = fmaxf(M, state_lse(s));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        if (M != -CUDART_INF_F)
+            for (int s0 = 0; s0 < total; s0 += kBatch) {
+                // all loads of the batch first, then the arithmetic in split order
+                load(s0);
+                add();
+            }
     }
     const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
     const size_t base = ((size_t)r * p.H + h) * kL + half * (kL / 2) + lane * 8;
