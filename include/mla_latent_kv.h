@@ -406,7 +406,7 @@ mla_status mla_page_scores(const void* q, const void* page_keys, int64_t num_blo
  * others the max_sel - sink_pages - local_pages with the highest scores (of equal scores the lower
  * page; -0 equals 0; NaN is below everything). Scores of the first and last pages are not read.
  *   scores        fp32, row r = b * Sq + t at scores + r * scores_stride, num_pages entries
- *                 (num_pages <= 49152; a longer seq_lens[b] sets MLA_DEV_SEQ_TOO_LONG and is cut)
+ *                 (num_pages <= 32768; a longer seq_lens[b] sets MLA_DEV_SEQ_TOO_LONG and is cut)
  *   max_sel       >= 1; sink_pages + local_pages <= max_sel
  *   pages         int32 [B, Sq, max_sel]: ascending page numbers, -1 behind the last
  */

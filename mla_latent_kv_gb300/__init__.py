@@ -35,6 +35,8 @@ class MlaError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load the native library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -363,47 +365,78 @@ def prefill(q, kv_c, k_pe, kv_cache, block_table, ctx_lens, query_start_loc, w_u
 
 
 # ------------------------------------------------------------------ shared prefix, selected pages
-def _tensor(name, t, dtype, shape):
-    """`t` as an argument the kernels read through its pointer: contiguous, of the dtype and shape
-    (None = any size)."""
-    if t.dtype != dtype or t.dim() != len(shape) or not t.is_contiguous() or \
-            any(want is not None and want != got for want, got in zip(shape, t.shape)):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape "
-                         f"{tuple('*' if d is None else d for d in shape)}, got {t.dtype} {tuple(t.shape)}")
-    return t
+# A decode step makes these calls once a layer, and the smallest take a few microseconds on the GPU:
+# they check their tensors with plain attribute reads and pass addresses as integers.
+def _is(name, t, dtype, dims):
+    """Refuse an argument that is not a contiguous tensor of the dtype and number of dimensions."""
+    if t.dtype is not dtype or t.ndim != dims or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor with {dims} dimensions, got {t.dtype} "
+                         f"{tuple(t.shape)} (contiguous={t.is_contiguous()})")
 
 
-def _here(t):
-    """`t`'s device, which must be the current one: the calls launch on the current device's stream."""
+def _is_shape(name, t, dtype, shape):
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)} (contiguous={t.is_contiguous()})")
+
+
+def _raw_stream(t, stream):
+    """The stream to launch on as an integer. The calls launch on the current device, which must be
+    the tensors' own."""
     import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    dev = t.get_device()  # -1: not a CUDA tensor
+    if dev < 0 or dev != torch.cuda.current_device():
         raise ValueError(f"tensors must be on the current CUDA device, got {t.device}")
-    return t.device
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _page_args(q, block_table, seq_lens):
+    """Checks of the query, block table and lengths -> (B, Sq, H)."""
+    import torch
+    _is("q", q, torch.bfloat16, 4)
+    B, Sq, H, width = q.shape
+    _is("block_table", block_table, torch.int32, 2)
+    _is_shape("seq_lens", seq_lens, torch.int32, (B,))
+    if width != D or block_table.shape[0] != B:
+        raise ValueError(f"q must be [B, Sq, H, {D}] and block_table [B, max_blocks], got {tuple(q.shape)} and "
+                         f"{tuple(block_table.shape)}")
+    return B, Sq, H
+
+
+_ROW_BYTES = {KV_BF16: 2 * D, KV_FP8: D + 8}
 
 
 def _cache_blocks(kv_cache, kv_dtype, num_blocks):
     """Blocks of the cache, checked against its size when given."""
-    rb = row_bytes(kv_dtype)
-    if rb < 0:
+    rb = _ROW_BYTES.get(kv_dtype)
+    if rb is None:
         raise MlaError(ERR_INVALID_ARG, f"unknown kv_dtype {kv_dtype}")
-    have = kv_cache.numel() * kv_cache.element_size() // (PAGE * rb)
+    have = kv_cache.nbytes // (PAGE * rb)
     if not kv_cache.is_contiguous() or (num_blocks is not None and num_blocks > have):
         raise ValueError(f"kv_cache must be contiguous and hold num_blocks={num_blocks} pages (it holds {have})")
     return have if num_blocks is None else int(num_blocks)
 
 
-def _work_buf(workspace, need, device):
-    """A workspace of at least `need` bytes and its size."""
+def _attention_bufs(q, B, Sq, H, o_latent, o_dtype, lse, workspace, need):
+    """The outputs and the workspace, made when not given -> (o_latent, its dtype code, lse, workspace,
+    workspace bytes)."""
     import torch
-    if workspace is None:
-        return (torch.empty(need, dtype=torch.uint8, device=device), need) if need else (None, 0)
-    return workspace, workspace.numel() * workspace.element_size()
+    o_dtype = _dt_code(o_latent, o_dtype)
+    o_latent = _out_buf(o_latent, (B, Sq, H, L), o_dtype, q.device)
+    lse = _out_buf(lse, (B, Sq, H), DT_F32, q.device)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    return o_latent, o_dtype, lse, workspace, 0 if workspace is None else workspace.nbytes
+
+
+def _a(t):
+    return None if t is None else t.data_ptr()
 
 
 def decode_shared_prefix_workspace_bytes(B: int, Sq: int, H: int, prefix_len: int, max_seq_len: int,
                                          kv_dtype: int = KV_BF16, num_splits: int = -1) -> int:
-    return int(lib().mla_decode_shared_prefix_workspace_bytes(kv_dtype, B, Sq, H, int(prefix_len), num_splits,
-                                                              int(max_seq_len)))
+    return lib().mla_decode_shared_prefix_workspace_bytes(kv_dtype, B, Sq, H, int(prefix_len), num_splits,
+                                                          int(max_seq_len))
 
 
 def decode_shared_prefix(q, kv_cache, block_table, seq_lens, max_seq_len, prefix_len, scale, kv_dtype=KV_BF16,
@@ -412,22 +445,17 @@ def decode_shared_prefix(q, kv_cache, block_table, seq_lens, max_seq_len, prefix
     """decode() of a batch whose requests share their first prefix_len tokens (a multiple of 64): the
     first prefix_len / 64 entries of block_table's rows name the same pages, read once for all
     -> (o_latent [B,Sq,H,512], lse [B,Sq,H])."""
-    import torch
-    B, Sq, H = q.shape[0], q.shape[1], q.shape[2]
-    _tensor("q", q, torch.bfloat16, (B, Sq, H, D))
-    _tensor("block_table", block_table, torch.int32, (B, None))
-    _tensor("seq_lens", seq_lens, torch.int32, (B,))
+    B, Sq, H = _page_args(q, block_table, seq_lens)
     nb = _cache_blocks(kv_cache, kv_dtype, num_blocks)
-    _here(q)
-    need = decode_shared_prefix_workspace_bytes(B, Sq, H, prefix_len, max_seq_len, kv_dtype, num_splits)
-    workspace, ws_bytes = _work_buf(workspace, need, q.device)
-    o_dtype = _dt_code(o_latent, o_dtype)
-    o_latent = _out_buf(o_latent, (B, Sq, H, L), o_dtype, q.device)
-    lse = _out_buf(lse, (B, Sq, H), DT_F32, q.device)
-    _check(lib().mla_decode_shared_prefix(_p(q), _p(kv_cache), kv_dtype, nb, _p(block_table), block_table.shape[1],
-                                          _p(seq_lens), int(max_seq_len), int(prefix_len), B, Sq, H, float(scale),
-                                          int(num_splits), _p(workspace), ws_bytes, _p(o_latent), o_dtype, _p(lse),
-                                          _p(dev_status), _stream(stream)))
+    s = _raw_stream(q, stream)
+    l = lib()
+    need = 0 if workspace is not None else l.mla_decode_shared_prefix_workspace_bytes(
+        kv_dtype, B, Sq, H, int(prefix_len), num_splits, int(max_seq_len))
+    o_latent, o_dtype, lse, workspace, ws_bytes = _attention_bufs(q, B, Sq, H, o_latent, o_dtype, lse, workspace, need)
+    _check(l.mla_decode_shared_prefix(q.data_ptr(), kv_cache.data_ptr(), kv_dtype, nb, block_table.data_ptr(),
+                                      block_table.shape[1], seq_lens.data_ptr(), int(max_seq_len), int(prefix_len), B,
+                                      Sq, H, float(scale), int(num_splits), _a(workspace), ws_bytes, o_latent.data_ptr(),
+                                      o_dtype, lse.data_ptr(), _a(dev_status), s))
     return o_latent, lse
 
 
@@ -437,18 +465,18 @@ def page_keys(kv_cache, block_table, seq_lens, max_new_len, kv_dtype=KV_BF16, st
     (start_lens None: all of them) -> page_keys bf16 [num_blocks, 576], written in place when given
     (other pages' keys stay)."""
     import torch
-    B = block_table.shape[0]
-    _tensor("block_table", block_table, torch.int32, (B, None))
-    _tensor("seq_lens", seq_lens, torch.int32, (B,))
+    _is("block_table", block_table, torch.int32, 2)
+    B, max_blocks = block_table.shape
+    _is_shape("seq_lens", seq_lens, torch.int32, (B,))
     if start_lens is not None:
-        _tensor("start_lens", start_lens, torch.int32, (B,))
+        _is_shape("start_lens", start_lens, torch.int32, (B,))
     nb = _cache_blocks(kv_cache, kv_dtype, num_blocks)
-    _here(kv_cache)
+    s = _raw_stream(kv_cache, stream)
     if page_keys is None:
         page_keys = torch.zeros((nb, D), dtype=torch.bfloat16, device=kv_cache.device)
-    _tensor("page_keys", page_keys, torch.bfloat16, (nb, D))
-    _check(lib().mla_page_keys(_p(kv_cache), kv_dtype, nb, _p(block_table), block_table.shape[1], _p(start_lens),
-                               _p(seq_lens), int(max_new_len), B, _p(page_keys), _p(dev_status), _stream(stream)))
+    _is_shape("page_keys", page_keys, torch.bfloat16, (nb, D))
+    _check(lib().mla_page_keys(kv_cache.data_ptr(), kv_dtype, nb, block_table.data_ptr(), max_blocks, _a(start_lens),
+                               seq_lens.data_ptr(), int(max_new_len), B, page_keys.data_ptr(), _a(dev_status), s))
     return page_keys
 
 
@@ -456,19 +484,16 @@ def page_scores(q, page_keys, block_table, seq_lens, max_seq_len, scale, scores=
     """Score of every page for every query row, max over heads of scale * <q, page key>
     -> fp32 [B, Sq, ceil(max_seq_len / 64)], -inf past a row's pages."""
     import torch
-    B, Sq, H = q.shape[0], q.shape[1], q.shape[2]
-    _tensor("q", q, torch.bfloat16, (B, Sq, H, D))
-    _tensor("page_keys", page_keys, torch.bfloat16, (None, D))
-    _tensor("block_table", block_table, torch.int32, (B, None))
-    _tensor("seq_lens", seq_lens, torch.int32, (B,))
-    _here(q)
+    B, Sq, H = _page_args(q, block_table, seq_lens)
+    _is_shape("page_keys", page_keys, torch.bfloat16, (page_keys.shape[0], D))
+    s = _raw_stream(q, stream)
     width = -(-int(max_seq_len) // PAGE)
     if scores is None:
         scores = torch.empty((B, Sq, width), dtype=torch.float32, device=q.device)
-    _tensor("scores", scores, torch.float32, (B, Sq, width))
-    _check(lib().mla_page_scores(_p(q), _p(page_keys), page_keys.shape[0], _p(block_table), block_table.shape[1],
-                                 _p(seq_lens), int(max_seq_len), B, Sq, H, float(scale), _p(scores), _p(dev_status),
-                                 _stream(stream)))
+    _is_shape("scores", scores, torch.float32, (B, Sq, width))
+    _check(lib().mla_page_scores(q.data_ptr(), page_keys.data_ptr(), page_keys.shape[0], block_table.data_ptr(),
+                                 block_table.shape[1], seq_lens.data_ptr(), int(max_seq_len), B, Sq, H, float(scale),
+                                 scores.data_ptr(), _a(dev_status), s))
     return scores
 
 
@@ -478,24 +503,27 @@ def select_pages(scores, seq_lens, max_sel, sink_pages=1, local_pages=1, pages=N
     behind the last."""
     import torch
     B, Sq, width = scores.shape
-    if scores.dtype != torch.float32 or (width > 1 and scores.stride(2) != 1) or \
-            (B > 1 and Sq > 1 and scores.stride(0) != Sq * scores.stride(1)):
+    if scores.is_contiguous():
+        stride = width
+    elif (width > 1 and scores.stride(2) != 1) or (B > 1 and Sq > 1 and scores.stride(0) != Sq * scores.stride(1)):
         raise ValueError("scores must be fp32 [B, Sq, num_pages] with unit inner stride and evenly spaced rows")
-    # dimensions of one element have strides of no meaning
-    stride = scores.stride(1) if Sq > 1 else (scores.stride(0) if B > 1 else width)
-    _tensor("seq_lens", seq_lens, torch.int32, (B,))
-    _here(scores)
+    else:  # dimensions of one element have strides of no meaning
+        stride = scores.stride(1) if Sq > 1 else (scores.stride(0) if B > 1 else width)
+    if scores.dtype is not torch.float32:
+        raise ValueError(f"scores must be fp32, got {scores.dtype}")
+    _is_shape("seq_lens", seq_lens, torch.int32, (B,))
+    s = _raw_stream(scores, stream)
     if pages is None:
         pages = torch.empty((B, Sq, max_sel), dtype=torch.int32, device=scores.device)
-    _tensor("pages", pages, torch.int32, (B, Sq, max_sel))
-    _check(lib().mla_select_pages(_p(scores), int(stride), width, _p(seq_lens), B, Sq, int(max_sel), int(sink_pages),
-                                  int(local_pages), _p(pages), _p(dev_status), _stream(stream)))
+    _is_shape("pages", pages, torch.int32, (B, Sq, max_sel))
+    _check(lib().mla_select_pages(scores.data_ptr(), stride, width, seq_lens.data_ptr(), B, Sq, int(max_sel),
+                                  int(sink_pages), int(local_pages), pages.data_ptr(), _a(dev_status), s))
     return pages
 
 
 def decode_sparse_workspace_bytes(B: int, Sq: int, H: int, max_sel: int, kv_dtype: int = KV_BF16,
                                   num_splits: int = -1) -> int:
-    return int(lib().mla_decode_sparse_workspace_bytes(kv_dtype, B, Sq, H, int(max_sel), num_splits))
+    return lib().mla_decode_sparse_workspace_bytes(kv_dtype, B, Sq, H, int(max_sel), num_splits)
 
 
 def decode_sparse(q, kv_cache, block_table, seq_lens, pages, scale, kv_dtype=KV_BF16, num_splits=-1, workspace=None,
@@ -503,20 +531,18 @@ def decode_sparse(q, kv_cache, block_table, seq_lens, pages, scale, kv_dtype=KV_
     """decode() with each query row's attention limited to its selected pages [B, Sq, max_sel] int32
     (ascending, -1 skipped) -> (o_latent [B,Sq,H,512], lse [B,Sq,H])."""
     import torch
-    B, Sq, H = q.shape[0], q.shape[1], q.shape[2]
-    _tensor("q", q, torch.bfloat16, (B, Sq, H, D))
-    _tensor("block_table", block_table, torch.int32, (B, None))
-    _tensor("seq_lens", seq_lens, torch.int32, (B,))
-    _tensor("pages", pages, torch.int32, (B, Sq, None))
-    nb = _cache_blocks(kv_cache, kv_dtype, num_blocks)
-    _here(q)
+    B, Sq, H = _page_args(q, block_table, seq_lens)
+    _is("pages", pages, torch.int32, 3)
     K = pages.shape[2]
-    workspace, ws_bytes = _work_buf(workspace, decode_sparse_workspace_bytes(B, Sq, H, K, kv_dtype, num_splits),
-                                    q.device)
-    o_dtype = _dt_code(o_latent, o_dtype)
-    o_latent = _out_buf(o_latent, (B, Sq, H, L), o_dtype, q.device)
-    lse = _out_buf(lse, (B, Sq, H), DT_F32, q.device)
-    _check(lib().mla_decode_sparse(_p(q), _p(kv_cache), kv_dtype, nb, _p(block_table), block_table.shape[1],
-                                   _p(seq_lens), _p(pages), K, B, Sq, H, float(scale), int(num_splits), _p(workspace),
-                                   ws_bytes, _p(o_latent), o_dtype, _p(lse), _p(dev_status), _stream(stream)))
+    if pages.shape[0] != B or pages.shape[1] != Sq:
+        raise ValueError(f"pages must be [{B}, {Sq}, max_sel], got {tuple(pages.shape)}")
+    nb = _cache_blocks(kv_cache, kv_dtype, num_blocks)
+    s = _raw_stream(q, stream)
+    l = lib()
+    need = 0 if workspace is not None else l.mla_decode_sparse_workspace_bytes(kv_dtype, B, Sq, H, K, num_splits)
+    o_latent, o_dtype, lse, workspace, ws_bytes = _attention_bufs(q, B, Sq, H, o_latent, o_dtype, lse, workspace, need)
+    _check(l.mla_decode_sparse(q.data_ptr(), kv_cache.data_ptr(), kv_dtype, nb, block_table.data_ptr(),
+                               block_table.shape[1], seq_lens.data_ptr(), pages.data_ptr(), K, B, Sq, H, float(scale),
+                               int(num_splits), _a(workspace), ws_bytes, o_latent.data_ptr(), o_dtype, lse.data_ptr(),
+                               _a(dev_status), s))
     return o_latent, lse

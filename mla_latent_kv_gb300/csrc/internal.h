@@ -195,7 +195,7 @@ struct SparseTableArgs {
     int32_t* lens;              // [B * Sq] their tokens
     int32_t* dev_status;        // or null
 };
-constexpr int kMaxSelectWidth = 49152;  // pages of a row whose keys fit the shared memory of a CTA
+constexpr int kMaxSelectWidth = 32768;  // pages of a row: 32 keys a thread in one CTA
 cudaError_t launch_page_keys(const PageKeysArgs& a, bool fp8, cudaStream_t s);
 cudaError_t launch_page_scores(const PageScoresArgs& a, cudaStream_t s);
 cudaError_t launch_select_pages(const SelectArgs& a, cudaStream_t s);

@@ -1,7 +1,5 @@
 // pages.cu -- the page-level steps of sparse decode: mean keys of cache pages, the choice of pages
 // from their scores, and the page tables that the decode kernels read.
-#include <math_constants.h>
-
 #include "internal.h"
 #include "sm103_ptx.cuh"
 
@@ -118,12 +116,13 @@ __global__ void __launch_bounds__(kKeyThreads) page_keys_kernel(PageKeysArgs p) 
 // taken; else the first `sink`, the last `local` and, of the others, the K - sink - local best
 // scores (equal scores: the lower page; NaN below everything). The list is ascending, -1 behind.
 //
-// One CTA per row. Scores become order-preserving 32-bit keys in shared memory, and the key T of
-// the last page taken is found bit by bit from the top: T keeps a bit if at least `need` keys
-// are >= T with it. That is 32 counting passes over shared memory, with no atomics (a histogram's
-// would collide: scores share their exponents) and the same answer in any order. One scan then
-// places the pages.
-// ------------------------------------------------------------------------------------------
+// One CTA per row. Scores become order-preserving 32-bit keys, and the key T of the last page taken
+// is found bit by bit from the top: T keeps a bit if at least `need` keys are >= T with it. Counting
+// has no atomics (a histogram's would collide: scores share their exponents) and gives the same
+// answer in any order. Bits that all keys share are skipped, and the search ends as soon as exactly
+// `need` keys are >= T. A thread keeps kPer consecutive keys in registers: a pass is then mostly
+// compares, where with four keys a thread its reductions and barriers took three times as long
+// (256 rows of 2048 pages: 21 us). One scan then places the pages.
 __device__ __forceinline__ uint32_t score_key(float x) {
     const uint32_t u = __float_as_uint(x);
     if ((u & 0x7fffffffu) > 0x7f800000u) return 0u;       // NaN
@@ -131,9 +130,20 @@ __device__ __forceinline__ uint32_t score_key(float x) {
     return (z & 0x80000000u) ? ~z : (z | 0x80000000u);    // never 0
 }
 
+// The sum of a warp-uniform-per-warp count over the block. `slot` alternates between two buffers, so that
+// one barrier a call is enough.
+__device__ __forceinline__ int block_count(int c, int (*buf)[32], int slot, int nw, int warp, int lane) {
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (nw == 1) return c;
+    if (lane == 0) buf[slot][warp] = c;
+    __syncthreads();
+    return __reduce_add_sync(0xffffffffu, lane < nw ? buf[slot][lane] : 0);
+}
+
+template <int kPer>
 __global__ void __launch_bounds__(1024) select_pages_kernel(SelectArgs p) {
-    extern __shared__ uint32_t key[];
     __shared__ int s_cnt[2][32];
+    __shared__ uint32_t s_and[32], s_or[32];
     __shared__ int2 s_scan[32];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -154,34 +164,66 @@ __global__ void __launch_bounds__(1024) select_pages_kernel(SelectArgs p) {
     const int c0 = p.sink, c1 = np - p.local;  // candidates [c0, c1): c1 - c0 > need
     const int need = p.K - p.sink - p.local;
     const float* src = p.scores + (size_t)r * p.stride;
-    for (int i = c0 + tid; i < c1; i += nt) key[i] = score_key(src[i]);
-    __syncthreads();
+    // This thread's pages i0 .. i0 + kPer - 1. Pages that are no candidates have key 0, which no trial
+    // value counts (trials are > 0); a NaN candidate's key is 0 too, and T = 0 takes those last.
+    const int i0 = tid * kPer;
+    static_assert(kPer <= 32, "a bit a page below");
+    uint32_t key[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int i = i0 + k;
+        key[k] = i >= c0 && i < c1 ? score_key(src[i]) : 0u;
+    }
     uint32_t T = 0;
     if (need > 0) {
-        for (int bit = 31; bit >= 0; --bit) {
+        uint32_t all_and = 0xffffffffu, all_or = 0u;  // of the candidates' keys
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int i = i0 + k;
+            if (i >= c0 && i < c1) {
+                all_and &= key[k];
+                all_or |= key[k];
+            }
+        }
+        all_and = __reduce_and_sync(0xffffffffu, all_and);
+        all_or = __reduce_or_sync(0xffffffffu, all_or);
+        if (nw > 1) {
+            if (lane == 0) {
+                s_and[warp] = all_and;
+                s_or[warp] = all_or;
+            }
+            __syncthreads();
+            all_and = __reduce_and_sync(0xffffffffu, lane < nw ? s_and[lane] : 0xffffffffu);
+            all_or = __reduce_or_sync(0xffffffffu, lane < nw ? s_or[lane] : 0u);
+        }
+        const uint32_t differ = all_and ^ all_or;
+        const int top = differ ? 31 - __clz(differ) : -1;  // the highest bit in which two keys differ
+        T = top < 31 ? all_and & ~((2u << top) - 1u) : 0u;  // what is above it
+        if (top < 0) T = all_and;
+        for (int bit = top; bit >= 0; --bit) {
             const uint32_t trial = T | (1u << bit);
             int c = 0;
-            for (int i = c0 + tid; i < c1; i += nt) c += key[i] >= trial ? 1 : 0;
-            c = __reduce_add_sync(0xffffffffu, c);
-            if (nw > 1) {  // two buffers: a pass's counts are read while the next pass writes the other
-                if (lane == 0) s_cnt[bit & 1][warp] = c;
-                __syncthreads();
-                c = __reduce_add_sync(0xffffffffu, lane < nw ? s_cnt[bit & 1][lane] : 0);
-            }
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) c += key[k] >= trial ? 1 : 0;
+            c = block_count(c, s_cnt, bit & 1, nw, warp, lane);
             if (c >= need) T = trial;
+            if (c == need) break;
         }
     }
-    // Each thread takes a run of consecutive pages: those above T (or forced) and those equal to T.
-    const int per = (np + nt - 1) / nt;
-    const int i0 = min(np, tid * per), i1 = min(np, i0 + per);
-    int above = 0, equal = 0;
-    for (int i = i0; i < i1; ++i) {
-        const bool forced = i < c0 || i >= c1;
-        const bool gt = need > 0 && !forced && key[i] > T;
-        above += forced || gt ? 1 : 0;
-        equal += need > 0 && !forced && key[i] == T ? 1 : 0;
+    // Pages above T (or forced) and those equal to T, in this thread's run of pages.
+    uint32_t forced = 0, above = 0, equal = 0;  // one bit a page
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int i = i0 + k;
+        if (i < np && (i < c0 || i >= c1)) forced |= 1u << k;
+        if (need > 0 && i >= c0 && i < c1) {
+            if (key[k] > T) above |= 1u << k;
+            if (key[k] == T) equal |= 1u << k;
+        }
     }
-    int2 inc = make_int2(above, equal);
+    above |= forced;
+    const int na = __popc(above), ne = __popc(equal);
+    int2 inc = make_int2(na, ne);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, inc.x, o), y = __shfl_up_sync(0xffffffffu, inc.y, o);
@@ -192,7 +234,7 @@ __global__ void __launch_bounds__(1024) select_pages_kernel(SelectArgs p) {
     }
     if (lane == 31) s_scan[warp] = inc;
     __syncthreads();
-    int2 before = make_int2(inc.x - above, inc.y - equal), all = make_int2(0, 0);
+    int2 before = make_int2(inc.x - na, inc.y - ne), all = make_int2(0, 0);
     for (int w = 0; w < nw; ++w) {
         const int2 v = s_scan[w];
         if (w < warp) {
@@ -203,11 +245,11 @@ __global__ void __launch_bounds__(1024) select_pages_kernel(SelectArgs p) {
     }
     const int ties = p.K - all.x;  // pages equal to T that are taken, the lowest first
     int at = before.x + min(before.y, ties), eq = before.y;
-    for (int i = i0; i < i1; ++i) {
-        const bool forced = i < c0 || i >= c1;
-        bool take = forced || (need > 0 && key[i] > T);
-        if (need > 0 && !forced && key[i] == T) take = eq++ < ties;
-        if (take) out[at++] = i;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        bool take = (above >> k) & 1u;
+        if ((equal >> k) & 1u) take = eq++ < ties;
+        if (take) out[at++] = i0 + k;
     }
 }
 
@@ -265,17 +307,14 @@ cudaError_t launch_page_keys(const PageKeysArgs& a, bool fp8, cudaStream_t s) {
 }
 
 cudaError_t launch_select_pages(const SelectArgs& a, cudaStream_t s) {
-    // about four pages a thread: a row of 64 pages is one warp's (no block barriers), one of 4096 a
-    // full block's
-    int threads = (a.width / 4 + 31) / 32 * 32;
-    threads = threads < 32 ? 32 : (threads > 1024 ? 1024 : threads);
-    const size_t smem = (size_t)a.width * sizeof(uint32_t);
-    if (smem > 40 * 1024) {  // with the static part, over the default limit of 48 KB
-        const cudaError_t e =
-            cudaFuncSetAttribute(select_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_pdl(select_pages_kernel, dim3((unsigned)(a.B * a.Sq)), dim3(threads), smem, s, a);
+    // Two pages a thread while a row fits two warps, else 16, and 32 once 1024 threads do not reach.
+    const int per = a.width <= 128 ? 2 : a.width <= 16384 ? 16 : 32;
+    int threads = ((a.width + per - 1) / per + 31) / 32 * 32;
+    if (threads < 32) threads = 32;
+    auto* kernel = per == 2    ? select_pages_kernel<2>
+                   : per == 16 ? select_pages_kernel<16>
+                               : select_pages_kernel<32>;
+    return launch_pdl(kernel, dim3((unsigned)(a.B * a.Sq)), dim3(threads), 0, s, a);
 }
 
 cudaError_t launch_sparse_table(const SparseTableArgs& a, cudaStream_t s) {

@@ -220,7 +220,7 @@ def test_page_scores_nan_and_bad_blocks():
 
 # --------------------------------------------------------------------------------------- select
 @pytest.mark.parametrize("K,sink,local", [(1, 0, 0), (1, 1, 0), (1, 0, 1), (4, 0, 0), (16, 1, 1), (16, 8, 8), (64, 2, 3)])
-@pytest.mark.parametrize("width", [1, 31, 64, 300, 2049, 5001])
+@pytest.mark.parametrize("width", [1, 31, 64, 129, 300, 2049, 5001, 16385])
 def test_select_pages(K, sink, local, width):
     import torch
     import mla_latent_kv_gb300 as mla
@@ -249,10 +249,10 @@ def test_select_pages_widest_strided_and_too_long():
     import torch
     import mla_latent_kv_gb300 as mla
     rng = np.random.default_rng(5)
-    wide = rng.standard_normal((1, 1, 49152)).astype(np.float32)
-    lens = dev(np.array([49152 * PAGE], np.int32))
+    wide = rng.standard_normal((1, 1, 32768)).astype(np.float32)
+    lens = dev(np.array([32768 * PAGE], np.int32))
     got = mla.select_pages(dev(wide), lens, 100, 1, 1).cpu().numpy()[0, 0]
-    assert list(got) == select_rule(wide[0, 0], 49152 * PAGE, 100, 1, 1)
+    assert list(got) == select_rule(wide[0, 0], 32768 * PAGE, 100, 1, 1)
     s = dev(rng.standard_normal((3, 1, 40)).astype(np.float32))[:, :, :20]  # rows 40 apart
     st = _status()
     lens = np.array([1000, 20 * PAGE, 20 * PAGE + 1], np.int32)
