@@ -329,7 +329,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 // (which cannot time out); after an abort the waits return at once.
                 const int page = kPPG * gi + pg2, buf = gi & 1;
                 size_t sc = 0;               // the quarter's first token of the page, in float4 units
-                float4 ks[kScaled ? 8 : 1];  // k_scale of its 32 tokens, loaded while S is on its way
+                float4 ks[kScaled ? 8 : 1];  // k_scale of its 32 tokens
                 if constexpr (kScaled) {
                     sc = ((size_t)(page0 + min(page, npages - 1)) * kPage + 32 * sub) / 4;
                     const float4* src = reinterpret_cast<const float4*>(p.k_scales) + sc;
@@ -349,14 +349,15 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(-CUDART_INF_F);
                 }
+                auto pair = [&](int j) { return make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])); };
                 float4 vs[kScaled ? 8 : 1];  // v_scale of this quarter's 32 tokens, on their way early
                 if constexpr (kScaled) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        s[4 * j] = __float_as_uint(__uint_as_float(s[4 * j]) * ks[j].x);
-                        s[4 * j + 1] = __float_as_uint(__uint_as_float(s[4 * j + 1]) * ks[j].y);
-                        s[4 * j + 2] = __float_as_uint(__uint_as_float(s[4 * j + 2]) * ks[j].z);
-                        s[4 * j + 3] = __float_as_uint(__uint_as_float(s[4 * j + 3]) * ks[j].w);
+                    for (int j = 0; j < 16; ++j) {
+                        const float2 x = mul2(pair(j), j & 1 ? make_float2(ks[j >> 1].z, ks[j >> 1].w)
+                                                             : make_float2(ks[j >> 1].x, ks[j >> 1].y));
+                        s[2 * j] = __float_as_uint(x.x);
+                        s[2 * j + 1] = __float_as_uint(x.y);
                     }
                     const float4* src = reinterpret_cast<const float4*>(p.v_scales) + sc;
 #pragma unroll
@@ -370,8 +371,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 float lm4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-                for (int j = 0; j < 32; ++j) lm4[j & 3] = fmaxf(lm4[j & 3], __uint_as_float(s[j]));
-                const float lm = fmaxf(fmaxf(lm4[0], lm4[1]), fmaxf(lm4[2], lm4[3]));
+                for (int j = 0; j < 16; ++j) lm4[j & 3] = max3(lm4[j & 3], pair(j).x, pair(j).y);
+                const float lm = max3(lm4[0], lm4[1], fmaxf(lm4[2], lm4[3]));
                 // Does any row's part pass the threshold? The barrier also keeps the next exchange's
                 // writes of mx behind this one's reads.
                 const bool any = named_bar_or(kBarOr, kSoftThreads, lm * sl2 > m_run + kRescaleThreshold);
@@ -388,20 +389,18 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 const float mref = m_run == -CUDART_INF_F ? 0.f : m_run;  // nothing seen yet: weights 0
                 uint32_t pk[16];
-                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+                float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    float a0 = fast_exp2(fmaf(__uint_as_float(s[2 * j]), sl2, -mref));
-                    float a1 = fast_exp2(fmaf(__uint_as_float(s[2 * j + 1]), sl2, -mref));
-                    l4[2 * (j & 1)] += a0;
-                    l4[2 * (j & 1) + 1] += a1;
-                    if constexpr (kScaled) {
-                        a0 *= j & 1 ? vs[j >> 1].z : vs[j >> 1].x;
-                        a1 *= j & 1 ? vs[j >> 1].w : vs[j >> 1].y;
-                    }
-                    pk[j] = pack_bf16x2(a0, a1);
+                    float2 a = fma2(pair(j), make_float2(sl2, sl2), make_float2(-mref, -mref));
+                    a = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+                    l2[j & 1] = add2(l2[j & 1], a);
+                    if constexpr (kScaled)
+                        a = mul2(a, j & 1 ? make_float2(vs[j >> 1].z, vs[j >> 1].w) : make_float2(vs[j >> 1].x, vs[j >> 1].y));
+                    pk[j] = pack_bf16x2(a.x, a.y);
                 }
-                l_run += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                l2[0] = add2(l2[0], l2[1]);
+                l_run += l2[0].x + l2[0].y;
                 // the page's staging buffers take turns: this one is free once the copy of two groups
                 // ago has landed
                 const int sbi = 2 * (gi & 1) + pg2;

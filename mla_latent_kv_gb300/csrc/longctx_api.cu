@@ -93,6 +93,11 @@ bool plan_prefix(mla_kv_dtype kv, int rows, int H, int prefix_len, int num_split
         w->decode = off;
     }
     const int own_len = std::max(0, max_seq_len - pages * mla::kPage);
+    // With more rows than SM pairs mla_decode's default builds a schedule on the device, about 10 us
+    // ahead of everything else. Behind a prefix the requests' own tokens are usually few: up to 32
+    // pages each row is one unit instead.
+    if (num_splits == -1 && w->splits > 0 && own_len <= 32 * mla::kPage && rows > 76)
+        num_splits = 1;
     w->own_splits = mla_resolve_num_splits(num_splits, rows, 1, H, own_len);
     if (w->own_splits < 1 && w->own_splits != -2) return false;
     w->total = w->decode + mla::workspace_layout(kv, rows, rows, H, w->own_splits, own_len, w->splits > 0).total;
