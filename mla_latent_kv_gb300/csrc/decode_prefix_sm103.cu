@@ -57,8 +57,8 @@ using namespace ptx;
 using dec::store_rows;
 using dec::warp_wait;
 
-constexpr int kThreads = 576;  // warp 0 TMA, warp 1 MMA, warps 2-17 softmax / 2-5 helpers, 2-17 epilogue
-constexpr int kSoftThreads = kThreads - 64;
+constexpr int kThreads = 608;  // warp 0 TMA, 1 MMA, 2-17 softmax / 2-5 helpers, 2-17 epilogue, 18 P copies
+constexpr int kSoftThreads = 512;
 constexpr int kTileRows = 256;
 constexpr int kPPG = 2;                      // pages per group, one per scores CTA
 constexpr int kPageBox = kPage * 128;        // one page's rows of one 64-dim panel (8 KB)
@@ -108,7 +108,8 @@ enum : int {
     B_QFULL = B_SEMPTY + 2,             // CTAs 0, 1: Q landed in shared memory
     B_QREADY,                           // CTAs 0, 1: Q latent dims moved to TMEM (512 threads)
     B_QPEER,                            // CTA 0: CTA 1's Q moved
-    B_STAGEFREE,                        // [4] CTAs 0, 1: staging buffer's copy has landed
+    B_STAGEFULL,                        // [4] CTAs 0, 1: staging buffer written by the page's 8 softmax warps
+    B_STAGEFREE = B_STAGEFULL + kStages,  // [4] CTAs 0, 1: staging buffer's copy has landed
     B_PEMPTY = B_STAGEFREE + kStages,         // [kPBufs] all: PV MMAs of the page in P buffer b completed
     B_VFULL = B_PEMPTY + kPBufs,        // [kVStages] CTA 2: V stage landed in both output CTAs
     B_VEMPTY = B_VFULL + kVStages,      // [kVStages] CTAs 2, 3: V stage consumed
@@ -129,7 +130,7 @@ constexpr uint32_t kSCol = 256;  // scores: Q latent in columns [0, 256), S buff
 constexpr uint32_t kIdescQK = idesc_bf16_f32(256, 128, false, false);
 constexpr uint32_t kIdescPV = idesc_bf16_f32(256, 256, false, true);
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr uint32_t kBarMax = 1, kBarOr = 2, kBarQuarter0 = 3, kBarStage0 = 5;
+constexpr uint32_t kBarMax = 1, kBarOr = 2, kBarQuarter0 = 3;
 constexpr uint32_t kBarEpi = 1;  // [4] the epilogue's warp sets (output CTAs)
 
 template <bool kScaled>
@@ -164,6 +165,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t cnt = 1;
             if (i >= B_SEMPTY && i < B_SEMPTY + 2) cnt = 32;
             if (i == B_QREADY) cnt = kSoftThreads;
+            if (i >= B_STAGEFULL && i < B_STAGEFULL + kStages) cnt = 8;
             if (i >= B_READY && i < B_READY + kPBufs) cnt = 8;
             bar_init(bar(i), cnt);
         }
@@ -280,6 +282,22 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     if (ok && leader) mma_pair_commit(bar(B_SFULL + buf), 0x3);
                 }
             }
+        } else if (warp == 18) {
+            // ------------------------- P copies -------------------------
+            // One thread sends each staged page, so that the softmax neither waits for the output
+            // CTA's buffer nor for the issue.
+            if (lane == 0) {
+                const uint32_t pbuf_remote = map_to_rank(sbase + OFF_PB, 2u + (uint32_t)side);
+                const uint32_t pfull_remote = map_to_rank(bar(B_PFULL), 2u + (uint32_t)side);
+                for (int page = 0; page < npages; ++page) {
+                    const int sbi = page & 3, pb = page % kPBufs, up = page / kPBufs;
+                    if (!wait_bar(bar(B_STAGEFULL + sbi), (page >> 2) & 1, abort, ds)) break;
+                    if (up > 0 && !wait_bar<true>(bar(B_PEMPTY + pb), (up - 1) & 1, abort, ds)) break;
+                    if (*abort) break;
+                    bulk_copy_to_peer(pbuf_remote + pb * kPBufStride, sbase + OFF_STAGE + sbi * kPBufStride, kPMsgBytes,
+                                      pfull_remote + 8u * pb);
+                }
+            }
         } else {
             // ------------------------- softmax warps (512 threads) -------------------------
             // Quarter `quarter` of the warps owns 32 columns of each group's S: half of page `pg2`.
@@ -322,8 +340,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             const float sl2 = p.scale * 1.4426950408889634f;  // exp2 domain
             float m_run = -CUDART_INF_F, l_run = 0.f;          // each quarter keeps its own sum
             const uint32_t out_rank = 2u + (uint32_t)side;
-            const uint32_t pbuf_remote = map_to_rank(sbase + OFF_PB, out_rank);
-            const uint32_t pfull_remote = map_to_rank(bar(B_PFULL), out_rank);
             for (int gi = 0; gi < ngroups; ++gi) {
                 // No early exit from this loop: all 512 threads must pass the same named barriers
                 // (which cannot time out); after an abort the waits return at once.
@@ -416,13 +432,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     if (sub == 0 && row == 0)
                         *reinterpret_cast<uint32_t*>(stage + kPBytes + 512) = (pg2 == 0 && any && gi > 0) ? 1u : 0u;
                     fence_proxy_async_cta();  // generic writes before the bulk copy reads them
-                }
-                named_bar(kBarStage0 + pg2, kSoftThreads / 2);
-                if (sub == 0 && row == 0 && page < npages && okS) {
-                    const int pb = page % kPBufs, up = page / kPBufs;
-                    if (up == 0 || wait_bar<true>(bar(B_PEMPTY + pb), (up - 1) & 1, abort, ds))
-                        bulk_copy_to_peer(pbuf_remote + pb * kPBufStride, sbase + OFF_STAGE + sbi * kPBufStride,
-                                          kPMsgBytes, pfull_remote + 8u * pb);
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(bar(B_STAGEFULL + sbi));
                 }
             }
             // combine the quarters' sums, ship the final statistics
@@ -497,7 +508,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 volatile int dummy = 0;
                 wait_bar<true>(bar(B_PEMPTY + pg % kPBufs), (pg / kPBufs) & 1, *abort ? &dummy : abort, ds);
             }
-        } else {
+        } else if (warp < 18) {
             // ------------- helper warps 2-5: P arrival, rescale; warps 2-17: the epilogue -------------
             const int row = 32 * (warp & 3) + lane;
             const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
