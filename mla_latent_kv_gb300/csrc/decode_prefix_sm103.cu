@@ -115,7 +115,7 @@ enum : int {
     B_VEMPTY = B_VFULL + kVStages,      // [kVStages] CTAs 2, 3: V stage consumed
     B_PFULL = B_VEMPTY + kVStages,      // [kPBufs] CTAs 2, 3: P message landed
     B_READY = B_PFULL + kPBufs,         // [kPBufs] CTA 2: the 8 helper warps of the pair are done with the page
-    B_STATS = B_READY + kPBufs,         // CTAs 2, 3: final row statistics written
+    B_STATS = B_READY + kPBufs,         // CTAs 2, 3: final row statistics written, last P copy issued
     B_COUNT
 };
 static_assert(8 * B_COUNT <= 512, "barrier slots");
@@ -165,6 +165,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t cnt = 1;
             if (i >= B_SEMPTY && i < B_SEMPTY + 2) cnt = 32;
             if (i == B_QREADY) cnt = kSoftThreads;
+            if (i == B_STATS) cnt = 2;
             if (i >= B_STAGEFULL && i < B_STAGEFULL + kStages) cnt = 8;
             if (i >= B_READY && i < B_READY + kPBufs) cnt = 8;
             bar_init(bar(i), cnt);
@@ -289,13 +290,25 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             if (lane == 0) {
                 const uint32_t pbuf_remote = map_to_rank(sbase + OFF_PB, 2u + (uint32_t)side);
                 const uint32_t pfull_remote = map_to_rank(bar(B_PFULL), 2u + (uint32_t)side);
+                int sent = 0;
                 for (int page = 0; page < npages; ++page) {
                     const int sbi = page & 3, pb = page % kPBufs, up = page / kPBufs;
                     if (!wait_bar(bar(B_STAGEFULL + sbi), (page >> 2) & 1, abort, ds)) break;
                     if (up > 0 && !wait_bar<true>(bar(B_PEMPTY + pb), (up - 1) & 1, abort, ds)) break;
                     if (*abort) break;
+                    ++sent;
                     bulk_copy_to_peer(pbuf_remote + pb * kPBufStride, sbase + OFF_STAGE + sbi * kPBufStride, kPMsgBytes,
                                       pfull_remote + 8u * pb);
+                }
+                // The output CTA may now wait for its last page: the page kPBufs earlier is done, so
+                // a wait by parity cannot take that page's phase for the last one's. (The softmax
+                // is past its last page before that, and must not give this arrival.)
+                bar_arrive_remote(bar(B_STATS), 2u + (uint32_t)side);
+                // nothing may still be on its way to this CTA when it exits: the last multicast
+                // commits of the output pair
+                for (int pg = (sent > kPBufs ? sent - kPBufs : 0); pg < sent; ++pg) {
+                    volatile int dummy = 0;
+                    wait_bar<true>(bar(B_PEMPTY + pg % kPBufs), (pg / kPBufs) & 1, *abort ? &dummy : abort, ds);
                 }
             }
         } else {
@@ -445,15 +458,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 st_cluster_u32(map_to_rank(sbase + OFF_STAT_M, out_rank) + 4u * row, __float_as_uint(m_run));
                 st_cluster_u32(map_to_rank(sbase + OFF_STAT_L, out_rank) + 4u * row, __float_as_uint(l_run));
                 named_bar(kBarQuarter0, 128);
-                if (tid == 64) {
-                    bar_arrive_remote(bar(B_STATS), out_rank);
-                    // nothing may still be on its way to this CTA when it exits: the last
-                    // multicast commits of the output pair
-                    for (int pg = (npages > kPBufs ? npages - kPBufs : 0); pg < npages; ++pg) {
-                        volatile int dummy = 0;
-                        wait_bar<true>(bar(B_PEMPTY + pg % kPBufs), (pg / kPBufs) & 1, *abort ? &dummy : abort, ds);
-                    }
-                }
+                if (tid == 64) bar_arrive_remote(bar(B_STATS), out_rank);
             }
         }
     } else {
@@ -503,8 +508,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            // teardown: the last commits have landed in this CTA
-            for (int pg = (npages > kPBufs ? npages - kPBufs : 0); pg < npages; ++pg) {
+            // teardown: the last commits have landed in this CTA (in CTA 3, which does not follow the
+            // pages here, the epilogue's wait for the last page stands for it)
+            for (int pg = side == 1 ? npages : (npages > kPBufs ? npages - kPBufs : 0); pg < npages; ++pg) {
                 volatile int dummy = 0;
                 wait_bar<true>(bar(B_PEMPTY + pg % kPBufs), (pg / kPBufs) & 1, *abort ? &dummy : abort, ds);
             }
@@ -666,9 +672,16 @@ void prefix_split(int64_t flat_rows, int pages, int clusters, int* splits, int* 
     }
 }
 
-cudaError_t launch_decode_prefix(const PrefixArgs& in, const uint8_t* cache, bool fp8, uint16_t* widened,
-                                 float* scales, cudaStream_t s) {
+cudaError_t launch_prefix_widen(const PrefixArgs& a, const uint8_t* cache, uint16_t* widened, float* scales,
+                                cudaStream_t s) {
+    return launch_pdl(prefix_widen_kernel, dim3((unsigned)(a.prefix_pages * kPage / 8)), dim3(256), 0, s, a, cache,
+                      widened, scales, scales + (size_t)a.prefix_pages * kPage);
+}
+
+cudaError_t launch_decode_prefix(const PrefixArgs& in, const uint8_t* cache, const uint16_t* widened,
+                                 const float* scales, cudaStream_t s) {
     PrefixArgs a = in;
+    const bool fp8 = widened != nullptr;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -677,13 +690,9 @@ cudaError_t launch_decode_prefix(const PrefixArgs& in, const uint8_t* cache, boo
     const void* base = cache;
     uint64_t rows = (uint64_t)a.num_blocks * kPage;
     if (fp8) {
-        float* v_scales = scales + (size_t)a.prefix_pages * kPage;
-        e = launch_pdl(prefix_widen_kernel, dim3((unsigned)(a.prefix_pages * kPage / 8)), dim3(256), 0, s, a, cache,
-                       widened, scales, v_scales);
-        if (e != cudaSuccess) return e;
         a.block_table = nullptr;
         a.k_scales = scales;
-        a.v_scales = v_scales;
+        a.v_scales = scales + (size_t)a.prefix_pages * kPage;
         base = widened;
         rows = (uint64_t)a.prefix_pages * kPage;
     }

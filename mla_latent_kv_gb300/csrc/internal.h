@@ -20,7 +20,8 @@ constexpr int kFp8RowBytes = kD + 8;  // 584
 // What a decode kernel may read before the kernel ahead of it in the stream has ended: weights, cache
 // and block table (the default: kernels of the library write none of them; q and a device-built
 // schedule wait), nothing (the one ahead writes the lengths and the block table), or everything
-// (the one ahead began only after all before it had ended, and writes nothing that is read here).
+// (the one ahead began only after all before it had ended, and writes nothing that is read here:
+// the second of two kernels that run side by side).
 enum { kOrderDefault = 0, kOrderWaitFirst = 1, kOrderFree = 2 };
 
 // Everything a decode launch needs, resolved and validated on the host.
@@ -244,10 +245,12 @@ struct PrefixArgs {
 };
 int prefix_clusters();  // clusters of the prefix kernel that run at once on the current device, or -1
 void prefix_split(int64_t flat_rows, int pages, int clusters, int* splits, int* pages_per_split);
-// FP8: the prefix's rows are widened into `widened` [prefix tokens, 576] and `scales` [2, prefix
-// tokens] first.
-cudaError_t launch_decode_prefix(const PrefixArgs& a, const uint8_t* cache, bool fp8, uint16_t* widened,
-                                 float* scales, cudaStream_t s);
+// FP8: launch_prefix_widen first writes the prefix's rows to `widened` [prefix tokens, 576] and
+// their scales to `scales` [2, prefix tokens].
+cudaError_t launch_prefix_widen(const PrefixArgs& a, const uint8_t* cache, uint16_t* widened, float* scales,
+                                cudaStream_t s);
+cudaError_t launch_decode_prefix(const PrefixArgs& a, const uint8_t* cache, const uint16_t* widened,
+                                 const float* scales, cudaStream_t s);
 
 // Record an error for mla_last_error_detail() and return `st` (printf-style message).
 mla_status set_error(mla_status st, const char* fmt, ...);

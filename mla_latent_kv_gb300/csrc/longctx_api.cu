@@ -57,17 +57,20 @@ struct PrefixPlan {
     int own_splits;                      // resolved, of the requests' own tokens
     size_t widened, scales, part_o, part_lse, decode, total;
 };
-// The prefix kernel's launch, as a step of the decode that follows it.
+// The prefix kernel's launches, as a step of the decode that follows them.
 struct PrefixLaunch {
     mla::PrefixArgs a;
     const uint8_t* cache;
-    bool fp8;
-    uint16_t* widened;
+    uint16_t* widened;  // null: the cache is bf16
     float* scales;
     cudaStream_t stream;
     static cudaError_t run(void* self) {
         const PrefixLaunch& l = *static_cast<const PrefixLaunch*>(self);
-        return mla::launch_decode_prefix(l.a, l.cache, l.fp8, l.widened, l.scales, l.stream);
+        if (l.widened) {
+            const cudaError_t e = mla::launch_prefix_widen(l.a, l.cache, l.widened, l.scales, l.stream);
+            if (e != cudaSuccess) return e;
+        }
+        return mla::launch_decode_prefix(l.a, l.cache, l.widened, l.scales, l.stream);
     }
 };
 bool plan_prefix(mla_kv_dtype kv, int rows, int H, int prefix_len, int num_splits, int max_seq_len, PrefixPlan* w) {
@@ -346,9 +349,11 @@ mla_status mla_decode_shared_prefix(const void* q, const void* kv_cache, mla_kv_
         // The prefix kernel goes between the schedule and the decode of the requests' own tokens. It
         // lets that one start once all of its clusters run, which is after everything ahead of this
         // call has ended: the decode takes the SMs that the prefix leaves and reads what it likes.
+        // (The other way round, with the prefix filling up behind the short units, those took longer:
+        // 64 rows of 128 heads over 4096 + 512 tokens 97 us instead of 88.)
         launch.cache = (const uint8_t*)kv_cache;
-        launch.fp8 = kv_dtype == MLA_KV_FP8_E4M3_SCALED;
-        launch.widened = (uint16_t*)(ws + w.widened);
+        const bool fp8 = kv_dtype == MLA_KV_FP8_E4M3_SCALED;
+        launch.widened = fp8 ? (uint16_t*)(ws + w.widened) : nullptr;
         launch.scales = (float*)(ws + w.scales);
         launch.stream = (cudaStream_t)stream;
         x.between = &PrefixLaunch::run;

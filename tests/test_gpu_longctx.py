@@ -100,6 +100,26 @@ def test_shared_prefix_equals_decode_at_scale():
     assert torch.isfinite(o).all()
 
 
+@pytest.mark.parametrize("kv", [BF, F8])
+def test_shared_prefix_repeats_bit_for_bit(kv):
+    """Forty calls over a workspace of NaN: a partial state that is stored too early, or read before it
+    is stored, shows as another result (the output CTAs' waits by barrier parity depend on it)."""
+    import torch
+    import mla_latent_kv_gb300 as mla
+    B, H, prefix = 96, 16, 8192
+    c = paged_case([prefix + 1 + 5 * b for b in range(B)], 1, H, kv, seed=18, prefix=prefix)
+    ws = torch.empty(mla.decode_shared_prefix_workspace_bytes(B, 1, H, prefix, c["max_len"], kv), dtype=torch.uint8,
+                     device="cuda")
+    first = None
+    for _ in range(40):
+        ws.fill_(0xFF)
+        o, lse = _prefix(c, workspace=ws)
+        if first is None:
+            first = (o, lse)
+            assert torch.isfinite(o).all()
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+
+
 def test_shared_prefix_bad_prefix_block_is_reported():
     c = paged_case([200, 210], 1, 16, BF, seed=16, prefix=128)
     c["table"][0, 1] = c["num_blocks"] + 3
