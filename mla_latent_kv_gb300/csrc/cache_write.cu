@@ -29,7 +29,8 @@ __global__ void __launch_bounds__(kWarps * 32)
     cache_write_kernel(const uint16_t* __restrict__ kv_c, int64_t st_c, const uint16_t* __restrict__ k_pe,
                        int64_t st_pe, const int64_t* __restrict__ slots, int T, uint8_t* __restrict__ cache,
                        int fp8, int64_t num_blocks, float kv_scale, int32_t* dev_status) {
-    ptx::griddep_launch_dependents();
+    // No early signal to the kernels behind: a decode reads cache pages before its own wait, on the
+    // grounds that no kernel it may overtake writes them.
     ptx::griddep_wait();  // the rows come from, and the cache may still be read by, earlier kernels
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * kTok;

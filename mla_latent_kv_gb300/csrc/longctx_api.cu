@@ -73,34 +73,57 @@ struct PrefixLaunch {
         return mla::launch_decode_prefix(l.a, l.cache, l.widened, l.scales, l.stream);
     }
 };
+// Whether the prefix kernel is worth its launch, its partial states and their merge: estimated times in
+// us of the call with it and of the decode kernels alone, fitted to graph replays of both at 1..128
+// requests, 16..128 heads, 64..16384 prefix tokens and 64 or 512 own ones. Measured at the border, with
+// and without: 128 rows of 16 heads, 256 + 64 tokens 47 and 43, 1024 + 64 tokens 51 and 69; 32 rows of
+// 128 heads, 4096 + 64 tokens 56 and 56, 16384 + 64 tokens 103 and 166; 8 rows of 16 heads, 4096 + 64
+// tokens 31 and 24, 16384 + 64 tokens 34 and 49.
+bool prefix_pays(bool fp8, int rows, int H, int pages, int own_pages, int clusters, int splits, int per) {
+    const double page = fp8 ? 2.3 : 1.6;  // of one row on one of 76 SM pairs, the machine full
+    const int pairs = 76;
+    const double alone = 12 + (rows > pairs ? 11 : 0) + page * rows * (pages + own_pages) / pairs;
+    const int64_t units = ((int64_t)rows * H + 255) / 256 * splits;
+    const double waves = (double)((units + clusters - 1) / clusters);
+    const double prefix = waves * (per * (fp8 ? 0.75 : 0.62) + 9) + (fp8 ? 3 : 0);
+    const double states = (splits + 1.0) * rows * H * (mla::kL + 1) * 8 / 5e6;  // written and read
+    return prefix + 12 + page * rows * own_pages / pairs + 4 + states < alone;
+}
+
 bool plan_prefix(mla_kv_dtype kv, int rows, int H, int prefix_len, int num_splits, int max_seq_len, PrefixPlan* w) {
     // tokens past max_seq_len are no request's
-    const int pages = std::min(prefix_len, (max_seq_len + mla::kPage - 1) / mla::kPage * mla::kPage) / mla::kPage;
-    w->pages = pages;
+    const int seen = (max_seq_len + mla::kPage - 1) / mla::kPage;
+    const int pages = std::min(prefix_len / mla::kPage, seen);
     const int64_t flat = (int64_t)rows * H;
+    const bool fp8 = kv == MLA_KV_FP8_E4M3_SCALED;
     if (pages > 0) {
         const int clusters = mla::prefix_clusters();
         if (clusters < 1) return false;
-        mla::prefix_split(flat, pages, clusters, &w->splits, &w->pages_per_split);
-        size_t off = 0;
-        if (kv == MLA_KV_FP8_E4M3_SCALED) {
-            w->widened = off;
-            off += up256((size_t)pages * mla::kPage * mla::kBf16RowBytes);
-            w->scales = off;
-            off += up256((size_t)pages * mla::kPage * 2 * sizeof(float));
+        int splits, per;
+        mla::prefix_split(flat, pages, clusters, &splits, &per);
+        if (prefix_pays(fp8, rows, H, pages, seen - pages, clusters, splits, per)) {
+            w->pages = pages;
+            w->splits = splits;
+            w->pages_per_split = per;
+            size_t off = 0;
+            if (fp8) {
+                w->widened = off;
+                off += up256((size_t)pages * mla::kPage * mla::kBf16RowBytes);
+                w->scales = off;
+                off += up256((size_t)pages * mla::kPage * 2 * sizeof(float));
+            }
+            w->part_o = off;
+            off += up256((size_t)splits * flat * mla::kL * sizeof(float));
+            w->part_lse = off;
+            off += up256((size_t)splits * flat * sizeof(float));
+            w->decode = off;
         }
-        w->part_o = off;
-        off += up256((size_t)w->splits * flat * mla::kL * sizeof(float));
-        w->part_lse = off;
-        off += up256((size_t)w->splits * flat * sizeof(float));
-        w->decode = off;
     }
-    const int own_len = std::max(0, max_seq_len - pages * mla::kPage);
+    const int own_len = std::max(0, max_seq_len - w->pages * mla::kPage);
     // With more rows than SM pairs mla_decode's default builds a schedule on the device, about 10 us
     // ahead of everything else. Behind a prefix the requests' own tokens are usually few: up to 32
-    // pages each row is one unit instead.
-    if (num_splits == -1 && w->splits > 0 && own_len <= 32 * mla::kPage && rows > 76)
-        num_splits = 1;
+    // pages each row is one unit instead (2048 rows of 16 heads, up to 1000 own tokens: 150 -> 140 us).
+    if (num_splits == -1 && w->splits > 0 && own_len <= 32 * mla::kPage && rows > 76) num_splits = 1;
     w->own_splits = mla_resolve_num_splits(num_splits, rows, 1, H, own_len);
     if (w->own_splits < 1 && w->own_splits != -2) return false;
     w->total = w->decode + mla::workspace_layout(kv, rows, rows, H, w->own_splits, own_len, w->splits > 0).total;

@@ -17,26 +17,41 @@ def _status():
 
 
 # -------------------------------------------------------------------------------- shared prefix
-def _prefix(c, num_splits=-1, status=None, **kw):
+# Small calls run on the decode kernels alone, larger ones on the prefix kernel too (`_kernel` says
+# which from the workspace: its partial states come on top of the decode's).
+def _prefix(c, num_splits=-1, status=None, max_len=None, **kw):
     import mla_latent_kv_gb300 as mla
-    return mla.decode_shared_prefix(c["q"], c["cache"], c["table"], c["seq_lens"], c["max_len"], c["prefix"], c["scale"],
-                                    kv_dtype=c["kv"], num_splits=num_splits, dev_status=status,
+    return mla.decode_shared_prefix(c["q"], c["cache"], c["table"], c["seq_lens"], max_len or c["max_len"], c["prefix"],
+                                    c["scale"], kv_dtype=c["kv"], num_splits=num_splits, dev_status=status,
                                     num_blocks=c["num_blocks"], **kw)
 
 
+def _kernel(c, num_splits=-1):
+    import mla_latent_kv_gb300 as mla
+    B, Sq, H = c["B"], c["Sq"], c["H"]
+    S = mla.resolve_num_splits(num_splits, B, Sq, H, c["max_len"])
+    return mla.decode_shared_prefix_workspace_bytes(B, Sq, H, c["prefix"], c["max_len"], c["kv"], num_splits) != \
+        mla.workspace_bytes(B, Sq, H, S, c["kv"], c["max_len"])
+
+
 @pytest.mark.parametrize("kv", [BF, F8])
-@pytest.mark.parametrize("B,Sq,H,prefix,suffix", [
-    (1, 1, 1, 64, [1]),                      # one row of one head, one page
-    (2, 1, 16, 128, [172, 3]),
-    (3, 1, 20, 192, [1, 64, 65]),            # odd number of prefix pages, heads not a tile
-    (5, 2, 128, 640, [2, 63, 130, 64, 7]),   # ten row tiles
-    (9, 3, 37, 320, [3, 5, 64, 66, 200, 4, 9, 128, 129]),
-    (2, 1, 128, 4096, [1, 100]),             # a long prefix, few rows: divided over the device
-    (130, 1, 8, 1024, [1 + b % 90 for b in range(130)]),  # more rows than SM pairs
+@pytest.mark.parametrize("B,Sq,H,prefix,suffix,kernel", [
+    (1, 1, 1, 64, [1], False),                      # one row of one head, one page
+    (2, 1, 16, 128, [172, 3], False),
+    (3, 1, 20, 192, [1, 64, 65], False),
+    (9, 3, 37, 320, [3, 5, 64, 66, 200, 4, 9, 128, 129], False),
+    (2, 1, 128, 4096, [1, 100], False),
+    (150, 1, 5, 448, [1 + b % 70 for b in range(150)], True),      # 750 rows: the last tile a partial one
+    (101, 2, 7, 704, [2 + b % 130 for b in range(101)], True),     # 11 pages, ranges of an even number
+    (200, 1, 1, 960, [1 + b % 64 for b in range(200)], True),      # one tile, 200 of its 256 rows
+    (130, 1, 8, 1024, [1 + b % 90 for b in range(130)], True),
+    (33, 3, 37, 1984, [3 + 9 * b for b in range(33)], True),       # 31 pages, 37 heads
+    (36, 1, 128, 4160, [1 + 16 * b for b in range(36)], True),     # whole tiles, 65 pages
 ])
-def test_shared_prefix(kv, B, Sq, H, prefix, suffix):
+def test_shared_prefix(kv, B, Sq, H, prefix, suffix, kernel):
     c = paged_case([prefix + s for s in suffix], Sq, H, kv, seed=B * 100 + H, prefix=prefix,
                    scale_v=0.5 if kv == F8 else None)
+    assert _kernel(c) == kernel
     st = _status()
     o, lse = _prefix(c, status=st)
     assert int(st.item()) == 0
@@ -45,36 +60,53 @@ def test_shared_prefix(kv, B, Sq, H, prefix, suffix):
 
 @pytest.mark.parametrize("kv", [BF, F8])
 @pytest.mark.parametrize("num_splits", [1, 3, 0, -1, -2])
-def test_shared_prefix_suffix_splits_and_bf16_output(kv, num_splits):
+@pytest.mark.parametrize("B", [4, 112])
+def test_shared_prefix_suffix_splits_and_bf16_output(kv, num_splits, B):
     import mla_latent_kv_gb300 as mla
-    c = paged_case([576 + s for s in (1, 700, 64, 129)], 1, 32, kv, seed=7, prefix=576)
+    c = paged_case([640 + (1, 700, 64, 129)[b % 4] for b in range(B)], 1, 12, kv, seed=7, prefix=640)
+    assert _kernel(c, num_splits) == (B == 112)
     o, lse = _prefix(c, num_splits, o_dtype=mla.DT_BF16)
     check_attention(o, lse, attend(c), bf16_out=True)
 
 
 @pytest.mark.parametrize("kv", [BF, F8])
-def test_shared_prefix_rows_inside_the_prefix(kv):
+@pytest.mark.parametrize("B", [10, 140])
+def test_shared_prefix_rows_inside_the_prefix(kv, B):
     """Requests shorter than the prefix see their own tokens only; empty slots give o = 0, lse = -inf."""
-    lens = [256 + 70, 0, 1, 2, 64, 100, 255, 256, 257, 0]
-    c = paged_case(lens, 2, 40, kv, seed=11, prefix=256)
+    lens = [[640 + 70, 0, 1, 2, 64, 100, 255, 640, 641, 0][b % 10] for b in range(B)]
+    c = paged_case(lens, 2, 6, kv, seed=11, prefix=640)
+    assert _kernel(c) == (B == 140)
     o, lse = _prefix(c)
     check_attention(o, lse, attend(c))
 
 
 @pytest.mark.parametrize("kv", [BF, F8])
 def test_shared_prefix_every_slot_empty_and_no_prefix(kv):
-    c = paged_case([0, 0, 0], 1, 16, kv, seed=12, prefix=128)
-    o, lse = _prefix(c)
-    check_attention(o, lse, attend(c))
+    c = paged_case([0] * 120, 1, 16, kv, seed=12, prefix=704)
+    for max_len in (0, 704, 704 + 64):  # a captured step's bound, whatever the slots hold
+        c["max_len"] = max_len
+        assert _kernel(c) == (max_len > 0)
+        o, lse = _prefix(dict(c, table=torch_pad(c["table"], 13)), max_len=max_len)
+        check_attention(o, lse, attend(c))
     c = paged_case([300, 5], 1, 16, kv, seed=13, prefix=0)
     o, lse = _prefix(c)
     check_attention(o, lse, attend(c))
 
 
-def test_shared_prefix_moving_maximum():
+def torch_pad(table, cols):
+    """The table with -1 columns behind, `cols` in all."""
+    import torch
+    out = torch.full((table.shape[0], cols), -1, dtype=torch.int32, device="cuda")
+    out[:, :table.shape[1]] = table
+    return out
+
+
+@pytest.mark.parametrize("B", [2, 130])
+def test_shared_prefix_moving_maximum(B):
     """Keys that grow along the prefix: the running maximum moves past the rescale threshold often."""
     import torch
-    c = paged_case([1024 + 40, 1024 + 3], 1, 64, BF, seed=14, prefix=1024)
+    c = paged_case([1024 + (40, 3)[b % 2] for b in range(B)], 1, 9, BF, seed=14, prefix=1024)
+    assert _kernel(c) == (B == 130)
     rows = c["cache"].view(torch.bfloat16).view(c["num_blocks"], PAGE, D)
     for i, blk in enumerate(c["full_table"][0, :16]):
         rows[int(blk)] *= 1.0 + i
@@ -120,8 +152,11 @@ def test_shared_prefix_repeats_bit_for_bit(kv):
         assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
 
 
-def test_shared_prefix_bad_prefix_block_is_reported():
-    c = paged_case([200, 210], 1, 16, BF, seed=16, prefix=128)
+@pytest.mark.parametrize("kv", [BF, F8])
+@pytest.mark.parametrize("B", [2, 128])
+def test_shared_prefix_bad_prefix_block_is_reported(kv, B):
+    c = paged_case([700] * B, 1, 16, kv, seed=16, prefix=640)
+    assert _kernel(c) == (B == 128)
     c["table"][0, 1] = c["num_blocks"] + 3
     st = _status()
     _prefix(c, status=st)
@@ -131,8 +166,8 @@ def test_shared_prefix_bad_prefix_block_is_reported():
 def test_shared_prefix_workspace_is_checked():
     import torch
     import mla_latent_kv_gb300 as mla
-    c = paged_case([600, 610], 1, 128, BF, seed=17, prefix=512)
-    need = mla.decode_shared_prefix_workspace_bytes(2, 1, 128, 512, c["max_len"])
+    c = paged_case([700 + b for b in range(128)], 1, 16, BF, seed=17, prefix=640)
+    need = mla.decode_shared_prefix_workspace_bytes(128, 1, 16, 640, c["max_len"])
     if need:
         with pytest.raises(mla.MlaError) as e:
             _prefix(c, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
@@ -428,8 +463,9 @@ def test_shared_prefix_step_in_a_graph(kv):
     two captured calls that take turns on one workspace."""
     import torch
     import mla_latent_kv_gb300 as mla
-    B, H, prefix = 6, 64, 512
-    c = paged_case([prefix + s for s in (1, 70, 300, 64, 5, 129)], 1, H, kv, seed=97, prefix=prefix)
+    B, H, prefix = 120, 16, 640
+    c = paged_case([prefix + (1, 70, 300, 64, 5, 129)[b % 6] for b in range(B)], 1, H, kv, seed=97, prefix=prefix)
+    assert _kernel(c)
     rng = np.random.default_rng(98)
     e = mi.e2e_case(B, 1, H, [64] * B, seed=99)
     qn, qp = bf16(e["q_nope"]).view(B, H, 128), bf16(e["q_pe"]).view(B, H, 64)
