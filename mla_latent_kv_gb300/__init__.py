@@ -422,8 +422,11 @@ def _attention_bufs(q, B, Sq, H, o_latent, o_dtype, lse, workspace, need):
     workspace bytes)."""
     import torch
     o_dtype = _dt_code(o_latent, o_dtype)
-    o_latent = _out_buf(o_latent, (B, Sq, H, L), o_dtype, q.device)
-    lse = _out_buf(lse, (B, Sq, H), DT_F32, q.device)
+    if o_latent is None or o_latent.shape != (B, Sq, H, L) or not o_latent.is_contiguous() or \
+            o_latent.dtype is not (torch.float32 if o_dtype == DT_F32 else torch.bfloat16):
+        o_latent = _out_buf(o_latent, (B, Sq, H, L), o_dtype, q.device)  # makes it, or says what is wrong
+    if lse is None or lse.shape != (B, Sq, H) or not lse.is_contiguous() or lse.dtype is not torch.float32:
+        lse = _out_buf(lse, (B, Sq, H), DT_F32, q.device)
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     return o_latent, o_dtype, lse, workspace, 0 if workspace is None else workspace.nbytes
