@@ -170,13 +170,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // fetches the first group's block-table entries while the length is still on its way
     // (validated once the page count is known).
     int blk_early[kPPG] = {-1, -1, -1, -1};
-    const bool early_blocks =
-        p.plan_units == nullptr && p.qsl == nullptr && p.order != kOrderWaitFirst && unit % p.num_splits == 0;
-    if (early_blocks && tid == 0 && rank == 0) {
+    const bool early_blocks = p.plan_units == nullptr && p.qsl == nullptr && unit % p.num_splits == 0;
+    auto fetch_blocks = [&]() {
+        if (!early_blocks || tid != 0 || rank != 0) return;
 #pragma unroll
         for (int q = 0; q < kPPG; ++q)
             if (p.base / kPage + q < p.max_blocks) blk_early[q] = ld_nc_s32(table_entry(p, unit / p.num_splits / p.Sq, q));
-    }
+    };
+    if (p.order != kOrderWaitFirst) fetch_blocks();
     RowGeom g{};
     if (!p.plan_units && p.order != kOrderWaitFirst)
         g = row_geometry(p, unit, tid == 0 && rank == 0);  // its loads overlap the set-up
@@ -217,6 +218,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             cluster_sync();
             return;
         }
+        if (p.order == kOrderWaitFirst) fetch_blocks();
         g = row_geometry(p, unit, tid == 0 && rank == 0);
     }
     const int npages = g.npages;
