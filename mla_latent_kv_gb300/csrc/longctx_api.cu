@@ -124,7 +124,7 @@ bool plan_prefix(mla_kv_dtype kv, int rows, int H, int prefix_len, int num_split
     // ahead of everything else. Behind a prefix the requests' own tokens are usually few: up to 32
     // pages each row is one unit instead (2048 rows of 16 heads, up to 1000 own tokens: 150 -> 140 us).
     if (num_splits == -1 && w->splits > 0 && own_len <= 32 * mla::kPage && rows > 76) num_splits = 1;
-    w->own_splits = mla_resolve_num_splits(num_splits, rows, 1, H, own_len);
+    w->own_splits = mla::resolve_splits(mla::few_heads(kv, H), num_splits, rows, H, own_len);
     if (w->own_splits < 1 && w->own_splits != -2) return false;
     w->total = w->decode + mla::workspace_layout(kv, rows, rows, H, w->own_splits, own_len, w->splits > 0).total;
     return true;
@@ -243,7 +243,7 @@ size_t mla_decode_sparse_workspace_bytes(mla_kv_dtype kv_dtype, int B, int Sq, i
         max_sel > INT32_MAX / mla::kPage || (int64_t)B * Sq > INT32_MAX / MLA_MAX_HEADS)
         return 0;
     const int rows = B * Sq;
-    const int S = mla_resolve_num_splits(num_splits, rows, 1, H, max_sel * mla::kPage);
+    const int S = mla::resolve_splits(mla::few_heads(kv_dtype, H), num_splits, rows, H, max_sel * mla::kPage);
     if (S < 1 && S != -2) return 0;
     return sparse_layout(kv_dtype, rows, H, max_sel, S).total;
 }
@@ -274,7 +274,7 @@ mla_status mla_decode_sparse(const void* q, const void* kv_cache, mla_kv_dtype k
     if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(o_latent))
         return set_error(MLA_ERR_UNSUPPORTED, "%s: q, kv_cache and o_latent must be 16-byte aligned", who);
     const int rows = B * Sq;
-    const int S = mla_resolve_num_splits(num_splits, rows, 1, H, max_sel * mla::kPage);
+    const int S = mla::resolve_splits(mla::few_heads(kv_dtype, H), num_splits, rows, H, max_sel * mla::kPage);
     if (S < 1 && S != -2) return set_error(MLA_ERR_CUDA, "%s: could not resolve num_splits (no CUDA device?)", who);
     const SparseLayout w = sparse_layout(kv_dtype, rows, H, max_sel, S);
     if (!workspace || workspace_bytes < w.total)
@@ -297,6 +297,7 @@ mla_status mla_decode_sparse(const void* q, const void* kv_cache, mla_kv_dtype k
     if (e != cudaSuccess) return cuda_error(e, who);
     mla::DecodeExtra x;
     x.who = who;
+    x.few = mla::few_heads(kv_dtype, H);
     x.order = mla::kOrderWaitFirst;
     return mla::decode_impl(q, kv_cache, kv_dtype, num_blocks, t.table, max_sel, t.lens, nullptr, max_sel * mla::kPage,
                             rows, 1, rows, H, scale, S, (char*)workspace + w.decode, w.total - w.decode, o_latent,
@@ -327,6 +328,7 @@ mla_status mla_decode_shared_prefix(const void* q, const void* kv_cache, mla_kv_
                          (long long)max_blocks * mla::kPage);
     mla::DecodeExtra x;
     x.who = who;
+    x.few = mla::few_heads(kv_dtype, H);
     x.shared_pages = prefix_len / mla::kPage;
     auto decode = [&](int splits, void* ws, size_t bytes) {
         return mla::decode_impl(q, kv_cache, kv_dtype, num_blocks, block_table, max_blocks, seq_lens, nullptr,

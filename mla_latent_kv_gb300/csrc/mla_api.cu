@@ -87,6 +87,26 @@ mla_status set_error(mla_status st, const char* fmt, ...) {
 }
 
 mla_status set_ok() { return ok(); }
+
+int resolve_splits(bool few, int num_splits, int rows, int H, int max_seq_len) {
+    if (!few || num_splits != -1) return mla_resolve_num_splits(num_splits, rows, 1, H, max_seq_len);
+    const int sms = device_sm_count();
+    if (sms < 1) return -1;
+    if (rows > sms) return -2;
+    // one SM a unit; a unit's fixed part is about six pages' time
+    const int pages = std::max(1, (max_seq_len + kPage - 1) / kPage);
+    int best = 1;
+    double least = 1e300;
+    for (int S = 1; S <= pages; ++S) {
+        const int64_t waves = ((int64_t)rows * S + sms - 1) / sms;
+        const double t = (double)waves * ((pages + S - 1) / S + 6) + (S > 1 ? 3 + 0.002 * rows * H * S / 64 : 0);
+        if (t < least * 0.999) {
+            least = t;
+            best = S;
+        }
+    }
+    return best;
+}
 }  // namespace mla
 
 extern "C" {
@@ -237,10 +257,10 @@ mla_status decode_impl(const void* q, const void* kv_cache, mla_kv_dtype kv_dtyp
     if (rows * H > (int64_t)INT32_MAX)
         return fail(MLA_ERR_UNSUPPORTED, "%s: rows*H=%lld too large", x.who, (long long)(rows * H));
     if (x.check_only) return ok();
-    int S = mla_resolve_num_splits(num_splits, (int)rows, 1, H, std::max(0, max_seq_len - x.base));
+    int S = mla::resolve_splits(x.few, num_splits, (int)rows, H, std::max(0, max_seq_len - x.base));
     const bool planned = S == -2;
     if (S < 1 && !planned) return fail(MLA_ERR_CUDA, "%s: could not resolve num_splits (no CUDA device?)", x.who);
-    const int pairs = planned ? std::max(1, device_sm_count() / 2) : 1;
+    const int pairs = planned ? std::max(1, device_sm_count() / 2) : 1;  // the schedule's size, also for few heads
     const int64_t max_units = planned ? mla::plan_max_units(rows, pairs) : rows * S;
     if (max_units > (int64_t)1 << 30)
         return fail(MLA_ERR_UNSUPPORTED, "%s: %lld work units too many", x.who, (long long)max_units);
@@ -297,14 +317,16 @@ mla_status decode_impl(const void* q, const void* kv_cache, mla_kv_dtype kv_dtyp
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e = cudaSuccess;
     if (planned) {
-        e = mla::launch_plan(a, pairs, st);
+        e = mla::launch_plan(a, x.few ? 2 * pairs : pairs, st);
         if (e != cudaSuccess) return cuda_fail(e, x.who, "schedule launch");
     }
     if (x.between) {
         e = x.between(x.between_arg);
         if (e != cudaSuccess) return cuda_fail(e, x.who, "launch");
     }
-    e = fp8 ? mla::launch_decode_fp8_sm103(a, st) : mla::launch_decode_sm103(a, st);
+    e = fp8     ? mla::launch_decode_fp8_sm103(a, st)
+        : x.few ? mla::launch_decode_few_sm103(a, st)
+                : mla::launch_decode_sm103(a, st);
     if (e != cudaSuccess) return cuda_fail(e, x.who, "decode launch");
     if (planned || S > 1 || x.all_partial) {
         e = mla::launch_merge(a, st);

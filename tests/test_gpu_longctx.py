@@ -28,10 +28,9 @@ def _prefix(c, num_splits=-1, status=None, max_len=None, **kw):
 
 def _kernel(c, num_splits=-1):
     import mla_latent_kv_gb300 as mla
-    B, Sq, H = c["B"], c["Sq"], c["H"]
-    S = mla.resolve_num_splits(num_splits, B, Sq, H, c["max_len"])
-    return mla.decode_shared_prefix_workspace_bytes(B, Sq, H, c["prefix"], c["max_len"], c["kv"], num_splits) != \
-        mla.workspace_bytes(B, Sq, H, S, c["kv"], c["max_len"])
+    need = [mla.decode_shared_prefix_workspace_bytes(c["B"], c["Sq"], c["H"], prefix, c["max_len"], c["kv"], num_splits)
+            for prefix in (c["prefix"], 0)]
+    return need[0] != need[1]
 
 
 @pytest.mark.parametrize("kv", [BF, F8])
@@ -358,6 +357,30 @@ def test_sparse_decode(kv, num_splits, Sq, H, K, lens):
         check_attention(o, lse, attend(c, lists))
 
 
+@pytest.mark.parametrize("H", [1, 8, 16, 17, 32, 33, 48, 49, 64, 65])
+@pytest.mark.parametrize("num_splits", [1, 3])
+def test_sparse_decode_head_counts_over_long_rows(H, num_splits):
+    """Up to 64 heads of a bf16 cache take a kernel of their own; rings wrap several times."""
+    import torch
+    lens = [64 * 40 + 7, 64 * 23, 1, 130]
+    c = paged_case(lens, 1, H, BF, seed=84)
+    rows = c["cache"].view(torch.bfloat16).view(c["num_blocks"], PAGE, D)
+    for i, blk in enumerate(c["full_table"][0, :41]):  # a running maximum that moves late, too
+        if i in (9, 30):
+            rows[int(blk)] *= 6.0
+    pages, lists = _pick(c, 45, 85, gaps=True)
+    pages[0], lists[0] = _all(lens[0], 45)
+    st = _status()
+    o, lse = _sparse(c, pages, num_splits, st)
+    assert int(st.item()) == 0
+    check_attention(o, lse, attend(c, lists))
+
+
+def _all(n, K):
+    ids = list(range(-(-n // PAGE)))
+    return np.array([ids + [-1] * (K - len(ids))], np.int32), [ids]
+
+
 def test_sparse_decode_many_rows_bf16_output():
     import mla_latent_kv_gb300 as mla
     lens = [1 + (37 * b) % 900 for b in range(100)]
@@ -370,7 +393,7 @@ def test_sparse_decode_many_rows_bf16_output():
 def test_sparse_decode_of_all_pages_is_decode():
     import torch
     import mla_latent_kv_gb300 as mla
-    c = paged_case([700, 64, 1, 1000], 1, 64, BF, seed=92)
+    c = paged_case([700, 64, 1, 1000], 1, 65, BF, seed=92)
     pages = np.full((4, 1, 16), -1, np.int32)
     for b, n in enumerate(c["lens"]):
         pages[b, 0, :-(-int(n) // PAGE)] = np.arange(-(-int(n) // PAGE))
