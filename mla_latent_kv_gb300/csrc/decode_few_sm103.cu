@@ -3,7 +3,7 @@
 // What it computes is what the decode kernel does for a unit: one query row, tokens [j0, j1). That
 // kernel puts the heads on the tensor core's M side (128 rows, of which 16 heads use an eighth) and
 // needs two SMs for the 128 x 512 accumulator. With few heads the operands are swapped: the tokens
-// and the latent dims are the M side, the heads the N side (N = 16, 32, 48 or 64):
+// and the latent dims are the M side, the heads the N side (N = 16, 32 or 64):
 //     S^T[token, head] = K Q^T     36 MMAs a page, M = 128 (the page's 64 rows; the other 64 are
 //                                  whatever follows in shared memory, and their results unused)
 //     O^T[dim, head] += V^T P^T    4 blocks of 128 dims x 4 steps of 16 tokens, V^T read from the same
@@ -41,7 +41,7 @@ namespace {
 using namespace ptx;
 using namespace dec;
 
-constexpr int kThreads = 384;           // warp 0 TMA, warp 1 MMA, warps 4-11 softmax and epilogue
+constexpr int kThreads = 384;           // warp 0 TMA, 1 MMA, 2-3 L2 prefetch, 4-11 softmax and epilogue
 constexpr int kWork = 256;
 constexpr int kPanel = kPage * 128;     // one page's rows of one 64-dim panel (8 KB)
 constexpr int kPair = 2 * kPanel;
@@ -49,6 +49,7 @@ constexpr int kCtrl = 4096;
 constexpr int kSmemLimit = 232448;
 constexpr int kMaxPairs = 11, kMaxRopes = 3;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr int kAhead = 3;               // pages between the softmax's progress and the page prefetched into L2
 
 // Shared memory for N = 2 NH heads: the rings first, since an MMA of M = 128 reads 8 KB past a panel.
 template <int NH>
@@ -56,8 +57,8 @@ struct Layout {
     static constexpr int N = 2 * NH;
     static constexpr int kQPanel = N * 128;  // N heads x 64 dims
     static constexpr int kP = N * 128;       // N heads x 64 tokens
-    static constexpr int kRopes = NH <= 16 ? 3 : NH <= 24 ? 2 : 1;
-    static constexpr int kPBufs = NH <= 24 ? 2 : 1;
+    static constexpr int kRopes = NH <= 16 ? 3 : 1;
+    static constexpr int kPBufs = NH <= 16 ? 2 : 1;
     static constexpr int kPairs = (kSmemLimit - kCtrl - 9 * kQPanel - kPBufs * kP - kRopes * kPanel) / kPair;
     static constexpr int kRing = kCtrl;
     static constexpr int kRope = kRing + kPairs * kPair;
@@ -85,22 +86,38 @@ enum : int {
 };
 static_assert(8 * B_COUNT <= 512, "barrier slots");
 constexpr int OFF_TMEM = 512, OFF_ABORT = 516;
+constexpr int OFF_PROG = 520;    // pages whose softmax is done (paces the L2 prefetch)
 constexpr int OFF_MX = 1024;     // f32 [2][64] maxima of the two token quarters; at the end sums of l
 constexpr int OFF_LT = 1536;     // f32 [2][64] sums of lt
 constexpr int OFF_ALPHA = 2048;  // f32 [64]
 constexpr int OFF_M = 2304;      // f32 [64] final running maxima (log2 units)
 constexpr uint32_t kBarOr = 1, kBarWork = 2;
 
-__device__ __forceinline__ float warp_max(float x) {
+// The maximum or sum over the warp of each of v[0 .. NH), NH a power of two up to 32: in each step a lane
+// keeps half of its values and gives the other half away, so that it ends with the value of index
+// reduced_index<NH>(lane) in v[0] after 31 exchanges at most (one value at a time takes 5 NH).
+template <int NH, bool kMax, int O = 16, int n = NH>
+__device__ __forceinline__ void warp_reduce(float (&v)[NH], int lane) {
+    auto op = [](float a, float b) { return kMax ? fmaxf(a, b) : a + b; };
+    if constexpr (n > 1) {
+        const bool up = (lane & O) != 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-    return x;
+        for (int k = 0; k < n / 2; ++k) {
+            const float other = __shfl_xor_sync(0xffffffffu, up ? v[k] : v[k + n / 2], O);
+            v[k] = op(up ? v[k + n / 2] : v[k], other);
+        }
+    } else {
+        v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], O));
+    }
+    if constexpr (O > 1) warp_reduce<NH, kMax, O / 2, (n > 1 ? n / 2 : 1)>(v, lane);
 }
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
+template <int NH>
+__device__ __forceinline__ int reduced_index(int lane) {
+    return NH == 32 ? lane : NH == 16 ? lane >> 1 : lane >> 2;
 }
+
+// Hint: bring the 128-byte line at `ptr` into L2 (no effect on correctness).
+__device__ __forceinline__ void prefetch_l2(const void* ptr) { asm volatile("prefetch.global.L2 [%0];" ::"l"(ptr)); }
 
 template <int NH>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -126,6 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto bar = [&](int i) -> uint32_t { return sbase + 8u * (uint32_t)i; };
     if (tid == 0) {
         *abort = 0;
+        *reinterpret_cast<volatile int*>(smem + OFF_PROG) = 0;
         for (int i = 0; i < B_COUNT; ++i) {
             uint32_t cnt = 1;
             if (i >= B_SE && i < B_SE + 2) cnt = 4;
@@ -306,11 +324,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool any = named_bar_or(kBarOr, kWork, need);
             if (any) {
                 if (tokens) {
+                    float x[NH];
 #pragma unroll
-                    for (int k = 0; k < NH; ++k) {
-                        const float x = warp_max(__uint_as_float(s[k]));
-                        if (lane == 0) mx[64 * quarter + h0 + k] = x;
-                    }
+                    for (int k = 0; k < NH; ++k) x[k] = __uint_as_float(s[k]);
+                    warp_reduce<NH, true>(x, lane);
+                    mx[64 * quarter + h0 + reduced_index<NH>(lane)] = x[0];
                 }
                 named_bar(kBarWork, kWork);
                 if (tokens) {
@@ -375,58 +393,86 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_cta();  // P and the zeros, before the MMAs read them
             tc_fence_before();
             bar_arrive(bar(B_PF + buf));
+            if (wtid == 0) *reinterpret_cast<volatile int*>(smem + OFF_PROG) = i + 1;
         }
         // sums over the tokens; l and lt of the two quarters meet in shared memory
         named_bar(kBarWork, kWork);
         if (tokens) {
+            if (quarter == 0 && lane == 0) {
 #pragma unroll
-            for (int k = 0; k < NH; ++k) {
-                const float a = warp_sum(l[k]), b = warp_sum(lt[k]);
-                if (lane == 0) {
-                    mx[64 * quarter + h0 + k] = a;
-                    lts[64 * quarter + h0 + k] = b;
-                    if (quarter == 0) m_s[h0 + k] = m[k];
-                }
+                for (int k = 0; k < NH; ++k) m_s[h0 + k] = m[k];
             }
+            warp_reduce<NH, false>(l, lane);
+            warp_reduce<NH, false>(lt, lane);
+            mx[64 * quarter + h0 + reduced_index<NH>(lane)] = l[0];
+            lts[64 * quarter + h0 + reduced_index<NH>(lane)] = lt[0];
         }
         output_wait(p, unit);
         const bool has_o = npages > 0 && !*abort;
         const bool o_ok = has_o && warp_wait(bar(B_PE + ((npages - 1) & 1)), ((npages - 1) >> 1) & 1, abort, ds);
         tc_fence_after();
         named_bar(kBarWork, kWork);
-        if (wtid < p.H) {
+        if (wtid < N) {
             const float lv = mx[wtid] + mx[64 + wtid], ltv = lts[wtid] + lts[64 + wtid];
-            const float lse = !o_ok || !(lv > 0.f) ? -CUDART_INF_F : (m_s[wtid] + log2f(ltv)) * 0.6931471805599453f;
-            if (g.slot >= 0)
-                p.part_lse[(size_t)g.slot * p.H + wtid] = lse;
-            else if (p.lse)
-                p.lse[(size_t)g.r * p.H + wtid] = lse;
+            const bool empty = !o_ok || !(lv > 0.f);
+            alpha_s[wtid] = empty ? 0.f : 1.f / lv;
+            if (wtid < p.H) {
+                const float lse = empty ? -CUDART_INF_F : (m_s[wtid] + log2f(ltv)) * 0.6931471805599453f;
+                if (g.slot >= 0)
+                    p.part_lse[(size_t)g.slot * p.H + wtid] = lse;
+                else if (p.lse)
+                    p.lse[(size_t)g.r * p.H + wtid] = lse;
+            }
         }
+        named_bar(kBarWork, kWork);
         // O^T / l: a warp's lanes are 32 consecutive dims of one head, so its stores are whole lines
         const bool f32 = g.slot >= 0 || p.o_dtype == MLA_DT_F32;
         const size_t row = (size_t)(g.slot >= 0 ? g.slot : g.r) * p.H;
         float* of = g.slot >= 0 ? p.part_o : (float*)p.o_latent;
         uint16_t* oh = (uint16_t*)p.o_latent;
-#pragma unroll 1
-        for (int b = 2 * set; b < 2 * set + 2; ++b) {
-            const int dim = 128 * b + 32 * quarter + lane;
-#pragma unroll 1
-            for (int hb = 0; hb < p.H; hb += 8) {
-                uint32_t v[8];
-                tmem_ld8(tmem + lane_base + Lay::kO + (uint32_t)(b * N + hb), v);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int dim = 128 * (2 * set + b) + 32 * quarter + lane;
+#pragma unroll
+            for (int hb = 0; hb < N; hb += 16) {
+                uint32_t v[16];
+                const uint32_t col = tmem + lane_base + Lay::kO + (uint32_t)((2 * set + b) * N + hb);
+                tmem_ld8(col, v);
+                tmem_ld8(col + 8u, v + 8);
                 tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 16; ++k) {
                     const int h = hb + k;
-                    if (h >= p.H) break;
-                    const float lv = mx[h] + mx[64 + h];
-                    const float x = o_ok && lv > 0.f ? __uint_as_float(v[k]) / lv : 0.f;
-                    if (f32)
-                        of[(row + h) * kL + dim] = x;
-                    else
-                        oh[(row + h) * kL + dim] = (uint16_t)(pack_bf16x2(x, 0.f) & 0xffffu);
+                    const float inv = alpha_s[h];
+                    const float x = inv > 0.f ? __uint_as_float(v[k]) * inv : 0.f;  // an empty row: O may hold anything
+                    if (h < p.H) {
+                        if (f32)
+                            of[(row + h) * kL + dim] = x;
+                        else
+                            oh[(row + h) * kL + dim] = (uint16_t)(pack_bf16x2(x, 0.f) & 0xffffu);
+                    }
                 }
             }
+        }
+    } else {
+        // Warps 2, 3: pages that the ring has no room for yet are brought into L2, kAhead pages
+        // past the last one whose softmax is done. Only a hint: gives up quietly if it falls behind.
+        const volatile int* prog = reinterpret_cast<const volatile int*>(smem + OFF_PROG);
+        int spins = 0;
+        for (int t = 2; t < npages; ++t) {
+            bool go = true;
+            while (*prog < t - kAhead) {
+                if (*abort || ++spins > (1 << 20)) {
+                    go = false;
+                    break;
+                }
+                __nanosleep(128);
+            }
+            if (!go) break;
+            const int32_t blk = *table_entry(p, g.b, g.page0 + t);
+            if (blk < 0 || (int64_t)blk >= p.num_blocks) continue;
+            const uint8_t* page = p.cache + (size_t)blk * (kPage * kBf16RowBytes);
+            for (int q = tid - 64; q < kPage * kBf16RowBytes / 128; q += 64) prefetch_l2(page + 128 * q);
         }
     }
 
@@ -476,7 +522,6 @@ cudaError_t launch(const DecodeArgs& a, cudaStream_t s) {
 cudaError_t launch_decode_few_sm103(const DecodeArgs& a, cudaStream_t s) {
     if (a.H <= 16) return launch<8>(a, s);
     if (a.H <= 32) return launch<16>(a, s);
-    if (a.H <= 48) return launch<24>(a, s);
     return launch<32>(a, s);
 }
 

@@ -93,13 +93,14 @@ int resolve_splits(bool few, int num_splits, int rows, int H, int max_seq_len) {
     const int sms = device_sm_count();
     if (sms < 1) return -1;
     if (rows > sms) return -2;
-    // one SM a unit; a unit's fixed part is about six pages' time
+    // us: one SM a unit, 1.5 a page and 9 for its start and end; the merge takes 3 and 0.1 a split
     const int pages = std::max(1, (max_seq_len + kPage - 1) / kPage);
     int best = 1;
     double least = 1e300;
     for (int S = 1; S <= pages; ++S) {
         const int64_t waves = ((int64_t)rows * S + sms - 1) / sms;
-        const double t = (double)waves * ((pages + S - 1) / S + 6) + (S > 1 ? 3 + 0.002 * rows * H * S / 64 : 0);
+        const double t = (double)waves * (1.5 * ((pages + S - 1) / S) + 9) +
+                         (S > 1 ? 3 + 0.1 * S + (double)rows * H * S * (kL + 1) * 8 / 5e6 : 0);
         if (t < least * 0.999) {
             least = t;
             best = S;
