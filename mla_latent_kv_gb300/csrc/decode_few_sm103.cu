@@ -1,9 +1,9 @@
-// decode_few_sm103.cu -- paged MLA decode over the bf16 cache for at most 64 heads, one SM per unit.
+// decode_few_sm103.cu -- paged MLA decode over the bf16 cache for at most 32 heads, one SM per unit.
 //
 // What it computes is what the decode kernel does for a unit: one query row, tokens [j0, j1). That
 // kernel puts the heads on the tensor core's M side (128 rows, of which 16 heads use an eighth) and
 // needs two SMs for the 128 x 512 accumulator. With few heads the operands are swapped: the tokens
-// and the latent dims are the M side, the heads the N side (N = 16, 32 or 64):
+// and the latent dims are the M side, the heads the N side (N = 16 or 32):
 //     S^T[token, head] = K Q^T     36 MMAs a page, M = 128 (the page's 64 rows; the other 64 are
 //                                  whatever follows in shared memory, and their results unused)
 //     O^T[dim, head] += V^T P^T    4 blocks of 128 dims x 4 steps of 16 tokens, V^T read from the same
@@ -12,7 +12,9 @@
 // never leaves it, and 152 units run at once.
 //
 // Bound: 74 KB a page from memory against about 52 MMAs of 50 cycles: at 152 units the cache stream
-// is the limit. 16 KB pairs of 64-dim panels go through a ring of 8 to 11 slots (two pages and more), the
+// is the limit. Measured over 64 rows of 128 selected pages of 16 heads: 122 us, 5.0 TB/s of pages
+// (few rows: 12 us for one of 16 pages, latency). Half as many bytes in flight, or prefetching further
+// ahead of the ring, was slower (144 us at 6 pages instead of kAhead). 16 KB pairs of 64-dim panels go through a ring of 10 or 11 slots (two pages and more), the
 // rope panels through one of their own; one thread loads, one warp issues, and eight warps do the rest: the
 // 64 tokens are lanes 0-63 of S^T (two lane quarters), each of two warp sets taking half of the heads.
 // A thread holds one token's scores of its heads; the row maximum over tokens is only formed when some
@@ -47,7 +49,7 @@ constexpr int kPanel = kPage * 128;     // one page's rows of one 64-dim panel (
 constexpr int kPair = 2 * kPanel;
 constexpr int kCtrl = 4096;
 constexpr int kSmemLimit = 232448;
-constexpr int kMaxPairs = 11, kMaxRopes = 3;
+constexpr int kMaxPairs = 11, kMaxRopes = 2;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr int kAhead = 3;               // pages between the softmax's progress and the page prefetched into L2
 
@@ -57,8 +59,8 @@ struct Layout {
     static constexpr int N = 2 * NH;
     static constexpr int kQPanel = N * 128;  // N heads x 64 dims
     static constexpr int kP = N * 128;       // N heads x 64 tokens
-    static constexpr int kRopes = NH <= 16 ? 3 : 1;
-    static constexpr int kPBufs = NH <= 16 ? 2 : 1;
+    static constexpr int kRopes = 2;
+    static constexpr int kPBufs = 2;
     static constexpr int kPairs = (kSmemLimit - kCtrl - 9 * kQPanel - kPBufs * kP - kRopes * kPanel) / kPair;
     static constexpr int kRing = kCtrl;
     static constexpr int kRope = kRing + kPairs * kPair;
@@ -66,22 +68,20 @@ struct Layout {
     static constexpr int kPBuf = kQ + 9 * kQPanel;
     static constexpr int kBytes = kPBuf + kPBufs * kP;
     // a page's scores are issued before the previous page's output: both pages' pairs are held
-    static_assert(kPairs >= 8 && kPairs <= kMaxPairs && kRopes <= kMaxRopes && kBytes <= kSmemLimit, "ring");
+    static_assert(kPairs >= 8 && kPairs <= 11 && kPairs <= kMaxPairs && kRopes <= kMaxRopes && kBytes <= kSmemLimit, "ring");
     static_assert(9 * kQPanel >= kPanel, "the last rope panel's MMA reads 8 KB on, into Q");
-    static constexpr uint32_t kCols = 6 * N <= 128 ? 128 : 6 * N <= 256 ? 256 : 512;  // a power of two
+    static constexpr uint32_t kCols = 6 * N <= 128 ? 128 : 256;  // a power of two
     static constexpr uint32_t kO = 2 * N;  // S^T buffers at 0 and N, O^T blocks from here
 };
 
 enum : int {
     B_KF = 0,                   // pair landed
-    B_KE = B_KF + kMaxPairs,    // pair's QK and PV MMAs completed
-    B_RF = B_KE + kMaxPairs,    // rope panel landed
-    B_RE = B_RF + kMaxRopes,    // rope panel's QK MMAs completed
-    B_Q = B_RE + kMaxRopes,     // Q landed
-    B_SF,                       // [2] S^T ready
+    B_RF = B_KF + kMaxPairs,    // rope panel landed
+    B_Q = B_RF + kMaxRopes,     // Q landed
+    B_SF,                       // [2] S^T of the page (by its parity) ready: its rope slot is free
     B_SE = B_SF + 2,            // [2] S^T read (one arrival of each of the four token warps)
     B_PF = B_SE + 2,            // [2] P written, O^T rescaled, V rows past the last token zeroed (256)
-    B_PE = B_PF + 2,            // [2] PV MMAs of the page (by its parity) completed
+    B_PE = B_PF + 2,            // [2] PV MMAs of the page completed: its pair slots are free
     B_COUNT = B_PE + 2
 };
 static_assert(8 * B_COUNT <= 512, "barrier slots");
@@ -93,9 +93,9 @@ constexpr int OFF_ALPHA = 2048;  // f32 [64]
 constexpr int OFF_M = 2304;      // f32 [64] final running maxima (log2 units)
 constexpr uint32_t kBarOr = 1, kBarWork = 2;
 
-// The maximum or sum over the warp of each of v[0 .. NH), NH a power of two up to 32: in each step a lane
+// The maximum or sum over the warp of each of v[0 .. NH), NH 8 or 16: in each step a lane
 // keeps half of its values and gives the other half away, so that it ends with the value of index
-// reduced_index<NH>(lane) in v[0] after 31 exchanges at most (one value at a time takes 5 NH).
+// reduced_index<NH>(lane) in v[0] after 9 or 16 exchanges (one value at a time takes 5 NH).
 template <int NH, bool kMax, int O = 16, int n = NH>
 __device__ __forceinline__ void warp_reduce(float (&v)[NH], int lane) {
     auto op = [](float a, float b) { return kMax ? fmaxf(a, b) : a + b; };
@@ -113,7 +113,7 @@ __device__ __forceinline__ void warp_reduce(float (&v)[NH], int lane) {
 }
 template <int NH>
 __device__ __forceinline__ int reduced_index(int lane) {
-    return NH == 32 ? lane : NH == 16 ? lane >> 1 : lane >> 2;
+    return NH == 16 ? lane >> 1 : lane >> 2;
 }
 
 // Hint: bring the 128-byte line at `ptr` into L2 (no effect on correctness).
@@ -177,14 +177,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_prefetch_desc(&rope_map);
             tma_prefetch_desc(&q_map);
             const int oob = (int)(p.num_blocks * kPage);  // one past the cache: TMA fills zeros
+            // A commit costs the issuing warp about 50 ns, so there are two a page: the slots are
+            // freed page by page, and the thread follows the pages' barriers in order. Each wait is
+            // for a phase at most one behind: a page's loads ask for the page two earlier (or a
+            // later one), and no page after it can be scored or summed before it is loaded.
             bool q_issued = false, ok = true;
             int pairs = 0, ropes = 0;  // issued
+            int scored = 0, summed = 0;  // pages whose QK, whose PV MMAs are known to have completed
+            auto follow = [&](int& done, int upto, int bars) -> bool {
+                for (; done <= upto; ++done)
+                    if (!wait_bar(bar(bars + (done & 1)), (done >> 1) & 1, abort, ds)) return false;
+                return true;
+            };
             for (int i = 0; i < npages && ok; ++i) {
                 const int blk = page_block(p, g.b, g.page0 + i);
                 const int y = blk < 0 ? oob : blk * kPage;
                 for (int b = 0; b < 4; ++b) {
-                    const int m = 4 * i + b, slot = m % Lay::kPairs, k = m / Lay::kPairs;
-                    if (k > 0 && !(ok = wait_bar(bar(B_KE + slot), (k - 1) & 1, abort, ds))) break;
+                    const int m = 4 * i + b, slot = m % Lay::kPairs;
+                    if (m >= Lay::kPairs && !(ok = follow(summed, (m - Lay::kPairs) / 4, B_PE))) break;
                     bar_arrive_expect_tx(bar(B_KF + slot), kPair);
                     tma_load_3d(sbase + Lay::kRing + slot * kPair, &pair_map, bar(B_KF + slot), 0, y, 2 * b);
                     ++pairs;
@@ -197,8 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tma_load_2d(sbase + Lay::kQ + pn * Lay::kQPanel, &q_map, bar(B_Q), pn * 64, g.r * p.H);
                     q_issued = true;
                 }
-                const int slot = i % Lay::kRopes, k = i / Lay::kRopes;
-                if (k > 0 && !(ok = wait_bar(bar(B_RE + slot), (k - 1) & 1, abort, ds))) break;
+                const int slot = i % Lay::kRopes;
+                if (i >= Lay::kRopes && !(ok = follow(scored, i - Lay::kRopes, B_SF))) break;
                 bar_arrive_expect_tx(bar(B_RF + slot), kPanel);
                 tma_load_3d(sbase + Lay::kRope + slot * kPanel, &rope_map, bar(B_RF + slot), 0, y, 8);
                 ++ropes;
@@ -214,11 +224,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     dummy = 0;
                     wait_bar(bar(B_RF + m % Lay::kRopes), (m / Lay::kRopes) & 1, &dummy, nullptr);
                 }
-            } else {  // teardown: the MMAs have consumed the last slots, no commit is on its way here
-                for (int m = max(0, pairs - Lay::kPairs); m < pairs; ++m)
-                    wait_bar(bar(B_KE + m % Lay::kPairs), (m / Lay::kPairs) & 1, abort, ds);
-                for (int m = max(0, ropes - Lay::kRopes); m < ropes; ++m)
-                    wait_bar(bar(B_RE + m % Lay::kRopes), (m / Lay::kRopes) & 1, abort, ds);
+            } else {  // teardown: the MMAs have read everything, no commit is on its way here
+                follow(scored, npages - 1, B_SF);
+                follow(summed, npages - 1, B_PE);
             }
         }
     } else if (warp == 1) {
@@ -255,10 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 4; ++j)
                         if (leader)
                             mma_ss(d, a0 + (uint64_t)(2 * j), q0 + (uint64_t)((8 * Lay::kQPanel + 32 * j) >> 4), kIdescQK, 1u);
-                    if (leader) {
-                        mma_commit(bar(B_RE + rs));
-                        mma_commit(bar(B_SF + buf));
-                    }
+                    if (leader) mma_commit(bar(B_SF + buf));
                 }
                 if (i > 0) {
                     const int j = i - 1, buf = j & 1;
@@ -274,7 +279,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (leader)
                                 mma_ss(tmem + Lay::kO + (uint32_t)(b * N), a0 + (uint64_t)((k * 2048) >> 4),
                                        b0 + (uint64_t)(2 * k), kIdescPV, k > 0 ? 1u : (j > 0 ? 1u : 0u));
-                        if (leader) mma_commit(bar(B_KE + slot));
                     }
                     if (leader) mma_commit(bar(B_PE + buf));
                 }
@@ -520,9 +524,7 @@ cudaError_t launch(const DecodeArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_decode_few_sm103(const DecodeArgs& a, cudaStream_t s) {
-    if (a.H <= 16) return launch<8>(a, s);
-    if (a.H <= 32) return launch<16>(a, s);
-    return launch<32>(a, s);
+    return a.H <= 16 ? launch<8>(a, s) : launch<16>(a, s);
 }
 
 }  // namespace mla

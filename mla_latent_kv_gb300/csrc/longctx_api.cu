@@ -80,9 +80,11 @@ struct PrefixLaunch {
 // 128 heads, 4096 + 64 tokens 56 and 56, 16384 + 64 tokens 103 and 166; 8 rows of 16 heads, 4096 + 64
 // tokens 31 and 24, 16384 + 64 tokens 34 and 49.
 bool prefix_pays(bool fp8, int rows, int H, int pages, int own_pages, int clusters, int splits, int per) {
-    const double page = fp8 ? 2.3 : 1.6;  // of one row on one of 76 SM pairs, the machine full
+    // of one row's page on one of 76 SM pairs, the machine full
+    const bool few = mla::few_heads(fp8 ? MLA_KV_FP8_E4M3_SCALED : MLA_KV_BF16, H);
+    const double page = fp8 ? 2.3 : few ? 1.15 : 1.6;
     const int pairs = 76;
-    const double alone = 12 + (rows > pairs ? 11 : 0) + page * rows * (pages + own_pages) / pairs;
+    const double alone = 12 + (rows > (few ? 2 * pairs : pairs) ? 11 : 0) + page * rows * (pages + own_pages) / pairs;
     const int64_t units = ((int64_t)rows * H + 255) / 256 * splits;
     const double waves = (double)((units + clusters - 1) / clusters);
     const double prefix = waves * (per * (fp8 ? 0.75 : 0.62) + 9) + (fp8 ? 3 : 0);

@@ -40,7 +40,8 @@ def _kernel(c, num_splits=-1):
     (3, 1, 20, 192, [1, 64, 65], False),
     (9, 3, 37, 320, [3, 5, 64, 66, 200, 4, 9, 128, 129], False),
     (2, 1, 128, 4096, [1, 100], False),
-    (150, 1, 5, 448, [1 + b % 70 for b in range(150)], True),      # 750 rows: the last tile a partial one
+    (150, 1, 5, 448, [1 + b % 70 for b in range(150)], None),      # 750 rows: the last tile a partial one
+    (160, 1, 5, 448, [1 + b % 70 for b in range(160)], True),      # 800 rows, 7 pages
     (101, 2, 7, 704, [2 + b % 130 for b in range(101)], True),     # 11 pages, ranges of an even number
     (200, 1, 1, 960, [1 + b % 64 for b in range(200)], True),      # one tile, 200 of its 256 rows
     (130, 1, 8, 1024, [1 + b % 90 for b in range(130)], True),
@@ -50,7 +51,7 @@ def _kernel(c, num_splits=-1):
 def test_shared_prefix(kv, B, Sq, H, prefix, suffix, kernel):
     c = paged_case([prefix + s for s in suffix], Sq, H, kv, seed=B * 100 + H, prefix=prefix,
                    scale_v=0.5 if kv == F8 else None)
-    assert _kernel(c) == kernel
+    assert kernel is None or _kernel(c) == kernel  # None: on one side of the border by the cache's type
     st = _status()
     o, lse = _prefix(c, status=st)
     assert int(st.item()) == 0
@@ -59,11 +60,12 @@ def test_shared_prefix(kv, B, Sq, H, prefix, suffix, kernel):
 
 @pytest.mark.parametrize("kv", [BF, F8])
 @pytest.mark.parametrize("num_splits", [1, 3, 0, -1, -2])
-@pytest.mark.parametrize("B", [4, 112])
+@pytest.mark.parametrize("B", [4, 112, 160])
 def test_shared_prefix_suffix_splits_and_bf16_output(kv, num_splits, B):
     import mla_latent_kv_gb300 as mla
     c = paged_case([640 + (1, 700, 64, 129)[b % 4] for b in range(B)], 1, 12, kv, seed=7, prefix=640)
-    assert _kernel(c, num_splits) == (B == 112)
+    if B != 112:
+        assert _kernel(c, num_splits) == (B == 160)
     o, lse = _prefix(c, num_splits, o_dtype=mla.DT_BF16)
     check_attention(o, lse, attend(c), bf16_out=True)
 
@@ -81,7 +83,7 @@ def test_shared_prefix_rows_inside_the_prefix(kv, B):
 
 @pytest.mark.parametrize("kv", [BF, F8])
 def test_shared_prefix_every_slot_empty_and_no_prefix(kv):
-    c = paged_case([0] * 120, 1, 16, kv, seed=12, prefix=704)
+    c = paged_case([0] * 160, 1, 16, kv, seed=12, prefix=704)
     for max_len in (0, 704, 704 + 64):  # a captured step's bound, whatever the slots hold
         c["max_len"] = max_len
         assert _kernel(c) == (max_len > 0)
@@ -152,10 +154,10 @@ def test_shared_prefix_repeats_bit_for_bit(kv):
 
 
 @pytest.mark.parametrize("kv", [BF, F8])
-@pytest.mark.parametrize("B", [2, 128])
+@pytest.mark.parametrize("B", [2, 160])
 def test_shared_prefix_bad_prefix_block_is_reported(kv, B):
     c = paged_case([700] * B, 1, 16, kv, seed=16, prefix=640)
-    assert _kernel(c) == (B == 128)
+    assert _kernel(c) == (B == 160)
     c["table"][0, 1] = c["num_blocks"] + 3
     st = _status()
     _prefix(c, status=st)
@@ -165,8 +167,8 @@ def test_shared_prefix_bad_prefix_block_is_reported(kv, B):
 def test_shared_prefix_workspace_is_checked():
     import torch
     import mla_latent_kv_gb300 as mla
-    c = paged_case([700 + b for b in range(128)], 1, 16, BF, seed=17, prefix=640)
-    need = mla.decode_shared_prefix_workspace_bytes(128, 1, 16, 640, c["max_len"])
+    c = paged_case([700 + b for b in range(160)], 1, 16, BF, seed=17, prefix=640)
+    need = mla.decode_shared_prefix_workspace_bytes(160, 1, 16, 640, c["max_len"])
     if need:
         with pytest.raises(mla.MlaError) as e:
             _prefix(c, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
@@ -360,7 +362,7 @@ def test_sparse_decode(kv, num_splits, Sq, H, K, lens):
 @pytest.mark.parametrize("H", [1, 8, 16, 17, 32, 33, 48, 49, 64, 65])
 @pytest.mark.parametrize("num_splits", [1, 3])
 def test_sparse_decode_head_counts_over_long_rows(H, num_splits):
-    """Up to 64 heads of a bf16 cache take a kernel of their own; rings wrap several times."""
+    """Few heads of a bf16 cache take a kernel of their own; rings wrap several times."""
     import torch
     lens = [64 * 40 + 7, 64 * 23, 1, 130]
     c = paged_case(lens, 1, H, BF, seed=84)
@@ -486,7 +488,7 @@ def test_shared_prefix_step_in_a_graph(kv):
     two captured calls that take turns on one workspace."""
     import torch
     import mla_latent_kv_gb300 as mla
-    B, H, prefix = 120, 16, 640
+    B, H, prefix = 180, 16, 640
     c = paged_case([prefix + (1, 70, 300, 64, 5, 129)[b % 6] for b in range(B)], 1, H, kv, seed=97, prefix=prefix)
     assert _kernel(c)
     rng = np.random.default_rng(98)
