@@ -380,13 +380,16 @@ def _is_shape(name, t, dtype, shape):
                          f"{tuple(t.shape)} (contiguous={t.is_contiguous()})")
 
 
-def _raw_stream(t, stream):
+def _raw_stream(stream, t, *others):
     """The stream to launch on as an integer. The calls launch on the current device, which must be
-    the tensors' own."""
+    that of every tensor."""
     import torch
     dev = t.get_device()  # -1: not a CUDA tensor
     if dev < 0 or dev != torch.cuda.current_device():
         raise ValueError(f"tensors must be on the current CUDA device, got {t.device}")
+    for x in others:
+        if x is not None and x.get_device() != dev:
+            raise ValueError(f"tensors must be on one CUDA device, got {t.device} and {x.device}")
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
@@ -429,6 +432,8 @@ def _attention_bufs(q, B, Sq, H, o_latent, o_dtype, lse, workspace, need):
         lse = _out_buf(lse, (B, Sq, H), DT_F32, q.device)
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     return o_latent, o_dtype, lse, workspace, 0 if workspace is None else workspace.nbytes
 
 
@@ -450,11 +455,11 @@ def decode_shared_prefix(q, kv_cache, block_table, seq_lens, max_seq_len, prefix
     -> (o_latent [B,Sq,H,512], lse [B,Sq,H])."""
     B, Sq, H = _page_args(q, block_table, seq_lens)
     nb = _cache_blocks(kv_cache, kv_dtype, num_blocks)
-    s = _raw_stream(q, stream)
     l = lib()
     need = 0 if workspace is not None else l.mla_decode_shared_prefix_workspace_bytes(
         kv_dtype, B, Sq, H, int(prefix_len), num_splits, int(max_seq_len))
     o_latent, o_dtype, lse, workspace, ws_bytes = _attention_bufs(q, B, Sq, H, o_latent, o_dtype, lse, workspace, need)
+    s = _raw_stream(stream, q, kv_cache, block_table, seq_lens, o_latent, lse, workspace, dev_status)
     _check(l.mla_decode_shared_prefix(q.data_ptr(), kv_cache.data_ptr(), kv_dtype, nb, block_table.data_ptr(),
                                       block_table.shape[1], seq_lens.data_ptr(), int(max_seq_len), int(prefix_len), B,
                                       Sq, H, float(scale), int(num_splits), _a(workspace), ws_bytes, o_latent.data_ptr(),
@@ -474,10 +479,10 @@ def page_keys(kv_cache, block_table, seq_lens, max_new_len, kv_dtype=KV_BF16, st
     if start_lens is not None:
         _is_shape("start_lens", start_lens, torch.int32, (B,))
     nb = _cache_blocks(kv_cache, kv_dtype, num_blocks)
-    s = _raw_stream(kv_cache, stream)
     if page_keys is None:
         page_keys = torch.zeros((nb, D), dtype=torch.bfloat16, device=kv_cache.device)
     _is_shape("page_keys", page_keys, torch.bfloat16, (nb, D))
+    s = _raw_stream(stream, kv_cache, block_table, start_lens, seq_lens, page_keys, dev_status)
     _check(lib().mla_page_keys(kv_cache.data_ptr(), kv_dtype, nb, block_table.data_ptr(), max_blocks, _a(start_lens),
                                seq_lens.data_ptr(), int(max_new_len), B, page_keys.data_ptr(), _a(dev_status), s))
     return page_keys
@@ -489,11 +494,11 @@ def page_scores(q, page_keys, block_table, seq_lens, max_seq_len, scale, scores=
     import torch
     B, Sq, H = _page_args(q, block_table, seq_lens)
     _is_shape("page_keys", page_keys, torch.bfloat16, (page_keys.shape[0], D))
-    s = _raw_stream(q, stream)
     width = -(-int(max_seq_len) // PAGE)
     if scores is None:
         scores = torch.empty((B, Sq, width), dtype=torch.float32, device=q.device)
     _is_shape("scores", scores, torch.float32, (B, Sq, width))
+    s = _raw_stream(stream, q, page_keys, block_table, seq_lens, scores, dev_status)
     _check(lib().mla_page_scores(q.data_ptr(), page_keys.data_ptr(), page_keys.shape[0], block_table.data_ptr(),
                                  block_table.shape[1], seq_lens.data_ptr(), int(max_seq_len), B, Sq, H, float(scale),
                                  scores.data_ptr(), _a(dev_status), s))
@@ -515,10 +520,10 @@ def select_pages(scores, seq_lens, max_sel, sink_pages=1, local_pages=1, pages=N
     if scores.dtype is not torch.float32:
         raise ValueError(f"scores must be fp32, got {scores.dtype}")
     _is_shape("seq_lens", seq_lens, torch.int32, (B,))
-    s = _raw_stream(scores, stream)
     if pages is None:
         pages = torch.empty((B, Sq, max_sel), dtype=torch.int32, device=scores.device)
     _is_shape("pages", pages, torch.int32, (B, Sq, max_sel))
+    s = _raw_stream(stream, scores, seq_lens, pages, dev_status)
     _check(lib().mla_select_pages(scores.data_ptr(), stride, width, seq_lens.data_ptr(), B, Sq, int(max_sel),
                                   int(sink_pages), int(local_pages), pages.data_ptr(), _a(dev_status), s))
     return pages
@@ -540,10 +545,10 @@ def decode_sparse(q, kv_cache, block_table, seq_lens, pages, scale, kv_dtype=KV_
     if pages.shape[0] != B or pages.shape[1] != Sq:
         raise ValueError(f"pages must be [{B}, {Sq}, max_sel], got {tuple(pages.shape)}")
     nb = _cache_blocks(kv_cache, kv_dtype, num_blocks)
-    s = _raw_stream(q, stream)
     l = lib()
     need = 0 if workspace is not None else l.mla_decode_sparse_workspace_bytes(kv_dtype, B, Sq, H, K, num_splits)
     o_latent, o_dtype, lse, workspace, ws_bytes = _attention_bufs(q, B, Sq, H, o_latent, o_dtype, lse, workspace, need)
+    s = _raw_stream(stream, q, kv_cache, block_table, seq_lens, pages, o_latent, lse, workspace, dev_status)
     _check(l.mla_decode_sparse(q.data_ptr(), kv_cache.data_ptr(), kv_dtype, nb, block_table.data_ptr(),
                                block_table.shape[1], seq_lens.data_ptr(), pages.data_ptr(), K, B, Sq, H, float(scale),
                                int(num_splits), _a(workspace), ws_bytes, o_latent.data_ptr(), o_dtype, lse.data_ptr(),

@@ -94,6 +94,34 @@ def test_shared_prefix_every_slot_empty_and_no_prefix(kv):
     check_attention(o, lse, attend(c))
 
 
+@pytest.mark.parametrize("kv", [BF, F8])
+@pytest.mark.parametrize("num_splits", [1, 2, -2])
+def test_shared_prefix_no_tokens_of_their_own(kv, num_splits):
+    """Nothing behind the prefix in any request: the prefix's states alone make the result."""
+    lens = [[704, 703, 64, 1, 0][b % 5] for b in range(160)]
+    c = paged_case(lens, 1, 16, kv, seed=19, prefix=704, extra_cols=3)
+    assert _kernel(c)
+    st = _status()
+    o, lse = _prefix(c, num_splits, status=st, max_len=704 + 128)
+    assert int(st.item()) == 0
+    check_attention(o, lse, attend(c))
+
+
+@pytest.mark.parametrize("B", [3, 180])
+def test_shared_prefix_length_past_the_bound_is_reported(B):
+    """As for decode, such a request's result is undefined; the others' are right."""
+    import torch
+    import mla_latent_kv_gb300 as mla
+    c = paged_case([640 + 60 + b % 40 for b in range(B)], 2, 8, BF, seed=21, prefix=640)
+    st = _status()
+    bound = c["max_len"] - 1
+    o, lse = _prefix(c, status=st, max_len=bound)
+    assert int(st.item()) == mla.DEV_SEQ_TOO_LONG
+    fits = torch.from_numpy(c["lens"] <= bound).cuda()
+    assert 0 < int(fits.sum()) < B
+    check_attention(o[fits], lse[fits], [x[fits] for x in attend(c)])
+
+
 def torch_pad(table, cols):
     """The table with -1 columns behind, `cols` in all."""
     import torch
@@ -301,6 +329,19 @@ def test_select_pages(K, sink, local, width):
             assert list(pages[b, t]) == want + [-1] * (K - len(want)), (b, t)
 
 
+def test_page_scores_length_past_the_bound_is_reported_and_cut():
+    import torch
+    import mla_latent_kv_gb300 as mla
+    c = paged_case([64 * 4, 64 * 7, 9], 1, 16, BF, seed=46)
+    keys = bf16(mi.normal_bf16(np.random.default_rng(47), (c["num_blocks"], D), std=0.125))
+    st = _status()
+    args = (c["q"], keys, c["table"], c["seq_lens"])
+    got = mla.page_scores(*args, 64 * 5, c["scale"], dev_status=st)
+    assert int(st.item()) == mla.DEV_SEQ_TOO_LONG
+    want = mla.page_scores(*args, 64 * 7, c["scale"])
+    assert torch.equal(got, want[:, :, :5]) and torch.isfinite(got[1]).all()
+
+
 def test_select_pages_widest_strided_and_too_long():
     import torch
     import mla_latent_kv_gb300 as mla
@@ -357,6 +398,19 @@ def test_sparse_decode(kv, num_splits, Sq, H, K, lens):
         o, lse = _sparse(c, pages, num_splits, st)
         assert int(st.item()) == 0
         check_attention(o, lse, attend(c, lists))
+
+
+@pytest.mark.parametrize("kv,H", [(BF, 16), (BF, 128), (F8, 16)])
+def test_sparse_decode_length_past_the_table_is_reported_and_cut(kv, H):
+    import mla_latent_kv_gb300 as mla
+    c = paged_case([64 * 6, 64 * 6, 70], 2, H, kv, seed=88)
+    pages, lists = _pick(c, 4, 89)
+    pages[0, :, :], lists[0] = np.array([0, 2, 4, 5], np.int32), [[0, 2, 4, 5]] * 2
+    c["seq_lens"][0] = c["table"].shape[1] * PAGE + 1  # read as the table's 384 tokens
+    st = _status()
+    o, lse = _sparse(c, pages, status=st)
+    assert int(st.item()) == mla.DEV_SEQ_TOO_LONG
+    check_attention(o, lse, attend(c, lists))
 
 
 @pytest.mark.parametrize("H", [1, 8, 16, 17, 32, 33, 48, 49, 64, 65])
@@ -525,3 +579,70 @@ def test_shared_prefix_step_in_a_graph(kv):
     torch.cuda.synchronize()
     check_attention(ol, lse, attend(c))
     assert not torch.equal(out, first)
+
+
+def test_tensors_elsewhere_are_refused():
+    """A tensor that the GPU cannot read is refused before anything is launched."""
+    import torch
+    import mla_latent_kv_gb300 as mla
+    c = paged_case([200, 100], 1, 16, BF, seed=120)
+    keys = torch.zeros((c["num_blocks"], D), dtype=torch.bfloat16, device="cuda")
+    pages = torch.zeros((2, 1, 1), dtype=torch.int32, device="cuda")
+    scores = torch.zeros((2, 1, 4), device="cuda")
+    host = c["seq_lens"].cpu()
+    st = torch.zeros(1, dtype=torch.int32)
+    calls = [lambda lens, **kw: mla.decode_shared_prefix(c["q"], c["cache"], c["table"], lens, 200, 0, 0.1, **kw),
+             lambda lens, **kw: mla.page_keys(c["cache"], c["table"], lens, 200, **kw),
+             lambda lens, **kw: mla.page_scores(c["q"], keys, c["table"], lens, 200, 0.1, **kw),
+             lambda lens, **kw: mla.select_pages(scores, lens, 2, **kw),
+             lambda lens, **kw: mla.decode_sparse(c["q"], c["cache"], c["table"], lens, pages, 0.1, **kw)]
+    for call in calls:
+        with pytest.raises(ValueError):
+            call(host)
+        with pytest.raises(ValueError):
+            call(c["seq_lens"], dev_status=st)
+    for call in (calls[0], calls[4]):
+        with pytest.raises(ValueError):
+            call(c["seq_lens"], workspace=torch.empty(1 << 22, dtype=torch.uint8))
+        with pytest.raises(ValueError):
+            call(c["seq_lens"], workspace=torch.empty(1 << 22, dtype=torch.uint8, device="cuda")[::2])
+    torch.cuda.synchronize()
+
+
+_FIRST_CALL = """
+import sys
+import numpy as np, torch
+sys.path.insert(0, "tests")
+import mla_inputs
+from longctx_util import attend, check_attention, paged_case
+import mla_latent_kv_gb300 as mla
+c = paged_case([640 + 1 + b for b in range(180)], 1, 16, mla_inputs.KV_BF16, seed=130, prefix=640)
+keys = torch.zeros((c["num_blocks"], 576), dtype=torch.bfloat16, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+full = torch.from_numpy(c["full_table"]).cuda()
+with torch.cuda.graph(g):
+    o, lse = mla.decode_shared_prefix(c["q"], c["cache"], c["table"], c["seq_lens"], c["max_len"], 640, c["scale"],
+                                      num_blocks=c["num_blocks"])
+    mla.page_keys(c["cache"], full, c["seq_lens"], c["max_len"], page_keys=keys, num_blocks=c["num_blocks"])
+    s = mla.page_scores(c["q"], keys, full, c["seq_lens"], c["max_len"], c["scale"])
+    pages = mla.select_pages(s, c["seq_lens"], 4)
+    o2, lse2 = mla.decode_sparse(c["q"], c["cache"], full, c["seq_lens"], pages, c["scale"], num_blocks=c["num_blocks"])
+g.replay()
+torch.cuda.synchronize()
+check_attention(o, lse, attend(c))
+picked = pages.cpu().numpy()
+check_attention(o2, lse2, attend(c, [[[p for p in row if p >= 0] for row in req] for req in picked]))
+print("same")
+"""
+
+
+def test_a_process_may_begin_with_a_capture():
+    """The first calls of a process, captured into a graph: one-time set-up must not end the capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300,
+                       env=dict(os.environ, PYTHONPATH=root))
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
