@@ -14,6 +14,7 @@
 
 #include <cstring>
 
+#include "decode_common.cuh"
 #include "internal.h"
 #include "sm103_ptx.cuh"
 
@@ -69,9 +70,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     page_scores_kernel(const __grid_constant__ CUtensorMap q_map, const PageScoresArgs p, int tiles, uint32_t idesc) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_addr(smem);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int r = (int)(blockIdx.x / tiles), tile = (int)(blockIdx.x % tiles);
     const int b = r / p.Sq, t = r % p.Sq;
+    volatile int* abort = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
+    int32_t* ds = p.dev_status;
+    auto bar = [&](int i) -> uint32_t { return sbase + 8u * (uint32_t)i; };
+    if (warp == 4 && lane == 0) {
+        tma_prefetch_desc(&q_map);
+        *abort = 0;
+        for (int i = 0; i < B_COUNT; ++i) bar_init(bar(i), i < B_QFULL ? 128u : 1u);
+        fence_barrier_init();
+    }
+    if (warp == 5) {
+        tmem_alloc(sbase + OFF_TMEM, kTmemCols);
+        tmem_relinquish();
+    }
     griddep_wait();  // q, the keys and the lengths may be earlier kernels' outputs
     griddep_launch_dependents();
     int seq = p.seq_lens[b];
@@ -83,25 +98,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int np = (n + kPage - 1) / kPage;
     const int first = tile * kTile;
     float* out = p.scores + (size_t)r * p.width;
-    if (first >= np) {  // no page in sight
+    const bool misplaced = (sbase & 1023u) != 0;  // the swizzled tiles need 1024-byte alignment; never expected
+    if (first >= np || misplaced) {                // no page in sight
         for (int i = first + tid; i < min(p.width, first + kTile); i += kThreads) out[i] = -CUDART_INF_F;
+        if (misplaced && tid == 0 && ds) atomicOr(ds, MLA_DEV_WAIT_TIMEOUT);
+        __syncthreads();
+        if (warp == 5) tmem_dealloc(*reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM), kTmemCols);
         return;
-    }
-    if (sbase & 1023u) {  // the swizzled tiles need 1024-byte alignment; never expected
-        if (tid == 0 && p.dev_status) atomicOr(p.dev_status, MLA_DEV_WAIT_TIMEOUT);
-        return;
-    }
-    volatile int* abort = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
-    int32_t* ds = p.dev_status;
-    auto bar = [&](int i) -> uint32_t { return sbase + 8u * (uint32_t)i; };
-    if (tid == 128) {
-        *abort = 0;
-        for (int i = 0; i < B_COUNT; ++i) bar_init(bar(i), i < B_QFULL ? 128u : 1u);
-        fence_barrier_init();
-    }
-    if (warp == 5) {
-        tmem_alloc(sbase + OFF_TMEM, kTmemCols);
-        tmem_relinquish();
     }
     const int live = min(kTile, np - first);
     uint32_t bad = 0;  // bit i: row i of this thread has no block
@@ -134,11 +137,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM), 0);
     const int nq = (p.H + 15) / 16 * 16;  // rows of a q panel: the heads, rounded up to the MMA's N
     if (warp == 4) {
         if (lane == 0) {
-            tma_prefetch_desc(&q_map);
             bool ok = true;
             int issued = 0;
             for (int pn = 0; pn < kPanels && ok; ++pn) {
@@ -155,26 +157,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
         }
     } else if (warp == 5) {
-        if (lane == 0) {
-            bool ok = true;
-            int done = 0;
-            for (int pn = 0; pn < kPanels && ok; ++pn) {
-                const int slot = pn % kQSlots;
-                if (!(ok = wait_bar(bar(B_QFULL + slot), (pn / kQSlots) & 1, abort, ds))) break;
-                if (!(ok = wait_bar(bar(B_AFULL + pn), 0, abort, ds))) break;
+        // the whole warp runs the loop and one elected lane issues (see the decode kernel)
+        const bool leader = elect_one();
+        bool ok = true;
+        int done = 0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_ss(tmem, smem_desc_sw128(sbase + OFF_A + pn * kPanelBytes + 32 * k, 16, 1024),
-                           smem_desc_sw128(sbase + OFF_Q + slot * kPanelBytes + 32 * k, 16, 1024), idesc,
-                           (pn | k) ? 1u : 0u);
-                mma_commit(bar(B_QEMPTY + slot));
-                ++done;
-            }
-            mma_commit(bar(B_DONE));
-            for (int m = max(0, done - kQSlots); m < done; ++m) {  // the last commits land before teardown
-                volatile int dummy = 0;
-                wait_bar(bar(B_QEMPTY + m % kQSlots), (m / kQSlots) & 1, &dummy, nullptr);
-            }
+        for (int pn = 0; pn < kPanels; ++pn) {
+            constexpr int kStep = 32 >> 4;  // of a descriptor, 16 dims on
+            const int slot = pn % kQSlots;
+            if (ok) ok = dec::warp_wait(bar(B_QFULL + slot), (pn / kQSlots) & 1, abort, ds);
+            if (ok) ok = dec::warp_wait(bar(B_AFULL + pn), 0, abort, ds);
+            if (!ok) continue;
+            const uint64_t a0 = smem_desc_sw128(sbase + OFF_A + pn * kPanelBytes, 16, 1024);
+            const uint64_t b0 = smem_desc_sw128(sbase + OFF_Q + slot * kPanelBytes, 16, 1024);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (leader) mma_ss(tmem, a0 + (uint64_t)(kStep * k), b0 + (uint64_t)(kStep * k), idesc, (pn | k) ? 1u : 0u);
+            if (leader) mma_commit(bar(B_QEMPTY + slot));
+            ++done;
+        }
+        if (leader) mma_commit(bar(B_DONE));
+        for (int m = max(0, done - kQSlots); m < done; ++m) {  // the last commits land before teardown
+            volatile int dummy = 0;
+            dec::warp_wait(bar(B_QEMPTY + m % kQSlots), (m / kQSlots) & 1, &dummy, nullptr);
         }
     } else {
         publish_panels<0>(sbase);
