@@ -13,10 +13,11 @@
 //
 // Bound: 74 KB a page from memory against about 52 MMAs of 50 cycles: at 152 units the cache stream
 // is the limit. Measured over 64 rows of 128 selected pages of 16 heads: 122 us, 5.0 TB/s of pages
-// (few rows: 12 us for one of 16 pages, latency). Half as many bytes in flight, or prefetching further
-// ahead of the ring, was slower (144 us at 6 pages instead of kAhead). 16 KB pairs of 64-dim panels go through a ring of 10 or 11 slots (two pages and more), the
-// rope panels through one of their own; one thread loads, one warp issues, and eight warps do the rest: the
-// 64 tokens are lanes 0-63 of S^T (two lane quarters), each of two warp sets taking half of the heads.
+// (one row of 16 pages: 12 us, latency). Prefetching further ahead of the ring was slower (kAhead = 6:
+// 144 us). 16 KB pairs of 64-dim panels go through a ring of 10 or 11 slots (two pages and more), the
+// rope panels through one of their own; one thread loads, one warp issues, and eight warps do the
+// rest: the 64 tokens are lanes 0-63 of S^T (two lane quarters), each of two warp sets taking half of
+// the heads.
 // A thread holds one token's scores of its heads; the row maximum over tokens is only formed when some
 // score passes its head's running maximum by 2^8 (one barrier with an OR tells), so that a page
 // usually needs no reduction across threads. Sums are kept per thread and reduced once at the end:

@@ -17,7 +17,7 @@
 //   - CTA 0 loads raw e4m3 rows by TMA. A 584-byte row stride cannot be tiled, so the cache is
 //     viewed as 1168-byte row pairs: a 208-byte box at x = 192 t reads panel triple t (dims
 //     [192 t, 192 t + 192)) of the even rows, and at x = 576 + 192 t the same dims of the odd rows
-//     shifted by 8 bytes. Four converter warps widen each triple into three 128-byte swizzled bf16
+//     shifted by 8 bytes. Eight converter warps widen each triple into three 128-byte swizzled bf16
 //     K panels (the MMA's K-major layout) and, for the last triple, copy the scales out.
 //   - CTA 1 copies whole half pages (18,688 contiguous bytes) with one bulk copy each; eight
 //     converter warps widen the first 512 dims into the MN-major V tile and zero the rows past the
@@ -25,6 +25,10 @@
 //   - Each softmax half stages its page of P (and the rescale factors) in its own shared memory
 //     and sends it with one bulk shared-to-shared copy: per-thread remote stores would queue in
 //     the same memory pipe as the converter warps' loads and stores.
+// Bound: widening. 128 rows of 8192 tokens take 540 us, 2.3 us a page and SM pair, against 0.6 us of
+// MMAs on the busier of the two SMs; with four K converter warps, and MMAs issued from a diverged
+// lane, it was 921. Two sets of converter warps that take turns (662) and another spread of the raw
+// loads over the banks were slower.
 // All waits are bounded; on a timeout the kernel winds down and reports MLA_DEV_WAIT_TIMEOUT.
 #include <cuda.h>
 #include <cuda_bf16.h>

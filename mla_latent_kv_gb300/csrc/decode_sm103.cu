@@ -8,7 +8,9 @@
 // One thread-block cluster of two CTAs per (query row, split) unit. Pages are taken four at a
 // time ("groups" of 256 tokens) so that every tensor-core instruction has N = 256: with N = 256
 // the tensor core holds enough queued work to hide the ~130-cycle gap that each blocking
-// synchronisation of the issuing thread leaves, so the pipe stays busy between ring slots.
+// synchronisation of the issuing warp leaves, so the pipe stays busy between ring slots. The whole
+// warp runs the issuing loop, converged, and one elected lane issues: issued from inside a diverged
+// branch, each MMA took at least 140 cycles whatever its size (64 rows of 4096 tokens: 109 -> 99 us).
 //
 //   CTA 0 ("scores")  Q: the 512 latent dims (128 heads x 512 bf16) are loaded once by TMA and
 //                     kept in tensor memory; the 64 rope dims stay in shared memory.

@@ -134,7 +134,8 @@ __host__ __device__ inline void split_range(int n, int S, int s, int* j0, int* j
 
 // Launch with programmatic stream serialization: the kernel may start while the preceding
 // kernel of the stream finishes, once that kernel has signalled (griddepcontrol); every kernel
-// of this library calls ptx::griddep_wait() before it touches data another of its kernels writes.
+// of this library calls ptx::griddep_wait() before it touches data another of its kernels writes. (The
+// decode kernels read cache pages before that: cache_write, which writes them, does not signal early.)
 template <typename... Params, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                        Args... args) {

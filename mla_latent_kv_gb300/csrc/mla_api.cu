@@ -97,7 +97,7 @@ int resolve_splits(bool few, int num_splits, int rows, int H, int max_seq_len) {
     const int pages = std::max(1, (max_seq_len + kPage - 1) / kPage);
     int best = 1;
     double least = 1e300;
-    for (int S = 1; S <= pages; ++S) {
+    for (int S = 1; S <= std::min(pages, 2 * sms); ++S) {  // past one wave each further one costs its 9
         const int64_t waves = ((int64_t)rows * S + sms - 1) / sms;
         const double t = (double)waves * (1.5 * ((pages + S - 1) / S) + 9) +
                          (S > 1 ? 3 + 0.1 * S + (double)rows * H * S * (kL + 1) * 8 / 5e6 : 0);
