@@ -67,6 +67,12 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     return __all_sync(0xffffffffu, ok);
 }
 
+// One arrival for the whole warp, after what its lanes did (a lane each would be serialised at the barrier).
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
+    __syncwarp();
+    if (lane == 0) ptx::bar_arrive(bar);
+}
+
 // A unit's output rows, O * inv from tensor memory, to global memory: 128 rows of 512 columns as
 // panels of 128 bytes a row (32 fp32 or 64 bf16 columns), each written to a swizzled shared tile and
 // stored by TMA as one box, so that global writes are whole lines. kSets sets of four warps (one

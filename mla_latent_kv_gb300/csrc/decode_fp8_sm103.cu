@@ -113,22 +113,22 @@ __device__ __forceinline__ uint32_t q_panel_off(int pn) {
 // lands on CTA 0's B_PEMPTY slots.
 enum : int {
     B_RAWFULL = 0,                       // [kRawSlots] CTA0: raw triple landed (TMA tx)
-    B_RAWEMPTY = B_RAWFULL + kRawSlots,  // [kRawSlots] CTA0: raw triple widened (256 converter threads)
-    B_KFULL = B_RAWEMPTY + kRawSlots,    // [kKSlots] CTA0: bf16 triple written (256 converter threads)
+    B_RAWEMPTY = B_RAWFULL + kRawSlots,  // [kRawSlots] CTA0: raw triple widened (8 converter warps)
+    B_KFULL = B_RAWEMPTY + kRawSlots,    // [kKSlots] CTA0: bf16 triple written (8 converter warps)
     B_KEMPTY = B_KFULL + kKSlots,        // [kKSlots] CTA0: bf16 triple consumed by the QK MMAs
     B_SFULL = B_KEMPTY + kKSlots,        // [2] CTA0: S buffer ready
-    B_SEMPTY = B_SFULL + 2,              // [2] CTA0: S buffer read by the softmax warps (256)
-    B_SCFULL = B_SEMPTY + 2,             // [2] CTA0: a group's scales written (256 converter threads)
-    B_SCEMPTY = B_SCFULL + 2,            // [2] CTA0: a group's scales read (256 softmax threads)
+    B_SEMPTY = B_SFULL + 2,              // [2] CTA0: S buffer read (8 softmax warps)
+    B_SCFULL = B_SEMPTY + 2,             // [2] CTA0: a group's scales written (8 converter warps)
+    B_SCEMPTY = B_SCFULL + 2,            // [2] CTA0: a group's scales read (8 softmax warps)
     B_QFULL = B_SCEMPTY + 2,             // CTA0: Q landed in shared memory (TMA tx)
-    B_QREADY,                            // CTA0: Q latent dims moved to TMEM (256)
+    B_QREADY,                            // CTA0: Q latent dims moved to TMEM (8 warps)
     B_PEMPTY,                            // [kPBufs] both CTAs: PV MMA of the page in P buffer b completed
     B_VRAWFULL = B_PEMPTY + kPBufs,      // [kVRawSlots] CTA1: raw half page landed (bulk tx)
-    B_VRAWEMPTY = B_VRAWFULL + kVRawSlots,  // [kVRawSlots] CTA1: raw half page widened (256)
-    B_VFULL = B_VRAWEMPTY + kVRawSlots,  // [kVStages] CTA1: V stage written (256 converter threads)
+    B_VRAWEMPTY = B_VRAWFULL + kVRawSlots,  // [kVRawSlots] CTA1: raw half page widened (8 warps)
+    B_VFULL = B_VRAWEMPTY + kVRawSlots,  // [kVStages] CTA1: V stage written (8 converter warps)
     B_VEMPTY = B_VFULL + kVStages,       // [kVStages] CTA1: V stage consumed
     B_PFULL = B_VEMPTY + kVStages,       // [kPBufs] CTA1: P message landed (bulk copy bytes from CTA0)
-    B_READY = B_PFULL + kPBufs,          // [kPBufs] CTA1: O rescaled for the page (128 helper threads)
+    B_READY = B_PFULL + kPBufs,          // [kPBufs] CTA1: O rescaled for the page (4 helper warps)
     B_STATS = B_READY + kPBufs,          // CTA1: final row statistics written by CTA0
     B_STAGEFREE,                         // [2] CTA0: a half's last P message has landed in CTA 1
     B_COUNT = B_STAGEFREE + 2
@@ -187,11 +187,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         *abort = 0;
         for (int i = 0; i < B_COUNT; ++i) {
             uint32_t cnt = 1;
-            if (i >= B_READY && i < B_READY + kPBufs) cnt = 128;
+            if (i >= B_READY && i < B_READY + kPBufs) cnt = 4;  // helper warps
             if ((i >= B_RAWEMPTY && i < B_RAWEMPTY + kRawSlots) || (i >= B_KFULL && i < B_KFULL + kKSlots) ||
                 (i >= B_SCFULL && i < B_SCFULL + 2) || (i >= B_SEMPTY && i < B_SEMPTY + 2) || (i >= B_SCEMPTY && i < B_SCEMPTY + 2) || i == B_QREADY ||
                 (i >= B_VRAWEMPTY && i < B_VRAWEMPTY + kVRawSlots) || (i >= B_VFULL && i < B_VFULL + kVStages))
-                cnt = 256;
+                cnt = 8;  // converter or softmax warps
             bar_init(bar(i), cnt);
         }
         if (rank == 1)  // P buffers armed for their first message before CTA 0 can send one
@@ -354,7 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                bar_arrive(bar(B_QREADY));
+                warp_arrive(bar(B_QREADY), lane);
             }
             const float sl2 = p.scale * 1.4426950408889634f;  // exp2 domain
             // Both sums are of the unscaled weights exp(s - m): v_scale only enters P as the MMA
@@ -376,7 +376,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tmem_ld32(scol + 32u, s[1]);
                     tmem_wait_ld();
                     tc_fence_before();
-                    bar_arrive(bar(B_SEMPTY + sb));
+                    warp_arrive(bar(B_SEMPTY + sb), lane);
                 } else {
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
@@ -451,7 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         l_run += sum;
                     }
                 }
-                bar_arrive(bar(B_SCEMPTY + sb));
+                warp_arrive(bar(B_SCEMPTY + sb), lane);
                 // P goes to CTA 1 as one bulk copy per page from this half's staging buffer (the
                 // copy engine moves it; per-thread remote stores would queue behind the converter
                 // warps' shared-memory traffic). The buffer is rewritten only after the previous
@@ -528,23 +528,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const uint32_t src = raw + e * (kBoxBytes + 8) + (rr >> 1) * kBoxW + 8 * c;
                         const uint32_t dst = kb + rr * 128 + ((c ^ (rr & 7)) << 4);
                         const bool two = np == kPPG;
-                        uint2 v[3][4];
-#pragma unroll
-                        for (int i = 0; i < 3; ++i)
-#pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                v[i][u] = u < 2 || two ? lds_u2(src + (u >> 1) * 2 * kBoxBytes + (u & 1) * 16 * kBoxW + 64 * i)
-                                                       : make_uint2(0u, 0u);
                         // the bf16 slot: its previous triple's MMAs have completed (the first two
                         // uses: Q's panels have been moved out to TMEM)
                         ok = m >= kKSlots ? warp_wait(bar(B_KEMPTY + ks), ((m / kKSlots) - 1) & 1, abort, ds)
                                           : warp_wait(bar(B_QREADY), 0, abort, ds);
                         if (!ok) break;
-#pragma unroll
-                        for (int i = 0; i < 3; ++i)
+#pragma unroll 1
+                        for (int i = 0; i < 3; ++i) {
+                            uint2 v[4];
 #pragma unroll
                             for (int u = 0; u < 4; ++u)
-                                if (u < 2 || two) sts_u4(dst + i * kKPanelBytes + u * 32 * 128, widen8(v[i][u]));
+                                v[u] = u < 2 || two ? lds_u2(src + (u >> 1) * 2 * kBoxBytes + (u & 1) * 16 * kBoxW + 64 * i)
+                                                       : make_uint2(0u, 0u);
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                if (u < 2 || two) sts_u4(dst + i * kKPanelBytes + u * 32 * 128, widen8(v[u]));
+                        }
                         if (t == 2) {
                             // the group's scales, for the softmax warps: (k_scale, v_scale) sit in the
                             // 8 bytes after the row's 576 codes. Rows past the last visible token get
@@ -562,11 +561,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                 reinterpret_cast<float*>(smem + OFF_KSC)[128 * sb + ctid] = sc.x;
                                 reinterpret_cast<float*>(smem + OFF_VSC)[128 * sb + ctid] = sc.y;
                             }
-                            bar_arrive(bar(B_SCFULL + sb));
+                            warp_arrive(bar(B_SCFULL + sb), lane);
                         }
                         fence_proxy_async_cta();  // generic-proxy writes before the MMAs read them
-                        bar_arrive(bar(B_KFULL + ks));
-                        bar_arrive(bar(B_RAWEMPTY + rs));
+                        warp_arrive(bar(B_KFULL + ks), lane);
+                        warp_arrive(bar(B_RAWEMPTY + rs), lane);
                     }
                 }
             }
@@ -679,7 +678,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tmem_wait_st();
                     }
                     tc_fence_before();
-                    bar_arrive(bar(B_READY + pb));
+                    warp_arrive(bar(B_READY + pb), lane);
                     pages_ready = i + 1;
                 }
             } else if (warp < 14) {
@@ -703,21 +702,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const int c = ctid & 7, pn = (ctid >> 3) & 7, r0 = ctid >> 6;  // r0 < 4
                         const uint32_t src = raw + r0 * kFp8RowBytes + 64 * pn + 8 * c;
                         const int left = copied ? valid - kVRows * hf - r0 : 0;  // rows k with 4 k < left are read
-                        uint2 v[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            v[k] = 4 * k < left ? lds_u2(src + k * 4 * kFp8RowBytes) : make_uint2(0u, 0u);
                         if (hs >= kVStages &&
                             !(ok = warp_wait(bar(B_VEMPTY + st), ((hs / kVStages) - 1) & 1, abort, ds)))
                             break;
                         // rows r0 + 4 k are r0 (k even) or r0 + 4 (k odd) within the swizzle's eight
                         const uint32_t dst0 = vb + pn * kVBox + r0 * 128 + ((c ^ r0) << 4);
                         const uint32_t dst1 = vb + pn * kVBox + (r0 + 4) * 128 + ((c ^ (r0 + 4)) << 4);
+#pragma unroll 1
+                        for (int k0 = 0; k0 < 8; k0 += 4) {
+                            uint2 v[4];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) sts_u4((k & 1 ? dst1 : dst0) + (k >> 1) * 1024, widen8(v[k]));
+                            for (int k = 0; k < 4; ++k)
+                                v[k] = 4 * (k0 + k) < left ? lds_u2(src + (k0 + k) * 4 * kFp8RowBytes) : make_uint2(0u, 0u);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) sts_u4((k & 1 ? dst1 : dst0) + ((k0 + k) >> 1) * 1024, widen8(v[k]));
+                        }
                         fence_proxy_async_cta();  // generic-proxy writes before the MMAs read them
-                        bar_arrive(bar(B_VFULL + st));
-                        bar_arrive(bar(B_VRAWEMPTY + rs));
+                        warp_arrive(bar(B_VFULL + st), lane);
+                        warp_arrive(bar(B_VRAWEMPTY + rs), lane);
                     }
                 }
             }
