@@ -25,10 +25,13 @@
 //   - Each softmax half stages its page of P (and the rescale factors) in its own shared memory
 //     and sends it with one bulk shared-to-shared copy: per-thread remote stores would queue in
 //     the same memory pipe as the converter warps' loads and stores.
-// Bound: widening. 128 rows of 8192 tokens take 540 us, 2.3 us a page and SM pair, against 0.6 us of
-// MMAs on the busier of the two SMs; with four K converter warps, and MMAs issued from a diverged
-// lane, it was 921. Two sets of converter warps that take turns (662) and another spread of the raw
-// loads over the banks were slower.
+// Bound: the converters' and the softmax's chains on one SM. 128 rows of 8192 tokens take 479 us, 1.6 us
+// a page and SM pair in steady state, against 0.6 us of MMAs on the busier of the two SMs; without the
+// widening arithmetic it would be 450. With four K converter warps, and MMAs issued from a diverged
+// lane, it was 921; the converters' code in straight lines (all of a triple's codes in registers) and an
+// arrival of every lane at their barriers cost 534. Slower than either: two sets of converter warps
+// that take turns (662), the next triple's codes loaded ahead (742, or 497 in a loop), twelve K and
+// sixteen V converter warps (491), another spread of the raw loads over the banks.
 // All waits are bounded; on a timeout the kernel winds down and reports MLA_DEV_WAIT_TIMEOUT.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -521,9 +524,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         // Panel i, rows R = rr + 32 u of the two pages: page u / 2, row pair
                         // (rr >> 1) + 16 (u % 2), parity rr & 1 (odd rows start 8 bytes in), so that
                         // every address is the thread's base plus a constant: these warps share
-                        // their schedulers with the softmax and pay for each instruction. All loads,
-                        // then the widen-and-stores: the compiler cannot move a load above an
-                        // earlier store to shared memory, so batching keeps loads in flight.
+                        // their schedulers with the softmax and pay for each instruction. A loop
+                        // over the panels, not unrolled, keeps the code small; within a panel all
+                        // loads come before the widen-and-stores, since the compiler cannot move a
+                        // load above an earlier store to shared memory.
                         const int c = ctid & 7, rr = ctid >> 3, e = rr & 1;
                         const uint32_t src = raw + e * (kBoxBytes + 8) + (rr >> 1) * kBoxW + 8 * c;
                         const uint32_t dst = kb + rr * 128 + ((c ^ (rr & 7)) << 4);
@@ -697,8 +701,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const bool copied = *reinterpret_cast<const volatile int*>(raw_ok + rs) != 0;
                         const uint32_t raw = sbase + OFF_VRAW + rs * kHalfPageBytes;
                         const uint32_t vb = sbase + OFF_V + st * kVStageBytes;
-                        // Chunk c of panel pn, rows r0 + 4 k: constant offsets, and all eight loads
-                        // first, before the wait for the stage (see the K converters)
+                        // Chunk c of panel pn, rows r0 + 4 k: constant offsets, four loads at a time
+                        // in a loop (see the K converters)
                         const int c = ctid & 7, pn = (ctid >> 3) & 7, r0 = ctid >> 6;  // r0 < 4
                         const uint32_t src = raw + r0 * kFp8RowBytes + 64 * pn + 8 * c;
                         const int left = copied ? valid - kVRows * hf - r0 : 0;  // rows k with 4 k < left are read
