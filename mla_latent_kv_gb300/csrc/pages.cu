@@ -123,8 +123,9 @@ __global__ void __launch_bounds__(kKeyThreads) page_keys_kernel(PageKeysArgs p) 
 // answer in any order. Bits that all keys share are skipped, and the search ends as soon as exactly
 // `need` keys are >= T. A thread keeps kPer consecutive keys in registers: a pass is then mostly
 // compares, where with four keys a thread its reductions and barriers took three times as long
-// (256 rows of 2048 pages: 21 us, now 9.8; 64 rows of 64 pages 3.7). Bound by the search's chain of up
-// to 32 reductions and barriers. One scan then places the pages.
+// (256 rows of 2048 pages: 21 us, now 9.8, or 7.5 in a captured graph; 64 rows of 64 pages 2.5). Bound by
+// the search's chain of up to 32 reductions and barriers; two bits a round, three counts each, gained 5 %
+// there and lost 15 % on rows of 16384 pages. One scan then places the pages.
 __device__ __forceinline__ uint32_t score_key(float x) {
     const uint32_t u = __float_as_uint(x);
     if ((u & 0x7fffffffu) > 0x7f800000u) return 0u;       // NaN
@@ -263,12 +264,14 @@ __global__ void __launch_bounds__(1024) select_pages_kernel(SelectArgs p) {
 // entries take 3.6 us, the latency of two dependent loads and a launch.
 // ------------------------------------------------------------------------------------------
 __global__ void __launch_bounds__(128) sparse_table_kernel(SparseTableArgs p) {
+    const int r = (int)blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const bool live = r < p.B * p.Sq;
+    const int b = live ? r / p.Sq : 0, t = live ? r % p.Sq : 0;
+    int seq = p.seq_lens[b];  // no kernel of the library writes it
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const int r = (int)blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (r >= p.B * p.Sq) return;
-    const int b = r / p.Sq, t = r % p.Sq;
-    int seq = p.seq_lens[b];
+    if (!live) return;
+    int next = lane < p.K ? p.pages[(size_t)r * p.K + lane] : -1;
     const int64_t cap = (int64_t)p.max_blocks * kPage;
     if (seq < 0 || seq > cap) {
         if (lane == 0 && p.dev_status) atomicOr(p.dev_status, MLA_DEV_SEQ_TOO_LONG);
@@ -278,8 +281,8 @@ __global__ void __launch_bounds__(128) sparse_table_kernel(SparseTableArgs p) {
     const int np = (n + kPage - 1) / kPage;
     int top = -1, count = 0;  // largest entry so far; entries taken
     for (int k0 = 0; k0 < p.K; k0 += 32) {
-        const int k = k0 + lane;
-        const int e = k < p.K ? p.pages[(size_t)r * p.K + k] : -1;
+        const int e = next;
+        next = lane < p.K - k0 - 32 ? p.pages[(size_t)r * p.K + k0 + 32 + lane] : -1;
         const int in = e < np ? e : -1;  // an entry outside the row's pages shadows none behind it
         int m = in;                      // inclusive running maximum
 #pragma unroll
