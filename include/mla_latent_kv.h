@@ -183,7 +183,8 @@ mla_status mla_absorb_q(const void* q_nope, int64_t q_nope_stride_t, int64_t q_n
  *   block_table int32 [B, max_blocks] contiguous; only entries j/64 for j < seq_lens[b] are read
  *   seq_lens    int32 [B]: KV tokens of request b INCLUDING its Sq new ones (already written)
  *   max_seq_len host upper bound of seq_lens (used for planning; exceeding it sets
- *               MLA_DEV_SEQ_TOO_LONG and the row's output is undefined)
+ *               MLA_DEV_SEQ_TOO_LONG and the row's output is undefined; with a bound of 0, or a
+ *               cache of 0 blocks, every row is an empty one)
  *   num_splits  split-KV request, see mla_resolve_num_splits (1 = no split, deterministic
  *               per-row reduction order independent of the batch, [vLLM-MLA, FlashMLA section])
  *   workspace   device scratch of >= mla_decode_workspace_bytes_kv(kv_dtype, B, Sq, H,

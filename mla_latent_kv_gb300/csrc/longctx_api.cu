@@ -347,6 +347,8 @@ mla_status mla_decode_shared_prefix(const void* q, const void* kv_cache, mla_kv_
     PrefixPlan w{};
     if (!plan_prefix(kv_dtype, B * Sq, H, prefix_len, num_splits, max_seq_len, &w))
         return set_error(MLA_ERR_CUDA, "%s: could not plan the call (no CUDA device?)", who);
+    if (w.splits > 0 && num_blocks == 0)
+        return set_error(MLA_ERR_INVALID_ARG, "%s: prefix_len=%d in a cache without blocks", who, prefix_len);
     if (w.total > 0 && (!workspace || workspace_bytes < w.total))
         return set_error(MLA_ERR_WORKSPACE_TOO_SMALL, "%s: workspace %zu bytes < %zu needed", who,
                          workspace ? workspace_bytes : (size_t)0, w.total);

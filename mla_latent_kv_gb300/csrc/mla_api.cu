@@ -280,7 +280,9 @@ mla_status decode_impl(const void* q, const void* kv_cache, mla_kv_dtype kv_dtyp
     a.kv_dtype = kv_dtype;
     a.num_blocks = num_blocks;
     a.block_table = block_table;
-    a.max_blocks = max_blocks;
+    // No cache to describe to TMA (no blocks, or a bound of 0, with which pointers may be null): no
+    // request sees a token then, and a positive length is reported as too long.
+    a.max_blocks = num_blocks > 0 && max_seq_len > 0 ? max_blocks : 0;
     a.seq_lens = seq_lens;
     a.max_seq_len = max_seq_len;
     a.B = B;

@@ -122,6 +122,29 @@ def test_shared_prefix_length_past_the_bound_is_reported(B):
     check_attention(o[fits], lse[fits], [x[fits] for x in attend(c)])
 
 
+@pytest.mark.parametrize("kv,H", [(BF, 16), (BF, 128), (F8, 16)])
+@pytest.mark.parametrize("bound,blocks", [(0, None), (200, 0)])
+def test_a_bound_of_zero_or_no_blocks_reads_no_cache(kv, H, bound, blocks):
+    """Lengths above a bound of 0, or in a cache of no blocks, are reported, and every row is empty."""
+    import torch
+    import mla_latent_kv_gb300 as mla
+    c = paged_case([200, 0, 64], 1, H, kv, seed=22)
+    nb = c["num_blocks"] if blocks is None else blocks
+    for num_splits in (1, 3, -2):
+        for call in ("decode", "prefix") + (("sparse",) if blocks == 0 else ()):  # that one has no bound
+            st = _status()
+            kw = dict(kv_dtype=kv, num_splits=num_splits, dev_status=st, num_blocks=nb)
+            if call == "decode":
+                o, lse = mla.decode(c["q"], c["cache"], c["table"], c["seq_lens"], bound, c["scale"], **kw)
+            elif call == "prefix":
+                o, lse = mla.decode_shared_prefix(c["q"], c["cache"], c["table"], c["seq_lens"], bound, 64, c["scale"], **kw)
+            else:
+                pages = torch.tensor([[[0, 1]], [[-1, -1]], [[0, -1]]], dtype=torch.int32, device="cuda")
+                o, lse = mla.decode_sparse(c["q"], c["cache"], c["table"], c["seq_lens"], pages, c["scale"], **kw)
+            assert int(st.item()) & mla.DEV_SEQ_TOO_LONG, (call, num_splits)
+            assert bool((o == 0).all()) and bool((lse == -math.inf).all()), (call, num_splits)
+
+
 def torch_pad(table, cols):
     """The table with -1 columns behind, `cols` in all."""
     import torch
