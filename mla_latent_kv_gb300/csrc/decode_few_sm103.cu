@@ -1,8 +1,8 @@
-// decode_few_sm103.cu -- paged MLA decode over the bf16 cache for at most 32 heads, one SM per unit.
+// decode_few_sm103.cu -- paged MLA decode for at most 32 heads, one SM per unit.
 //
-// What it computes is what the decode kernel does for a unit: one query row, tokens [j0, j1). That
-// kernel puts the heads on the tensor core's M side (128 rows, of which 16 heads use an eighth) and
-// needs two SMs for the 128 x 512 accumulator. With few heads the operands are swapped: the tokens
+// What it computes is what the decode kernels do for a unit: one query row, tokens [j0, j1). Those
+// kernels put the heads on the tensor core's M side (128 rows, of which 16 heads use an eighth) and
+// need two SMs for the 128 x 512 accumulator. With few heads the operands are swapped: the tokens
 // and the latent dims are the M side, the heads the N side (N = 16 or 32):
 //     S^T[token, head] = K Q^T     36 MMAs a page, M = 128 (the page's 64 rows; the other 64 are
 //                                  whatever follows in shared memory, and their results unused)
@@ -11,18 +11,26 @@
 // O^T takes 4 N columns of tensor memory and S^T two buffers of N, so everything fits one SM, P
 // never leaves it, and 152 units run at once.
 //
-// Bound: 74 KB a page from memory against about 52 MMAs of 50 cycles: at 152 units the cache stream
-// is the limit. Measured over 64 rows of 128 selected pages of 16 heads: 122 us, 5.0 TB/s of pages
-// (one row of 16 pages: 12 us, latency). Prefetching further ahead of the ring was slower (kAhead = 6:
-// 144 us). 16 KB pairs of 64-dim panels go through a ring of 10 or 11 slots (two pages and more), the
-// rope panels through one of their own; one thread loads, one warp issues, and eight warps do the
-// rest: the 64 tokens are lanes 0-63 of S^T (two lane quarters), each of two warp sets taking half of
-// the heads.
+// Bound, bf16 cache: 74 KB a page from memory against about 52 MMAs of 50 cycles: at 152 units the cache
+// stream is the limit. Measured over 64 rows of 128 selected pages of 16 heads: 122 us, 5.0 TB/s of pages
+// (one row of 16 pages: 12 us, latency; the decode kernel takes 160 and 20). Prefetching further ahead
+// of the ring was slower (6 pages instead of 3: 144 us). 16 KB pairs of 64-dim panels go through a
+// ring of 10 or 11 slots (two pages and more), the rope panels through one of their own; one thread
+// loads, one warp issues, and eight warps do the rest: the 64 tokens are lanes 0-63 of S^T (two lane
+// quarters), each of two warp sets taking half of the heads.
 // A thread holds one token's scores of its heads; the row maximum over tokens is only formed when some
 // score passes its head's running maximum by 2^8 (one barrier with an OR tells), so that a page
 // usually needs no reduction across threads. Sums are kept per thread and reduced once at the end:
 // l of the bf16-rounded weights normalises O (as the MMA sees them), lt of the unrounded ones gives
 // the LSE.
+//
+// FP8 cache: eight more warps load a page's codes straight into registers, one page ahead, and widen
+// them into the same ring (a page is widened once for both products, where the decode kernel's two SMs
+// widen it once each). A token's k_scale multiplies the scores of the thread that holds it, its
+// v_scale the weight before its one rounding; both sums are of the unscaled weights. Bound: the widening
+// warps and the 1.4 us of MMAs a page: 64 rows of 128 pages of 16 heads 135 us, of 32 heads 150 (the decode
+// kernel: 230), one row of 16 pages 12.6 (19.5). Waiting for a page's slots pair by pair in a loop cost
+// 149 and 175 us, a ring of two pages 147 and 163, without the L2 prefetch 173.
 //
 // All waits are bounded (see sm103_ptx.cuh).
 #include <cuda.h>
@@ -44,15 +52,18 @@ namespace {
 using namespace ptx;
 using namespace dec;
 
-constexpr int kThreads = 384;           // warp 0 TMA, 1 MMA, 2-3 L2 prefetch, 4-11 softmax and epilogue
+// warp 0 TMA, 1 MMA, 2-3 L2 prefetch, 4-11 softmax and epilogue, FP8: 12-19 converters
+constexpr int threads_of(bool fp8) { return fp8 ? 640 : 384; }
 constexpr int kWork = 256;
+constexpr int kConvWarps = 8;
 constexpr int kPanel = kPage * 128;     // one page's rows of one 64-dim panel (8 KB)
 constexpr int kPair = 2 * kPanel;
 constexpr int kCtrl = 4096;
 constexpr int kSmemLimit = 232448;
 constexpr int kMaxPairs = 11, kMaxRopes = 2;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr int kAhead = 3;               // pages between the softmax's progress and the page prefetched into L2
+// pages between the softmax's progress and the page prefetched into L2
+constexpr int ahead_of(bool fp8) { return fp8 ? 2 : 3; }
 
 // Shared memory for N = 2 NH heads: the rings first, since an MMA of M = 128 reads 8 KB past a panel.
 template <int NH>
@@ -117,11 +128,19 @@ __device__ __forceinline__ int reduced_index(int lane) {
     return NH == 16 ? lane >> 1 : lane >> 2;
 }
 
+// Eight e4m3 codes -> eight bf16 (exact), as one 16-byte chunk of a bf16 row.
+__device__ __forceinline__ uint4 widen8(uint2 v) {
+    uint4 o;
+    e4m3x4_to_bf16x4(v.x, o.x, o.y);
+    e4m3x4_to_bf16x4(v.y, o.z, o.w);
+    return o;
+}
+
 // Hint: bring the 128-byte line at `ptr` into L2 (no effect on correctness).
 __device__ __forceinline__ void prefetch_l2(const void* ptr) { asm volatile("prefetch.global.L2 [%0];" ::"l"(ptr)); }
 
-template <int NH>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int NH, bool kFp8>
+__global__ void __launch_bounds__(threads_of(kFp8), 1)
     decode_few_kernel(const __grid_constant__ CUtensorMap pair_map, const __grid_constant__ CUtensorMap rope_map,
                       const __grid_constant__ CUtensorMap q_map, const DecodeArgs p) {
     using Lay = Layout<NH>;
@@ -149,6 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t cnt = 1;
             if (i >= B_SE && i < B_SE + 2) cnt = 4;
             if (i >= B_PF && i < B_PF + 2) cnt = kWork;
+            if (kFp8 && i < B_Q) cnt = kConvWarps;  // panels widened by the converter warps
             bar_init(bar(i), cnt);
         }
         fence_barrier_init();
@@ -172,7 +192,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int npages = g.npages;
 
-    if (warp == 0) {
+    if (kFp8 && warp == 0) {
+        if (lane == 0 && npages > 0) {
+            tma_prefetch_desc(&q_map);
+            if (p.order != kOrderFree) griddep_wait();
+            bar_arrive_expect_tx(bar(B_Q), 9 * Lay::kQPanel);
+            for (int pn = 0; pn < 9; ++pn)
+                tma_load_2d(sbase + Lay::kQ + pn * Lay::kQPanel, &q_map, bar(B_Q), pn * 64, g.r * p.H);
+            volatile int dummy = 0;  // it has landed before the CTA can exit, also after an abort
+            wait_bar(bar(B_Q), 0, &dummy, nullptr);
+        }
+    } else if (warp == 0) {
         if (lane == 0 && npages > 0) {
             tma_prefetch_desc(&pair_map);
             tma_prefetch_desc(&rope_map);
@@ -248,6 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int b = 0; b < 4; ++b) {
                         const int m = 4 * i + b, slot = m % Lay::kPairs;
                         if (!(ok = warp_wait(bar(B_KF + slot), (m / Lay::kPairs) & 1, abort, ds))) break;
+                        if (kFp8) tc_fence_after();  // written by the converter warps
                         const uint64_t a0 = smem_desc_sw128(sbase + Lay::kRing + slot * kPair, 16, 1024);
 #pragma unroll
                         for (int j = 0; j < 8; ++j)  // two panels of four steps
@@ -259,6 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     const int rs = i % Lay::kRopes;
                     if (!(ok = warp_wait(bar(B_RF + rs), (i / Lay::kRopes) & 1, abort, ds))) break;
+                    if (kFp8) tc_fence_after();
                     const uint64_t a0 = smem_desc_sw128(sbase + Lay::kRope + rs * kPanel, 16, 1024);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -285,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && warp < 12) {
         const int quarter = warp & 3, set = (warp - 4) >> 2;
         const int h0 = set * NH;               // this set's heads [h0, h0 + NH)
         const bool tokens = quarter < 2;       // holds tokens 32 quarter + lane
@@ -303,10 +335,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             m[k] = -CUDART_INF_F;
             l[k] = lt[k] = 0.f;
         }
+        // FP8: (k_scale, v_scale) of this thread's token, a page ahead; 0 where there is no token
+        float2 scale = make_float2(0.f, 0.f), scale_next = scale;
+        int blk_next = -1;  // the block two pages ahead
+        auto block_of = [&](int i) -> int {
+            if (i >= npages) return -1;
+            const int32_t blk = *table_entry(p, g.b, g.page0 + i);
+            return (int64_t)blk < p.num_blocks ? blk : -1;
+        };
+        auto scale_of = [&](int i, int blk) -> float2 {
+            if (blk < 0 || token >= valid_rows(g, i)) return make_float2(0.f, 0.f);
+            return __ldcg(reinterpret_cast<const float2*>(p.cache + ((size_t)blk * kPage + token) * kFp8RowBytes + kD));
+        };
+        if (kFp8 && tokens) {
+            scale_next = scale_of(0, block_of(0));
+            blk_next = block_of(1);
+        }
         for (int i = 0; i < npages; ++i) {
             // No early exit: all 256 threads must pass the same named barriers (which cannot time
             // out); after an abort the waits return at once and the work is skipped.
             const int buf = i & 1, valid = valid_rows(g, i);
+            if (kFp8 && tokens) {
+                scale = scale_next;
+                scale_next = scale_of(i + 1, blk_next);
+                blk_next = block_of(i + 2);
+            }
             const bool okS = warp_wait(bar(B_SF + buf), (i >> 1) & 1, abort, ds);
             uint32_t s[NH];
             bool need = false;
@@ -322,6 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 #pragma unroll
                 for (int k = 0; k < NH; ++k) {  // tokens past the last and heads past H have no weight
+                    if (kFp8) s[k] = __float_as_uint(__uint_as_float(s[k]) * scale.x);  // K = codes * k_scale
                     if (!okS || token >= valid || h0 + k >= p.H) s[k] = __float_as_uint(-CUDART_INF_F);
                     need |= __uint_as_float(s[k]) * sl2 > m[k] + kRescaleThreshold;
                 }
@@ -380,14 +434,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int h = h0 + k;
                     // a head past H keeps m = -inf: its weights are 0, not exp2(-inf + inf)
                     const float e = m[k] == -CUDART_INF_F ? 0.f : fast_exp2(fmaf(__uint_as_float(s[k]), sl2, -m[k]));
-                    const uint32_t r = pack_bf16x2(e, 0.f) & 0xffffu;
+                    // V = codes * v_scale: the scale multiplies the weight before its one rounding, and
+                    // both sums are of the unscaled weights
+                    const uint32_t r = pack_bf16x2(kFp8 ? e * scale.y : e, 0.f) & 0xffffu;
                     lt[k] += e;
-                    l[k] += bf16_lo_f(r);
+                    if (!kFp8) l[k] += bf16_lo_f(r);
                     *reinterpret_cast<uint16_t*>(pb + h * 128 + (((token >> 3) ^ (h & 7)) << 4) + (token & 7) * 2) =
                         (uint16_t)r;
                 }
             }
-            if (valid < kPage) {  // V rows past the last token may hold anything, also NaN: 0 * NaN
+            if (!kFp8 && valid < kPage) {  // V rows past the last token may hold anything, also NaN: 0 * NaN
                 for (int q = wtid; q < (kPage - valid) * 64; q += kWork) {
                     const int row = valid + q / 64, pn = (q >> 3) & 7, c = q & 7;
                     const int slot = (4 * i + (pn >> 1)) % Lay::kPairs;
@@ -407,9 +463,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < NH; ++k) m_s[h0 + k] = m[k];
             }
-            warp_reduce<NH, false>(l, lane);
+            if (!kFp8) warp_reduce<NH, false>(l, lane);
             warp_reduce<NH, false>(lt, lane);
-            mx[64 * quarter + h0 + reduced_index<NH>(lane)] = l[0];
+            mx[64 * quarter + h0 + reduced_index<NH>(lane)] = kFp8 ? lt[0] : l[0];
             lts[64 * quarter + h0 + reduced_index<NH>(lane)] = lt[0];
         }
         output_wait(p, unit);
@@ -459,6 +515,75 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
+    } else if (kFp8 && warp >= 12) {
+        // ---------------- converter warps 12-19 (256 threads), FP8 ----------------
+        // They load a page's codes from global memory into registers while they widen the page before
+        // it, 8 codes a load: of pair b, row r0 + 16 k, chunk cc of its 16; of the rope panel, row
+        // q0 + 32 k, chunk qc of 8. Rows past the last token and pages without a block are zero, so
+        // that stale or NaN codes cannot leak through 0 * NaN.
+        const int ctid = tid - 384;
+        const int r0 = ctid >> 4, cc = ctid & 15, q0 = ctid >> 3, qc = ctid & 7;
+        const uint32_t pair_dst = sbase + Lay::kRing + (cc >> 3) * kPanel + r0 * 128 + (((cc & 7) ^ (r0 & 7)) << 4);
+        const uint32_t rope_dst = sbase + Lay::kRope + q0 * 128 + ((qc ^ (q0 & 7)) << 4);
+        uint2 v[4][4], w[2];
+        const uint8_t* src = nullptr;  // of the page being loaded
+        int rows = 0;                  // its rows that hold tokens
+        auto open = [&](int i) {
+            rows = 0;
+            if (i >= npages) return;
+            const int blk = page_block(p, g.b, g.page0 + i);
+            if (blk < 0) return;
+            rows = valid_rows(g, i);
+            src = p.cache + (size_t)blk * (kPage * kFp8RowBytes);
+        };
+        auto load_pair = [&](int b) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int row = r0 + 16 * k;
+                v[b][k] = make_uint2(0u, 0u);
+                if (row < rows) v[b][k] = __ldcg(reinterpret_cast<const uint2*>(src + row * kFp8RowBytes + 128 * b + 8 * cc));
+            }
+        };
+        auto load_rope = [&]() {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int row = q0 + 32 * k;
+                w[k] = make_uint2(0u, 0u);
+                if (row < rows) w[k] = __ldcg(reinterpret_cast<const uint2*>(src + row * kFp8RowBytes + kL + 8 * qc));
+            }
+        };
+        if (npages > 0) {
+            open(0);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) load_pair(b);
+            load_rope();
+        }
+        // A page's first kWaitAt pairs go where pairs of the page three earlier were, which completed
+        // before the page ahead of this one was written; the others wait for the page two earlier.
+        constexpr int kWaitAt = Lay::kPairs - 8;
+        static_assert(kWaitAt >= 0 && kWaitAt < 4 && Lay::kRopes == 2, "ring");
+        bool ok = true;
+        for (int i = 0; i < npages && ok; ++i) {
+            open(i + 1);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                if (b == kWaitAt && i >= 2) ok = warp_wait(bar(B_PE + (i & 1)), ((i - 2) >> 1) & 1, abort, ds);
+                if (!ok) break;
+                const int slot = (4 * i + b) % Lay::kPairs;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sts_u4(pair_dst + slot * kPair + k * 16 * 128, widen8(v[b][k]));
+                fence_proxy_async_cta();  // generic-proxy writes before the MMAs read them
+                warp_arrive(bar(B_KF + slot), lane);
+                load_pair(b);
+            }
+            if (!ok) break;
+            const int rs = i % Lay::kRopes;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) sts_u4(rope_dst + rs * kPanel + k * 32 * 128, widen8(w[k]));
+            fence_proxy_async_cta();
+            warp_arrive(bar(B_RF + rs), lane);
+            load_rope();
+        }
     } else {
         // Warps 2, 3: pages that the ring has no room for yet are brought into L2, kAhead pages
         // past the last one whose softmax is done. Only a hint: gives up quietly if it falls behind.
@@ -466,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int spins = 0;
         for (int t = 2; t < npages; ++t) {
             bool go = true;
-            while (*prog < t - kAhead) {
+            while (*prog < t - ahead_of(kFp8)) {
                 if (*abort || ++spins > (1 << 20)) {
                     go = false;
                     break;
@@ -476,8 +601,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!go) break;
             const int32_t blk = *table_entry(p, g.b, g.page0 + t);
             if (blk < 0 || (int64_t)blk >= p.num_blocks) continue;
-            const uint8_t* page = p.cache + (size_t)blk * (kPage * kBf16RowBytes);
-            for (int q = tid - 64; q < kPage * kBf16RowBytes / 128; q += 64) prefetch_l2(page + 128 * q);
+            constexpr int kPageBytes = kPage * (kFp8 ? kFp8RowBytes : kBf16RowBytes);
+            const uint8_t* page = p.cache + (size_t)blk * kPageBytes;
+            for (int q = tid - 64; q < kPageBytes / 128; q += 64) prefetch_l2(page + 128 * q);
         }
     }
 
@@ -486,14 +612,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc(tmem, Lay::kCols);
 }
 
-template <int NH>
+template <int NH, bool kFp8>
 cudaError_t launch(const DecodeArgs& a, cudaStream_t s) {
     static int done[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !done[dev]) {
-        e = cudaFuncSetAttribute(decode_few_kernel<NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<NH>::kBytes);
+        e = cudaFuncSetAttribute(decode_few_kernel<NH, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<NH>::kBytes);
         if (e != cudaSuccess) return e;
         if (dev < 64) done[dev] = 1;
     }
@@ -502,15 +628,16 @@ cudaError_t launch(const DecodeArgs& a, cudaStream_t s) {
     memset(&rope_map, 0, sizeof rope_map);
     memset(&q_map, 0, sizeof q_map);
     if (a.num_blocks > 0 && a.max_seq_len > 0) {
-        // the cache's rows as [panel of 64 dims][row][64]
-        const uint64_t dims[3] = {64, (uint64_t)a.num_blocks * kPage, (uint64_t)(kD / 64)};
-        const uint64_t strides[2] = {(uint64_t)kBf16RowBytes, 128};
-        uint32_t box[3] = {64, (uint32_t)kPage, 2};
-        e = encode_tmap(&pair_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.cache, dims, strides, box, true);
-        if (e != cudaSuccess) return e;
-        box[2] = 1;
-        e = encode_tmap(&rope_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.cache, dims, strides, box, true);
-        if (e != cudaSuccess) return e;
+        if constexpr (!kFp8) {  // the cache's rows as [panel of 64 dims][row][64]
+            const uint64_t dims[3] = {64, (uint64_t)a.num_blocks * kPage, (uint64_t)(kD / 64)};
+            const uint64_t strides[2] = {(uint64_t)kBf16RowBytes, 128};
+            uint32_t box[3] = {64, (uint32_t)kPage, 2};
+            e = encode_tmap(&pair_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.cache, dims, strides, box, true);
+            if (e != cudaSuccess) return e;
+            box[2] = 1;
+            e = encode_tmap(&rope_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.cache, dims, strides, box, true);
+            if (e != cudaSuccess) return e;
+        }
         const uint64_t qdims[2] = {(uint64_t)kD, (uint64_t)a.rows * a.H};
         const uint64_t qstrides[1] = {(uint64_t)kD * 2};
         const uint32_t qbox[2] = {64, 2 * NH};
@@ -518,14 +645,15 @@ cudaError_t launch(const DecodeArgs& a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
     }
     const int64_t units = a.plan_units ? a.plan_max_units : (int64_t)a.rows * a.num_splits;
-    return launch_pdl(decode_few_kernel<NH>, dim3((unsigned)units), dim3(kThreads), Layout<NH>::kBytes, s, pair_map,
+    return launch_pdl(decode_few_kernel<NH, kFp8>, dim3((unsigned)units), dim3(threads_of(kFp8)), Layout<NH>::kBytes, s, pair_map,
                       rope_map, q_map, a);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_few_sm103(const DecodeArgs& a, cudaStream_t s) {
-    return a.H <= 16 ? launch<8>(a, s) : launch<16>(a, s);
+    if (a.kv_dtype == MLA_KV_FP8_E4M3_SCALED) return a.H <= 16 ? launch<8, true>(a, s) : launch<16, true>(a, s);
+    return a.H <= 16 ? launch<8, false>(a, s) : launch<16, false>(a, s);
 }
 
 }  // namespace mla

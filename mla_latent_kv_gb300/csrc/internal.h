@@ -228,8 +228,9 @@ mla_status decode_impl(const void* q, const void* kv_cache, mla_kv_dtype kv_dtyp
 // Whether a decode takes the kernel for few heads, and the split count of its units (as
 // mla_resolve_num_splits, which counts pairs of SMs). At 32 heads it took 25 against 33 us (32 rows of
 // 32 pages), 71 against 121 (128 rows of 32), 134 against 160 (64 rows of 128); with room for 64 heads
-// 37 against 36, 92 against 121 and 176 against 160: the ring then holds two pages only.
-inline bool few_heads(int kv_dtype, int H) { return kv_dtype == MLA_KV_BF16 && H <= 32; }
+// 37 against 36, 92 against 121 and 176 against 160: the ring then holds two pages only. FP8 cache, 32
+// heads: 27 against 44, 77 against 149, 150 against 230.
+inline bool few_heads(int H) { return H <= 32; }
 int resolve_splits(bool few, int num_splits, int rows, int H, int max_seq_len);
 
 // Clear the detail string and return MLA_OK.
@@ -266,7 +267,7 @@ mla_status set_error(mla_status st, const char* fmt, ...);
 
 cudaError_t launch_decode_sm103(const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_decode_fp8_sm103(const DecodeArgs& a, cudaStream_t s);
-cudaError_t launch_decode_few_sm103(const DecodeArgs& a, cudaStream_t s);  // bf16 cache, H <= 32
+cudaError_t launch_decode_few_sm103(const DecodeArgs& a, cudaStream_t s);  // H <= 32
 cudaError_t launch_merge(const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_plan(const DecodeArgs& a, int pairs, cudaStream_t s);
 cudaError_t launch_cache_write(const uint16_t* kv_c, int64_t st_c, const uint16_t* k_pe, int64_t st_pe,

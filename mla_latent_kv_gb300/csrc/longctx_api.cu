@@ -75,14 +75,15 @@ struct PrefixLaunch {
 };
 // Whether the prefix kernel is worth its launch, its partial states and their merge: estimated times in
 // us of the call with it and of the decode kernels alone, fitted to graph replays of both at 1..128
-// requests, 16..128 heads, 64..16384 prefix tokens and 64 or 512 own ones. Measured at the border, with
-// and without: 128 rows of 16 heads, 256 + 64 tokens 47 and 43, 1024 + 64 tokens 51 and 69; 32 rows of
+// requests, 8..128 heads, 64..16384 prefix tokens and 64 or 512 own ones. Measured at the border, with
+// and without: 128 rows of 16 heads, 256 + 64 tokens 21 and 12, 1024 + 64 tokens 29 and 31; 32 rows of
 // 128 heads, 4096 + 64 tokens 56 and 56, 16384 + 64 tokens 103 and 166; 8 rows of 16 heads, 4096 + 64
-// tokens 31 and 24, 16384 + 64 tokens 34 and 49.
+// tokens 26 and 15, 16384 + 64 tokens 30 and 31. FP8 cache: 128 rows of 16 heads, 1024 + 64 tokens 32 and
+// 37, 4096 + 64 tokens 41 and 128; 32 rows of 128 heads, 1024 + 64 tokens 44 and 36, 4096 + 64 60 and 77.
 bool prefix_pays(bool fp8, int rows, int H, int pages, int own_pages, int clusters, int splits, int per) {
     // of one row's page on one of 76 SM pairs, the machine full
-    const bool few = mla::few_heads(fp8 ? MLA_KV_FP8_E4M3_SCALED : MLA_KV_BF16, H);
-    const double page = fp8 ? 2.3 : few ? 1.15 : 1.6;
+    const bool few = mla::few_heads(H);
+    const double page = fp8 ? (!few ? 2.1 : H > 16 ? 1.2 : 1.0) : few ? 1.15 : 1.6;
     const int pairs = 76;
     const double alone = 12 + (rows > (few ? 2 * pairs : pairs) ? 11 : 0) + page * rows * (pages + own_pages) / pairs;
     const int64_t units = ((int64_t)rows * H + 255) / 256 * splits;
@@ -126,7 +127,7 @@ bool plan_prefix(mla_kv_dtype kv, int rows, int H, int prefix_len, int num_split
     // ahead of everything else. Behind a prefix the requests' own tokens are usually few: up to 32
     // pages each row is one unit instead (2048 rows of 16 heads, up to 1000 own tokens: 150 -> 140 us).
     if (num_splits == -1 && w->splits > 0 && own_len <= 32 * mla::kPage && rows > 76) num_splits = 1;
-    w->own_splits = mla::resolve_splits(mla::few_heads(kv, H), num_splits, rows, H, own_len);
+    w->own_splits = mla::resolve_splits(mla::few_heads(H), num_splits, rows, H, own_len);
     if (w->own_splits < 1 && w->own_splits != -2) return false;
     w->total = w->decode + mla::workspace_layout(kv, rows, rows, H, w->own_splits, own_len, w->splits > 0).total;
     return true;
@@ -245,7 +246,7 @@ size_t mla_decode_sparse_workspace_bytes(mla_kv_dtype kv_dtype, int B, int Sq, i
         max_sel > INT32_MAX / mla::kPage || (int64_t)B * Sq > INT32_MAX / MLA_MAX_HEADS)
         return 0;
     const int rows = B * Sq;
-    const int S = mla::resolve_splits(mla::few_heads(kv_dtype, H), num_splits, rows, H, max_sel * mla::kPage);
+    const int S = mla::resolve_splits(mla::few_heads(H), num_splits, rows, H, max_sel * mla::kPage);
     if (S < 1 && S != -2) return 0;
     return sparse_layout(kv_dtype, rows, H, max_sel, S).total;
 }
@@ -276,7 +277,7 @@ mla_status mla_decode_sparse(const void* q, const void* kv_cache, mla_kv_dtype k
     if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(o_latent))
         return set_error(MLA_ERR_UNSUPPORTED, "%s: q, kv_cache and o_latent must be 16-byte aligned", who);
     const int rows = B * Sq;
-    const int S = mla::resolve_splits(mla::few_heads(kv_dtype, H), num_splits, rows, H, max_sel * mla::kPage);
+    const int S = mla::resolve_splits(mla::few_heads(H), num_splits, rows, H, max_sel * mla::kPage);
     if (S < 1 && S != -2) return set_error(MLA_ERR_CUDA, "%s: could not resolve num_splits (no CUDA device?)", who);
     const SparseLayout w = sparse_layout(kv_dtype, rows, H, max_sel, S);
     if (!workspace || workspace_bytes < w.total)
@@ -299,7 +300,7 @@ mla_status mla_decode_sparse(const void* q, const void* kv_cache, mla_kv_dtype k
     if (e != cudaSuccess) return cuda_error(e, who);
     mla::DecodeExtra x;
     x.who = who;
-    x.few = mla::few_heads(kv_dtype, H);
+    x.few = mla::few_heads(H);
     x.order = mla::kOrderWaitFirst;
     return mla::decode_impl(q, kv_cache, kv_dtype, num_blocks, t.table, max_sel, t.lens, nullptr, max_sel * mla::kPage,
                             rows, 1, rows, H, scale, S, (char*)workspace + w.decode, w.total - w.decode, o_latent,
@@ -330,7 +331,7 @@ mla_status mla_decode_shared_prefix(const void* q, const void* kv_cache, mla_kv_
                          (long long)max_blocks * mla::kPage);
     mla::DecodeExtra x;
     x.who = who;
-    x.few = mla::few_heads(kv_dtype, H);
+    x.few = mla::few_heads(H);
     x.shared_pages = prefix_len / mla::kPage;
     auto decode = [&](int splits, void* ws, size_t bytes) {
         return mla::decode_impl(q, kv_cache, kv_dtype, num_blocks, block_table, max_blocks, seq_lens, nullptr,

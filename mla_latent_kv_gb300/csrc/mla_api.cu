@@ -327,9 +327,9 @@ mla_status decode_impl(const void* q, const void* kv_cache, mla_kv_dtype kv_dtyp
         e = x.between(x.between_arg);
         if (e != cudaSuccess) return cuda_fail(e, x.who, "launch");
     }
-    e = fp8     ? mla::launch_decode_fp8_sm103(a, st)
-        : x.few ? mla::launch_decode_few_sm103(a, st)
-                : mla::launch_decode_sm103(a, st);
+    e = x.few ? mla::launch_decode_few_sm103(a, st)
+        : fp8 ? mla::launch_decode_fp8_sm103(a, st)
+              : mla::launch_decode_sm103(a, st);
     if (e != cudaSuccess) return cuda_fail(e, x.who, "decode launch");
     if (planned || S > 1 || x.all_partial) {
         e = mla::launch_merge(a, st);

@@ -122,7 +122,7 @@ def test_shared_prefix_length_past_the_bound_is_reported(B):
     check_attention(o[fits], lse[fits], [x[fits] for x in attend(c)])
 
 
-@pytest.mark.parametrize("kv,H", [(BF, 16), (BF, 128), (F8, 16)])
+@pytest.mark.parametrize("kv,H", [(BF, 16), (BF, 128), (F8, 16), (F8, 48)])
 @pytest.mark.parametrize("bound,blocks", [(0, None), (200, 0)])
 def test_a_bound_of_zero_or_no_blocks_reads_no_cache(kv, H, bound, blocks):
     """Lengths above a bound of 0, or in a cache of no blocks, are reported, and every row is empty."""
@@ -423,7 +423,7 @@ def test_sparse_decode(kv, num_splits, Sq, H, K, lens):
         check_attention(o, lse, attend(c, lists))
 
 
-@pytest.mark.parametrize("kv,H", [(BF, 16), (BF, 128), (F8, 16)])
+@pytest.mark.parametrize("kv,H", [(BF, 16), (BF, 128), (F8, 16), (F8, 48)])
 def test_sparse_decode_length_past_the_table_is_reported_and_cut(kv, H):
     import mla_latent_kv_gb300 as mla
     c = paged_case([64 * 6, 64 * 6, 70], 2, H, kv, seed=88)
@@ -438,12 +438,16 @@ def test_sparse_decode_length_past_the_table_is_reported_and_cut(kv, H):
 
 @pytest.mark.parametrize("H", [1, 8, 16, 17, 32, 33, 48, 49, 64, 65])
 @pytest.mark.parametrize("num_splits", [1, 3])
-def test_sparse_decode_head_counts_over_long_rows(H, num_splits):
-    """Few heads of a bf16 cache take a kernel of their own; rings wrap several times."""
+@pytest.mark.parametrize("kv", [BF, F8])
+def test_sparse_decode_head_counts_over_long_rows(kv, H, num_splits):
+    """Few heads take a kernel of their own; rings wrap several times."""
     import torch
     lens = [64 * 40 + 7, 64 * 23, 1, 130]
-    c = paged_case(lens, 1, H, BF, seed=84)
-    rows = c["cache"].view(torch.bfloat16).view(c["num_blocks"], PAGE, D)
+    c = paged_case(lens, 1, H, kv, seed=84, scale_v=0.5 if kv == F8 else None)
+    if kv == BF:
+        rows = c["cache"].view(torch.bfloat16).view(c["num_blocks"], PAGE, D)
+    else:  # the two scales of each row, views into the cache
+        rows = c["cache"].view(c["num_blocks"], PAGE, D + 8).view(torch.float32)[..., D // 4:]
     for i, blk in enumerate(c["full_table"][0, :41]):  # a running maximum that moves late, too
         if i in (9, 30):
             rows[int(blk)] *= 6.0
