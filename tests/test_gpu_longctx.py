@@ -608,6 +608,39 @@ def test_shared_prefix_step_in_a_graph(kv):
     assert not torch.equal(out, first)
 
 
+@pytest.mark.parametrize("H", [16, 128])
+def test_two_streams_at_once(H):
+    """Calls of two streams, each with its own workspace, do not disturb one another."""
+    import torch
+    import mla_latent_kv_gb300 as mla
+    B, prefix = 64, 4096
+    cases = [paged_case([prefix + 1 + (37 * b + s) % 400 for b in range(B)], 1, H, kv, seed=140 + s, prefix=prefix)
+             for s, kv in enumerate((BF, F8))]
+    streams = [torch.cuda.Stream() for _ in cases]
+    full = [dev(c["full_table"]) for c in cases]
+    pages = [torch.sort(torch.stack([torch.randperm(64)[:24] for _ in range(B)]), 1)[0].int().view(B, 1, 24).cuda()
+             for _ in cases]
+
+    def both(i):
+        c = cases[i]
+        o, lse = _prefix(c)
+        o2, lse2 = mla.decode_sparse(c["q"], c["cache"], full[i], c["seq_lens"], pages[i], c["scale"],
+                                     kv_dtype=c["kv"], num_blocks=c["num_blocks"])
+        return o, lse, o2, lse2
+
+    alone = [both(i) for i in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(both(i))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out in got[i]:
+            assert all(torch.equal(x, y) for x, y in zip(out, alone[i]))
+
+
 def test_tensors_elsewhere_are_refused():
     """A tensor that the GPU cannot read is refused before anything is launched."""
     import torch
