@@ -380,17 +380,23 @@ def _is_shape(name, t, dtype, shape):
                          f"{tuple(t.shape)} (contiguous={t.is_contiguous()})")
 
 
+_C = None  # torch._C, once a call has tensors
+
+
 def _raw_stream(stream, t, *others):
     """The stream to launch on as an integer. The calls launch on the current device, which must be
     that of every tensor."""
-    import torch
+    global _C
+    if _C is None:
+        import torch
+        _C = torch._C
     dev = t.get_device()  # -1: not a CUDA tensor
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != _C._cuda_getDevice():
         raise ValueError(f"tensors must be on the current CUDA device, got {t.device}")
     for x in others:
         if x is not None and x.get_device() != dev:
             raise ValueError(f"tensors must be on one CUDA device, got {t.device} and {x.device}")
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return _C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _page_args(q, block_table, seq_lens):
