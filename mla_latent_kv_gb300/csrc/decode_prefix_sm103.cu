@@ -29,9 +29,9 @@
 //       8 pair MMAs of M = 256 x N = 256 x K = 16, V read as an MN-major operand from the TMA tile.
 //       Helper warps rescale O when a group's maximum moved. Epilogue: fp32 O / l by TMA stores.
 //
-// Measured: 2048 flat rows over 32768 tokens 97 us, 1.51 PFLOP/s; 8192 rows over 4096 tokens 64 us,
-// 1.15 (32 units of one range each: 4 of 36 clusters idle, and the start, the end and the 17 MB of
-// partial states weigh more). Steady state is 1.2 us a group, against 1.11 of MMAs at full rate: the
+// Measured: 2048 flat rows over 32768 tokens 96 us, 1.51 PFLOP/s; 8192 rows over 4096 tokens 55 us,
+// 1.33 (32 units of one range each: 4 of 36 clusters idle, and the 9 us to the first weights, the 9 us from
+// the last scores to the end and the 17 MB of partial states weigh more). Steady state is 1.2 us a group, against 1.11 of MMAs at full rate: the
 // 64 or 72 KB of a group from L2 come in just behind them. What it took, on the first size with the requests' own
 // tokens: sixteen softmax warps for eight 293 -> 258 us (the softmax was the longest stage); arrivals at a
 // peer's barrier that publish nothing without the cluster-wide release, which takes 0.9 us, 258 -> 209;

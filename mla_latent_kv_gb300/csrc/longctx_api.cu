@@ -125,8 +125,12 @@ bool plan_prefix(mla_kv_dtype kv, int rows, int H, int prefix_len, int num_split
     const int own_len = std::max(0, max_seq_len - w->pages * mla::kPage);
     // With more rows than SM pairs mla_decode's default builds a schedule on the device, about 10 us
     // ahead of everything else. Behind a prefix the requests' own tokens are usually few: up to 32
-    // pages each row is one unit instead (2048 rows of 16 heads, up to 1000 own tokens: 150 -> 140 us).
-    if (num_splits == -1 && w->splits > 0 && own_len <= 32 * mla::kPage && rows > 76) num_splits = 1;
+    // pages each row is one unit instead (128 rows of 16 heads, up to 1000 own tokens: 150 -> 140 us), or two
+    // for few heads and more than 12 pages, which shortens the tail behind the prefix (the same 74 -> 68 us
+    // over 8192 shared tokens, FP8 83 -> 78, up to 2000 tokens 99 -> 89 and 115 -> 99; up to 300 tokens of 32
+    // heads one unit takes 68 and two 71, and 256 rows up to 1000 tokens 104 and 105).
+    if (num_splits == -1 && w->splits > 0 && own_len <= 32 * mla::kPage && rows > 76)
+        num_splits = mla::few_heads(H) && own_len > 12 * mla::kPage ? 2 : 1;
     w->own_splits = mla::resolve_splits(mla::few_heads(H), num_splits, rows, H, own_len);
     if (w->own_splits < 1 && w->own_splits != -2) return false;
     w->total = w->decode + mla::workspace_layout(kv, rows, rows, H, w->own_splits, own_len, w->splits > 0).total;
