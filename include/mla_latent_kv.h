@@ -422,7 +422,8 @@ mla_status mla_select_pages(const float* scores, int64_t scores_stride, int num_
  *                are padded with it. An entry that is not above every entry before it, or not one
  *                of the row's ceil(n / 64) pages, sets MLA_DEV_BAD_PAGE and is skipped.
  *   max_sel      1 <= max_sel <= (2^31 - 1) / 64; a row without pages gets o = 0, lse = -inf
- *   num_splits   as mla_decode, over each row's selected tokens
+ *   num_splits   as mla_decode, over each row's selected tokens; -1 is a uniform split of the library's
+ *                choice, whatever the number of rows
  *   workspace    >= mla_decode_sparse_workspace_bytes(...) bytes for the same arguments, 256-byte
  *                aligned (the rows' page tables and split-KV partials), contents undefined
  * All other arguments, results and errors as mla_decode.

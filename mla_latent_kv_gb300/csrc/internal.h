@@ -262,6 +262,8 @@ cudaError_t launch_prefix_widen(const PrefixArgs& a, const uint8_t* cache, uint1
 cudaError_t launch_decode_prefix(const PrefixArgs& a, const uint8_t* cache, const uint16_t* widened,
                                  const float* scales, cudaStream_t s);
 
+int device_sm_count();  // of the current device, or -1
+
 // Record an error for mla_last_error_detail() and return `st` (printf-style message).
 mla_status set_error(mla_status st, const char* fmt, ...);
 

@@ -42,6 +42,9 @@ mla_status cuda_fail(cudaError_t e, const char* who, const char* what) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+}  // namespace
+
+namespace mla {
 int device_sm_count() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return -1;
@@ -50,9 +53,6 @@ int device_sm_count() {
     return sms;
 }
 
-}  // namespace
-
-namespace mla {
 WorkspaceLayout workspace_layout(int kv_dtype, int B, int64_t rows, int H, int num_splits, int max_seq_len,
                                  bool all_partial) {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -144,8 +144,8 @@ int mla_default_num_splits(int max_seq_len, int sm_count) {
 int mla_resolve_num_splits(int num_splits, int B, int Sq, int H, int max_seq_len) {
     if (num_splits > 0) return num_splits;
     if (num_splits < -2 || B < 0 || Sq < 1 || H < 1 || max_seq_len < 0) return -1;
-    if (num_splits == -2) return device_sm_count() >= 1 ? -2 : -1;  // decided per row on the device
-    int sms = device_sm_count();
+    if (num_splits == -2) return mla::device_sm_count() >= 1 ? -2 : -1;  // decided per row on the device
+    int sms = mla::device_sm_count();
     if (sms < 1) return -1;
     if (num_splits == 0) return mla_default_num_splits(max_seq_len, sms);
     // More query rows than SM pairs: the units run in several waves, and how they pack depends on
