@@ -682,7 +682,7 @@ void prefix_split(int64_t flat_rows, int pages, int clusters, int* splits, int* 
     double best = 1e300;
     *splits = 1;
     *pages_per_split = (pages + 1) / 2 * 2;
-    for (int S = 1; S <= (pages + 1) / 2 && S <= 4096; ++S) {
+    for (int S = 1; S <= (pages + 1) / 2 && S <= 3 * clusters; ++S) {  // more never fill waves better
         const int per = ((pages + S - 1) / S + 1) / 2 * 2;
         const int used = (pages + per - 1) / per;  // ranges that hold pages
         if (used < S && S > 1) continue;
