@@ -65,7 +65,8 @@ using namespace ptx;
 using dec::store_rows;
 using dec::warp_wait;
 
-constexpr int kThreads = 608;  // warp 0 TMA, 1 MMA, 2-17 softmax / 2-5 helpers, 2-17 epilogue, 18 P copies
+// warp 0 TMA, 1 MMA, 2-17 softmax / 2-5 helpers, 6-9 CTA 3's relay, 2-17 epilogue, 18 P copies
+constexpr int kThreads = 608;
 constexpr int kSoftThreads = 512;
 constexpr int kTileRows = 256;
 constexpr int kPPG = 2;                      // pages per group, one per scores CTA
@@ -122,11 +123,13 @@ enum : int {
     B_VFULL = B_PEMPTY + kPBufs,        // [kVStages] CTA 2: V stage landed in both output CTAs
     B_VEMPTY = B_VFULL + kVStages,      // [kVStages] CTAs 2, 3: V stage consumed
     B_PFULL = B_VEMPTY + kVStages,      // [kPBufs] CTAs 2, 3: P message landed
-    B_READY = B_PFULL + kPBufs,         // [kPBufs] CTA 2: the 8 helper warps of the pair are done with the page
-    B_STATS = B_READY + kPBufs,         // CTAs 2, 3: final row statistics written, last P copy issued
+    B_READY = B_PFULL + kPBufs,         // [kPBufs] CTA 2: its 4 helper warps and CTA 3 are done with the page
+    B_PEER = B_READY + kPBufs,          // [kPBufs] CTA 3: its 4 helper warps are done with the page
+    B_STATS = B_PEER + kPBufs,          // CTAs 2, 3: final row statistics written, last P copy issued
     B_COUNT
 };
 static_assert(8 * B_COUNT <= 512, "barrier slots");
+constexpr int kRelayWarps = 4;    // of CTA 3, from warp 6 on: pages announced to CTA 2 in turn
 constexpr int OFF_TMEM = 512;
 constexpr int OFF_ABORT = 516;
 constexpr int OFF_MX = 1024;      // scores: f32 [4][128] exchange between the column quarters
@@ -175,7 +178,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             if (i == B_QREADY) cnt = kSoftThreads;
             if (i == B_STATS) cnt = 2;
             if (i >= B_STAGEFULL && i < B_STAGEFULL + kStages) cnt = 8;
-            if (i >= B_READY && i < B_READY + kPBufs) cnt = 8;
+            if (i >= B_READY && i < B_READY + kPBufs) cnt = 5;
+            if (i >= B_PEER && i < B_PEER + kPBufs) cnt = 4;
             bar_init(bar(i), cnt);
         }
         if (!scores)  // P buffers armed for their first message before a scores CTA can send one
@@ -570,13 +574,27 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     tmem_wait_st();
                 }
                 tc_fence_before();
-                // P came through the async proxy into this CTA and is read by MMAs that CTA 2
-                // issues: it is made visible along this warp's arrival
+                // P came through the async proxy into this CTA, and O may have been rescaled here; both
+                // are read by MMAs that CTA 2 issues. CTA 2's warps tell its MMA warp themselves, CTA 3's
+                // through the relay below.
                 fence_proxy_async_cta();
-                __syncwarp();
-                if (lane == 0) bar_arrive_remote_relaxed(bar(B_READY + pb), 2);
+                dec::warp_arrive(bar((side == 0 ? B_READY : B_PEER) + pb), lane);
                 pages_ready = i + 1;
             }
+            // CTA 3's pages are announced to CTA 2 by an arrival that releases at cluster scope, since it
+            // publishes the helpers' writes. That takes most of a microsecond, so warps that have nothing
+            // else to do before the epilogue take the pages in turn; the P buffers cover its latency (64 rows
+            // of 128 heads over 4096 + 512 tokens 86 us, 128 rows of 16 heads over 32768 + 1000 120).
+            if (side == 1 && warp >= 6 && warp < 6 + kRelayWarps && lane == 0) {
+                for (int i = warp - 6; i < npages; i += kRelayWarps) {
+                    const int pb = i % kPBufs;
+                    if (!wait_bar(bar(B_PEER + pb), (i / kPBufs) & 1, abort, ds)) break;
+                    tc_fence_after();
+                    tc_fence_before();
+                    bar_arrive_remote(bar(B_READY + pb), 2);
+                }
+            }
+            __syncwarp();
             const bool has_o = npages > 0 && pages_ready == npages && !*abort;
             wait_bar<true>(bar(B_STATS), 0, abort, ds);
             const bool o_ok = has_o && wait_bar<true>(bar(B_PEMPTY + (npages - 1) % kPBufs),

@@ -184,6 +184,36 @@ def test_shared_prefix_equals_decode_at_scale():
     assert torch.isfinite(o).all()
 
 
+def _mark_pages(c):
+    """Prefix page i holds a large value in dim i: its part of the result's dim i is the page's own, so that
+    another page's values, or another page's weights, show there."""
+    import torch
+    n = c["prefix"] // PAGE
+    assert n <= L
+    for i, blk in enumerate(c["full_table"][0, :n]):
+        if c["kv"] == BF:
+            c["cache"].view(torch.bfloat16).view(c["num_blocks"], PAGE, D)[int(blk), :, i] = 16.0
+        else:
+            c["cache"].view(c["num_blocks"], PAGE, D + 8)[int(blk), :, i] = 0x7E  # 448, the largest code
+
+
+@pytest.mark.parametrize("kv,B,H", [(BF, 128, 16), (F8, 128, 16), (BF, 24, 128), (F8, 30, 128)])
+def test_shared_prefix_values_at_scale(kv, B, H):
+    """16384 shared tokens, in several ranges of many pages each, against the definition: the bound is of
+    each element, where one page's own part of a result is several times the bound."""
+    c = paged_case([16384 + 1 + 7 * b for b in range(B)], 1, H, kv, seed=23, prefix=16384,
+                   scale_v=0.5 if kv == F8 else None)
+    _mark_pages(c)
+    assert _kernel(c)
+    st = _status()
+    o, lse = _prefix(c, status=st)
+    assert int(st.item()) == 0
+    want = attend(c)
+    check_attention(o, lse, want)
+    own = want[0][..., :256] / want[2][..., :256]  # dim i of page i, in units of the bound
+    assert own.abs().median().item() > 2
+
+
 @pytest.mark.parametrize("kv", [BF, F8])
 def test_shared_prefix_repeats_bit_for_bit(kv):
     """Forty calls over a workspace of NaN: a partial state that is stored too early, or read before it
