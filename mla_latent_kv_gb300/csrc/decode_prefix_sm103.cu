@@ -371,11 +371,11 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 const int page = kPPG * gi + pg2, buf = gi & 1;
                 size_t sc = 0;               // the quarter's first token of the page, in float4 units
                 float4 ks[kScaled ? 8 : 1];  // k_scale of its 32 tokens
-                if constexpr (kScaled) {
+                if constexpr (kScaled) {  // plain loads: the widening kernel wrote them while this one began
                     sc = ((size_t)(page0 + min(page, npages - 1)) * kPage + 32 * sub) / 4;
                     const float4* src = reinterpret_cast<const float4*>(p.k_scales) + sc;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) ks[j] = __ldg(src + j);
+                    for (int j = 0; j < 8; ++j) ks[j] = src[j];
                 }
                 const bool okS = warp_wait<true>(bar(B_SFULL + buf), (gi >> 1) & 1, abort, ds);
                 uint32_t s[32];
@@ -402,7 +402,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     const float4* src = reinterpret_cast<const float4*>(p.v_scales) + sc;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) vs[j] = __ldg(src + j);
+                    for (int j = 0; j < 8; ++j) vs[j] = src[j];
                 }
                 // No row of the warp sees any of these tokens (an empty slot's heads): no weights to compute.
                 // Masked like any other, three empty slots of 64 made their clusters the last to end, by 8 us

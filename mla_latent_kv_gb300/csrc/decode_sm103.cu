@@ -68,11 +68,11 @@ using namespace dec;
 // Hint: bring the 128-byte line at `ptr` into L2 (no effect on correctness).
 __device__ __forceinline__ void prefetch_l2(const void* ptr) { asm volatile("prefetch.global.L2 [%0];" ::"l"(ptr)); }
 
-// A 32-bit global load through the non-coherent path, issued where it stands in program order
-// (the asm is volatile), for data that no kernel of the grid writes.
-__device__ __forceinline__ int ld_nc_s32(const int32_t* ptr) {
+// A 32-bit global load, issued where it stands in program order (the asm is volatile). Not through the
+// non-coherent path: behind sparse_table_kernel the table is written while this kernel's set-up runs.
+__device__ __forceinline__ int ld_s32(const int32_t* ptr) {
     int v;
-    asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(ptr));
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(ptr) : "memory");
     return v;
 }
 
@@ -177,7 +177,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!early_blocks || tid != 0 || rank != 0) return;
 #pragma unroll
         for (int q = 0; q < kPPG; ++q)
-            if (p.base / kPage + q < p.max_blocks) blk_early[q] = ld_nc_s32(table_entry(p, unit / p.num_splits / p.Sq, q));
+            if (p.base / kPage + q < p.max_blocks) blk_early[q] = ld_s32(table_entry(p, unit / p.num_splits / p.Sq, q));
     };
     if (p.order != kOrderWaitFirst) fetch_blocks();
     RowGeom g{};

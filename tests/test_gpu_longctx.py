@@ -671,6 +671,43 @@ def test_two_streams_at_once(H):
             assert all(torch.equal(x, y) for x, y in zip(out, alone[i]))
 
 
+@pytest.mark.parametrize("kv,H", [(BF, 16), (BF, 128), (F8, 16), (F8, 48)])
+def test_calls_take_turns_on_one_workspace(kv, H):
+    """Calls with other caches, scales, tables and pages, back to back over one workspace: each reads what
+    its own kernels wrote there, not what the call before left."""
+    import torch
+    import mla_latent_kv_gb300 as mla
+    B, prefix, K = 160, 704, 7
+    cases = [paged_case([prefix + 1 + (37 * b + s) % 200 for b in range(B)], 1, H, kv, seed=150 + s, prefix=prefix,
+                        scale_v=(0.5, 3.0)[s] if kv == F8 else None) for s in range(2)]
+    assert all(_kernel(c) for c in cases)
+    full = [dev(c["full_table"]) for c in cases]
+    picked = [_pick(c, K, 152 + s)[0] for s, c in enumerate(cases)]
+    picked = [dev(x) for x in picked]
+    need = max([mla.decode_sparse_workspace_bytes(B, 1, H, K, kv)] +
+               [mla.decode_shared_prefix_workspace_bytes(B, 1, H, prefix, c["max_len"], kv) for c in cases])
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def sparse(i):
+        c = cases[i]
+        return mla.decode_sparse(c["q"], c["cache"], full[i], c["seq_lens"], picked[i], c["scale"], kv_dtype=kv,
+                                 workspace=ws, num_blocks=c["num_blocks"])
+
+    for call in (lambda i: _prefix(cases[i], workspace=ws), sparse):
+        alone = []
+        for i in range(2):
+            torch.cuda.synchronize()
+            ws.fill_(0xFF)
+            torch.cuda.synchronize()
+            alone.append(call(i))
+            torch.cuda.synchronize()
+        got = [call(i % 2) for i in range(20)]
+        torch.cuda.synchronize()
+        for i, (o, lse) in enumerate(got):
+            assert torch.equal(o, alone[i % 2][0]) and torch.equal(lse, alone[i % 2][1]), i
+        assert not torch.equal(alone[0][0], alone[1][0])
+
+
 def test_tensors_elsewhere_are_refused():
     """A tensor that the GPU cannot read is refused before anything is launched."""
     import torch
