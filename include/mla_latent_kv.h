@@ -26,6 +26,10 @@
  *     seq_len larger than max_blocks*64, a bounded wait that ran out) are OR-ed as MLA_DEV_*
  *     bits into the optional int32 `dev_status` in device memory; the caller reads it after
  *     synchronising. The kernels never trap.
+ *   - Kernels are launched with programmatic stream serialization, and the decode kernels read the
+ *     cache, block_table and seq_lens, other kernels their weights, before they wait for the kernel
+ *     ahead. Any kernel may write them ahead of a call, but one that signals its dependents early
+ *     (griddepcontrol.launch_dependents, cudaTriggerProgrammaticLaunchCompletion) must not.
  *   - bf16 means IEEE bfloat16 bits; all layouts are row-major, last index fastest.
  */
 #ifndef MLA_LATENT_KV_H

@@ -267,10 +267,10 @@ __global__ void __launch_bounds__(128) sparse_table_kernel(SparseTableArgs p) {
     const int r = (int)blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const bool live = r < p.B * p.Sq;
     const int b = live ? r / p.Sq : 0, t = live ? r % p.Sq : 0;
-    int seq = p.seq_lens[b];  // no kernel of the library writes it
-    ptx::griddep_wait();
+    ptx::griddep_wait();  // the lengths, too, may be a caller's kernel's output
     ptx::griddep_launch_dependents();
     if (!live) return;
+    int seq = p.seq_lens[b];
     int next = lane < p.K ? p.pages[(size_t)r * p.K + lane] : -1;
     const int64_t cap = (int64_t)p.max_blocks * kPage;
     if (seq < 0 || seq > cap) {

@@ -708,6 +708,46 @@ def test_calls_take_turns_on_one_workspace(kv, H):
         assert not torch.equal(alone[0][0], alone[1][0])
 
 
+@pytest.mark.parametrize("H", [16, 128])
+def test_lengths_and_tables_written_just_ahead(H):
+    """Lengths and block tables that a kernel writes directly ahead of the calls, eager and in a graph."""
+    import torch
+    import mla_latent_kv_gb300 as mla
+    cases = [paged_case([1 + (97 * b + 31 * s) % 900 for b in range(40)], 1, H, BF, seed=160 + s, extra_cols=4)
+             for s in range(2)]
+    cols, K = max(c["table"].shape[1] for c in cases), 6
+    tables = [torch_pad(c["table"], cols) for c in cases]
+    picked = [dev(_pick(c, K, 162 + s)[0]) for s, c in enumerate(cases)]
+    blocks = max(c["num_blocks"] for c in cases)
+    cache = torch.zeros((blocks, PAGE * 1152), dtype=torch.uint8, device="cuda")
+    cache[:cases[0]["num_blocks"]] = cases[0]["cache"].view(-1, PAGE * 1152)
+    q, table, lens, pages = cases[0]["q"], tables[0].clone(), cases[0]["seq_lens"].clone(), picked[0].clone()
+    cache.view(torch.bfloat16).nan_to_num_(0.0)  # the second table's lengths reach rows that the first leaves unwritten
+    max_len = cols * PAGE
+
+    def calls(i):
+        for dst, src in ((table, tables[i]), (pages, picked[i]), (lens, cases[i]["seq_lens"])):
+            dst.copy_(src)
+        sparse = mla.decode_sparse(q, cache, table, lens, pages, 0.07, num_blocks=blocks)
+        lens.copy_(cases[i]["seq_lens"])
+        return sparse + mla.decode_shared_prefix(q, cache, table, lens, max_len, 0, 0.07, num_blocks=blocks)
+
+    alone = []
+    for i in range(2):
+        torch.cuda.synchronize()
+        alone.append(calls(i))
+    torch.cuda.synchronize()
+    g, outs = torch.cuda.CUDAGraph(), []
+    with torch.cuda.graph(g):
+        outs = [calls(i % 2) for i in range(6)]
+    g.replay()
+    outs += [calls(i % 2) for i in range(6)]
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        assert all(torch.equal(x, y) for x, y in zip(out, alone[i % 2])), i
+    assert not torch.equal(alone[0][0], alone[1][0])
+
+
 def test_tensors_elsewhere_are_refused():
     """A tensor that the GPU cannot read is refused before anything is launched."""
     import torch
