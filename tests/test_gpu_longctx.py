@@ -671,6 +671,54 @@ def test_two_streams_at_once(H):
             assert all(torch.equal(x, y) for x, y in zip(out, alone[i]))
 
 
+@pytest.mark.parametrize("H", [16, 128])
+def test_stream_argument_with_buffers_of_the_calls_own(H):
+    """Calls given stream= and no buffers, issued from one thread for two streams while the current stream
+    takes and fills memory: each gives what it gives alone."""
+    import torch
+    import mla_latent_kv_gb300 as mla
+    B, prefix = 64, 4096
+    cases = [paged_case([prefix + 1 + (37 * b + s) % 400 for b in range(B)], 1, H, kv, seed=170 + s, prefix=prefix)
+             for s, kv in enumerate((BF, F8))]
+    full = [dev(c["full_table"]) for c in cases]
+    pages = [torch.sort(torch.stack([torch.randperm(64)[:24] for _ in range(B)]), 1)[0].int().view(B, 1, 24).cuda()
+             for _ in cases]
+    junk = []
+
+    def busy():  # whatever the current stream's pool holds free is taken and overwritten
+        junk[:] = [torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda") for n in (1 << 14, 1 << 20, 1 << 23, 1 << 26)]
+        junk.clear()
+
+    def calls(i, stream):
+        c = cases[i]
+        kw = dict(kv_dtype=c["kv"], num_blocks=c["num_blocks"], stream=stream)
+        out = []
+        out += mla.decode_shared_prefix(c["q"], c["cache"], c["table"], c["seq_lens"], c["max_len"], prefix, c["scale"], **kw)
+        busy()
+        out += mla.decode_sparse(c["q"], c["cache"], full[i], c["seq_lens"], pages[i], c["scale"], **kw)
+        busy()
+        out += mla.decode(c["q"], c["cache"], full[i], c["seq_lens"], c["max_len"], c["scale"], num_splits=3, **kw)
+        busy()
+        keys = mla.page_keys(c["cache"], full[i], c["seq_lens"], c["max_len"], **kw)
+        busy()
+        s = mla.page_scores(c["q"], keys, full[i], c["seq_lens"], c["max_len"], c["scale"], stream=stream)
+        busy()
+        return out + [keys, s, mla.select_pages(s, c["seq_lens"], 8, stream=stream)]
+
+    alone = [calls(i, None) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(4):
+        for i in range(2):
+            busy()
+            got[i].append(calls(i, streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out in got[i]:
+            assert all(torch.equal(x, y) for x, y in zip(out, alone[i]))
+
+
 @pytest.mark.parametrize("kv,H", [(BF, 16), (BF, 128), (F8, 16), (F8, 48)])
 def test_calls_take_turns_on_one_workspace(kv, H):
     """Calls with other caches, scales, tables and pages, back to back over one workspace: each reads what

@@ -1,5 +1,6 @@
 """Argument checks of the shared-prefix and selected-page calls: refused on the host, nothing launched."""
 import ctypes
+import types
 
 import numpy as np
 import pytest
@@ -133,6 +134,75 @@ def test_binding_refuses_wrong_tensors():
         mla.select_pages(torch.zeros(2, 1, 8).double(), seq, 4)
     with pytest.raises(ValueError):
         mla.select_pages(torch.zeros(2, 1, 8), seq, 4)  # not on the device
+
+
+class _FakeLib:
+    """Stands for the native library: sizes are 4096 bytes, every call succeeds and launches nothing."""
+
+    def __getattr__(self, name):
+        if name == "mla_kv_row_bytes":
+            return lambda kv: {0: 1152, 1: 584}[kv]
+        if name == "mla_resolve_num_splits":
+            return lambda *a: 2
+        return lambda *a: 4096 if "workspace_bytes" in name else 0
+
+
+@pytest.mark.parametrize("call", ["absorb_q", "decode", "decode_noalloc", "decode_varlen", "out_proj", "prefill",
+                                  "decode_shared_prefix", "page_keys", "page_scores", "select_pages", "decode_sparse"])
+def test_buffers_are_made_on_the_stream_that_uses_them(call, monkeypatch):
+    """A call with stream= makes its outputs and workspace on that stream: from its pool, so that the memory
+    is not given to other work while the call's kernels run, and filled there, so that they follow the fill."""
+    torch = pytest.importorskip("torch")
+    here, made, used = [], [], []
+
+    class OnStream:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            here.append(self.stream.name)
+
+        def __exit__(self, *exc):
+            here.pop()
+
+    def recorded(make):
+        def f(*a, **kw):
+            made.append(here[-1] if here else "current")
+            return make(*a, **kw)
+        return f
+
+    z = lambda *shape, dtype=torch.bfloat16: torch.zeros(shape, dtype=dtype)  # noqa: E731
+    i32 = torch.int32
+    q, cache, table, lens, starts = z(2, 1, 16, 576), z(8, 64 * 576), z(2, 4, dtype=i32), z(2, dtype=i32), z(3, dtype=i32)
+    w_uk_t, w_uv = z(16, 128, 512), z(16, 512, 128)
+    args = {
+        "absorb_q": (z(2, 16, 128), z(2, 16, 64), w_uk_t),
+        "decode": (q, cache, table, lens, 200, 0.07),
+        "decode_noalloc": (q, cache, table, lens, 200, 0.07),
+        "decode_varlen": (q[:, 0], cache, table, lens, starts, 200, 0.07),
+        "out_proj": (z(2, 16, 512), w_uv),
+        "prefill": (z(2, 16, 192), z(2, 512), z(2, 64), cache, table, lens, starts, w_uk_t, w_uv, 0.07),
+        "decode_shared_prefix": (q, cache, table, lens, 200, 64, 0.07),
+        "page_keys": (cache, table, lens, 200),
+        "page_scores": (q, z(8, 576), table, lens, 200, 0.07),
+        "select_pages": (z(2, 1, 4, dtype=torch.float32), lens, 2),
+        "decode_sparse": (q, cache, table, lens, z(2, 1, 2, dtype=i32), 0.07),
+    }[call]
+    monkeypatch.setattr(mla, "lib", _FakeLib)
+    monkeypatch.setattr(mla, "_stream", lambda *a: None)
+    monkeypatch.setattr(mla, "_raw_stream", lambda *a: 0)
+    monkeypatch.setattr(torch.cuda, "stream", OnStream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda s: types.SimpleNamespace(device=0, name=s))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: "current")
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: used.append((t.data_ptr(), s)))
+    monkeypatch.setattr(torch, "empty", recorded(torch.empty))
+    monkeypatch.setattr(torch, "zeros", recorded(torch.zeros))
+    for given, where in (({}, "current"), ({"stream": types.SimpleNamespace(cuda_stream="side")}, "side")):
+        made.clear()
+        out = getattr(mla, call)(*args, **given)
+        assert made and set(made) == {where}, (given, made)
+        outs = out if isinstance(out, tuple) else (out,)
+        assert used == [(t.data_ptr(), "current") for t in outs if given]  # kept while the caller's stream reads them
 
 
 def test_the_plain_rule_of_the_choice():
