@@ -155,18 +155,22 @@ def _stream(stream):
 
 
 def _on(stream, name, args):
-    """This module's `name`(**args) with `stream` as the current stream: outputs and workspace that the call
-    makes come from that stream's memory pool and are filled there. Made on another stream, their memory
-    could be given to that stream's later work while this one's kernels still use it. The results are
-    marked as used on the caller's current stream too, which is to wait for `stream` before it reads
-    them. (A call passes its own locals(), before it has any but its arguments.)"""
+    """This module's `name`, of the arguments among `args` (a call's own locals()), with `stream` as the
+    current stream: for a call that makes outputs or a workspace itself. They come from that stream's
+    memory pool and are filled there; made on another stream, their memory could be given to that
+    stream's later work while this one's kernels still use it. The results are marked as used on the
+    caller's current stream too, which is to wait for `stream` before it reads them."""
     import torch
+    call = globals()[name]
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(stream.cuda_stream)
     caller = torch.cuda.current_stream(stream.device)
+    args = {a: args[a] for a in call.__code__.co_varnames[:call.__code__.co_argcount]}
     args["stream"] = None
+    if stream == caller:
+        return call(**args)
     with torch.cuda.stream(stream):
-        out = globals()[name](**args)
+        out = call(**args)
     for t in out if isinstance(out, tuple) else (out,):
         t.record_stream(caller)
     return out
@@ -179,16 +183,16 @@ def _p(t):
 def absorb_q(q_nope, q_pe, w_uk_t, out=None, stream=None):
     """q_nope [T,H,128] bf16 (any token/head strides, unit stride inside a head), q_pe [T,H,64]
     bf16 or None, W_UK_T [H,128,512] bf16 -> q [T,H,576] bf16."""
-    if stream is not None:
-        return _on(stream, "absorb_q", locals())
     import torch
     T, H = q_nope.shape[0], q_nope.shape[1]
     assert q_nope.stride(2) == 1 and w_uk_t.is_contiguous()
+    if stream is not None and out is None:
+        return _on(stream, "absorb_q", locals())
     if out is None:
         out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q_nope.device)
     spt, sph = (q_pe.stride(0), q_pe.stride(1)) if q_pe is not None else (0, 0)
     _check(lib().mla_absorb_q(_p(q_nope), q_nope.stride(0), q_nope.stride(1), _p(q_pe), spt, sph,
-                              _p(w_uk_t), _p(out), T, H, _stream(None)))
+                              _p(w_uk_t), _p(out), T, H, _stream(stream)))
     return out
 
 
@@ -223,8 +227,6 @@ def decode(q, kv_cache, block_table, seq_lens, max_seq_len, scale, kv_dtype=KV_B
            num_blocks=None):
     """q [B,Sq,H,576] bf16, kv_cache [num_blocks, 64*row_bytes] uint8 (or a bf16 view), block_table
     [B,max_blocks] int32, seq_lens [B] int32 -> (o_latent [B,Sq,H,512], lse [B,Sq,H])."""
-    if stream is not None:
-        return _on(stream, "decode", locals())
     import torch
     B, Sq, H = q.shape[0], q.shape[1], q.shape[2]
     dev = q.device
@@ -232,6 +234,8 @@ def decode(q, kv_cache, block_table, seq_lens, max_seq_len, scale, kv_dtype=KV_B
         num_blocks = kv_cache.numel() * kv_cache.element_size() // (PAGE * row_bytes(kv_dtype))
     S = resolve_num_splits(num_splits, B, Sq, H, max_seq_len)
     need = workspace_bytes(B, Sq, H, S, kv_dtype, max_seq_len)
+    if stream is not None and (o_latent is None or lse is None or (need and workspace is None)):
+        return _on(stream, "decode", locals())
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     o_dtype = _dt_code(o_latent, o_dtype)
@@ -241,7 +245,7 @@ def decode(q, kv_cache, block_table, seq_lens, max_seq_len, scale, kv_dtype=KV_B
     _check(lib().mla_decode(_p(q), _p(kv_cache), kv_dtype, int(num_blocks), _p(block_table),
                             block_table.shape[1], _p(seq_lens), int(max_seq_len), B, Sq, H, float(scale),
                             int(S), _p(workspace), ws_bytes, _p(o_latent), o_dtype, _p(lse), _p(dev_status),
-                            _stream(None)))
+                            _stream(stream)))
     return o_latent, lse
 
 
@@ -265,20 +269,20 @@ def decode_noalloc(q, kv_cache, block_table, seq_lens, max_seq_len, scale, kv_dt
                    o_latent=None, o_dtype=None, lse=None, dev_status=None, stream=None, num_blocks=None):
     """decode() through mla_decode_noalloc: the split-KV scratch is the library's own fixed device
     array, so no workspace is passed (outputs are still made here when not given)."""
-    if stream is not None:
-        return _on(stream, "decode_noalloc", locals())
     import torch
     B, Sq, H = q.shape[0], q.shape[1], q.shape[2]
     dev = q.device
     if num_blocks is None:
         num_blocks = kv_cache.numel() * kv_cache.element_size() // (PAGE * row_bytes(kv_dtype))
+    if stream is not None and (o_latent is None or lse is None):
+        return _on(stream, "decode_noalloc", locals())
     o_dtype = _dt_code(o_latent, o_dtype)
     o_latent = _out_buf(o_latent, (B, Sq, H, L), o_dtype, dev)
     lse = _out_buf(lse, (B, Sq, H), DT_F32, dev)
     _check(lib().mla_decode_noalloc(_p(q), _p(kv_cache), kv_dtype, int(num_blocks), _p(block_table),
                                     block_table.shape[1], _p(seq_lens), int(max_seq_len), B, Sq, H, float(scale),
                                     int(num_splits), _p(o_latent), o_dtype, _p(lse), _p(dev_status),
-                                    _stream(None)))
+                                    _stream(stream)))
     return o_latent, lse
 
 
@@ -287,8 +291,6 @@ def decode_varlen(q, kv_cache, block_table, seq_lens, query_start_loc, max_seq_l
                   num_blocks=None):
     """q [total_q, H, 576] bf16 packed by query_start_loc [B + 1] int32 (device) ->
     (o_latent [total_q, H, 512], lse [total_q, H])."""
-    if stream is not None:
-        return _on(stream, "decode_varlen", locals())
     import torch
     total_q, H = q.shape[0], q.shape[1]
     B = int(query_start_loc.shape[0]) - 1
@@ -297,6 +299,8 @@ def decode_varlen(q, kv_cache, block_table, seq_lens, query_start_loc, max_seq_l
         num_blocks = kv_cache.numel() * kv_cache.element_size() // (PAGE * row_bytes(kv_dtype))
     S = resolve_num_splits(num_splits, max(total_q, 1), 1, H, max_seq_len)
     need = int(lib().mla_decode_varlen_workspace_bytes(kv_dtype, B, total_q, H, S, max_seq_len))
+    if stream is not None and (o_latent is None or lse is None or (need and workspace is None)):
+        return _on(stream, "decode_varlen", locals())
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     o_dtype = _dt_code(o_latent, o_dtype)
@@ -306,7 +310,7 @@ def decode_varlen(q, kv_cache, block_table, seq_lens, query_start_loc, max_seq_l
     _check(lib().mla_decode_varlen(_p(q), _p(kv_cache), kv_dtype, int(num_blocks), _p(block_table),
                                    block_table.shape[1], _p(seq_lens), _p(query_start_loc), int(max_seq_len), B,
                                    total_q, H, float(scale), int(S), _p(workspace), ws_bytes, _p(o_latent), o_dtype,
-                                   _p(lse), _p(dev_status), _stream(None)))
+                                   _p(lse), _p(dev_status), _stream(stream)))
     return o_latent, lse
 
 
@@ -326,16 +330,16 @@ def cache_write(kv_c, k_pe, slot_mapping, kv_cache, kv_dtype=KV_BF16, kv_scale=0
 def out_proj(o_latent, w_uv, out=None, out_dtype=None, stream=None):
     """o_latent [T,H,512] fp32/bf16, W_UV [H,512,128] bf16 -> o [T,H,128] (fp32 unless out_dtype or
     a given `out` says bf16)."""
-    if stream is not None:
-        return _on(stream, "out_proj", locals())
     import torch
     T, H = o_latent.shape[0], o_latent.shape[1]
     if o_latent.dtype not in (torch.float32, torch.bfloat16) or not o_latent.is_contiguous():
         raise ValueError(f"o_latent must be a contiguous fp32 or bf16 tensor, got {o_latent.dtype}")
     in_dtype = DT_F32 if o_latent.dtype == torch.float32 else DT_BF16
     out_dtype = _dt_code(out, out_dtype)
+    if stream is not None and out is None:
+        return _on(stream, "out_proj", locals())
     out = _out_buf(out, (T, H, V), out_dtype, o_latent.device)
-    _check(lib().mla_out_proj(_p(o_latent), in_dtype, _p(w_uv), _p(out), out_dtype, T, H, _stream(None)))
+    _check(lib().mla_out_proj(_p(o_latent), in_dtype, _p(w_uv), _p(out), out_dtype, T, H, _stream(stream)))
     return out
 
 
@@ -364,12 +368,12 @@ def prefill(q, kv_c, k_pe, kv_cache, block_table, ctx_lens, query_start_loc, w_u
     ctx_lens [B] and query_start_loc [B + 1] int32 device tensors (read once on the host for the
     launch plan, unless host copies are passed as ctx_lens_host / query_start_loc_host int32 CPU
     tensors) -> (o [total_q, H, 128] fp32, lse [total_q, H] fp32)."""
-    if stream is not None:
-        return _on(stream, "prefill", locals())
     import torch
     total_q, H = q.shape[0], q.shape[1]
     B = int(query_start_loc.shape[0]) - 1
     dev = q.device
+    if stream is not None and any(x is None for x in (ctx_lens_host, query_start_loc_host, workspace, o, lse)):
+        return _on(stream, "prefill", locals())
     ctx_host = ctx_lens.to("cpu", torch.int32).contiguous() if ctx_lens_host is None else ctx_lens_host
     qsl_host = query_start_loc.to("cpu", torch.int32).contiguous() if query_start_loc_host is None \
         else query_start_loc_host
@@ -390,7 +394,7 @@ def prefill(q, kv_c, k_pe, kv_cache, block_table, ctx_lens, query_start_loc, w_u
                              _p(block_table), block_table.shape[1], _p(ctx_lens), _p(query_start_loc),
                              ctypes.c_void_p(ctx_host.data_ptr()), ctypes.c_void_p(qsl_host.data_ptr()), B, H,
                              _p(w_uk_t), _p(w_uv), float(scale), int(chunk_rows), _p(workspace), ws_bytes, _p(o),
-                             _p(lse), _p(dev_status), _stream(None)))
+                             _p(lse), _p(dev_status), _stream(stream)))
     return o, lse
 
 
@@ -413,9 +417,9 @@ def _is_shape(name, t, dtype, shape):
 _C = None  # torch._C, once a call has tensors
 
 
-def _raw_stream(t, *others):
-    """The current stream as an integer. The calls launch on the current device, which must be that of
-    every tensor."""
+def _raw_stream(stream, t, *others):
+    """The stream to launch on as an integer. The calls launch on the current device, which must be
+    that of every tensor."""
     global _C
     if _C is None:
         import torch
@@ -426,7 +430,7 @@ def _raw_stream(t, *others):
     for x in others:
         if x is not None and x.get_device() != dev:
             raise ValueError(f"tensors must be on one CUDA device, got {t.device} and {x.device}")
-    return _C._cuda_getCurrentRawStream(dev)
+    return _C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _page_args(q, block_table, seq_lens):
@@ -489,15 +493,15 @@ def decode_shared_prefix(q, kv_cache, block_table, seq_lens, max_seq_len, prefix
     """decode() of a batch whose requests share their first prefix_len tokens (a multiple of 64): the
     first prefix_len / 64 entries of block_table's rows name the same pages, read once for all
     -> (o_latent [B,Sq,H,512], lse [B,Sq,H])."""
-    if stream is not None:
-        return _on(stream, "decode_shared_prefix", locals())
     B, Sq, H = _page_args(q, block_table, seq_lens)
     nb = _cache_blocks(kv_cache, kv_dtype, num_blocks)
     l = lib()
     need = 0 if workspace is not None else l.mla_decode_shared_prefix_workspace_bytes(
         kv_dtype, B, Sq, H, int(prefix_len), num_splits, int(max_seq_len))
+    if stream is not None and (o_latent is None or lse is None or (need and workspace is None)):
+        return _on(stream, "decode_shared_prefix", locals())
     o_latent, o_dtype, lse, workspace, ws_bytes = _attention_bufs(q, B, Sq, H, o_latent, o_dtype, lse, workspace, need)
-    s = _raw_stream(q, kv_cache, block_table, seq_lens, o_latent, lse, workspace, dev_status)
+    s = _raw_stream(stream, q, kv_cache, block_table, seq_lens, o_latent, lse, workspace, dev_status)
     _check(l.mla_decode_shared_prefix(q.data_ptr(), kv_cache.data_ptr(), kv_dtype, nb, block_table.data_ptr(),
                                       block_table.shape[1], seq_lens.data_ptr(), int(max_seq_len), int(prefix_len), B,
                                       Sq, H, float(scale), int(num_splits), _a(workspace), ws_bytes, o_latent.data_ptr(),
@@ -510,8 +514,6 @@ def page_keys(kv_cache, block_table, seq_lens, max_new_len, kv_dtype=KV_BF16, st
     """Mean key of every page that holds any of each request's tokens start_lens[b] .. seq_lens[b] - 1
     (start_lens None: all of them) -> page_keys bf16 [num_blocks, 576], written in place when given
     (other pages' keys stay)."""
-    if stream is not None:
-        return _on(stream, "page_keys", locals())
     import torch
     _is("block_table", block_table, torch.int32, 2)
     B, max_blocks = block_table.shape
@@ -519,10 +521,12 @@ def page_keys(kv_cache, block_table, seq_lens, max_new_len, kv_dtype=KV_BF16, st
     if start_lens is not None:
         _is_shape("start_lens", start_lens, torch.int32, (B,))
     nb = _cache_blocks(kv_cache, kv_dtype, num_blocks)
+    if stream is not None and page_keys is None:
+        return _on(stream, "page_keys", locals())
     if page_keys is None:
         page_keys = torch.zeros((nb, D), dtype=torch.bfloat16, device=kv_cache.device)
     _is_shape("page_keys", page_keys, torch.bfloat16, (nb, D))
-    s = _raw_stream(kv_cache, block_table, start_lens, seq_lens, page_keys, dev_status)
+    s = _raw_stream(stream, kv_cache, block_table, start_lens, seq_lens, page_keys, dev_status)
     _check(lib().mla_page_keys(kv_cache.data_ptr(), kv_dtype, nb, block_table.data_ptr(), max_blocks, _a(start_lens),
                                seq_lens.data_ptr(), int(max_new_len), B, page_keys.data_ptr(), _a(dev_status), s))
     return page_keys
@@ -531,16 +535,16 @@ def page_keys(kv_cache, block_table, seq_lens, max_new_len, kv_dtype=KV_BF16, st
 def page_scores(q, page_keys, block_table, seq_lens, max_seq_len, scale, scores=None, dev_status=None, stream=None):
     """Score of every page for every query row, max over heads of scale * <q, page key>
     -> fp32 [B, Sq, ceil(max_seq_len / 64)], -inf past a row's pages."""
-    if stream is not None:
-        return _on(stream, "page_scores", locals())
     import torch
     B, Sq, H = _page_args(q, block_table, seq_lens)
     _is_shape("page_keys", page_keys, torch.bfloat16, (page_keys.shape[0], D))
     width = -(-int(max_seq_len) // PAGE)
+    if stream is not None and scores is None:
+        return _on(stream, "page_scores", locals())
     if scores is None:
         scores = torch.empty((B, Sq, width), dtype=torch.float32, device=q.device)
     _is_shape("scores", scores, torch.float32, (B, Sq, width))
-    s = _raw_stream(q, page_keys, block_table, seq_lens, scores, dev_status)
+    s = _raw_stream(stream, q, page_keys, block_table, seq_lens, scores, dev_status)
     _check(lib().mla_page_scores(q.data_ptr(), page_keys.data_ptr(), page_keys.shape[0], block_table.data_ptr(),
                                  block_table.shape[1], seq_lens.data_ptr(), int(max_seq_len), B, Sq, H, float(scale),
                                  scores.data_ptr(), _a(dev_status), s))
@@ -551,8 +555,6 @@ def select_pages(scores, seq_lens, max_sel, sink_pages=1, local_pages=1, pages=N
     """The pages of each query row from scores [B, Sq, num_pages] (rows may be strided): the first
     sink_pages, the last local_pages, and the best others -> int32 [B, Sq, max_sel], ascending, -1
     behind the last."""
-    if stream is not None:
-        return _on(stream, "select_pages", locals())
     import torch
     B, Sq, width = scores.shape
     if scores.is_contiguous():
@@ -564,10 +566,12 @@ def select_pages(scores, seq_lens, max_sel, sink_pages=1, local_pages=1, pages=N
     if scores.dtype is not torch.float32:
         raise ValueError(f"scores must be fp32, got {scores.dtype}")
     _is_shape("seq_lens", seq_lens, torch.int32, (B,))
+    if stream is not None and pages is None:
+        return _on(stream, "select_pages", locals())
     if pages is None:
         pages = torch.empty((B, Sq, max_sel), dtype=torch.int32, device=scores.device)
     _is_shape("pages", pages, torch.int32, (B, Sq, max_sel))
-    s = _raw_stream(scores, seq_lens, pages, dev_status)
+    s = _raw_stream(stream, scores, seq_lens, pages, dev_status)
     _check(lib().mla_select_pages(scores.data_ptr(), stride, width, seq_lens.data_ptr(), B, Sq, int(max_sel),
                                   int(sink_pages), int(local_pages), pages.data_ptr(), _a(dev_status), s))
     return pages
@@ -582,8 +586,6 @@ def decode_sparse(q, kv_cache, block_table, seq_lens, pages, scale, kv_dtype=KV_
                   o_latent=None, o_dtype=None, lse=None, dev_status=None, stream=None, num_blocks=None):
     """decode() with each query row's attention limited to its selected pages [B, Sq, max_sel] int32
     (ascending, -1 skipped) -> (o_latent [B,Sq,H,512], lse [B,Sq,H])."""
-    if stream is not None:
-        return _on(stream, "decode_sparse", locals())
     import torch
     B, Sq, H = _page_args(q, block_table, seq_lens)
     _is("pages", pages, torch.int32, 3)
@@ -593,8 +595,10 @@ def decode_sparse(q, kv_cache, block_table, seq_lens, pages, scale, kv_dtype=KV_
     nb = _cache_blocks(kv_cache, kv_dtype, num_blocks)
     l = lib()
     need = 0 if workspace is not None else l.mla_decode_sparse_workspace_bytes(kv_dtype, B, Sq, H, K, num_splits)
+    if stream is not None and (o_latent is None or lse is None or (need and workspace is None)):
+        return _on(stream, "decode_sparse", locals())
     o_latent, o_dtype, lse, workspace, ws_bytes = _attention_bufs(q, B, Sq, H, o_latent, o_dtype, lse, workspace, need)
-    s = _raw_stream(q, kv_cache, block_table, seq_lens, pages, o_latent, lse, workspace, dev_status)
+    s = _raw_stream(stream, q, kv_cache, block_table, seq_lens, pages, o_latent, lse, workspace, dev_status)
     _check(l.mla_decode_sparse(q.data_ptr(), kv_cache.data_ptr(), kv_dtype, nb, block_table.data_ptr(),
                                block_table.shape[1], seq_lens.data_ptr(), pages.data_ptr(), K, B, Sq, H, float(scale),
                                int(num_splits), _a(workspace), ws_bytes, o_latent.data_ptr(), o_dtype, lse.data_ptr(),

@@ -153,7 +153,7 @@ def test_buffers_are_made_on_the_stream_that_uses_them(call, monkeypatch):
     """A call with stream= makes its outputs and workspace on that stream: from its pool, so that the memory
     is not given to other work while the call's kernels run, and filled there, so that they follow the fill."""
     torch = pytest.importorskip("torch")
-    here, made, used = [], [], []
+    here, made, used, launched = [], [], [], []
 
     class OnStream:
         def __init__(self, stream):
@@ -203,6 +203,23 @@ def test_buffers_are_made_on_the_stream_that_uses_them(call, monkeypatch):
         assert made and set(made) == {where}, (given, made)
         outs = out if isinstance(out, tuple) else (out,)
         assert used == [(t.data_ptr(), "current") for t in outs if given]  # kept while the caller's stream reads them
+    # a call that is given every buffer makes none, and goes to the stream as it is
+    made.clear()
+    used.clear()
+    monkeypatch.setattr(torch.cuda, "stream", None)
+    monkeypatch.setattr(mla, "_stream", launched.append)
+    monkeypatch.setattr(mla, "_raw_stream", lambda s, *t: launched.append(s))
+    ws = z(4096, dtype=torch.uint8)
+    names = {"absorb_q": ("out",), "out_proj": ("out",), "decode_noalloc": ("o_latent", "lse"), "prefill": ("o", "lse"),
+             "page_keys": ("page_keys",), "page_scores": ("scores",), "select_pages": ("pages",)}
+    given = dict(zip(names.get(call, ("o_latent", "lse")), outs), stream="side")
+    if call in ("decode", "decode_varlen", "decode_shared_prefix", "decode_sparse", "prefill"):
+        given["workspace"] = ws
+    if call == "prefill":
+        given.update(ctx_lens_host=lens, query_start_loc_host=starts)
+    made.clear()
+    getattr(mla, call)(*args, **given)
+    assert made == [] and used == [] and launched == ["side"]
 
 
 def test_the_plain_rule_of_the_choice():
