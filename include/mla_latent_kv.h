@@ -179,7 +179,8 @@ mla_status mla_absorb_q(const void* q_nope, int64_t q_nope_stride_t, int64_t q_n
  *     o_latent[b,t,h,:] = sum_j exp(s_j - lse) * V_j                   (512 values)
  * where row j of request b is cache[block_table[b, j / 64], j % 64, :], K_j is its 576 values
  * and V_j its first 512 values (dequantised per row for the FP8 format). A row with n == 0
- * gets o_latent = 0 and lse = -inf. `scale` is the caller's softmax scale; for DeepSeek-V3 it
+ * gets o_latent = 0 and lse = -inf, and so does one whose scores are all -inf. A NaN or +inf score of
+ * a visible token makes the row's o_latent and lse NaN. `scale` is the caller's softmax scale; for DeepSeek-V3 it
  * is 1/sqrt(192), not 1/sqrt(576) ([vLLM-MLA, two-algorithms section]).
  *
  *   q           bf16 [B, Sq, H, 576] contiguous (16-byte aligned)

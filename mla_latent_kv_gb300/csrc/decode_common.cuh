@@ -8,6 +8,10 @@
 namespace mla {
 namespace dec {
 
+// A running maximum before any score. Finite, so that the weight of a masked score (-inf) is
+// exp2(-inf) = 0 from the start and only that of a NaN score is NaN.
+constexpr float kNoMax = -3.402823466e38f;
+
 struct RowGeom {
     int r, b, t, j0, j1, npages, page0;
     int slot;  // partial-output slot, or -1: this unit writes the row's final output

@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1)
         float m[NH], l[NH], lt[NH];
 #pragma unroll
         for (int k = 0; k < NH; ++k) {
-            m[k] = -CUDART_INF_F;
+            m[k] = kNoMax;
             l[k] = lt[k] = 0.f;
         }
         // FP8: (k_scale, v_scale) of this thread's token, a page ahead; 0 where there is no token
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1)
                         const float mt = fmaxf(mx[h0 + k], mx[64 + h0 + k]) * sl2;  // scale > 0
                         float a = 1.f;
                         if (mt > m[k] + kRescaleThreshold) {
-                            a = fast_exp2(m[k] - mt);  // 0 while m = -inf
+                            a = fast_exp2(m[k] - mt);  // 0 the first time
                             m[k] = mt;
                         }
                         l[k] *= a;
@@ -432,8 +432,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1)
 #pragma unroll
                 for (int k = 0; k < NH; ++k) {
                     const int h = h0 + k;
-                    // a head past H keeps m = -inf: its weights are 0, not exp2(-inf + inf)
-                    const float e = m[k] == -CUDART_INF_F ? 0.f : fast_exp2(fmaf(__uint_as_float(s[k]), sl2, -m[k]));
+                    const float e = fast_exp2(fmaf(__uint_as_float(s[k]), sl2, -m[k]));
                     // V = codes * v_scale: the scale multiplies the weight before its one rounding, and
                     // both sums are of the unscaled weights
                     const uint32_t r = pack_bf16x2(kFp8 ? e * scale.y : e, 0.f) & 0xffffu;
@@ -475,7 +474,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1)
         named_bar(kBarWork, kWork);
         if (wtid < N) {
             const float lv = mx[wtid] + mx[64 + wtid], ltv = lts[wtid] + lts[64 + wtid];
-            const bool empty = !o_ok || !(lv > 0.f);
+            const bool empty = !o_ok || lv == 0.f;  // no token has a weight; a NaN sum is a NaN result
             alpha_s[wtid] = empty ? 0.f : 1.f / lv;
             if (wtid < p.H) {
                 const float lse = empty ? -CUDART_INF_F : (m_s[wtid] + log2f(ltv)) * 0.6931471805599453f;
@@ -505,7 +504,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1)
                 for (int k = 0; k < 16; ++k) {
                     const int h = hb + k;
                     const float inv = alpha_s[h];
-                    const float x = inv > 0.f ? __uint_as_float(v[k]) * inv : 0.f;  // an empty row: O may hold anything
+                    const float x = inv != 0.f ? __uint_as_float(v[k]) * inv : 0.f;  // an empty row: O may hold anything
                     if (h < p.H) {
                         if (f32)
                             of[(row + h) * kL + dim] = x;

@@ -362,7 +362,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const float sl2 = p.scale * 1.4426950408889634f;  // exp2 domain
             // Both sums are of the unscaled weights exp(s - m): v_scale only enters P as the MMA
             // sees it. Each half keeps its own sums (same running max); they are added at the end.
-            float m_run = -CUDART_INF_F, l_run = 0.f, lt_run = 0.f;
+            float m_run = kNoMax, l_run = 0.f, lt_run = 0.f;
             const uint32_t pbuf_remote = map_to_rank(sbase + OFF_PB, 1);
             const uint32_t pfull_remote = map_to_rank(bar(B_PFULL), 1);
             for (int gi = 0; gi < ngroups; ++gi) {
@@ -426,7 +426,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const bool resc = mt > m_run + kRescaleThreshold;
                 float alpha = 1.f;
                 if (resc) {
-                    alpha = fast_exp2(m_run - mt);  // 0 on the first group (m_run = -inf)
+                    alpha = fast_exp2(m_run - mt);  // 0 on the first group
                     m_run = mt;
                 }
                 l_run *= alpha;
@@ -741,7 +741,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const float l = reinterpret_cast<volatile float*>(smem + OFF_STAT_L)[row];
                 const float lt = reinterpret_cast<volatile float*>(smem + OFF_STAT_LT)[row];
                 const bool use_o = __all_sync(0xffffffffu, o_ok);
-                const bool empty = !use_o || !(l > 0.f);
+                const bool empty = !use_o || l == 0.f;  // no token has a weight; a NaN sum is a NaN result
                 const float inv = empty ? 0.f : 1.f / l;
                 const float lse_v = empty ? -CUDART_INF_F : (m + log2f(lt)) * 0.6931471805599453f;
                 const bool live = row < p.H;

@@ -603,7 +603,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             const float m = reinterpret_cast<volatile float*>(smem + OFF_STAT_M)[row];
             const float l = reinterpret_cast<volatile float*>(smem + OFF_STAT_L)[row];
             const bool use_o = __all_sync(0xffffffffu, o_ok);
-            const bool empty = !use_o || !(l > 0.f);
+            const bool empty = !use_o || l == 0.f;  // no token has a weight; a NaN sum is a NaN result
             const float inv = empty ? 0.f : 1.f / l;
             const int64_t flat = (int64_t)rows0 + row;
             if (eset == 0 && flat < p.flat_rows)

@@ -72,6 +72,8 @@ __device__ __forceinline__ void merge_item(const DecodeArgs& p, int64_t r, int h
                                                    : p.part_o + (((size_t)slot0 + (s - npre)) * p.H + h) * kL + dim);
     };
 
+    // A NaN state counts as the largest: its weight, the sum and the result are NaN then.
+    auto top = [](float a, float b) { return fmaxf(a, b != b ? CUDART_INF_F : b); };
     constexpr int kBatch = batch_of(kPre);
     float acc[8];
 #pragma unroll
@@ -110,10 +112,10 @@ __device__ __forceinline__ void merge_item(const DecodeArgs& p, int64_t r, int h
     if (total <= kBatch) {  // one batch: the maximum comes from the loads that are on their way anyway
         load(0);
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) M = fmaxf(M, ls[u]);
+        for (int u = 0; u < kBatch; ++u) M = top(M, ls[u]);
         add();
     } else {
-        for (int s = lane; s < total; s += 32) M = fmaxf(M, state_lse(s));
+        for (int s = lane; s < total; s += 32) M = top(M, state_lse(s));
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
         if (M != -CUDART_INF_F)
@@ -123,7 +125,7 @@ __device__ __forceinline__ void merge_item(const DecodeArgs& p, int64_t r, int h
                 add();
             }
     }
-    const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+    const float inv = wsum != 0.f ? 1.f / wsum : 0.f;
     const size_t base = ((size_t)r * p.H + h) * kL + half * (kL / 2) + lane * 8;
     if (p.o_dtype == MLA_DT_F32) {
         float4* dst = reinterpret_cast<float4*>((float*)p.o_latent + base);
@@ -135,7 +137,7 @@ __device__ __forceinline__ void merge_item(const DecodeArgs& p, int64_t r, int h
 #pragma unroll
         for (int i = 0; i < 4; ++i) dst[i] = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
     }
-    if (half == 0 && lane == 0 && p.lse) p.lse[(size_t)r * p.H + h] = wsum > 0.f ? M + __logf(wsum) : -CUDART_INF_F;
+    if (half == 0 && lane == 0 && p.lse) p.lse[(size_t)r * p.H + h] = wsum != 0.f ? M + __logf(wsum) : -CUDART_INF_F;
 }
 
 }  // namespace

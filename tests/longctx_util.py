@@ -116,6 +116,18 @@ def check_attention(o, lse, want, bf16_out=False):
         assert over <= 0, f"lse is {over} over its bound"
 
 
+def check_with_nan(o, lse, want):
+    """check_attention where the definition is finite, and NaN exactly where it is NaN. (Of a score of +inf
+    the definition's lse is +inf, the kernels' NaN.)"""
+    import torch
+    o_ref, lse_ref, tol_o, tol_lse = want
+    bad = lse_ref.isnan() | (lse_ref == math.inf)
+    assert torch.equal(o.isnan(), o_ref.isnan()) and torch.equal(lse.isnan(), bad)
+    z = lambda x, m: torch.where(m, torch.zeros_like(x), x)  # noqa: E731
+    check_attention(z(o, o.isnan()), z(lse, bad),
+                    (z(o_ref, o_ref.isnan()), z(lse_ref, bad), z(tol_o, o_ref.isnan()), z(tol_lse, bad)))
+
+
 def select_rule(scores, n, K, sink, local):
     """The selection's definition for one row: scores [width] (numpy), n visible tokens."""
     np_ = -(-n // PAGE)

@@ -5,7 +5,8 @@ import numpy as np
 import pytest
 
 import mla_inputs as mi
-from longctx_util import D, L, PAGE, attend, bf16, check_attention, dev, keys_values, paged_case, select_rule
+from longctx_util import (D, L, PAGE, attend, bf16, check_attention, check_with_nan, dev, keys_values, paged_case,
+                          select_rule)
 
 pytestmark = pytest.mark.gpu
 BF, F8 = mi.KV_BF16, mi.KV_FP8
@@ -258,6 +259,73 @@ def test_shared_prefix_workspace_is_checked():
     o, lse = _prefix(c, workspace=ws[:need])
     check_attention(o, lse, attend(c))
     assert bool((ws[need:] == 0xFF).all())
+
+
+# --------------------------------------------------------------------------- NaN in cached rows
+def _plant(c, b, token, what):
+    """Token `token` of request b holds NaN: one value of its row, or (FP8) its k_scale or v_scale. "inf" is
+    an infinite value in its row (bf16), "page" a NaN in every row of its page."""
+    import torch
+    blk = int(c["full_table"][b, token // PAGE])
+    rows = slice(None) if what == "page" else token % PAGE
+    if c["kv"] == BF:
+        c["cache"].view(torch.bfloat16).view(c["num_blocks"], PAGE, D)[blk, rows, 70] = \
+            math.inf if what == "inf" else math.nan
+    else:
+        sc = c["cache"].view(c["num_blocks"], PAGE, D + 8)[blk, rows, D:].view(torch.float32)
+        sc[..., 1 if what == "v" else 0] = math.nan
+
+
+_NAN = [(BF, 128, "row"), (BF, 128, "page"), (BF, 128, "inf"), (BF, 16, "row"), (BF, 16, "page"), (BF, 32, "inf"),
+        (F8, 128, "row"), (F8, 128, "page"), (F8, 128, "v"), (F8, 16, "row"), (F8, 16, "page"), (F8, 32, "v")]
+
+
+@pytest.mark.parametrize("kv,H,what", _NAN)
+@pytest.mark.parametrize("num_splits", [1, 3, 7, -2])
+def test_a_nan_key_is_a_nan_result(kv, H, what, num_splits):
+    """A row that sees a NaN key has a NaN result, whatever its split and its place; the others none."""
+    import mla_latent_kv_gb300 as mla
+    lens = [700, 700, 700, 64, 3, 700, 129]
+    c = paged_case(lens, 2, H, kv, seed=200)
+    for b, token in ((0, 0), (1, 300), (2, 699), (3, 1), (5, 639)):  # the third: seen by its last row only
+        _plant(c, b, token, what)
+    want = attend(c)
+    assert want[0].isnan().any()
+    o, lse = mla.decode(c["q"], c["cache"], c["table"], c["seq_lens"], c["max_len"], c["scale"], kv_dtype=kv,
+                        num_splits=num_splits, num_blocks=c["num_blocks"])
+    check_with_nan(o, lse, want)
+    lists, K = [], 6
+    table = np.full((len(lens), 2, K), -1, np.int32)
+    for b, n in enumerate(lens):
+        lists.append([])
+        for t in range(2):
+            total = -(-(n - (1 - t)) // PAGE)
+            ids = [p for p in (0, 2, 4, 9, 10) if p < total and not (b == 5 and p == 9)]
+            table[b, t, :len(ids)] = ids
+            lists[-1].append(ids)
+    o, lse = _sparse(c, table, num_splits)
+    check_with_nan(o, lse, attend(c, lists))
+
+
+@pytest.mark.parametrize("kv,H,what", _NAN)
+@pytest.mark.parametrize("B", [4, 160])
+def test_a_nan_key_in_the_shared_prefix(kv, H, what, B):
+    """Every request that sees it has a NaN result, also over many ranges; a NaN among one request's own
+    tokens stays with that request."""
+    c = paged_case([1024 + 1 + 11 * (b % 20) for b in range(B)], 1, H, kv, seed=201, prefix=1024)
+    assert H != 16 or _kernel(c) == (B == 160)
+    _plant(c, 1, 1024 + 5, what)
+    want = attend(c)
+    o, lse = _prefix(c)
+    check_with_nan(o, lse, want)
+    assert want[0][1].isnan().any() and not want[0][0].isnan().any()
+    for token in (0, 500, 1023):
+        c = paged_case([1024 + 1 + 11 * (b % 20) for b in range(B)], 1, H, kv, seed=202, prefix=1024)
+        _plant(c, 0, token, what)
+        want = attend(c)
+        o, lse = _prefix(c)
+        check_with_nan(o, lse, want)
+        assert want[0].isnan().any(-1).all()
 
 
 # ------------------------------------------------------------------------------------ page keys
