@@ -345,7 +345,9 @@ mla_status mla_decode_noalloc(const void* q, const void* kv_cache, mla_kv_dtype 
  * whole batch. The first prefix_len / 64 entries of every block_table row name the same pages;
  * only row 0's are used for the prefix, so the others may hold anything there. All prefix_len
  * tokens must have been written. A request with seq_lens[b] < prefix_len (an empty slot of a padded
- * batch, say) attends to its seq_lens[b] first prefix tokens only, 0 giving o = 0, lse = -inf.
+ * batch, say) attends to its seq_lens[b] first prefix tokens only, 0 giving o = 0, lse = -inf; what the
+ * others hold, NaN too, does not reach it. Such a request reads a part of its tokens by itself, so
+ * that many of them, not empty, make the call slower.
  *   prefix_len   a multiple of 64, 0 <= prefix_len <= max_blocks * 64; seq_lens counts it
  *   num_splits   as mla_decode, for the part of each request behind the prefix; how the prefix
  *                itself is divided over the device is the library's choice

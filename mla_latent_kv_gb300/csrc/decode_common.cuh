@@ -30,8 +30,11 @@ __device__ __forceinline__ RowGeom row_geometry(const DecodeArgs& p, int unit, b
         g.slot = u.w;
     } else {  // uniform splits: unit = row * S + split
         const int S = p.num_splits;
+        int base;
         g.r = unit / S;
-        split_range(visible_tokens(p, g.r, report), S, unit % S, &g.j0, &g.j1);
+        split_range(visible_tokens(p, g.r, report, &base), S, unit % S, &g.j0, &g.j1);
+        g.j0 += base;
+        g.j1 += base;
         g.slot = S > 1 || p.all_partial ? unit : -1;
     }
     int q_len;
@@ -41,8 +44,8 @@ __device__ __forceinline__ RowGeom row_geometry(const DecodeArgs& p, int unit, b
     return g;
 }
 
-// Physical block of page `pg` (counted from the base) of request b, or -1 (reported as MLA_DEV_BAD_BLOCK_ID) if the
-// block-table entry is outside the cache.
+// Physical block of page `pg` of request b, or -1 (reported as MLA_DEV_BAD_BLOCK_ID) if the block-table
+// entry is outside the cache.
 __device__ __forceinline__ int page_block(const DecodeArgs& p, int b, int pg) {
     const int32_t blk = *table_entry(p, b, pg);
     if (blk < 0 || (int64_t)blk >= p.num_blocks) {

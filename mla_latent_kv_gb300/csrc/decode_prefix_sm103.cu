@@ -330,15 +330,17 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             const int row = 32 * (warp & 3) + lane;
             const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
             float* mx = reinterpret_cast<float*>(smem + OFF_MX);
-            // Tokens of this unit that the row may see (rows past the batch see all: never stored).
-            int lim = INT32_MAX;
+            // Whether the row sees all of this unit's tokens (rows past the batch: never stored). If not it
+            // takes none of them here, and the decode of its own tokens starts with this range: a weight
+            // of 0 would not keep what its unseen tokens hold out of the sum, should that be NaN.
+            bool sees = true;
             const int64_t flat = (int64_t)rows0 + row;
             if (flat < p.flat_rows) {
                 const int r = (int)(flat / p.H), b = r / p.Sq, t = r % p.Sq;
                 const int seq = min(max(p.seq_lens[b], 0), p.max_seq_len);
-                lim = max(0, seq - (p.Sq - 1 - t)) - page0 * kPage;
+                sees = seq - (p.Sq - 1 - t) >= (page0 + npages) * kPage;
             }
-            const int warp_lim = __reduce_min_sync(0xffffffffu, lim);
+            const bool all_see = __all_sync(0xffffffffu, sees);
             if (npages > 0) {
                 // Q latent dims: this quarter moves panels 2 quarter and 2 quarter + 1 into TMEM
                 const bool okq = warp_wait(bar(B_QFULL), 0, abort, ds);
@@ -404,17 +406,17 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) vs[j] = src[j];
                 }
-                // No row of the warp sees any of these tokens (an empty slot's heads): no weights to compute.
+                // No row of the warp sees these tokens (an empty slot's heads): no weights to compute.
                 // Masked like any other, three empty slots of 64 made their clusters the last to end, by 8 us
                 // of 63. (Not with scales: it spills there, 265 against 249 us a call.)
                 bool dead = false;
-                if (page >= npages || warp_lim < (page + 1) * kPage) {  // some row does not see all of the page
-                    const int v = page >= npages ? 0 : lim - page * kPage - 32 * sub;
-                    if constexpr (!kScaled) dead = __all_sync(0xffffffffu, v <= 0);
+                if (page >= npages || !all_see) {
+                    const bool none = page >= npages || !sees;
+                    if constexpr (!kScaled) dead = __all_sync(0xffffffffu, none);
                     if (!dead) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (j >= v) s[j] = __float_as_uint(-CUDART_INF_F);
+                            if (none) s[j] = __float_as_uint(-CUDART_INF_F);
                     }
                 }
                 float lm = -CUDART_INF_F;

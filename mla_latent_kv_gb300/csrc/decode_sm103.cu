@@ -170,14 +170,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int unit = (int)(blockIdx.x >> 1);
     // The first split of a row starts at page 0 whatever the row's length, so the K producer
     // fetches the first group's block-table entries while the length is still on its way
-    // (validated once the page count is known).
+    // (validated once the page count is known). Behind a prefix that is the page after it, unless the row
+    // turns out to end inside the prefix.
     int blk_early[kPPG] = {-1, -1, -1, -1};
     const bool early_blocks = p.plan_units == nullptr && p.qsl == nullptr && unit % p.num_splits == 0;
     auto fetch_blocks = [&]() {
         if (!early_blocks || tid != 0 || rank != 0) return;
 #pragma unroll
         for (int q = 0; q < kPPG; ++q)
-            if (p.base / kPage + q < p.max_blocks) blk_early[q] = ld_s32(table_entry(p, unit / p.num_splits / p.Sq, q));
+            if (p.base / kPage + q < p.max_blocks)
+                blk_early[q] = ld_s32(table_entry(p, unit / p.num_splits / p.Sq, p.base / kPage + q));
     };
     if (p.order != kOrderWaitFirst) fetch_blocks();
     RowGeom g{};
@@ -244,7 +246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int np = min(kPPG, npages - kPPG * gi);
                     for (int q = 0; q < np; ++q) {
                         int blk;
-                        if (gi == 0 && early_blocks) {  // the entry fetched early: same checks as page_block
+                        if (gi == 0 && early_blocks && g.page0 == p.base / kPage) {  // the entry fetched early: same checks as page_block
                             blk = blk_early[q];
                             if (blk < 0 || (int64_t)blk >= p.num_blocks) {
                                 if (p.dev_status) atomicOr(p.dev_status, MLA_DEV_BAD_BLOCK_ID);

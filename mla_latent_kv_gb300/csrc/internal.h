@@ -40,7 +40,8 @@ struct DecodeArgs {
     float scale;
     int num_splits;             // resolved, >= 1
     int shared_pages;           // the first pages of every request are those of block_table's row 0
-    int base;                   // tokens (whole pages) at the front of every request that are left out
+    int base;                   // tokens (whole pages) at the front of every request that are left out;
+    int base_step;              // a row that sees only a part of them leaves out whole multiples of this
     int all_partial;            // every unit writes a partial state, also the only one of its row
     int order;                  // kOrder*: what the kernel may read before the preceding one ends
     const float* pre_o;         // partial states of every row over the base tokens, merged with the
@@ -84,10 +85,11 @@ __device__ __forceinline__ void row_request(const DecodeArgs& p, int r, int* b, 
     *q_len = p.qsl[lo + 1] - p.qsl[lo];
 }
 
-// Visible tokens of query row r past the base: seq_len - (q_len - 1 - t) - base, clamped at 0, with seq_len clamped
-// to what the block table can hold; an out-of-range seq_len sets
-// MLA_DEV_SEQ_TOO_LONG when `report`.
-__device__ __forceinline__ int visible_tokens(const DecodeArgs& p, int r, bool report) {
+// Visible tokens of query row r past its base, and that base in *base: the row sees
+// n = seq_len - (q_len - 1 - t) tokens, clamped at 0, with seq_len clamped to what the block table can
+// hold, and leaves out the first p.base of them or, if it sees fewer, the ranges of base_step tokens that
+// it sees whole. An out-of-range seq_len sets MLA_DEV_SEQ_TOO_LONG when `report`.
+__device__ __forceinline__ int visible_tokens(const DecodeArgs& p, int r, bool report, int* base) {
     int b, t, q_len;
     row_request(p, r, &b, &t, &q_len);
     int seq = p.seq_lens[b];
@@ -96,13 +98,13 @@ __device__ __forceinline__ int visible_tokens(const DecodeArgs& p, int r, bool r
         if (report && p.dev_status) atomicOr(p.dev_status, MLA_DEV_SEQ_TOO_LONG);
         seq = seq < 0 ? 0 : (seq > cap ? cap : seq);
     }
-    const int n = seq - (q_len - 1 - t) - p.base;
-    return n < 0 ? 0 : n;
+    const int n = max(0, seq - (q_len - 1 - t));
+    *base = n >= p.base ? p.base : n / p.base_step * p.base_step;
+    return n - *base;
 }
 
-// The block-table entry of page `pg` (counted from the base) of request b.
-__device__ __forceinline__ const int32_t* table_entry(const DecodeArgs& p, int b, int pg) {
-    const int page = p.base / MLA_PAGE_SIZE + pg;
+// The block-table entry of page `page` of request b.
+__device__ __forceinline__ const int32_t* table_entry(const DecodeArgs& p, int b, int page) {
     return p.block_table + (page < p.shared_pages ? (size_t)page : (size_t)b * p.max_blocks + page);
 }
 
@@ -209,7 +211,7 @@ struct DecodeExtra {
     bool few = false;                // the kernel for few heads, one SM a unit, see below
     bool check_only = false;         // return after the argument checks that need no device
     int shared_pages = 0;            // see DecodeArgs
-    int base = 0;
+    int base = 0, base_step = 0;
     bool all_partial = false;
     int order = kOrderDefault;
     // launched between the schedule and the decode (null: nothing); its error ends the call

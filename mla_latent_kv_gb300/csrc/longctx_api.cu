@@ -123,7 +123,7 @@ bool prefix_pays(bool fp8, int rows, int H, int pages, int own_pages, int cluste
 bool plan_prefix(mla_kv_dtype kv, int rows, int H, int prefix_len, int num_splits, int max_seq_len, PrefixPlan* w) {
     // tokens past max_seq_len are no request's
     const int seen = (max_seq_len + mla::kPage - 1) / mla::kPage;
-    const int pages = std::min(prefix_len / mla::kPage, seen);
+    const int pages = std::min(prefix_len, max_seq_len) / mla::kPage;
     const int64_t flat = (int64_t)rows * H;
     const bool fp8 = kv == MLA_KV_FP8_E4M3_SCALED;
     if (pages > 0) {
@@ -406,6 +406,7 @@ mla_status mla_decode_shared_prefix(const void* q, const void* kv_cache, mla_kv_
         a.part_lse = (float*)(ws + w.part_lse);
         a.dev_status = dev_status;
         x.base = w.pages * mla::kPage;
+        x.base_step = w.pages_per_split * mla::kPage;
         x.all_partial = true;
         // The prefix kernel goes between the schedule and the decode of the requests' own tokens. It
         // lets that one start once all of its clusters run, which is after everything ahead of this

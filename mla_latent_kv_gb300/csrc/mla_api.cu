@@ -294,6 +294,7 @@ mla_status decode_impl(const void* q, const void* kv_cache, mla_kv_dtype kv_dtyp
     a.num_splits = planned ? 1 : S;
     a.shared_pages = x.shared_pages;
     a.base = x.base;
+    a.base_step = x.base_step;
     a.all_partial = x.all_partial ? 1 : 0;
     a.order = x.order;
     a.pre_o = x.pre_o;

@@ -70,12 +70,16 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(DecodeArgs p, int pairs)
     unsigned long long tot = 0;
     int mx = 0;
     for (int r = r0; r < r1; ++r) {
-        const int n = visible_tokens(p, r, true);
+        int base;
+        const int n = visible_tokens(p, r, true, &base);
         if (r < kSmemRows) s_n[r] = n;
         tot += (unsigned long long)pages_of(n);
         mx = max(mx, pages_of(n));
     }
-    auto tokens = [&](int r) { return r < kSmemRows ? s_n[r] : visible_tokens(p, r, false); };
+    auto tokens = [&](int r) {
+        int base;
+        return r < kSmemRows ? s_n[r] : visible_tokens(p, r, false, &base);
+    };
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, off);
     mx = (int)__reduce_max_sync(0xffffffffu, (unsigned)mx);
@@ -229,15 +233,17 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(DecodeArgs p, int pairs)
         const int n = tokens(r);
         const int pg = pages_of(n);
         const int S = units_of(pg, c);
+        int at = 0;  // the row's first token here
+        if (p.base > 0) visible_tokens(p, r, false, &at);
         if (S == 1 && p.all_partial) {  // its one unit writes a partial state like the others
             const int slot = base[kBuckets + 1]++;
-            units[base[bucket_of(pg, c)]++] = make_int4(r, 0, n, slot);
+            units[base[bucket_of(pg, c)]++] = make_int4(r, at, at + n, slot);
             rows[r] = make_int2(slot, 1);
             split_rows[base[kBuckets]++] = r;
             continue;
         }
         if (S == 1) {
-            units[base[bucket_of(pg, c)]++] = make_int4(r, 0, n, -1);
+            units[base[bucket_of(pg, c)]++] = make_int4(r, at, at + n, -1);
             rows[r] = make_int2(-1, 1);
             continue;
         }
@@ -251,7 +257,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(DecodeArgs p, int pairs)
                 split_range(n, S, k, &j0, &j1);
             }
             const int b = rem && k == S - 1 ? bucket_of(pg - (S - 1) * c, c) : 0;
-            units[base[b]++] = make_int4(r, j0, j1, slot0 + k);
+            units[base[b]++] = make_int4(r, at + j0, at + j1, slot0 + k);
         }
         rows[r] = make_int2(slot0, S);
         split_rows[base[kBuckets]++] = r;

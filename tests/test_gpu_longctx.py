@@ -328,6 +328,25 @@ def test_a_nan_key_in_the_shared_prefix(kv, H, what, B):
         assert want[0].isnan().any(-1).all()
 
 
+@pytest.mark.parametrize("kv,H,what", _NAN)
+@pytest.mark.parametrize("B,prefix,num_splits", [(10, 640, -1), (160, 960, -1), (160, 960, 1), (160, 960, 3), (160, 960, -2),
+                                                 (40, 8192, -1), (40, 8192, -2)])
+def test_nan_in_the_prefix_past_a_request_that_ends_inside_it(kv, H, what, B, prefix, num_splits):
+    """Requests that see only a part of the prefix are not touched by what its other tokens hold."""
+    lens = [(prefix + 70, 0, 1, 2, 64, 301, 302, 303, 512, prefix - 1, prefix, prefix + 1, 600)[b % 13] for b in range(B)]
+    c = paged_case(lens, 2, H, kv, seed=203, prefix=prefix)
+    assert H != 16 or _kernel(c, num_splits) == (B > 10)
+    _plant(c, 0, 301, what)
+    _plant(c, 0, prefix - 1, what)
+    want = attend(c)
+    st = _status()
+    o, lse = _prefix(c, num_splits, st)
+    assert int(st.item()) == 0
+    check_with_nan(o, lse, want)
+    touched = want[0].isnan().view(B, -1).any(1).tolist()
+    assert touched[:5] == [True, False, False, False, False] and touched[6]  # length 302: it sees the first one
+
+
 # ------------------------------------------------------------------------------------ page keys
 @pytest.mark.parametrize("kv", [BF, F8])
 @pytest.mark.parametrize("lens,starts", [
