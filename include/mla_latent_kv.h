@@ -101,8 +101,8 @@ mla_status mla_selftest_wait_timeout(int32_t* dev_status, int32_t* out, mla_stre
  * every code c = 0..255, the bf16 bits the kernel produces for it.
  *   out   device uint16[256], caller-owned
  * Every finite code's value is a bf16 value, and the kernel must produce it exactly (subnormal
- * codes included); the two NaN codes 0x7F and 0xFF, which mla_cache_write never stores (it
- * saturates), come out as +480 and -480. Asynchronous on `stream`. MLA_ERR_INVALID_ARG if out is
+ * codes included); the two NaN codes 0x7F and 0xFF, which mla_cache_write stores for no number (it
+ * saturates), come out as +480 and -480, in every decode call and in mla_page_keys. Asynchronous on `stream`. MLA_ERR_INVALID_ARG if out is
  * NULL, MLA_ERR_CUDA if the launch fails. */
 mla_status mla_selftest_e4m3_widen(uint16_t* out, mla_stream_t stream);
 

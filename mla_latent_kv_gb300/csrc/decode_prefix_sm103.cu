@@ -645,9 +645,10 @@ __global__ void __launch_bounds__(256) prefix_widen_kernel(PrefixArgs p, const u
         if (c >= kD / 8) continue;
         uint2 v = make_uint2(0u, 0u);
         if (!bad) v = *reinterpret_cast<const uint2*>(src + 8 * c);
-        *reinterpret_cast<uint4*>(x + (size_t)token * kD + 8 * c) =
-            make_uint4(e4m3x2_to_bf16x2(v.x & 0xffffu), e4m3x2_to_bf16x2(v.x >> 16), e4m3x2_to_bf16x2(v.y & 0xffffu),
-                       e4m3x2_to_bf16x2(v.y >> 16));
+        uint4 w;  // as the decode kernels read the codes
+        e4m3x4_to_bf16x4(v.x, w.x, w.y);
+        e4m3x4_to_bf16x4(v.y, w.z, w.w);
+        *reinterpret_cast<uint4*>(x + (size_t)token * kD + 8 * c) = w;
     }
     if (lane == 0) {
         const float2 sc = bad ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2*>(src + kD);

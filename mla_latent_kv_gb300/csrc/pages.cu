@@ -65,13 +65,14 @@ __global__ void __launch_bounds__(kKeyThreads) page_keys_kernel(PageKeysArgs p) 
         }
 #pragma unroll
         for (int i = 0; i < kRowsPer; ++i) {
-            const uint32_t w[4] = {v[i].x & 0xffffu, v[i].x >> 16, v[i].y & 0xffffu, v[i].y >> 16};
+            uint32_t h[4];  // as the decode kernels read the codes
+            ptx::e4m3x4_to_bf16x4(v[i].x, h[0], h[1]);
+            ptx::e4m3x4_to_bf16x4(v[i].y, h[2], h[3]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint32_t h = ptx::e4m3x2_to_bf16x2(w[j]);
                 if (row0 + i < valid) {
-                    acc[2 * j] += ptx::bf16_lo_f(h) * ks[i];
-                    acc[2 * j + 1] += ptx::bf16_hi_f(h) * ks[i];
+                    acc[2 * j] += ptx::bf16_lo_f(h[j]) * ks[i];
+                    acc[2 * j + 1] += ptx::bf16_hi_f(h[j]) * ks[i];
                 }
             }
         }

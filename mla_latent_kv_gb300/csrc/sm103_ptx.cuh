@@ -523,8 +523,8 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two_bytes) {
 // is a quarter of the arithmetic pipes'). A code's magnitude bits eeee.mmm placed at bits 4-10 of a
 // bf16 are that bf16's exponent and leading mantissa bits, so the bf16 reads as the code's value
 // times 2^-120 -- for e = 0 as a bf16 subnormal, which is exactly the e4m3 subnormal m/8 * 2^-6
-// times 2^-120. One exact bf16 multiply by 2^120 restores the value. The two e4m3 NaN codes (never
-// written by the cache writer, which saturates) come out as +-480.
+// times 2^-120. One exact bf16 multiply by 2^120 restores the value. The two e4m3 NaN codes (written
+// for no number: the cache writer saturates) come out as +-480.
 __device__ __forceinline__ void e4m3x4_to_bf16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
     constexpr uint32_t kTwoPow120 = 0x7B807B80u;  // bf16x2 (2^120, 2^120)
     const uint32_t a = __byte_perm(w, 0u, 0x1404);  // [0, code0, 0, code1]

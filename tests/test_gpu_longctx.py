@@ -347,6 +347,40 @@ def test_nan_in_the_prefix_past_a_request_that_ends_inside_it(kv, H, what, B, pr
     assert touched[:5] == [True, False, False, False, False] and touched[6]  # length 302: it sees the first one
 
 
+@pytest.mark.parametrize("H", [16, 128])
+@pytest.mark.parametrize("B", [4, 160])
+def test_nan_codes_read_alike_everywhere(H, B, monkeypatch):
+    """The e4m3 codes 0x7F and 0xFF, which the cache writer stores for no number, read +-480 in the decode
+    kernels: so they do in a shared prefix, whichever kernel reads it, and in the page keys."""
+    import torch
+    import longctx_util
+    import mla_latent_kv_gb300 as mla
+    c = paged_case([1024 + 30 + b % 100 for b in range(B)], 1, H, F8, seed=204, prefix=1024)
+    assert H != 16 or _kernel(c) == (B > 4)
+    raw = c["cache"].view(c["num_blocks"], PAGE, D + 8)
+    for page, row, dim, code in ((0, 3, 7, 0x7F), (5, 63, 511, 0xFF), (15, 0, 570, 0x7F), (16, 1, 100, 0xFF)):
+        raw[int(c["full_table"][0, page]), row, dim] = code
+
+    def read_480(case):
+        r = case["cache"].view(case["num_blocks"], PAGE, D + 8)
+        code = r[..., :D].contiguous()
+        x = code.view(torch.float8_e4m3fn).double()
+        x = torch.where(x.isnan(), torch.where(code > 127, -480.0, 480.0), x)
+        sc = r[..., D:].contiguous().view(torch.float32).double()
+        return x * sc[..., :1], x[..., :L] * sc[..., 1:]
+
+    monkeypatch.setattr(longctx_util, "keys_values", read_480)
+    o, lse = _prefix(c)
+    check_attention(o, lse, attend(c))
+    keys = mla.page_keys(c["cache"], dev(c["full_table"]), c["seq_lens"], c["max_len"], kv_dtype=F8,
+                         num_blocks=c["num_blocks"])
+    for page in (0, 5, 15, 16):
+        blk = int(c["full_table"][0, page])
+        rows = read_480(c)[0][blk, :min(PAGE, int(c["lens"][0]) - page * PAGE)]
+        tol = 2.0 ** -8 * rows.mean(0).abs() + 66 * 2.0 ** -24 * rows.abs().mean(0)
+        assert bool(((keys[blk].double() - rows.mean(0)).abs() <= tol).all()), page
+
+
 # ------------------------------------------------------------------------------------ page keys
 @pytest.mark.parametrize("kv", [BF, F8])
 @pytest.mark.parametrize("lens,starts", [
