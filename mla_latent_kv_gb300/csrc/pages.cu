@@ -202,8 +202,7 @@ __global__ void __launch_bounds__(1024) select_pages_kernel(SelectArgs p) {
         }
         const uint32_t differ = all_and ^ all_or;
         const int top = differ ? 31 - __clz(differ) : -1;  // the highest bit in which two keys differ
-        T = top < 31 ? all_and & ~((2u << top) - 1u) : 0u;  // what is above it
-        if (top < 0) T = all_and;
+        T = differ ? all_and & ~(0xffffffffu >> __clz(differ)) : all_and;  // what is above it
         for (int bit = top; bit >= 0; --bit) {
             const uint32_t trial = T | (1u << bit);
             int c = 0;
