@@ -433,6 +433,15 @@ def _raw_stream(stream, t, *others):
     return _C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+def _check_status(t):
+    """Refuse a dev_status that is not int32 with an element: the kernels OR bits into its first word."""
+    if t is None:
+        return
+    import torch
+    if t.dtype is not torch.int32 or t.numel() < 1:
+        raise ValueError(f"dev_status must be an int32 tensor of at least one element, got {t.dtype} {tuple(t.shape)}")
+
+
 def _page_args(q, block_table, seq_lens):
     """Checks of the query, block table and lengths -> (B, Sq, H)."""
     import torch
@@ -501,6 +510,7 @@ def decode_shared_prefix(q, kv_cache, block_table, seq_lens, max_seq_len, prefix
     if stream is not None and (o_latent is None or lse is None or (need and workspace is None)):
         return _on(stream, "decode_shared_prefix", locals())
     o_latent, o_dtype, lse, workspace, ws_bytes = _attention_bufs(q, B, Sq, H, o_latent, o_dtype, lse, workspace, need)
+    _check_status(dev_status)
     s = _raw_stream(stream, q, kv_cache, block_table, seq_lens, o_latent, lse, workspace, dev_status)
     _check(l.mla_decode_shared_prefix(q.data_ptr(), kv_cache.data_ptr(), kv_dtype, nb, block_table.data_ptr(),
                                       block_table.shape[1], seq_lens.data_ptr(), int(max_seq_len), int(prefix_len), B,
@@ -526,6 +536,7 @@ def page_keys(kv_cache, block_table, seq_lens, max_new_len, kv_dtype=KV_BF16, st
     if page_keys is None:
         page_keys = torch.zeros((nb, D), dtype=torch.bfloat16, device=kv_cache.device)
     _is_shape("page_keys", page_keys, torch.bfloat16, (nb, D))
+    _check_status(dev_status)
     s = _raw_stream(stream, kv_cache, block_table, start_lens, seq_lens, page_keys, dev_status)
     _check(lib().mla_page_keys(kv_cache.data_ptr(), kv_dtype, nb, block_table.data_ptr(), max_blocks, _a(start_lens),
                                seq_lens.data_ptr(), int(max_new_len), B, page_keys.data_ptr(), _a(dev_status), s))
@@ -544,6 +555,7 @@ def page_scores(q, page_keys, block_table, seq_lens, max_seq_len, scale, scores=
     if scores is None:
         scores = torch.empty((B, Sq, width), dtype=torch.float32, device=q.device)
     _is_shape("scores", scores, torch.float32, (B, Sq, width))
+    _check_status(dev_status)
     s = _raw_stream(stream, q, page_keys, block_table, seq_lens, scores, dev_status)
     _check(lib().mla_page_scores(q.data_ptr(), page_keys.data_ptr(), page_keys.shape[0], block_table.data_ptr(),
                                  block_table.shape[1], seq_lens.data_ptr(), int(max_seq_len), B, Sq, H, float(scale),
@@ -571,6 +583,7 @@ def select_pages(scores, seq_lens, max_sel, sink_pages=1, local_pages=1, pages=N
     if pages is None:
         pages = torch.empty((B, Sq, max_sel), dtype=torch.int32, device=scores.device)
     _is_shape("pages", pages, torch.int32, (B, Sq, max_sel))
+    _check_status(dev_status)
     s = _raw_stream(stream, scores, seq_lens, pages, dev_status)
     _check(lib().mla_select_pages(scores.data_ptr(), stride, width, seq_lens.data_ptr(), B, Sq, int(max_sel),
                                   int(sink_pages), int(local_pages), pages.data_ptr(), _a(dev_status), s))
@@ -598,6 +611,7 @@ def decode_sparse(q, kv_cache, block_table, seq_lens, pages, scale, kv_dtype=KV_
     if stream is not None and (o_latent is None or lse is None or (need and workspace is None)):
         return _on(stream, "decode_sparse", locals())
     o_latent, o_dtype, lse, workspace, ws_bytes = _attention_bufs(q, B, Sq, H, o_latent, o_dtype, lse, workspace, need)
+    _check_status(dev_status)
     s = _raw_stream(stream, q, kv_cache, block_table, seq_lens, pages, o_latent, lse, workspace, dev_status)
     _check(l.mla_decode_sparse(q.data_ptr(), kv_cache.data_ptr(), kv_dtype, nb, block_table.data_ptr(),
                                block_table.shape[1], seq_lens.data_ptr(), pages.data_ptr(), K, B, Sq, H, float(scale),

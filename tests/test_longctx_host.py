@@ -136,6 +136,24 @@ def test_binding_refuses_wrong_tensors():
         mla.select_pages(torch.zeros(2, 1, 8), seq, 4)  # not on the device
 
 
+def test_binding_refuses_a_status_word_of_another_type():
+    """The kernels OR bits into four bytes: one byte, another type or nothing at all is refused."""
+    torch = pytest.importorskip("torch")
+    i32, bf = torch.int32, torch.bfloat16
+    q, cache = torch.zeros(2, 1, 16, 576, dtype=bf), torch.zeros(8, 64 * 1152, dtype=torch.uint8)
+    table, seq = torch.zeros(2, 4, dtype=i32), torch.zeros(2, dtype=i32)
+    keys, scores, pages = torch.zeros(8, 576, dtype=bf), torch.zeros(2, 1, 4), torch.zeros(2, 1, 2, dtype=i32)
+    bufs = dict(o_latent=torch.zeros(2, 1, 16, 512), lse=torch.zeros(2, 1, 16), workspace=torch.zeros(4096, dtype=torch.uint8))
+    for st in (torch.zeros(1, dtype=torch.uint8), torch.zeros(1, dtype=torch.int64), torch.zeros(1), torch.zeros(0, dtype=i32)):
+        for call in (lambda: mla.decode_shared_prefix(q, cache, table, seq, 100, 64, 0.07, dev_status=st, **bufs),
+                     lambda: mla.page_keys(cache, table, seq, 100, page_keys=keys, dev_status=st),
+                     lambda: mla.page_scores(q, keys, table, seq, 256, 0.07, scores=scores, dev_status=st),
+                     lambda: mla.select_pages(scores, seq, 2, pages=pages, dev_status=st),
+                     lambda: mla.decode_sparse(q, cache, table, seq, pages, 0.07, dev_status=st, **bufs)):
+            with pytest.raises(ValueError, match="dev_status"):
+                call()
+
+
 class _FakeLib:
     """Stands for the native library: sizes are 4096 bytes, every call succeeds and launches nothing."""
 
