@@ -230,9 +230,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ============================== scores CTA ==============================
         if (warp == 0) {
             if (lane == 0 && npages > 0) {
-                // raw K triples: group gi, triple t -> ring slot (3 gi + t) % kRawSlots; the cache
-                // is never written by this library's kernels, so the loads start before the
-                // preceding kernel has finished; Q (that kernel's output) waits for it
+                // raw K triples: group gi, triple t -> ring slot (3 gi + t) % kRawSlots; the kernel
+                // ahead does not write the cache (cache_write lets nothing start early), so the
+                // loads start before it has finished; Q (that kernel's output) waits for it
                 tma_prefetch_desc(&q_map);
                 tma_prefetch_desc(&raw_map);
                 bool q_issued = false;

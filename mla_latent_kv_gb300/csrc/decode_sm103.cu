@@ -234,7 +234,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (lane == 0 && npages > 0) {
                 tma_prefetch_desc(&kv_map);
                 // The K panels go out before the preceding kernel (which may be writing q) has
-                // finished: no kernel of this library writes the cache. CTA 1 prefetches the
+                // finished: it does not write the cache (cache_write, which does, lets nothing start
+                // before it has ended). CTA 1 prefetches the
                 // pages into L2 ahead of these loads, with plain prefetch instructions: bulk
                 // prefetches issued here would queue in this SM's TMA unit, the narrow point of
                 // the K stream.

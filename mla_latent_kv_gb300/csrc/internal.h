@@ -17,9 +17,9 @@ constexpr int kPage = MLA_PAGE_SIZE;  // 64 tokens per page
 constexpr int kBf16RowBytes = 2 * kD; // 1152
 constexpr int kFp8RowBytes = kD + 8;  // 584
 
-// What a decode kernel may read before the kernel ahead of it in the stream has ended: weights, cache
-// and block table (the default: kernels of the library write none of them; q and a device-built
-// schedule wait), nothing (the one ahead writes the lengths and the block table), or everything
+// What a decode kernel may read before the kernel ahead of it in the stream has ended: cache, block
+// table and lengths (the default: no kernel of the library that signals early writes them; q and a
+// device-built schedule wait), nothing (the one ahead writes the lengths and the block table), or everything
 // (the one ahead began only after all before it had ended, and writes nothing that is read here:
 // the second of two kernels that run side by side).
 enum { kOrderDefault = 0, kOrderWaitFirst = 1, kOrderFree = 2 };

@@ -121,7 +121,7 @@ bool prefix_pays(bool fp8, int rows, int H, int pages, int own_pages, int cluste
 }
 
 bool plan_prefix(mla_kv_dtype kv, int rows, int H, int prefix_len, int num_splits, int max_seq_len, PrefixPlan* w) {
-    // tokens past max_seq_len are no request's
+    // tokens past max_seq_len are no request's; a page that it cuts is left to the requests' own tokens
     const int seen = (max_seq_len + mla::kPage - 1) / mla::kPage;
     const int pages = std::min(prefix_len, max_seq_len) / mla::kPage;
     const int64_t flat = (int64_t)rows * H;

@@ -177,10 +177,10 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
 
 // ------------------------------------------------------------------------------------------
 // Programmatic dependent launch. A kernel of this library signals at its start that the next
-// kernel in the stream may be scheduled; that kernel does its setup and loads only data no
-// kernel of this library writes (weights, KV cache pages, block table), then waits here for
-// the preceding grid to complete (and its memory to be visible) before it reads anything else
-// or writes anything at all.
+// kernel in the stream may be scheduled; that kernel does its setup and loads only data that no
+// kernel it may overtake writes (weights, KV cache pages, block table, lengths: cache_write does
+// not signal, and a decode of selected pages waits first), then waits here for the preceding grid
+// to complete (and its memory to be visible) before it reads anything else or writes anything at all.
 // ------------------------------------------------------------------------------------------
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch_dependents() {
