@@ -96,6 +96,20 @@ def test_shared_prefix_every_slot_empty_and_no_prefix(kv):
 
 
 @pytest.mark.parametrize("kv", [BF, F8])
+@pytest.mark.parametrize("H", [16, 40])
+@pytest.mark.parametrize("num_splits", [-1, 1, 3, -2])
+def test_shared_prefix_longer_than_the_bound(kv, H, num_splits):
+    """A bound on the lengths that ends inside a page of the prefix: that page is read by each request itself."""
+    lens = [(1800, 1792, 1799, 0, 1728, 65, 1, 1793)[b % 8] for b in range(160)]
+    c = paged_case(lens, 2, H, kv, seed=24, prefix=2560)
+    assert c["max_len"] == 1800 and _kernel(c, num_splits)
+    st = _status()
+    o, lse = _prefix(c, num_splits, st)
+    assert int(st.item()) == 0
+    check_attention(o, lse, attend(c))
+
+
+@pytest.mark.parametrize("kv", [BF, F8])
 @pytest.mark.parametrize("num_splits", [1, 2, -2])
 def test_shared_prefix_no_tokens_of_their_own(kv, num_splits):
     """Nothing behind the prefix in any request: the prefix's states alone make the result."""
