@@ -79,6 +79,9 @@ typedef enum { MLA_DT_F32 = 0, MLA_DT_BF16 = 1 } mla_dtype;
 #define MLA_DEV_WAIT_TIMEOUT 0x4 /* a bounded pipeline wait expired; outputs are invalid */
 #define MLA_DEV_BAD_SLOT 0x8     /* mla_cache_write: a slot at or beyond num_blocks * 64 (skipped) */
 #define MLA_DEV_BAD_PAGE 0x10    /* mla_decode_sparse: a selected page out of order or out of range (skipped) */
+#define MLA_DEV_BAD_BRANCH 0x20  /* mla_accept_tokens: a path out of order or out of range (cut there) */
+#define MLA_DEV_BAD_PARENT 0x40  /* mla_fork_pages: a parent outside [-1, B) (nothing done) */
+#define MLA_DEV_NO_PAGES 0x80    /* mla_fork_pages: fewer free pages than the new rows need (nothing done) */
 
 /* Human-readable name of a status. Never NULL. */
 const char* mla_status_string(mla_status s);
@@ -441,6 +444,130 @@ mla_status mla_decode_sparse(const void* q, const void* kv_cache, mla_kv_dtype k
                              int max_sel, int B, int Sq, int H, float scale, int num_splits, void* workspace,
                              size_t workspace_bytes, void* o_latent, mla_dtype o_dtype, float* lse,
                              int32_t* dev_status, mla_stream_t stream);
+
+/*
+ * A step with drafted tokens: rotary positions (alone, or with the cache write), attention of a tree of
+ * drafts, the accepted branch's rows moved together, and the pages of the requests that go on. All of them
+ * work from device memory, so that a step needs no host decision and can be captured.
+ *
+ * mla_rope_frequencies: radians per position of the 32 pairs of a rope part, inv_freq[i] = base^(-2 i / 64),
+ * for longer contexts than a model was trained on scaled as YaRN does: pairs that make at least beta_fast
+ * turns over the trained positions keep their frequency, those that make at most beta_slow turns get 1 / factor
+ * of it, the ones between a share of both that is linear in i,
+ *     pair(n) = 64 ln(trained / (2 pi n)) / (2 ln base),   low = max(floor(pair(beta_fast)), 0),
+ *     high = min(ceil(pair(beta_slow)), 63),   ramp = clamp((i - low) / max(high - low, 0.001), 0, 1),
+ *     inv_freq[i] = base^(-2 i / 64) (ramp / factor + 1 - ramp).
+ * factor 1 leaves them unscaled (the last three arguments are not read). Other scalings are the caller's own
+ * 32 numbers. Host only.
+ *   inv_freq   double[32] in HOST memory (written)
+ */
+mla_status mla_rope_frequencies(double base, double factor, int trained, double beta_fast, double beta_slow,
+                                double* inv_freq);
+
+/*
+ * mla_rope: every pair (u, v) of token t's rope parts turns by its position m = positions[t],
+ *     (u, v) -> mscale (u cos(m w_i) - v sin(m w_i),  v cos(m w_i) + u sin(m w_i)),   w_i = inv_freq[i]
+ * with fp32 arithmetic and one rounding to bf16. Angles are kept as exact fractions of a turn whatever the
+ * position (w_i as a multiple of 2^-64 turns), positions may be negative: those turn back, which for
+ * mscale = 1 is the inverse and the gradient.
+ *   x          bf16 [T, N, 64], element (t, n, r) at x[t * x_stride_t + n * x_stride_n + r]: a part of a longer
+ *              head row where the strides say so (q of mla_prefill, k_pe with N = 1)
+ *   adjacent   1: pair i is (x[2 i], x[2 i + 1]);  0: (x[i], x[i + 32])
+ *   positions  int32 [T] in device memory
+ *   inv_freq   double[32] in HOST memory, read before the call returns
+ *   mscale     factor on the result (the attention factor of some scaled models), usually 1
+ *   out        bf16 [T, N, 64] with strides of its own; may be x with its strides, else must not overlap it
+ * Strides in elements, multiples of 8; pointers 16-byte aligned. T >= 0 (0 launches nothing), N >= 1.
+ */
+mla_status mla_rope(const void* x, int64_t x_stride_t, int64_t x_stride_n, const int32_t* positions,
+                    const double* inv_freq, float mscale, int adjacent, void* out, int64_t out_stride_t,
+                    int64_t out_stride_n, int T, int N, mla_stream_t stream);
+
+/*
+ * mla_rope_cache_write: mla_rope of k_pe and, if given, of q_pe, and mla_cache_write of the rows
+ * [kv_c[t] || turned k_pe[t]], in one launch. q_out is usually the last 64 dims of the absorbed queries
+ * (mla_absorb_q with q_pe = NULL leaves them alone). A row's turned values are rounded once: to bf16, or from
+ * fp32 to the FP8 row (whose scale is of the turned row). A padding token's (slot < 0) queries are turned
+ * all the same.
+ *   q_pe, q_out  bf16 [T, H, 64] with strides; both NULL for the rows alone (H is not read then)
+ * All other arguments, limits and errors as the two calls; q_out must not overlap the other inputs.
+ */
+mla_status mla_rope_cache_write(const void* kv_c, int64_t kv_c_stride_t, const void* k_pe, int64_t k_pe_stride_t,
+                                const void* q_pe, int64_t q_pe_stride_t, int64_t q_pe_stride_h, void* q_out,
+                                int64_t q_out_stride_t, int64_t q_out_stride_h, const int32_t* positions,
+                                const double* inv_freq, float mscale, int adjacent, const int64_t* slot_mapping,
+                                int T, int H, void* kv_cache, mla_kv_dtype kv_dtype, int64_t num_blocks,
+                                float kv_scale, int32_t* dev_status, mla_stream_t stream);
+
+/*
+ * mla_decode_tree: mla_decode of requests whose last Sq tokens are drafts of several continuations. Query
+ * row t of request b is draft t; it sees all tokens before the drafts and, of the drafts, those whose bits are
+ * set in tree_mask[b, t] (its ancestors and itself):
+ *     n = seq_lens[b] - Sq,   row t sees token j < n, and token n + i iff (tree_mask[b, t] >> i) & 1.
+ * A mask of the low t + 1 bits is mla_decode's causal order. A request with seq_lens[b] < Sq has only its last
+ * seq_lens[b] drafts; with 0 it is an empty slot. A row that sees nothing gets o_latent = 0, lse = -inf. What a
+ * row does not see, NaN and infinities too, does not reach it. The drafts' rows have been written (they may
+ * repeat positions: those are in the keys, by mla_rope).
+ *   tree_mask  uint64 [B, Sq] in device memory; bits from Sq on are not read
+ *   workspace  >= mla_decode_tree_workspace_bytes for the same arguments, 256-byte aligned, contents undefined
+ * 1 <= Sq <= 64. All other arguments, results, limits and errors as mla_decode; how a request's tokens are
+ * divided over the device is the library's choice (from B, Sq, H and max_seq_len).
+ */
+size_t mla_decode_tree_workspace_bytes(mla_kv_dtype kv_dtype, int B, int Sq, int H, int max_seq_len);
+mla_status mla_decode_tree(const void* q, const void* kv_cache, mla_kv_dtype kv_dtype, int64_t num_blocks,
+                           const int32_t* block_table, int max_blocks, const int32_t* seq_lens,
+                           const uint64_t* tree_mask, int max_seq_len, int B, int Sq, int H, float scale,
+                           void* workspace, size_t workspace_bytes, void* o_latent, mla_dtype o_dtype, float* lse,
+                           int32_t* dev_status, mla_stream_t stream);
+
+/*
+ * mla_accept_tokens: after a tree step, the rows of the accepted drafts become the tokens behind those before
+ * the drafts. With n = max(0, seq_lens[b] - Sq) and the accepted branch path[b, 0 .. counts[b]), for each layer
+ *     row n + i  <-  row seq_lens[b] - Sq + path[b, i],      new_lens[b] = n + counts[b].
+ * Other rows, those behind new_lens[b] too, are left as they are. The branch ascends, as ancestors come before
+ * their descendants; an entry that does not, or that is no draft of the request, sets MLA_DEV_BAD_BRANCH and
+ * ends the branch before it. Requests must not share the pages that hold drafts.
+ *   kv_cache   [layers, num_blocks, 64, mla_kv_row_bytes(kv_dtype)] bytes, one block table for all layers
+ *   path       int32 [B, Sq], counts int32 [B], in device memory
+ *   new_lens   int32 [B], another buffer than seq_lens
+ * A row in a block outside the cache sets MLA_DEV_BAD_BLOCK_ID and is not moved. 1 <= Sq <= 64, layers >= 1.
+ */
+mla_status mla_accept_tokens(void* kv_cache, mla_kv_dtype kv_dtype, int layers, int64_t num_blocks,
+                             const int32_t* block_table, int max_blocks, const int32_t* seq_lens,
+                             const int32_t* path, const int32_t* counts, int B, int Sq, int32_t* new_lens,
+                             int32_t* dev_status, mla_stream_t stream);
+
+/*
+ * mla_fork_pages: the next state of a pool of pages. A state is a block table [B, max_blocks], page_counts [B]
+ * (the pages a row holds: its first entries), seq_lens [B] (its tokens, page_counts[b] * 64 at most) and refs
+ * [num_blocks] (holders of each page, 0: free). Row r of the new state goes on from row parents[r] of the old
+ * one, or starts empty for -1; an old row that nobody goes on from is dropped, one with several children forked.
+ *   - A new row has its parent's tokens and pages for max(its tokens, room[r]) of them.
+ *   - Pages full of tokens are shared by all children. The first child (the lowest r) also keeps the other
+ *     pages that it needs and that nobody else holds. Every other page is taken from the free ones, the lowest
+ *     first, in the order of the rows and of their pages; one that stands for a page held in part gets the
+ *     row's tokens of it copied, in every layer (nothing behind them).
+ *   - Pages are free if refs was 0 before the call; what the call gives back is free in the next.
+ *   - new_table's entries behind a row's pages are -1.
+ * So continuing a batch, adding, forking, reordering and ending requests, and room for a step's tokens are all
+ * one call. The old state is not changed. If it cannot be done (too few free pages, MLA_DEV_NO_PAGES; a
+ * parent outside [-1, B), MLA_DEV_BAD_PARENT; a length or count that does not fit max_blocks,
+ * MLA_DEV_SEQ_TOO_LONG), no cache row is written, new_refs equals refs and every new row is empty: the caller
+ * goes on from the old state. An entry outside the cache among a row's pages sets MLA_DEV_BAD_BLOCK_ID; it is
+ * passed on and not counted.
+ *   kv_cache   [layers, num_blocks, 64, mla_kv_row_bytes(kv_dtype)] bytes; layers 0: the tables alone
+ *   parents, room  int32 [B2];  new_table int32 [B2, max_blocks], new_counts, new_lens int32 [B2], new_refs int32
+ *              [num_blocks]: other buffers than the old state's
+ *   workspace  >= mla_fork_pages_workspace_bytes(B, B2, num_blocks) bytes, 256-byte aligned, contents undefined
+ * All but the host numbers in device memory. B, B2 <= 8192.
+ */
+size_t mla_fork_pages_workspace_bytes(int B, int B2, int64_t num_blocks);
+mla_status mla_fork_pages(void* kv_cache, mla_kv_dtype kv_dtype, int layers, int64_t num_blocks,
+                          const int32_t* block_table, int max_blocks, const int32_t* page_counts,
+                          const int32_t* seq_lens, const int32_t* refs, int B, const int32_t* parents,
+                          const int32_t* room, int B2, int32_t* new_table, int32_t* new_counts, int32_t* new_lens,
+                          int32_t* new_refs, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                          mla_stream_t stream);
 
 #ifdef __cplusplus
 }

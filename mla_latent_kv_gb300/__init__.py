@@ -20,7 +20,9 @@ KV_BF16, KV_FP8 = 0, 1
 DT_F32, DT_BF16 = 0, 1
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE_TOO_SMALL, ERR_CUDA = range(5)
 DEV_BAD_BLOCK_ID, DEV_SEQ_TOO_LONG, DEV_WAIT_TIMEOUT, DEV_BAD_SLOT, DEV_BAD_PAGE = 0x1, 0x2, 0x4, 0x8, 0x10
+DEV_BAD_BRANCH, DEV_BAD_PARENT, DEV_NO_PAGES = 0x20, 0x40, 0x80
 L, R, D, P, V, PAGE, MAX_HEADS = 512, 64, 576, 128, 128, 64, 128
+MAX_DRAFTS = 64
 
 _lock = threading.Lock()
 _lib = None
@@ -104,6 +106,26 @@ def lib() -> ctypes.CDLL:
         l.mla_decode_sparse.restype = i32
         l.mla_decode_sparse.argtypes = [vp, vp, i32, i64, vp, i32, vp, vp, i32, i32, i32, i32, f32, i32, vp, sz, vp,
                                         i32, vp, vp, vp]
+        f64 = ctypes.c_double
+        l.mla_rope_frequencies.restype = i32
+        l.mla_rope_frequencies.argtypes = [f64, f64, i32, f64, f64, vp]
+        l.mla_rope.restype = i32
+        l.mla_rope.argtypes = [vp, i64, i64, vp, vp, f32, i32, vp, i64, i64, i32, i32, vp]
+        l.mla_rope_cache_write.restype = i32
+        l.mla_rope_cache_write.argtypes = [vp, i64, vp, i64, vp, i64, i64, vp, i64, i64, vp, vp, f32, i32, vp, i32, i32, vp,
+                                           i32, i64, f32, vp, vp]
+        l.mla_decode_tree_workspace_bytes.restype = sz
+        l.mla_decode_tree_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        l.mla_decode_tree.restype = i32
+        l.mla_decode_tree.argtypes = [vp, vp, i32, i64, vp, i32, vp, vp, i32, i32, i32, i32, f32, vp, sz, vp, i32, vp, vp,
+                                      vp]
+        l.mla_accept_tokens.restype = i32
+        l.mla_accept_tokens.argtypes = [vp, i32, i32, i64, vp, i32, vp, vp, vp, i32, i32, vp, vp, vp]
+        l.mla_fork_pages_workspace_bytes.restype = sz
+        l.mla_fork_pages_workspace_bytes.argtypes = [i32, i32, i64]
+        l.mla_fork_pages.restype = i32
+        l.mla_fork_pages.argtypes = [vp, i32, i32, i64, vp, i32, vp, vp, vp, i32, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp,
+                                     vp]
         _lib = l
         return l
 
@@ -618,3 +640,197 @@ def decode_sparse(q, kv_cache, block_table, seq_lens, pages, scale, kv_dtype=KV_
                                int(num_splits), _a(workspace), ws_bytes, o_latent.data_ptr(), o_dtype, lse.data_ptr(),
                                _a(dev_status), s))
     return o_latent, lse
+
+
+# ----------------------------------------------------- rotary positions, drafted tokens, the page pool
+def rope_frequencies(base=10000.0, factor=1.0, trained=4096, beta_fast=32.0, beta_slow=1.0):
+    """Radians per position of a rope part's 32 pairs, a float64 CPU tensor; factor > 1: scaled as YaRN does for
+    contexts longer than the `trained` positions."""
+    import torch
+    out = torch.empty(R // 2, dtype=torch.float64, device="cpu")
+    _check(lib().mla_rope_frequencies(float(base), float(factor), int(trained), float(beta_fast), float(beta_slow),
+                                      out.data_ptr()))
+    return out
+
+
+def _is_freq(t):
+    import torch
+    if t.dtype is not torch.float64 or t.shape != (R // 2,) or not t.is_contiguous() or t.device.type != "cpu":
+        raise ValueError(f"inv_freq must be a contiguous float64 CPU tensor of {R // 2} elements, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+
+
+def _is_rows(name, t, shape):
+    """Refuse a tensor that is not bf16 of the shape with unit inner stride (its rows may be strided)."""
+    import torch
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.stride(-1) != 1:
+        raise ValueError(f"{name} must be bf16 of shape {tuple(shape)} with unit inner stride, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+
+
+def _strides(t):
+    """Strides of all dimensions but the last; dimensions of one element have strides of no meaning."""
+    return [s if n > 1 else 0 for n, s in zip(t.shape[:-1], t.stride()[:-1])]
+
+
+def rope(x, positions, inv_freq, adjacent=True, mscale=1.0, out=None, stream=None):
+    """x [T, N, 64] bf16 (a part of longer rows where the strides say so) turned by positions [T] int32 and
+    inv_freq (rope_frequencies) -> bf16 [T, N, 64]. `out` may be x itself. adjacent: pairs (2i, 2i+1), else
+    (i, i+32). Negative positions turn back."""
+    import torch
+    if x.ndim != 3 or x.shape[2] != R:
+        raise ValueError(f"x must be [T, N, {R}], got {tuple(x.shape)}")
+    _is_rows("x", x, x.shape)
+    T, N = x.shape[0], x.shape[1]
+    _is_shape("positions", positions, torch.int32, (T,))
+    _is_freq(inv_freq)
+    if stream is not None and out is None:
+        return _on(stream, "rope", locals())
+    if out is None:
+        out = torch.empty((T, N, R), dtype=torch.bfloat16, device=x.device)
+    _is_rows("out", out, x.shape)
+    s = _raw_stream(stream, x, positions, out)
+    (xt, xn), (ot, on) = _strides(x), _strides(out)
+    _check(lib().mla_rope(x.data_ptr(), xt, xn, positions.data_ptr(), inv_freq.data_ptr(), float(mscale), 1 if adjacent else 0,
+                          out.data_ptr(), ot, on, T, N, s))
+    return out
+
+
+def rope_cache_write(kv_c, k_pe, positions, inv_freq, slot_mapping, kv_cache, kv_dtype=KV_BF16, adjacent=True, mscale=1.0,
+                     kv_scale=0.0, q_pe=None, q_out=None, dev_status=None, stream=None, num_blocks=None):
+    """cache_write() of kv_c [T, 512] and of k_pe [T, 64] turned as by rope(), and, if given, rope() of
+    q_pe [T, H, 64] into q_out (the last 64 dims of the absorbed queries, say), in one launch -> kv_cache."""
+    import torch
+    T = slot_mapping.shape[0]
+    _is_shape("slot_mapping", slot_mapping, torch.int64, (T,))
+    _is_rows("kv_c", kv_c, (T, L))
+    _is_rows("k_pe", k_pe, (T, R))
+    _is_shape("positions", positions, torch.int32, (T,))
+    _is_freq(inv_freq)
+    if (q_pe is None) != (q_out is None):
+        raise ValueError("q_pe and q_out go together")
+    H, qs, os = 1, (0, 0), (0, 0)
+    if q_pe is not None:
+        H = q_pe.shape[1]
+        _is_rows("q_pe", q_pe, (T, H, R))
+        _is_rows("q_out", q_out, (T, H, R))
+        qs, os = _strides(q_pe), _strides(q_out)
+    nb = _cache_blocks(kv_cache, kv_dtype, num_blocks)
+    _check_status(dev_status)
+    s = _raw_stream(stream, kv_cache, kv_c, k_pe, positions, slot_mapping, q_pe, q_out, dev_status)
+    _check(lib().mla_rope_cache_write(kv_c.data_ptr(), *_strides(kv_c), k_pe.data_ptr(), *_strides(k_pe), _a(q_pe), *qs,
+                                      _a(q_out), *os, positions.data_ptr(), inv_freq.data_ptr(), float(mscale),
+                                      1 if adjacent else 0, slot_mapping.data_ptr(), T, H, kv_cache.data_ptr(), kv_dtype, nb,
+                                      float(kv_scale), _a(dev_status), s))
+    return kv_cache
+
+
+def decode_tree_workspace_bytes(B: int, Sq: int, H: int, max_seq_len: int, kv_dtype: int = KV_BF16) -> int:
+    return lib().mla_decode_tree_workspace_bytes(kv_dtype, B, Sq, H, int(max_seq_len))
+
+
+def decode_tree(q, kv_cache, block_table, seq_lens, tree_mask, max_seq_len, scale, kv_dtype=KV_BF16, workspace=None,
+                o_latent=None, o_dtype=None, lse=None, dev_status=None, stream=None, num_blocks=None):
+    """decode() of requests whose last Sq tokens are drafts: row t sees the tokens before them and the drafts
+    whose bits are set in tree_mask [B, Sq] int64 -> (o_latent [B,Sq,H,512], lse [B,Sq,H])."""
+    import torch
+    B, Sq, H = _page_args(q, block_table, seq_lens)
+    _is_shape("tree_mask", tree_mask, torch.int64, (B, Sq))
+    nb = _cache_blocks(kv_cache, kv_dtype, num_blocks)
+    l = lib()
+    need = 0 if workspace is not None else l.mla_decode_tree_workspace_bytes(kv_dtype, B, Sq, H, int(max_seq_len))
+    if stream is not None and (o_latent is None or lse is None or (need and workspace is None)):
+        return _on(stream, "decode_tree", locals())
+    o_latent, o_dtype, lse, workspace, ws_bytes = _attention_bufs(q, B, Sq, H, o_latent, o_dtype, lse, workspace, need)
+    _check_status(dev_status)
+    s = _raw_stream(stream, q, kv_cache, block_table, seq_lens, tree_mask, o_latent, lse, workspace, dev_status)
+    _check(l.mla_decode_tree(q.data_ptr(), kv_cache.data_ptr(), kv_dtype, nb, block_table.data_ptr(), block_table.shape[1],
+                             seq_lens.data_ptr(), tree_mask.data_ptr(), int(max_seq_len), B, Sq, H, float(scale),
+                             _a(workspace), ws_bytes, o_latent.data_ptr(), o_dtype, lse.data_ptr(), _a(dev_status), s))
+    return o_latent, lse
+
+
+def _layer_blocks(kv_cache, kv_dtype):
+    """(layers, blocks) of a cache [num_blocks, ...] or [layers, num_blocks, ...] of whole pages."""
+    rb = _ROW_BYTES.get(kv_dtype)
+    if rb is None:
+        raise MlaError(ERR_INVALID_ARG, f"unknown kv_dtype {kv_dtype}")
+    page = kv_cache.shape[-1] * kv_cache.element_size()
+    if kv_cache.ndim not in (2, 3) or page != PAGE * rb or not kv_cache.is_contiguous():
+        raise ValueError(f"kv_cache must be contiguous [num_blocks, page] or [layers, num_blocks, page] with pages of "
+                         f"{PAGE * rb} bytes, got {tuple(kv_cache.shape)} {kv_cache.dtype}")
+    return (1 if kv_cache.ndim == 2 else kv_cache.shape[0]), kv_cache.shape[-2]
+
+
+def accept_tokens(kv_cache, block_table, seq_lens, path, counts, kv_dtype=KV_BF16, new_lens=None, dev_status=None,
+                  stream=None):
+    """The accepted drafts path[b, :counts[b]] (ascending, of the Sq = path.shape[1] last tokens) become the tokens
+    behind those before the drafts, in every layer of kv_cache [num_blocks, page] or [layers, num_blocks, page]
+    -> new_lens [B] int32."""
+    import torch
+    _is("block_table", block_table, torch.int32, 2)
+    B = block_table.shape[0]
+    _is_shape("seq_lens", seq_lens, torch.int32, (B,))
+    _is("path", path, torch.int32, 2)
+    _is_shape("counts", counts, torch.int32, (B,))
+    if path.shape[0] != B:
+        raise ValueError(f"path must be [{B}, Sq], got {tuple(path.shape)}")
+    layers, nb = _layer_blocks(kv_cache, kv_dtype)
+    if stream is not None and new_lens is None:
+        return _on(stream, "accept_tokens", locals())
+    if new_lens is None:
+        new_lens = torch.empty((B,), dtype=torch.int32, device=seq_lens.device)
+    _is_shape("new_lens", new_lens, torch.int32, (B,))
+    _check_status(dev_status)
+    s = _raw_stream(stream, kv_cache, block_table, seq_lens, path, counts, new_lens, dev_status)
+    _check(lib().mla_accept_tokens(kv_cache.data_ptr(), kv_dtype, layers, nb, block_table.data_ptr(), block_table.shape[1],
+                                   seq_lens.data_ptr(), path.data_ptr(), counts.data_ptr(), B, path.shape[1],
+                                   new_lens.data_ptr(), _a(dev_status), s))
+    return new_lens
+
+
+def fork_pages_workspace_bytes(B: int, B2: int, num_blocks: int) -> int:
+    return lib().mla_fork_pages_workspace_bytes(B, B2, int(num_blocks))
+
+
+def fork_pages(kv_cache, block_table, page_counts, seq_lens, refs, parents, room, kv_dtype=KV_BF16, out=None,
+               workspace=None, dev_status=None, stream=None):
+    """The page pool's next state: row r goes on from row parents[r] (-1: a new one) with pages for room[r] tokens;
+    rows that nobody goes on from are dropped, pages held in part are copied in every layer of kv_cache
+    [num_blocks, page] or [layers, num_blocks, page] where rows part -> (table [B2, max_blocks], page_counts [B2],
+    seq_lens [B2], refs [num_blocks]), written into the tuple `out` when given (other buffers than the old state's)."""
+    import torch
+    i32 = torch.int32
+    _is("block_table", block_table, i32, 2)
+    B, max_blocks = block_table.shape
+    _is_shape("page_counts", page_counts, i32, (B,))
+    _is_shape("seq_lens", seq_lens, i32, (B,))
+    layers, nb = _layer_blocks(kv_cache, kv_dtype)
+    _is_shape("refs", refs, i32, (nb,))
+    _is("parents", parents, i32, 1)
+    B2 = parents.shape[0]
+    _is_shape("room", room, i32, (B2,))
+    if stream is not None and (out is None or workspace is None):
+        return _on(stream, "fork_pages", locals())
+    if out is None:
+        made = {"dtype": i32, "device": refs.device}
+        out = (torch.empty((B2, max_blocks), **made), torch.empty((B2,), **made), torch.empty((B2,), **made),
+               torch.empty((nb,), **made))
+    table, counts, lens, new_refs = out
+    _is_shape("out[0]", table, i32, (B2, max_blocks))
+    _is_shape("out[1]", counts, i32, (B2,))
+    _is_shape("out[2]", lens, i32, (B2,))
+    _is_shape("out[3]", new_refs, i32, (nb,))
+    l = lib()
+    if workspace is None:
+        workspace = torch.empty(l.mla_fork_pages_workspace_bytes(B, B2, nb), dtype=torch.uint8, device=refs.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _check_status(dev_status)
+    s = _raw_stream(stream, refs, kv_cache, block_table, page_counts, seq_lens, parents, room, table, counts, lens, new_refs,
+                    workspace, dev_status)
+    _check(l.mla_fork_pages(kv_cache.data_ptr(), kv_dtype, layers, nb, block_table.data_ptr(), max_blocks,
+                            page_counts.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), B, parents.data_ptr(),
+                            room.data_ptr(), B2, table.data_ptr(), counts.data_ptr(), lens.data_ptr(), new_refs.data_ptr(),
+                            workspace.data_ptr(), workspace.nbytes, _a(dev_status), s))
+    return table, counts, lens, new_refs

@@ -1,0 +1,377 @@
+// drafts_api.cu -- the entry points of a serving step with drafted tokens: rotary positions, decode of a
+// tree of drafts, and the page pool between steps. Host-side validation and launches, by the rules of
+// mla_api.cu: nothing is allocated, freed or synchronised, and every argument is checked before the first
+// launch.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "internal.h"
+
+namespace {
+
+using mla::set_error;
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+bool known_kv(mla_kv_dtype d) { return d == MLA_KV_BF16 || d == MLA_KV_FP8_E4M3_SCALED; }
+
+mla_status cuda_error(cudaError_t e, const char* who) {
+    return set_error(MLA_ERR_CUDA, "%s launch: %s (%s)", who, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
+// ------------------------------------------------------------------------------------ positions
+// The checks and arguments that the two rotary calls share; x == null: no heads.
+mla_status rope_args(const char* who, const void* x, int64_t x_t, int64_t x_n, const int32_t* positions,
+                     const double* inv_freq, float mscale, int adjacent, void* out, int64_t out_t, int64_t out_n, int T,
+                     int N, mla::RopeArgs* a) {
+    if (T < 0 || N < 1) return set_error(MLA_ERR_INVALID_ARG, "%s: T=%d, %d heads", who, T, N);
+    if (!inv_freq) return set_error(MLA_ERR_INVALID_ARG, "%s: null inv_freq", who);
+    if (adjacent != 0 && adjacent != 1) return set_error(MLA_ERR_INVALID_ARG, "%s: adjacent=%d", who, adjacent);
+    if (!std::isfinite(mscale)) return set_error(MLA_ERR_INVALID_ARG, "%s: mscale is not finite", who);
+    for (int i = 0; i < mla::kPairs; ++i) {
+        // turns per position, modulo whole turns, in units of 2^-64
+        if (!std::isfinite(inv_freq[i])) return set_error(MLA_ERR_INVALID_ARG, "%s: inv_freq[%d] is not finite", who, i);
+        const double turns = inv_freq[i] / 6.283185307179586476925286766559;
+        const double frac = turns - std::floor(turns);
+        a->step[i] = frac < 1.0 ? (uint64_t)(frac * 18446744073709551616.0) : 0;
+    }
+    if (T == 0) return MLA_OK;
+    if (!positions) return set_error(MLA_ERR_INVALID_ARG, "%s: null pointer", who);
+    if (x || out) {
+        if (!x || !out) return set_error(MLA_ERR_INVALID_ARG, "%s: null pointer", who);
+        if (!aligned16(x) || !aligned16(out) || x_t % 8 || x_n % 8 || out_t % 8 || out_n % 8)
+            return set_error(MLA_ERR_UNSUPPORTED, "%s: 16-byte aligned pointers and strides of multiples of 8 needed", who);
+        if ((T > 1 && out_t == 0) || (N > 1 && out_n == 0))
+            return set_error(MLA_ERR_INVALID_ARG, "%s: the result's rows overlap", who);
+    }
+    if ((int64_t)T * (N / 32 + 2) > (int64_t)INT32_MAX)
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: %d tokens of %d heads too many", who, T, N);
+    a->mscale = mscale;
+    a->adjacent = adjacent;
+    a->positions = positions;
+    a->T = T;
+    a->x = (const uint16_t*)x;
+    a->x_t = x_t;
+    a->x_n = x_n;
+    a->out = (uint16_t*)out;
+    a->out_t = out_t;
+    a->out_n = out_n;
+    a->N = N;
+    return MLA_OK;
+}
+
+// ------------------------------------------------------------------------------------ tree
+// How a tree call runs, and its workspace: the rings of widened pages (FP8), then the partial states.
+struct TreePlan {
+    int tiles, splits, pages_per_split;
+    int64_t units;
+    size_t ring, scales, part_o, part_lse, total;
+};
+bool plan_tree(mla_kv_dtype kv, int B, int Sq, int H, int max_seq_len, TreePlan* w) {
+    const int clusters = mla::prefix_clusters();
+    if (clusters < 1) return false;
+    const int64_t flat = (int64_t)Sq * H;
+    w->tiles = (int)((flat + 255) / 256);
+    mla::tree_split((int64_t)B * w->tiles, B * flat, (max_seq_len + mla::kPage - 1) / mla::kPage, clusters, &w->splits,
+                    &w->pages_per_split);
+    w->units = (int64_t)B * w->tiles * w->splits;
+    size_t off = 0;
+    if (kv == MLA_KV_FP8_E4M3_SCALED) {
+        const size_t rows = (size_t)w->units * mla::kTreeRing * mla::kTreeGroup;
+        w->ring = off;
+        off += up256(rows * mla::kBf16RowBytes);
+        w->scales = off;
+        off += up256(rows * 2 * sizeof(float));
+    }
+    if (w->splits > 1) {
+        w->part_o = off;
+        off += up256((size_t)w->splits * B * flat * mla::kL * sizeof(float));
+        w->part_lse = off;
+        off += up256((size_t)w->splits * B * flat * sizeof(float));
+    }
+    w->total = off;
+    return true;
+}
+bool tree_shape(int B, int Sq, int H) {
+    return B >= 0 && Sq >= 1 && Sq <= mla::kTreeMaxDrafts && H >= 1 && H <= MLA_MAX_HEADS &&
+           (int64_t)B * Sq <= INT32_MAX / MLA_MAX_HEADS;
+}
+
+// ------------------------------------------------------------------------------------ pool
+mla_status check_pool(const char* who, const void* cache, mla_kv_dtype kv, int layers, int64_t num_blocks, int max_blocks) {
+    if (!known_kv(kv)) return set_error(MLA_ERR_INVALID_ARG, "%s: unknown kv_dtype %d", who, (int)kv);
+    if (layers < 0 || num_blocks < 0 || max_blocks < 0)
+        return set_error(MLA_ERR_INVALID_ARG, "%s: layers=%d, num_blocks=%lld, max_blocks=%d", who, layers,
+                         (long long)num_blocks, max_blocks);
+    if (num_blocks > (int64_t)(INT32_MAX / mla::kPage) || max_blocks > INT32_MAX / mla::kPage || layers > 65535)
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: num_blocks=%lld, max_blocks=%d or layers=%d too large", who,
+                         (long long)num_blocks, max_blocks, layers);
+    if (layers > 0 && num_blocks > 0 && !cache) return set_error(MLA_ERR_INVALID_ARG, "%s: null pointer", who);
+    if (!aligned16(cache)) return set_error(MLA_ERR_UNSUPPORTED, "%s: kv_cache must be 16-byte aligned", who);
+    return MLA_OK;
+}
+
+struct ForkLayout {
+    size_t rows, heirs, fresh, total;
+};
+ForkLayout fork_layout(int B, int B2, int64_t num_blocks) {
+    ForkLayout w{};
+    w.rows = 256;
+    w.heirs = w.rows + up256((size_t)B2 * sizeof(int4));
+    w.fresh = w.heirs + up256((size_t)B * sizeof(int32_t));
+    w.total = w.fresh + up256((size_t)num_blocks * sizeof(int32_t));
+    return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+mla_status mla_rope_frequencies(double base, double factor, int trained, double beta_fast, double beta_slow, double* inv_freq) {
+    const char* who = "mla_rope_frequencies";
+    if (!inv_freq) return set_error(MLA_ERR_INVALID_ARG, "%s: null pointer", who);
+    if (!std::isfinite(base) || base <= 1.0 || !std::isfinite(factor) || factor < 1.0)
+        return set_error(MLA_ERR_INVALID_ARG, "%s: base=%g must be above 1 and factor=%g at least 1", who, base, factor);
+    const bool scaled = factor > 1.0;
+    if (scaled && (trained < 1 || !(beta_slow > 0.0) || !(beta_fast >= beta_slow) || !std::isfinite(beta_fast)))
+        return set_error(MLA_ERR_INVALID_ARG, "%s: trained=%d, beta_fast=%g, beta_slow=%g", who, trained, beta_fast, beta_slow);
+    // the pair (not a whole number) that makes `turns` turns over the trained positions
+    auto pair_of = [&](double turns) {
+        return mla::kR * std::log(trained / (turns * 6.283185307179586476925286766559)) / (2.0 * std::log(base));
+    };
+    const double low = scaled ? std::max(std::floor(pair_of(beta_fast)), 0.0) : 0.0;
+    const double high = scaled ? std::min(std::ceil(pair_of(beta_slow)), mla::kR - 1.0) : 0.0;
+    for (int i = 0; i < mla::kPairs; ++i) {
+        const double w = std::pow(base, -2.0 * i / mla::kR);
+        const double ramp = scaled ? std::min(1.0, std::max(0.0, (i - low) / std::max(high - low, 0.001))) : 0.0;
+        inv_freq[i] = w / factor * ramp + w * (1.0 - ramp);
+    }
+    return mla::set_ok();
+}
+
+mla_status mla_rope(const void* x, int64_t x_stride_t, int64_t x_stride_n, const int32_t* positions, const double* inv_freq,
+                    float mscale, int adjacent, void* out, int64_t out_stride_t, int64_t out_stride_n, int T, int N,
+                    mla_stream_t stream) {
+    const char* who = "mla_rope";
+    mla::RopeArgs a{};
+    const mla_status st = rope_args(who, x, x_stride_t, x_stride_n, positions, inv_freq, mscale, adjacent, out, out_stride_t,
+                                    out_stride_n, T, N, &a);
+    if (st != MLA_OK) return st;
+    if (T == 0) return mla::set_ok();
+    if (!x) return set_error(MLA_ERR_INVALID_ARG, "%s: null pointer", who);
+    const cudaError_t e = mla::launch_rope(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? mla::set_ok() : cuda_error(e, who);
+}
+
+mla_status mla_rope_cache_write(const void* kv_c, int64_t kv_c_stride_t, const void* k_pe, int64_t k_pe_stride_t,
+                                const void* q_pe, int64_t q_pe_stride_t, int64_t q_pe_stride_h, void* q_out,
+                                int64_t q_out_stride_t, int64_t q_out_stride_h, const int32_t* positions,
+                                const double* inv_freq, float mscale, int adjacent, const int64_t* slot_mapping, int T, int H,
+                                void* kv_cache, mla_kv_dtype kv_dtype, int64_t num_blocks, float kv_scale,
+                                int32_t* dev_status, mla_stream_t stream) {
+    const char* who = "mla_rope_cache_write";
+    if (!known_kv(kv_dtype)) return set_error(MLA_ERR_INVALID_ARG, "%s: unknown kv_dtype %d", who, (int)kv_dtype);
+    if (num_blocks < 0) return set_error(MLA_ERR_INVALID_ARG, "%s: negative num_blocks", who);
+    if (!std::isfinite(kv_scale)) return set_error(MLA_ERR_INVALID_ARG, "%s: kv_scale is not finite", who);
+    mla::RopeArgs a{};
+    const mla_status st = rope_args(who, q_pe, q_pe_stride_t, q_pe_stride_h, positions, inv_freq, mscale, adjacent, q_out,
+                                    q_out_stride_t, q_out_stride_h, T, q_pe ? H : 1, &a);
+    if (st != MLA_OK) return st;
+    if (T == 0) return mla::set_ok();
+    if (!kv_c || !k_pe || !slot_mapping || !kv_cache) return set_error(MLA_ERR_INVALID_ARG, "%s: null pointer", who);
+    if (!aligned16(kv_c) || !aligned16(k_pe) || !aligned16(kv_cache) || kv_c_stride_t % 8 || k_pe_stride_t % 8)
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: 16-byte aligned pointers and strides of multiples of 8 needed", who);
+    mla::RopeRows r{};
+    r.kv_c = (const uint16_t*)kv_c;
+    r.st_c = kv_c_stride_t;
+    r.k_pe = (const uint16_t*)k_pe;
+    r.st_pe = k_pe_stride_t;
+    r.slots = slot_mapping;
+    r.cache = (uint8_t*)kv_cache;
+    r.num_blocks = num_blocks;
+    r.kv_scale = kv_scale;
+    r.dev_status = dev_status;
+    const cudaError_t e = mla::launch_rope_cache_write(a, r, kv_dtype == MLA_KV_FP8_E4M3_SCALED, (cudaStream_t)stream);
+    return e == cudaSuccess ? mla::set_ok() : cuda_error(e, who);
+}
+
+size_t mla_decode_tree_workspace_bytes(mla_kv_dtype kv_dtype, int B, int Sq, int H, int max_seq_len) {
+    TreePlan w{};
+    if (!known_kv(kv_dtype) || !tree_shape(B, Sq, H) || B < 1 || max_seq_len < 0) return 0;
+    return plan_tree(kv_dtype, B, Sq, H, max_seq_len, &w) ? w.total : 0;
+}
+
+mla_status mla_decode_tree(const void* q, const void* kv_cache, mla_kv_dtype kv_dtype, int64_t num_blocks,
+                           const int32_t* block_table, int max_blocks, const int32_t* seq_lens, const uint64_t* tree_mask,
+                           int max_seq_len, int B, int Sq, int H, float scale, void* workspace, size_t workspace_bytes,
+                           void* o_latent, mla_dtype o_dtype, float* lse, int32_t* dev_status, mla_stream_t stream) {
+    const char* who = "mla_decode_tree";
+    if (Sq > mla::kTreeMaxDrafts)
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: Sq=%d drafts, at most %d", who, Sq, mla::kTreeMaxDrafts);
+    if (B < 0 || Sq < 1) return set_error(MLA_ERR_INVALID_ARG, "%s: B=%d, Sq=%d", who, B, Sq);
+    // What mla_decode refuses is refused by the same checks.
+    mla::DecodeExtra x;
+    x.who = who;
+    x.check_only = true;
+    const mla_status checked = mla::decode_impl(q, kv_cache, kv_dtype, num_blocks, block_table, max_blocks, seq_lens, nullptr,
+                                                max_seq_len, B, Sq, (int64_t)B * Sq, H, scale, 1, nullptr, 0, o_latent,
+                                                o_dtype, lse, dev_status, stream, x);
+    if (checked != MLA_OK || B == 0) return checked;
+    if (!tree_mask) return set_error(MLA_ERR_INVALID_ARG, "%s: null pointer", who);
+    if (!tree_shape(B, Sq, H)) return set_error(MLA_ERR_UNSUPPORTED, "%s: %lld query rows too many", who, (long long)B * Sq);
+    TreePlan w{};
+    if (!plan_tree(kv_dtype, B, Sq, H, max_seq_len, &w))
+        return set_error(MLA_ERR_CUDA, "%s: could not plan the call (no CUDA device?)", who);
+    if (w.units > INT32_MAX / 4) return set_error(MLA_ERR_UNSUPPORTED, "%s: %lld work units too many", who, (long long)w.units);
+    if (w.total > 0 && (!workspace || workspace_bytes < w.total))
+        return set_error(MLA_ERR_WORKSPACE_TOO_SMALL, "%s: workspace %zu bytes < %zu needed", who,
+                         workspace ? workspace_bytes : (size_t)0, w.total);
+    if (w.total > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: workspace must be 256-byte aligned", who);
+    const bool fp8 = kv_dtype == MLA_KV_FP8_E4M3_SCALED;
+    char* ws = (char*)workspace;
+    mla::PrefixArgs a{};
+    a.q = (const uint16_t*)q;
+    a.flat_rows = Sq * H;
+    a.block_table = block_table;
+    a.max_blocks = max_blocks;
+    a.num_blocks = num_blocks;
+    a.splits = w.splits;
+    a.pages_per_split = w.pages_per_split;
+    a.seq_lens = seq_lens;
+    // no cache: no request sees a token, and a positive length is reported as too long
+    a.max_seq_len = num_blocks > 0 ? max_seq_len : 0;
+    a.B = B;
+    a.tiles = w.tiles;
+    a.Sq = Sq;
+    a.H = H;
+    a.scale = scale;
+    a.masks = tree_mask;
+    a.cache = (const uint8_t*)kv_cache;
+    a.lse = lse;
+    a.dev_status = dev_status;
+    if (fp8) {
+        a.ring = (uint8_t*)(ws + w.ring);
+        a.ring_scales = (float*)(ws + w.scales);
+    }
+    if (w.splits > 1) {
+        a.part_o = (float*)(ws + w.part_o);
+        a.part_lse = (float*)(ws + w.part_lse);
+    }
+    cudaStream_t s = (cudaStream_t)stream;
+    const bool f32 = w.splits > 1 || o_dtype == MLA_DT_F32;
+    cudaError_t e = mla::launch_decode_tree(a, fp8, f32, w.splits > 1 ? (void*)a.part_o : o_latent, s);
+    if (e != cudaSuccess) return cuda_error(e, who);
+    if (w.splits > 1) {
+        mla::DecodeArgs m{};  // every row's states are "pre" states, none its own
+        m.B = B;
+        m.Sq = Sq;
+        m.rows = B * Sq;
+        m.H = H;
+        m.pre_o = a.part_o;
+        m.pre_lse = a.part_lse;
+        m.pre_splits = w.splits;
+        m.o_latent = o_latent;
+        m.o_dtype = o_dtype;
+        m.lse = lse;
+        e = mla::launch_merge(m, s);
+        if (e != cudaSuccess) return cuda_error(e, who);
+    }
+    return mla::set_ok();
+}
+
+mla_status mla_accept_tokens(void* kv_cache, mla_kv_dtype kv_dtype, int layers, int64_t num_blocks, const int32_t* block_table,
+                             int max_blocks, const int32_t* seq_lens, const int32_t* path, const int32_t* counts, int B, int Sq,
+                             int32_t* new_lens, int32_t* dev_status, mla_stream_t stream) {
+    const char* who = "mla_accept_tokens";
+    if (B < 0 || Sq < 1) return set_error(MLA_ERR_INVALID_ARG, "%s: B=%d, Sq=%d", who, B, Sq);
+    if (Sq > mla::kTreeMaxDrafts)
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: Sq=%d drafts, at most %d", who, Sq, mla::kTreeMaxDrafts);
+    const mla_status st = check_pool(who, kv_cache, kv_dtype, layers, num_blocks, max_blocks);
+    if (st != MLA_OK) return st;
+    if (B == 0) return mla::set_ok();
+    if (layers < 1) return set_error(MLA_ERR_INVALID_ARG, "%s: layers=%d", who, layers);
+    if (!seq_lens || !path || !counts || !new_lens || (max_blocks > 0 && !block_table))
+        return set_error(MLA_ERR_INVALID_ARG, "%s: null pointer", who);
+    if (new_lens == seq_lens) return set_error(MLA_ERR_INVALID_ARG, "%s: new_lens must not be seq_lens", who);
+    mla::AcceptArgs a{};
+    a.cache = (uint8_t*)kv_cache;
+    a.layers = layers;
+    a.num_blocks = num_blocks;
+    a.block_table = block_table;
+    a.max_blocks = max_blocks;
+    a.seq_lens = seq_lens;
+    a.path = path;
+    a.counts = counts;
+    a.B = B;
+    a.Sq = Sq;
+    a.new_lens = new_lens;
+    a.dev_status = dev_status;
+    const cudaError_t e = mla::launch_accept_tokens(a, kv_dtype == MLA_KV_FP8_E4M3_SCALED, (cudaStream_t)stream);
+    return e == cudaSuccess ? mla::set_ok() : cuda_error(e, who);
+}
+
+size_t mla_fork_pages_workspace_bytes(int B, int B2, int64_t num_blocks) {
+    if (B < 0 || B2 < 0 || num_blocks < 0 || num_blocks > (int64_t)(INT32_MAX / mla::kPage)) return 0;
+    return fork_layout(B, B2, num_blocks).total;
+}
+
+mla_status mla_fork_pages(void* kv_cache, mla_kv_dtype kv_dtype, int layers, int64_t num_blocks, const int32_t* block_table,
+                          int max_blocks, const int32_t* page_counts, const int32_t* seq_lens, const int32_t* refs, int B,
+                          const int32_t* parents, const int32_t* room, int B2, int32_t* new_table, int32_t* new_counts,
+                          int32_t* new_lens, int32_t* new_refs, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                          mla_stream_t stream) {
+    const char* who = "mla_fork_pages";
+    if (B < 0 || B2 < 0) return set_error(MLA_ERR_INVALID_ARG, "%s: B=%d, B2=%d", who, B, B2);
+    const mla_status st = check_pool(who, kv_cache, kv_dtype, layers, num_blocks, max_blocks);
+    if (st != MLA_OK) return st;
+    if (B > mla::kMaxPoolRows || B2 > mla::kMaxPoolRows || (int64_t)std::max(B, B2) * max_blocks > INT32_MAX)
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: %d and %d rows of %d pages (at most %d rows)", who, B, B2, max_blocks,
+                         mla::kMaxPoolRows);
+    if (B == 0 && B2 == 0 && num_blocks == 0) return mla::set_ok();
+    if ((num_blocks > 0 && (!refs || !new_refs)) || (B > 0 && (!page_counts || !seq_lens)) ||
+        (B2 > 0 && (!parents || !room || !new_counts || !new_lens)) || (B > 0 && max_blocks > 0 && !block_table) ||
+        (B2 > 0 && max_blocks > 0 && !new_table))
+        return set_error(MLA_ERR_INVALID_ARG, "%s: null pointer", who);
+    if ((refs && refs == new_refs) || (block_table && block_table == new_table) || (page_counts && page_counts == new_counts) ||
+        (seq_lens && seq_lens == new_lens))
+        return set_error(MLA_ERR_INVALID_ARG, "%s: the new state must not be the old one's buffers", who);
+    const int page = mla::kPage * (kv_dtype == MLA_KV_BF16 ? mla::kBf16RowBytes : mla::kFp8RowBytes);
+    if ((int64_t)B2 * (1 + (int64_t)layers * (page / 16384 + 1)) + B > (int64_t)INT32_MAX)
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: %d rows of %d layers too many", who, B2, layers);
+    const ForkLayout w = fork_layout(B, B2, num_blocks);
+    if (!workspace || workspace_bytes < w.total)
+        return set_error(MLA_ERR_WORKSPACE_TOO_SMALL, "%s: workspace %zu bytes < %zu needed", who,
+                         workspace ? workspace_bytes : (size_t)0, w.total);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: workspace must be 256-byte aligned", who);
+    char* ws = (char*)workspace;
+    mla::ForkArgs a{};
+    a.cache = (uint8_t*)kv_cache;
+    a.layers = layers;
+    a.num_blocks = num_blocks;
+    a.table = block_table;
+    a.counts = page_counts;
+    a.lens = seq_lens;
+    a.refs = refs;
+    a.B = B;
+    a.max_blocks = max_blocks;
+    a.parents = parents;
+    a.room = room;
+    a.B2 = B2;
+    a.new_table = new_table;
+    a.new_counts = new_counts;
+    a.new_lens = new_lens;
+    a.new_refs = new_refs;
+    a.head = (int32_t*)ws;
+    a.rows = (int4*)(ws + w.rows);
+    a.heirs = (int32_t*)(ws + w.heirs);
+    a.fresh = (int32_t*)(ws + w.fresh);
+    a.dev_status = dev_status;
+    const cudaError_t e = mla::launch_fork_pages(a, kv_dtype == MLA_KV_FP8_E4M3_SCALED, (cudaStream_t)stream);
+    return e == cudaSuccess ? mla::set_ok() : cuda_error(e, who);
+}
+
+}  // extern "C"

@@ -254,7 +254,21 @@ struct PrefixArgs {
     float* part_o;              // fp32 [splits, flat_rows, 512]
     float* part_lse;            // fp32 [splits, flat_rows]
     int32_t* dev_status;        // or null
+    // Trees: every request's own pages, flat_rows = Sq * H rows of each request, outputs [splits, B, flat_rows]
+    // (part_o null: one split, written to the final outputs).
+    int B, tiles, max_blocks;
+    const uint64_t* masks;      // [B, Sq]
+    const uint8_t* cache;
+    float* lse;                 // final, or null
+    int o_bf16;                 // final output in bf16
+    uint8_t* ring;              // FP8: [units, kTreeRing, 2 pages] widened rows,
+    float* ring_scales;         // and [units, kTreeRing, 2, 2 pages] their k_scales and v_scales
 };
+constexpr int kTreeRing = 4;    // groups of two pages that a unit widens ahead
+constexpr int kTreeGroup = 2 * kPage;
+constexpr int kTreeMaxDrafts = 64;  // bits of a mask
+void tree_split(int64_t units, int64_t flat_rows, int pages, int clusters, int* splits, int* pages_per_split);
+cudaError_t launch_decode_tree(const PrefixArgs& a, bool fp8, bool out_f32, void* out, cudaStream_t s);
 int prefix_clusters();  // clusters of the prefix kernel that run at once on the current device, or -1
 void prefix_split(int64_t flat_rows, int pages, int clusters, int* splits, int* pages_per_split);
 // FP8: launch_prefix_widen first writes the prefix's rows to `widened` [prefix tokens, 576] and
@@ -263,6 +277,76 @@ cudaError_t launch_prefix_widen(const PrefixArgs& a, const uint8_t* cache, uint1
                                 cudaStream_t s);
 cudaError_t launch_decode_prefix(const PrefixArgs& a, const uint8_t* cache, const uint16_t* widened,
                                  const float* scales, cudaStream_t s);
+
+// ---- rotary positions, drafted tokens, the page pool ------------------------------------------------
+constexpr int kPairs = kR / 2;  // 32 pairs of a rope part
+struct RopeArgs {
+    uint64_t step[kPairs];      // turns per position of each pair, in units of 2^-64
+    float mscale;
+    int adjacent;               // pairs (2 i, 2 i + 1), else (i, i + 32)
+    const int32_t* positions;   // [T]
+    int T;
+    const uint16_t* x;          // [T, N, 64] at x + t * x_t + n * x_n (null: no heads), and the result
+    int64_t x_t, x_n;
+    uint16_t* out;
+    int64_t out_t, out_n;
+    int N;
+};
+struct RopeRows {               // the cache rows of the same tokens
+    const uint16_t* kv_c;       // [T, 512], row stride st_c
+    int64_t st_c;
+    const uint16_t* k_pe;       // [T, 64], row stride st_pe
+    int64_t st_pe;
+    const int64_t* slots;       // [T]
+    uint8_t* cache;
+    int64_t num_blocks;
+    float kv_scale;
+    int32_t* dev_status;        // or null
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
+cudaError_t launch_rope_cache_write(const RopeArgs& a, const RopeRows& r, bool fp8, cudaStream_t s);
+
+struct AcceptArgs {
+    uint8_t* cache;             // [layers, num_blocks, 64, row_bytes]
+    int layers;
+    int64_t num_blocks;
+    const int32_t* block_table; // [B, max_blocks]
+    int max_blocks;
+    const int32_t* seq_lens;    // [B], the Sq drafted tokens among them
+    const int32_t* path;        // [B, Sq] accepted drafts, ascending
+    const int32_t* counts;      // [B]
+    int B, Sq;
+    int32_t* new_lens;          // [B]
+    int32_t* dev_status;        // or null
+};
+cudaError_t launch_accept_tokens(const AcceptArgs& a, bool fp8, cudaStream_t s);
+
+// One page pool state to the next, see mla_fork_pages. The plan of the first kernel, in the workspace: a
+// header, a record per new row, each old row's heir, and the pages that are taken.
+constexpr int kMaxPoolRows = 8192;
+struct ForkArgs {
+    uint8_t* cache;             // [layers, num_blocks, 64, row_bytes]
+    int layers;
+    int64_t num_blocks;
+    const int32_t* table;       // [B, max_blocks]
+    const int32_t* counts;      // [B]
+    const int32_t* lens;        // [B]
+    const int32_t* refs;        // [num_blocks]
+    int B, max_blocks;
+    const int32_t* parents;     // [B2]
+    const int32_t* room;        // [B2]
+    int B2;
+    int32_t* new_table;         // [B2, max_blocks]
+    int32_t* new_counts;        // [B2]
+    int32_t* new_lens;          // [B2]
+    int32_t* new_refs;          // [num_blocks]
+    int32_t* head;              // [0]: the call failed
+    int4* rows;                 // [B2]: parent or -1, pages, first of its taken pages, kFork* bits
+    int32_t* heirs;             // [B]: new row that keeps the old row's pages, or -1
+    int32_t* fresh;             // [num_blocks]
+    int32_t* dev_status;        // or null
+};
+cudaError_t launch_fork_pages(const ForkArgs& a, bool fp8, cudaStream_t s);
 
 int device_sm_count();  // of the current device, or -1
 

@@ -1,0 +1,328 @@
+// pool.cu -- the page pool between decode steps: accepted drafts moved to the front of their request
+// (mla_accept_tokens), and one state of the pool made from another (mla_fork_pages).
+//
+// Both are copies of whole cache rows with a little bookkeeping on the device, so that a step that decides
+// there (how many drafts were accepted, which beams go on) needs no host in between. Bound: latency; the
+// rows moved are a few per request and layer.
+//
+// None of these kernels signals its dependents early: they write cache rows, block tables and lengths, which
+// a decode reads before its own wait.
+#include <climits>
+
+#include "internal.h"
+#include "sm103_ptx.cuh"
+
+namespace mla {
+namespace {
+
+// ------------------------------------------------------------------------------------------
+// Accepted drafts. Draft path[i] of a request moves to place i behind the tokens before its drafts. The path
+// ascends, so place i <= path[i]: rows are read and written in order, and no row is overwritten before it
+// was read. One block per (request, layer); a thread owns one column chunk of the rows and moves eight rows
+// at a time, all of their loads first.
+// ------------------------------------------------------------------------------------------
+constexpr int kAcceptThreads = 96;  // >= 73 chunks and >= 64 drafts
+constexpr int kAcceptBatch = 8;
+
+template <class Chunk, int kRowBytes>
+__global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptArgs p) {
+    constexpr int kChunks = kRowBytes / (int)sizeof(Chunk);
+    static_assert(kChunks * (int)sizeof(Chunk) == kRowBytes && kChunks <= kAcceptThreads, "chunks of a row");
+    ptx::griddep_wait();
+    const int b = (int)blockIdx.x, layer = (int)blockIdx.y, tid = threadIdx.x;
+    __shared__ int n_s;
+    __shared__ int64_t src_s[kTreeMaxDrafts], dst_s[kTreeMaxDrafts];  // rows of the cache
+    const int cap = p.max_blocks * kPage;
+    int seq = p.seq_lens[b];
+    const bool bad_len = seq < 0 || seq > cap;
+    seq = min(max(seq, 0), cap);
+    const int first = max(seq - p.Sq, 0);       // tokens before the drafts
+    const int gone = max(p.Sq - seq, 0);        // drafts that are not there: the first ones
+    const int want = p.counts[b];
+    if (tid == 0) n_s = min(max(want, 0), p.Sq);
+    __syncthreads();
+    int place = -1;
+    if (tid < p.Sq && tid < want) {
+        place = p.path[(size_t)b * p.Sq + tid];
+        const int before = tid > 0 ? p.path[(size_t)b * p.Sq + tid - 1] : gone - 1;
+        if (place <= before || place >= p.Sq) atomicMin(&n_s, tid);
+    }
+    __syncthreads();
+    const int n = n_s;
+    bool bad_block = false;
+    if (tid < n) {
+        auto row_of = [&](int token) -> int64_t {
+            const int32_t blk = p.block_table[(size_t)b * p.max_blocks + token / kPage];
+            return blk < 0 || (int64_t)blk >= p.num_blocks ? -1 : (int64_t)blk * kPage + token % kPage;
+        };
+        const int64_t s = row_of(seq - p.Sq + place), d = row_of(first + tid);
+        bad_block = s < 0 || d < 0;
+        src_s[tid] = s;
+        dst_s[tid] = bad_block || s == d ? -1 : d;
+    }
+    __syncthreads();
+    if (layer == 0) {
+        if (tid == 0) {
+            p.new_lens[b] = first + n;
+            int bits = (bad_len ? MLA_DEV_SEQ_TOO_LONG : 0) | (n != want ? MLA_DEV_BAD_BRANCH : 0);
+            if (bits && p.dev_status) atomicOr(p.dev_status, bits);
+        }
+        if (bad_block && p.dev_status) atomicOr(p.dev_status, MLA_DEV_BAD_BLOCK_ID);
+    }
+    if (tid >= kChunks) return;
+    uint8_t* base = p.cache + (size_t)layer * p.num_blocks * (kPage * kRowBytes) + tid * sizeof(Chunk);
+    for (int i0 = 0; i0 < n; i0 += kAcceptBatch) {
+        Chunk v[kAcceptBatch];
+#pragma unroll
+        for (int u = 0; u < kAcceptBatch; ++u)
+            if (i0 + u < n && dst_s[i0 + u] >= 0) v[u] = *reinterpret_cast<const Chunk*>(base + src_s[i0 + u] * kRowBytes);
+#pragma unroll
+        for (int u = 0; u < kAcceptBatch; ++u)
+            if (i0 + u < n && dst_s[i0 + u] >= 0) *reinterpret_cast<Chunk*>(base + dst_s[i0 + u] * kRowBytes) = v[u];
+    }
+}
+
+// ------------------------------------------------------------------------------------------
+// The pool's next state. The plan kernel's block 0 finds each old row's heir (its first child), counts the
+// pages every new row has to take and finds that many free ones, lowest first; its other blocks copy the
+// reference counts. The second kernel writes the new rows, applies the changes of the counts (sums of +1
+// and -1, in any order) and copies the rows of pages that are held in part by more than one.
+// ------------------------------------------------------------------------------------------
+enum : int { kForkHeir = 1, kForkCopy = 2 };
+constexpr int kPlanThreads = 1024;
+constexpr int kRefsPerThread = 8;  // of a step of the free-page search
+constexpr int kForkThreads = 256;
+constexpr int kCopyBytes = kForkThreads * 4 * 16;  // of a copy block
+
+// Whether the heir of an old row keeps the row's page j: the pages full of tokens that it may share, and of
+// the others those that nobody else holds (tokens will be written there).
+__device__ __forceinline__ bool heir_keeps(const ForkArgs& p, const int32_t* row, int j, int whole, int held, int need) {
+    if (j < whole) return true;
+    if (j >= held || j >= need) return false;
+    const int32_t page = row[j];
+    return page >= 0 && (int64_t)page < p.num_blocks && p.refs[page] == 1;
+}
+
+// Exclusive prefix sum of v over the block's threads, and the total.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (int)blockDim.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int s = lane < warps ? warp_sums[lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        if (lane < warps) warp_sums[lane] = s;
+    }
+    __syncthreads();
+    const int base = warp > 0 ? warp_sums[warp - 1] : 0;
+    *total = warp_sums[warps - 1];
+    __syncthreads();
+    return base + x - v;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs p) {
+    ptx::griddep_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (blockIdx.x > 0) {
+        const int64_t step = (int64_t)(gridDim.x - 1) * kPlanThreads;
+        for (int64_t i = (int64_t)(blockIdx.x - 1) * kPlanThreads + tid; i < p.num_blocks; i += step) p.new_refs[i] = p.refs[i];
+        return;
+    }
+    __shared__ int heir_s[kMaxPoolRows];
+    __shared__ int sums[kPlanThreads / 32];
+    __shared__ int bits_s;
+    int ref[kRefsPerThread];  // of this thread's pages, a step ahead
+    auto load_refs = [&](int64_t at) {
+#pragma unroll
+        for (int k = 0; k < kRefsPerThread; ++k) {
+            const int64_t i = at + (int64_t)tid * kRefsPerThread + k;
+            ref[k] = i < p.num_blocks ? p.refs[i] : 1;
+        }
+    };
+    load_refs(0);
+    if (tid == 0) bits_s = 0;
+    for (int b = tid; b < p.B; b += kPlanThreads) heir_s[b] = INT_MAX;
+    __syncthreads();
+    for (int r = tid; r < p.B2; r += kPlanThreads) {
+        const int parent = p.parents[r];
+        if (parent >= p.B || parent < -1)
+            atomicOr(&bits_s, MLA_DEV_BAD_PARENT);
+        else if (parent >= 0)
+            atomicMin(&heir_s[parent], r);
+    }
+    __syncthreads();
+    for (int b = tid; b < p.B; b += kPlanThreads) {
+        p.heirs[b] = heir_s[b] == INT_MAX ? -1 : heir_s[b];
+        const int n = p.lens[b], held = p.counts[b];
+        if (n < 0 || held < 0 || held > p.max_blocks || (n + (int64_t)kPage - 1) / kPage > held)
+            atomicOr(&bits_s, MLA_DEV_SEQ_TOO_LONG);
+    }
+    __syncthreads();
+    if (bits_s == 0) {  // parents and lengths are good
+        for (int r = warp; r < p.B2; r += kPlanThreads / 32) {
+            const int parent = p.parents[r], room = p.room[r];
+            const int n = parent >= 0 ? p.lens[parent] : 0, held = parent >= 0 ? p.counts[parent] : 0;
+            const int whole = n / kPage;
+            const int64_t want = ((int64_t)max(n, room) + kPage - 1) / kPage;
+            const int need = (int)min(want, (int64_t)p.max_blocks);
+            if (want > p.max_blocks && lane == 0) atomicOr(&bits_s, MLA_DEV_SEQ_TOO_LONG);
+            const bool heir = parent >= 0 && heir_s[parent] == r;
+            const int32_t* row = p.table + (size_t)max(parent, 0) * p.max_blocks;
+            int take = need - whole, flags = heir ? kForkHeir : 0;
+            bool first = false;  // the page behind the whole ones is kept
+            if (heir)
+                for (int j = whole + lane; j - lane < min(held, need); j += 32) {
+                    const uint32_t kept = __ballot_sync(0xffffffffu, heir_keeps(p, row, j, whole, held, need));
+                    take -= __popc(kept);
+                    if (j - lane == whole) first = kept & 1u;
+                }
+            if (n % kPage && !first) flags |= kForkCopy;
+            if (lane == 0) p.rows[r] = make_int4(parent, need, take, flags);
+        }
+    }
+    __syncthreads();
+    int total = 0;
+    if (bits_s == 0) {
+        for (int r0 = 0; r0 < p.B2; r0 += kPlanThreads) {  // takes -> first of the taken pages
+            const int r = r0 + tid;
+            int sum;
+            const int at = total + block_scan(r < p.B2 ? p.rows[r].z : 0, sums, &sum);
+            if (r < p.B2) p.rows[r].z = at;
+            // more than there are pages, at the latest after this many rows: no overflow below
+            total = (int)min((int64_t)total + sum, (int64_t)INT_MAX / 2);
+        }
+        int got = 0;
+        for (int64_t at = 0; at < p.num_blocks && got < total; at += kPlanThreads * kRefsPerThread) {
+            int mine = 0;
+            uint32_t free = 0;
+#pragma unroll
+            for (int k = 0; k < kRefsPerThread; ++k)
+                if (ref[k] == 0) {
+                    free |= 1u << k;
+                    ++mine;
+                }
+            load_refs(at + kPlanThreads * kRefsPerThread);
+            int sum;
+            int to = got + block_scan(mine, sums, &sum);
+            for (; free; free &= free - 1, ++to)
+                if (to < total) p.fresh[to] = (int32_t)(at + (int64_t)tid * kRefsPerThread + __ffs(free) - 1);
+            got += sum;
+        }
+        if (tid == 0 && got < total) atomicOr(&bits_s, MLA_DEV_NO_PAGES);
+    }
+    __syncthreads();
+    if (tid == 0) {
+        p.head[0] = bits_s != 0;
+        if (bits_s && p.dev_status) atomicOr(p.dev_status, bits_s);
+    }
+}
+
+template <int kRowBytes>
+__global__ void __launch_bounds__(kForkThreads) fork_apply_kernel(const ForkArgs p, int copy_blocks) {
+    ptx::griddep_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const bool failed = p.head[0] != 0;
+    int64_t u = blockIdx.x;
+    auto in_pool = [&](int32_t page) -> bool {
+        const bool ok = page >= 0 && (int64_t)page < p.num_blocks;
+        if (!ok && p.dev_status) atomicOr(p.dev_status, MLA_DEV_BAD_BLOCK_ID);
+        return ok;
+    };
+    if (u < p.B2) {  // ---- a new row
+        __shared__ int counts[kForkThreads / 32];
+        const int r = (int)u;
+        int32_t* to = p.new_table + (size_t)r * p.max_blocks;
+        const int4 rec = failed ? make_int4(-1, 0, 0, 0) : p.rows[r];
+        const int n = rec.x >= 0 ? p.lens[rec.x] : 0, held = rec.x >= 0 ? p.counts[rec.x] : 0;
+        const int whole = n / kPage, need = rec.y;
+        const bool heir = rec.w & kForkHeir;
+        const int32_t* from = p.table + (size_t)max(rec.x, 0) * p.max_blocks;
+        int taken = rec.z;
+        for (int j0 = 0; j0 < p.max_blocks; j0 += kForkThreads) {
+            const int j = j0 + tid;
+            const bool keep = j < need && (heir ? heir_keeps(p, from, j, whole, held, need) : j < whole);
+            const bool take = j < need && !keep;
+            // this page's place among the taken ones
+            const uint32_t takes = __ballot_sync(0xffffffffu, take);
+            if (lane == 0) counts[warp] = __popc(takes);
+            __syncthreads();
+            int at = taken + __popc(takes & ((1u << lane) - 1u));
+            for (int w = 0; w < kForkThreads / 32; ++w) {
+                if (w < warp) at += counts[w];
+                taken += counts[w];
+            }
+            __syncthreads();
+            if (j >= p.max_blocks) continue;
+            int32_t page = -1;
+            if (keep) page = from[j];
+            if (take) page = p.fresh[at];
+            if ((take || (keep && !heir)) && in_pool(page)) atomicAdd(p.new_refs + page, 1);
+            to[j] = page;
+        }
+        if (tid == 0) {
+            p.new_counts[r] = need;
+            p.new_lens[r] = n;
+        }
+        return;
+    }
+    if (failed) return;
+    u -= p.B2;
+    if (u < p.B) {  // ---- an old row: what its heir does not keep is given back
+        const int b = (int)u, r = p.heirs[b];
+        const int held = p.counts[b], whole = r >= 0 ? p.lens[b] / kPage : 0, need = r >= 0 ? p.rows[r].y : 0;
+        const int32_t* row = p.table + (size_t)b * p.max_blocks;
+        for (int j = (r >= 0 ? whole : 0) + tid; j < held; j += kForkThreads)
+            if (!(r >= 0 && heir_keeps(p, row, j, whole, held, need)) && in_pool(row[j])) atomicSub(p.new_refs + row[j], 1);
+        return;
+    }
+    u -= p.B;  // ---- a part of a new row's copied page, in one layer
+    const int r = (int)(u / ((int64_t)copy_blocks * p.layers));
+    const int part = (int)(u % copy_blocks), layer = (int)(u / copy_blocks % p.layers);
+    const int4 rec = p.rows[r];
+    if (!(rec.w & kForkCopy)) return;
+    const int n = p.lens[rec.x];
+    const int32_t from = p.table[(size_t)rec.x * p.max_blocks + n / kPage], to = p.fresh[rec.z];
+    if (!in_pool(from)) return;
+    constexpr size_t kPageBytes = (size_t)kPage * kRowBytes;
+    const int bytes = n % kPage * kRowBytes, at = part * kCopyBytes + tid * 16;
+    const uint8_t* src = p.cache + ((size_t)layer * p.num_blocks + from) * kPageBytes;
+    uint8_t* dst = p.cache + ((size_t)layer * p.num_blocks + to) * kPageBytes;
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (at + k * kForkThreads * 16 + 16 <= bytes) v[k] = *reinterpret_cast<const uint4*>(src + at + k * kForkThreads * 16);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (at + k * kForkThreads * 16 + 16 <= bytes) *reinterpret_cast<uint4*>(dst + at + k * kForkThreads * 16) = v[k];
+    if (kRowBytes % 16 && part == 0 && tid == 0 && bytes % 16)  // rows of 584 bytes: an odd number of 8-byte words
+        *reinterpret_cast<uint2*>(dst + bytes - 8) = *reinterpret_cast<const uint2*>(src + bytes - 8);
+}
+
+}  // namespace
+
+cudaError_t launch_accept_tokens(const AcceptArgs& a, bool fp8, cudaStream_t s) {
+    return launch_pdl(fp8 ? accept_kernel<uint2, kFp8RowBytes> : accept_kernel<uint4, kBf16RowBytes>,
+                      dim3((unsigned)a.B, (unsigned)a.layers), dim3(kAcceptThreads), 0, s, a);
+}
+
+cudaError_t launch_fork_pages(const ForkArgs& a, bool fp8, cudaStream_t s) {
+    const int64_t refs = (a.num_blocks + kPlanThreads - 1) / kPlanThreads;
+    cudaError_t e = launch_pdl(fork_plan_kernel, dim3((unsigned)(1 + (refs < 64 ? refs : 64))), dim3(kPlanThreads), 0, s, a);
+    if (e != cudaSuccess) return e;
+    const int page = kPage * (fp8 ? kFp8RowBytes : kBf16RowBytes), copy_blocks = (page + kCopyBytes - 1) / kCopyBytes;
+    const int64_t blocks = (int64_t)a.B2 + a.B + (int64_t)a.B2 * a.layers * copy_blocks;
+    return launch_pdl(fp8 ? fork_apply_kernel<kFp8RowBytes> : fork_apply_kernel<kBf16RowBytes>, dim3((unsigned)blocks),
+                      dim3(kForkThreads), 0, s, a, copy_blocks);
+}
+
+}  // namespace mla
