@@ -145,5 +145,21 @@ __device__ __forceinline__ int valid_rows(const RowGeom& g, int page) {
     return page < g.npages ? min(kPage, g.j1 - (g.j0 + kPage * page)) : 0;
 }
 
+// Infinities and NaNs among the eight bf16 at shared address `addr` become 0. For V rows of tokens that a row
+// may not see: a weight of 0 would not keep them out of its sum. A row that does see such a token has a NaN
+// score (or an infinite one that takes no part) and needs no help from V.
+__device__ __forceinline__ void zero_nonfinite(uint32_t addr) {
+    auto bad = [](uint32_t& w) -> bool {
+        uint32_t x = w;
+        if ((w & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+        if ((w & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
+        const bool found = x != w;
+        w = x;
+        return found;
+    };
+    uint4 v = ptx::lds_u4(addr);
+    if (bad(v.x) | bad(v.y) | bad(v.z) | bad(v.w)) ptx::sts_u4(addr, v);
+}
+
 }  // namespace dec
 }  // namespace mla

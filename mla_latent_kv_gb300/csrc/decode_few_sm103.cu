@@ -139,7 +139,8 @@ __device__ __forceinline__ uint4 widen8(uint2 v) {
 // Hint: bring the 128-byte line at `ptr` into L2 (no effect on correctness).
 __device__ __forceinline__ void prefetch_l2(const void* ptr) { asm volatile("prefetch.global.L2 [%0];" ::"l"(ptr)); }
 
-template <int NH, bool kFp8>
+// kTree: a request's drafts as one row, see DecodeArgs.
+template <int NH, bool kFp8, bool kTree>
 __global__ void __launch_bounds__(threads_of(kFp8), 1)
     decode_few_kernel(const __grid_constant__ CUtensorMap pair_map, const __grid_constant__ CUtensorMap rope_map,
                       const __grid_constant__ CUtensorMap q_map, const DecodeArgs p) {
@@ -336,6 +337,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1)
             l[k] = lt[k] = 0.f;
         }
         // FP8: (k_scale, v_scale) of this thread's token, a page ahead; 0 where there is no token
+        const int drafts0 = kTree ? drafts_start(p, g.b) : 0;  // trees: tokens before the drafts
         float2 scale = make_float2(0.f, 0.f), scale_next = scale;
         int blk_next = -1;  // the block two pages ahead
         auto block_of = [&](int i) -> int {
@@ -377,7 +379,19 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1)
                 for (int k = 0; k < NH; ++k) {  // tokens past the last and heads past H have no weight
                     if (kFp8) s[k] = __float_as_uint(__uint_as_float(s[k]) * scale.x);  // K = codes * k_scale
                     if (!okS || token >= valid || h0 + k >= p.H) s[k] = __float_as_uint(-CUDART_INF_F);
-                    need |= __uint_as_float(s[k]) * sl2 > m[k] + kRescaleThreshold;
+                    if (!kTree) need |= __uint_as_float(s[k]) * sl2 > m[k] + kRescaleThreshold;
+                }
+                if (kTree) {
+                    // Which of its heads see this thread's token. The masks are read behind the scores' wait,
+                    // which the wait for the kernel ahead precedes.
+                    const int draft = g.j0 + kPage * i + token - drafts0;
+                    if (draft >= 0 && okS) {
+#pragma unroll
+                        for (int k = 0; k < NH; ++k)
+                            if (draft >= kTreeMaxDrafts || !(draft_mask(p, g.b, h0 + k) >> draft & 1)) s[k] = __float_as_uint(-CUDART_INF_F);
+                    }
+#pragma unroll
+                    for (int k = 0; k < NH; ++k) need |= __uint_as_float(s[k]) * sl2 > m[k] + kRescaleThreshold;
                 }
             }
             const bool any = named_bar_or(kBarOr, kWork, need);
@@ -435,7 +449,9 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1)
                     const float e = fast_exp2(fmaf(__uint_as_float(s[k]), sl2, -m[k]));
                     // V = codes * v_scale: the scale multiplies the weight before its one rounding, and
                     // both sums are of the unscaled weights
-                    const uint32_t r = pack_bf16x2(kFp8 ? e * scale.y : e, 0.f) & 0xffffu;
+                    // (trees: a hidden token has no weight, whatever its scale is)
+                    const bool hidden = kTree && kFp8 && s[k] == __float_as_uint(-CUDART_INF_F);
+                    const uint32_t r = hidden ? 0u : pack_bf16x2(kFp8 ? e * scale.y : e, 0.f) & 0xffffu;
                     lt[k] += e;
                     if (!kFp8) l[k] += bf16_lo_f(r);
                     *reinterpret_cast<uint16_t*>(pb + h * 128 + (((token >> 3) ^ (h & 7)) << 4) + (token & 7) * 2) =
@@ -448,6 +464,13 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1)
                     const int slot = (4 * i + (pn >> 1)) % Lay::kPairs;
                     *reinterpret_cast<uint4*>(smem + Lay::kRing + slot * kPair + (pn & 1) * kPanel + row * 128 + c * 16) =
                         make_uint4(0, 0, 0, 0);
+                }
+            }
+            if (kTree && !kFp8 && g.j0 + kPage * (i + 1) > drafts0) {  // the page's drafts, hidden from some heads
+                for (int q = wtid; q < 8 * kPanel / 16; q += kWork) {
+                    const int pn = q / (kPanel / 16);
+                    zero_nonfinite(sbase + Lay::kRing + (uint32_t)(((4 * i + (pn >> 1)) % Lay::kPairs) * kPair + (pn & 1) * kPanel +
+                                                                  16 * (q % (kPanel / 16))));
                 }
             }
             fence_proxy_async_cta();  // P and the zeros, before the MMAs read them
@@ -611,14 +634,14 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1)
     if (warp == 1) tmem_dealloc(tmem, Lay::kCols);
 }
 
-template <int NH, bool kFp8>
+template <int NH, bool kFp8, bool kTree>
 cudaError_t launch(const DecodeArgs& a, cudaStream_t s) {
     static int done[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !done[dev]) {
-        e = cudaFuncSetAttribute(decode_few_kernel<NH, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<NH>::kBytes);
+        e = cudaFuncSetAttribute(decode_few_kernel<NH, kFp8, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<NH>::kBytes);
         if (e != cudaSuccess) return e;
         if (dev < 64) done[dev] = 1;
     }
@@ -644,15 +667,20 @@ cudaError_t launch(const DecodeArgs& a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
     }
     const int64_t units = a.plan_units ? a.plan_max_units : (int64_t)a.rows * a.num_splits;
-    return launch_pdl(decode_few_kernel<NH, kFp8>, dim3((unsigned)units), dim3(threads_of(kFp8)), Layout<NH>::kBytes, s, pair_map,
+    return launch_pdl(decode_few_kernel<NH, kFp8, kTree>, dim3((unsigned)units), dim3(threads_of(kFp8)), Layout<NH>::kBytes, s, pair_map,
                       rope_map, q_map, a);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_few_sm103(const DecodeArgs& a, cudaStream_t s) {
-    if (a.kv_dtype == MLA_KV_FP8_E4M3_SCALED) return a.H <= 16 ? launch<8, true>(a, s) : launch<16, true>(a, s);
-    return a.H <= 16 ? launch<8, false>(a, s) : launch<16, false>(a, s);
+    const bool few = a.H <= 16;
+    if (a.kv_dtype == MLA_KV_FP8_E4M3_SCALED) {
+        if (a.masks) return few ? launch<8, true, true>(a, s) : launch<16, true, true>(a, s);
+        return few ? launch<8, true, false>(a, s) : launch<16, true, false>(a, s);
+    }
+    if (a.masks) return few ? launch<8, false, true>(a, s) : launch<16, false, true>(a, s);
+    return few ? launch<8, false, false>(a, s) : launch<16, false, false>(a, s);
 }
 
 }  // namespace mla

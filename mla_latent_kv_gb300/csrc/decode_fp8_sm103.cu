@@ -165,6 +165,8 @@ __device__ __forceinline__ uint4 widen8(uint2 v) {
     return o;
 }
 
+// kTree: a request's drafts as one row, see DecodeArgs.
+template <bool kTree>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     decode_fp8_kernel(const __grid_constant__ CUtensorMap raw_map, const __grid_constant__ CUtensorMap q_map,
                       const __grid_constant__ CUtensorMap o_map, const __grid_constant__ CUtensorMap p_map,
@@ -363,6 +365,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // Both sums are of the unscaled weights exp(s - m): v_scale only enters P as the MMA
             // sees it. Each half keeps its own sums (same running max); they are added at the end.
             float m_run = kNoMax, l_run = 0.f, lt_run = 0.f;
+            // trees: the drafts that the row sees, and its tokens before them. Read behind the wait for Q, which
+            // the wait for the kernel ahead precedes.
+            const uint64_t mask = kTree && npages > 0 ? draft_mask(p, g.b, row) : 0;
+            const int drafts0 = kTree ? drafts_start(p, g.b) : 0;
             const uint32_t pbuf_remote = map_to_rank(sbase + OFF_PB, 1);
             const uint32_t pfull_remote = map_to_rank(bar(B_PFULL), 1);
             for (int gi = 0; gi < ngroups; ++gi) {
@@ -416,6 +422,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         for (int j = 0; j < 32; ++j)
                             if (32 * c + j >= valid) s[c][j] = __float_as_uint(-CUDART_INF_F);
                 }
+                const int at = kTree ? g.j0 + kPage * page - drafts0 : 0;  // the page's first token among the drafts
+                const bool drafts = kTree && at > -kPage;
+                if (drafts) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t seen = seen_tokens(mask, at + 32 * c);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (!(seen >> j & 1u)) s[c][j] = __float_as_uint(-CUDART_INF_F);
+                    }
+                }
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -455,6 +472,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
                 warp_arrive(bar(B_SCEMPTY + sb), lane);
+                if (drafts) {  // a hidden draft's weight is 0 whatever its scale is
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t seen = seen_tokens(mask, at + 32 * c);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            pk[16 * c + j] &= (seen >> (2 * j) & 1u ? 0xffffu : 0u) | (seen >> (2 * j + 1) & 1u ? 0xffff0000u : 0u);
+                    }
+                }
                 // P goes to CTA 1 as one bulk copy per page from this half's staging buffer (the
                 // copy engine moves it; per-thread remote stores would queue behind the converter
                 // warps' shared-memory traffic). The buffer is rewritten only after the previous
@@ -771,18 +797,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();
 }
 
-int g_attr_done[64] = {};
+int g_attr_done[2][64] = {};
 
 }  // namespace
 
 cudaError_t launch_decode_fp8_sm103(const DecodeArgs& a, cudaStream_t s) {
+    const bool tree = a.masks != nullptr;
+    auto* kernel = tree ? decode_fp8_kernel<true> : decode_fp8_kernel<false>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev < 64 && !g_attr_done[dev]) {
-        e = cudaFuncSetAttribute(decode_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (dev < 64 && !g_attr_done[tree][dev]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         if (e != cudaSuccess) return e;
-        g_attr_done[dev] = 1;
+        g_attr_done[tree][dev] = 1;
     }
     CUtensorMap raw_map, q_map, o_map, p_map;
     memset(&raw_map, 0, sizeof raw_map);
@@ -824,7 +852,7 @@ cudaError_t launch_decode_fp8_sm103(const DecodeArgs& a, cudaStream_t s) {
         e = encode_tmap(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.q, qdims, qstrides, qbox, true);
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl(decode_fp8_kernel, dim3((unsigned)(2 * units)), dim3(kThreads), kSmemBytes, s, raw_map, q_map,
+    return launch_pdl(kernel, dim3((unsigned)(2 * units)), dim3(kThreads), kSmemBytes, s, raw_map, q_map,
                       o_map, p_map, a);
 }
 

@@ -129,15 +129,12 @@ enum : int {
     B_STATS = B_PEER + kPBufs,          // CTAs 2, 3: final row statistics written, last P copy issued
     B_VLAND,                            // [2] trees, CTAs 2, 3: this CTA's half of a drafted page's V landed
     B_VCLEAN = B_VLAND + 2,             // [2] trees, CTA 2: both halves hold no NaN (16 warps)
-    B_WIDE = B_VCLEAN + 2,              // [kTreeRing] trees, FP8, all: both pages of the group are widened
-    B_WIDEN = B_WIDE + kTreeRing,       // [kTreeRing] trees, FP8, CTAs 2, 3: this CTA's page of the group is (8 warps)
-    B_COUNT = B_WIDEN + kTreeRing
+    B_COUNT = B_VCLEAN + 2
 };
-static_assert(8 * B_COUNT <= 640, "barrier slots");
-static_assert(kTreeRing <= kPBufs, "a parity wait tells a ring slot's use from the one before it");
+static_assert(8 * B_COUNT <= 512, "barrier slots");
 constexpr int kRelayWarps = 4;    // of CTA 3, from warp 6 on: pages announced to CTA 2 in turn
-constexpr int OFF_TMEM = 640;
-constexpr int OFF_ABORT = 644;
+constexpr int OFF_TMEM = 512;
+constexpr int OFF_ABORT = 516;
 constexpr int OFF_MX = 1024;      // scores: f32 [4][128] exchange between the column quarters
 constexpr int OFF_STAT_M = 2048;  // output: f32 [128] final running max (log2 units)
 constexpr int OFF_STAT_L = 2560;  // output: f32 [128] row sum
@@ -156,56 +153,6 @@ __device__ __forceinline__ uint4 widen8(uint2 v) {
     e4m3x4_to_bf16x4(v.x, w.x, w.y);
     e4m3x4_to_bf16x4(v.y, w.z, w.w);
     return w;
-}
-
-// Both bf16 of the word with an infinity or NaN replaced by 0; whether there was one.
-__device__ __forceinline__ bool zero_nonfinite(uint32_t& w) {
-    uint32_t x = w;
-    if ((w & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
-    if ((w & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
-    const bool found = x != w;
-    w = x;
-    return found;
-}
-
-// The widening warps of one output CTA: page kPPG g + side of every group g of the unit, and its scales.
-template <int kWarps, class Block, class Slot, class Free, class Done>
-__device__ __forceinline__ void widen_pages(const PrefixArgs& p, int tid, int side, int npages, int ngroups, Block page_block,
-                                            Slot ring_slot, Free wait_free, Done done) {
-    constexpr int kN = 32 * kWarps, kChunks = kPage * kD / 8, kLoads = kChunks / kN;  // 8 codes a load
-    static_assert(kChunks % kN == 0 && kN >= kPage, "a page's chunks");
-    uint2 v[kLoads];
-    float2 sc = make_float2(0.f, 0.f);
-    auto load = [&](int g) {
-        const int page = kPPG * g + side;
-        const int blk = page < npages ? page_block(page) : -1;
-        const uint8_t* src = p.cache + (size_t)max(blk, 0) * (kPage * kFp8RowBytes);
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k) {  // a row's 72 chunks are followed by its scales
-            const int c = k * kN + tid;
-            v[k] = make_uint2(0u, 0u);
-            if (blk >= 0) v[k] = __ldcg(reinterpret_cast<const uint2*>(src + 8 * (c + c / (kD / 8))));
-        }
-        sc = make_float2(0.f, 0.f);
-        if (blk >= 0 && tid < kPage) sc = __ldcg(reinterpret_cast<const float2*>(src + tid * kFp8RowBytes + kD));
-    };
-    load(0);
-    for (int g = 0; g < ngroups; ++g) {
-        if (g >= kTreeRing && !wait_free(g)) break;
-        const size_t slot = ring_slot(g);
-        uint4* dst = reinterpret_cast<uint4*>(p.ring + (slot * kPPG + side) * (kPage * kBf16RowBytes));
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k) dst[k * kN + tid] = widen8(v[k]);
-        if (tid < kPage) {  // k_scales and v_scales of the slot: [2][64] each
-            float* s = p.ring_scales + slot * 2 * kPPG * kPage + side * kPage + tid;
-            s[0] = sc.x;
-            s[kPPG * kPage] = sc.y;
-        }
-        if (g + 1 < ngroups) load(g + 1);
-        fence_proxy_async_all();  // the copies read what ordinary stores wrote
-        __syncwarp();
-        if (tid % 32 == 0) done(g);
-    }
 }
 
 template <bool kScaled, bool kTree>
@@ -274,8 +221,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             if (i >= B_READY && i < B_READY + kPBufs) cnt = 5;
             if (i >= B_PEER && i < B_PEER + kPBufs) cnt = 4;
             if (i >= B_VCLEAN && i < B_VCLEAN + 2) cnt = 2 * kAuxWarps;
-            if (i >= B_WIDE && i < B_WIDE + kTreeRing) cnt = 2;
-            if (i >= B_WIDEN && i < B_WIDEN + kTreeRing) cnt = kAuxWarps;
             bar_init(bar(i), cnt);
         }
         if (!scores)  // P buffers armed for their first message before a scores CTA can send one
@@ -303,24 +248,14 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         }
         return blk;
     };
-    // The ring slot of a group of widened pages (trees, FP8), in groups.
-    auto ring_slot = [&](int g) -> size_t { return (size_t)unit * kTreeRing + g % kTreeRing; };
     // First row of the unit's page i behind the keys' tensor map (out of range: TMA fills zeros).
     auto page_row = [&](int i) -> int {
         if (i >= npages) return p.key_rows;
-        if (kTree && kScaled) return ((int)ring_slot(i / kPPG) * kPPG + i % kPPG) * kPage;
+        if (kTree && kScaled) return (req * p.wide_pages + page0 + i) * kPage;
         if (!kTree && !p.block_table) return (page0 + i) * kPage;  // widened prefix: its pages in order
         const int blk = page_block(i);
         return blk < 0 ? p.key_rows : blk * kPage;
     };
-    // Trees, FP8: the group's pages are widened. Their bytes were written by ordinary stores and are read by
-    // TMA copies (`tma`) or ordinary loads.
-    auto wait_wide = [&](int g, bool tma) -> bool {
-        const bool ok = wait_bar<true>(bar(B_WIDE + g % kTreeRing), (g / kTreeRing) & 1, abort, ds);
-        if (tma) fence_proxy_async_all();
-        return ok;
-    };
-
     if (scores) {
         if (warp == 0) {
             if (lane == 0 && npages > 0) {
@@ -333,7 +268,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 int issued = 0;
                 bool ok = true;
                 for (int gi = 0; gi < ngroups && ok; ++gi) {
-                    if (kTree && kScaled && !(ok = wait_wide(gi, true))) break;
                     const int y = page_row(kPPG * gi + side);
                     for (int t = 0; t < 3; ++t) {
                         const int m = 3 * gi + t, slot = m % kSlots, k = m / kSlots;
@@ -449,7 +383,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             const int64_t flat = (int64_t)rows0 + row;
             uint64_t mask = 0;  // trees: the drafted tokens that the row sees
             if (kTree && flat < p.flat_rows) {
-                mask = p.masks[(size_t)req * p.Sq + (int)flat / p.H];
+                mask = __ldcg(reinterpret_cast<const unsigned long long*>(p.masks) + (size_t)req * p.Sq + (int)flat / p.H);
                 if (p.Sq < 64) mask &= (1ull << p.Sq) - 1;
             }
             if (!kTree && flat < p.flat_rows) {
@@ -490,13 +424,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 const int page = kPPG * gi + pg2, buf = gi & 1;
                 size_t sc = 0;               // the quarter's first token of the page, in float4 units
                 float4 ks[kScaled ? 8 : 1];  // k_scale of its 32 tokens
-                if constexpr (kScaled) {  // plain loads: the widening kernel or warps wrote them while this one ran
-                    if constexpr (kTree) {
-                        wait_wide(gi, false);
-                        sc = (ring_slot(gi) * 2 * kPPG * kPage + (page < npages ? pg2 : 0) * kPage + 32 * sub) / 4;
-                    } else {
-                        sc = ((size_t)(page0 + min(page, npages - 1)) * kPage + 32 * sub) / 4;
-                    }
+                if constexpr (kScaled) {  // plain loads: the widening kernel wrote them while this one began
+                    const size_t first = kTree ? (size_t)req * p.wide_pages + page0 : (size_t)page0;
+                    sc = ((first + min(page, npages - 1)) * kPage + 32 * sub) / 4;
                     const float4* src = reinterpret_cast<const float4*>(p.k_scales) + sc;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) ks[j] = src[j];
@@ -532,10 +462,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     // bit c: the row sees token 32 sub + c of the page. Everything before the drafted tokens is
                     // seen, what is behind them (past the request's end too) is not.
                     const int at = (page0 + page) * kPage + 32 * sub - drafts0;
-                    const uint32_t seen = at >= 64    ? 0u
-                                          : at >= 0   ? (uint32_t)(mask >> at)
-                                          : at > -32  ? ((uint32_t)mask << -at) | ((1u << -at) - 1u)
-                                                      : 0xffffffffu;
+                    const uint32_t seen = seen_tokens(mask, at);
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (!(seen >> j & 1u)) {
@@ -638,7 +565,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 tma_prefetch_desc(&v_map);
                 int issued = 0;
                 for (int i = 0; i < npages; ++i) {
-                    if (kTree && kScaled && i % kPPG == 0 && !wait_wide(i / kPPG, true)) break;
                     const int y = page_row(i);
                     const int st = i % kVStages, k = i / kVStages;
                     if (k > 0 && !wait_bar<true>(bar(B_VEMPTY + st), (k - 1) & 1, abort, ds)) break;
@@ -756,25 +682,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                         const uint32_t v = sbase + OFF_V + (i % kVStages) * kVStageBytes + 16u * (uint32_t)(tid - 32 * kAuxWarp0);
 #pragma unroll
                         for (int c = 0; c < kVStageBytes; c += 32 * kAuxWarps * 16) {
-                            uint4 x = lds_u4(v + c);
-                            if (zero_nonfinite(x.x) | zero_nonfinite(x.y) | zero_nonfinite(x.z) | zero_nonfinite(x.w))
-                                sts_u4(v + c, x);
+                            dec::zero_nonfinite(v + c);
                         }
                         fence_proxy_async_cta();
                         __syncwarp();
                         if (lane == 0) bar_arrive_remote(bar(B_VCLEAN + i - drafted), 2);
                     }
                 }
-            }
-            if constexpr (kTree && kScaled) {
-                // CTA 2 + i widens page 2 g + i of each group into the group's slot of the unit's ring in the
-                // workspace (which stays in L2), codes a page ahead in registers.
-                if (warp >= kAuxWarp0) widen_pages<kAuxWarps>(p, tid - 32 * kAuxWarp0, side, npages, ngroups, page_block, ring_slot,
-                    [&](int g) {  // the slot's last pages have been scored and summed by then
-                        const int pg = kPPG * (g - kTreeRing) + 1;
-                        return warp_wait<true>(bar(B_PEMPTY + pg % kPBufs), (pg / kPBufs) & 1, abort, ds);
-                    },
-                    [&](int g) { bar_arrive(bar(B_WIDEN + g % kTreeRing)); });
             }
             __syncwarp();
             const bool has_o = npages > 0 && pages_ready == npages && !*abort;
@@ -799,14 +713,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             else
                 store_rows<true, 4, 3, kBarEpi>(smem, sbase, OFF_V, tmem + lane_base, row, eset, (ctid & 127) == 0, true,
                                                 empty, inv, &o_map, rows0, slab, rows0 < p.flat_rows);
-        } else if (kTree && kScaled && lane == 0) {
-            // Warp 18 tells all four CTAs of each widened page: the release at cluster scope takes most of a
-            // microsecond, which the widening warps need not spend.
-            for (int g = 0; g < ngroups; ++g) {
-                if (!wait_bar(bar(B_WIDEN + g % kTreeRing), (g / kTreeRing) & 1, abort, ds)) break;
-                fence_acq_rel_cluster();
-                for (uint32_t r = 0; r < 4; ++r) bar_arrive_remote_relaxed(bar(B_WIDE + g % kTreeRing), r);
-            }
         }
     }
 
@@ -818,31 +724,36 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------------------------------
-// FP8 prefix -> bf16 rows (exact) and scales, once per call. One warp per token: lanes take
-// 8-byte chunks of the 576 codes.
+// FP8 pages -> bf16 rows (exact) and scales, once per call: the prefix's, or those of every request of a
+// tree call. One warp per token: lanes take 8-byte chunks of the 576 codes.
 // ------------------------------------------------------------------------------------------
+template <bool kTree>
 __global__ void __launch_bounds__(256) prefix_widen_kernel(PrefixArgs p, const uint8_t* cache, uint16_t* x,
                                                            float* k_scales, float* v_scales) {
     griddep_wait();
     griddep_launch_dependents();
     const int token = (int)blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (token >= p.prefix_pages * kPage) return;
-    const int32_t blk = p.block_table[token / kPage];
+    const int req = kTree ? (int)blockIdx.y : 0;
+    // a tree's last page is widened whole: its rows behind the request's end are not seen
+    const int tokens = kTree ? (min(max(p.seq_lens[req], 0), p.max_seq_len) + kPage - 1) / kPage * kPage : p.prefix_pages * kPage;
+    if (token >= tokens) return;
+    const int32_t blk = p.block_table[(kTree ? (size_t)req * p.max_blocks : (size_t)0) + token / kPage];
     const bool bad = blk < 0 || (int64_t)blk >= p.num_blocks;
     if (bad && lane == 0 && p.dev_status) atomicOr(p.dev_status, MLA_DEV_BAD_BLOCK_ID);
     const uint8_t* src = cache + ((size_t)(bad ? 0 : blk) * kPage + token % kPage) * kFp8RowBytes;
+    const size_t row = kTree ? (size_t)req * p.wide_pages * kPage + token : (size_t)token;
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
         const int c = lane + 32 * i;
         if (c >= kD / 8) continue;
         uint2 v = make_uint2(0u, 0u);
         if (!bad) v = *reinterpret_cast<const uint2*>(src + 8 * c);
-        *reinterpret_cast<uint4*>(x + (size_t)token * kD + 8 * c) = widen8(v);
+        *reinterpret_cast<uint4*>(x + row * kD + 8 * c) = widen8(v);
     }
     if (lane == 0) {
         const float2 sc = bad ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2*>(src + kD);
-        k_scales[token] = sc.x;
-        v_scales[token] = sc.y;
+        k_scales[row] = sc.x;
+        v_scales[row] = sc.y;
     }
 }
 
@@ -949,7 +860,7 @@ void prefix_split(int64_t flat_rows, int pages, int clusters, int* splits, int* 
 
 cudaError_t launch_prefix_widen(const PrefixArgs& a, const uint8_t* cache, uint16_t* widened, float* scales,
                                 cudaStream_t s) {
-    return launch_pdl(prefix_widen_kernel, dim3((unsigned)(a.prefix_pages * kPage / 8)), dim3(256), 0, s, a, cache,
+    return launch_pdl(prefix_widen_kernel<false>, dim3((unsigned)(a.prefix_pages * kPage / 8)), dim3(256), 0, s, a, cache,
                       widened, scales, scales + (size_t)a.prefix_pages * kPage);
 }
 
@@ -1002,8 +913,10 @@ void tree_split(int64_t units, int64_t flat_rows, int pages, int clusters, int* 
     }
 }
 
-cudaError_t launch_decode_tree(const PrefixArgs& in, bool fp8, bool out_f32, void* out, cudaStream_t s) {
+cudaError_t launch_decode_tree(const PrefixArgs& in, const uint8_t* cache, uint16_t* widened, float* scales, bool out_f32,
+                               void* out, cudaStream_t s) {
     PrefixArgs a = in;
+    const bool fp8 = widened != nullptr;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -1012,14 +925,19 @@ cudaError_t launch_decode_tree(const PrefixArgs& in, bool fp8, bool out_f32, voi
     const int64_t units = (int64_t)a.splits * a.B * a.tiles;
     uint64_t rows = (uint64_t)a.num_blocks * kPage;
     if (fp8) {
-        a.k_scales = a.ring_scales;
-        a.v_scales = a.ring_scales + kPPG * kPage;
-        rows = (uint64_t)units * kTreeRing * kPPG * kPage;
+        rows = (uint64_t)a.B * a.wide_pages * kPage;
+        a.k_scales = scales;
+        a.v_scales = scales + rows;
+        if (rows > 0) {
+            e = launch_pdl(prefix_widen_kernel<true>, dim3((unsigned)(a.wide_pages * kPage / 8), (unsigned)a.B), dim3(256), 0, s,
+                           a, cache, widened, scales, scales + rows);
+            if (e != cudaSuccess) return e;
+        }
     }
     a.key_rows = (int)rows;
     a.o_bf16 = !out_f32;
     CUtensorMap k_map, v_map, q_map, o_map;
-    e = encode_maps(a, fp8 ? a.ring : a.cache, rows, (uint64_t)a.B, out, out_f32, (uint64_t)a.splits * a.B, &k_map, &v_map, &q_map,
+    e = encode_maps(a, fp8 ? (const void*)widened : cache, rows, (uint64_t)a.B, out, out_f32, (uint64_t)a.splits * a.B, &k_map, &v_map, &q_map,
                     &o_map);
     if (e != cudaSuccess) return e;
     return launch_pdl(kernel_of(fp8, true), dim3((unsigned)(4 * units)), dim3(kThreads), kSmemBytes, s, k_map, v_map, q_map, o_map,

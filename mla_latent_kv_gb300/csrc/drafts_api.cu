@@ -63,24 +63,33 @@ mla_status rope_args(const char* who, const void* x, int64_t x_t, int64_t x_n, c
 }
 
 // ------------------------------------------------------------------------------------ tree
-// How a tree call runs, and its workspace: the rings of widened pages (FP8), then the partial states.
+// How a tree call runs, and its workspace. At most 128 (draft, head) pairs are one row of so many heads for
+// the decode kernels (splits: theirs); more go 256 at a time through the prefix kernel, over each request's
+// pages: the widened rows (FP8), then the partial states.
 struct TreePlan {
-    int tiles, splits, pages_per_split;
-    int64_t units;
-    size_t ring, scales, part_o, part_lse, total;
+    bool rows;
+    int splits, tiles, pages_per_split, wide_pages;
+    size_t scales, part_o, part_lse, total;
 };
 bool plan_tree(mla_kv_dtype kv, int B, int Sq, int H, int max_seq_len, TreePlan* w) {
+    const int64_t flat = (int64_t)Sq * H;
+    const int pages = (max_seq_len + mla::kPage - 1) / mla::kPage;
+    w->rows = flat <= MLA_MAX_HEADS;
+    if (w->rows) {
+        const bool few = mla::few_heads((int)flat);
+        w->splits = mla::resolve_splits(few, -1, B, (int)flat, max_seq_len);
+        if (w->splits < 1 && w->splits != -2) return false;
+        w->total = mla::workspace_layout(kv, B, B, (int)flat, w->splits, max_seq_len).total;
+        return true;
+    }
     const int clusters = mla::prefix_clusters();
     if (clusters < 1) return false;
-    const int64_t flat = (int64_t)Sq * H;
     w->tiles = (int)((flat + 255) / 256);
-    mla::tree_split((int64_t)B * w->tiles, B * flat, (max_seq_len + mla::kPage - 1) / mla::kPage, clusters, &w->splits,
-                    &w->pages_per_split);
-    w->units = (int64_t)B * w->tiles * w->splits;
+    mla::tree_split((int64_t)B * w->tiles, B * flat, pages, clusters, &w->splits, &w->pages_per_split);
     size_t off = 0;
     if (kv == MLA_KV_FP8_E4M3_SCALED) {
-        const size_t rows = (size_t)w->units * mla::kTreeRing * mla::kTreeGroup;
-        w->ring = off;
+        w->wide_pages = pages;
+        const size_t rows = (size_t)B * pages * mla::kPage;
         off += up256(rows * mla::kBf16RowBytes);
         w->scales = off;
         off += up256(rows * 2 * sizeof(float));
@@ -224,12 +233,23 @@ mla_status mla_decode_tree(const void* q, const void* kv_cache, mla_kv_dtype kv_
     TreePlan w{};
     if (!plan_tree(kv_dtype, B, Sq, H, max_seq_len, &w))
         return set_error(MLA_ERR_CUDA, "%s: could not plan the call (no CUDA device?)", who);
-    if (w.units > INT32_MAX / 4) return set_error(MLA_ERR_UNSUPPORTED, "%s: %lld work units too many", who, (long long)w.units);
+    if (!w.rows && ((int64_t)w.splits * B * w.tiles > INT32_MAX / 4 || (int64_t)B * w.wide_pages > INT32_MAX / mla::kPage || B > 65535))
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: %d requests of %d tokens too many", who, B, max_seq_len);
     if (w.total > 0 && (!workspace || workspace_bytes < w.total))
         return set_error(MLA_ERR_WORKSPACE_TOO_SMALL, "%s: workspace %zu bytes < %zu needed", who,
                          workspace ? workspace_bytes : (size_t)0, w.total);
     if (w.total > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return set_error(MLA_ERR_UNSUPPORTED, "%s: workspace must be 256-byte aligned", who);
+    if (w.rows) {
+        x.check_only = false;
+        x.few = mla::few_heads(Sq * H);
+        x.masks = tree_mask;
+        x.tree_drafts = Sq;
+        x.tree_heads = H;
+        return mla::decode_impl(q, kv_cache, kv_dtype, num_blocks, block_table, max_blocks, seq_lens, nullptr, max_seq_len, B, 1,
+                                B, Sq * H, scale, w.splits, workspace, workspace_bytes, o_latent, o_dtype, lse, dev_status,
+                                stream, x);
+    }
     const bool fp8 = kv_dtype == MLA_KV_FP8_E4M3_SCALED;
     char* ws = (char*)workspace;
     mla::PrefixArgs a{};
@@ -249,20 +269,17 @@ mla_status mla_decode_tree(const void* q, const void* kv_cache, mla_kv_dtype kv_
     a.H = H;
     a.scale = scale;
     a.masks = tree_mask;
-    a.cache = (const uint8_t*)kv_cache;
     a.lse = lse;
     a.dev_status = dev_status;
-    if (fp8) {
-        a.ring = (uint8_t*)(ws + w.ring);
-        a.ring_scales = (float*)(ws + w.scales);
-    }
+    a.wide_pages = w.wide_pages;
     if (w.splits > 1) {
         a.part_o = (float*)(ws + w.part_o);
         a.part_lse = (float*)(ws + w.part_lse);
     }
     cudaStream_t s = (cudaStream_t)stream;
     const bool f32 = w.splits > 1 || o_dtype == MLA_DT_F32;
-    cudaError_t e = mla::launch_decode_tree(a, fp8, f32, w.splits > 1 ? (void*)a.part_o : o_latent, s);
+    cudaError_t e = mla::launch_decode_tree(a, (const uint8_t*)kv_cache, fp8 ? (uint16_t*)ws : nullptr, (float*)(ws + w.scales), f32,
+                                            w.splits > 1 ? (void*)a.part_o : o_latent, s);
     if (e != cudaSuccess) return cuda_error(e, who);
     if (w.splits > 1) {
         mla::DecodeArgs m{};  // every row's states are "pre" states, none its own

@@ -61,7 +61,30 @@ struct DecodeArgs {
     const int* plan_count;      // [0] units actually planned, [1] split rows (rows with partials)
     const int* plan_split_rows; // the split rows' indices, plan_count[1] of them
     int plan_max_units;         // the grid is sized for this many units
+    // Trees of at most 128 (draft, head) pairs: one query row a request, whose "heads" are the pairs. Pair h
+    // is draft h / tree_heads and sees the bits of its mask among the request's last tree_drafts tokens.
+    const uint64_t* masks;      // [B, tree_drafts], null: no tree
+    int tree_drafts, tree_heads;
 };
+
+// Tokens of request b before its drafts (below 0: the first drafts are not there).
+__device__ __forceinline__ int drafts_start(const DecodeArgs& p, int b) {
+    return min(max(p.seq_lens[b], 0), p.max_blocks * MLA_PAGE_SIZE) - p.tree_drafts;
+}
+// The drafts that pair h of request b sees; none for pairs past the last.
+__device__ __forceinline__ uint64_t draft_mask(const DecodeArgs& p, int b, int h) {
+    if (h >= p.H) return 0;
+    const uint64_t m = __ldcg(reinterpret_cast<const unsigned long long*>(p.masks) + (size_t)b * p.tree_drafts + h / p.tree_heads);
+    return p.tree_drafts < 64 ? m & ((1ull << p.tree_drafts) - 1) : m;
+}
+// Bit c: the token `at + c` places behind the request's first draft is seen (c < 32). Those before the
+// drafts are, those behind the last are not.
+__device__ __forceinline__ uint32_t seen_tokens(uint64_t mask, int at) {
+    return at >= 64    ? 0u
+           : at >= 0   ? (uint32_t)(mask >> at)
+           : at > -32  ? ((uint32_t)mask << -at) | ((1u << -at) - 1u)
+                       : 0xffffffffu;
+}
 
 // Request b, position t and query length of query row r: uniform rows are r = b * Sq + t;
 // packed rows belong to the last request whose first row is <= r (binary search of qsl).
@@ -220,6 +243,8 @@ struct DecodeExtra {
     const float* pre_o = nullptr;
     const float* pre_lse = nullptr;
     int pre_splits = 0;
+    const uint64_t* masks = nullptr;  // see DecodeArgs
+    int tree_drafts = 0, tree_heads = 0;
 };
 mla_status decode_impl(const void* q, const void* kv_cache, mla_kv_dtype kv_dtype, int64_t num_blocks,
                        const int32_t* block_table, int max_blocks, const int32_t* seq_lens, const int32_t* qsl,
@@ -258,17 +283,16 @@ struct PrefixArgs {
     // (part_o null: one split, written to the final outputs).
     int B, tiles, max_blocks;
     const uint64_t* masks;      // [B, Sq]
-    const uint8_t* cache;
     float* lse;                 // final, or null
     int o_bf16;                 // final output in bf16
-    uint8_t* ring;              // FP8: [units, kTreeRing, 2 pages] widened rows,
-    float* ring_scales;         // and [units, kTreeRing, 2, 2 pages] their k_scales and v_scales
+    int wide_pages;             // FP8: pages of each request's widened rows, [B, wide_pages, 64]
 };
-constexpr int kTreeRing = 4;    // groups of two pages that a unit widens ahead
-constexpr int kTreeGroup = 2 * kPage;
 constexpr int kTreeMaxDrafts = 64;  // bits of a mask
 void tree_split(int64_t units, int64_t flat_rows, int pages, int clusters, int* splits, int* pages_per_split);
-cudaError_t launch_decode_tree(const PrefixArgs& a, bool fp8, bool out_f32, void* out, cudaStream_t s);
+// FP8: the requests' rows are first widened to `widened` [B, wide_pages, 64, 576], their scales to `scales`
+// [2, B, wide_pages, 64].
+cudaError_t launch_decode_tree(const PrefixArgs& a, const uint8_t* cache, uint16_t* widened, float* scales, bool out_f32,
+                               void* out, cudaStream_t s);
 int prefix_clusters();  // clusters of the prefix kernel that run at once on the current device, or -1
 void prefix_split(int64_t flat_rows, int pages, int clusters, int* splits, int* pages_per_split);
 // FP8: launch_prefix_widen first writes the prefix's rows to `widened` [prefix tokens, 576] and

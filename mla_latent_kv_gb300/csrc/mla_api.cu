@@ -297,6 +297,9 @@ mla_status decode_impl(const void* q, const void* kv_cache, mla_kv_dtype kv_dtyp
     a.base_step = x.base_step;
     a.all_partial = x.all_partial ? 1 : 0;
     a.order = x.order;
+    a.masks = x.masks;
+    a.tree_drafts = x.tree_drafts;
+    a.tree_heads = x.tree_heads;
     a.pre_o = x.pre_o;
     a.pre_lse = x.pre_lse;
     a.pre_splits = x.pre_splits;

@@ -89,8 +89,6 @@ __device__ __forceinline__ void bar_arrive_remote_relaxed(uint32_t bar, uint32_t
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(ra) : "memory");
 }
 
-__device__ __forceinline__ void fence_acq_rel_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
-
 __device__ __forceinline__ bool bar_try_wait(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -275,9 +273,6 @@ __device__ __forceinline__ void sts_u4(uint32_t addr, uint4 v) {
 __device__ __forceinline__ void fence_proxy_async_cta() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
-
-// The same for every state space: global memory written by ordinary stores and read by bulk copies, too.
-__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // ------------------------------------------------------------------------------------------
 // tcgen05: tensor memory and MMA

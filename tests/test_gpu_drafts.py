@@ -202,6 +202,7 @@ def _tree(c, o_dtype=None, status=None, max_len=None, **kw):
     (1, 1, [1]), (1, 16, [64, 65, 0]), (4, 16, [4, 68, 700]), (5, 3, [5, 6, 63, 64, 69, 70, 128, 133]),
     (64, 2, [64, 65, 127, 128, 190, 191]), (63, 1, [63, 126, 127, 2000]), (7, 128, [7, 900]), (33, 40, [700, 40]),
     (2, 128, [130, 129]), (3, 43, [2, 1, 0, 3, 200]), (64, 128, [64, 100]), (16, 17, [300 + i for i in range(40)]),
+    (2, 16, [2, 65, 66, 129, 200]), (16, 2, [16, 79, 80, 81, 300]), (17, 1, [17, 20, 80]), (3, 11, [3, 130]), (32, 4, [40, 100, 33]),
 ])
 def test_decode_tree(Sq, H, lens, kv):
     c = tree_case(lens, Sq, H, kv, seed=Sq * 1000 + H, scale_v=1.7 if kv == F8 else None)
@@ -215,14 +216,13 @@ def test_decode_tree(Sq, H, lens, kv):
 
 @pytest.mark.parametrize("kv", [BF, F8])
 @pytest.mark.parametrize("B,Sq,H,length,max_len", [(1, 4, 16, 9000, 9000), (3, 3, 128, 2500, 2500), (2, 9, 31, 3000, 40000),
-                                                   (70, 2, 20, 500, 500)])
+                                                   (70, 2, 20, 500, 500), (1, 2, 9, 20000, 20000), (90, 2, 8, 700, 9000), (90, 4, 24, 700, 9000)])
 def test_decode_tree_splits(B, Sq, H, length, max_len, kv):
     """Ranges of a request's pages joined by their log-sums; ranges behind a short request's end are empty."""
     import mla_latent_kv_gb300 as mla
     lens = [length] + [max(Sq, length * (b + 1) // (3 * B) - 17 * b) for b in range(1, B)]
     c = tree_case(lens, Sq, H, kv, seed=length, extra_cols=-(-max_len // PAGE) - -(-length // PAGE))
-    split = mla.decode_tree_workspace_bytes(B, Sq, H, max_len, BF) > 0
-    assert split == (B < 70)
+    assert B > 50 or mla.decode_tree_workspace_bytes(B, Sq, H, max_len, BF) > 0
     want = attend_tree(c)
     check_attention(*_tree(c, max_len=max_len), want)
     check_attention(*_tree(c, max_len=max_len, o_dtype=mla.DT_BF16), want, bf16_out=True)
@@ -248,14 +248,15 @@ def _row(c, b, token):
 
 @pytest.mark.parametrize("kv", [BF, F8])
 @pytest.mark.parametrize("inf", [False, True])
-def test_decode_tree_hidden_drafts_do_not_matter(kv, inf):
+@pytest.mark.parametrize("H", [5, 21, 45])  # 30, 126 and 270 pairs: each of the kernels
+def test_decode_tree_hidden_drafts_do_not_matter(H, kv, inf):
     """Drafts that no row sees, and whatever is behind the end, may hold anything."""
     Sq, lens = 6, [70, 134, 6, 200, 3]
     masks = tree_masks(5, Sq, 3)
     masks[:, :] &= ~(1 << 4)         # nobody sees draft 4
     masks[1, 2] = 0                  # sees the context alone
     masks[2, 1] = 0                  # sees nothing
-    c = tree_case(lens, Sq, 21, kv, 4, masks=masks)
+    c = tree_case(lens, Sq, H, kv, 4, masks=masks)
     want = attend_tree(c)
     rows = [_row(c, b, n - Sq + 4) for b, n in enumerate(lens) if n - Sq + 4 >= 0]
     for b, n in enumerate(lens):
@@ -267,10 +268,11 @@ def test_decode_tree_hidden_drafts_do_not_matter(kv, inf):
 
 
 @pytest.mark.parametrize("kv", [BF, F8])
-def test_decode_tree_nan_reaches_only_its_own_branch(kv):
+@pytest.mark.parametrize("H", [4, 15, 20])
+def test_decode_tree_nan_reaches_only_its_own_branch(H, kv):
     """A NaN draft is seen by its descendants alone; the others' results are as if it were not there."""
     Sq, lens = 8, [72, 130, 300]
-    c = tree_case(lens, Sq, 20, kv, 8)
+    c = tree_case(lens, Sq, H, kv, 8)
     clean = attend_tree(c)
     _fill_rows(c, [_row(c, b, n - Sq + 2) for b, n in enumerate(lens)])
     sees = ((c["masks_host"] >> 2) & 1).astype(bool)
@@ -285,19 +287,21 @@ def test_decode_tree_nan_reaches_only_its_own_branch(kv):
                 check_attention(o[b:b + 1, t:t + 1], lse[b:b + 1, t:t + 1], part)
 
 
-def test_decode_tree_nan_in_the_context():
-    c = tree_case([200, 100], 3, 16, BF, 10)
+@pytest.mark.parametrize("H", [5, 16, 128])
+def test_decode_tree_nan_in_the_context(H):
+    c = tree_case([200, 100], 3, H, BF, 10)
     _fill_rows(c, [_row(c, 0, 50)])
     check_with_nan(*_tree(c), attend_tree(c))
 
 
 @pytest.mark.parametrize("kv", [BF, F8])
-def test_decode_tree_empty_rows(kv):
+@pytest.mark.parametrize("H", [9, 40, 100])
+def test_decode_tree_empty_rows(H, kv):
     """Masks of no bits without a context, empty slots, and a bound of 0."""
     import torch
     masks = np.zeros((4, 3), np.int64)
     masks[1] = [1, 0, 5]
-    c = tree_case([3, 3, 0, 67], 3, 9, kv, 12, masks=masks)
+    c = tree_case([3, 3, 0, 67], 3, H, kv, 12, masks=masks)
     check_attention(*_tree(c), attend_tree(c))
     c["seq_lens"] = torch.zeros_like(c["seq_lens"])
     import mla_latent_kv_gb300 as mla
@@ -306,12 +310,13 @@ def test_decode_tree_empty_rows(kv):
 
 
 @pytest.mark.parametrize("kv", [BF, F8])
-def test_decode_tree_with_a_causal_mask_is_decode(kv):
+@pytest.mark.parametrize("H", [6, 25, 128])
+def test_decode_tree_with_a_causal_mask_is_decode(H, kv):
     """Bits from Sq on are not read, and the low t + 1 bits are mla_decode's order."""
     import mla_latent_kv_gb300 as mla
     Sq = 5
     masks = np.tile(np.array([(1 << t + 1) - 1 | -1 << Sq for t in range(Sq)], np.int64), (4, 1))
-    c = tree_case([5, 64, 131, 2], Sq, 128, kv, 14, masks=masks)
+    c = tree_case([5, 64, 131, 2], Sq, H, kv, 14, masks=masks)
     o, lse = _tree(c)
     o1, lse1 = mla.decode(c["q"], c["cache"], c["table"], c["seq_lens"], c["max_len"], c["scale"], kv_dtype=kv, num_splits=1)
     o_ref, lse_ref, tol_o, tol_lse = attend_tree(c)
@@ -326,13 +331,15 @@ def torch_isinf(x):
     return torch.isinf(x)
 
 
-def test_decode_tree_reports_bad_blocks_and_lengths():
+@pytest.mark.parametrize("kv", [BF, F8])
+@pytest.mark.parametrize("H", [8, 16, 128])
+def test_decode_tree_reports_bad_blocks_and_lengths(H, kv):
     import mla_latent_kv_gb300 as mla
-    c = tree_case([200, 100], 3, 16, BF, 16)
+    c = tree_case([200, 100], 3, H, kv, 16)
     for bad in (c["num_blocks"], -1, 2 ** 31 - 1):
         table, st = c["table"].clone(), _status()
         table[0, 1] = bad
-        o, lse = mla.decode_tree(c["q"], c["cache"], table, c["seq_lens"], c["masks"], 200, c["scale"],
+        o, lse = mla.decode_tree(c["q"], c["cache"], table, c["seq_lens"], c["masks"], 200, c["scale"], kv_dtype=kv,
                                  num_blocks=c["num_blocks"], dev_status=st)
         assert st.item() == mla.DEV_BAD_BLOCK_ID
         part = [x[1:] for x in attend_tree(c)]
@@ -340,17 +347,19 @@ def test_decode_tree_reports_bad_blocks_and_lengths():
     for n in (201, -1):
         st, lens = _status(), c["seq_lens"].clone()
         lens[0] = n
-        mla.decode_tree(c["q"], c["cache"], c["table"], lens, c["masks"], 200, c["scale"], num_blocks=c["num_blocks"], dev_status=st)
+        mla.decode_tree(c["q"], c["cache"], c["table"], lens, c["masks"], 200, c["scale"], kv_dtype=kv, num_blocks=c["num_blocks"],
+                        dev_status=st)
         assert st.item() == mla.DEV_SEQ_TOO_LONG
 
 
 @pytest.mark.parametrize("kv", [BF, F8])
-def test_decode_tree_replayed_with_other_inputs(kv):
+@pytest.mark.parametrize("H", [8, 16, 65])
+def test_decode_tree_replayed_with_other_inputs(H, kv):
     """A captured call reads lengths, tables, masks and cache anew, with a workspace that another call used."""
     import torch
 
     import mla_latent_kv_gb300 as mla
-    a, b = tree_case([3000, 400], 4, 16, kv, 18), tree_case([2900, 1400], 4, 16, kv, 19)
+    a, b = tree_case([3000, 400], 4, H, kv, 18), tree_case([2900, 1400], 4, H, kv, 19)
     nb = max(a["num_blocks"], b["num_blocks"])
     width = max(a["table"].shape[1], b["table"].shape[1])
 
@@ -362,8 +371,8 @@ def test_decode_tree_replayed_with_other_inputs(kv):
         return cache, table
     cache, table = padded(a)
     q, lens, masks = a["q"].clone(), a["seq_lens"].clone(), a["masks"].clone()
-    ws = torch.empty(mla.decode_tree_workspace_bytes(2, 4, 16, 3000, kv), dtype=torch.uint8, device="cuda")
-    o, lse = torch.empty((2, 4, 16, L), device="cuda"), torch.empty((2, 4, 16), device="cuda")
+    ws = torch.empty(mla.decode_tree_workspace_bytes(2, 4, H, 3000, kv), dtype=torch.uint8, device="cuda")
+    o, lse = torch.empty((2, 4, H, L), device="cuda"), torch.empty((2, 4, H), device="cuda")
     call = lambda: mla.decode_tree(q, cache, table, lens, masks, 3000, a["scale"], kv_dtype=kv, workspace=ws, o_latent=o, lse=lse)  # noqa: E731
     call()
     torch.cuda.synchronize()
@@ -388,7 +397,7 @@ def test_decode_tree_replayed_with_other_inputs(kv):
 def test_decode_tree_on_two_streams():
     """Calls of two streams at once, each with its own workspace, also one made by the call."""
     import torch
-    cs = [tree_case([5000, 300, 64], 6, 16, kv, 20 + kv) for kv in (BF, F8)]
+    cs = [tree_case([5000, 300, 64], 6, H, kv, 20 + kv) for kv in (BF, F8) for H in (5, 16, 50)]
     want = [attend_tree(c) for c in cs]
     streams = [torch.cuda.Stream() for _ in cs]
     torch.cuda.synchronize()
