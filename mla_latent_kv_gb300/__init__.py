@@ -655,22 +655,19 @@ def rope_frequencies(base=10000.0, factor=1.0, trained=4096, beta_fast=32.0, bet
 
 def _is_freq(t):
     import torch
-    if t.dtype is not torch.float64 or t.shape != (R // 2,) or not t.is_contiguous() or t.device.type != "cpu":
+    if t.dtype is not torch.float64 or t.shape != (R // 2,) or not t.is_contiguous() or not t.is_cpu:
         raise ValueError(f"inv_freq must be a contiguous float64 CPU tensor of {R // 2} elements, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
 
 
-def _is_rows(name, t, shape):
-    """Refuse a tensor that is not bf16 of the shape with unit inner stride (its rows may be strided)."""
+def _row_strides(name, t, shape):
+    """Strides of a bf16 tensor of the shape with unit inner stride, else refused."""
     import torch
-    if t.dtype is not torch.bfloat16 or t.shape != shape or t.stride(-1) != 1:
+    s = t.stride()
+    if t.dtype is not torch.bfloat16 or t.shape != shape or s[-1] != 1:
         raise ValueError(f"{name} must be bf16 of shape {tuple(shape)} with unit inner stride, got {t.dtype} "
-                         f"{tuple(t.shape)} with strides {t.stride()}")
-
-
-def _strides(t):
-    """Strides of all dimensions but the last; dimensions of one element have strides of no meaning."""
-    return [s if n > 1 else 0 for n, s in zip(t.shape[:-1], t.stride()[:-1])]
+                         f"{tuple(t.shape)} with strides {s}")
+    return s
 
 
 def rope(x, positions, inv_freq, adjacent=True, mscale=1.0, out=None, stream=None):
@@ -678,21 +675,21 @@ def rope(x, positions, inv_freq, adjacent=True, mscale=1.0, out=None, stream=Non
     inv_freq (rope_frequencies) -> bf16 [T, N, 64]. `out` may be x itself. adjacent: pairs (2i, 2i+1), else
     (i, i+32). Negative positions turn back."""
     import torch
-    if x.ndim != 3 or x.shape[2] != R:
-        raise ValueError(f"x must be [T, N, {R}], got {tuple(x.shape)}")
-    _is_rows("x", x, x.shape)
-    T, N = x.shape[0], x.shape[1]
+    shape = x.shape
+    if len(shape) != 3 or shape[2] != R:
+        raise ValueError(f"x must be [T, N, {R}], got {tuple(shape)}")
+    xs = _row_strides("x", x, shape)
+    T, N = shape[0], shape[1]
     _is_shape("positions", positions, torch.int32, (T,))
     _is_freq(inv_freq)
-    if stream is not None and out is None:
-        return _on(stream, "rope", locals())
     if out is None:
+        if stream is not None:
+            return _on(stream, "rope", locals())
         out = torch.empty((T, N, R), dtype=torch.bfloat16, device=x.device)
-    _is_rows("out", out, x.shape)
+    os = _row_strides("out", out, shape)
     s = _raw_stream(stream, x, positions, out)
-    (xt, xn), (ot, on) = _strides(x), _strides(out)
-    _check(lib().mla_rope(x.data_ptr(), xt, xn, positions.data_ptr(), inv_freq.data_ptr(), float(mscale), 1 if adjacent else 0,
-                          out.data_ptr(), ot, on, T, N, s))
+    _check(lib().mla_rope(x.data_ptr(), xs[0], xs[1], positions.data_ptr(), inv_freq.data_ptr(), mscale, 1 if adjacent else 0,
+                          out.data_ptr(), os[0], os[1], T, N, s))
     return out
 
 
@@ -703,8 +700,7 @@ def rope_cache_write(kv_c, k_pe, positions, inv_freq, slot_mapping, kv_cache, kv
     import torch
     T = slot_mapping.shape[0]
     _is_shape("slot_mapping", slot_mapping, torch.int64, (T,))
-    _is_rows("kv_c", kv_c, (T, L))
-    _is_rows("k_pe", k_pe, (T, R))
+    cs, ps = _row_strides("kv_c", kv_c, (T, L)), _row_strides("k_pe", k_pe, (T, R))
     _is_shape("positions", positions, torch.int32, (T,))
     _is_freq(inv_freq)
     if (q_pe is None) != (q_out is None):
@@ -712,16 +708,14 @@ def rope_cache_write(kv_c, k_pe, positions, inv_freq, slot_mapping, kv_cache, kv
     H, qs, os = 1, (0, 0), (0, 0)
     if q_pe is not None:
         H = q_pe.shape[1]
-        _is_rows("q_pe", q_pe, (T, H, R))
-        _is_rows("q_out", q_out, (T, H, R))
-        qs, os = _strides(q_pe), _strides(q_out)
+        qs, os = _row_strides("q_pe", q_pe, (T, H, R)), _row_strides("q_out", q_out, (T, H, R))
     nb = _cache_blocks(kv_cache, kv_dtype, num_blocks)
     _check_status(dev_status)
     s = _raw_stream(stream, kv_cache, kv_c, k_pe, positions, slot_mapping, q_pe, q_out, dev_status)
-    _check(lib().mla_rope_cache_write(kv_c.data_ptr(), *_strides(kv_c), k_pe.data_ptr(), *_strides(k_pe), _a(q_pe), *qs,
-                                      _a(q_out), *os, positions.data_ptr(), inv_freq.data_ptr(), float(mscale),
-                                      1 if adjacent else 0, slot_mapping.data_ptr(), T, H, kv_cache.data_ptr(), kv_dtype, nb,
-                                      float(kv_scale), _a(dev_status), s))
+    _check(lib().mla_rope_cache_write(kv_c.data_ptr(), cs[0], k_pe.data_ptr(), ps[0], _a(q_pe), qs[0], qs[1], _a(q_out), os[0],
+                                      os[1], positions.data_ptr(), inv_freq.data_ptr(), mscale, 1 if adjacent else 0,
+                                      slot_mapping.data_ptr(), T, H, kv_cache.data_ptr(), kv_dtype, nb, kv_scale,
+                                      _a(dev_status), s))
     return kv_cache
 
 

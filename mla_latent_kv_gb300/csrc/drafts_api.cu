@@ -41,7 +41,8 @@ mla_status rope_args(const char* who, const void* x, int64_t x_t, int64_t x_n, c
     if (!positions) return set_error(MLA_ERR_INVALID_ARG, "%s: null pointer", who);
     if (x || out) {
         if (!x || !out) return set_error(MLA_ERR_INVALID_ARG, "%s: null pointer", who);
-        if (!aligned16(x) || !aligned16(out) || x_t % 8 || x_n % 8 || out_t % 8 || out_n % 8)
+        // (strides over a single token or head have no meaning)
+        if (!aligned16(x) || !aligned16(out) || (T > 1 && (x_t % 8 || out_t % 8)) || (N > 1 && (x_n % 8 || out_n % 8)))
             return set_error(MLA_ERR_UNSUPPORTED, "%s: 16-byte aligned pointers and strides of multiples of 8 needed", who);
         if ((T > 1 && out_t == 0) || (N > 1 && out_n == 0))
             return set_error(MLA_ERR_INVALID_ARG, "%s: the result's rows overlap", who);
@@ -190,7 +191,8 @@ mla_status mla_rope_cache_write(const void* kv_c, int64_t kv_c_stride_t, const v
     if (st != MLA_OK) return st;
     if (T == 0) return mla::set_ok();
     if (!kv_c || !k_pe || !slot_mapping || !kv_cache) return set_error(MLA_ERR_INVALID_ARG, "%s: null pointer", who);
-    if (!aligned16(kv_c) || !aligned16(k_pe) || !aligned16(kv_cache) || kv_c_stride_t % 8 || k_pe_stride_t % 8)
+    if (!aligned16(kv_c) || !aligned16(k_pe) || !aligned16(kv_cache) ||
+        (T > 1 && (kv_c_stride_t % 8 || k_pe_stride_t % 8)))
         return set_error(MLA_ERR_UNSUPPORTED, "%s: 16-byte aligned pointers and strides of multiples of 8 needed", who);
     mla::RopeRows r{};
     r.kv_c = (const uint16_t*)kv_c;
