@@ -69,7 +69,6 @@ using dec::warp_wait;
 constexpr int kThreads = 608;
 constexpr int kSoftThreads = 512;
 constexpr int kTileRows = 256;
-constexpr int kAuxWarp0 = 10, kAuxWarps = 8;  // of the output CTAs: drafted pages' V, widening
 constexpr int kPPG = 2;                      // pages per group, one per scores CTA
 constexpr int kPageBox = kPage * 128;        // one page's rows of one 64-dim panel (8 KB)
 constexpr int kSlotPanels = 3;
@@ -127,9 +126,7 @@ enum : int {
     B_READY = B_PFULL + kPBufs,         // [kPBufs] CTA 2: its 4 helper warps and CTA 3 are done with the page
     B_PEER = B_READY + kPBufs,          // [kPBufs] CTA 3: its 4 helper warps are done with the page
     B_STATS = B_PEER + kPBufs,          // CTAs 2, 3: final row statistics written, last P copy issued
-    B_VLAND,                            // [2] trees, CTAs 2, 3: this CTA's half of a drafted page's V landed
-    B_VCLEAN = B_VLAND + 2,             // [2] trees, CTA 2: both halves hold no NaN (16 warps)
-    B_COUNT = B_VCLEAN + 2
+    B_COUNT
 };
 static_assert(8 * B_COUNT <= 512, "barrier slots");
 constexpr int kRelayWarps = 4;    // of CTA 3, from warp 6 on: pages announced to CTA 2 in turn
@@ -147,15 +144,7 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr uint32_t kBarMax = 1, kBarOr = 2, kBarQuarter0 = 3;
 constexpr uint32_t kBarEpi = 1;  // [4] the epilogue's warp sets (output CTAs)
 
-// Eight e4m3 codes -> eight bf16, as the decode kernels read them.
-__device__ __forceinline__ uint4 widen8(uint2 v) {
-    uint4 w;
-    e4m3x4_to_bf16x4(v.x, w.x, w.y);
-    e4m3x4_to_bf16x4(v.y, w.z, w.w);
-    return w;
-}
-
-template <bool kScaled, bool kTree>
+template <bool kScaled>
 __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     decode_prefix_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                          const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap o_map,
@@ -172,43 +161,14 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         return;  // all CTAs of the cluster see the same alignment and leave together
     }
     const int unit = (int)(blockIdx.x >> 2);
+    const int tile = unit / p.splits, split = unit % p.splits;
+    const int page0 = min(p.prefix_pages, split * p.pages_per_split);
+    const int npages = min(p.prefix_pages, page0 + p.pages_per_split) - page0;
+    const int ngroups = (npages + kPPG - 1) / kPPG;
+    const int rows0 = tile * kTileRows + 128 * side;  // first flat row of this CTA
     volatile int* abort = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
     int32_t* ds = p.dev_status;
     auto bar = [&](int i) -> uint32_t { return sbase + 8u * (uint32_t)i; };
-    int tile, split, pages, req = 0;  // the request's (or the prefix's) pages
-    int drafts0 = 0;                  // trees: tokens before the drafted ones (below 0: the first are not there)
-    if constexpr (kTree) {
-        // unit = (split, request, tile): a request's tiles run side by side and read its pages from L2, and
-        // the ranges behind short requests' ends come last
-        tile = unit % p.tiles;
-        req = unit / p.tiles % p.B;
-        split = unit / p.tiles / p.B;
-        int seq = p.seq_lens[req];
-        if (seq < 0 || seq > p.max_seq_len) {
-            if (tid == 0 && ds) atomicOr(ds, MLA_DEV_SEQ_TOO_LONG);
-            seq = min(max(seq, 0), p.max_seq_len);
-        }
-        pages = (seq + kPage - 1) / kPage;
-        drafts0 = seq - p.Sq;
-    } else {
-        tile = unit / p.splits;
-        split = unit % p.splits;
-        pages = p.prefix_pages;
-    }
-    const int page0 = min(pages, split * p.pages_per_split);
-    const int npages = min(pages, page0 + p.pages_per_split) - page0;
-    const int ngroups = (npages + kPPG - 1) / kPPG;
-    const int rows0 = tile * kTileRows + 128 * side;  // first flat row of this CTA
-    // trees: the first of the unit's pages that holds drafted tokens or the end of the request (at most two do)
-    const int drafted = kTree ? max(0, max(drafts0, 0) / kPage - page0) : npages;
-    const int slab = kTree ? split * p.B + req : split;  // of the outputs
-    if (kTree && npages == 0 && p.part_o) {  // an empty partial state: the merge reads no more than its lse
-        griddep_wait();
-        const int row = tid & 127;
-        if (rank >= 2 && tid < 128 && rows0 + row < p.flat_rows)
-            p.part_lse[(size_t)slab * p.flat_rows + rows0 + row] = -CUDART_INF_F;
-        return;
-    }
 
     if (tid == 0) {
         *abort = 0;
@@ -220,7 +180,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             if (i >= B_STAGEFULL && i < B_STAGEFULL + kStages) cnt = 8;
             if (i >= B_READY && i < B_READY + kPBufs) cnt = 5;
             if (i >= B_PEER && i < B_PEER + kPBufs) cnt = 4;
-            if (i >= B_VCLEAN && i < B_VCLEAN + 2) cnt = 2 * kAuxWarps;
             bar_init(bar(i), cnt);
         }
         if (!scores)  // P buffers armed for their first message before a scores CTA can send one
@@ -239,23 +198,18 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     griddep_wait();  // q, the cache and the lengths may be earlier kernels' outputs
     if (tid == 0) griddep_launch_dependents();
 
-    // Block of the unit's page i, or -1 (reported) where the table's entry is outside the cache.
-    auto page_block = [&](int i) -> int {
-        const int32_t blk = p.block_table[(kTree ? (size_t)req * p.max_blocks : (size_t)0) + page0 + i];
-        if (blk < 0 || (int64_t)blk >= p.num_blocks) {
-            if (ds) atomicOr(ds, MLA_DEV_BAD_BLOCK_ID);
-            return -1;
-        }
-        return blk;
-    };
-    // First row of the unit's page i behind the keys' tensor map (out of range: TMA fills zeros).
+    // First cache row of the unit's page i (out of range: TMA fills zeros).
     auto page_row = [&](int i) -> int {
         if (i >= npages) return p.key_rows;
-        if (kTree && kScaled) return (req * p.wide_pages + page0 + i) * kPage;
-        if (!kTree && !p.block_table) return (page0 + i) * kPage;  // widened prefix: its pages in order
-        const int blk = page_block(i);
-        return blk < 0 ? p.key_rows : blk * kPage;
+        if (!p.block_table) return (page0 + i) * kPage;  // widened prefix: its pages in order
+        const int32_t blk = p.block_table[page0 + i];
+        if (blk < 0 || (int64_t)blk >= p.num_blocks) {
+            if (ds) atomicOr(ds, MLA_DEV_BAD_BLOCK_ID);
+            return p.key_rows;
+        }
+        return blk * kPage;
     };
+
     if (scores) {
         if (warp == 0) {
             if (lane == 0 && npages > 0) {
@@ -263,8 +217,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 tma_prefetch_desc(&q_map);
                 bar_arrive_expect_tx(bar(B_QFULL), 9 * kQPanelBytes);
                 for (int qn = 0; qn < 8; ++qn)
-                    tma_load_3d(sbase + q_panel_off(qn), &q_map, bar(B_QFULL), qn * 64, rows0, req);
-                tma_load_3d(sbase + OFF_QROPE, &q_map, bar(B_QFULL), 8 * 64, rows0, req);
+                    tma_load_2d(sbase + q_panel_off(qn), &q_map, bar(B_QFULL), qn * 64, rows0);
+                tma_load_2d(sbase + OFF_QROPE, &q_map, bar(B_QFULL), 8 * 64, rows0);
                 int issued = 0;
                 bool ok = true;
                 for (int gi = 0; gi < ngroups && ok; ++gi) {
@@ -381,17 +335,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             // of 0 would not keep what its unseen tokens hold out of the sum, should that be NaN.
             bool sees = true;
             const int64_t flat = (int64_t)rows0 + row;
-            uint64_t mask = 0;  // trees: the drafted tokens that the row sees
-            if (kTree && flat < p.flat_rows) {
-                mask = __ldcg(reinterpret_cast<const unsigned long long*>(p.masks) + (size_t)req * p.Sq + (int)flat / p.H);
-                if (p.Sq < 64) mask &= (1ull << p.Sq) - 1;
-            }
-            if (!kTree && flat < p.flat_rows) {
+            if (flat < p.flat_rows) {
                 const int r = (int)(flat / p.H), b = r / p.Sq, t = r % p.Sq;
                 const int seq = min(max(p.seq_lens[b], 0), p.max_seq_len);
                 sees = seq - (p.Sq - 1 - t) >= (page0 + npages) * kPage;
             }
-            const bool all_see = kTree || __all_sync(0xffffffffu, sees);
+            const bool all_see = __all_sync(0xffffffffu, sees);
             if (npages > 0) {
                 // Q latent dims: this quarter moves panels 2 quarter and 2 quarter + 1 into TMEM
                 const bool okq = warp_wait(bar(B_QFULL), 0, abort, ds);
@@ -425,8 +374,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 size_t sc = 0;               // the quarter's first token of the page, in float4 units
                 float4 ks[kScaled ? 8 : 1];  // k_scale of its 32 tokens
                 if constexpr (kScaled) {  // plain loads: the widening kernel wrote them while this one began
-                    const size_t first = kTree ? (size_t)req * p.wide_pages + page0 : (size_t)page0;
-                    sc = ((first + min(page, npages - 1)) * kPage + 32 * sub) / 4;
+                    sc = ((size_t)(page0 + min(page, npages - 1)) * kPage + 32 * sub) / 4;
                     const float4* src = reinterpret_cast<const float4*>(p.k_scales) + sc;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) ks[j] = src[j];
@@ -457,21 +405,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     const float4* src = reinterpret_cast<const float4*>(p.v_scales) + sc;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) vs[j] = src[j];
-                }
-                if (kTree && page >= drafted && page < npages) {
-                    // bit c: the row sees token 32 sub + c of the page. Everything before the drafted tokens is
-                    // seen, what is behind them (past the request's end too) is not.
-                    const int at = (page0 + page) * kPage + 32 * sub - drafts0;
-                    const uint32_t seen = seen_tokens(mask, at);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (!(seen >> j & 1u)) {
-                            s[j] = __float_as_uint(-CUDART_INF_F);
-                            if constexpr (kScaled) {  // not seen, whatever its scale is
-                                float4& v = vs[j >> 2];
-                                (j & 3) == 0 ? v.x = 0.f : (j & 3) == 1 ? v.y = 0.f : (j & 3) == 2 ? v.z = 0.f : v.w = 0.f;
-                            }
-                        }
                 }
                 // No row of the warp sees these tokens (an empty slot's heads): no weights to compute.
                 // Masked like any other, three empty slots of 64 made their clusters the last to end, by 8 us
@@ -568,13 +501,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     const int y = page_row(i);
                     const int st = i % kVStages, k = i / kVStages;
                     if (k > 0 && !wait_bar<true>(bar(B_VEMPTY + st), (k - 1) & 1, abort, ds)) break;
-                    uint32_t full = map_to_rank(bar(B_VFULL + st), 2);
-                    if (kTree && !kScaled && i >= drafted) {  // to be looked over in each CTA first
-                        bar_arrive_expect_tx(bar(B_VLAND + i - drafted), kVStageBytes);
-                        full = map_to_rank(bar(B_VLAND + i - drafted), rank);
-                    } else if (side == 0) {
-                        bar_arrive_expect_tx(bar(B_VFULL + st), 2 * kVStageBytes);
-                    }
+                    if (side == 0) bar_arrive_expect_tx(bar(B_VFULL + st), 2 * kVStageBytes);
+                    const uint32_t full = map_to_rank(bar(B_VFULL + st), 2);
                     const uint32_t dst = sbase + OFF_V + st * kVStageBytes;
                     tma_load_3d_pair(dst, &v_map, full, 0, y, 2 * side);
                     tma_load_3d_pair(dst + 2 * kPageBox, &v_map, full, 0, y, 4 + 2 * side);
@@ -592,11 +520,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < npages && ok; ++i) {
                     const int pb = i % kPBufs, st = i % kVStages;
                     if (!(ok = warp_wait<true>(bar(B_READY + pb), (i / kPBufs) & 1, abort, ds))) break;
-                    if (kTree && !kScaled && i >= drafted)
-                        ok = warp_wait<true>(bar(B_VCLEAN + i - drafted), 0, abort, ds);
-                    else
-                        ok = warp_wait<true>(bar(B_VFULL + st), (i / kVStages) & 1, abort, ds);
-                    if (!ok) break;
+                    if (!(ok = warp_wait<true>(bar(B_VFULL + st), (i / kVStages) & 1, abort, ds))) break;
                     tc_fence_after();  // after a rescale by the helper warps' tcgen05.st
                     const uint64_t ad0 = smem_desc_sw128(sbase + OFF_PB + pb * kPBufStride, 16, 1024);
                     const uint64_t bd0 = smem_desc_sw128(sbase + OFF_V + st * kVStageBytes, kPageBox, 1024);
@@ -672,24 +596,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     bar_arrive_remote(bar(B_READY + pb), 2);
                 }
             }
-            if constexpr (kTree && !kScaled) {
-                // The drafted tokens and the cache rows behind them may be hidden from a row, and a weight of 0
-                // would not keep a NaN or infinity of theirs out of its sum. A row that does see such a token
-                // has a NaN score (an infinite one that is not taken) and needs no help from V: they become 0.
-                if (warp >= kAuxWarp0) {
-                    for (int i = drafted; i < npages; ++i) {
-                        if (!warp_wait(bar(B_VLAND + i - drafted), 0, abort, ds)) break;
-                        const uint32_t v = sbase + OFF_V + (i % kVStages) * kVStageBytes + 16u * (uint32_t)(tid - 32 * kAuxWarp0);
-#pragma unroll
-                        for (int c = 0; c < kVStageBytes; c += 32 * kAuxWarps * 16) {
-                            dec::zero_nonfinite(v + c);
-                        }
-                        fence_proxy_async_cta();
-                        __syncwarp();
-                        if (lane == 0) bar_arrive_remote(bar(B_VCLEAN + i - drafted), 2);
-                    }
-                }
-            }
             __syncwarp();
             const bool has_o = npages > 0 && pages_ready == npages && !*abort;
             wait_bar<true>(bar(B_STATS), 0, abort, ds);
@@ -702,17 +608,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             const bool empty = !use_o || l == 0.f;  // no token has a weight; a NaN sum is a NaN result
             const float inv = empty ? 0.f : 1.f / l;
             const int64_t flat = (int64_t)rows0 + row;
-            float* lse = kTree && !p.part_o ? p.lse : p.part_lse;
-            if (eset == 0 && flat < p.flat_rows && (!kTree || lse))
-                lse[(size_t)slab * p.flat_rows + flat] = empty ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
+            if (eset == 0 && flat < p.flat_rows)
+                p.part_lse[(size_t)split * p.flat_rows + flat] =
+                    empty ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
             // O / l leaves through TMA stores over the V ring and the P buffers; rows past the batch
             // are cut off by the tensor map
-            if (kTree && p.o_bf16)
-                store_rows<false, 4, 3, kBarEpi>(smem, sbase, OFF_V, tmem + lane_base, row, eset, (ctid & 127) == 0, true,
-                                                 empty, inv, &o_map, rows0, slab, rows0 < p.flat_rows);
-            else
-                store_rows<true, 4, 3, kBarEpi>(smem, sbase, OFF_V, tmem + lane_base, row, eset, (ctid & 127) == 0, true,
-                                                empty, inv, &o_map, rows0, slab, rows0 < p.flat_rows);
+            store_rows<true, 4, 3, kBarEpi>(smem, sbase, OFF_V, tmem + lane_base, row, eset, (ctid & 127) == 0, true,
+                                            empty, inv, &o_map, rows0, split, rows0 < p.flat_rows);
         }
     }
 
@@ -724,90 +626,47 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------------------------------
-// FP8 pages -> bf16 rows (exact) and scales, once per call: the prefix's, or those of every request of a
-// tree call. One warp per token: lanes take 8-byte chunks of the 576 codes.
+// FP8 prefix -> bf16 rows (exact) and scales, once per call. One warp per token: lanes take
+// 8-byte chunks of the 576 codes.
 // ------------------------------------------------------------------------------------------
-template <bool kTree>
 __global__ void __launch_bounds__(256) prefix_widen_kernel(PrefixArgs p, const uint8_t* cache, uint16_t* x,
                                                            float* k_scales, float* v_scales) {
     griddep_wait();
     griddep_launch_dependents();
     const int token = (int)blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int req = kTree ? (int)blockIdx.y : 0;
-    // a tree's last page is widened whole: its rows behind the request's end are not seen
-    const int tokens = kTree ? (min(max(p.seq_lens[req], 0), p.max_seq_len) + kPage - 1) / kPage * kPage : p.prefix_pages * kPage;
-    if (token >= tokens) return;
-    const int32_t blk = p.block_table[(kTree ? (size_t)req * p.max_blocks : (size_t)0) + token / kPage];
+    if (token >= p.prefix_pages * kPage) return;
+    const int32_t blk = p.block_table[token / kPage];
     const bool bad = blk < 0 || (int64_t)blk >= p.num_blocks;
     if (bad && lane == 0 && p.dev_status) atomicOr(p.dev_status, MLA_DEV_BAD_BLOCK_ID);
     const uint8_t* src = cache + ((size_t)(bad ? 0 : blk) * kPage + token % kPage) * kFp8RowBytes;
-    const size_t row = kTree ? (size_t)req * p.wide_pages * kPage + token : (size_t)token;
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
         const int c = lane + 32 * i;
         if (c >= kD / 8) continue;
         uint2 v = make_uint2(0u, 0u);
         if (!bad) v = *reinterpret_cast<const uint2*>(src + 8 * c);
-        *reinterpret_cast<uint4*>(x + row * kD + 8 * c) = widen8(v);
+        uint4 w;  // as the decode kernels read the codes
+        e4m3x4_to_bf16x4(v.x, w.x, w.y);
+        e4m3x4_to_bf16x4(v.y, w.z, w.w);
+        *reinterpret_cast<uint4*>(x + (size_t)token * kD + 8 * c) = w;
     }
     if (lane == 0) {
         const float2 sc = bad ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2*>(src + kD);
-        k_scales[row] = sc.x;
-        v_scales[row] = sc.y;
+        k_scales[token] = sc.x;
+        v_scales[token] = sc.y;
     }
 }
 
-using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, const PrefixArgs);
-int g_attr_done[4][64] = {};
+int g_attr_done[2][64] = {};
 int g_clusters[64] = {};
 
-Kernel kernel_of(bool scaled, bool tree) {
-    if (tree) return scaled ? decode_prefix_kernel<true, true> : decode_prefix_kernel<false, true>;
-    return scaled ? decode_prefix_kernel<true, false> : decode_prefix_kernel<false, false>;
-}
-
-cudaError_t set_attr(int dev, bool scaled, bool tree) {
-    int* done = g_attr_done[2 * tree + scaled];
-    if (dev < 64 && done[dev]) return cudaSuccess;
+cudaError_t set_attr(int dev, bool scaled) {
+    if (dev < 64 && g_attr_done[scaled][dev]) return cudaSuccess;
     const cudaError_t e =
-        cudaFuncSetAttribute(kernel_of(scaled, tree), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e == cudaSuccess && dev < 64) done[dev] = 1;
+        scaled ? cudaFuncSetAttribute(decode_prefix_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes)
+               : cudaFuncSetAttribute(decode_prefix_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e == cudaSuccess && dev < 64) g_attr_done[scaled][dev] = 1;
     return e;
-}
-
-// Tensor maps of the bf16 rows at `base` (K and V boxes), of q [requests, flat_rows, 576] and of the output
-// [slabs, flat_rows, 512].
-cudaError_t encode_maps(const PrefixArgs& a, const void* base, uint64_t rows, uint64_t requests, const void* out, bool f32,
-                        uint64_t slabs, CUtensorMap* k_map, CUtensorMap* v_map, CUtensorMap* q_map, CUtensorMap* o_map) {
-    memset(k_map, 0, sizeof *k_map);
-    memset(v_map, 0, sizeof *v_map);
-    memset(q_map, 0, sizeof *q_map);
-    memset(o_map, 0, sizeof *o_map);
-    cudaError_t e = cudaSuccess;
-    if (rows > 0) {
-        // the rows as [panel of 64 dims][row][64]: one box is several panels of a page
-        const uint64_t dims[3] = {64, rows, (uint64_t)(kD / 64)};
-        const uint64_t strides[2] = {(uint64_t)kBf16RowBytes, 128};
-        const uint32_t kbox[3] = {64, (uint32_t)kPage, (uint32_t)kSlotPanels};
-        e = encode_tmap(k_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, kbox, true);
-        if (e != cudaSuccess) return e;
-        const uint32_t vbox[3] = {64, (uint32_t)kPage, 2};
-        e = encode_tmap(v_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, vbox, true);
-        if (e != cudaSuccess) return e;
-    }
-    {
-        const uint64_t dims[3] = {(uint64_t)kD, (uint64_t)a.flat_rows, requests};
-        const uint64_t strides[2] = {(uint64_t)kD * 2, (uint64_t)a.flat_rows * kD * 2};
-        const uint32_t box[3] = {64, 128, 1};
-        e = encode_tmap(q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, dims, strides, box, true);
-        if (e != cudaSuccess) return e;
-    }
-    const uint64_t size = f32 ? 4 : 2;
-    const uint64_t dims[3] = {(uint64_t)kL, (uint64_t)a.flat_rows, slabs};
-    const uint64_t strides[2] = {(uint64_t)kL * size, (uint64_t)a.flat_rows * kL * size};
-    const uint32_t box[3] = {f32 ? 32u : 64u, 128, 1};
-    return encode_tmap(o_map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, out, dims, strides,
-                       box, true);
 }
 
 }  // namespace
@@ -816,7 +675,7 @@ int prefix_clusters() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return -1;
     if (dev < 64 && g_clusters[dev] > 0) return g_clusters[dev];
-    if (set_attr(dev, false, false) != cudaSuccess) return -1;
+    if (set_attr(dev, false) != cudaSuccess) return -1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(4);
     cfg.blockDim = dim3(kThreads);
@@ -829,7 +688,7 @@ int prefix_clusters() {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel_of(false, false), &cfg) != cudaSuccess || n < 1) return -1;
+    if (cudaOccupancyMaxActiveClusters(&n, decode_prefix_kernel<false>, &cfg) != cudaSuccess || n < 1) return -1;
     if (dev < 64) g_clusters[dev] = n;
     return n;
 }
@@ -860,7 +719,7 @@ void prefix_split(int64_t flat_rows, int pages, int clusters, int* splits, int* 
 
 cudaError_t launch_prefix_widen(const PrefixArgs& a, const uint8_t* cache, uint16_t* widened, float* scales,
                                 cudaStream_t s) {
-    return launch_pdl(prefix_widen_kernel<false>, dim3((unsigned)(a.prefix_pages * kPage / 8)), dim3(256), 0, s, a, cache,
+    return launch_pdl(prefix_widen_kernel, dim3((unsigned)(a.prefix_pages * kPage / 8)), dim3(256), 0, s, a, cache,
                       widened, scales, scales + (size_t)a.prefix_pages * kPage);
 }
 
@@ -871,7 +730,7 @@ cudaError_t launch_decode_prefix(const PrefixArgs& in, const uint8_t* cache, con
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    e = set_attr(dev, fp8, false);
+    e = set_attr(dev, fp8);
     if (e != cudaSuccess) return e;
     const void* base = cache;
     uint64_t rows = (uint64_t)a.num_blocks * kPage;
@@ -884,64 +743,41 @@ cudaError_t launch_decode_prefix(const PrefixArgs& in, const uint8_t* cache, con
     }
     a.key_rows = (int)rows;
     CUtensorMap k_map, v_map, q_map, o_map;
-    e = encode_maps(a, base, rows, 1, a.part_o, true, (uint64_t)a.splits, &k_map, &v_map, &q_map, &o_map);
-    if (e != cudaSuccess) return e;
+    memset(&k_map, 0, sizeof k_map);
+    memset(&v_map, 0, sizeof v_map);
+    memset(&q_map, 0, sizeof q_map);
+    memset(&o_map, 0, sizeof o_map);
+    {
+        // the rows as [panel of 64 dims][row][64]: one box is several panels of a page
+        const uint64_t dims[3] = {64, rows, (uint64_t)(kD / 64)};
+        const uint64_t strides[2] = {(uint64_t)kBf16RowBytes, 128};
+        const uint32_t kbox[3] = {64, (uint32_t)kPage, (uint32_t)kSlotPanels};
+        e = encode_tmap(&k_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, kbox, true);
+        if (e != cudaSuccess) return e;
+        const uint32_t vbox[3] = {64, (uint32_t)kPage, 2};
+        e = encode_tmap(&v_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, vbox, true);
+        if (e != cudaSuccess) return e;
+    }
+    {
+        const uint64_t dims[2] = {(uint64_t)kD, (uint64_t)a.flat_rows};
+        const uint64_t strides[1] = {(uint64_t)kD * 2};
+        const uint32_t box[2] = {64, 128};
+        e = encode_tmap(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.q, dims, strides, box, true);
+        if (e != cudaSuccess) return e;
+    }
+    {
+        const uint64_t dims[3] = {(uint64_t)kL, (uint64_t)a.flat_rows, (uint64_t)a.splits};
+        const uint64_t strides[2] = {(uint64_t)kL * 4, (uint64_t)a.flat_rows * kL * 4};
+        const uint32_t box[3] = {32, 128, 1};
+        e = encode_tmap(&o_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, a.part_o, dims, strides, box, true);
+        if (e != cudaSuccess) return e;
+    }
     const int64_t tiles = ((int64_t)a.flat_rows + kTileRows - 1) / kTileRows;
     const dim3 grid((unsigned)(4 * tiles * a.splits));
-    return launch_pdl(kernel_of(fp8, false), grid, dim3(kThreads), kSmemBytes, s, k_map, v_map, q_map, o_map, a);
-}
-
-// The split of requests of `pages` pages, B * tiles units a range: ranges of an even number of pages.
-void tree_split(int64_t units, int64_t flat_rows, int pages, int clusters, int* splits, int* pages_per_split) {
-    // As for a prefix, but one range of all pages needs no partial states and no merge (its launch: 6 page-times).
-    constexpr double kUnitPages = 14.0, kMerge = 6.0;
-    const double partial = (double)flat_rows * (kL + 1) * 8.0 / 5.0e6 / 0.6;
-    double best = 1e300;
-    *splits = 1;
-    *pages_per_split = (pages + 1) / 2 * 2;
-    for (int S = 1; S <= (pages + 1) / 2 && S <= 3 * clusters; ++S) {
-        const int per = ((pages + S - 1) / S + 1) / 2 * 2;
-        const int used = (pages + per - 1) / per;
-        if (used < S && S > 1) continue;
-        const int64_t waves = (units * S + clusters - 1) / clusters;
-        const double t = (double)waves * (per + kUnitPages) + (S > 1 ? kMerge + S * partial : 0.0);
-        if (t < best * 0.999) {
-            best = t;
-            *splits = S;
-            *pages_per_split = per;
-        }
-    }
-}
-
-cudaError_t launch_decode_tree(const PrefixArgs& in, const uint8_t* cache, uint16_t* widened, float* scales, bool out_f32,
-                               void* out, cudaStream_t s) {
-    PrefixArgs a = in;
-    const bool fp8 = widened != nullptr;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    e = set_attr(dev, fp8, true);
-    if (e != cudaSuccess) return e;
-    const int64_t units = (int64_t)a.splits * a.B * a.tiles;
-    uint64_t rows = (uint64_t)a.num_blocks * kPage;
-    if (fp8) {
-        rows = (uint64_t)a.B * a.wide_pages * kPage;
-        a.k_scales = scales;
-        a.v_scales = scales + rows;
-        if (rows > 0) {
-            e = launch_pdl(prefix_widen_kernel<true>, dim3((unsigned)(a.wide_pages * kPage / 8), (unsigned)a.B), dim3(256), 0, s,
-                           a, cache, widened, scales, scales + rows);
-            if (e != cudaSuccess) return e;
-        }
-    }
-    a.key_rows = (int)rows;
-    a.o_bf16 = !out_f32;
-    CUtensorMap k_map, v_map, q_map, o_map;
-    e = encode_maps(a, fp8 ? (const void*)widened : cache, rows, (uint64_t)a.B, out, out_f32, (uint64_t)a.splits * a.B, &k_map, &v_map, &q_map,
-                    &o_map);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(kernel_of(fp8, true), dim3((unsigned)(4 * units)), dim3(kThreads), kSmemBytes, s, k_map, v_map, q_map, o_map,
-                      a);
+    return fp8 ? launch_pdl(decode_prefix_kernel<true>, grid, dim3(kThreads), kSmemBytes, s, k_map, v_map, q_map,
+                            o_map, a)
+               : launch_pdl(decode_prefix_kernel<false>, grid, dim3(kThreads), kSmemBytes, s, k_map, v_map, q_map,
+                            o_map, a);
 }
 
 }  // namespace mla

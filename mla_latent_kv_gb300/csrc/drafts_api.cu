@@ -65,8 +65,8 @@ mla_status rope_args(const char* who, const void* x, int64_t x_t, int64_t x_n, c
 
 // ------------------------------------------------------------------------------------ tree
 // How a tree call runs, and its workspace. At most 128 (draft, head) pairs are one row of so many heads for
-// the decode kernels (splits: theirs); more go 256 at a time through the prefix kernel, over each request's
-// pages: the widened rows (FP8), then the partial states.
+// the decode kernels (splits: theirs). More go through a kernel of their own, 256 at a time; its workspace is the
+// widened rows (FP8), then the partial states.
 struct TreePlan {
     bool rows;
     int splits, tiles, pages_per_split, wide_pages;
@@ -83,7 +83,7 @@ bool plan_tree(mla_kv_dtype kv, int B, int Sq, int H, int max_seq_len, TreePlan*
         w->total = mla::workspace_layout(kv, B, B, (int)flat, w->splits, max_seq_len).total;
         return true;
     }
-    const int clusters = mla::prefix_clusters();
+    const int clusters = mla::tree_clusters();
     if (clusters < 1) return false;
     w->tiles = (int)((flat + 255) / 256);
     mla::tree_split((int64_t)B * w->tiles, B * flat, pages, clusters, &w->splits, &w->pages_per_split);
@@ -254,34 +254,34 @@ mla_status mla_decode_tree(const void* q, const void* kv_cache, mla_kv_dtype kv_
     }
     const bool fp8 = kv_dtype == MLA_KV_FP8_E4M3_SCALED;
     char* ws = (char*)workspace;
-    mla::PrefixArgs a{};
+    mla::TreeArgs a{};
     a.q = (const uint16_t*)q;
     a.flat_rows = Sq * H;
+    a.B = B;
+    a.Sq = Sq;
+    a.H = H;
+    a.tiles = w.tiles;
     a.block_table = block_table;
     a.max_blocks = max_blocks;
     a.num_blocks = num_blocks;
-    a.splits = w.splits;
-    a.pages_per_split = w.pages_per_split;
     a.seq_lens = seq_lens;
     // no cache: no request sees a token, and a positive length is reported as too long
     a.max_seq_len = num_blocks > 0 ? max_seq_len : 0;
-    a.B = B;
-    a.tiles = w.tiles;
-    a.Sq = Sq;
-    a.H = H;
-    a.scale = scale;
     a.masks = tree_mask;
-    a.lse = lse;
-    a.dev_status = dev_status;
+    a.scale = scale;
+    a.splits = w.splits;
+    a.pages_per_split = w.pages_per_split;
     a.wide_pages = w.wide_pages;
+    a.o = o_latent;
+    a.lse = lse;
+    a.o_bf16 = w.splits == 1 && o_dtype == MLA_DT_BF16;
     if (w.splits > 1) {
         a.part_o = (float*)(ws + w.part_o);
         a.part_lse = (float*)(ws + w.part_lse);
     }
+    a.dev_status = dev_status;
     cudaStream_t s = (cudaStream_t)stream;
-    const bool f32 = w.splits > 1 || o_dtype == MLA_DT_F32;
-    cudaError_t e = mla::launch_decode_tree(a, (const uint8_t*)kv_cache, fp8 ? (uint16_t*)ws : nullptr, (float*)(ws + w.scales), f32,
-                                            w.splits > 1 ? (void*)a.part_o : o_latent, s);
+    cudaError_t e = mla::launch_decode_tree(a, (const uint8_t*)kv_cache, fp8 ? (uint16_t*)ws : nullptr, (float*)(ws + w.scales), s);
     if (e != cudaSuccess) return cuda_error(e, who);
     if (w.splits > 1) {
         mla::DecodeArgs m{};  // every row's states are "pre" states, none its own

@@ -279,20 +279,7 @@ struct PrefixArgs {
     float* part_o;              // fp32 [splits, flat_rows, 512]
     float* part_lse;            // fp32 [splits, flat_rows]
     int32_t* dev_status;        // or null
-    // Trees: every request's own pages, flat_rows = Sq * H rows of each request, outputs [splits, B, flat_rows]
-    // (part_o null: one split, written to the final outputs).
-    int B, tiles, max_blocks;
-    const uint64_t* masks;      // [B, Sq]
-    float* lse;                 // final, or null
-    int o_bf16;                 // final output in bf16
-    int wide_pages;             // FP8: pages of each request's widened rows, [B, wide_pages, 64]
 };
-constexpr int kTreeMaxDrafts = 64;  // bits of a mask
-void tree_split(int64_t units, int64_t flat_rows, int pages, int clusters, int* splits, int* pages_per_split);
-// FP8: the requests' rows are first widened to `widened` [B, wide_pages, 64, 576], their scales to `scales`
-// [2, B, wide_pages, 64].
-cudaError_t launch_decode_tree(const PrefixArgs& a, const uint8_t* cache, uint16_t* widened, float* scales, bool out_f32,
-                               void* out, cudaStream_t s);
 int prefix_clusters();  // clusters of the prefix kernel that run at once on the current device, or -1
 void prefix_split(int64_t flat_rows, int pages, int clusters, int* splits, int* pages_per_split);
 // FP8: launch_prefix_widen first writes the prefix's rows to `widened` [prefix tokens, 576] and
@@ -371,6 +358,39 @@ struct ForkArgs {
     int32_t* dev_status;        // or null
 };
 cudaError_t launch_fork_pages(const ForkArgs& a, bool fp8, cudaStream_t s);
+
+// ---- decode of drafted trees, more than 128 (draft, head) pairs a request ------------------------
+constexpr int kTreeMaxDrafts = 64;  // bits of a mask
+struct TreeArgs {
+    const uint16_t* q;          // bf16 [B, flat_rows, 576]
+    int flat_rows;              // Sq * H of a request
+    int B, Sq, H;
+    int tiles;                  // of 256 flat rows
+    const int32_t* block_table; // [B, max_blocks]
+    int max_blocks;
+    int64_t num_blocks;
+    const int32_t* seq_lens;    // [B], the drafts among them
+    int max_seq_len;
+    const uint64_t* masks;      // [B, Sq]
+    float scale;
+    int splits, pages_per_split;
+    int64_t units;              // splits * B * tiles
+    int key_rows;               // rows behind the keys' tensor map
+    int wide_pages;             // FP8: pages of each request's widened rows, [B, wide_pages, 64]
+    const float* k_scales;      // and their scales
+    const float* v_scales;
+    void* o;                    // [B, flat_rows, 512], fp32 or bf16
+    float* lse;                 // [B, flat_rows] or null
+    float* part_o;              // more than one split: fp32 [splits, B, flat_rows, 512]
+    float* part_lse;            // [splits, B, flat_rows]
+    int o_bf16;                 // o in bf16 (and one split)
+    int32_t* dev_status;        // or null
+};
+int tree_clusters();  // clusters of the tree kernel that run at once on the current device, or -1
+void tree_split(int64_t units, int64_t flat_rows, int pages, int clusters, int* splits, int* pages_per_split);
+// FP8: the requests' rows are first widened to `widened` [B, wide_pages, 64, 576], their scales to `scales`
+// [2, B, wide_pages, 64].
+cudaError_t launch_decode_tree(const TreeArgs& a, const uint8_t* cache, uint16_t* widened, float* scales, cudaStream_t s);
 
 int device_sm_count();  // of the current device, or -1
 
