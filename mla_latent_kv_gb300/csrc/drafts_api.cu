@@ -47,7 +47,7 @@ mla_status rope_args(const char* who, const void* x, int64_t x_t, int64_t x_n, c
         if ((T > 1 && out_t == 0) || (N > 1 && out_n == 0))
             return set_error(MLA_ERR_INVALID_ARG, "%s: the result's rows overlap", who);
     }
-    if ((int64_t)T * (N / 32 + 2) > (int64_t)INT32_MAX)
+    if ((int64_t)T * (N / 8 + 2) > (int64_t)INT32_MAX)
         return set_error(MLA_ERR_UNSUPPORTED, "%s: %d tokens of %d heads too many", who, T, N);
     a->mscale = mscale;
     a->adjacent = adjacent;
@@ -124,12 +124,13 @@ mla_status check_pool(const char* who, const void* cache, mla_kv_dtype kv, int l
 }
 
 struct ForkLayout {
-    size_t rows, heirs, fresh, total;
+    size_t rows, copies, heirs, fresh, total;
 };
 ForkLayout fork_layout(int B, int B2, int64_t num_blocks) {
     ForkLayout w{};
     w.rows = 256;
-    w.heirs = w.rows + up256((size_t)B2 * sizeof(int4));
+    w.copies = w.rows + up256((size_t)B2 * sizeof(int4));
+    w.heirs = w.copies + up256((size_t)B2 * sizeof(int4));
     w.fresh = w.heirs + up256((size_t)B * sizeof(int32_t));
     w.total = w.fresh + up256((size_t)num_blocks * sizeof(int32_t));
     return w;
@@ -386,6 +387,7 @@ mla_status mla_fork_pages(void* kv_cache, mla_kv_dtype kv_dtype, int layers, int
     a.new_refs = new_refs;
     a.head = (int32_t*)ws;
     a.rows = (int4*)(ws + w.rows);
+    a.copies = (int4*)(ws + w.copies);
     a.heirs = (int32_t*)(ws + w.heirs);
     a.fresh = (int32_t*)(ws + w.fresh);
     a.dev_status = dev_status;

@@ -352,7 +352,8 @@ struct ForkArgs {
     int32_t* new_lens;          // [B2]
     int32_t* new_refs;          // [num_blocks]
     int32_t* head;              // [0]: the call failed
-    int4* rows;                 // [B2]: parent or -1, pages, first of its taken pages, kFork* bits
+    int4* rows;                 // [B2]: parent or -1, pages, first of its taken pages, whether the parent's heir
+    int4* copies;               // [B2]: rows [2] of page [0] go to page [1]
     int32_t* heirs;             // [B]: new row that keeps the old row's pages, or -1
     int32_t* fresh;             // [num_blocks]
     int32_t* dev_status;        // or null

@@ -5,8 +5,8 @@
 // there (how many drafts were accepted, which beams go on) needs no host in between. Bound: latency; the
 // rows moved are a few per request and layer.
 //
-// None of these kernels signals its dependents early: they write cache rows, block tables and lengths, which
-// a decode reads before its own wait.
+// No kernel that writes cache rows, block tables or lengths signals its dependents early: a decode reads them
+// before its own wait.
 #include <climits>
 
 #include "internal.h"
@@ -88,7 +88,6 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptArgs
 // reference counts. The second kernel writes the new rows, applies the changes of the counts (sums of +1
 // and -1, in any order) and copies the rows of pages that are held in part by more than one.
 // ------------------------------------------------------------------------------------------
-enum : int { kForkHeir = 1, kForkCopy = 2 };
 constexpr int kPlanThreads = 1024;
 constexpr int kRefsPerThread = 8;  // of a step of the free-page search
 constexpr int kForkThreads = 256;
@@ -132,7 +131,10 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
 
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs p) {
     ptx::griddep_wait();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // The second kernel waits for this one before anything else, and the kernel behind it for that one, which
+    // signals nothing: it may be scheduled now.
+    ptx::griddep_launch_dependents();
+    const int tid = threadIdx.x;
     if (blockIdx.x > 0) {
         const int64_t step = (int64_t)(gridDim.x - 1) * kPlanThreads;
         for (int64_t i = (int64_t)(blockIdx.x - 1) * kPlanThreads + tid; i < p.num_blocks; i += step) p.new_refs[i] = p.refs[i];
@@ -169,25 +171,27 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs 
     }
     __syncthreads();
     if (bits_s == 0) {  // parents and lengths are good
-        for (int r = warp; r < p.B2; r += kPlanThreads / 32) {
+        for (int r = tid; r < p.B2; r += kPlanThreads) {
             const int parent = p.parents[r], room = p.room[r];
             const int n = parent >= 0 ? p.lens[parent] : 0, held = parent >= 0 ? p.counts[parent] : 0;
             const int whole = n / kPage;
             const int64_t want = ((int64_t)max(n, room) + kPage - 1) / kPage;
             const int need = (int)min(want, (int64_t)p.max_blocks);
-            if (want > p.max_blocks && lane == 0) atomicOr(&bits_s, MLA_DEV_SEQ_TOO_LONG);
+            if (want > p.max_blocks) atomicOr(&bits_s, MLA_DEV_SEQ_TOO_LONG);
             const bool heir = parent >= 0 && heir_s[parent] == r;
             const int32_t* row = p.table + (size_t)max(parent, 0) * p.max_blocks;
-            int take = need - whole, flags = heir ? kForkHeir : 0;
+            int take = need - whole;
             bool first = false;  // the page behind the whole ones is kept
-            if (heir)
-                for (int j = whole + lane; j - lane < min(held, need); j += 32) {
-                    const uint32_t kept = __ballot_sync(0xffffffffu, heir_keeps(p, row, j, whole, held, need));
-                    take -= __popc(kept);
-                    if (j - lane == whole) first = kept & 1u;
+            // usually one or two pages: the one held in part, and room
+            for (int j = whole; heir && j < min(held, need); ++j)
+                if (heir_keeps(p, row, j, whole, held, need)) {
+                    --take;
+                    first |= j == whole;
                 }
-            if (n % kPage && !first) flags |= kForkCopy;
-            if (lane == 0) p.rows[r] = make_int4(parent, need, take, flags);
+            const bool copy = n % kPage && !first;
+            p.rows[r] = make_int4(parent, need, take, heir ? 1 : 0);
+            // where its rows come from; where they go is known later
+            p.copies[r] = make_int4(copy ? row[whole] : -1, 0, copy ? n % kPage : 0, 0);
         }
     }
     __syncthreads();
@@ -219,6 +223,10 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs 
             got += sum;
         }
         if (tid == 0 && got < total) atomicOr(&bits_s, MLA_DEV_NO_PAGES);
+        __syncthreads();
+        // a copied page is the first that its row takes
+        for (int r = tid; r < p.B2 && bits_s == 0; r += kPlanThreads)
+            if (p.copies[r].z > 0) p.copies[r].y = p.fresh[p.rows[r].z];
     }
     __syncthreads();
     if (tid == 0) {
@@ -245,7 +253,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_apply_kernel(const ForkArgs
         const int4 rec = failed ? make_int4(-1, 0, 0, 0) : p.rows[r];
         const int n = rec.x >= 0 ? p.lens[rec.x] : 0, held = rec.x >= 0 ? p.counts[rec.x] : 0;
         const int whole = n / kPage, need = rec.y;
-        const bool heir = rec.w & kForkHeir;
+        const bool heir = rec.w != 0;
         const int32_t* from = p.table + (size_t)max(rec.x, 0) * p.max_blocks;
         int taken = rec.z;
         for (int j0 = 0; j0 < p.max_blocks; j0 += kForkThreads) {
@@ -288,15 +296,12 @@ __global__ void __launch_bounds__(kForkThreads) fork_apply_kernel(const ForkArgs
     u -= p.B;  // ---- a part of a new row's copied page, in one layer
     const int r = (int)(u / ((int64_t)copy_blocks * p.layers));
     const int part = (int)(u % copy_blocks), layer = (int)(u / copy_blocks % p.layers);
-    const int4 rec = p.rows[r];
-    if (!(rec.w & kForkCopy)) return;
-    const int n = p.lens[rec.x];
-    const int32_t from = p.table[(size_t)rec.x * p.max_blocks + n / kPage], to = p.fresh[rec.z];
-    if (!in_pool(from)) return;
+    const int4 rec = p.copies[r];
+    const int bytes = rec.z * kRowBytes, at = part * kCopyBytes + tid * 16;
+    if (part * kCopyBytes >= bytes || !in_pool(rec.x)) return;
     constexpr size_t kPageBytes = (size_t)kPage * kRowBytes;
-    const int bytes = n % kPage * kRowBytes, at = part * kCopyBytes + tid * 16;
-    const uint8_t* src = p.cache + ((size_t)layer * p.num_blocks + from) * kPageBytes;
-    uint8_t* dst = p.cache + ((size_t)layer * p.num_blocks + to) * kPageBytes;
+    const uint8_t* src = p.cache + ((size_t)layer * p.num_blocks + rec.x) * kPageBytes;
+    uint8_t* dst = p.cache + ((size_t)layer * p.num_blocks + rec.y) * kPageBytes;
     uint4 v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)

@@ -7,8 +7,8 @@
 // for the step's own 2^-65 (2^-34 of a turn at 2^31 tokens). Its leading bits go to sincospi in fp32.
 // (In fp32, m * w_i alone is off by 0.004 rad at 131072 tokens.)
 //
-// One warp per 32 heads of a token: each lane computes one pair's cosine and sine, four lanes share a head's
-// row (pairs 8 c .. 8 c + 7 are lane c's, in both layouts) and get theirs by shuffles; four rows' loads are
+// One warp per 32 heads of a token (8 or 16 where there are few): each lane computes one pair's cosine and sine, four lanes share a head's
+// row (pairs 8 c .. 8 c + 7 are lane c's, in both layouts) and get theirs by shuffles; up to four rows' loads are
 // in flight before the first is used. A thread writes what it read and no more, so that the result may
 // replace its input. Bound: memory, 256 bytes a head.
 #include "internal.h"
@@ -18,8 +18,8 @@ namespace mla {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kRowsPerLane = 4;           // head rows of a lane
-constexpr int kHeads = 8 * kRowsPerLane;  // heads of a warp
+// Head rows of a lane: a warp has eight times as many heads of a token.
+constexpr int rows_per_lane(int heads) { return heads > 16 ? 4 : heads > 8 ? 2 : 1; }
 
 // (cos, sin) of this lane's pair at position m, times mscale.
 __device__ __forceinline__ float2 turn_of(const RopeArgs& p, int m, int lane) {
@@ -48,16 +48,17 @@ __device__ __forceinline__ void unpack8(uint4 w, float* x) {
     }
 }
 
-// Heads [kHeads * part, ...) of token t, by one warp.
+// Heads [8 kRows part, ...) of token t, by one warp.
+template <int kRows>
 __device__ __forceinline__ void rope_heads(const RopeArgs& p, int t, int part, int lane) {
     const float2 mine = turn_of(p, p.positions[t], lane);
     const int c = lane & 3;
     // the lane's 16 values: two chunks of 8, side by side or half a row apart
     const int c0 = p.adjacent ? 2 * c : c, c1 = p.adjacent ? 2 * c + 1 : c + 4;
-    uint4 w[kRowsPerLane][2];
+    uint4 w[kRows][2];
 #pragma unroll
-    for (int r = 0; r < kRowsPerLane; ++r) {
-        const int n = kHeads * part + 8 * r + (lane >> 2);
+    for (int r = 0; r < kRows; ++r) {
+        const int n = 8 * kRows * part + 8 * r + (lane >> 2);
         if (n >= p.N) continue;
         const uint16_t* src = p.x + t * p.x_t + n * p.x_n;
         w[r][0] = *reinterpret_cast<const uint4*>(src + 8 * c0);
@@ -68,8 +69,8 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& p, int t, int part, i
     for (int k = 0; k < 8; ++k)
         tr[k] = make_float2(__shfl_sync(0xffffffffu, mine.x, 8 * c + k), __shfl_sync(0xffffffffu, mine.y, 8 * c + k));
 #pragma unroll
-    for (int r = 0; r < kRowsPerLane; ++r) {
-        const int n = kHeads * part + 8 * r + (lane >> 2);
+    for (int r = 0; r < kRows; ++r) {
+        const int n = 8 * kRows * part + 8 * r + (lane >> 2);
         if (n >= p.N) continue;
         float x[16];
         unpack8(w[r][0], x);
@@ -159,39 +160,52 @@ __device__ __forceinline__ void rope_row(const RopeArgs& p, const RopeRows& r, i
     }
 }
 
+template <int kRows>
 __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeArgs p) {
     // No early signal to the kernels behind: the result may be a part of a cache, which a decode reads
     // before its own wait.
     ptx::griddep_wait();
-    const int parts = (p.N + kHeads - 1) / kHeads;
+    const int parts = (p.N + 8 * kRows - 1) / (8 * kRows);
     const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (w < (int64_t)p.T * parts) rope_heads(p, (int)(w / parts), (int)(w % parts), threadIdx.x & 31);
+    if (w < (int64_t)p.T * parts) rope_heads<kRows>(p, (int)(w / parts), (int)(w % parts), threadIdx.x & 31);
 }
 
-template <bool kFp8>
+template <bool kFp8, int kRows>
 __global__ void __launch_bounds__(kWarps * 32) rope_cache_write_kernel(const RopeArgs p, const RopeRows r) {
     ptx::griddep_wait();  // no early signal, as above
-    const int parts = p.x ? (p.N + kHeads - 1) / kHeads : 0;
+    const int parts = p.x ? (p.N + 8 * kRows - 1) / (8 * kRows) : 0;
     const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (w < p.T)
         rope_row<kFp8>(p, r, (int)w, lane);
     else if (w < (int64_t)p.T * (parts + 1))
-        rope_heads(p, (int)((w - p.T) / parts), (int)((w - p.T) % parts), lane);
+        rope_heads<kRows>(p, (int)((w - p.T) / parts), (int)((w - p.T) % parts), lane);
 }
 
 unsigned blocks_of(int64_t warps) { return (unsigned)((warps + kWarps - 1) / kWarps); }
 
+template <int kRows>
+cudaError_t launch(const RopeArgs& a, cudaStream_t s) {
+    const int64_t parts = (a.N + 8 * kRows - 1) / (8 * kRows);
+    return launch_pdl(rope_kernel<kRows>, dim3(blocks_of(a.T * parts)), dim3(kWarps * 32), 0, s, a);
+}
+template <bool kFp8, int kRows>
+cudaError_t launch(const RopeArgs& a, const RopeRows& r, cudaStream_t s) {
+    const int64_t parts = a.x ? (a.N + 8 * kRows - 1) / (8 * kRows) : 0;
+    return launch_pdl(rope_cache_write_kernel<kFp8, kRows>, dim3(blocks_of(a.T * (parts + 1))), dim3(kWarps * 32), 0, s, a, r);
+}
+
 }  // namespace
 
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
-    return launch_pdl(rope_kernel, dim3(blocks_of((int64_t)a.T * ((a.N + kHeads - 1) / kHeads))), dim3(kWarps * 32), 0, s, a);
+    const int rows = rows_per_lane(a.N);
+    return rows == 4 ? launch<4>(a, s) : rows == 2 ? launch<2>(a, s) : launch<1>(a, s);
 }
 
 cudaError_t launch_rope_cache_write(const RopeArgs& a, const RopeRows& r, bool fp8, cudaStream_t s) {
-    const int64_t parts = a.x ? (a.N + kHeads - 1) / kHeads : 0;
-    return launch_pdl(fp8 ? rope_cache_write_kernel<true> : rope_cache_write_kernel<false>,
-                      dim3(blocks_of((int64_t)a.T * (parts + 1))), dim3(kWarps * 32), 0, s, a, r);
+    const int rows = rows_per_lane(a.N);
+    if (fp8) return rows == 4 ? launch<true, 4>(a, r, s) : rows == 2 ? launch<true, 2>(a, r, s) : launch<true, 1>(a, r, s);
+    return rows == 4 ? launch<false, 4>(a, r, s) : rows == 2 ? launch<false, 2>(a, r, s) : launch<false, 1>(a, r, s);
 }
 
 }  // namespace mla

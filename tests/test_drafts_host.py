@@ -104,7 +104,7 @@ def test_fork_pages_refusals(lib):  # noqa: F811
     assert call(ws=ctypes.c_void_p(0x1010)) == mla.ERR_UNSUPPORTED
     assert call(B=0, B2=0, nb=0) == mla.OK
     assert lib.mla_fork_pages_workspace_bytes(-1, 1, 1) == 0
-    assert lib.mla_fork_pages_workspace_bytes(2, 3, 8) >= 256 + 3 * 16 + 2 * 4 + 8 * 4
+    assert lib.mla_fork_pages_workspace_bytes(2, 3, 8) >= 256 + 3 * 32 + 2 * 4 + 8 * 4
 
 
 def test_frequencies(lib):  # noqa: F811
