@@ -14,6 +14,7 @@ import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libmla_latent_kv.so")
+BINDING_PATH = os.path.join(HERE, "_build", "_mla_torch.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "mla_latent_kv.h")
 
 KV_BF16, KV_FP8 = 0, 1
@@ -653,70 +654,48 @@ def rope_frequencies(base=10000.0, factor=1.0, trained=4096, beta_fast=32.0, bet
     return out
 
 
-def _is_freq(t):
-    import torch
-    if t.dtype is not torch.float64 or t.shape != (R // 2,) or not t.is_contiguous() or not t.is_cpu:
-        raise ValueError(f"inv_freq must be a contiguous float64 CPU tensor of {R // 2} elements, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
+_torch_binding = None
 
 
-def _row_strides(name, t, shape):
-    """Strides of a bf16 tensor of the shape with unit inner stride, else refused."""
-    import torch
-    s = t.stride()
-    if t.dtype is not torch.bfloat16 or t.shape != shape or s[-1] != 1:
-        raise ValueError(f"{name} must be bf16 of shape {tuple(shape)} with unit inner stride, got {t.dtype} "
-                         f"{tuple(t.shape)} with strides {s}")
-    return s
+def _native():
+    """The compiled torch side of these calls: it checks the tensors, makes what is not given and launches
+    (raises if it has not been built)."""
+    global _torch_binding
+    if _torch_binding is None:
+        lib()
+        import importlib.machinery
+        import importlib.util
+
+        import torch  # noqa: F401 (its libraries are loaded before the binding)
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"torch binding missing: {BINDING_PATH} (build it with `python -m mla_latent_kv_gb300.build`)")
+        loader = importlib.machinery.ExtensionFileLoader("_mla_torch", BINDING_PATH)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_mla_torch", loader))
+        loader.exec_module(module)
+        module.set_error(MlaError)
+        _torch_binding = module
+    return _torch_binding
 
 
 def rope(x, positions, inv_freq, adjacent=True, mscale=1.0, out=None, stream=None):
     """x [T, N, 64] bf16 (a part of longer rows where the strides say so) turned by positions [T] int32 and
     inv_freq (rope_frequencies) -> bf16 [T, N, 64]. `out` may be x itself. adjacent: pairs (2i, 2i+1), else
     (i, i+32). Negative positions turn back."""
-    import torch
-    shape = x.shape
-    if len(shape) != 3 or shape[2] != R:
-        raise ValueError(f"x must be [T, N, {R}], got {tuple(shape)}")
-    xs = _row_strides("x", x, shape)
-    T, N = shape[0], shape[1]
-    _is_shape("positions", positions, torch.int32, (T,))
-    _is_freq(inv_freq)
-    if out is None:
-        if stream is not None:
+    if stream is not None:
+        if out is None:
             return _on(stream, "rope", locals())
-        out = torch.empty((T, N, R), dtype=torch.bfloat16, device=x.device)
-    os = _row_strides("out", out, shape)
-    s = _raw_stream(stream, x, positions, out)
-    _check(lib().mla_rope(x.data_ptr(), xs[0], xs[1], positions.data_ptr(), inv_freq.data_ptr(), mscale, 1 if adjacent else 0,
-                          out.data_ptr(), os[0], os[1], T, N, s))
-    return out
+        stream = stream.cuda_stream
+    return _native().rope(x, positions, inv_freq, adjacent, mscale, out, stream)
 
 
 def rope_cache_write(kv_c, k_pe, positions, inv_freq, slot_mapping, kv_cache, kv_dtype=KV_BF16, adjacent=True, mscale=1.0,
                      kv_scale=0.0, q_pe=None, q_out=None, dev_status=None, stream=None, num_blocks=None):
     """cache_write() of kv_c [T, 512] and of k_pe [T, 64] turned as by rope(), and, if given, rope() of
     q_pe [T, H, 64] into q_out (the last 64 dims of the absorbed queries, say), in one launch -> kv_cache."""
-    import torch
-    T = slot_mapping.shape[0]
-    _is_shape("slot_mapping", slot_mapping, torch.int64, (T,))
-    cs, ps = _row_strides("kv_c", kv_c, (T, L)), _row_strides("k_pe", k_pe, (T, R))
-    _is_shape("positions", positions, torch.int32, (T,))
-    _is_freq(inv_freq)
-    if (q_pe is None) != (q_out is None):
-        raise ValueError("q_pe and q_out go together")
-    H, qs, os = 1, (0, 0), (0, 0)
-    if q_pe is not None:
-        H = q_pe.shape[1]
-        qs, os = _row_strides("q_pe", q_pe, (T, H, R)), _row_strides("q_out", q_out, (T, H, R))
-    nb = _cache_blocks(kv_cache, kv_dtype, num_blocks)
-    _check_status(dev_status)
-    s = _raw_stream(stream, kv_cache, kv_c, k_pe, positions, slot_mapping, q_pe, q_out, dev_status)
-    _check(lib().mla_rope_cache_write(kv_c.data_ptr(), cs[0], k_pe.data_ptr(), ps[0], _a(q_pe), qs[0], qs[1], _a(q_out), os[0],
-                                      os[1], positions.data_ptr(), inv_freq.data_ptr(), mscale, 1 if adjacent else 0,
-                                      slot_mapping.data_ptr(), T, H, kv_cache.data_ptr(), kv_dtype, nb, kv_scale,
-                                      _a(dev_status), s))
-    return kv_cache
+    if stream is not None:
+        stream = stream.cuda_stream
+    return _native().rope_cache_write(kv_c, k_pe, positions, inv_freq, slot_mapping, kv_cache, kv_dtype, adjacent, mscale,
+                                      kv_scale, q_pe, q_out, dev_status, stream, num_blocks)
 
 
 def decode_tree_workspace_bytes(B: int, Sq: int, H: int, max_seq_len: int, kv_dtype: int = KV_BF16) -> int:
@@ -727,33 +706,12 @@ def decode_tree(q, kv_cache, block_table, seq_lens, tree_mask, max_seq_len, scal
                 o_latent=None, o_dtype=None, lse=None, dev_status=None, stream=None, num_blocks=None):
     """decode() of requests whose last Sq tokens are drafts: row t sees the tokens before them and the drafts
     whose bits are set in tree_mask [B, Sq] int64 -> (o_latent [B,Sq,H,512], lse [B,Sq,H])."""
-    import torch
-    B, Sq, H = _page_args(q, block_table, seq_lens)
-    _is_shape("tree_mask", tree_mask, torch.int64, (B, Sq))
-    nb = _cache_blocks(kv_cache, kv_dtype, num_blocks)
-    l = lib()
-    need = 0 if workspace is not None else l.mla_decode_tree_workspace_bytes(kv_dtype, B, Sq, H, int(max_seq_len))
-    if stream is not None and (o_latent is None or lse is None or (need and workspace is None)):
-        return _on(stream, "decode_tree", locals())
-    o_latent, o_dtype, lse, workspace, ws_bytes = _attention_bufs(q, B, Sq, H, o_latent, o_dtype, lse, workspace, need)
-    _check_status(dev_status)
-    s = _raw_stream(stream, q, kv_cache, block_table, seq_lens, tree_mask, o_latent, lse, workspace, dev_status)
-    _check(l.mla_decode_tree(q.data_ptr(), kv_cache.data_ptr(), kv_dtype, nb, block_table.data_ptr(), block_table.shape[1],
-                             seq_lens.data_ptr(), tree_mask.data_ptr(), int(max_seq_len), B, Sq, H, float(scale),
-                             _a(workspace), ws_bytes, o_latent.data_ptr(), o_dtype, lse.data_ptr(), _a(dev_status), s))
-    return o_latent, lse
-
-
-def _layer_blocks(kv_cache, kv_dtype):
-    """(layers, blocks) of a cache [num_blocks, ...] or [layers, num_blocks, ...] of whole pages."""
-    rb = _ROW_BYTES.get(kv_dtype)
-    if rb is None:
-        raise MlaError(ERR_INVALID_ARG, f"unknown kv_dtype {kv_dtype}")
-    page = kv_cache.shape[-1] * kv_cache.element_size()
-    if kv_cache.ndim not in (2, 3) or page != PAGE * rb or not kv_cache.is_contiguous():
-        raise ValueError(f"kv_cache must be contiguous [num_blocks, page] or [layers, num_blocks, page] with pages of "
-                         f"{PAGE * rb} bytes, got {tuple(kv_cache.shape)} {kv_cache.dtype}")
-    return (1 if kv_cache.ndim == 2 else kv_cache.shape[0]), kv_cache.shape[-2]
+    if stream is not None:
+        if o_latent is None or lse is None or workspace is None:
+            return _on(stream, "decode_tree", locals())
+        stream = stream.cuda_stream
+    return _native().decode_tree(q, kv_cache, block_table, seq_lens, tree_mask, max_seq_len, scale, kv_dtype, workspace,
+                                 o_latent, o_dtype, lse, dev_status, stream, num_blocks)
 
 
 def accept_tokens(kv_cache, block_table, seq_lens, path, counts, kv_dtype=KV_BF16, new_lens=None, dev_status=None,
@@ -761,26 +719,11 @@ def accept_tokens(kv_cache, block_table, seq_lens, path, counts, kv_dtype=KV_BF1
     """The accepted drafts path[b, :counts[b]] (ascending, of the Sq = path.shape[1] last tokens) become the tokens
     behind those before the drafts, in every layer of kv_cache [num_blocks, page] or [layers, num_blocks, page]
     -> new_lens [B] int32."""
-    import torch
-    _is("block_table", block_table, torch.int32, 2)
-    B = block_table.shape[0]
-    _is_shape("seq_lens", seq_lens, torch.int32, (B,))
-    _is("path", path, torch.int32, 2)
-    _is_shape("counts", counts, torch.int32, (B,))
-    if path.shape[0] != B:
-        raise ValueError(f"path must be [{B}, Sq], got {tuple(path.shape)}")
-    layers, nb = _layer_blocks(kv_cache, kv_dtype)
-    if stream is not None and new_lens is None:
-        return _on(stream, "accept_tokens", locals())
-    if new_lens is None:
-        new_lens = torch.empty((B,), dtype=torch.int32, device=seq_lens.device)
-    _is_shape("new_lens", new_lens, torch.int32, (B,))
-    _check_status(dev_status)
-    s = _raw_stream(stream, kv_cache, block_table, seq_lens, path, counts, new_lens, dev_status)
-    _check(lib().mla_accept_tokens(kv_cache.data_ptr(), kv_dtype, layers, nb, block_table.data_ptr(), block_table.shape[1],
-                                   seq_lens.data_ptr(), path.data_ptr(), counts.data_ptr(), B, path.shape[1],
-                                   new_lens.data_ptr(), _a(dev_status), s))
-    return new_lens
+    if stream is not None:
+        if new_lens is None:
+            return _on(stream, "accept_tokens", locals())
+        stream = stream.cuda_stream
+    return _native().accept_tokens(kv_cache, block_table, seq_lens, path, counts, kv_dtype, new_lens, dev_status, stream)
 
 
 def fork_pages_workspace_bytes(B: int, B2: int, num_blocks: int) -> int:
@@ -793,38 +736,9 @@ def fork_pages(kv_cache, block_table, page_counts, seq_lens, refs, parents, room
     rows that nobody goes on from are dropped, pages held in part are copied in every layer of kv_cache
     [num_blocks, page] or [layers, num_blocks, page] where rows part -> (table [B2, max_blocks], page_counts [B2],
     seq_lens [B2], refs [num_blocks]), written into the tuple `out` when given (other buffers than the old state's)."""
-    import torch
-    i32 = torch.int32
-    _is("block_table", block_table, i32, 2)
-    B, max_blocks = block_table.shape
-    _is_shape("page_counts", page_counts, i32, (B,))
-    _is_shape("seq_lens", seq_lens, i32, (B,))
-    layers, nb = _layer_blocks(kv_cache, kv_dtype)
-    _is_shape("refs", refs, i32, (nb,))
-    _is("parents", parents, i32, 1)
-    B2 = parents.shape[0]
-    _is_shape("room", room, i32, (B2,))
-    if stream is not None and (out is None or workspace is None):
-        return _on(stream, "fork_pages", locals())
-    if out is None:
-        made = {"dtype": i32, "device": refs.device}
-        out = (torch.empty((B2, max_blocks), **made), torch.empty((B2,), **made), torch.empty((B2,), **made),
-               torch.empty((nb,), **made))
-    table, counts, lens, new_refs = out
-    _is_shape("out[0]", table, i32, (B2, max_blocks))
-    _is_shape("out[1]", counts, i32, (B2,))
-    _is_shape("out[2]", lens, i32, (B2,))
-    _is_shape("out[3]", new_refs, i32, (nb,))
-    l = lib()
-    if workspace is None:
-        workspace = torch.empty(l.mla_fork_pages_workspace_bytes(B, B2, nb), dtype=torch.uint8, device=refs.device)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _check_status(dev_status)
-    s = _raw_stream(stream, refs, kv_cache, block_table, page_counts, seq_lens, parents, room, table, counts, lens, new_refs,
-                    workspace, dev_status)
-    _check(l.mla_fork_pages(kv_cache.data_ptr(), kv_dtype, layers, nb, block_table.data_ptr(), max_blocks,
-                            page_counts.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), B, parents.data_ptr(),
-                            room.data_ptr(), B2, table.data_ptr(), counts.data_ptr(), lens.data_ptr(), new_refs.data_ptr(),
-                            workspace.data_ptr(), workspace.nbytes, _a(dev_status), s))
-    return table, counts, lens, new_refs
+    if stream is not None:
+        if out is None or workspace is None:
+            return _on(stream, "fork_pages", locals())
+        stream = stream.cuda_stream
+    return _native().fork_pages(kv_cache, block_table, page_counts, seq_lens, refs, parents, room, kv_dtype, out, workspace,
+                                dev_status, stream)

@@ -1,10 +1,11 @@
-"""Build the CUDA library libmla_latent_kv.so in-tree (nvcc, sm_103a only).
+"""Build the CUDA library libmla_latent_kv.so (nvcc, sm_103a only) and the torch binding in-tree.
 
     python -m mla_latent_kv_gb300.build [--force] [--verbose]
 
 Each .cu under csrc/ is compiled in parallel to an object file, then linked into
 mla_latent_kv_gb300/_build/libmla_latent_kv.so (the CUDA runtime is linked statically, so the
-library loads on a machine without a GPU; CUDA calls then fail with MLA_ERR_CUDA).
+library loads on a machine without a GPU; CUDA calls then fail with MLA_ERR_CUDA). binding.cpp, which reads
+torch tensors, is compiled beside them by the host compiler into _build/_mla_torch.so and linked to the library.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +22,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmla_latent_kv.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(BUILD, "_mla_torch.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -33,19 +37,39 @@ def _nvcc() -> str:
     return p if os.path.exists(p) else "nvcc"
 
 
+def _cuda_home() -> str:
+    return os.environ.get("CUDA_HOME", "/usr/local/cuda")
+
+
+def _binding_cmd(obj):
+    import torch
+    home = os.path.dirname(torch.__file__)
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE,
+            "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(home, "include"),
+            "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(_cuda_home(), "include"), "-c", BINDING_SRC, "-o", obj]
+
+
+def _binding_link(obj, out):
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return [os.environ.get("CXX", "g++"), "-shared", "-o", out, obj, "-L", BUILD, "-l:" + os.path.basename(LIB),
+            "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs]
+
+
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
 def _deps():
-    return (sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+    return (sources() + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -58,27 +82,29 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-        cmd = [nvcc, *ARCH, *NVCC_FLAGS, *extra, "-c", src, "-o", obj]
+        cmd = _binding_cmd(obj) if src == BINDING_SRC else [nvcc, *ARCH, *NVCC_FLAGS, *extra, "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, r
 
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        results = list(ex.map(compile_one, sources()))
+        results = list(ex.map(compile_one, [BINDING_SRC] + sources()))
     failed = False
     for src, _, r in results:
         if r.returncode != 0 or (verbose and r.stderr):
             sys.stderr.write(f"--- {os.path.basename(src)}\n{r.stdout}{r.stderr}")
         failed |= r.returncode != 0
     if failed:
-        raise RuntimeError("nvcc failed; see messages above")
+        raise RuntimeError("a compiler failed; see messages above")
+    binding_obj = results[0][1]
     tmp = LIB + f".{os.getpid()}.tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *[o for _, o, _ in results],
+    cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *[o for _, o, _ in results[1:]],
            "-lpthread", "-ldl", "-lrt"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("nvcc link failed")
-    os.replace(tmp, LIB)
+    for cmd, out in ((cmd, LIB), (_binding_link(binding_obj, BINDING + f".{os.getpid()}.tmp"), BINDING)):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("link failed")
+        os.replace(out + f".{os.getpid()}.tmp", out)
     return LIB
 
 

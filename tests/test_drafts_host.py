@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 
 from drafts_util import accept_rule, fork_rule
-from test_longctx_host import _call, _FakeLib, lib  # noqa: F401 (lib: a fixture)
+from test_longctx_host import _call, lib  # noqa: F401 (lib: a fixture)
 
 mla = pytest.importorskip("mla_latent_kv_gb300")
 P = ctypes.c_void_p(0x1000)      # never dereferenced: every call here is refused first
@@ -143,7 +143,7 @@ def _args(torch):
 
 
 @pytest.mark.parametrize("call", ["rope", "rope_cache_write", "decode_tree", "accept_tokens", "fork_pages"])
-def test_binding_refuses_wrong_tensors(call):
+def test_binding_refuses_wrong_tensors(call, lib):  # noqa: F811
     torch = pytest.importorskip("torch")
     good = _args(torch)[call]
     for name, t in good.items():
@@ -164,8 +164,10 @@ def test_binding_refuses_wrong_tensors(call):
                 continue
             with pytest.raises((ValueError, mla.MlaError)):
                 getattr(mla, call)(**{**good, name: bad})
-    with pytest.raises(ValueError):  # not on the device
+    with pytest.raises(ValueError, match="device"):
         getattr(mla, call)(**good)
+    with pytest.raises(TypeError):
+        getattr(mla, call)(**{**good, next(iter(good)): None})
     if call != "rope":
         with pytest.raises(ValueError, match="dev_status"):
             getattr(mla, call)(**good, dev_status=torch.zeros(1))
@@ -173,9 +175,10 @@ def test_binding_refuses_wrong_tensors(call):
 
 @pytest.mark.parametrize("call", ["rope", "decode_tree", "accept_tokens", "fork_pages"])
 def test_buffers_are_made_on_the_stream_that_uses_them(call, monkeypatch):
-    """As the other calls: what a call with stream= makes itself, it makes on that stream."""
+    """As the other calls: what a call with stream= makes itself, it makes with that stream as the current one,
+    and a call that is given every buffer goes to the stream as it is."""
     torch = pytest.importorskip("torch")
-    here, made, used, launched = [], [], [], []
+    here, native, used = [], [], []
 
     class OnStream:
         def __init__(self, stream):
@@ -187,34 +190,31 @@ def test_buffers_are_made_on_the_stream_that_uses_them(call, monkeypatch):
         def __exit__(self, *exc):
             here.pop()
 
-    args, empty = _args(torch)[call], torch.empty
-
-    def recorded(*a, **kw):
-        made.append(here[-1] if here else "current")
-        return empty(*a, **kw)
-    monkeypatch.setattr(mla, "lib", _FakeLib)
-    monkeypatch.setattr(mla, "_raw_stream", lambda *a: 0)
+    class Native:
+        def __getattr__(self, name):
+            def f(*args):
+                native.append((here[-1] if here else "current", args[-2 if name == "decode_tree" else -1]))
+                return (torch.zeros(2),) * (2 if name == "decode_tree" else 4) if name in ("decode_tree", "fork_pages") \
+                    else torch.zeros(2)
+            return f
+    args = _args(torch)[call]
+    monkeypatch.setattr(mla, "_native", Native)
     monkeypatch.setattr(torch.cuda, "stream", OnStream)
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda s: types.SimpleNamespace(device=0, name=s))
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device: "current")
-    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: used.append((t.data_ptr(), s)))
-    monkeypatch.setattr(torch, "empty", recorded)
-    for given, where in (({}, "current"), ({"stream": types.SimpleNamespace(cuda_stream="side")}, "side")):
-        made.clear()
-        out = getattr(mla, call)(**args, **given)
-        assert made and set(made) == {where}
-        outs = out if isinstance(out, tuple) else (out,)
-        assert used == [(t.data_ptr(), "current") for t in outs if given]
-    made.clear()
-    used.clear()
-    monkeypatch.setattr(torch.cuda, "stream", None)
-    monkeypatch.setattr(mla, "_raw_stream", lambda s, *t: launched.append(s))
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: used.append(s))
+    side = types.SimpleNamespace(cuda_stream="side")
+    getattr(mla, call)(**args)
+    assert native == [("current", None)] and used == []
+    out = getattr(mla, call)(**args, stream=side)
+    assert native[1:] == [("side", None)]
+    assert used == ["current"] * (len(out) if isinstance(out, tuple) else 1)  # kept while the caller's stream reads them
     ws = torch.zeros(4096, dtype=torch.uint8)
     bufs = {"rope": lambda: dict(out=out), "accept_tokens": lambda: dict(new_lens=out),
             "decode_tree": lambda: dict(o_latent=out[0], lse=out[1], workspace=ws),
             "fork_pages": lambda: dict(out=out, workspace=ws)}[call]()
-    getattr(mla, call)(**args, **bufs, stream="side")
-    assert made == [] and used == [] and launched == ["side"]
+    getattr(mla, call)(**args, **bufs, stream=side)
+    assert native[2:] == [("current", "side")] and len(used) == (len(out) if isinstance(out, tuple) else 1)
 
 
 def test_the_plain_rules():
