@@ -153,8 +153,6 @@ constexpr uint32_t kBarStage0 = 5;                          // [2] one per softm
 constexpr uint32_t kBarEpi = 4;                             // [2] named barriers of CTA 1's epilogue sets
 constexpr int kPrefetchAhead = 8;  // pages (two groups) between the helpers' progress and the page prefetched into L2
 
-// kTree: a request's drafts as one row, see DecodeArgs.
-template <bool kTree>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     decode_sm103_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap kvh_map,
                         const __grid_constant__ CUtensorMap q_map,
@@ -381,10 +379,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // token dominates; lt sums the unrounded P for the LSE. Each half keeps its own sums
             // (same running max); they are added at the end.
             float m_run = kNoMax, l_run = 0.f, lt_run = 0.f;
-            // trees: the drafts that the row sees, and its tokens before them. Read behind the wait for Q, which
-            // the wait for the kernel ahead precedes.
-            const uint64_t mask = kTree && npages > 0 ? draft_mask(p, g.b, row) : 0;
-            const int drafts0 = kTree ? drafts_start(p, g.b) : 0;
             const uint32_t pbuf_remote = map_to_rank(sbase + OFF_PB, 1);
             const uint32_t pfull_remote = map_to_rank(bar(B_PFULL), 1);
             for (int gi = 0; gi < ngroups; ++gi) {
@@ -417,18 +411,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (j >= v) s[c][j] = __float_as_uint(-CUDART_INF_F);
-                    }
-                }
-                if (kTree) {
-                    const int at = g.j0 + kPage * pg0 - drafts0;  // the half's first token among the drafts
-                    if (at > -2 * kPage) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t seen = seen_tokens(mask, at + 32 * c);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (!(seen >> j & 1u)) s[c][j] = __float_as_uint(-CUDART_INF_F);
-                        }
                     }
                 }
 #pragma unroll
@@ -605,7 +587,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int ctid = tid - 64;  // 0..255; 0..127 are the helper warps
             const int eset = warp >= 6 ? 1 : 0;
             int pages_ready = warp >= 6 ? npages : 0;
-            const int drafts0 = kTree ? drafts_start(p, g.b) : 0;
             for (int i = 0; i < npages && warp < 6; ++i) {
                 const int pb = i % kPBufs, up = i / kPBufs;
                 if (!warp_wait(bar(B_PFULL + pb), up & 1, abort, ds)) break;
@@ -645,11 +626,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             *reinterpret_cast<uint4*>(smem + vb + pn * kVBox + rr * 128 + cc * 16) =
                                 make_uint4(0, 0, 0, 0);
                         }
-                        fence_proxy_async_cta();
-                    }
-                    if (kTree && vh > 0 && g.j0 + kPage * (i + 1) > drafts0) {  // the page's drafts, hidden from some
-                        const uint32_t vb = sbase + OFF_V + st * kVStageBytes;
-                        for (int q = ctid; q < kVStageBytes / 16; q += 128) zero_nonfinite(vb + 16 * q);
                         fence_proxy_async_cta();
                     }
                 }
@@ -725,20 +701,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();
 }
 
-int g_attr_done[2][64] = {};
+int g_attr_done[64] = {};
 
 }  // namespace
 
 cudaError_t launch_decode_sm103(const DecodeArgs& a, cudaStream_t s) {
-    const bool tree = a.masks != nullptr;
-    auto* kernel = tree ? decode_sm103_kernel<true> : decode_sm103_kernel<false>;
+    auto* kernel = decode_sm103_kernel;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev < 64 && !g_attr_done[tree][dev]) {
+    if (dev < 64 && !g_attr_done[dev]) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         if (e != cudaSuccess) return e;
-        g_attr_done[tree][dev] = 1;
+        g_attr_done[dev] = 1;
     }
     CUtensorMap kv_map, kvh_map, q_map, o_map, p_map;
     memset(&kv_map, 0, sizeof kv_map);

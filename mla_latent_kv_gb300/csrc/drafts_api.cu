@@ -64,9 +64,11 @@ mla_status rope_args(const char* who, const void* x, int64_t x_t, int64_t x_n, c
 }
 
 // ------------------------------------------------------------------------------------ tree
-// How a tree call runs, and its workspace. At most 128 (draft, head) pairs are one row of so many heads for
-// the decode kernels (splits: theirs). More go through a kernel of their own, 256 at a time; its workspace is the
-// widened rows (FP8), then the partial states.
+// How a tree call runs, and its workspace. At most 32 (draft, head) pairs, or 128 over an FP8 cache, are one row
+// of so many heads for the decode kernels (splits: theirs). More go through a kernel of their own, 256 at a time;
+// its workspace is the widened rows (FP8), then the partial states. Both sides of the border: 64 requests of up to
+// 8192 tokens, bf16, 32 pairs 131 us as a row and 147 by the tree kernel; 112 pairs 157 and 146, FP8 233 and 303;
+// 128 requests of up to 1000 tokens, 128 pairs, bf16 80 and 66, FP8 74 and 107.
 struct TreePlan {
     bool rows;
     int splits, tiles, pages_per_split, wide_pages;
@@ -75,10 +77,14 @@ struct TreePlan {
 bool plan_tree(mla_kv_dtype kv, int B, int Sq, int H, int max_seq_len, TreePlan* w) {
     const int64_t flat = (int64_t)Sq * H;
     const int pages = (max_seq_len + mla::kPage - 1) / mla::kPage;
-    w->rows = flat <= MLA_MAX_HEADS;
+    w->rows = mla::few_heads((int)std::min<int64_t>(flat, INT32_MAX)) || (kv == MLA_KV_FP8_E4M3_SCALED && flat <= MLA_MAX_HEADS);
     if (w->rows) {
         const bool few = mla::few_heads((int)flat);
-        w->splits = mla::resolve_splits(few, -1, B, (int)flat, max_seq_len);
+        // Over an FP8 cache with more than 32 pairs: short requests one unit each where there are more of them than SM
+        // pairs (128 of up to 1000 tokens 74 us, by the schedule built on the device 85), long ones by the schedule
+        // (64 of up to 8192 212 us, one unit each 222; 40 of them 145, three units each 157).
+        const int splits = few ? -1 : pages <= 32 && B > 76 ? 1 : pages >= 128 && B >= 4 ? -2 : -1;
+        w->splits = mla::resolve_splits(few, splits, B, (int)flat, max_seq_len);
         if (w->splits < 1 && w->splits != -2) return false;
         w->total = mla::workspace_layout(kv, B, B, (int)flat, w->splits, max_seq_len).total;
         return true;

@@ -61,7 +61,7 @@ struct DecodeArgs {
     const int* plan_count;      // [0] units actually planned, [1] split rows (rows with partials)
     const int* plan_split_rows; // the split rows' indices, plan_count[1] of them
     int plan_max_units;         // the grid is sized for this many units
-    // Trees of at most 128 (draft, head) pairs: one query row a request, whose "heads" are the pairs. Pair h
+    // Trees of few (draft, head) pairs: one query row a request, whose "heads" are the pairs. Pair h
     // is draft h / tree_heads and sees the bits of its mask among the request's last tree_drafts tokens.
     const uint64_t* masks;      // [B, tree_drafts], null: no tree
     int tree_drafts, tree_heads;
