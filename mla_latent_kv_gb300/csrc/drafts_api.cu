@@ -364,8 +364,7 @@ mla_status mla_fork_pages(void* kv_cache, mla_kv_dtype kv_dtype, int layers, int
     if ((refs && refs == new_refs) || (block_table && block_table == new_table) || (page_counts && page_counts == new_counts) ||
         (seq_lens && seq_lens == new_lens))
         return set_error(MLA_ERR_INVALID_ARG, "%s: the new state must not be the old one's buffers", who);
-    const int page = mla::kPage * (kv_dtype == MLA_KV_BF16 ? mla::kBf16RowBytes : mla::kFp8RowBytes);
-    if ((int64_t)B2 * (1 + (int64_t)layers * (page / 16384 + 1)) + B > (int64_t)INT32_MAX)
+    if ((int64_t)B2 * (1 + (int64_t)layers) + B > (int64_t)INT32_MAX)
         return set_error(MLA_ERR_UNSUPPORTED, "%s: %d rows of %d layers too many", who, B2, layers);
     const ForkLayout w = fork_layout(B, B2, num_blocks);
     if (!workspace || workspace_bytes < w.total)

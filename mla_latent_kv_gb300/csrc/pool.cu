@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptArgs
 constexpr int kPlanThreads = 1024;
 constexpr int kRefsPerThread = 8;  // of a step of the free-page search
 constexpr int kForkThreads = 256;
-constexpr int kCopyBytes = kForkThreads * 4 * 16;  // of a copy block
+constexpr int kCopyBatch = 5;  // 16-byte loads of a thread in flight
 
 // Whether the heir of an old row keeps the row's page j: the pages full of tokens that it may share, and of
 // the others those that nobody else holds (tokens will be written there).
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs 
 }
 
 template <int kRowBytes>
-__global__ void __launch_bounds__(kForkThreads) fork_apply_kernel(const ForkArgs p, int copy_blocks) {
+__global__ void __launch_bounds__(kForkThreads) fork_apply_kernel(const ForkArgs p) {
     ptx::griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool failed = p.head[0] != 0;
@@ -293,23 +293,24 @@ __global__ void __launch_bounds__(kForkThreads) fork_apply_kernel(const ForkArgs
             if (!(r >= 0 && heir_keeps(p, row, j, whole, held, need)) && in_pool(row[j])) atomicSub(p.new_refs + row[j], 1);
         return;
     }
-    u -= p.B;  // ---- a part of a new row's copied page, in one layer
-    const int r = (int)(u / ((int64_t)copy_blocks * p.layers));
-    const int part = (int)(u % copy_blocks), layer = (int)(u / copy_blocks % p.layers);
+    u -= p.B;  // ---- a new row's copied page, in one layer
+    const int r = (int)(u / p.layers), layer = (int)(u % p.layers);
     const int4 rec = p.copies[r];
-    const int bytes = rec.z * kRowBytes, at = part * kCopyBytes + tid * 16;
-    if (part * kCopyBytes >= bytes || !in_pool(rec.x)) return;
+    const int bytes = rec.z * kRowBytes;
+    if (bytes == 0 || !in_pool(rec.x)) return;
     constexpr size_t kPageBytes = (size_t)kPage * kRowBytes;
     const uint8_t* src = p.cache + ((size_t)layer * p.num_blocks + rec.x) * kPageBytes;
     uint8_t* dst = p.cache + ((size_t)layer * p.num_blocks + rec.y) * kPageBytes;
-    uint4 v[4];
+    for (int at = tid * 16; at + 16 <= bytes; at += kForkThreads * kCopyBatch * 16) {
+        uint4 v[kCopyBatch];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (at + k * kForkThreads * 16 + 16 <= bytes) v[k] = *reinterpret_cast<const uint4*>(src + at + k * kForkThreads * 16);
+        for (int k = 0; k < kCopyBatch; ++k)
+            if (at + k * kForkThreads * 16 + 16 <= bytes) v[k] = *reinterpret_cast<const uint4*>(src + at + k * kForkThreads * 16);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (at + k * kForkThreads * 16 + 16 <= bytes) *reinterpret_cast<uint4*>(dst + at + k * kForkThreads * 16) = v[k];
-    if (kRowBytes % 16 && part == 0 && tid == 0 && bytes % 16)  // rows of 584 bytes: an odd number of 8-byte words
+        for (int k = 0; k < kCopyBatch; ++k)
+            if (at + k * kForkThreads * 16 + 16 <= bytes) *reinterpret_cast<uint4*>(dst + at + k * kForkThreads * 16) = v[k];
+    }
+    if (kRowBytes % 16 && tid == 0 && bytes % 16)  // rows of 584 bytes: an odd number of 8-byte words
         *reinterpret_cast<uint2*>(dst + bytes - 8) = *reinterpret_cast<const uint2*>(src + bytes - 8);
 }
 
@@ -324,10 +325,9 @@ cudaError_t launch_fork_pages(const ForkArgs& a, bool fp8, cudaStream_t s) {
     const int64_t refs = (a.num_blocks + kPlanThreads - 1) / kPlanThreads;
     cudaError_t e = launch_pdl(fork_plan_kernel, dim3((unsigned)(1 + (refs < 64 ? refs : 64))), dim3(kPlanThreads), 0, s, a);
     if (e != cudaSuccess) return e;
-    const int page = kPage * (fp8 ? kFp8RowBytes : kBf16RowBytes), copy_blocks = (page + kCopyBytes - 1) / kCopyBytes;
-    const int64_t blocks = (int64_t)a.B2 + a.B + (int64_t)a.B2 * a.layers * copy_blocks;
+    const int64_t blocks = (int64_t)a.B2 + a.B + (int64_t)a.B2 * a.layers;
     return launch_pdl(fp8 ? fork_apply_kernel<kFp8RowBytes> : fork_apply_kernel<kBf16RowBytes>, dim3((unsigned)blocks),
-                      dim3(kForkThreads), 0, s, a, copy_blocks);
+                      dim3(kForkThreads), 0, s, a);
 }
 
 }  // namespace mla
