@@ -87,9 +87,10 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
 // named barrier (kBar0 + set) and its own storing thread, so a set never waits for another and its
 // stores overlap its next panels. (Two rounds of eight panels with a barrier of all warps and one
 // storing thread took 6.3 us of a 22 us unit.) `off`: the tiles' place in shared memory, idle by now;
-// rows with `zero` are written as 0, rows that are not `live` and panels without `store` not at all.
+// rows with `zero` are written as 0, rows that are not `live` and panels without `store` not at all. The stores
+// are complete at the end, without kComplete only their reads of the tiles.
 constexpr int kTileBytes = 128 * 128;
-template <bool kF32, int kSets, int kBufs, uint32_t kBar0>
+template <bool kF32, int kSets, int kBufs, uint32_t kBar0, bool kComplete = true>
 __device__ __forceinline__ void store_rows(uint8_t* smem, uint32_t sbase, int off, uint32_t taddr, int row, int set,
                                            bool issuer, bool live, bool zero, float inv, const void* map, int y, int z,
                                            bool store) {
@@ -137,7 +138,12 @@ __device__ __forceinline__ void store_rows(uint8_t* smem, uint32_t sbase, int of
         if (issuer && store) ptx::tma_store_3d(map, sbase + buf, panel * (kF32 ? 32 : 64), y, z);
         if (issuer) ptx::bulk_commit_group();
     }
-    if (issuer) ptx::bulk_wait_group<0>();  // the stores are complete before the CTA exits
+    if (issuer) {
+        if (kComplete)
+            ptx::bulk_wait_group<0>();  // the stores are complete before the CTA exits
+        else
+            ptx::bulk_wait_group_read<0>();
+    }
 }
 
 // Visible rows of the unit's page `page` (0 past its last page).

@@ -59,7 +59,8 @@ constexpr int kPageBox = kPage * 128;        // one page's rows of one 64-dim pa
 constexpr int kSlotPanels = 3;
 constexpr int kSlotBytes = kSlotPanels * kPageBox;  // 24 KB
 constexpr int kSlots = 5;                    // K ring of a scores CTA
-constexpr int kQPanelBytes = 128 * 128;      // 128 rows x 64 dims of Q (16 KB)
+constexpr int kQPanelBytes = 128 * 128;      // 128 rows x 64 dims of Q (16 KB), loaded as two halves of 64 rows
+constexpr int kQHalfBytes = kQPanelBytes / 2;
 constexpr int kPBufs = 5;                    // P buffers of an output CTA (one page each)
 constexpr int kVStages = 4;                  // V ring of an output CTA: a page's 4 panels each
 constexpr int kVStageBytes = 4 * kPageBox;   // 32 KB
@@ -68,13 +69,14 @@ constexpr int kPMsgBytes = (kPBytes + 512 + 4 + 15) / 16 * 16;  // P + alpha[128
 constexpr int kPBufStride = 17 * 1024;
 constexpr int kAuxWarp0 = 10, kAuxWarps = 8;
 constexpr int kRelayWarps = 4;               // of CTA 3, from warp 6 on
-constexpr int kCtrlBytes = 4096;
+constexpr int kCtrlBytes = 6144;
 // scores CTA
 constexpr int OFF_QROPE = kCtrlBytes;
 constexpr int OFF_RING = OFF_QROPE + kQPanelBytes;
 constexpr int kStages = 4;                   // P staging buffers: each of a group's pages has two
 constexpr int OFF_STAGE = OFF_RING + kSlots * kSlotBytes;
-constexpr int kSmem0 = OFF_STAGE + kStages * kPBufStride;
+constexpr int OFF_QX = OFF_STAGE + kStages * kPBufStride;  // one panel of Q
+constexpr int kSmem0 = OFF_QX + kQPanelBytes;
 // output CTA
 constexpr int OFF_V = kCtrlBytes;
 constexpr int OFF_PB = OFF_V + kVStages * kVStageBytes;
@@ -86,14 +88,16 @@ static_assert(OFF_RING % 1024 == 0 && OFF_STAGE % 1024 == 0 && OFF_PB % 1024 == 
                   kSlotBytes % 1024 == 0,
               "128-byte swizzled tiles need 1024-byte alignment");
 static_assert(OFF_V + 12 * dec::kTileBytes <= kSmem1, "epilogue tiles");
-// Q's latent panels land in the four staging buffers (panels 0-3) and at the end of the ring (panels
-// 4-7, over slots 2-4).
-static_assert(kSlots == 5 && kStages == 4 && 4 * kQPanelBytes <= 3 * kSlotBytes, "Q panel homes");
-constexpr int kQSlot0 = 2;  // the first ring slot that holds Q's panels for a while
-constexpr int OFF_Q47 = OFF_RING + kSlots * kSlotBytes - 4 * kQPanelBytes;
-static_assert(OFF_Q47 % 1024 == 0 && OFF_Q47 >= OFF_RING + kQSlot0 * kSlotBytes, "Q panel homes");
-__device__ __forceinline__ uint32_t q_panel_off(int pn) {
-    return pn < 4 ? OFF_STAGE + pn * kPBufStride : OFF_Q47 + (pn - 4) * kQPanelBytes;
+// Q's sixteen latent half panels land in the four staging buffers, a place of their own and the two ring
+// slots that the unit's keys need last, so that its first group loads beside Q.
+static_assert(kSlots == 5 && kStages == 4 && 3 * kQHalfBytes == kSlotBytes && kPBufStride >= kQPanelBytes, "Q panel homes");
+static_assert(OFF_QX % 1024 == 0, "Q panel homes");
+// `slot0`: the ring slot of the unit's first keys.
+__device__ __forceinline__ uint32_t q_half_off(int h, int slot0) {
+    if (h < 8) return OFF_STAGE + (h >> 1) * kPBufStride + (h & 1) * kQHalfBytes;
+    if (h < 10) return OFF_QX + (h - 8) * kQHalfBytes;
+    const int behind = h < 13 ? 3 : 4;
+    return OFF_RING + (slot0 + behind) % kSlots * kSlotBytes + (h - (h < 13 ? 10 : 13)) * kQHalfBytes;
 }
 
 // Barrier slots, one layout for all four CTAs (multicast commits land at the same offset in each).
@@ -125,9 +129,10 @@ constexpr int OFF_ABORT = 516;
 constexpr int OFF_MX = 1024;      // scores: f32 [4][128] exchange between the column quarters
 constexpr int OFF_STAT_M = 2048;  // output: f32 [128] final running max (log2 units)
 constexpr int OFF_STAT_L = 2560;  // output: f32 [128] row sum
-constexpr int kMaxSorted = 512;   // requests that are put in order of their lengths
-constexpr int OFF_ORDER = 3072;   // u16 [kMaxSorted] requests, longest first (their lengths pass by OFF_MX)
-static_assert(OFF_MX + 4 * kMaxSorted <= OFF_ORDER && OFF_ORDER + 2 * kMaxSorted <= kCtrlBytes, "control block");
+constexpr int kMaxSorted = 512;   // requests whose lengths are kept and, for more units than clusters, sorted
+constexpr int OFF_ORDER = 3072;   // u16 [kMaxSorted] requests, longest first
+constexpr int OFF_LENS = 4096;    // s32 [kMaxSorted] tokens of each request
+static_assert(OFF_ORDER + 2 * kMaxSorted <= OFF_LENS && OFF_LENS + 4 * kMaxSorted <= kCtrlBytes, "control block");
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256;  // scores: Q latent in columns [0, 256), S buffers at 256 and 384
@@ -172,34 +177,25 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     auto bar = [&](int i) -> uint32_t { return sbase + 8u * (uint32_t)i; };
     auto length = [&](int b) -> int { return min(max(p.seq_lens[b], 0), p.max_seq_len); };
 
-    // Requests in order of length (ties by number), every thread placing one.
-    const bool sorted = p.B <= kMaxSorted;
-    if (sorted) {
-        int* lens = reinterpret_cast<int*>(smem + OFF_MX);
-        if (tid < p.B) lens[tid] = length(tid);
-        __syncthreads();
-        if (tid < p.B) {
-            const int mine = lens[tid];
-            int place = 0;
-            for (int b = 0; b < p.B; ++b) place += lens[b] > mine || (lens[b] == mine && b < tid);
-            reinterpret_cast<uint16_t*>(smem + OFF_ORDER)[place] = (uint16_t)tid;
-        }
-    }
-    if (tid == 0) {
-        *abort = 0;
-        for (int i = 0; i < B_COUNT; ++i) {
-            uint32_t cnt = 1;
-            if (i >= B_SEMPTY && i < B_SEMPTY + 2) cnt = 32;
-            if (i == B_QREADY) cnt = kSoftThreads / 32;
-            if (i == B_STATS) cnt = 2;
-            if (i >= B_STAGEFULL && i < B_STAGEFULL + kStages) cnt = 8;
-            if (i >= B_READY && i < B_READY + kPBufs) cnt = 5;
-            if (i >= B_PEER && i < B_PEER + kPBufs) cnt = 4;
-            if (i >= B_VCLEAN && i < B_VCLEAN + 2) cnt = 2 * kAuxWarps;
-            bar_init(bar(i), cnt);
-        }
-        if (!scores)  // P buffers armed for their first message before a scores CTA can send one
-            for (int b = 0; b < kPBufs; ++b) bar_arrive_expect_tx(bar(B_PFULL + b), kPMsgBytes);
+    // Lengths, and the requests in their order (ties by number), every thread placing one.
+    const int clusters = (int)(gridDim.x >> 2), cluster = (int)(blockIdx.x >> 2);
+    const bool kept = p.B <= kMaxSorted, sorted = kept && p.units > clusters;
+    int* lens = reinterpret_cast<int*>(smem + OFF_LENS);
+    if (kept && tid < p.B) lens[tid] = length(tid);
+    if (tid == kThreads - 1) *abort = 0;
+    if (tid < B_COUNT) {
+        const int i = tid;
+        uint32_t cnt = 1;
+        if (i >= B_SEMPTY && i < B_SEMPTY + 2) cnt = 32;
+        if (i == B_QREADY) cnt = kSoftThreads / 32;
+        if (i == B_STATS) cnt = 2;
+        if (i >= B_STAGEFULL && i < B_STAGEFULL + kStages) cnt = 8;
+        if (i >= B_READY && i < B_READY + kPBufs) cnt = 5;
+        if (i >= B_PEER && i < B_PEER + kPBufs) cnt = 4;
+        if (i >= B_VCLEAN && i < B_VCLEAN + 2) cnt = 2 * kAuxWarps;
+        bar_init(bar(i), cnt);
+        // P buffers armed for their first message before a scores CTA can send one
+        if (!scores && i >= B_PFULL && i < B_PFULL + kPBufs) bar_arrive_expect_tx(bar(i), kPMsgBytes);
         fence_barrier_init();
     }
     if (warp == 0) {
@@ -209,7 +205,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    cluster_sync();  // every CTA's barriers exist before any remote arrive or copy
+    if (sorted && tid < p.B) {
+        const int mine = lens[tid];
+        int place = 0;
+        for (int b = 0; b < p.B; ++b) place += lens[b] > mine || (lens[b] == mine && b < tid);
+        reinterpret_cast<uint16_t*>(smem + OFF_ORDER)[place] = (uint16_t)tid;
+    }
+    cluster_sync();  // every CTA's barriers (and the order) exist before any remote arrive or copy
     const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM), 0);
     griddep_wait();  // q, the masks, the cache and the lengths may be earlier kernels' outputs
     if (tid == 0) griddep_launch_dependents();
@@ -217,7 +219,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     // The cluster's unit number k, of all units in the order (range of pages, request by length, tile): a
     // request's tiles run side by side and read its pages from L2, and ranges behind short requests' ends
     // come last.
-    const int clusters = (int)(gridDim.x >> 2), cluster = (int)(blockIdx.x >> 2);
     auto unit_of = [&](int k, Unit& u) -> bool {
         const int64_t i = (int64_t)k * clusters + (k & 1 ? clusters - 1 - cluster : cluster);
         if (i >= p.units) return false;
@@ -225,7 +226,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         u.tile = (int)(i % p.tiles);
         u.req = sorted ? (int)reinterpret_cast<const uint16_t*>(smem + OFF_ORDER)[place] : place;
         u.slab = split * p.B + u.req;
-        const int seq = length(u.req), pages = (seq + kPage - 1) / kPage;
+        const int seq = kept ? lens[u.req] : length(u.req), pages = (seq + kPage - 1) / kPage;
         u.page0 = min(pages, split * p.pages_per_split);
         u.npages = min(pages, u.page0 + p.pages_per_split) - u.page0;
         u.ngroups = (u.npages + kPPG - 1) / kPPG;
@@ -274,21 +275,20 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     if (rank == 0 && ds && (p.seq_lens[u.req] < 0 || p.seq_lens[u.req] > p.max_seq_len))
                         atomicOr(ds, MLA_DEV_SEQ_TOO_LONG);
                     if (u.npages == 0) continue;
+                    int y = page_row(u, side);  // looked up ahead of the waits
                     if (!(ok = drained())) break;
+                    const int slot0 = (int)(3 * g0 % kSlots);
                     bar_arrive_expect_tx(bar(B_QFULL), 9 * kQPanelBytes);
-                    for (int qn = 0; qn < 8; ++qn)
-                        tma_load_3d(sbase + q_panel_off(qn), &q_map, bar(B_QFULL), qn * 64, rows_of(u), u.req);
-                    tma_load_3d(sbase + OFF_QROPE, &q_map, bar(B_QFULL), 8 * 64, rows_of(u), u.req);
-                    bool q_moved = false;
+                    for (int h = 0; h < 18; ++h)
+                        tma_load_3d(sbase + (h < 16 ? q_half_off(h, slot0) : OFF_QROPE + (h - 16) * kQHalfBytes), &q_map,
+                                    bar(B_QFULL), (h >> 1) * 64, rows_of(u) + 64 * (h & 1), u.req);
                     for (int gi = 0; gi < u.ngroups && ok; ++gi) {
-                        const int y = page_row(u, kPPG * gi + side);
+                        if (gi > 0) y = page_row(u, kPPG * gi + side);
+                        // behind the first group: Q's panels have been moved out to TMEM
+                        if (gi == 1 && !(ok = wait_bar(bar(B_QREADY), n & 1, abort, ds))) break;
                         for (int t = 0; t < 3; ++t) {
                             const uint32_t m = 3 * (g0 + (uint32_t)gi) + (uint32_t)t;
                             const int slot = (int)(m % kSlots);
-                            if (slot >= kQSlot0 && !q_moved) {  // Q's panels have been moved out to TMEM
-                                if (!(ok = wait_bar(bar(B_QREADY), n & 1, abort, ds))) break;
-                                q_moved = true;
-                            }
                             if (m >= kSlots && !(ok = wait_bar<true>(bar(B_SLOTEMPTY + slot), (m / kSlots - 1) & 1, abort, ds))) break;
                             // both CTAs' bytes are counted on CTA 0's barrier
                             if (side == 0) bar_arrive_expect_tx(bar(B_SLOTFULL + slot), 2 * kSlotBytes);
@@ -419,12 +419,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     const bool okq = warp_wait(bar(B_QFULL), n & 1, abort, ds);
 #pragma unroll 1
                     for (int pn = 2 * quarter; pn < 2 * quarter + 2; ++pn) {
+                        const uint32_t home = q_half_off(2 * pn + (row >> 6), (int)(3 * g0 % kSlots)) + (row & 63) * 128;
                         uint32_t v[32];
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
                             uint4 x = make_uint4(0, 0, 0, 0);
                             if (okq)
-                                x = *reinterpret_cast<const uint4*>(smem + q_panel_off(pn) + row * 128 + ((c ^ (row & 7)) << 4));
+                                x = *reinterpret_cast<const uint4*>(smem + home + ((c ^ (row & 7)) << 4));
                             v[4 * c] = x.x;
                             v[4 * c + 1] = x.y;
                             v[4 * c + 2] = x.z;
@@ -733,10 +734,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 // cut off by the tensor map
                 const bool store = rows0 < p.flat_rows;
                 if (p.o_bf16)
-                    store_rows<false, 4, 3, kBarEpi>(smem, sbase, OFF_V, tmem + lane_base, row, eset, (ctid & 127) == 0, true,
+                    store_rows<false, 4, 3, kBarEpi, false>(smem, sbase, OFF_V, tmem + lane_base, row, eset, (ctid & 127) == 0, true,
                                                      empty, inv, &o_map, rows0, u.slab, store);
                 else
-                    store_rows<true, 4, 3, kBarEpi>(smem, sbase, OFF_V, tmem + lane_base, row, eset, (ctid & 127) == 0, true,
+                    store_rows<true, 4, 3, kBarEpi, false>(smem, sbase, OFF_V, tmem + lane_base, row, eset, (ctid & 127) == 0, true,
                                                     empty, inv, &o_map, rows0, u.slab, store);
                 // O, the statistics and the tiles have been read: the next unit's may come
                 tc_fence_before();
@@ -748,6 +749,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 next();
             }
+            if ((ctid & 127) == 0) bulk_wait_group<0>();  // the stores are complete before the CTA exits
         }
     }
 
@@ -903,7 +905,7 @@ cudaError_t launch_decode_tree(const TreeArgs& in, const uint8_t* cache, uint16_
     {
         const uint64_t dims[3] = {(uint64_t)kD, (uint64_t)a.flat_rows, (uint64_t)a.B};
         const uint64_t strides[2] = {(uint64_t)kD * 2, (uint64_t)a.flat_rows * kD * 2};
-        const uint32_t box[3] = {64, 128, 1};
+        const uint32_t box[3] = {64, 64, 1};
         e = encode_tmap(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, dims, strides, box, true);
         if (e != cudaSuccess) return e;
     }
