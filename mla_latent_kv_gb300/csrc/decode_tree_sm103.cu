@@ -50,7 +50,7 @@ using dec::store_rows;
 using dec::warp_wait;
 
 // scores: warp 0 TMA, 1 MMA, 2-17 softmax, 18 P copies
-// output: warp 0 TMA, 1 MMA, 2-5 helpers, 6-9 CTA 3's relay, 10-17 drafted pages' V, 2-17 epilogue
+// output: warp 0 TMA, 1 MMA, 2-5 helpers, 6-9 CTA 3's relay, 10-17 drafted pages' V, 2-17 epilogue, 18 L2 prefetch
 constexpr int kThreads = 608;
 constexpr int kSoftThreads = 512;
 constexpr int kTileRows = 256;
@@ -69,6 +69,7 @@ constexpr int kPMsgBytes = (kPBytes + 512 + 4 + 15) / 16 * 16;  // P + alpha[128
 constexpr int kPBufStride = 17 * 1024;
 constexpr int kAuxWarp0 = 10, kAuxWarps = 8;
 constexpr int kRelayWarps = 4;               // of CTA 3, from warp 6 on
+constexpr int kAhead = 10, kInRings = 6;     // pages between the helpers' progress and the one prefetched; in the rings
 constexpr int kCtrlBytes = 6144;
 // scores CTA
 constexpr int OFF_QROPE = kCtrlBytes;
@@ -126,6 +127,7 @@ enum : int {
 static_assert(8 * B_COUNT <= 512, "barrier slots");
 constexpr int OFF_TMEM = 512;
 constexpr int OFF_ABORT = 516;
+constexpr int OFF_PROG = 520;     // CTA 2: pages of all units that its helper warps have seen (paces the prefetch)
 constexpr int OFF_MX = 1024;      // scores: f32 [4][128] exchange between the column quarters
 constexpr int OFF_STAT_M = 2048;  // output: f32 [128] final running max (log2 units)
 constexpr int OFF_STAT_L = 2560;  // output: f32 [128] row sum
@@ -182,7 +184,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     const bool kept = p.B <= kMaxSorted, sorted = kept && p.units > clusters;
     int* lens = reinterpret_cast<int*>(smem + OFF_LENS);
     if (kept && tid < p.B) lens[tid] = length(tid);
-    if (tid == kThreads - 1) *abort = 0;
+    if (tid == kThreads - 1) {
+        *abort = 0;
+        *reinterpret_cast<volatile uint32_t*>(smem + OFF_PROG) = 0;
+    }
     if (tid < B_COUNT) {
         const int i = tid;
         uint32_t cnt = 1;
@@ -689,6 +694,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     // through the relay below.
                     fence_proxy_async_cta();
                     dec::warp_arrive(bar((side == 0 ? B_READY : B_PEER) + pb), lane);
+                    if (ctid == 0) *reinterpret_cast<volatile uint32_t*>(smem + OFF_PROG) = v + 1;
                 }
                 // CTA 3's pages are announced to CTA 2 by an arrival that releases at cluster scope, since it
                 // publishes the helpers' writes. That takes most of a microsecond, so warps that have nothing else
@@ -750,6 +756,24 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 next();
             }
             if ((ctid & 127) == 0) bulk_wait_group<0>();  // the stores are complete before the CTA exits
+        } else if (!kScaled && side == 0 && lane == 0 && p.tiles == 1) {
+            // Warp 18: the pages that the rings have no room for yet are brought into L2, the next unit's first ones
+            // too (64 requests of up to 8192 tokens, 112 pairs: 146 -> 139 us; with several tiles a request the others
+            // mostly find them there, and line by line it cost 5 to 8%). Only a hint: it gives up quietly.
+            const volatile uint32_t* prog = reinterpret_cast<const volatile uint32_t*>(smem + OFF_PROG);
+            bool go = true;
+            for (int k = 0; go && unit_of(k, u); next(), ++k)
+                for (int i = n == 0 ? kInRings : 0; i < u.npages && go; ++i) {
+                    for (int spins = 0; (int32_t)(*prog + kAhead - (kPPG * g0 + (uint32_t)i)) < 0; ++spins) {
+                        if (*abort || spins > (1 << 16)) {
+                            go = false;
+                            break;
+                        }
+                        __nanosleep(128);
+                    }
+                    const int y = page_row(u, i);
+                    if (go && y < p.key_rows) bulk_prefetch_l2(p.keys + (size_t)y * kBf16RowBytes, kPage * kBf16RowBytes);
+                }
         }
     }
 
@@ -885,6 +909,7 @@ cudaError_t launch_decode_tree(const TreeArgs& in, const uint8_t* cache, uint16_
         }
     }
     a.key_rows = (int)rows;
+    a.keys = fp8 ? (const uint8_t*)widened : cache;
     CUtensorMap k_map, v_map, q_map, o_map;
     memset(&k_map, 0, sizeof k_map);
     memset(&v_map, 0, sizeof v_map);

@@ -217,7 +217,8 @@ mla_status mla_rope_cache_write(const void* kv_c, int64_t kv_c_stride_t, const v
 
 size_t mla_decode_tree_workspace_bytes(mla_kv_dtype kv_dtype, int B, int Sq, int H, int max_seq_len) {
     TreePlan w{};
-    if (!known_kv(kv_dtype) || !tree_shape(B, Sq, H) || B < 1 || max_seq_len < 0) return 0;
+    if (!known_kv(kv_dtype) || !tree_shape(B, Sq, H) || B < 1 || max_seq_len < 0 || max_seq_len > INT32_MAX - mla::kPage)
+        return 0;
     return plan_tree(kv_dtype, B, Sq, H, max_seq_len, &w) ? w.total : 0;
 }
 
@@ -238,6 +239,8 @@ mla_status mla_decode_tree(const void* q, const void* kv_cache, mla_kv_dtype kv_
                                                 o_dtype, lse, dev_status, stream, x);
     if (checked != MLA_OK || B == 0) return checked;
     if (!tree_mask) return set_error(MLA_ERR_INVALID_ARG, "%s: null pointer", who);
+    if (max_seq_len > INT32_MAX - mla::kPage)
+        return set_error(MLA_ERR_UNSUPPORTED, "%s: max_seq_len=%d too large", who, max_seq_len);
     if (!tree_shape(B, Sq, H)) return set_error(MLA_ERR_UNSUPPORTED, "%s: %lld query rows too many", who, (long long)B * Sq);
     TreePlan w{};
     if (!plan_tree(kv_dtype, B, Sq, H, max_seq_len, &w))

@@ -376,7 +376,8 @@ struct TreeArgs {
     float scale;
     int splits, pages_per_split;
     int64_t units;              // splits * B * tiles
-    int key_rows;               // rows behind the keys' tensor map
+    const uint8_t* keys;        // the bf16 rows behind the keys' tensor map, and their number
+    int key_rows;
     int wide_pages;             // FP8: pages of each request's widened rows, [B, wide_pages, 64]
     const float* k_scales;      // and their scales
     const float* v_scales;

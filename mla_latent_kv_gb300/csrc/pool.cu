@@ -326,6 +326,7 @@ cudaError_t launch_fork_pages(const ForkArgs& a, bool fp8, cudaStream_t s) {
     cudaError_t e = launch_pdl(fork_plan_kernel, dim3((unsigned)(1 + (refs < 64 ? refs : 64))), dim3(kPlanThreads), 0, s, a);
     if (e != cudaSuccess) return e;
     const int64_t blocks = (int64_t)a.B2 + a.B + (int64_t)a.B2 * a.layers;
+    if (blocks == 0) return cudaSuccess;  // the counts alone were copied
     return launch_pdl(fp8 ? fork_apply_kernel<kFp8RowBytes> : fork_apply_kernel<kBf16RowBytes>, dim3((unsigned)blocks),
                       dim3(kForkThreads), 0, s, a);
 }

@@ -219,6 +219,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* gsrc, uint32
                  : "memory");
 }
 
+// Hint: bring `bytes` (a multiple of 16) from the 16-byte aligned address into L2.
+__device__ __forceinline__ void bulk_prefetch_l2(const void* gsrc, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(gsrc)), "r"(bytes) : "memory");
+}
+
 // TMA store of one box from this CTA's shared memory to global memory (elements outside the
 // tensor are not written), tracked by the issuing thread's bulk async-group.
 __device__ __forceinline__ void tma_store_3d(const void* map, uint32_t src, int32_t x, int32_t y, int32_t z) {

@@ -61,6 +61,7 @@ def test_decode_tree_refusals(lib):  # noqa: F811
     assert call(B=-2) == mla.ERR_INVALID_ARG and call(Sq=0) == mla.ERR_INVALID_ARG
     assert call(Sq=65) == mla.ERR_UNSUPPORTED
     assert call(max_len=257) == mla.ERR_INVALID_ARG and call(max_len=-1) == mla.ERR_INVALID_ARG
+    assert call(max_len=2 ** 31 - 1, max_blocks=2 ** 25) == mla.ERR_UNSUPPORTED
     for scale in (0.0, -1.0, float("nan"), float("inf")):
         assert call(scale=scale) == mla.ERR_INVALID_ARG
     for name in ("q", "cache", "table", "seq", "mask", "o"):
@@ -103,6 +104,8 @@ def test_fork_pages_refusals(lib):  # noqa: F811
     assert call(ws=None) == mla.ERR_WORKSPACE_TOO_SMALL and call(ws_bytes=64) == mla.ERR_WORKSPACE_TOO_SMALL
     assert call(ws=ctypes.c_void_p(0x1010)) == mla.ERR_UNSUPPORTED
     assert call(B=0, B2=0, nb=0) == mla.OK
+    assert call(B2=0, new_table=None, new_counts=None, new_lens=None, parents=None, room=None, ws=None) == \
+        mla.ERR_WORKSPACE_TOO_SMALL  # nothing else is missing then
     assert lib.mla_fork_pages_workspace_bytes(-1, 1, 1) == 0
     assert lib.mla_fork_pages_workspace_bytes(2, 3, 8) >= 256 + 3 * 32 + 2 * 4 + 8 * 4
 

@@ -394,6 +394,33 @@ def test_decode_tree_replayed_with_other_inputs(H, kv):
         check_attention(o, lse, attend_tree(c))
 
 
+@pytest.mark.parametrize("kv", [BF, F8])
+def test_decode_tree_of_many_requests(kv):
+    """More requests than are sorted by length, several units a cluster, pages of every parity."""
+    rng = np.random.default_rng(30)
+    lens = rng.integers(0, 330, 530)
+    c = tree_case(lens, 3, 44, kv, 31)
+    check_attention(*_tree(c), attend_tree(c))
+
+
+@pytest.mark.parametrize("kv", [BF, F8])
+@pytest.mark.parametrize("H", [16, 60])
+def test_decode_tree_calls_in_a_row(H, kv):
+    """Calls that take turns on one workspace and one output without a wait between them."""
+    import torch
+
+    import mla_latent_kv_gb300 as mla
+    cs = [tree_case([2500, 700, 66], 5, H, kv, 32), tree_case([64, 3000], 5, H, kv, 33)]
+    need = max(mla.decode_tree_workspace_bytes(c["B"], 5, H, c["max_len"], kv) for c in cs)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    outs = [(torch.empty((c["B"], 5, H, L), device="cuda"), torch.empty((c["B"], 5, H), device="cuda")) for c in cs]
+    for _ in range(4):
+        for c, (o, lse) in zip(cs, outs):
+            _tree(c, workspace=ws, o_latent=o, lse=lse)
+    for c, (o, lse) in zip(cs, outs):
+        check_attention(o, lse, attend_tree(c))
+
+
 def test_decode_tree_on_two_streams():
     """Calls of two streams at once, each with its own workspace, also one made by the call."""
     import torch
@@ -470,7 +497,7 @@ def test_accept_tokens_bad_branches():
 def _fork(p, parents, room, kv, status=None, layers=None, **kw):
     import mla_latent_kv_gb300 as mla
     host = p["cache"]
-    cache = dev(host.reshape(host.shape[0], host.shape[1], -1))
+    cache = dev(host.reshape(host.shape[0], host.shape[1], host.shape[2] * host.shape[3]))
     if layers == 0:
         cache = cache[:0]
     out = mla.fork_pages(cache, dev(p["table"]), dev(p["counts"]), dev(p["lens"]), dev(p["refs"]),
@@ -540,6 +567,72 @@ def test_fork_pages_bad_entries_are_not_counted():
     assert st.item() == mla.DEV_BAD_BLOCK_ID
     assert table[0, :4].tolist() == [3, 30, -5, 7] and table[1, :4].tolist() == [3, 30, -5, 0]
     assert refs[3] == 2 and refs[7] == 1 and refs[0] == 1 and refs[9] == 0 and refs.sum() == 4
+
+
+def test_fork_pages_from_and_to_nothing():
+    """A pool without rows, one that stays so, and one without pages."""
+    import mla_latent_kv_gb300 as mla
+    none = dict(cache=np.zeros((1, 9, PAGE, 1152), np.uint8), table=np.zeros((0, 5), np.int32), counts=np.zeros(0, np.int32),
+                lens=np.zeros(0, np.int32), refs=np.array([0, 3, 0, 0, 1, 0, 0, 0, 0], np.int32))
+    _, (table, counts, lens, refs) = _fork(none, [], [], BF)
+    assert table.shape == (0, 5) and np.array_equal(refs, none["refs"])
+    _, (table, counts, lens, refs) = _fork(none, [-1, -1], [100, -7], BF)
+    assert table.tolist() == [[0, 2, -1, -1, -1], [-1] * 5] and counts.tolist() == [2, 0] and lens.tolist() == [0, 0]
+    assert refs.tolist() == [1, 3, 1, 0, 1, 0, 0, 0, 0]
+    empty = dict(none, cache=np.zeros((2, 0, PAGE, 1152), np.uint8), refs=np.zeros(0, np.int32))
+    st = _status()
+    _, (table, counts, lens, refs) = _fork(empty, [-1], [1], BF, st)
+    assert st.item() == mla.DEV_NO_PAGES and counts.tolist() == [0] and refs.size == 0
+
+
+@pytest.mark.parametrize("kv", [BF, F8])
+def test_fork_pages_there_and_back(kv):
+    """Two buffers of the state take turns over many random steps, captured or not, on a stream of their own."""
+    import torch
+
+    import mla_latent_kv_gb300 as mla
+    rng = np.random.default_rng(4)
+    B, width, nb = 6, 6, 90
+    p = random_pool(B, width, nb, 1, kv, 9, 200)
+    cache = dev(p["cache"][0].reshape(nb, -1))
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    a = tuple(dev(p[k]) for k in ("table", "counts", "lens", "refs"))
+    b = (i32(B, width), i32(B), i32(B), i32(nb))
+    parents, room, st = i32(B), i32(B), _status()
+    ws = torch.empty(mla.fork_pages_workspace_bytes(B, B, nb), dtype=torch.uint8, device="cuda")
+
+    def step():
+        mla.fork_pages(cache, *a, parents, room, kv_dtype=kv, out=b, workspace=ws, dev_status=st)
+        for x, y in zip(a, b):
+            x.copy_(y)
+    host = dict(p)
+    side, graph = torch.cuda.Stream(), None
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for k in range(8):
+            par = rng.integers(-1, B, B)
+            own = np.where(par >= 0, host["lens"][par], 0)
+            need = np.minimum(own + rng.integers(0, 100, B), width * PAGE)
+            parents.copy_(dev(par.astype(np.int32)))
+            room.copy_(dev(need.astype(np.int32)))
+            ws.fill_(255)
+            if k == 4:
+                side.synchronize()
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph, stream=side):
+                    step()
+            graph.replay() if graph else step()
+            side.synchronize()
+            want = fork_rule(host["cache"], host["table"], host["counts"], host["lens"], host["refs"], par, need)
+            assert want is not None and st.item() == 0
+            host = dict(zip(("cache", "table", "counts", "lens", "refs"), want))
+            for x, name in zip(a, ("table", "counts", "lens", "refs")):
+                assert np.array_equal(x.cpu().numpy(), host[name]), (k, name)
+            assert np.array_equal(cache.cpu().numpy().reshape(host["cache"][0].shape), host["cache"][0])
+            # requests grow to the pages that they hold, as steps would make them
+            grown = np.minimum(host["lens"] + rng.integers(0, 80, B), host["counts"] * PAGE).astype(np.int32)
+            host["lens"] = grown
+            a[2].copy_(dev(grown))
 
 
 def test_fork_pages_tables_alone_and_no_rows():
