@@ -786,10 +786,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------------------------------
 // FP8 pages -> bf16 rows (exact) and scales, every request's, once per call. One block per page; a thread
-// takes nine chunks of 8 codes at a time, all of their loads first. A request's last page is widened whole:
-// what is behind its end is not seen.
+// takes nine chunks of 8 codes, all of their loads first (36 requests of 4 pages: 28 -> 24 us a call against two
+// rounds of 256 threads). A request's last page is widened whole: what is behind its end is not seen.
 // ------------------------------------------------------------------------------------------
-constexpr int kWidenThreads = 256, kChunks = kPage * kD / 8, kBatch = 9;
+constexpr int kWidenThreads = 512, kChunks = kPage * kD / 8, kBatch = 9;
 static_assert(kChunks % (kWidenThreads * kBatch) == 0, "a page's chunks");
 __global__ void __launch_bounds__(kWidenThreads) tree_widen_kernel(TreeArgs p, const uint8_t* cache, uint16_t* x,
                                                                    float* k_scales, float* v_scales) {
