@@ -4,13 +4,17 @@
 //     u' = mscale (u cos(m w_i) - v sin(m w_i)),   v' = mscale (v cos(m w_i) + u sin(m w_i))
 // The angle is only needed modulo a turn, so the host gives each pair's step w_i / 2 pi as a fraction of
 // 2^64 and the product m * step, which wraps at 2^64, is the turn's fraction: exact for any position but
-// for the step's own 2^-65 (2^-34 of a turn at 2^31 tokens). Its leading bits go to sincospi in fp32.
+// for the step's own rounding (2^-33 of a turn at 2^31 tokens). Its leading bits go to sincospi in fp32.
 // (In fp32, m * w_i alone is off by 0.004 rad at 131072 tokens.)
 //
-// One warp per 32 heads of a token (8 or 16 where there are few): each lane computes one pair's cosine and sine, four lanes share a head's
-// row (pairs 8 c .. 8 c + 7 are lane c's, in both layouts) and get theirs by shuffles; up to four rows' loads are
-// in flight before the first is used. A thread writes what it read and no more, so that the result may
-// replace its input. Bound: memory, 256 bytes a head.
+// Queries: one warp per 32 heads of a token (8 or 16 where there are few). Each lane computes one pair's cosine
+// and sine, four lanes share a head's row (pairs 8 c .. 8 c + 7 are lane c's, in both layouts) and get theirs by
+// shuffles; up to four rows' loads are in flight before the first is used. For fewer than eight heads a warp
+// takes eight head rows of as many tokens, and each lane computes the eight pairs that it turns. A thread writes
+// what it read and no more, so that the result may replace its input.
+// Cache rows: one warp per four tokens, whose rope parts are turned together, eight lanes each.
+//
+// Bound: memory, 256 bytes a head: 8192 tokens of 128 heads 44 us, 6.1 TB/s.
 #include "internal.h"
 #include "sm103_ptx.cuh"
 
@@ -18,12 +22,13 @@ namespace mla {
 namespace {
 
 constexpr int kWarps = 8;
-// Head rows of a lane: a warp has eight times as many heads of a token.
-constexpr int rows_per_lane(int heads) { return heads > 16 ? 4 : heads > 8 ? 2 : 1; }
+constexpr int kTokens = 4;  // cache rows of a warp
+// Head rows of a lane: a warp has eight times as many heads of a token (0: fewer than eight heads, see above).
+constexpr int rows_per_lane(int heads) { return heads > 16 ? 4 : heads > 8 ? 2 : heads == 8 ? 1 : 0; }
 
-// (cos, sin) of this lane's pair at position m, times mscale.
-__device__ __forceinline__ float2 turn_of(const RopeArgs& p, int m, int lane) {
-    const uint64_t turns = (uint64_t)(int64_t)m * p.step[lane];
+// (cos, sin) of a pair at position m, times mscale.
+__device__ __forceinline__ float2 turn_of(const RopeArgs& p, int m, int pair) {
+    const uint64_t turns = (uint64_t)(int64_t)m * p.step[pair];
     float s, c;
     sincospif((float)(int32_t)(uint32_t)(turns >> 32) * 4.6566128730773926e-10f, &s, &c);  // 2^-31: half turns
     return make_float2(c * p.mscale, s * p.mscale);
@@ -88,6 +93,39 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& p, int t, int part, i
     }
 }
 
+// The same for fewer than eight heads: rows [8 w, 8 w + 8) of all tokens' rows.
+template <>
+__device__ __forceinline__ void rope_heads<0>(const RopeArgs& p, int w, int, int lane) {
+    const int64_t row = (int64_t)w * 8 + (lane >> 2);
+    const int t = (int)(row / p.N), n = (int)(row % p.N), c = lane & 3;
+    if (row >= (int64_t)p.T * p.N) return;
+    const int c0 = p.adjacent ? 2 * c : c, c1 = p.adjacent ? 2 * c + 1 : c + 4;
+    const uint16_t* src = p.x + t * p.x_t + n * p.x_n;
+    const uint4 w0 = *reinterpret_cast<const uint4*>(src + 8 * c0), w1 = *reinterpret_cast<const uint4*>(src + 8 * c1);
+    const int m = p.positions[t];
+    float x[16];
+    unpack8(w0, x);
+    unpack8(w1, x + 8);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float2 tr = turn_of(p, m, 8 * c + k);
+        if (p.adjacent)
+            rotate(x[2 * k], x[2 * k + 1], tr);
+        else
+            rotate(x[k], x[8 + k], tr);
+    }
+    uint16_t* dst = p.out + t * p.out_t + n * p.out_n;
+    *reinterpret_cast<uint4*>(dst + 8 * c0) = pack8(x);
+    *reinterpret_cast<uint4*>(dst + 8 * c1) = pack8(x + 8);
+}
+
+// Warps that the heads take.
+template <int kRows>
+__host__ __device__ __forceinline__ int64_t head_warps(const RopeArgs& p) {
+    if (!p.x) return 0;
+    return kRows == 0 ? ((int64_t)p.T * p.N + 7) / 8 : (int64_t)p.T * ((p.N + 8 * kRows - 1) / (kRows == 0 ? 1 : 8 * kRows));
+}
+
 // Two binary32 values -> two OCP E4M3 bytes (lo at the lower address), nearest even, saturating.
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
     uint16_t r;
@@ -95,69 +133,102 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
     return r;
 }
 
-// The cache row of token t, by one warp: its 72 chunks of 8 values, chunks 64-71 (lanes 0-7) turned. A value
-// is rounded once, to bf16 or, from the fp32 of the rotation, to e4m3.
+// The cache rows of tokens [kTokens w, ...), by one warp. Each row is 72 chunks of 8 values: 64 of kv_c, two a
+// lane, and 8 of the turned k_pe, which lane 8 u + c holds for token u. A value is rounded once, to bf16 or, from
+// the fp32 of the rotation, to e4m3.
 template <bool kFp8>
-__device__ __forceinline__ void rope_row(const RopeArgs& p, const RopeRows& r, int t, int lane) {
-    const int64_t slot = r.slots[t];
-    if (slot < 0) return;  // padding
-    if (slot >= r.num_blocks * kPage) {
-        if (lane == 0 && r.dev_status) atomicOr(r.dev_status, MLA_DEV_BAD_SLOT);
-        return;
+__device__ __forceinline__ void rope_rows(const RopeArgs& p, const RopeRows& r, int64_t w, int lane) {
+    static_assert(kTokens * 8 == 32, "eight lanes a token");
+    const int64_t t0 = w * kTokens, mine = t0 + (lane >> 3);
+    uint4 pe = make_uint4(0u, 0u, 0u, 0u);
+    int m = 0;
+    int64_t slot = -1;  // of this lane's token; below 0: padding
+    if (mine < p.T) {
+        slot = r.slots[mine];
+        m = p.positions[mine];
+        pe = *reinterpret_cast<const uint4*>(r.k_pe + mine * r.st_pe + 8 * (lane & 7));
     }
-    uint4 w[3];
-    w[2] = make_uint4(0u, 0u, 0u, 0u);
+    uint4 v[2][2];  // kv_c of two tokens at a time
+    auto load = [&](int u, uint4 (&x)[2]) {
+        if (t0 + u >= p.T) return;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) w[i] = *reinterpret_cast<const uint4*>(r.kv_c + t * r.st_c + 8 * (lane + 32 * i));
-    if (lane < 8) w[2] = *reinterpret_cast<const uint4*>(r.k_pe + t * r.st_pe + 8 * lane);
-    const float2 mine = turn_of(p, p.positions[t], lane);
-    float x[8], y[8];
-    unpack8(w[2], x);
+        for (int i = 0; i < 2; ++i)
+            x[i] = *reinterpret_cast<const uint4*>(r.kv_c + (t0 + u) * r.st_c + 8 * (lane + 32 * i));
+    };
+    load(0, v[0]);
+    load(1, v[1]);
+    if (slot >= r.num_blocks * kPage) {
+        if ((lane & 7) == 0 && r.dev_status) atomicOr(r.dev_status, MLA_DEV_BAD_SLOT);
+        slot = -1;
+    }
+    float x[8];
+    unpack8(pe, x);
+    {
+        // chunk c has pairs 4 c .. 4 c + 3 or, in halves, one side of pairs 8 (c & 3) ..: then this lane and the one
+        // four further compute four pairs each and exchange them, with their values
+        const int c = lane & 7, pair0 = p.adjacent ? 4 * c : 8 * (c & 3) + 4 * (c >> 2);
+        float2 tr[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] = __shfl_xor_sync(0xffffffffu, x[k], 4);  // the pairs' other half
+        for (int k = 0; k < 4; ++k) tr[k] = turn_of(p, m, pair0 + k);
+        if (p.adjacent) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const int pair = p.adjacent ? 4 * (lane & 7) + (k >> 1) : 8 * (lane & 3) + k;
-        const float2 tr = make_float2(__shfl_sync(0xffffffffu, mine.x, pair), __shfl_sync(0xffffffffu, mine.y, pair));
-        if (!p.adjacent) {
-            if (lane & 4)
-                rotate(y[k], x[k], tr);
-            else
-                rotate(x[k], y[k], tr);
-        } else if (k & 1) {
-            rotate(x[k - 1], x[k], tr);
+            for (int k = 0; k < 4; ++k) rotate(x[2 * k], x[2 * k + 1], tr[k]);
+        } else {
+            const bool up = c & 4;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float other = __shfl_xor_sync(0xffffffffu, x[k], 4);
+                const float2 got = make_float2(__shfl_xor_sync(0xffffffffu, tr[k & 3].x, 4), __shfl_xor_sync(0xffffffffu, tr[k & 3].y, 4));
+                const float2 q = (k >= 4) == up ? tr[k & 3] : got;
+                x[k] = up ? x[k] * q.x + other * q.y : x[k] * q.x - other * q.y;
+            }
         }
     }
-    if constexpr (!kFp8) {
-        uint4* dst = reinterpret_cast<uint4*>(r.cache + slot * kBf16RowBytes);
-        dst[lane] = w[0];
-        dst[lane + 32] = w[1];
-        if (lane < 8) dst[lane + 64] = pack8(x);
-    } else {
-        float z[16];
-        unpack8(w[0], z);
-        unpack8(w[1], z + 8);
-        float amax = 0.f;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(z[k]));
+    for (int u = 0; u < kTokens; ++u) {
+        const int64_t at = __shfl_sync(0xffffffffu, slot, 8 * u);
+        const bool rope = (lane >> 3) == u;
+        const int chunk = 64 + (lane & 7);
+        uint4 kv[2] = {v[u & 1][0], v[u & 1][1]};
+        if (u + 2 < kTokens) load(u + 2, v[u & 1]);
+        if (at < 0) continue;
+        if constexpr (!kFp8) {
+            uint4* dst = reinterpret_cast<uint4*>(r.cache + at * kBf16RowBytes);
+            dst[lane] = kv[0];
+            dst[lane + 32] = kv[1];
+            if (rope) dst[chunk] = pack8(x);
+        } else {
+            float z[16], amax = 0.f;
+            unpack8(kv[0], z);
+            unpack8(kv[1], z + 8);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) amax = fmaxf(amax, lane < 8 ? fabsf(x[k]) : 0.f);
+            for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(z[k]));
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-        const float scale = r.kv_scale > 0.f ? r.kv_scale : (amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f);
-        const float inv = __frcp_rn(scale);
-        uint8_t* dst = r.cache + slot * kFp8RowBytes;  // 584-byte rows are 8-byte aligned
-        auto store = [&](int chunk, const float* v) {
-            uint32_t b[4];
+            for (int k = 0; k < 8; ++k) amax = fmaxf(amax, rope ? fabsf(x[k]) : 0.f);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] = f32x2_to_e4m3x2(__fmul_rn(v[2 * j], inv), __fmul_rn(v[2 * j + 1], inv));
-            reinterpret_cast<uint2*>(dst)[chunk] = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
-        };
-        store(lane, z);
-        store(lane + 32, z + 8);
-        if (lane < 8) store(lane + 64, x);
-        if (lane == 8) *reinterpret_cast<float2*>(dst + kD) = make_float2(scale, scale);
+            for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+            const float scale = r.kv_scale > 0.f ? r.kv_scale : (amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f);
+            const float inv = __frcp_rn(scale);
+            uint8_t* dst = r.cache + at * kFp8RowBytes;  // 584-byte rows are 8-byte aligned
+            auto store = [&](int c, const float* y) {
+                uint32_t b[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) b[j] = f32x2_to_e4m3x2(__fmul_rn(y[2 * j], inv), __fmul_rn(y[2 * j + 1], inv));
+                reinterpret_cast<uint2*>(dst)[c] = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+            };
+            store(lane, z);
+            store(lane + 32, z + 8);
+            if (rope) store(chunk, x);
+            if (lane == 0) *reinterpret_cast<float2*>(dst + kD) = make_float2(scale, scale);
+        }
     }
+}
+
+template <int kRows>
+__device__ __forceinline__ void head_warp(const RopeArgs& p, int64_t w, int lane) {
+    if (w >= head_warps<kRows>(p)) return;
+    const int parts = kRows == 0 ? 1 : (p.N + 8 * kRows - 1) / (kRows == 0 ? 1 : 8 * kRows);
+    rope_heads<kRows>(p, (int)(w / parts), (int)(w % parts), lane);
 }
 
 template <int kRows>
@@ -165,47 +236,55 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeArgs p) {
     // No early signal to the kernels behind: the result may be a part of a cache, which a decode reads
     // before its own wait.
     ptx::griddep_wait();
-    const int parts = (p.N + 8 * kRows - 1) / (8 * kRows);
     const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (w < (int64_t)p.T * parts) rope_heads<kRows>(p, (int)(w / parts), (int)(w % parts), threadIdx.x & 31);
+    head_warp<kRows>(p, w, threadIdx.x & 31);
 }
 
 template <bool kFp8, int kRows>
 __global__ void __launch_bounds__(kWarps * 32) rope_cache_write_kernel(const RopeArgs p, const RopeRows r) {
     ptx::griddep_wait();  // no early signal, as above
-    const int parts = p.x ? (p.N + 8 * kRows - 1) / (8 * kRows) : 0;
-    const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (w < p.T)
-        rope_row<kFp8>(p, r, (int)w, lane);
-    else if (w < (int64_t)p.T * (parts + 1))
-        rope_heads<kRows>(p, (int)((w - p.T) / parts), (int)((w - p.T) % parts), lane);
+    const int64_t rows = ((int64_t)p.T + kTokens - 1) / kTokens, w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (w < rows)
+        rope_rows<kFp8>(p, r, w, threadIdx.x & 31);
+    else
+        head_warp<kRows>(p, w - rows, threadIdx.x & 31);
 }
 
 unsigned blocks_of(int64_t warps) { return (unsigned)((warps + kWarps - 1) / kWarps); }
 
 template <int kRows>
 cudaError_t launch(const RopeArgs& a, cudaStream_t s) {
-    const int64_t parts = (a.N + 8 * kRows - 1) / (8 * kRows);
-    return launch_pdl(rope_kernel<kRows>, dim3(blocks_of(a.T * parts)), dim3(kWarps * 32), 0, s, a);
+    return launch_pdl(rope_kernel<kRows>, dim3(blocks_of(head_warps<kRows>(a))), dim3(kWarps * 32), 0, s, a);
 }
 template <bool kFp8, int kRows>
 cudaError_t launch(const RopeArgs& a, const RopeRows& r, cudaStream_t s) {
-    const int64_t parts = a.x ? (a.N + 8 * kRows - 1) / (8 * kRows) : 0;
-    return launch_pdl(rope_cache_write_kernel<kFp8, kRows>, dim3(blocks_of(a.T * (parts + 1))), dim3(kWarps * 32), 0, s, a, r);
+    const int64_t rows = ((int64_t)a.T + kTokens - 1) / kTokens;
+    return launch_pdl(rope_cache_write_kernel<kFp8, kRows>, dim3(blocks_of(rows + head_warps<kRows>(a))), dim3(kWarps * 32), 0, s,
+                      a, r);
+}
+template <bool kFp8>
+cudaError_t launch_write(const RopeArgs& a, const RopeRows& r, cudaStream_t s) {
+    switch (rows_per_lane(a.N)) {
+        case 4: return launch<kFp8, 4>(a, r, s);
+        case 2: return launch<kFp8, 2>(a, r, s);
+        case 1: return launch<kFp8, 1>(a, r, s);
+        default: return launch<kFp8, 0>(a, r, s);
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
-    const int rows = rows_per_lane(a.N);
-    return rows == 4 ? launch<4>(a, s) : rows == 2 ? launch<2>(a, s) : launch<1>(a, s);
+    switch (rows_per_lane(a.N)) {
+        case 4: return launch<4>(a, s);
+        case 2: return launch<2>(a, s);
+        case 1: return launch<1>(a, s);
+        default: return launch<0>(a, s);
+    }
 }
 
 cudaError_t launch_rope_cache_write(const RopeArgs& a, const RopeRows& r, bool fp8, cudaStream_t s) {
-    const int rows = rows_per_lane(a.N);
-    if (fp8) return rows == 4 ? launch<true, 4>(a, r, s) : rows == 2 ? launch<true, 2>(a, r, s) : launch<true, 1>(a, r, s);
-    return rows == 4 ? launch<false, 4>(a, r, s) : rows == 2 ? launch<false, 2>(a, r, s) : launch<false, 1>(a, r, s);
+    return fp8 ? launch_write<true>(a, r, s) : launch_write<false>(a, r, s);
 }
 
 }  // namespace mla
