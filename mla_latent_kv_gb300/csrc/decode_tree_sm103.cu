@@ -70,7 +70,7 @@ constexpr int kPBufStride = 17 * 1024;
 constexpr int kAuxWarp0 = 10, kAuxWarps = 8;
 constexpr int kRelayWarps = 4;               // of CTA 3, from warp 6 on
 constexpr int kAhead = 10, kInRings = 6;     // pages between the helpers' progress and the one prefetched; in the rings
-constexpr int kCtrlBytes = 6144;
+constexpr int kCtrlBytes = 7168;
 // scores CTA
 constexpr int OFF_QROPE = kCtrlBytes;
 constexpr int OFF_RING = OFF_QROPE + kQPanelBytes;
@@ -131,10 +131,14 @@ constexpr int OFF_PROG = 520;     // CTA 2: pages of all units that its helper w
 constexpr int OFF_MX = 1024;      // scores: f32 [4][128] exchange between the column quarters
 constexpr int OFF_STAT_M = 2048;  // output: f32 [128] final running max (log2 units)
 constexpr int OFF_STAT_L = 2560;  // output: f32 [128] row sum
-constexpr int kMaxSorted = 512;   // requests whose lengths are kept and, for more units than clusters, sorted
-constexpr int OFF_ORDER = 3072;   // u16 [kMaxSorted] requests, longest first
-constexpr int OFF_LENS = 4096;    // s32 [kMaxSorted] tokens of each request
-static_assert(OFF_ORDER + 2 * kMaxSorted <= OFF_LENS && OFF_LENS + 4 * kMaxSorted <= kCtrlBytes, "control block");
+constexpr int kMaxSorted = 240;   // requests whose lengths are kept and, for more units than clusters, sorted
+constexpr int OFF_ORDER = 544;    // u16 [kMaxSorted] requests, longest first
+constexpr int OFF_LENS = 3072;    // s32 [kMaxSorted] tokens of each request
+constexpr int OFF_SCALES = 4096;  // scores, FP8: f32 [3][2][128] k_scales and v_scales of three groups in turn
+constexpr int kScaleBytes = 2 * kPPG * kPage * 4;
+static_assert(OFF_ORDER + 2 * kMaxSorted <= OFF_MX && OFF_LENS + 4 * kMaxSorted <= OFF_SCALES &&
+                  OFF_SCALES + 3 * kScaleBytes <= kCtrlBytes,
+              "control block");
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256;  // scores: Q latent in columns [0, 256), S buffers at 256 and 384
@@ -442,20 +446,37 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     tc_fence_before();
                     dec::warp_arrive(bar(B_QREADY), lane);
                 }
+                // FP8: half of the threads bring one scale each of a group into shared memory, two groups ahead of
+                // its use. (Read from global memory by every thread they cost 0.2 us a group and spilled.)
+                const int ft = tid - 64;
+                float sc = 0.f;
+                auto scale_of = [&](int gi) -> float {
+                    const int page = min(kPPG * gi + (ft >> 6 & 1), u.npages - 1);
+                    const float* src = ft < kPPG * kPage ? p.k_scales : p.v_scales;
+                    return src[((size_t)u.req * p.wide_pages + u.page0 + page) * kPage + (ft & 63)];
+                };
+                auto put_scale = [&](uint32_t g, float x) {
+                    reinterpret_cast<float*>(smem + OFF_SCALES + g % 3 * kScaleBytes)[ft] = x;
+                };
+                if (kScaled) {
+                    if (ft < 2 * kPPG * kPage) {
+                        const float first = scale_of(0);
+                        sc = scale_of(1);
+                        put_scale(g0, first);
+                    }
+                    named_bar(kBarMax, kSoftThreads);
+                }
                 float m_run = -CUDART_INF_F, l_run = 0.f;  // each quarter keeps its own sum
                 for (int gi = 0; gi < u.ngroups; ++gi) {
                     // No early exit from this loop: all 512 threads must pass the same named barriers (which
                     // cannot time out); after an abort the waits return at once.
                     const uint32_t g = g0 + (uint32_t)gi;
                     const int page = kPPG * gi + pg2, buf = (int)(g & 1);
-                    size_t sc = 0;               // the quarter's first token of the page, in float4 units
-                    float4 ks[kScaled ? 8 : 1];  // k_scale of its 32 tokens
-                    if constexpr (kScaled) {     // plain loads: the widening kernel wrote them while this one began
-                        sc = (((size_t)u.req * p.wide_pages + u.page0 + min(page, u.npages - 1)) * kPage + 32 * sub) / 4;
-                        const float4* src = reinterpret_cast<const float4*>(p.k_scales) + sc;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) ks[j] = src[j];
+                    if (kScaled && ft < 2 * kPPG * kPage) {  // visible to all behind this group's barrier
+                        put_scale(g + 1, sc);
+                        sc = scale_of(gi + 2);
                     }
+                    const float4* scales = reinterpret_cast<const float4*>(smem + OFF_SCALES + g % 3 * kScaleBytes) + 8 * quarter;
                     const bool okS = warp_wait<true>(bar(B_SFULL + buf), (g >> 1) & 1, abort, ds);
                     uint32_t s[32];
                     if (okS) {
@@ -472,33 +493,24 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     auto pair = [&](int j) {
                         return make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
                     };
-                    float4 vs[kScaled ? 8 : 1];  // v_scale of this quarter's 32 tokens, on their way early
                     if constexpr (kScaled) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float2 x = mul2(pair(j), j & 1 ? make_float2(ks[j >> 1].z, ks[j >> 1].w)
-                                                                 : make_float2(ks[j >> 1].x, ks[j >> 1].y));
-                            s[2 * j] = __float_as_uint(x.x);
-                            s[2 * j + 1] = __float_as_uint(x.y);
+                        for (int j = 0; j < 16; j += 2) {
+                            const float4 k = scales[j >> 1];
+                            const float2 a = mul2(pair(j), make_float2(k.x, k.y)), b = mul2(pair(j + 1), make_float2(k.z, k.w));
+                            s[2 * j] = __float_as_uint(a.x);
+                            s[2 * j + 1] = __float_as_uint(a.y);
+                            s[2 * j + 2] = __float_as_uint(b.x);
+                            s[2 * j + 3] = __float_as_uint(b.y);
                         }
-                        const float4* src = reinterpret_cast<const float4*>(p.v_scales) + sc;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) vs[j] = src[j];
                     }
+                    // bit c: the row sees token 32 sub + c of the page; none of the page behind the last
+                    uint32_t seen = 0xffffffffu;
                     if (page >= u.drafted) {
-                        // bit c: the row sees token 32 sub + c of the page; none of the page behind the last
-                        const uint32_t seen = page < u.npages
-                                                  ? seen_tokens(mask, (u.page0 + page) * kPage + 32 * sub - u.drafts0)
-                                                  : 0u;
+                        seen = page < u.npages ? seen_tokens(mask, (u.page0 + page) * kPage + 32 * sub - u.drafts0) : 0u;
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (!(seen >> j & 1u)) {
-                                s[j] = __float_as_uint(-CUDART_INF_F);
-                                if constexpr (kScaled) {  // not seen, whatever its scale is
-                                    float4& v = vs[j >> 2];
-                                    (j & 3) == 0 ? v.x = 0.f : (j & 3) == 1 ? v.y = 0.f : (j & 3) == 2 ? v.z = 0.f : v.w = 0.f;
-                                }
-                            }
+                            if (!(seen >> j & 1u)) s[j] = __float_as_uint(-CUDART_INF_F);
                     }
                     float lm4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
@@ -528,9 +540,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                             a = make_float2(fast_exp2(a.x), fast_exp2(a.y));
                             l2[j & 1] = add2(l2[j & 1], a);
                             if constexpr (kScaled)
-                                a = mul2(a, j & 1 ? make_float2(vs[j >> 1].z, vs[j >> 1].w)
-                                                  : make_float2(vs[j >> 1].x, vs[j >> 1].y));
+                                a = mul2(a, reinterpret_cast<const float2*>(scales + kPPG * kPage / 4)[j]);
                             pk[j] = pack_bf16x2(a.x, a.y);
+                        }
+                        if (kScaled && page >= u.drafted) {  // a hidden token has no weight, whatever its scale is
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                pk[j] &= (seen >> (2 * j) & 1u ? 0xffffu : 0u) | (seen >> (2 * j + 1) & 1u ? 0xffff0000u : 0u);
                         }
                         l2[0] = add2(l2[0], l2[1]);
                         l_run += l2[0].x + l2[0].y;
