@@ -181,13 +181,17 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     volatile int* abort = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
     int32_t* ds = p.dev_status;
     auto bar = [&](int i) -> uint32_t { return sbase + 8u * (uint32_t)i; };
-    auto length = [&](int b) -> int { return min(max(p.seq_lens[b], 0), p.max_seq_len); };
+    auto length = [&](int b, bool report = false) -> int {
+        const int n = p.seq_lens[b];
+        if (report && ds && (n < 0 || n > p.max_seq_len)) atomicOr(ds, MLA_DEV_SEQ_TOO_LONG);
+        return min(max(n, 0), p.max_seq_len);
+    };
 
     // Lengths, and the requests in their order (ties by number), every thread placing one.
     const int clusters = (int)(gridDim.x >> 2), cluster = (int)(blockIdx.x >> 2);
-    const bool kept = p.B <= kMaxSorted, sorted = kept && p.units > clusters;
+    const bool kept = p.B <= kMaxSorted, sorted = kept && p.units > (int64_t)clusters;
     int* lens = reinterpret_cast<int*>(smem + OFF_LENS);
-    if (kept && tid < p.B) lens[tid] = length(tid);
+    if (kept && tid < p.B) lens[tid] = length(tid, blockIdx.x == 0);
     if (tid == kThreads - 1) {
         *abort = 0;
         *reinterpret_cast<volatile uint32_t*>(smem + OFF_PROG) = 0;
@@ -229,10 +233,11 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     // request's tiles run side by side and read its pages from L2, and ranges behind short requests' ends
     // come last.
     auto unit_of = [&](int k, Unit& u) -> bool {
-        const int64_t i = (int64_t)k * clusters + (k & 1 ? clusters - 1 - cluster : cluster);
-        if (i >= p.units) return false;
-        const int split = (int)(i / ((int64_t)p.B * p.tiles)), place = (int)(i / p.tiles % p.B);
-        u.tile = (int)(i % p.tiles);
+        const uint32_t i = (uint32_t)k * clusters + (uint32_t)(k & 1 ? clusters - 1 - cluster : cluster);
+        if (i >= (uint32_t)p.units) return false;
+        const uint32_t pairs = i / (uint32_t)p.tiles;  // of split and request
+        const int split = (int)(pairs / (uint32_t)p.B), place = (int)(pairs - (uint32_t)split * p.B);
+        u.tile = (int)(i - pairs * (uint32_t)p.tiles);
         u.req = sorted ? (int)reinterpret_cast<const uint16_t*>(smem + OFF_ORDER)[place] : place;
         u.slab = split * p.B + u.req;
         const int seq = kept ? lens[u.req] : length(u.req), pages = (seq + kPage - 1) / kPage;
@@ -281,8 +286,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     return true;
                 };
                 for (int k = 0; ok && unit_of(k, u); ++k) {
-                    if (rank == 0 && ds && (p.seq_lens[u.req] < 0 || p.seq_lens[u.req] > p.max_seq_len))
-                        atomicOr(ds, MLA_DEV_SEQ_TOO_LONG);
+                    if (!kept) length(u.req, rank == 0);
                     if (u.npages == 0) continue;
                     int y = page_row(u, side);  // looked up ahead of the waits
                     if (!(ok = drained())) break;
@@ -318,8 +322,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     if (u.npages == 0) continue;
                     if (!wait_bar(bar(B_QREADY), n & 1, abort, ds)) break;
                     tc_fence_after();
-                    tc_fence_before();
-                    bar_arrive_remote(bar(B_QPEER), 0);
+                    tc_fence_before();  // tensor memory alone is published: no release is needed
+                    bar_arrive_remote_relaxed(bar(B_QPEER), 0);
                     next();
                 }
             }
