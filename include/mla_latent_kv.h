@@ -506,7 +506,8 @@ mla_status mla_rope_cache_write(const void* kv_c, int64_t kv_c_stride_t, const v
  *     n = seq_lens[b] - Sq,   row t sees token j < n, and token n + i iff (tree_mask[b, t] >> i) & 1.
  * A mask of the low t + 1 bits is mla_decode's causal order. A request with seq_lens[b] < Sq has only its last
  * seq_lens[b] drafts; with 0 it is an empty slot. A row that sees nothing gets o_latent = 0, lse = -inf. What a
- * row does not see, NaN and infinities too, does not reach it. The drafts' rows have been written (they may
+ * row does not see, NaN and infinities too, does not reach it; a draft with a score of -inf has no part, whatever its
+ * values. The drafts' rows have been written (they may
  * repeat positions: those are in the keys, by mla_rope).
  *   tree_mask  uint64 [B, Sq] in device memory; bits from Sq on are not read
  *   workspace  >= mla_decode_tree_workspace_bytes for the same arguments, 256-byte aligned, contents undefined

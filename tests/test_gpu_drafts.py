@@ -767,3 +767,69 @@ def test_steps_together(kv, captured):
             else:
                 value = raw[:, :D].contiguous().view(torch.float8_e4m3fn).double() * raw[:, D:D + 4].contiguous().view(torch.float32).double()
                 assert ((value - K).abs() <= (2.0 ** -4 + 2.0 ** -7) * K.abs() + 2.0 ** -10 / 447 * K.abs().amax(1, keepdim=True)).all()
+
+
+# -------------------------------------------------------------------------------------- the binding
+def test_what_the_library_refuses_is_raised_with_its_reason():
+    """Arguments that only the C calls check, and buffers of the wrong size, type or place: nothing is launched."""
+    import torch
+
+    import mla_latent_kv_gb300 as mla
+    freq = mla.rope_frequencies()
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype, device="cuda")  # noqa: E731
+    i32 = torch.int32
+    with pytest.raises(mla.MlaError, match="mla_rope: 16-byte") as e:
+        mla.rope(z(3, 2, 72)[..., 4:68], z(3, dtype=i32), freq)
+    assert e.value.status == mla.ERR_UNSUPPORTED
+    with pytest.raises(mla.MlaError, match="mscale"):
+        mla.rope(z(3, 2, R), z(3, dtype=i32), freq, mscale=float("nan"))
+    with pytest.raises(ValueError, match="inv_freq"):
+        mla.rope(z(3, 2, R), z(3, dtype=i32), freq.cuda())
+    with pytest.raises(ValueError, match="positions"):
+        mla.rope(z(3, 2, R), z(3, dtype=torch.int64), freq)
+    with pytest.raises(ValueError, match="one CUDA device"):
+        mla.rope(z(3, 2, R), torch.zeros(3, dtype=i32), freq)
+    c = tree_case([70, 90], 3, 16, BF, 1)
+    args = (c["q"], c["cache"], c["table"], c["seq_lens"], c["masks"], 90)
+    with pytest.raises(mla.MlaError, match="scale"):
+        mla.decode_tree(*args, 0.0)
+    with pytest.raises(mla.MlaError, match="workspace") as e:
+        mla.fork_pages(z(4, PAGE * 576), z(2, 3, dtype=i32), z(2, dtype=i32), z(2, dtype=i32), z(4, dtype=i32), z(1, dtype=i32),
+                       z(1, dtype=i32), workspace=z(8, dtype=torch.uint8))
+    assert e.value.status == mla.ERR_WORKSPACE_TOO_SMALL
+    with pytest.raises(mla.MlaError, match="kv_dtype"):
+        mla.decode_tree(*args, 0.07, kv_dtype=7)
+    with pytest.raises(ValueError, match="o_latent"):
+        mla.decode_tree(*args, 0.07, o_latent=z(2, 3, 16, 511))
+    with pytest.raises(ValueError, match="lse"):
+        mla.decode_tree(*args, 0.07, lse=z(2, 3, 16))
+    with pytest.raises(ValueError, match="num_blocks"):
+        mla.decode_tree(*args, 0.07, num_blocks=c["num_blocks"] + 1)
+    many = tree_case([70], 2, 3, BF, 1)
+    with pytest.raises(mla.MlaError, match="65 drafts"):
+        mla.decode_tree(z(1, 65, 3, D), many["cache"], many["table"], many["seq_lens"], z(1, 65, dtype=torch.int64), 70, 0.07)
+    lens = z(2, dtype=i32)
+    with pytest.raises(mla.MlaError, match="seq_lens"):
+        mla.accept_tokens(z(4, PAGE * 576), z(2, 3, dtype=i32), lens, z(2, 5, dtype=i32), z(2, dtype=i32), new_lens=lens)
+    state = (z(2, 3, dtype=i32), z(2, dtype=i32), z(2, dtype=i32), z(4, dtype=i32))
+    with pytest.raises(mla.MlaError, match="old one's buffers"):
+        mla.fork_pages(z(4, PAGE * 576), *state, z(2, dtype=i32), z(2, dtype=i32), out=state)
+    with pytest.raises(TypeError, match="tuple"):
+        mla.fork_pages(z(4, PAGE * 576), *state, z(2, dtype=i32), z(2, dtype=i32), out=list(state))
+    with pytest.raises(ValueError, match="pages of"):
+        mla.fork_pages(z(4, PAGE * 500), *state, z(2, dtype=i32), z(2, dtype=i32))
+    torch.cuda.synchronize()
+
+
+def test_given_buffers_are_used_and_returned():
+    import torch
+
+    import mla_latent_kv_gb300 as mla
+    c = tree_case([70, 90], 3, 16, F8, 2)
+    o, lse = torch.zeros(2, 3, 16, L, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, 3, 16, device="cuda")
+    got = _tree(c, o_latent=o, lse=lse)
+    assert got[0] is o and got[1] is lse
+    check_attention(o, lse, attend_tree(c), bf16_out=True)
+    x, pos = torch.ones(2, 3, R, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    assert mla.rope(x, pos, mla.rope_frequencies(), out=x) is x and bool((x == 1).all())
+    assert mla.rope(x, pos, mla.rope_frequencies()).data_ptr() != x.data_ptr()
