@@ -141,7 +141,7 @@ constexpr int OFF_STAT_M = 2048;  // output: f32 [128] final running max (log2 u
 constexpr int OFF_STAT_L = 2560;  // output: f32 [128] row sum
 constexpr int kMaxSorted = 240;   // requests whose lengths are kept and, for more units than clusters, sorted
 constexpr int OFF_ORDER = 544;    // u16 [kMaxSorted] requests, longest first
-constexpr int OFF_LENS = 3072;    // s32 [kMaxSorted] tokens of each request
+constexpr int OFF_LENS = OFF_STAT_L + 512;  // s32 [kMaxSorted] tokens of each request
 constexpr int OFF_SCALES = 4096;  // scores, FP8: f32 [3][2][128] k_scales and v_scales of three groups in turn
 constexpr int kScaleBytes = 2 * kPPG * kPage * 4;
 static_assert(OFF_ORDER + 2 * kMaxSorted <= OFF_MX && OFF_LENS + 4 * kMaxSorted <= OFF_SCALES &&

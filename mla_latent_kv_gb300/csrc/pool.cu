@@ -92,6 +92,7 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptArgs
 // ------------------------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 constexpr int kRefsPerThread = 8;  // of a step of the free-page search
+constexpr int kFewPages = 4;       // pages behind a row's whole ones that one thread looks at
 constexpr int kForkThreads = 256;
 constexpr int kCopyBatch = 5;  // 16-byte loads of a thread in flight
 
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs 
     }
     __shared__ int heir_s[kMaxPoolRows];
     __shared__ int sums[kPlanThreads / 32];
-    __shared__ int bits_s;
+    __shared__ int bits_s, long_s;
     int ref[kRefsPerThread];  // of this thread's pages, a step ahead
     auto load_refs = [&](int64_t at) {
 #pragma unroll
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs 
         }
     };
     load_refs(0);
-    if (tid == 0) bits_s = 0;
+    if (tid == 0) bits_s = long_s = 0;
     for (int b = tid; b < p.B; b += kPlanThreads) heir_s[b] = INT_MAX;
     __syncthreads();
     for (int r = tid; r < p.B2; r += kPlanThreads) {
@@ -185,17 +186,33 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs 
             int take = need - whole;
             bool first = false;  // the page behind the whole ones is kept
             // usually one or two pages: the one held in part, and room
-            for (int j = whole; heir && j < min(held, need); ++j)
+            const int behind = heir ? min(held, need) - whole : 0;
+            if (behind > kFewPages) long_s = 1;
+            for (int j = whole; behind <= kFewPages && j < whole + behind; ++j)
                 if (heir_keeps(p, row, j, whole, held, need)) {
                     --take;
                     first |= j == whole;
                 }
+            if (behind > kFewPages) first = heir_keeps(p, row, whole, whole, held, need);
             const bool copy = n % kPage && !first;
             p.rows[r] = make_int4(parent, need, take, heir ? 1 : 0);
             // where its rows come from; where they go is known later
             p.copies[r] = make_int4(copy ? row[whole] : -1, 0, copy ? n % kPage : 0, 0);
         }
     }
+    __syncthreads();
+    if (bits_s == 0 && long_s)  // rows with much room: a warp each (2000 pages by one thread take milliseconds)
+        for (int r = tid >> 5; r < p.B2; r += kPlanThreads / 32) {
+            const int4 rec = p.rows[r];
+            if (!rec.w) continue;
+            const int held = p.counts[rec.x], whole = p.lens[rec.x] / kPage, end = min(held, rec.y);
+            if (end - whole <= kFewPages) continue;
+            const int32_t* row = p.table + (size_t)rec.x * p.max_blocks;
+            int kept = 0;
+            for (int j = whole + (tid & 31); j < end; j += 32) kept += heir_keeps(p, row, j, whole, held, rec.y);
+            kept = __reduce_add_sync(0xffffffffu, kept);
+            if ((tid & 31) == 0) p.rows[r].z -= kept;
+        }
     __syncthreads();
     int total = 0;
     if (bits_s == 0) {

@@ -569,6 +569,34 @@ def test_fork_pages_bad_entries_are_not_counted():
     assert refs[3] == 2 and refs[7] == 1 and refs[0] == 1 and refs[9] == 0 and refs.sum() == 4
 
 
+@pytest.mark.parametrize("kv", [BF, F8])
+def test_fork_pages_with_much_room(kv):
+    """Rows that hold many pages without tokens yet, some of them another holder's: kept, given back or replaced."""
+    rng = np.random.default_rng(8)
+    B, width, nb = 7, 400, 4000
+    row = {BF: 1152, F8: 584}[kv]
+    p = dict(cache=rng.integers(0, 256, (1, nb, PAGE, row), dtype=np.uint8), table=np.full((B, width), -1, np.int32),
+             counts=np.array([400, 300, 9, 5, 4, 3, 0], np.int32), lens=np.array([100, 64 * 250, 64 * 4, 5, 0, 190, 0], np.int32),
+             refs=np.zeros(nb, np.int32))
+    perm, at = rng.permutation(nb), 0
+    for b in range(B):
+        n = int(p["counts"][b])
+        p["table"][b, :n] = perm[at:at + n]
+        p["refs"][perm[at:at + n]] = 1
+        at += n
+    p["refs"][p["table"][0, [1, 5, 77, 300]]] += 1   # the page held in part and some of the room behind it
+    p["refs"][p["table"][1, 260:270]] += 1
+    for parents, room in (([0, 0, 1, 2, 3, 4, 5], [400 * PAGE, 300, 64 * 299, 64 * 9, 64 * 5, 1, 0]),
+                          ([1, 0, 6, 2], [0, 2000, 64 * 100, 64 * 300]), ([6, 5, 4, 3, 2, 1, 0], [1] * 7)):
+        want = fork_rule(p["cache"], p["table"], p["counts"], p["lens"], p["refs"], parents, room)
+        st = _status()
+        cache, got = _fork(p, parents, room, kv, st)
+        assert st.item() == 0
+        for g, w in zip(got, want[1:]):
+            assert np.array_equal(g, w)
+        assert np.array_equal(cache.cpu().numpy().reshape(p["cache"].shape), want[0])
+
+
 def test_fork_pages_from_and_to_nothing():
     """A pool without rows, one that stays so, and one without pages."""
     import mla_latent_kv_gb300 as mla
