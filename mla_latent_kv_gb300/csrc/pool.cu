@@ -92,6 +92,7 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptArgs
 // ------------------------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 constexpr int kRefsPerThread = 8;  // of a step of the free-page search
+constexpr int kSteps = 4;          // steps whose counts are on their way
 constexpr int kFewPages = 4;       // pages behind a row's whole ones that one thread looks at
 constexpr int kForkThreads = 256;
 constexpr int kCopyBatch = 5;  // 16-byte loads of a thread in flight
@@ -146,15 +147,32 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs 
     __shared__ int heir_s[kMaxPoolRows];
     __shared__ int sums[kPlanThreads / 32];
     __shared__ int bits_s, long_s;
-    int ref[kRefsPerThread];  // of this thread's pages, a step ahead
-    auto load_refs = [&](int64_t at) {
-#pragma unroll
-        for (int k = 0; k < kRefsPerThread; ++k) {
-            const int64_t i = at + (int64_t)tid * kRefsPerThread + k;
-            ref[k] = i < p.num_blocks ? p.refs[i] : 1;
-        }
+    // The counts of the thread's pages of a step, and a bit for each that is free. The first step's are loaded here, so
+    // that they have arrived when they are needed.
+    const bool wide = (reinterpret_cast<uintptr_t>(p.refs) & 15u) == 0;
+    struct Counts {
+        int4 a, b;
     };
-    load_refs(0);
+    auto load_counts = [&](int64_t step) -> Counts {
+        const int64_t i = (step * kPlanThreads + tid) * kRefsPerThread;
+        Counts c;
+        c.a = c.b = make_int4(1, 1, 1, 1);
+        if (wide && i + kRefsPerThread <= p.num_blocks) {
+            c.a = reinterpret_cast<const int4*>(p.refs + i)[0];
+            c.b = reinterpret_cast<const int4*>(p.refs + i)[1];
+        } else if (i < p.num_blocks) {
+            int* x[kRefsPerThread] = {&c.a.x, &c.a.y, &c.a.z, &c.a.w, &c.b.x, &c.b.y, &c.b.z, &c.b.w};
+#pragma unroll
+            for (int k = 0; k < kRefsPerThread; ++k)
+                if (i + k < p.num_blocks) *x[k] = p.refs[i + k];
+        }
+        return c;
+    };
+    auto free_pages = [](const Counts& c) -> uint32_t {
+        return (uint32_t)((c.a.x == 0) | (c.a.y == 0) << 1 | (c.a.z == 0) << 2 | (c.a.w == 0) << 3 | (c.b.x == 0) << 4 |
+                          (c.b.y == 0) << 5 | (c.b.z == 0) << 6 | (c.b.w == 0) << 7);
+    };
+    const Counts first_step = load_counts(0);
     if (tid == 0) bits_s = long_s = 0;
     for (int b = tid; b < p.B; b += kPlanThreads) heir_s[b] = INT_MAX;
     __syncthreads();
@@ -225,21 +243,32 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs 
             total = (int)min((int64_t)total + sum, (int64_t)INT_MAX / 2);
         }
         int got = 0;
-        for (int64_t at = 0; at < p.num_blocks && got < total; at += kPlanThreads * kRefsPerThread) {
-            int mine = 0;
-            uint32_t free = 0;
+        const int64_t steps = (p.num_blocks + kPlanThreads * kRefsPerThread - 1) / (kPlanThreads * kRefsPerThread);
+        uint32_t ahead[kSteps] = {free_pages(first_step), 0u, 0u, 0u};
+        static_assert(kSteps == 4, "the lists of four");
+        for (int64_t s0 = 0; s0 < steps && got < total; s0 += kSteps) {
+            uint32_t now[kSteps];
 #pragma unroll
-            for (int k = 0; k < kRefsPerThread; ++k)
-                if (ref[k] == 0) {
-                    free |= 1u << k;
-                    ++mine;
-                }
-            load_refs(at + kPlanThreads * kRefsPerThread);
-            int sum;
-            int to = got + block_scan(mine, sums, &sum);
-            for (; free; free &= free - 1, ++to)
-                if (to < total) p.fresh[to] = (int32_t)(at + (int64_t)tid * kRefsPerThread + __ffs(free) - 1);
-            got += sum;
+            for (int k = 0; k < kSteps; ++k) now[k] = ahead[k];
+            if (s0 == 0 && steps > 1) {
+#pragma unroll
+                for (int k = 1; k < kSteps; ++k) now[k] = free_pages(load_counts(k));
+            }
+            if (s0 + kSteps < steps) {
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) ahead[k] = free_pages(load_counts(s0 + k + kSteps));
+            }
+#pragma unroll 1
+            for (int k = 0; k < kSteps && got < total; ++k) {
+                uint32_t free = k == 0 ? now[0] : k == 1 ? now[1] : k == 2 ? now[2] : now[3];
+                if (!__syncthreads_or((int)free)) continue;  // all held
+                int sum;
+                int to = got + block_scan(__popc(free), sums, &sum);
+                const int64_t first = ((s0 + k) * kPlanThreads + tid) * kRefsPerThread;
+                for (; free; free &= free - 1, ++to)
+                    if (to < total) p.fresh[to] = (int32_t)(first + __ffs(free) - 1);
+                got += sum;
+            }
         }
         if (tid == 0 && got < total) atomicOr(&bits_s, MLA_DEV_NO_PAGES);
         __syncthreads();

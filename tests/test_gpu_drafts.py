@@ -597,6 +597,37 @@ def test_fork_pages_with_much_room(kv):
         assert np.array_equal(cache.cpu().numpy().reshape(p["cache"].shape), want[0])
 
 
+@pytest.mark.parametrize("nb,free", [(8192, [0, 8191]), (8193, [8192] + list(range(4000, 4030))), (70001, list(range(69000, 70001, 7))),
+                                     (40000, [0, 1, 8191, 8192, 16383, 32767, 32768, 39999])])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_fork_pages_in_large_pools(nb, free, offset):
+    """Free pages far behind, at the borders of the search's steps, and counts that are not 16-byte aligned."""
+    import torch
+
+    import mla_latent_kv_gb300 as mla
+    refs = np.ones(nb, np.int32)
+    refs[free] = 0
+    need = len(free) // 2 + 1
+    parents, room = [-1, -1], [64 * need, 64 * (len(free) - need)]
+    p = dict(cache=np.zeros((0, nb, 1, 1), np.uint8), table=np.full((1, 600), -1, np.int32), counts=np.zeros(1, np.int32),
+             lens=np.zeros(1, np.int32), refs=refs)
+    want = fork_rule(p["cache"], p["table"], p["counts"], p["lens"], refs, parents, room)
+    buf = torch.zeros(nb + 4, dtype=torch.int32, device="cuda")
+    at = buf[offset:offset + nb]
+    at.copy_(dev(refs))
+    cache = torch.zeros((0, nb, PAGE * 1152), dtype=torch.uint8, device="cuda")
+    for extra in (0, 1):
+        st = _status()
+        got = mla.fork_pages(cache, dev(p["table"]), dev(p["counts"]), dev(p["lens"]), at, dev(np.array(parents, np.int32)),
+                             dev(np.array(room, np.int32) + np.array([0, 64 * extra], np.int32)), dev_status=st)
+        if extra:
+            assert st.item() == mla.DEV_NO_PAGES
+        else:
+            assert st.item() == 0
+            for g, w in zip(got, want[1:]):
+                assert np.array_equal(g.cpu().numpy(), w)
+
+
 def test_fork_pages_from_and_to_nothing():
     """A pool without rows, one that stays so, and one without pages."""
     import mla_latent_kv_gb300 as mla
