@@ -512,7 +512,7 @@ mla_status mla_rope_cache_write(const void* kv_c, int64_t kv_c_stride_t, const v
  *   tree_mask  uint64 [B, Sq] in device memory; bits from Sq on are not read
  *   workspace  >= mla_decode_tree_workspace_bytes for the same arguments, 256-byte aligned, contents undefined
  * 1 <= Sq <= 64. All other arguments, results, limits and errors as mla_decode; how a request's tokens are
- * divided over the device is the library's choice (from B, Sq, H and max_seq_len).
+ * divided over the device is the library's choice (from B, Sq, H, max_seq_len and the lengths).
  */
 size_t mla_decode_tree_workspace_bytes(mla_kv_dtype kv_dtype, int B, int Sq, int H, int max_seq_len);
 mla_status mla_decode_tree(const void* q, const void* kv_cache, mla_kv_dtype kv_dtype, int64_t num_blocks,

@@ -1,9 +1,9 @@
 // decode_tree_sm103.cu -- mla_decode_tree of more than 32 (draft, head) pairs a request, or 128 over an FP8 cache:
 // all pairs of a request against its own pages, 256 at a time.
 //
-// For a flat row f = (draft t, head) of request b and a range of its pages:  S = scale * q[b, f] K^T over the
-// tokens that draft t sees,  P = softmax(S),  o[f] = P V,  written to the outputs or, where a request's pages are
-// divided, as a partial state (o, lse) that the merge combines.
+// For a flat row f = (draft t, head) of request b and its pages, or a part of them:  S = scale * q[b, f] K^T over the
+// tokens that draft t sees,  P = softmax(S),  o[f] = P V,  written to the outputs or, of a part, as a partial state
+// (o, lse) that the merge below combines.
 //
 // What bounds it: the drafts of a request read the same keys, so that this is the matrix product of the
 // prefix kernel (decode_prefix_sm103.cu, whose pipeline this one follows): two SMs work as a pair on 256 rows
@@ -15,11 +15,17 @@
 //   CTAs 2, 3 ("output")  hold the 256 x 512 fp32 accumulators (all of both SMs' tensor memory) and add P V;
 //       helper warps rescale O when a group's maximum moved. Epilogue: O / l by TMA stores.
 //
-// Clusters stay for all of their units (request, tile of 256 rows, range of pages). While the output CTAs
+// Clusters stay for all of their units (request, tile of 256 rows). While the output CTAs
 // finish one, the scores CTAs load the next one's queries, score and weigh its first two groups. Barriers
 // are used on by group numbers that run through all units; a unit's odd last page is followed by one of zeros,
-// so that a group is always two pages. Units go to clusters longest request first, back and forth: no
-// counter, and (simulated) within 2% of giving each next unit to the cluster with the least work.
+// so that a group is always two pages.
+//
+// Balance. Many units go to the clusters whole, longest request first, back and forth: no counter, and (simulated)
+// within 2% of giving each next unit to the cluster with the least work. A few units are cut (kCut): every cluster takes an
+// equal share of all requests' groups, wherever it begins and ends. Which of the two is the host's guess from the
+// longest length possible (tree_shares); the cuts are made on the device from the lengths. Against ranges of a fixed
+// number of pages, which the host chose before: 20 requests x 256 rows over 8000 to 16,000 tokens 134 -> 101 us, 8 x 1024
+// over up to 32,768 325 -> 272, 5 x 320 over up to 100,000 307 -> 236, 1 x 1024 over 131,072 the same.
 //
 // Measured: 16 requests x 32 drafts x 128 heads over up to 8192 tokens 560 us, 1.56 PFLOP/s (FP8 562 with the
 // widening, 1.70: the clocks go down less), 32 x 8 over up to 4096 150 us, 1.44; 64 x 7 drafts of 16 heads over up
@@ -40,6 +46,8 @@
 #include <cuda.h>
 #include <math_constants.h>
 
+#include <algorithm>
+#include <cmath>
 #include <cstring>
 
 #include "decode_common.cuh"
@@ -79,6 +87,8 @@ constexpr int kAuxWarp0 = 10, kAuxWarps = 8;
 constexpr int kRelayWarps = 4;               // of CTA 3, from warp 6 on
 constexpr int kAhead = 10, kInRings = 6;     // pages between the helpers' progress and the one prefetched; in the rings
 constexpr int kCtrlBytes = 7168;
+constexpr int kUnitGroups = 5;               // what a unit's start and end cost (7 us), in groups
+constexpr int kEdgeGroups = 3;               // no part of a unit is shorter, unless the shares are short
 // scores CTA
 constexpr int OFF_QROPE = kCtrlBytes;
 constexpr int OFF_RING = OFF_QROPE + kQPanelBytes;
@@ -140,11 +150,14 @@ constexpr int OFF_MX = 1024;      // scores: f32 [4][128] exchange between the c
 constexpr int OFF_STAT_M = 2048;  // output: f32 [128] final running max (log2 units)
 constexpr int OFF_STAT_L = 2560;  // output: f32 [128] row sum
 constexpr int kMaxSorted = 240;   // requests whose lengths are kept and, for more units than clusters, sorted
-constexpr int OFF_ORDER = 544;    // u16 [kMaxSorted] requests, longest first
+constexpr int OFF_ORDER = 544;    // u16 [kMaxSorted] requests, longest first; or the cuts:
+constexpr int OFF_CUTS = OFF_ORDER;          // Place [2] where the cluster's part begins and ends
+constexpr int OFF_BEFORE = OFF_CUTS + 32;    // u32 [kTreeMaxCut] weights of the requests before
 constexpr int OFF_LENS = OFF_STAT_L + 512;  // s32 [kMaxSorted] tokens of each request
 constexpr int OFF_SCALES = 4096;  // scores, FP8: f32 [3][2][128] k_scales and v_scales of three groups in turn
 constexpr int kScaleBytes = 2 * kPPG * kPage * 4;
-static_assert(OFF_ORDER + 2 * kMaxSorted <= OFF_MX && OFF_LENS + 4 * kMaxSorted <= OFF_SCALES &&
+static_assert(OFF_ORDER + 2 * kMaxSorted <= OFF_MX && OFF_BEFORE + 4 * kTreeMaxCut <= OFF_MX && kTreeMaxCut <= kMaxSorted &&
+                  OFF_LENS + 4 * kMaxSorted <= OFF_SCALES &&
                   OFF_SCALES + 3 * kScaleBytes <= kCtrlBytes,
               "control block");
 
@@ -162,19 +175,59 @@ __device__ __forceinline__ void settle() {
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
 }
 
-// One unit of a cluster's list.
+// A place in the row of all requests' groups.
+struct Place {
+    int req, group;
+};
+__device__ __forceinline__ bool before(const Place& a, const Place& b) {
+    return a.req < b.req || (a.req == b.req && a.group < b.group);
+}
+
+// One unit of a cluster's list, or a part of one.
 struct Unit {
-    int req, tile, slab;   // slab: index of the output [splits, B]
+    int req, tile, slab;   // slab: the request, of a part its partial state
+    bool part;
     int page0, npages, ngroups;
     int drafts0;           // the request's tokens before its drafts (below 0: the first are not there)
     int drafted;           // the first of the unit's pages that holds drafts (npages: none)
 };
 
-template <bool kScaled>
+// The cuts. The requests stand in a row, each as long as its groups and kUnitGroups for a unit's start and
+// end; the row is cut into equal shares, and a cluster goes through one share for one tile. (Clusters side by
+// side take a share's tiles, and find its pages in L2.) A cut that falls into a unit's fixed part, or leaves a few
+// groups before or behind it, moves to the unit's edge.
+__device__ __forceinline__ uint32_t unit_groups(int len) {
+    return ((uint32_t)((len + kPage - 1) / kPage) + kPPG - 1) / kPPG;
+}
+__device__ __forceinline__ uint32_t unit_weight(int len) { return len > 0 ? unit_groups(len) + kUnitGroups : 1u; }
+__device__ Place cut_of(const TreeArgs& p, const int* lens, const uint32_t* weights, int share) {
+    if (share == 0) return Place{0, 0};
+    if (share == p.shares) return Place{p.B, 0};
+    const uint32_t all = weights[p.B - 1] + unit_weight(lens[p.B - 1]);
+    // every share has a start of its own: the first request's is not counted
+    const uint32_t free = min(all - 1, (uint32_t)kUnitGroups);
+    const uint32_t cut = all - free < 1u << 26 ? (all - free) * (uint32_t)share / (uint32_t)p.shares  // 64 shares at most
+                                               : (uint32_t)((uint64_t)(all - free) * (uint32_t)share / (uint32_t)p.shares);
+    const uint32_t at = free + cut;
+    const int edge = (int)min((all - free) / (4u * (uint32_t)p.shares), (uint32_t)kEdgeGroups);
+    int lo = 0, hi = p.B - 1;  // the last request that begins at or before `at`
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (weights[mid] <= at)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const int groups = (int)unit_groups(lens[lo]), group = (int)(at - weights[lo]) - kUnitGroups;
+    return group <= edge ? Place{lo, 0} : groups - group > edge ? Place{lo, group} : Place{lo + 1, 0};
+}
+
+// kCut: units are cut (see cut_of). Instances of their own: with both in one, FP8's softmax spilled (562 -> 600 us).
+template <bool kScaled, bool kCut>
 __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     decode_tree_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                        const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap o_map,
-                       const TreeArgs p) {
+                       const __grid_constant__ CUtensorMap part_map, const TreeArgs p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_addr(smem);
     const int tid = threadIdx.x, lane = tid & 31;
@@ -197,7 +250,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
 
     // Lengths, and the requests in their order (ties by number), every thread placing one.
     const int clusters = (int)(gridDim.x >> 2), cluster = (int)(blockIdx.x >> 2);
-    const bool kept = p.B <= kMaxSorted, sorted = kept && p.units > (int64_t)clusters;
+    const bool kept = p.B <= kMaxSorted, sorted = kept && !kCut && p.units > (int64_t)clusters;
     int* lens = reinterpret_cast<int*>(smem + OFF_LENS);
     if (kept && tid < p.B) lens[tid] = length(tid, blockIdx.x == 0);
     if (tid == kThreads - 1) {
@@ -232,25 +285,45 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         for (int b = 0; b < p.B; ++b) place += lens[b] > mine || (lens[b] == mine && b < tid);
         reinterpret_cast<uint16_t*>(smem + OFF_ORDER)[place] = (uint16_t)tid;
     }
+    Place* cuts = reinterpret_cast<Place*>(smem + OFF_CUTS);
+    if constexpr (kCut) {
+        uint32_t* weights = reinterpret_cast<uint32_t*>(smem + OFF_BEFORE);
+        if (tid < p.B) {
+            uint32_t sum = 0;
+            for (int b = 0; b < tid; ++b) sum += unit_weight(lens[b]);
+            weights[tid] = sum;
+        }
+        __syncthreads();
+        if (tid < 2) cuts[tid] = cut_of(p, lens, weights, cluster / p.tiles + tid);
+    }
     cluster_sync();  // every CTA's barriers (and the order) exist before any remote arrive or copy
     const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM), 0);
     griddep_wait();  // q, the masks, the cache and the lengths may be earlier kernels' outputs
     if (tid == 0) griddep_launch_dependents();
 
-    // The cluster's unit number k, of all units in the order (range of pages, request by length, tile): a
-    // request's tiles run side by side and read its pages from L2, and ranges behind short requests' ends
-    // come last.
+    // The cluster's unit number k (u: the one before). Whole units: in the order (request by length, tile), so that a
+    // request's tiles run side by side and read its pages from L2. Cut ones: what lies between the cluster's cuts.
     auto unit_of = [&](int k, Unit& u) -> bool {
-        const uint32_t i = (uint32_t)k * clusters + (uint32_t)(k & 1 ? clusters - 1 - cluster : cluster);
-        if (i >= (uint32_t)p.units) return false;
-        const uint32_t pairs = i / (uint32_t)p.tiles;  // of split and request
-        const int split = (int)(pairs / (uint32_t)p.B), place = (int)(pairs - (uint32_t)split * p.B);
-        u.tile = (int)(i - pairs * (uint32_t)p.tiles);
-        u.req = sorted ? (int)reinterpret_cast<const uint16_t*>(smem + OFF_ORDER)[place] : place;
-        u.slab = split * p.B + u.req;
+        Place at{};
+        if constexpr (kCut) {
+            at = k > 0 ? Place{u.req + 1, 0} : cuts[0];
+            if (!before(at, cuts[1])) return false;
+            u.tile = cluster % p.tiles;
+        } else {
+            const uint32_t i = (uint32_t)k * clusters + (uint32_t)(k & 1 ? clusters - 1 - cluster : cluster);
+            if (i >= (uint32_t)p.units) return false;
+            at.req = (int)(i / (uint32_t)p.tiles);
+            u.tile = (int)(i - (uint32_t)at.req * (uint32_t)p.tiles);
+            if (sorted) at.req = (int)reinterpret_cast<const uint16_t*>(smem + OFF_ORDER)[at.req];
+        }
+        u.req = at.req;
         const int seq = kept ? lens[u.req] : length(u.req), pages = (seq + kPage - 1) / kPage;
-        u.page0 = min(pages, split * p.pages_per_split);
-        u.npages = min(pages, u.page0 + p.pages_per_split) - u.page0;
+        u.page0 = kPPG * at.group;
+        int end = pages;
+        if (kCut && cuts[1].req == u.req) end = min(pages, kPPG * cuts[1].group);
+        u.npages = end - u.page0;
+        u.part = kCut && u.npages < pages;
+        u.slab = u.part ? 2 * cluster + (at.group == 0) : u.req;
         u.ngroups = (u.npages + kPPG - 1) / kPPG;
         u.drafts0 = seq - p.Sq;
         u.drafted = min(u.npages, max(0, max(u.drafts0, 0) / kPage - u.page0));
@@ -675,14 +748,17 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
             const int ctid = tid - 64;  // 0..511; 0..127 are the helper warps
             const int eset = (warp - 2) >> 2;
-            float* lse_out = p.part_o ? p.part_lse : p.lse;
+            if (kCut && eset == 0 && cuts[0].group > 0 && !before(cuts[0], cuts[1]))  // a share of no groups amid a unit
+                p.part_lse[(size_t)2 * cluster * kTileRows + 128 * side + row] = -CUDART_INF_F;
             for (int k = 0; unit_of(k, u); ++k) {
                 const int rows0 = rows_of(u);
-                const size_t out_row = (size_t)u.slab * p.flat_rows + rows0 + row;
+                float* lse_out = u.part ? p.part_lse : p.lse;
+                const size_t out_row =
+                    u.part ? (size_t)u.slab * kTileRows + 128 * side + row : (size_t)u.slab * p.flat_rows + rows0 + row;
                 const bool live = rows0 + row < p.flat_rows;
-                if (u.npages == 0) {  // no token: an empty state (whose o the merge does not read), or the final zeros
+                if (u.npages == 0) {  // no token
                     if (eset == 0 && live && lse_out) lse_out[out_row] = -CUDART_INF_F;
-                    if (!p.part_o && live) {
+                    if (live) {
                         const int bytes = p.o_bf16 ? 2 * kL / 4 : 4 * kL / 4;  // of this warp set's quarter of the row
                         uint4* dst = reinterpret_cast<uint4*>((uint8_t*)p.o + out_row * 4 * bytes + (size_t)eset * bytes);
                         for (int c = 0; c < bytes / 16; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
@@ -767,12 +843,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 // O / l leaves through TMA stores over the V ring and the P buffers; rows past the request's are
                 // cut off by the tensor map
                 const bool store = rows0 < p.flat_rows;
-                if (p.o_bf16)
+                if (p.o_bf16 && !u.part)
                     store_rows<false, 4, 3, kBarEpi, false>(smem, sbase, OFF_V, tmem + lane_base, row, eset, (ctid & 127) == 0, true,
                                                      empty, inv, &o_map, rows0, u.slab, store);
                 else
                     store_rows<true, 4, 3, kBarEpi, false>(smem, sbase, OFF_V, tmem + lane_base, row, eset, (ctid & 127) == 0, true,
-                                                    empty, inv, &o_map, rows0, u.slab, store);
+                                                    empty, inv, u.part ? &part_map : &o_map, u.part ? 128 * side : rows0,
+                                                    u.slab, store);
                 // O, the statistics and the tiles have been read: the next unit's may come
                 tc_fence_before();
                 fence_proxy_async_cta();
@@ -784,6 +861,18 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 next();
             }
             if ((ctid & 127) == 0) bulk_wait_group<0>();  // the stores are complete before the CTA exits
+        } else if (kCut && side == 1) {
+            // Warp 18 of CTA 3: for the merge, the unit that ends in the cluster's share, and the share it begins in.
+            if (lane == 0) {
+                const Place from = cuts[0];
+                int share = -1;
+                if (from.group > 0 && cuts[1].req > from.req) {
+                    const uint32_t* weights = reinterpret_cast<const uint32_t*>(smem + OFF_BEFORE);
+                    share = cluster / p.tiles - 1;
+                    while (before(Place{from.req, 0}, cut_of(p, lens, weights, share))) --share;
+                }
+                p.pieces[cluster] = make_int2(from.req, share);
+            }
         } else if (!kScaled && side == 0 && lane == 0 && p.tiles == 1) {
             // Warp 18: the pages that the rings have no room for yet are brought into L2, the next unit's first ones
             // too (64 requests of up to 8192 tokens, 112 pairs: 146 -> 139 us; with several tiles a request the others
@@ -856,15 +945,109 @@ __global__ void __launch_bounds__(kWidenThreads) tree_widen_kernel(TreeArgs p, c
     }
 }
 
-int g_attr_done[2][64] = {};
+// ------------------------------------------------------------------------------------------
+// The states of a cut unit's parts -> its rows:  o = sum_i w_i o_i / sum_i w_i,  lse = M + log sum_i w_i,  w_i =
+// exp(lse_i - M), M the largest lse. Half a row a warp, four rows a block and turn. Up to
+// 28 MB are read once, 6 to 9 us with the launch. No more blocks than run at once: with one for every cluster and four
+// rows (2304) 3 x 256 rows over up to 3000 tokens took 24.8 us a call, 23.5 so.
+// ------------------------------------------------------------------------------------------
+constexpr int kMergeThreads = 256, kMergeRows = kMergeThreads / 64, kMergeBatch = 3, kMergeBlocks = 608;
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArgs p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    static_assert(kTreeMaxClusters == 64, "two a lane");
+    __shared__ int3 units_s[kTreeMaxClusters];  // (request, its first share, cluster of its last one)
+    __shared__ int n_s;
+    const int tid = threadIdx.x, lane = tid & 31, clusters = p.shares * p.tiles;
+    if (tid < 32) {
+        int found = 0;
+        int2 u[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) u[h] = 32 * h + lane < clusters ? p.pieces[32 * h + lane] : make_int2(0, -1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t cut = __ballot_sync(0xffffffffu, u[h].y >= 0);
+            if (u[h].y >= 0) units_s[found + __popc(cut & ((1u << lane) - 1u))] = make_int3(u[h].x, u[h].y, 32 * h + lane);
+            found += __popc(cut);
+        }
+        if (lane == 0) n_s = found;
+    }
+    __syncthreads();
+    const int chunks = (p.slab_rows + kMergeRows - 1) / kMergeRows, tasks = n_s * chunks, dim = (tid & 63) * 8;
+    for (int task = (int)blockIdx.x; task < tasks; task += (int)gridDim.x) {
+        const int3 unit = units_s[task / chunks];
+        const int row = task % chunks * kMergeRows + (tid >> 6), tile = unit.z % p.tiles, flat = tile * kTileRows + row;
+        if (flat >= p.flat_rows) continue;
+        // the unit's first part is its share's last one, the others their shares' first
+        const int n = unit.z / p.tiles - unit.y + 1;
+        auto slab_of = [&](int i) -> size_t { return 2 * (size_t)((unit.y + i) * p.tiles + tile) + (i == 0); };
+        float4 v[kMergeBatch][2];
+        float x[kMergeBatch];
+        auto load = [&](int i0) {
+#pragma unroll
+            for (int k = 0; k < kMergeBatch; ++k) {
+                x[k] = -CUDART_INF_F;
+                v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i0 + k >= n) continue;
+                const size_t slab = slab_of(i0 + k);
+                x[k] = p.part_lse[slab * kTileRows + row];
+                const float4* src = reinterpret_cast<const float4*>(p.part_o + (slab * p.slab_rows + row) * kL + dim);
+                v[k][0] = src[0];
+                v[k][1] = src[1];
+            }
+        };
+        load(0);
+        // a NaN state counts as the largest: its weight, the sum and the result are NaN then
+        float M = -CUDART_INF_F;
+        for (int i = lane; i < n; i += 32) {
+            const float y = p.part_lse[slab_of(i) * kTileRows + row];
+            M = fmaxf(M, y != y ? CUDART_INF_F : y);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float acc[8] = {}, sum = 0.f;
+        for (int i0 = 0; i0 < n && M != -CUDART_INF_F; i0 += kMergeBatch) {
+            if (i0 > 0) load(i0);
+#pragma unroll
+            for (int k = 0; k < kMergeBatch; ++k) {
+                if (x[k] == -CUDART_INF_F) continue;
+                const float w = __expf(x[k] - M);
+                sum += w;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    acc[4 * h] = fmaf(w, v[k][h].x, acc[4 * h]);
+                    acc[4 * h + 1] = fmaf(w, v[k][h].y, acc[4 * h + 1]);
+                    acc[4 * h + 2] = fmaf(w, v[k][h].z, acc[4 * h + 2]);
+                    acc[4 * h + 3] = fmaf(w, v[k][h].w, acc[4 * h + 3]);
+                }
+            }
+        }
+        const float inv = M == -CUDART_INF_F ? 0.f : 1.f / sum;
+        const size_t out = (size_t)unit.x * p.flat_rows + flat;
+        if ((tid & 63) == 0 && p.lse) p.lse[out] = M == -CUDART_INF_F ? M : M + logf(sum);
+        if (p.o_bf16) {
+            *reinterpret_cast<uint4*>((uint16_t*)p.o + out * kL + dim) =
+                make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                           pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+        } else {
+            float4* dst = reinterpret_cast<float4*>((float*)p.o + out * kL + dim);
+            dst[0] = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+            dst[1] = make_float4(acc[4] * inv, acc[5] * inv, acc[6] * inv, acc[7] * inv);
+        }
+    }
+}
+
+int g_attr_done[2][2][64] = {};
 int g_clusters[64] = {};
 
-cudaError_t set_attr(int dev, bool scaled) {
-    if (dev < 64 && g_attr_done[scaled][dev]) return cudaSuccess;
-    const cudaError_t e =
-        scaled ? cudaFuncSetAttribute(decode_tree_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes)
-               : cudaFuncSetAttribute(decode_tree_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e == cudaSuccess && dev < 64) g_attr_done[scaled][dev] = 1;
+using TreeKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, TreeArgs);
+const TreeKernel kKernels[2][2] = {{decode_tree_kernel<false, false>, decode_tree_kernel<false, true>},
+                                   {decode_tree_kernel<true, false>, decode_tree_kernel<true, true>}};  // [FP8][cut]
+
+cudaError_t set_attr(int dev, bool scaled, bool cut) {
+    if (dev < 64 && g_attr_done[scaled][cut][dev]) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kKernels[scaled][cut], cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e == cudaSuccess && dev < 64) g_attr_done[scaled][cut][dev] = 1;
     return e;
 }
 
@@ -874,7 +1057,7 @@ int tree_clusters() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return -1;
     if (dev < 64 && g_clusters[dev] > 0) return g_clusters[dev];
-    if (set_attr(dev, false) != cudaSuccess) return -1;
+    if (set_attr(dev, false, false) != cudaSuccess) return -1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(4);
     cfg.blockDim = dim3(kThreads);
@@ -887,32 +1070,30 @@ int tree_clusters() {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, decode_tree_kernel<false>, &cfg) != cudaSuccess || n < 1) return -1;
+    if (cudaOccupancyMaxActiveClusters(&n, kKernels[0][0], &cfg) != cudaSuccess || n < 1) return -1;
+    n = std::min(n, kTreeMaxClusters);
     if (dev < 64) g_clusters[dev] = n;
     return n;
 }
 
-// The split of requests of `pages` pages, `units` (request, tile) pairs: ranges of an even number of pages.
-void tree_split(int64_t units, int64_t flat_rows, int pages, int clusters, int* splits, int* pages_per_split) {
-    // Time of S splits: waves of units, each a range of pages and a fixed part, and, for more than one, the
-    // partial states written and read back and the merge's launch. In page-times of one cluster (about 0.6 us).
-    constexpr double kUnitPages = 14.0, kMerge = 6.0;
-    const double partial = (double)flat_rows * (kL + 1) * 8.0 / 5.0e6 / 0.6;  // bytes / (bytes per page-time)
-    double best = 1e300;
-    *splits = 1;
-    *pages_per_split = (pages + 1) / 2 * 2;
-    for (int S = 1; S <= (pages + 1) / 2 && S <= 3 * clusters; ++S) {  // more never fill waves better
-        const int per = ((pages + S - 1) / S + 1) / 2 * 2;
-        const int used = (pages + per - 1) / per;  // ranges that hold pages
-        if (used < S && S > 1) continue;
-        const int64_t waves = (units * S + clusters - 1) / clusters;
-        const double t = (double)waves * (per + kUnitPages) + (S > 1 ? kMerge + S * partial : 0.0);
-        if (t < best * 0.999) {
-            best = t;
-            *splits = S;
-            *pages_per_split = per;
-        }
-    }
+int tree_shares(int B, int tiles, int slab_rows, int pages, int clusters) {
+    // Times in groups (1.28 us), of requests half to all as long as the longest. Whole units: the balanced time, and
+    // the rest of the last turn.
+    if (B < 1 || B > kTreeMaxCut || pages < 2 * kPPG) return 0;
+    const double longest = (pages + kPPG - 1) / kPPG, usual = 0.75 * longest, units = (double)B * tiles;
+    const double turns = std::ceil(units / clusters), even = units / clusters * (usual + kUnitGroups);
+    const double whole = turns == 1 ? longest + kUnitGroups : even + 0.4 * (turns - units / clusters) * (longest + kUnitGroups);
+    // Cut: a request of few groups into fewer parts. One more takes G / n^2 of its G groups off each of n, and costs a
+    // third of a group of the merge's time, or its rows written and read (5 TB/s).
+    const double most = std::floor((double)clusters / tiles);
+    const double parts = std::min(std::sqrt(units * longest * 1562.0 / slab_rows) / units, 1.7 * std::sqrt(longest));
+    const double part = std::max(1.0, std::ceil(longest / parts));
+    const double shares = std::min(most, std::max((double)B, std::ceil((B * (longest + kUnitGroups) - kUnitGroups) / part)));
+    if (shares < 2) return 0;
+    // beside a share of the groups: a start of its own, the merge's launch, and the partial rows written and read
+    const double merge = 2.0 + 12.0 / 36 / kTileRows * shares * tiles * slab_rows;
+    const double cut = B * (usual + kUnitGroups) / shares + kUnitGroups + merge;
+    return cut < whole ? (int)shares : 0;
 }
 
 cudaError_t launch_decode_tree(const TreeArgs& in, const uint8_t* cache, uint16_t* widened, float* scales, cudaStream_t s) {
@@ -921,7 +1102,7 @@ cudaError_t launch_decode_tree(const TreeArgs& in, const uint8_t* cache, uint16_
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    e = set_attr(dev, fp8);
+    e = set_attr(dev, fp8, a.pieces != nullptr);
     if (e != cudaSuccess) return e;
     const int clusters = tree_clusters();
     if (clusters < 1) return cudaErrorUnknown;
@@ -938,11 +1119,12 @@ cudaError_t launch_decode_tree(const TreeArgs& in, const uint8_t* cache, uint16_
     }
     a.key_rows = (int)rows;
     a.keys = fp8 ? (const uint8_t*)widened : cache;
-    CUtensorMap k_map, v_map, q_map, o_map;
+    CUtensorMap k_map, v_map, q_map, o_map, part_map;
     memset(&k_map, 0, sizeof k_map);
     memset(&v_map, 0, sizeof v_map);
     memset(&q_map, 0, sizeof q_map);
     memset(&o_map, 0, sizeof o_map);
+    memset(&part_map, 0, sizeof part_map);
     if (rows > 0) {  // else no request has a page
         // the rows as [panel of 64 dims][row][64]: one box is several panels of a page
         const void* base = fp8 ? (const void*)widened : cache;
@@ -965,17 +1147,26 @@ cudaError_t launch_decode_tree(const TreeArgs& in, const uint8_t* cache, uint16_
     {
         const bool f32 = !a.o_bf16;
         const uint64_t size = f32 ? 4 : 2;
-        const uint64_t dims[3] = {(uint64_t)kL, (uint64_t)a.flat_rows, (uint64_t)a.splits * a.B};
+        const uint64_t dims[3] = {(uint64_t)kL, (uint64_t)a.flat_rows, (uint64_t)a.B};
         const uint64_t strides[2] = {(uint64_t)kL * size, (uint64_t)a.flat_rows * kL * size};
         const uint32_t box[3] = {f32 ? 32u : 64u, 128, 1};
         e = encode_tmap(&o_map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                        a.part_o ? (const void*)a.part_o : a.o, dims, strides, box, true);
+                        a.o, dims, strides, box, true);
         if (e != cudaSuccess) return e;
     }
-    a.units = (int64_t)a.splits * a.B * a.tiles;
-    const unsigned grid = 4 * (unsigned)(a.units < clusters ? a.units : clusters);
-    return fp8 ? launch_pdl(decode_tree_kernel<true>, dim3(grid), dim3(kThreads), kSmemBytes, s, k_map, v_map, q_map, o_map, a)
-               : launch_pdl(decode_tree_kernel<false>, dim3(grid), dim3(kThreads), kSmemBytes, s, k_map, v_map, q_map, o_map, a);
+    if (a.pieces) {
+        const uint64_t dims[3] = {(uint64_t)kL, (uint64_t)a.slab_rows, 2 * (uint64_t)a.shares * a.tiles};
+        const uint64_t strides[2] = {(uint64_t)kL * 4, (uint64_t)a.slab_rows * kL * 4};
+        const uint32_t box[3] = {32u, 128, 1};
+        e = encode_tmap(&part_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, a.part_o, dims, strides, box, true);
+        if (e != cudaSuccess) return e;
+    }
+    a.units = (int64_t)a.B * a.tiles;
+    const int64_t used = a.pieces ? (int64_t)a.shares * a.tiles : std::min<int64_t>(a.units, clusters);
+    e = launch_pdl(kKernels[fp8][a.pieces != nullptr], dim3(4u * (unsigned)used), dim3(kThreads), kSmemBytes, s, k_map, v_map,
+                   q_map, o_map, part_map, a);
+    if (e != cudaSuccess || !a.pieces) return e;
+    return launch_pdl(tree_merge_kernel, dim3(kMergeBlocks), dim3(kMergeThreads), 0, s, a);
 }
 
 }  // namespace mla

@@ -66,13 +66,13 @@ mla_status rope_args(const char* who, const void* x, int64_t x_t, int64_t x_n, c
 // ------------------------------------------------------------------------------------ tree
 // How a tree call runs, and its workspace. At most 32 (draft, head) pairs, or 128 over an FP8 cache, are one row
 // of so many heads for the decode kernels (splits: theirs). More go through a kernel of their own, 256 at a time;
-// its workspace is the widened rows (FP8), then the partial states. Both sides of the border: 64 requests of up to
+// its workspace is the widened rows (FP8), then, if units are cut, their parts' states. Both sides of the border: 64 requests of up to
 // 8192 tokens, bf16, 32 pairs 131 us as a row and 147 by the tree kernel; 112 pairs 157 and 146, FP8 233 and 303;
 // 128 requests of up to 1000 tokens, 128 pairs, bf16 80 and 66, FP8 74 and 107.
 struct TreePlan {
     bool rows;
-    int splits, tiles, pages_per_split, wide_pages;
-    size_t scales, part_o, part_lse, total;
+    int splits, tiles, shares, slab_rows, wide_pages;  // shares: that the requests are cut into, or 0
+    size_t scales, part_o, part_lse, pieces, total;
 };
 bool plan_tree(mla_kv_dtype kv, int B, int Sq, int H, int max_seq_len, TreePlan* w) {
     const int64_t flat = (int64_t)Sq * H;
@@ -92,7 +92,8 @@ bool plan_tree(mla_kv_dtype kv, int B, int Sq, int H, int max_seq_len, TreePlan*
     const int clusters = mla::tree_clusters();
     if (clusters < 1) return false;
     w->tiles = (int)((flat + 255) / 256);
-    mla::tree_split((int64_t)B * w->tiles, B * flat, pages, clusters, &w->splits, &w->pages_per_split);
+    w->slab_rows = (int)std::min<int64_t>(flat, 256);
+    w->shares = mla::tree_shares(B, w->tiles, w->slab_rows, pages, clusters);
     size_t off = 0;
     if (kv == MLA_KV_FP8_E4M3_SCALED) {
         w->wide_pages = pages;
@@ -101,11 +102,14 @@ bool plan_tree(mla_kv_dtype kv, int B, int Sq, int H, int max_seq_len, TreePlan*
         w->scales = off;
         off += up256(rows * 2 * sizeof(float));
     }
-    if (w->splits > 1) {
+    if (w->shares > 0) {
+        const size_t slabs = (size_t)2 * w->shares * w->tiles;
         w->part_o = off;
-        off += up256((size_t)w->splits * B * flat * mla::kL * sizeof(float));
+        off += up256(slabs * w->slab_rows * mla::kL * sizeof(float));
         w->part_lse = off;
-        off += up256((size_t)w->splits * B * flat * sizeof(float));
+        off += up256(slabs * 256 * sizeof(float));
+        w->pieces = off;
+        off += up256(slabs / 2 * sizeof(int2));
     }
     w->total = off;
     return true;
@@ -245,7 +249,7 @@ mla_status mla_decode_tree(const void* q, const void* kv_cache, mla_kv_dtype kv_
     TreePlan w{};
     if (!plan_tree(kv_dtype, B, Sq, H, max_seq_len, &w))
         return set_error(MLA_ERR_CUDA, "%s: could not plan the call (no CUDA device?)", who);
-    if (!w.rows && ((int64_t)w.splits * B * w.tiles > INT32_MAX / 4 || (int64_t)B * w.wide_pages > INT32_MAX / mla::kPage || B > 65535))
+    if (!w.rows && ((int64_t)B * w.tiles > INT32_MAX / 4 || (int64_t)B * w.wide_pages > INT32_MAX / mla::kPage || B > 65535))
         return set_error(MLA_ERR_UNSUPPORTED, "%s: %d requests of %d tokens too many", who, B, max_seq_len);
     if (w.total > 0 && (!workspace || workspace_bytes < w.total))
         return set_error(MLA_ERR_WORKSPACE_TOO_SMALL, "%s: workspace %zu bytes < %zu needed", who,
@@ -279,36 +283,21 @@ mla_status mla_decode_tree(const void* q, const void* kv_cache, mla_kv_dtype kv_
     a.max_seq_len = num_blocks > 0 ? max_seq_len : 0;
     a.masks = tree_mask;
     a.scale = scale;
-    a.splits = w.splits;
-    a.pages_per_split = w.pages_per_split;
     a.wide_pages = w.wide_pages;
     a.o = o_latent;
     a.lse = lse;
-    a.o_bf16 = w.splits == 1 && o_dtype == MLA_DT_BF16;
-    if (w.splits > 1) {
+    a.o_bf16 = o_dtype == MLA_DT_BF16;
+    if (w.shares > 0) {
+        a.shares = w.shares;
+        a.slab_rows = w.slab_rows;
         a.part_o = (float*)(ws + w.part_o);
         a.part_lse = (float*)(ws + w.part_lse);
+        a.pieces = (int2*)(ws + w.pieces);
     }
     a.dev_status = dev_status;
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e = mla::launch_decode_tree(a, (const uint8_t*)kv_cache, fp8 ? (uint16_t*)ws : nullptr, (float*)(ws + w.scales), s);
-    if (e != cudaSuccess) return cuda_error(e, who);
-    if (w.splits > 1) {
-        mla::DecodeArgs m{};  // every row's states are "pre" states, none its own
-        m.B = B;
-        m.Sq = Sq;
-        m.rows = B * Sq;
-        m.H = H;
-        m.pre_o = a.part_o;
-        m.pre_lse = a.part_lse;
-        m.pre_splits = w.splits;
-        m.o_latent = o_latent;
-        m.o_dtype = o_dtype;
-        m.lse = lse;
-        e = mla::launch_merge(m, s);
-        if (e != cudaSuccess) return cuda_error(e, who);
-    }
-    return mla::set_ok();
+    return e == cudaSuccess ? mla::set_ok() : cuda_error(e, who);
 }
 
 mla_status mla_accept_tokens(void* kv_cache, mla_kv_dtype kv_dtype, int layers, int64_t num_blocks, const int32_t* block_table,

@@ -362,6 +362,8 @@ cudaError_t launch_fork_pages(const ForkArgs& a, bool fp8, cudaStream_t s);
 
 // ---- decode of drafted trees, more than 128 (draft, head) pairs a request ------------------------
 constexpr int kTreeMaxDrafts = 64;  // bits of a mask
+constexpr int kTreeMaxCut = 112;    // requests whose units are cut
+constexpr int kTreeMaxClusters = 64;
 struct TreeArgs {
     const uint16_t* q;          // bf16 [B, flat_rows, 576]
     int flat_rows;              // Sq * H of a request
@@ -374,8 +376,8 @@ struct TreeArgs {
     int max_seq_len;
     const uint64_t* masks;      // [B, Sq]
     float scale;
-    int splits, pages_per_split;
-    int64_t units;              // splits * B * tiles
+    int64_t units;              // B * tiles
+    int shares;                 // of cut units, shares * tiles clusters run
     const uint8_t* keys;        // the bf16 rows behind the keys' tensor map, and their number
     int key_rows;
     int wide_pages;             // FP8: pages of each request's widened rows, [B, wide_pages, 64]
@@ -383,13 +385,17 @@ struct TreeArgs {
     const float* v_scales;
     void* o;                    // [B, flat_rows, 512], fp32 or bf16
     float* lse;                 // [B, flat_rows] or null
-    float* part_o;              // more than one split: fp32 [splits, B, flat_rows, 512]
-    float* part_lse;            // [splits, B, flat_rows]
-    int o_bf16;                 // o in bf16 (and one split)
+    int2* pieces;               // [clusters] (request, share) of the cut unit that ends in the cluster's share (share
+                                // -1: none), and where it begins; null: units are not cut
+    float* part_o;              // fp32 [2 clusters, slab_rows, 512]
+    float* part_lse;            // [2 clusters, 256]
+    int slab_rows;              // min(flat_rows, 256)
+    int o_bf16;                 // o in bf16
     int32_t* dev_status;        // or null
 };
 int tree_clusters();  // clusters of the tree kernel that run at once on the current device, or -1
-void tree_split(int64_t units, int64_t flat_rows, int pages, int clusters, int* splits, int* pages_per_split);
+// Shares into which the requests are cut (of `clusters` / tiles that can run at once), or 0: they are not.
+int tree_shares(int B, int tiles, int slab_rows, int pages, int clusters);
 // FP8: the requests' rows are first widened to `widened` [B, wide_pages, 64, 576], their scales to `scales`
 // [2, B, wide_pages, 64].
 cudaError_t launch_decode_tree(const TreeArgs& a, const uint8_t* cache, uint16_t* widened, float* scales, cudaStream_t s);

@@ -228,6 +228,53 @@ def test_decode_tree_splits(B, Sq, H, length, max_len, kv):
     check_attention(*_tree(c, max_len=max_len, o_dtype=mla.DT_BF16), want, bf16_out=True)
 
 
+@pytest.mark.parametrize("kv", [BF, F8])
+@pytest.mark.parametrize("lens,Sq,H,max_len", [
+    ([5000], 3, 128, 5000),                                          # one request in many parts, two tiles
+    ([12800, 64, 12672], 2, 64, 12800),                              # cuts at and beside the edges of units
+    ([0, 9000, 0, 7777, 1, 0], 6, 50, 9000),                         # empty slots first, between and last
+    ([40, 129, 20000, 3, 64, 700, 128, 65] + [90] * 12, 2, 90, 20000),  # one long request among short ones
+    ([0, 0, 0, 0], 2, 128, 20000),                                   # nothing at all
+    ([2, 0, 1, 2], 2, 128, 20000),                                   # drafts alone, shares of no group
+    ([300 + 97 * b for b in range(24)], 2, 120, 16000),              # far fewer tokens than the bound allows
+    ([2000, 1500, 1700, 1999], 10, 128, 2000),                       # too little to be cut among seven clusters a tile
+    ([9000, 1500], 10, 128, 9000),                                   # five tiles: 35 clusters
+    ([64 * (1 + b % 3) - b % 2 for b in range(112)], 2, 17, 30000),  # as many requests as are cut
+    ([64 * (1 + b % 3) - b % 2 for b in range(113)], 2, 17, 30000),  # one more: whole units
+])
+def test_decode_tree_cut_requests(lens, Sq, H, max_len, kv):
+    """Requests that are cut into shares wherever they end, and the merge of a request's parts."""
+    import torch
+
+    import mla_latent_kv_gb300 as mla
+    c = tree_case(lens, Sq, H, kv, seed=sum(lens) + H, extra_cols=max(0, -(-max_len // PAGE) - -(-max(lens + [1]) // PAGE)))
+    want, st = attend_tree(c), _status()
+    o, lse = _tree(c, max_len=max_len, status=st)
+    check_attention(o, lse, want)
+    again = _tree(c, max_len=max_len)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    check_attention(*_tree(c, max_len=max_len, o_dtype=mla.DT_BF16), want, bf16_out=True)
+    assert st.item() == 0
+    if Sq * H > 32:  # partial states: the requests were cut
+        assert (mla.decode_tree_workspace_bytes(len(lens), Sq, H, max_len, BF) > 0) == (len(lens) <= 112 and lens[0] != 2000)
+
+
+@pytest.mark.parametrize("kv", [BF, F8])
+def test_decode_tree_cut_requests_replayed(kv):
+    """The cuts follow the lengths on the device: a captured call with the lengths of another step, and back."""
+    import torch
+    c = tree_case([9000] * 6, 4, 60, kv, seed=5)
+    g = torch.cuda.CUDAGraph()
+    _tree(c)
+    with torch.cuda.graph(g):
+        o, lse = _tree(c)
+    for lens in ([50, 9000, 4, 0, 8999, 64], [0, 0, 0, 0, 0, 3], [9000, 40, 6000, 3000, 9000, 100]):
+        c["seq_lens"].copy_(torch.tensor(lens, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        check_attention(o, lse, attend_tree(dict(c, lens=lens)))
+
+
 def _fill_rows(c, rows, value=None, inf=False):
     """Put NaN (or inf) into cache rows (block, place): every element for bf16, the scales for FP8."""
     import torch
