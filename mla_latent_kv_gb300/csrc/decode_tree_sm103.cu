@@ -27,12 +27,13 @@
 // number of pages, which the host chose before: 20 requests x 256 rows over 8000 to 16,000 tokens 134 -> 101 us, 8 x 1024
 // over up to 32,768 325 -> 272, 5 x 320 over up to 100,000 307 -> 236, 1 x 1024 over 131,072 the same.
 //
-// Measured: 16 requests x 32 drafts x 128 heads over up to 8192 tokens 560 us, 1.56 PFLOP/s (FP8 562 with the
-// widening, 1.70: the clocks go down less), 32 x 8 over up to 4096 150 us, 1.44; 64 x 7 drafts of 16 heads over up
+// Measured: 16 requests x 32 drafts x 128 heads over up to 8192 tokens 550 us, 1.59 PFLOP/s (FP8 553 with the
+// widening, 1.73), 32 x 8 over up to 4096 146 us, 1.47; 64 x 7 drafts of 16 heads over up
 // to 8192 tokens 140 us: less than half of the rows are in use there. A group takes 1.28 us, its 2304 cycles
-// of scores MMAs at the clock that the power leaves; a unit's change 7 us, the first scores 9 after the start.
+// of scores MMAs at the clock that the power leaves; a unit's change 6 us, the first scores 9 after the start.
 // What it took, on the 32 x 8 drafts: one launch a unit 174 us; clusters that stay, longest first 154; first keys
-// beside Q, lengths in shared memory 152; an arrival without a release, no 64-bit divisions 150. FP8 scales from
+// beside Q, lengths in shared memory 152; an arrival without a release, no 64-bit divisions 148; a later unit's Q loaded
+// when the last scores are done, not the last weights, 146 (FP8, 16 x 32: 562 -> 552). FP8 scales from
 // shared memory instead of global, 16 x 32 drafts: 614 -> 564 us.
 //
 // What hides drafts: the pages that hold any (two at most) are masked token by token. Their V rows are looked
@@ -106,17 +107,20 @@ static_assert(kPMsgBytes <= kPBufStride, "P message");
 static_assert(OFF_RING % 1024 == 0 && OFF_STAGE % 1024 == 0 && OFF_PB % 1024 == 0 && kPBufStride % 1024 == 0 &&
                   kSlotBytes % 1024 == 0,
               "128-byte swizzled tiles need 1024-byte alignment");
-static_assert(OFF_V + 12 * dec::kTileBytes <= kSmem1, "epilogue tiles");
-// Q's sixteen latent half panels land in the four staging buffers, a place of their own and the two ring
-// slots that the unit's keys need last, so that its first group loads beside Q.
+static_assert(8 * dec::kTileBytes <= kVStages * kVStageBytes, "epilogue tiles");
+// Q's sixteen latent half panels land where nothing else is. The first unit's: in the four staging buffers, a place of
+// their own and the two ring slots that its keys need last, so that its first group loads beside Q. A later unit's, whose
+// load begins when the last scores of the one before are done: in the two staging buffers that are not those of that
+// group, their own place and all ring slots but the first, so that a third of the first group loads beside it.
 static_assert(kSlots == 5 && kStages == 4 && 3 * kQHalfBytes == kSlotBytes && kPBufStride >= kQPanelBytes, "Q panel homes");
 static_assert(OFF_QX % 1024 == 0, "Q panel homes");
-// `slot0`: the ring slot of the unit's first keys.
-__device__ __forceinline__ uint32_t q_half_off(int h, int slot0) {
-    if (h < 8) return OFF_STAGE + (h >> 1) * kPBufStride + (h & 1) * kQHalfBytes;
-    if (h < 10) return OFF_QX + (h - 8) * kQHalfBytes;
-    const int behind = h < 13 ? 3 : 4;
-    return OFF_RING + (slot0 + behind) % kSlots * kSlotBytes + (h - (h < 13 ? 10 : 13)) * kQHalfBytes;
+__device__ __forceinline__ uint32_t q_half_off(int h, uint32_t g0) {  // g0: groups of the units before
+    const int staged = g0 == 0 ? 8 : 4, slot0 = g0 == 0 ? 3 : (int)(3 * g0 + 1) % kSlots, stage0 = g0 == 0 ? 0 : 2 * (int)(g0 & 1);
+    if (h < staged) return OFF_STAGE + (stage0 + (h >> 1)) * kPBufStride + (h & 1) * kQHalfBytes;
+    h -= staged;
+    if (h < 2) return OFF_QX + h * kQHalfBytes;
+    h -= 2;
+    return OFF_RING + (slot0 + h / 3) % kSlots * kSlotBytes + h % 3 * kQHalfBytes;
 }
 
 // Barrier slots, one layout for all four CTAs (multicast commits land at the same offset in each).
@@ -357,11 +361,11 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 tma_prefetch_desc(&k_map);
                 tma_prefetch_desc(&q_map);
                 bool ok = true;
-                // the K ring's slots and the staging buffers as the groups before g0 left them
-                auto drained = [&]() -> bool {
+                // the K ring's slots and the staging buffers (of the last group too) as the groups before g0 left them
+                auto drained = [&](bool all) -> bool {
                     for (uint32_t m = 3 * g0 > kSlots ? 3 * g0 - kSlots : 0; m < 3 * g0; ++m)
                         if (!wait_bar<true>(bar(B_SLOTEMPTY + (int)(m % kSlots)), (m / kSlots) & 1, abort, ds)) return false;
-                    for (uint32_t g = g0 > 2 ? g0 - 2 : 0; g < g0; ++g)
+                    for (uint32_t g = g0 > 2 ? g0 - 2 : 0; g + !all < g0; ++g)
                         for (int q = 0; q < kPPG; ++q)
                             if (!wait_bar<true>(bar(B_STAGEFREE + 2 * (int)(g & 1) + q), (g >> 1) & 1, abort, ds)) return false;
                     return true;
@@ -370,17 +374,23 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     if (!kept) length(u.req, rank == 0);
                     if (u.npages == 0) continue;
                     int y = page_row(u, side);  // looked up ahead of the waits
-                    if (!(ok = drained())) break;
-                    const int slot0 = (int)(3 * g0 % kSlots);
+                    if (!(ok = drained(false))) break;
                     bar_arrive_expect_tx(bar(B_QFULL), 9 * kQPanelBytes);
-                    for (int h = 0; h < 18; ++h)
-                        tma_load_3d(sbase + (h < 16 ? q_half_off(h, slot0) : OFF_QROPE + (h - 16) * kQHalfBytes), &q_map,
-                                    bar(B_QFULL), (h >> 1) * 64, rows_of(u) + 64 * (h & 1), u.req);
+                    auto load_q = [&](uint32_t groups) {
+#pragma unroll
+                        for (int h = 0; h < 18; ++h)
+                            tma_load_3d(sbase + (h < 16 ? q_half_off(h, groups) : OFF_QROPE + (h - 16) * kQHalfBytes), &q_map,
+                                        bar(B_QFULL), (h >> 1) * 64, rows_of(u) + 64 * (h & 1), u.req);
+                    };
+                    if (g0 == 0)
+                        load_q(0);  // constants
+                    else
+                        load_q(g0);
                     for (int gi = 0; gi < u.ngroups && ok; ++gi) {
                         if (gi > 0) y = page_row(u, kPPG * gi + side);
-                        // behind the first group: Q's panels have been moved out to TMEM
-                        if (gi == 1 && !(ok = wait_bar(bar(B_QREADY), n & 1, abort, ds))) break;
                         for (int t = 0; t < 3; ++t) {
+                            // behind what loads beside Q: its panels have been moved out to TMEM
+                            if (3 * gi + t == (n == 0 ? 3 : 1) && !(ok = wait_bar(bar(B_QREADY), n & 1, abort, ds))) break;
                             const uint32_t m = 3 * (g0 + (uint32_t)gi) + (uint32_t)t;
                             const int slot = (int)(m % kSlots);
                             if (m >= kSlots && !(ok = wait_bar<true>(bar(B_SLOTEMPTY + slot), (m / kSlots - 1) & 1, abort, ds))) break;
@@ -394,7 +404,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 // Teardown: the MMAs have consumed the last slots, so every copy has landed and no commit is
                 // still on its way here.
-                if (!ok || !drained()) settle();
+                if (!ok || !drained(true)) settle();
             }
         } else if (warp == 1) {
             if (lane == 0 && side == 1) {
@@ -467,8 +477,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 bool ok = true;
                 for (int k = 0; ok && unit_of(k, u); ++k) {
                     if (u.npages == 0) continue;
-                    // the buffers hold the unit before's output tiles until it is stored
-                    if (n > 0 && !(ok = wait_bar<true>(bar(B_DONE), (n - 1) & 1, abort, ds))) break;
                     for (uint32_t page = 2 * g0; page < 2 * (g0 + (uint32_t)u.ngroups) && ok; ++page) {
                         const int sbi = (int)(page & 3), pb = (int)(page % kPBufs);
                         ok = wait_bar(bar(B_STAGEFULL + sbi), (page >> 2) & 1, abort, ds) &&
@@ -513,7 +521,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                     const bool okq = warp_wait(bar(B_QFULL), n & 1, abort, ds);
 #pragma unroll 1
                     for (int pn = 2 * quarter; pn < 2 * quarter + 2; ++pn) {
-                        const uint32_t home = q_half_off(2 * pn + (row >> 6), (int)(3 * g0 % kSlots)) + (row & 63) * 128;
+                        const uint32_t home = q_half_off(2 * pn + (row >> 6), g0) + (row & 63) * 128;
                         uint32_t v[32];
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
@@ -677,10 +685,11 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 bool ok = true;
                 for (int k = 0; ok && unit_of(k, u); ++k) {
                     if (u.npages == 0) continue;
+                    int y = page_row(u, 0);  // looked up ahead of the wait
                     // the ring holds the unit before's output tiles until it is stored
                     if (n > 0 && !(ok = wait_bar(bar(B_DONE), (n - 1) & 1, abort, ds))) break;
                     for (int i = 0; i < kPPG * u.ngroups; ++i) {
-                        const int y = page_row(u, i);
+                        if (i > 0) y = page_row(u, i);
                         const uint32_t v = kPPG * g0 + (uint32_t)i;
                         const int st = (int)(v % kVStages);
                         if (v >= kVStages && !(ok = wait_bar<true>(bar(B_VEMPTY + st), (v / kVStages - 1) & 1, abort, ds))) break;
@@ -840,14 +849,14 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 const float inv = empty ? 0.f : 1.f / l;
                 if (eset == 0 && live && lse_out)
                     lse_out[out_row] = empty ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
-                // O / l leaves through TMA stores over the V ring and the P buffers; rows past the request's are
+                // O / l leaves through TMA stores over the V ring; rows past the request's are
                 // cut off by the tensor map
                 const bool store = rows0 < p.flat_rows;
                 if (p.o_bf16 && !u.part)
-                    store_rows<false, 4, 3, kBarEpi, false>(smem, sbase, OFF_V, tmem + lane_base, row, eset, (ctid & 127) == 0, true,
+                    store_rows<false, 4, 2, kBarEpi, false>(smem, sbase, OFF_V, tmem + lane_base, row, eset, (ctid & 127) == 0, true,
                                                      empty, inv, &o_map, rows0, u.slab, store);
                 else
-                    store_rows<true, 4, 3, kBarEpi, false>(smem, sbase, OFF_V, tmem + lane_base, row, eset, (ctid & 127) == 0, true,
+                    store_rows<true, 4, 2, kBarEpi, false>(smem, sbase, OFF_V, tmem + lane_base, row, eset, (ctid & 127) == 0, true,
                                                     empty, inv, u.part ? &part_map : &o_map, u.part ? 128 * side : rows0,
                                                     u.slab, store);
                 // O, the statistics and the tiles have been read: the next unit's may come
