@@ -179,17 +179,18 @@ __device__ __forceinline__ void settle() {
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
 }
 
-// A place in the row of all requests' groups.
+// A place in the row of all groups: group `group` of entry `entry` (request entry % B of round entry / B).
 struct Place {
-    int req, group;
+    int entry, group;
 };
 __device__ __forceinline__ bool before(const Place& a, const Place& b) {
-    return a.req < b.req || (a.req == b.req && a.group < b.group);
+    return a.entry < b.entry || (a.entry == b.entry && a.group < b.group);
 }
 
 // One unit of a cluster's list, or a part of one.
 struct Unit {
-    int req, tile, slab;   // slab: the request, of a part its partial state
+    int entry, req, tile;  // entry: of the row, where units are cut
+    int slab;              // the request, of a part its partial state
     bool part;
     int page0, npages, ngroups;
     int drafts0;           // the request's tokens before its drafts (below 0: the first are not there)
@@ -197,33 +198,42 @@ struct Unit {
 };
 
 // The cuts. The requests stand in a row, each as long as its groups and kUnitGroups for a unit's start and
-// end; the row is cut into equal shares, and a cluster goes through one share for one tile. (Clusters side by
-// side take a share's tiles, and find its pages in L2.) A cut that falls into a unit's fixed part, or leaves a few
-// groups before or behind it, moves to the unit's edge.
+// end; the row is cut into equal shares. `lanes` clusters side by side go through one share for as many tiles (and find
+// its pages in L2); with fewer lanes than tiles the row has a round of all requests for each set of them. A cut that falls
+// into a unit's fixed part, or leaves a few groups before or behind it, moves to the unit's edge.
 __device__ __forceinline__ uint32_t unit_groups(int len) {
     return ((uint32_t)((len + kPage - 1) / kPage) + kPPG - 1) / kPPG;
 }
 __device__ __forceinline__ uint32_t unit_weight(int len) { return len > 0 ? unit_groups(len) + kUnitGroups : 1u; }
 __device__ Place cut_of(const TreeArgs& p, const int* lens, const uint32_t* weights, int share) {
     if (share == 0) return Place{0, 0};
-    if (share == p.shares) return Place{p.B, 0};
-    const uint32_t all = weights[p.B - 1] + unit_weight(lens[p.B - 1]);
+    const uint32_t rounds = (uint32_t)(p.tiles / p.lanes), round = weights[p.B - 1] + unit_weight(lens[p.B - 1]);
+    if (share == p.shares) return Place{p.B * (int)rounds, 0};
+    const uint64_t all = (uint64_t)round * rounds;
     // every share has a start of its own: the first request's is not counted
-    const uint32_t free = min(all - 1, (uint32_t)kUnitGroups);
-    const uint32_t cut = all - free < 1u << 26 ? (all - free) * (uint32_t)share / (uint32_t)p.shares  // 64 shares at most
-                                               : (uint32_t)((uint64_t)(all - free) * (uint32_t)share / (uint32_t)p.shares);
-    const uint32_t at = free + cut;
-    const int edge = (int)min((all - free) / (4u * (uint32_t)p.shares), (uint32_t)kEdgeGroups);
-    int lo = 0, hi = p.B - 1;  // the last request that begins at or before `at`
+    const uint64_t free = min(all - 1, (uint64_t)kUnitGroups), rest = all - free;
+    uint64_t at = free;
+    uint32_t nth;
+    if (all < 1u << 26) {  // 64 shares at most
+        at += (uint32_t)rest * (uint32_t)share / (uint32_t)p.shares;
+        nth = (uint32_t)at / round;
+    } else {
+        at += rest * (uint32_t)share / (uint32_t)p.shares;
+        nth = (uint32_t)(at / round);
+    }
+    const uint32_t in = (uint32_t)(at - (uint64_t)nth * round);
+    const int edge = (int)min((uint32_t)min(rest, (uint64_t)UINT32_MAX) / (4u * (uint32_t)p.shares), (uint32_t)kEdgeGroups);
+    int lo = 0, hi = p.B - 1;  // the last request that begins at or before `in`
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (weights[mid] <= at)
+        if (weights[mid] <= in)
             lo = mid;
         else
             hi = mid - 1;
     }
-    const int groups = (int)unit_groups(lens[lo]), group = (int)(at - weights[lo]) - kUnitGroups;
-    return group <= edge ? Place{lo, 0} : groups - group > edge ? Place{lo, group} : Place{lo + 1, 0};
+    const int groups = (int)unit_groups(lens[lo]), group = (int)(in - weights[lo]) - kUnitGroups;
+    const int entry = (int)nth * p.B + lo;
+    return group <= edge ? Place{entry, 0} : groups - group > edge ? Place{entry, group} : Place{entry + 1, 0};
 }
 
 // kCut: units are cut (see cut_of). Instances of their own: with both in one, FP8's softmax spilled (562 -> 600 us).
@@ -298,7 +308,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             weights[tid] = sum;
         }
         __syncthreads();
-        if (tid < 2) cuts[tid] = cut_of(p, lens, weights, cluster / p.tiles + tid);
+        if (tid < 2) cuts[tid] = cut_of(p, lens, weights, cluster / p.lanes + tid);
     }
     cluster_sync();  // every CTA's barriers (and the order) exist before any remote arrive or copy
     const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM), 0);
@@ -310,21 +320,22 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     auto unit_of = [&](int k, Unit& u) -> bool {
         Place at{};
         if constexpr (kCut) {
-            at = k > 0 ? Place{u.req + 1, 0} : cuts[0];
+            at = k > 0 ? Place{u.entry + 1, 0} : cuts[0];
             if (!before(at, cuts[1])) return false;
-            u.tile = cluster % p.tiles;
+            u.entry = at.entry;
+            u.req = at.entry % p.B;
+            u.tile = at.entry / p.B * p.lanes + cluster % p.lanes;
         } else {
             const uint32_t i = (uint32_t)k * clusters + (uint32_t)(k & 1 ? clusters - 1 - cluster : cluster);
             if (i >= (uint32_t)p.units) return false;
-            at.req = (int)(i / (uint32_t)p.tiles);
-            u.tile = (int)(i - (uint32_t)at.req * (uint32_t)p.tiles);
-            if (sorted) at.req = (int)reinterpret_cast<const uint16_t*>(smem + OFF_ORDER)[at.req];
+            u.req = (int)(i / (uint32_t)p.tiles);
+            u.tile = (int)(i - (uint32_t)u.req * (uint32_t)p.tiles);
+            if (sorted) u.req = (int)reinterpret_cast<const uint16_t*>(smem + OFF_ORDER)[u.req];
         }
-        u.req = at.req;
         const int seq = kept ? lens[u.req] : length(u.req), pages = (seq + kPage - 1) / kPage;
         u.page0 = kPPG * at.group;
         int end = pages;
-        if (kCut && cuts[1].req == u.req) end = min(pages, kPPG * cuts[1].group);
+        if (kCut && cuts[1].entry == u.entry) end = min(pages, kPPG * cuts[1].group);
         u.npages = end - u.page0;
         u.part = kCut && u.npages < pages;
         u.slab = u.part ? 2 * cluster + (at.group == 0) : u.req;
@@ -875,12 +886,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             if (lane == 0) {
                 const Place from = cuts[0];
                 int share = -1;
-                if (from.group > 0 && cuts[1].req > from.req) {
+                if (from.group > 0 && cuts[1].entry > from.entry) {
                     const uint32_t* weights = reinterpret_cast<const uint32_t*>(smem + OFF_BEFORE);
-                    share = cluster / p.tiles - 1;
-                    while (before(Place{from.req, 0}, cut_of(p, lens, weights, share))) --share;
+                    share = cluster / p.lanes - 1;
+                    while (before(Place{from.entry, 0}, cut_of(p, lens, weights, share))) --share;
                 }
-                p.pieces[cluster] = make_int2(from.req, share);
+                p.pieces[cluster] = make_int2(from.entry, share);
             }
         } else if (!kScaled && side == 0 && lane == 0 && p.tiles == 1) {
             // Warp 18: the pages that the rings have no room for yet are brought into L2, the next unit's first ones
@@ -965,9 +976,9 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArg
     griddep_launch_dependents();
     griddep_wait();
     static_assert(kTreeMaxClusters == 64, "two a lane");
-    __shared__ int3 units_s[kTreeMaxClusters];  // (request, its first share, cluster of its last one)
+    __shared__ int3 units_s[kTreeMaxClusters];  // (entry, its first share, cluster of its last one)
     __shared__ int n_s;
-    const int tid = threadIdx.x, lane = tid & 31, clusters = p.shares * p.tiles;
+    const int tid = threadIdx.x, lane = tid & 31, clusters = p.shares * p.lanes;
     if (tid < 32) {
         int found = 0;
         int2 u[2];
@@ -985,11 +996,12 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArg
     const int chunks = (p.slab_rows + kMergeRows - 1) / kMergeRows, tasks = n_s * chunks, dim = (tid & 63) * 8;
     for (int task = (int)blockIdx.x; task < tasks; task += (int)gridDim.x) {
         const int3 unit = units_s[task / chunks];
-        const int row = task % chunks * kMergeRows + (tid >> 6), tile = unit.z % p.tiles, flat = tile * kTileRows + row;
+        const int row = task % chunks * kMergeRows + (tid >> 6), side = unit.z % p.lanes;
+        const int flat = (unit.x / p.B * p.lanes + side) * kTileRows + row;
         if (flat >= p.flat_rows) continue;
         // the unit's first part is its share's last one, the others their shares' first
-        const int n = unit.z / p.tiles - unit.y + 1;
-        auto slab_of = [&](int i) -> size_t { return 2 * (size_t)((unit.y + i) * p.tiles + tile) + (i == 0); };
+        const int n = unit.z / p.lanes - unit.y + 1;
+        auto slab_of = [&](int i) -> size_t { return 2 * (size_t)((unit.y + i) * p.lanes + side) + (i == 0); };
         float4 v[kMergeBatch][2];
         float x[kMergeBatch];
         auto load = [&](int i0) {
@@ -1032,7 +1044,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArg
             }
         }
         const float inv = M == -CUDART_INF_F ? 0.f : 1.f / sum;
-        const size_t out = (size_t)unit.x * p.flat_rows + flat;
+        const size_t out = (size_t)(unit.x % p.B) * p.flat_rows + flat;
         if ((tid & 63) == 0 && p.lse) p.lse[out] = M == -CUDART_INF_F ? M : M + logf(sum);
         if (p.o_bf16) {
             *reinterpret_cast<uint4*>((uint16_t*)p.o + out * kL + dim) =
@@ -1085,24 +1097,35 @@ int tree_clusters() {
     return n;
 }
 
-int tree_shares(int B, int tiles, int slab_rows, int pages, int clusters) {
+int tree_shares(int B, int tiles, int slab_rows, int pages, int clusters, int* lanes) {
     // Times in groups (1.28 us), of requests half to all as long as the longest. Whole units: the balanced time, and
     // the rest of the last turn.
     if (B < 1 || B > kTreeMaxCut || pages < 2 * kPPG) return 0;
     const double longest = (pages + kPPG - 1) / kPPG, usual = 0.75 * longest, units = (double)B * tiles;
     const double turns = std::ceil(units / clusters), even = units / clusters * (usual + kUnitGroups);
-    const double whole = turns == 1 ? longest + kUnitGroups : even + 0.4 * (turns - units / clusters) * (longest + kUnitGroups);
+    double best = turns == 1 ? longest + kUnitGroups : even + 0.4 * (turns - units / clusters) * (longest + kUnitGroups);
     // Cut: a request of few groups into fewer parts. One more takes G / n^2 of its G groups off each of n, and costs a
     // third of a group of the merge's time, or its rows written and read (5 TB/s).
-    const double most = std::floor((double)clusters / tiles);
     const double parts = std::min(std::sqrt(units * longest * 1562.0 / slab_rows) / units, 1.7 * std::sqrt(longest));
     const double part = std::max(1.0, std::ceil(longest / parts));
-    const double shares = std::min(most, std::max((double)B, std::ceil((B * (longest + kUnitGroups) - kUnitGroups) / part)));
-    if (shares < 2) return 0;
-    // beside a share of the groups: a start of its own, the merge's launch, and the partial rows written and read
-    const double merge = 2.0 + 12.0 / 36 / kTileRows * shares * tiles * slab_rows;
-    const double cut = B * (usual + kUnitGroups) / shares + kUnitGroups + merge;
-    return cut < whole ? (int)shares : 0;
+    int found = 0;
+    for (int n = 1; n <= tiles && n <= clusters; ++n) {
+        if (tiles % n) continue;
+        const double requests = (double)B * (tiles / n);
+        const double shares = std::min(std::floor((double)clusters / n),
+                                       std::max(requests, std::ceil((requests * (longest + kUnitGroups) - kUnitGroups) / part)));
+        if (shares < 2) continue;
+        // beside a share of the groups: a start of its own, the merge's launch, and the partial rows written and read;
+        // tiles that do not go through a share side by side find less of it in L2 (1 lane for 4 tiles: 10%)
+        const double merge = 2.0 + 12.0 / 36 / kTileRows * shares * n * slab_rows;
+        const double cut = requests * (usual + kUnitGroups) / shares * (1.0 + 0.05 * std::log2((double)tiles / n)) + kUnitGroups + merge;
+        if (cut < best) {
+            best = cut;
+            found = (int)shares;
+            *lanes = n;
+        }
+    }
+    return found;
 }
 
 cudaError_t launch_decode_tree(const TreeArgs& in, const uint8_t* cache, uint16_t* widened, float* scales, cudaStream_t s) {
@@ -1164,14 +1187,14 @@ cudaError_t launch_decode_tree(const TreeArgs& in, const uint8_t* cache, uint16_
         if (e != cudaSuccess) return e;
     }
     if (a.pieces) {
-        const uint64_t dims[3] = {(uint64_t)kL, (uint64_t)a.slab_rows, 2 * (uint64_t)a.shares * a.tiles};
+        const uint64_t dims[3] = {(uint64_t)kL, (uint64_t)a.slab_rows, 2 * (uint64_t)a.shares * a.lanes};
         const uint64_t strides[2] = {(uint64_t)kL * 4, (uint64_t)a.slab_rows * kL * 4};
         const uint32_t box[3] = {32u, 128, 1};
         e = encode_tmap(&part_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, a.part_o, dims, strides, box, true);
         if (e != cudaSuccess) return e;
     }
     a.units = (int64_t)a.B * a.tiles;
-    const int64_t used = a.pieces ? (int64_t)a.shares * a.tiles : std::min<int64_t>(a.units, clusters);
+    const int64_t used = a.pieces ? (int64_t)a.shares * a.lanes : std::min<int64_t>(a.units, clusters);
     e = launch_pdl(kKernels[fp8][a.pieces != nullptr], dim3(4u * (unsigned)used), dim3(kThreads), kSmemBytes, s, k_map, v_map,
                    q_map, o_map, part_map, a);
     if (e != cudaSuccess || !a.pieces) return e;

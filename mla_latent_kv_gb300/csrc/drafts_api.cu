@@ -71,7 +71,7 @@ mla_status rope_args(const char* who, const void* x, int64_t x_t, int64_t x_n, c
 // 128 requests of up to 1000 tokens, 128 pairs, bf16 80 and 66, FP8 74 and 107.
 struct TreePlan {
     bool rows;
-    int splits, tiles, shares, slab_rows, wide_pages;  // shares: that the requests are cut into, or 0
+    int splits, tiles, shares, lanes, slab_rows, wide_pages;  // shares: that the requests are cut into, or 0
     size_t scales, part_o, part_lse, pieces, total;
 };
 bool plan_tree(mla_kv_dtype kv, int B, int Sq, int H, int max_seq_len, TreePlan* w) {
@@ -93,7 +93,7 @@ bool plan_tree(mla_kv_dtype kv, int B, int Sq, int H, int max_seq_len, TreePlan*
     if (clusters < 1) return false;
     w->tiles = (int)((flat + 255) / 256);
     w->slab_rows = (int)std::min<int64_t>(flat, 256);
-    w->shares = mla::tree_shares(B, w->tiles, w->slab_rows, pages, clusters);
+    w->shares = mla::tree_shares(B, w->tiles, w->slab_rows, pages, clusters, &w->lanes);
     size_t off = 0;
     if (kv == MLA_KV_FP8_E4M3_SCALED) {
         w->wide_pages = pages;
@@ -103,7 +103,7 @@ bool plan_tree(mla_kv_dtype kv, int B, int Sq, int H, int max_seq_len, TreePlan*
         off += up256(rows * 2 * sizeof(float));
     }
     if (w->shares > 0) {
-        const size_t slabs = (size_t)2 * w->shares * w->tiles;
+        const size_t slabs = (size_t)2 * w->shares * w->lanes;
         w->part_o = off;
         off += up256(slabs * w->slab_rows * mla::kL * sizeof(float));
         w->part_lse = off;
@@ -289,6 +289,7 @@ mla_status mla_decode_tree(const void* q, const void* kv_cache, mla_kv_dtype kv_
     a.o_bf16 = o_dtype == MLA_DT_BF16;
     if (w.shares > 0) {
         a.shares = w.shares;
+        a.lanes = w.lanes;
         a.slab_rows = w.slab_rows;
         a.part_o = (float*)(ws + w.part_o);
         a.part_lse = (float*)(ws + w.part_lse);

@@ -377,7 +377,7 @@ struct TreeArgs {
     const uint64_t* masks;      // [B, Sq]
     float scale;
     int64_t units;              // B * tiles
-    int shares;                 // of cut units, shares * tiles clusters run
+    int shares, lanes;          // of cut units: shares * lanes clusters run, lanes divides tiles
     const uint8_t* keys;        // the bf16 rows behind the keys' tensor map, and their number
     int key_rows;
     int wide_pages;             // FP8: pages of each request's widened rows, [B, wide_pages, 64]
@@ -385,8 +385,8 @@ struct TreeArgs {
     const float* v_scales;
     void* o;                    // [B, flat_rows, 512], fp32 or bf16
     float* lse;                 // [B, flat_rows] or null
-    int2* pieces;               // [clusters] (request, share) of the cut unit that ends in the cluster's share (share
-                                // -1: none), and where it begins; null: units are not cut
+    int2* pieces;               // [clusters] (entry, share) of the cut unit that ends in the cluster's share and the share
+                                // in which it begins (-1: none ends there); null: units are not cut
     float* part_o;              // fp32 [2 clusters, slab_rows, 512]
     float* part_lse;            // [2 clusters, 256]
     int slab_rows;              // min(flat_rows, 256)
@@ -394,8 +394,8 @@ struct TreeArgs {
     int32_t* dev_status;        // or null
 };
 int tree_clusters();  // clusters of the tree kernel that run at once on the current device, or -1
-// Shares into which the requests are cut (of `clusters` / tiles that can run at once), or 0: they are not.
-int tree_shares(int B, int tiles, int slab_rows, int pages, int clusters);
+// Shares into which the requests are cut for `lanes` tiles at once, or 0: they are not.
+int tree_shares(int B, int tiles, int slab_rows, int pages, int clusters, int* lanes);
 // FP8: the requests' rows are first widened to `widened` [B, wide_pages, 64, 576], their scales to `scales`
 // [2, B, wide_pages, 64].
 cudaError_t launch_decode_tree(const TreeArgs& a, const uint8_t* cache, uint16_t* widened, float* scales, cudaStream_t s);

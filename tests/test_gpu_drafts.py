@@ -239,6 +239,9 @@ def test_decode_tree_splits(B, Sq, H, length, max_len, kv):
     ([300 + 97 * b for b in range(24)], 2, 120, 16000),              # far fewer tokens than the bound allows
     ([2000, 1500, 1700, 1999], 10, 128, 2000),                       # too little to be cut among seven clusters a tile
     ([9000, 1500], 10, 128, 9000),                                   # five tiles: 35 clusters
+    ([9000], 20, 128, 9000),                                         # ten tiles, five at a time
+    ([6000, 3001], 26, 128, 6000),                                   # thirteen, enough clusters for whole units
+    ([20000], 26, 128, 20000),                                       # one at a time
     ([64 * (1 + b % 3) - b % 2 for b in range(112)], 2, 17, 30000),  # as many requests as are cut
     ([64 * (1 + b % 3) - b % 2 for b in range(113)], 2, 17, 30000),  # one more: whole units
 ])
@@ -256,7 +259,7 @@ def test_decode_tree_cut_requests(lens, Sq, H, max_len, kv):
     check_attention(*_tree(c, max_len=max_len, o_dtype=mla.DT_BF16), want, bf16_out=True)
     assert st.item() == 0
     if Sq * H > 32:  # partial states: the requests were cut
-        assert (mla.decode_tree_workspace_bytes(len(lens), Sq, H, max_len, BF) > 0) == (len(lens) <= 112 and lens[0] != 2000)
+        assert (mla.decode_tree_workspace_bytes(len(lens), Sq, H, max_len, BF) > 0) == (len(lens) <= 112 and lens[0] not in (2000, 6000))
 
 
 @pytest.mark.parametrize("kv", [BF, F8])
