@@ -337,6 +337,56 @@ def test_decode_tree_nan_reaches_only_its_own_branch(H, kv):
                 check_attention(o[b:b + 1, t:t + 1], lse[b:b + 1, t:t + 1], part)
 
 
+def test_decode_tree_cut_requests_with_nan():
+    """A NaN token in one part of a request is all of its rows' result, and nobody else's."""
+    c = tree_case([9000, 6000, 7001], 3, 60, BF, seed=21)
+    _fill_rows(c, [_row(c, 1, 2500)])
+    check_with_nan(*_tree(c), attend_tree(c))
+
+
+@pytest.mark.parametrize("kv", [BF, F8])
+def test_decode_tree_cut_requests_report_bad_blocks_and_lengths(kv):
+    import mla_latent_kv_gb300 as mla
+    c = tree_case([9000, 6000, 7001], 3, 60, kv, 22)
+    want = attend_tree(c)
+    table, st = c["table"].clone(), _status()
+    table[1, 40] = c["num_blocks"]
+    o, lse = _tree(dict(c, table=table), status=st)
+    assert st.item() == mla.DEV_BAD_BLOCK_ID
+    for b in (0, 2):
+        check_attention(o[b:b + 1], lse[b:b + 1], [x[b:b + 1] for x in want])
+    for n in (9001, -1):  # as the bound, as no token
+        st, lens = _status(), c["seq_lens"].clone()
+        lens[0] = n
+        o, lse = _tree(dict(c, seq_lens=lens), status=st)
+        assert st.item() == mla.DEV_SEQ_TOO_LONG
+        check_attention(o[1:], lse[1:], [x[1:] for x in want])
+
+
+@pytest.mark.parametrize("kv", [BF, F8])
+def test_decode_tree_cut_requests_share_a_workspace(kv):
+    """Calls one behind the other in one workspace, and two at once on two streams in their own."""
+    import torch
+
+    import mla_latent_kv_gb300 as mla
+    cs = [tree_case(lens, 2, 100, kv, 30 + i) for i, lens in enumerate([[9000, 50, 4000], [300, 9000, 8000]])]
+    wants = [attend_tree(c) for c in cs]
+    size = mla.decode_tree_workspace_bytes(3, 2, 100, 9000, kv)
+    ws = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    results = [_tree(cs[i % 2], max_len=9000, workspace=ws[0]) for i in range(6)]
+    for i, r in enumerate(results):
+        check_attention(*r, wants[i % 2])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [(torch.empty((3, 2, 100, L), device="cuda"), torch.empty((3, 2, 100), device="cuda")) for _ in range(2)]
+    for _ in range(4):
+        for i in range(2):
+            _tree(cs[i], max_len=9000, workspace=ws[i], o_latent=outs[i][0], lse=outs[i][1], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        check_attention(*outs[i], wants[i])
+
+
 @pytest.mark.parametrize("H", [5, 16, 128])
 def test_decode_tree_nan_in_the_context(H):
     c = tree_case([200, 100], 3, H, BF, 10)
