@@ -81,9 +81,11 @@ bool plan_tree(mla_kv_dtype kv, int B, int Sq, int H, int max_seq_len, TreePlan*
     if (w->rows) {
         const bool few = mla::few_heads((int)flat);
         // Over an FP8 cache with more than 32 pairs: short requests one unit each where there are more of them than SM
-        // pairs (128 of up to 1000 tokens 74 us, by the schedule built on the device 85), long ones by the schedule
-        // (64 of up to 8192 212 us, one unit each 222; 40 of them 145, three units each 157).
-        const int splits = few ? -1 : pages <= 32 && B > 76 ? 1 : pages >= 128 && B >= 4 ? -2 : -1;
+        // pairs (128 of up to 1000 tokens 74 us, by the schedule built on the device 85); much work by the schedule
+        // (64 of up to 8192 tokens 223 us, ranges of a fixed length 233; 30 of up to 6000 91 and 102; 40 of up to 20,000 288
+        // and 327), little by ranges, which need no plan (5 of up to 12,000 42 us, by the schedule 60).
+        const bool much = pages >= 90 && B >= 4 && (int64_t)B * pages > 2500;
+        const int splits = few ? -1 : pages <= 32 && B > 76 ? 1 : much ? -2 : -1;
         w->splits = mla::resolve_splits(few, splits, B, (int)flat, max_seq_len);
         if (w->splits < 1 && w->splits != -2) return false;
         w->total = mla::workspace_layout(kv, B, B, (int)flat, w->splits, max_seq_len).total;
