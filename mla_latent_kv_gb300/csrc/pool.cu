@@ -323,7 +323,8 @@ __global__ void __launch_bounds__(kForkThreads) fork_apply_kernel(const ForkArgs
             int32_t page = -1;
             if (keep) page = from[j];
             if (take) page = p.fresh[at];
-            if ((take || (keep && !heir)) && in_pool(page)) atomicAdd(p.new_refs + page, 1);
+            // the heir's kept pages were looked at by nobody else: reported here, and counted already
+            if ((take || keep) && in_pool(page) && !(keep && heir)) atomicAdd(p.new_refs + page, 1);
             to[j] = page;
         }
         if (tid == 0) {

@@ -1,0 +1,47 @@
+"""Calls of a step with drafted tokens that lie at the edge of what their documentation allows, on the GPU."""
+import numpy as np
+import pytest
+
+import mla_inputs as mi
+from longctx_util import PAGE, dev
+
+pytestmark = pytest.mark.gpu
+BF, F8 = mi.KV_BF16, mi.KV_FP8
+
+
+def _status():
+    import torch
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+# ---------------------------------------------------------------------------------------- page pool
+@pytest.mark.parametrize("parents", [[0], [0, -1], [-1, 0], [0, 1], [1, 0], [0, 0], [1]])
+@pytest.mark.parametrize("page", [0, 2, 3])
+@pytest.mark.parametrize("bad", [30, -5, 2 ** 31 - 1])
+def test_fork_pages_reports_every_bad_entry(parents, page, bad):
+    """A row's entry outside the cache is reported whoever goes on from the row: its first child alone too, and
+    in a page full of tokens too."""
+    import mla_latent_kv_gb300 as mla
+    table = np.array([[3, 4, 5, 6, -1], [9, -1, -1, -1, -1]], np.int32)
+    table[0, page] = bad
+    counts, lens = np.array([4, 1], np.int32), np.array([200, 10], np.int32)
+    refs = np.zeros(30, np.int32)
+    refs[[p for p in table.ravel() if 0 <= p < 30]] = 1
+    host = np.random.default_rng(0).integers(0, 256, (30, PAGE * 1152), dtype=np.uint8)
+    cache, st = dev(host), _status()
+    room = [int(lens[p]) if p >= 0 else 0 for p in parents]
+    got = mla.fork_pages(cache, dev(table), dev(counts), dev(lens), dev(refs), dev(np.array(parents, np.int32)),
+                         dev(np.array(room, np.int32)), dev_status=st)
+    assert st.item() == mla.DEV_BAD_BLOCK_ID
+    new, new_counts, new_lens, new_refs = [x.cpu().numpy() for x in got]
+    assert new_counts.tolist() == [-(-n // PAGE) for n in room] and new_lens.tolist() == room
+    want = np.zeros(30, np.int32)
+    for r, p in enumerate(parents):
+        for j in range(new_counts[r]):
+            if j < lens[p] // PAGE:
+                assert new[r, j] == table[p, j]  # passed on
+            if 0 <= new[r, j] < 30:
+                want[new[r, j]] += 1
+    assert np.array_equal(new_refs, want)        # and not counted
+    before = np.flatnonzero(refs)
+    assert np.array_equal(cache.cpu().numpy()[before], host[before])
