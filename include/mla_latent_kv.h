@@ -467,9 +467,9 @@ mla_status mla_rope_frequencies(double base, double factor, int trained, double 
 /*
  * mla_rope: every pair (u, v) of token t's rope parts turns by its position m = positions[t],
  *     (u, v) -> mscale (u cos(m w_i) - v sin(m w_i),  v cos(m w_i) + u sin(m w_i)),   w_i = inv_freq[i]
- * with fp32 arithmetic and one rounding to bf16. Angles are kept as exact fractions of a turn whatever the
- * position (w_i as a multiple of 2^-64 turns), positions may be negative: those turn back, which for
- * mscale = 1 is the inverse and the gradient.
+ * with fp32 arithmetic and one rounding to bf16. Angles are kept as fractions of a turn, off by less than 2^-31 of
+ * one whatever the position (w_i rounded to a multiple of 2^-64 turns; the angle's leading 32 bits are used, as
+ * fp32). Positions may be negative: those turn back, which for mscale = 1 is the inverse and the gradient.
  *   x          bf16 [T, N, 64], element (t, n, r) at x[t * x_stride_t + n * x_stride_n + r]: a part of a longer
  *              head row where the strides say so (q of mla_prefill, k_pe with N = 1)
  *   adjacent   1: pair i is (x[2 i], x[2 i + 1]);  0: (x[i], x[i + 32])

@@ -22,6 +22,19 @@ mla_status cuda_error(cudaError_t e, const char* who) {
 }
 
 // ------------------------------------------------------------------------------------ positions
+// w / 2 pi, modulo whole turns, in units of 2^-64: rounded once. A double's quotient alone is off by 2^-56 of a turn
+// for the fast pairs, 2^-25 after 2^31 positions, so that the product with 1 / 2 pi is taken in two doubles.
+uint64_t step_of(double w) {
+    constexpr double kHigh = 0x1.45f306dc9c883p-3, kLow = -0x1.6b01ec5417056p-57;  // 1 / 2 pi
+    const double high = std::fma(w, kHigh, 0.0);  // (as an fma: not to be contracted with the difference below)
+    const double low = std::fma(w, kLow, std::fma(w, kHigh, -high));
+    // without their whole turns, which leaves no error, in units of 2^-64: 2^63 at most
+    const double a = (high - std::nearbyint(high)) * 0x1p64, b = (low - std::nearbyint(low)) * 0x1p64;
+    auto integer = [](double x) { return x < 0 ? -(uint64_t)(-x) : (uint64_t)x; };
+    const double whole = std::nearbyint(a);
+    return integer(whole) + integer(std::nearbyint(b + (a - whole)));
+}
+
 // The checks and arguments that the two rotary calls share; x == null: no heads.
 mla_status rope_args(const char* who, const void* x, int64_t x_t, int64_t x_n, const int32_t* positions,
                      const double* inv_freq, float mscale, int adjacent, void* out, int64_t out_t, int64_t out_n, int T,
@@ -31,11 +44,8 @@ mla_status rope_args(const char* who, const void* x, int64_t x_t, int64_t x_n, c
     if (adjacent != 0 && adjacent != 1) return set_error(MLA_ERR_INVALID_ARG, "%s: adjacent=%d", who, adjacent);
     if (!std::isfinite(mscale)) return set_error(MLA_ERR_INVALID_ARG, "%s: mscale is not finite", who);
     for (int i = 0; i < mla::kPairs; ++i) {
-        // turns per position, modulo whole turns, in units of 2^-64
         if (!std::isfinite(inv_freq[i])) return set_error(MLA_ERR_INVALID_ARG, "%s: inv_freq[%d] is not finite", who, i);
-        const double turns = inv_freq[i] / 6.283185307179586476925286766559;
-        const double frac = turns - std::floor(turns);
-        a->step[i] = frac < 1.0 ? (uint64_t)(frac * 18446744073709551616.0) : 0;
+        a->step[i] = step_of(inv_freq[i]);
     }
     if (T == 0) return MLA_OK;
     if (!positions) return set_error(MLA_ERR_INVALID_ARG, "%s: null pointer", who);

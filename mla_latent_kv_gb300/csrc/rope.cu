@@ -3,8 +3,8 @@
 // A rope part's 64 values are 32 pairs; pair i of a token at position m turns by m * w_i:
 //     u' = mscale (u cos(m w_i) - v sin(m w_i)),   v' = mscale (v cos(m w_i) + u sin(m w_i))
 // The angle is only needed modulo a turn, so the host gives each pair's step w_i / 2 pi as a fraction of
-// 2^64 and the product m * step, which wraps at 2^64, is the turn's fraction: exact for any position but
-// for the step's own rounding (2^-33 of a turn at 2^31 tokens). Its leading bits go to sincospi in fp32.
+// 2^64, rounded once, and the product m * step, which wraps at 2^64, is the turn's fraction: exact for any position
+// but for the step's rounding (2^-34 of a turn at 2^31 tokens). Its leading 32 bits go to sincospi in fp32.
 // (In fp32, m * w_i alone is off by 0.004 rad at 131072 tokens.)
 //
 // Queries: one warp per 32 heads of a token (8 or 16 where there are few). Each lane computes one pair's cosine

@@ -1,4 +1,7 @@
 """Calls of a step with drafted tokens that lie at the edge of what their documentation allows, on the GPU."""
+import math
+from fractions import Fraction
+
 import numpy as np
 import pytest
 
@@ -7,6 +10,8 @@ from longctx_util import PAGE, dev
 
 pytestmark = pytest.mark.gpu
 BF, F8 = mi.KV_BF16, mi.KV_FP8
+R = 64
+TWO_PI = Fraction(62831853071795864769252867665590057684, 10 ** 37)
 
 
 def _status():
@@ -45,3 +50,34 @@ def test_fork_pages_reports_every_bad_entry(parents, page, bad):
     assert np.array_equal(new_refs, want)        # and not counted
     before = np.flatnonzero(refs)
     assert np.array_equal(cache.cpu().numpy()[before], host[before])
+
+
+# -------------------------------------------------------------------------------- rotary positions
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("base", [10000.0, 500000.0])
+def test_rope_small_angles_at_far_positions(base, sign):
+    """Positions near 2^31 that end within a few millionths of a whole turn: the sine has the angle's own relative
+    accuracy in bf16, so that it shows the angle's absolute error.
+
+    A pair's step is off by half of 2^-64 of a turn, 2^-34 turns after 2^31 positions, and the angle's leading 32 bits
+    leave out less than 2^-32: together under 2^-31 turns, 2^-28.3 rad. Then sincospi and the products in fp32,
+    2^-20 relative with room, and one rounding to bf16, 2^-8."""
+    import torch
+
+    import mla_latent_kv_gb300 as mla
+    freq = mla.rope_frequencies(base)
+    top = np.arange(2 ** 31 - 2 ** 22, 2 ** 31 - 1, dtype=np.uint64)
+    positions = []
+    for w in freq.tolist():
+        step = np.uint64(round(Fraction(w) / TWO_PI * 2 ** 64) % 2 ** 64)
+        off = (top * step).view(np.int64)
+        size = np.abs(off.astype(np.float64))
+        positions.append(sign * int(top[np.argmin(np.where(size > 2.0 ** 41, size, np.inf))]))
+    x = np.zeros((32, 1, R), np.float32)
+    x[..., 0::2] = 1.0
+    got = mla.rope(torch.from_numpy(x).to(torch.bfloat16).cuda(), dev(np.array(positions, np.int32)), freq).double().cpu()
+    for i, (m, w) in enumerate(zip(positions, freq.tolist())):
+        turn = Fraction(w) * m / TWO_PI
+        want = math.sin(float((turn - round(turn)) * TWO_PI))
+        assert abs(want) < 0.02
+        assert abs(got[i, 0, 2 * i + 1].item() - want) <= (2.0 ** -8 + 2.0 ** -20) * abs(want) + 2.0 ** -28.3, (i, m)
