@@ -1128,9 +1128,9 @@ int tree_shares(int B, int tiles, int slab_rows, int pages, int clusters, int* l
     return found;
 }
 
-cudaError_t launch_decode_tree(const TreeArgs& in, const uint8_t* cache, uint16_t* widened, float* scales, cudaStream_t s) {
+cudaError_t launch_decode_tree(const TreeArgs& in, bool fp8, const uint8_t* cache, uint16_t* widened, float* scales,
+                               cudaStream_t s) {
     TreeArgs a = in;
-    const bool fp8 = widened != nullptr;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -1138,9 +1138,10 @@ cudaError_t launch_decode_tree(const TreeArgs& in, const uint8_t* cache, uint16_
     if (e != cudaSuccess) return e;
     const int clusters = tree_clusters();
     if (clusters < 1) return cudaErrorUnknown;
-    uint64_t rows = (uint64_t)a.num_blocks * kPage;
+    // with a bound of 0 no request has a page, and cache, table and workspace may be null
+    uint64_t rows = a.max_seq_len > 0 ? (uint64_t)a.num_blocks * kPage : 0;
     if (fp8) {
-        rows = (uint64_t)a.B * a.wide_pages * kPage;
+        rows = a.max_seq_len > 0 ? (uint64_t)a.B * a.wide_pages * kPage : 0;
         a.k_scales = scales;
         a.v_scales = scales + rows;
         if (rows > 0) {
@@ -1157,7 +1158,7 @@ cudaError_t launch_decode_tree(const TreeArgs& in, const uint8_t* cache, uint16_
     memset(&q_map, 0, sizeof q_map);
     memset(&o_map, 0, sizeof o_map);
     memset(&part_map, 0, sizeof part_map);
-    if (rows > 0) {  // else no request has a page
+    if (rows > 0) {
         // the rows as [panel of 64 dims][row][64]: one box is several panels of a page
         const void* base = fp8 ? (const void*)widened : cache;
         const uint64_t dims[3] = {64, rows, (uint64_t)(kD / 64)};

@@ -309,7 +309,8 @@ mla_status mla_decode_tree(const void* q, const void* kv_cache, mla_kv_dtype kv_
     }
     a.dev_status = dev_status;
     cudaStream_t s = (cudaStream_t)stream;
-    cudaError_t e = mla::launch_decode_tree(a, (const uint8_t*)kv_cache, fp8 ? (uint16_t*)ws : nullptr, (float*)(ws + w.scales), s);
+    const cudaError_t e = mla::launch_decode_tree(a, fp8, (const uint8_t*)kv_cache, fp8 ? (uint16_t*)ws : nullptr,
+                                                  fp8 ? (float*)(ws + w.scales) : nullptr, s);
     return e == cudaSuccess ? mla::set_ok() : cuda_error(e, who);
 }
 

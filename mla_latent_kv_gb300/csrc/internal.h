@@ -398,7 +398,8 @@ int tree_clusters();  // clusters of the tree kernel that run at once on the cur
 int tree_shares(int B, int tiles, int slab_rows, int pages, int clusters, int* lanes);
 // FP8: the requests' rows are first widened to `widened` [B, wide_pages, 64, 576], their scales to `scales`
 // [2, B, wide_pages, 64].
-cudaError_t launch_decode_tree(const TreeArgs& a, const uint8_t* cache, uint16_t* widened, float* scales, cudaStream_t s);
+cudaError_t launch_decode_tree(const TreeArgs& a, bool fp8, const uint8_t* cache, uint16_t* widened, float* scales,
+                               cudaStream_t s);
 
 int device_sm_count();  // of the current device, or -1
 

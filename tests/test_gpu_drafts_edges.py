@@ -81,3 +81,32 @@ def test_rope_small_angles_at_far_positions(base, sign):
         want = math.sin(float((turn - round(turn)) * TWO_PI))
         assert abs(want) < 0.02
         assert abs(got[i, 0, 2 * i + 1].item() - want) <= (2.0 ** -8 + 2.0 ** -20) * abs(want) + 2.0 ** -28.3, (i, m)
+
+
+# ------------------------------------------------------------------------------------------ trees
+@pytest.mark.parametrize("kv", [BF, F8])
+@pytest.mark.parametrize("Sq,H", [(1, 1), (2, 16), (3, 11), (2, 64), (3, 43), (4, 128)])  # either side of 32 and 128 pairs
+@pytest.mark.parametrize("B", [1, 90])
+def test_decode_tree_with_a_bound_of_zero_needs_no_cache(B, Sq, H, kv):
+    """Every row is an empty one, as in mla_decode, and a positive length is reported; the cache, the table and the
+    workspace may be null though the cache is said to have blocks."""
+    import torch
+
+    import mla_latent_kv_gb300 as mla
+    lib = mla.lib()
+    q = torch.ones((B, Sq, H, 576), dtype=torch.bfloat16, device="cuda")
+    masks = torch.full((B, Sq), -1, dtype=torch.int64, device="cuda")
+    need = mla.decode_tree_workspace_bytes(B, Sq, H, 0, kv)
+    ws = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+    for length in (0, 5):
+        lens = torch.full((B,), length, dtype=torch.int32, device="cuda")
+        for max_blocks in (0, 4):
+            o = torch.full((B, Sq, H, 512), 7.0, device="cuda")
+            lse, st = torch.full((B, Sq, H), 7.0, device="cuda"), _status()
+            p = lambda t: t.data_ptr()  # noqa: E731
+            rc = lib.mla_decode_tree(p(q), None, kv, 8, None, max_blocks, p(lens), p(masks), 0, B, Sq, H, 0.07,
+                                     p(ws) if need else None, need, p(o), mla.DT_F32, p(lse), p(st),
+                                     torch.cuda.current_stream().cuda_stream)
+            assert rc == mla.OK, lib.mla_last_error_detail()
+            assert bool((o == 0).all()) and bool((lse == -math.inf).all())
+            assert st.item() == (mla.DEV_SEQ_TOO_LONG if length else 0)
