@@ -207,7 +207,9 @@ mla_status mla_rope_cache_write(const void* kv_c, int64_t kv_c_stride_t, const v
     const char* who = "mla_rope_cache_write";
     if (!known_kv(kv_dtype)) return set_error(MLA_ERR_INVALID_ARG, "%s: unknown kv_dtype %d", who, (int)kv_dtype);
     if (num_blocks < 0) return set_error(MLA_ERR_INVALID_ARG, "%s: negative num_blocks", who);
-    if (!std::isfinite(kv_scale)) return set_error(MLA_ERR_INVALID_ARG, "%s: kv_scale is not finite", who);
+    if (num_blocks > (int64_t)1 << 40) return set_error(MLA_ERR_UNSUPPORTED, "%s: num_blocks too large", who);
+    if (!(kv_scale >= 0.f) || std::isinf(kv_scale))
+        return set_error(MLA_ERR_INVALID_ARG, "%s: kv_scale must be finite and >= 0 (0 = per-token)", who);
     mla::RopeArgs a{};
     const mla_status st = rope_args(who, q_pe, q_pe_stride_t, q_pe_stride_h, positions, inv_freq, mscale, adjacent, q_out,
                                     q_out_stride_t, q_out_stride_h, T, q_pe ? H : 1, &a);
