@@ -530,7 +530,7 @@ mla_status mla_decode_tree(const void* q, const void* kv_cache, mla_kv_dtype kv_
  * ends the branch before it. Requests must not share the pages that hold drafts.
  *   kv_cache   [layers, num_blocks, 64, mla_kv_row_bytes(kv_dtype)] bytes, one block table for all layers
  *   path       int32 [B, Sq], counts int32 [B], in device memory
- *   new_lens   int32 [B], another buffer than seq_lens
+ *   new_lens   int32 [B], a buffer that overlaps no input
  * A row in a block outside the cache sets MLA_DEV_BAD_BLOCK_ID and is not moved. 1 <= Sq <= 64, layers >= 1.
  */
 mla_status mla_accept_tokens(void* kv_cache, mla_kv_dtype kv_dtype, int layers, int64_t num_blocks,
@@ -558,7 +558,7 @@ mla_status mla_accept_tokens(void* kv_cache, mla_kv_dtype kv_dtype, int layers, 
  * passed on and not counted.
  *   kv_cache   [layers, num_blocks, 64, mla_kv_row_bytes(kv_dtype)] bytes; layers 0: the tables alone
  *   parents, room  int32 [B2];  new_table int32 [B2, max_blocks], new_counts, new_lens int32 [B2], new_refs int32
- *              [num_blocks]: other buffers than the old state's
+ *              [num_blocks]: buffers that overlap none of the old state's
  *   workspace  >= mla_fork_pages_workspace_bytes(B, B2, num_blocks) bytes, 256-byte aligned, contents undefined
  * All but the host numbers in device memory. B, B2 <= 8192.
  */

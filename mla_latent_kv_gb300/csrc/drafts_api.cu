@@ -15,6 +15,11 @@ using mla::set_error;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+// Whether the buffers of m and n int32 have an element in common.
+bool overlap(const int32_t* a, int64_t m, const int32_t* b, int64_t n) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + 4 * (uintptr_t)n && y < x + 4 * (uintptr_t)m;
+}
 bool known_kv(mla_kv_dtype d) { return d == MLA_KV_BF16 || d == MLA_KV_FP8_E4M3_SCALED; }
 
 mla_status cuda_error(cudaError_t e, const char* who) {
@@ -329,7 +334,10 @@ mla_status mla_accept_tokens(void* kv_cache, mla_kv_dtype kv_dtype, int layers, 
     if (layers < 1) return set_error(MLA_ERR_INVALID_ARG, "%s: layers=%d", who, layers);
     if (!seq_lens || !path || !counts || !new_lens || (max_blocks > 0 && !block_table))
         return set_error(MLA_ERR_INVALID_ARG, "%s: null pointer", who);
-    if (new_lens == seq_lens) return set_error(MLA_ERR_INVALID_ARG, "%s: new_lens must not be seq_lens", who);
+    // (every layer's blocks read the inputs)
+    if (overlap(new_lens, B, seq_lens, B) || overlap(new_lens, B, counts, B) || overlap(new_lens, B, path, (int64_t)B * Sq) ||
+        overlap(new_lens, B, block_table, (int64_t)B * max_blocks))
+        return set_error(MLA_ERR_INVALID_ARG, "%s: new_lens must not be seq_lens, nor overlap another input", who);
     mla::AcceptArgs a{};
     a.cache = (uint8_t*)kv_cache;
     a.layers = layers;
@@ -369,9 +377,16 @@ mla_status mla_fork_pages(void* kv_cache, mla_kv_dtype kv_dtype, int layers, int
         (B2 > 0 && (!parents || !room || !new_counts || !new_lens)) || (B > 0 && max_blocks > 0 && !block_table) ||
         (B2 > 0 && max_blocks > 0 && !new_table))
         return set_error(MLA_ERR_INVALID_ARG, "%s: null pointer", who);
-    if ((refs && refs == new_refs) || (block_table && block_table == new_table) || (page_counts && page_counts == new_counts) ||
-        (seq_lens && seq_lens == new_lens))
-        return set_error(MLA_ERR_INVALID_ARG, "%s: the new state must not be the old one's buffers", who);
+    struct Buffer {
+        const int32_t* at;
+        int64_t n;
+    };
+    const Buffer before[4] = {{block_table, (int64_t)B * max_blocks}, {page_counts, B}, {seq_lens, B}, {refs, num_blocks}};
+    const Buffer after[4] = {{new_table, (int64_t)B2 * max_blocks}, {new_counts, B2}, {new_lens, B2}, {new_refs, num_blocks}};
+    for (const Buffer& x : before)
+        for (const Buffer& y : after)
+            if (overlap(x.at, x.n, y.at, y.n))
+                return set_error(MLA_ERR_INVALID_ARG, "%s: the new state must not be the old one's buffers, nor overlap them", who);
     if ((int64_t)B2 * (1 + (int64_t)layers) + B > (int64_t)INT32_MAX)
         return set_error(MLA_ERR_UNSUPPORTED, "%s: %d rows of %d layers too many", who, B2, layers);
     const ForkLayout w = fork_layout(B, B2, num_blocks);
