@@ -659,7 +659,7 @@ _torch_binding = None
 
 def _native():
     """The compiled torch side of these calls: it checks the tensors, makes what is not given and launches
-    (raises if it has not been built)."""
+    (raises if it has not been built, or for another torch)."""
     global _torch_binding
     if _torch_binding is None:
         lib()
@@ -669,6 +669,10 @@ def _native():
         import torch  # noqa: F401 (its libraries are loaded before the binding)
         if not os.path.exists(BINDING_PATH):
             raise RuntimeError(f"torch binding missing: {BINDING_PATH} (build it with `python -m mla_latent_kv_gb300.build`)")
+        from . import build
+        if build.binding_built_for() != build.built_for():
+            raise RuntimeError(f"torch binding {BINDING_PATH} was built for {build.binding_built_for()}, this is "
+                               f"{build.built_for()} (build it again with `python -m mla_latent_kv_gb300.build`)")
         loader = importlib.machinery.ExtensionFileLoader("_mla_torch", BINDING_PATH)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_mla_torch", loader))
         loader.exec_module(module)

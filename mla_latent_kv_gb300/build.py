@@ -37,6 +37,21 @@ def _nvcc() -> str:
     return p if os.path.exists(p) else "nvcc"
 
 
+def built_for() -> str:
+    """What a torch binding built here is for: its object follows the layouts of this torch's headers and of this Python."""
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
+def binding_built_for() -> str | None:
+    """What the torch binding that is there was built for, None if there is none (or nothing says so)."""
+    try:
+        with open(BINDING + ".built_for") as f:
+            return f.read() if os.path.exists(BINDING) else None
+    except OSError:
+        return None
+
+
 def _cuda_home() -> str:
     return os.environ.get("CUDA_HOME", "/usr/local/cuda")
 
@@ -69,6 +84,8 @@ def _deps():
 def up_to_date() -> bool:
     if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
+    if binding_built_for() != built_for():  # of another torch or Python, or brought from elsewhere
+        return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
@@ -99,12 +116,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
     tmp = LIB + f".{os.getpid()}.tmp"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *[o for _, o, _ in results[1:]],
            "-lpthread", "-ldl", "-lrt"]
+    if os.path.exists(BINDING + ".built_for"):
+        os.remove(BINDING + ".built_for")
     for cmd, out in ((cmd, LIB), (_binding_link(binding_obj, BINDING + f".{os.getpid()}.tmp"), BINDING)):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(out + f".{os.getpid()}.tmp", out)
+    with open(BINDING + ".built_for", "w") as f:
+        f.write(built_for())
     return LIB
 
 
