@@ -5,7 +5,8 @@
 Each .cu under csrc/ is compiled in parallel to an object file, then linked into
 mla_latent_kv_gb300/_build/libmla_latent_kv.so (the CUDA runtime is linked statically, so the
 library loads on a machine without a GPU; CUDA calls then fail with MLA_ERR_CUDA). binding.cpp, which reads
-torch tensors, is compiled beside them by the host compiler into _build/_mla_torch.so and linked to the library.
+torch tensors, is compiled beside them by the host compiler into _build/_mla_torch.so and linked to the library;
+without torch, which the library does not need, it is left out.
 """
 from __future__ import annotations
 
@@ -37,6 +38,14 @@ def _nvcc() -> str:
     return p if os.path.exists(p) else "nvcc"
 
 
+def has_torch() -> bool:
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return False
+    return True
+
+
 def built_for() -> str:
     """What a torch binding built here is for: its object follows the layouts of this torch's headers and of this Python."""
     import torch
@@ -65,10 +74,10 @@ def _binding_cmd(obj):
             "-isystem", os.path.join(_cuda_home(), "include"), "-c", BINDING_SRC, "-o", obj]
 
 
-def _binding_link(obj, out):
+def _binding_link(obj):
     import torch
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
-    return [os.environ.get("CXX", "g++"), "-shared", "-o", out, obj, "-L", BUILD, "-l:" + os.path.basename(LIB),
+    return [os.environ.get("CXX", "g++"), "-shared", obj, "-L", BUILD, "-l:" + os.path.basename(LIB),
             "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs]
 
 
@@ -77,17 +86,21 @@ def sources():
 
 
 def _deps():
-    return (sources() + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+    return (sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
+def _newer(out, deps) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(d) <= os.path.getmtime(out) for d in deps)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    if not _newer(LIB, _deps()):
         return False
-    if binding_built_for() != built_for():  # of another torch or Python, or brought from elsewhere
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    if not has_torch():
+        return True
+    # a binding of another torch or Python, or brought from elsewhere, is built again
+    return _newer(BINDING, _deps() + [BINDING_SRC]) and binding_built_for() == built_for()
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -96,6 +109,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     extra = ["-Xptxas", "-v"] if verbose else []
+    with_torch = has_torch()
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
@@ -103,29 +117,35 @@ def build(force: bool = False, verbose: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, r
 
-    with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        results = list(ex.map(compile_one, [BINDING_SRC] + sources()))
-    failed = False
-    for src, _, r in results:
-        if r.returncode != 0 or (verbose and r.stderr):
-            sys.stderr.write(f"--- {os.path.basename(src)}\n{r.stdout}{r.stderr}")
-        failed |= r.returncode != 0
-    if failed:
-        raise RuntimeError("a compiler failed; see messages above")
-    binding_obj = results[0][1]
-    tmp = LIB + f".{os.getpid()}.tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *[o for _, o, _ in results[1:]],
-           "-lpthread", "-ldl", "-lrt"]
-    if os.path.exists(BINDING + ".built_for"):
-        os.remove(BINDING + ".built_for")
-    for cmd, out in ((cmd, LIB), (_binding_link(binding_obj, BINDING + f".{os.getpid()}.tmp"), BINDING)):
-        r = subprocess.run(cmd, capture_output=True, text=True)
+    def report(results):
+        """Prints what the compilers said; raises if one failed."""
+        for src, _, r in results:
+            if r.returncode != 0 or (verbose and r.stderr):
+                sys.stderr.write(f"--- {os.path.basename(src)}\n{r.stdout}{r.stderr}")
+        if any(r.returncode != 0 for _, _, r in results):
+            raise RuntimeError("a compiler failed; see messages above")
+
+    def link(cmd, out):
+        tmp = out + f".{os.getpid()}.tmp"
+        r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
         if r.returncode != 0:
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link failed")
-        os.replace(out + f".{os.getpid()}.tmp", out)
-    with open(BINDING + ".built_for", "w") as f:
-        f.write(built_for())
+        os.replace(tmp, out)
+
+    with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        results = list(ex.map(compile_one, ([BINDING_SRC] if with_torch else []) + sources()))
+    of_library = [x for x in results if x[0] != BINDING_SRC]
+    report(of_library)
+    link([nvcc, *ARCH, "-shared", "-cudart", "static", *[obj for _, obj, _ in of_library], "-lpthread", "-ldl", "-lrt"], LIB)
+    # the binding last: where it cannot be built, the library is there
+    if with_torch:
+        report(results[:1])
+        if os.path.exists(BINDING + ".built_for"):
+            os.remove(BINDING + ".built_for")
+        link(_binding_link(results[0][1]), BINDING)
+        with open(BINDING + ".built_for", "w") as f:
+            f.write(built_for())
     return LIB
 
 
