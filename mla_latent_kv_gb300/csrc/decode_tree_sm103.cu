@@ -932,7 +932,7 @@ __global__ void __launch_bounds__(kWidenThreads) tree_widen_kernel(TreeArgs p, c
                                                                    float* k_scales, float* v_scales) {
     griddep_wait();
     griddep_launch_dependents();
-    const int page = (int)blockIdx.x, req = (int)blockIdx.y, tid = threadIdx.x;
+    const int req = (int)(blockIdx.x / (unsigned)p.wide_pages), page = (int)(blockIdx.x % (unsigned)p.wide_pages), tid = threadIdx.x;
     if (page >= (min(max(p.seq_lens[req], 0), p.max_seq_len) + kPage - 1) / kPage) return;
     const int32_t blk = p.block_table[(size_t)req * p.max_blocks + page];
     const bool bad = blk < 0 || (int64_t)blk >= p.num_blocks;
@@ -1145,7 +1145,7 @@ cudaError_t launch_decode_tree(const TreeArgs& in, bool fp8, const uint8_t* cach
         a.k_scales = scales;
         a.v_scales = scales + rows;
         if (rows > 0) {
-            e = launch_pdl(tree_widen_kernel, dim3((unsigned)a.wide_pages, (unsigned)a.B), dim3(kWidenThreads), 0, s, a, cache,
+            e = launch_pdl(tree_widen_kernel, dim3((unsigned)(rows / kPage)), dim3(kWidenThreads), 0, s, a, cache,
                            widened, scales, scales + rows);
             if (e != cudaSuccess) return e;
         }

@@ -268,7 +268,7 @@ mla_status mla_decode_tree(const void* q, const void* kv_cache, mla_kv_dtype kv_
     TreePlan w{};
     if (!plan_tree(kv_dtype, B, Sq, H, max_seq_len, &w))
         return set_error(MLA_ERR_CUDA, "%s: could not plan the call (no CUDA device?)", who);
-    if (!w.rows && ((int64_t)B * w.tiles > INT32_MAX / 4 || (int64_t)B * w.wide_pages > INT32_MAX / mla::kPage || B > 65535))
+    if (!w.rows && ((int64_t)B * w.tiles > INT32_MAX / 4 || (int64_t)B * w.wide_pages > INT32_MAX / mla::kPage))
         return set_error(MLA_ERR_UNSUPPORTED, "%s: %d requests of %d tokens too many", who, B, max_seq_len);
     if (w.total > 0 && (!workspace || workspace_bytes < w.total))
         return set_error(MLA_ERR_WORKSPACE_TOO_SMALL, "%s: workspace %zu bytes < %zu needed", who,

@@ -6,7 +6,8 @@ import numpy as np
 import pytest
 
 import mla_inputs as mi
-from longctx_util import PAGE, dev
+from drafts_util import attend_tree, tree_masks
+from longctx_util import PAGE, check_attention, dev, paged_case
 
 pytestmark = pytest.mark.gpu
 BF, F8 = mi.KV_BF16, mi.KV_FP8
@@ -110,3 +111,25 @@ def test_decode_tree_with_a_bound_of_zero_needs_no_cache(B, Sq, H, kv):
             assert rc == mla.OK, lib.mla_last_error_detail()
             assert bool((o == 0).all()) and bool((lse == -math.inf).all())
             assert st.item() == (mla.DEV_SEQ_TOO_LONG if length else 0)
+
+
+@pytest.mark.parametrize("Sq,H,kv", [(1, 33, BF), (3, 43, BF), (3, 43, F8), (2, 2, F8), (1, 40, F8)])
+def test_decode_tree_of_more_requests_than_a_grid_is_high(Sq, H, kv):
+    """70,000 requests of a page each, as mla_decode takes them; some of them checked in 64 bits."""
+    import torch
+
+    import mla_latent_kv_gb300 as mla
+    B = 70000
+    c = paged_case([PAGE] * 40, 1, 1, kv, 40)
+    rng = np.random.default_rng(41)
+    pages, lens = c["full_table"][rng.integers(0, 40, B), :1], rng.integers(0, PAGE + 1, B)
+    masks = np.tile(tree_masks(50, Sq, 42), (B // 50, 1))
+    q = torch.empty((B, Sq, H, 576), dtype=torch.bfloat16, device="cuda")
+    q.normal_(generator=torch.Generator(device="cuda").manual_seed(43))
+    st = _status()
+    o, lse = mla.decode_tree(q, c["cache"], dev(pages), dev(lens.astype(np.int32)), dev(masks), PAGE, c["scale"], kv_dtype=kv,
+                             o_dtype=mla.DT_BF16, dev_status=st, num_blocks=c["num_blocks"])
+    assert st.item() == 0 and not bool(o.isnan().any())
+    some = [0, 1, 32767, 65534, 65535, 65536, 65537, B - 2, B - 1]
+    part = dict(c, B=len(some), Sq=Sq, H=H, lens=lens[some], full_table=pages[some], q=q[some], masks_host=masks[some])
+    check_attention(o[some], lse[some], attend_tree(part), bf16_out=True)
