@@ -18,13 +18,6 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kTok = 4;  // tokens per warp: all their loads are in flight before any is used
 
-// Two binary32 values -> two OCP E4M3 bytes (lo at the lower address), nearest even, saturating.
-__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 __global__ void __launch_bounds__(kWarps * 32)
     cache_write_kernel(const uint16_t* __restrict__ kv_c, int64_t st_c, const uint16_t* __restrict__ k_pe,
                        int64_t st_pe, const int64_t* __restrict__ slots, int T, uint8_t* __restrict__ cache,
@@ -86,7 +79,7 @@ __global__ void __launch_bounds__(kWarps * 32)
             uint32_t b[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                b[j] = f32x2_to_e4m3x2(__fmul_rn(ptx::bf16_lo_f(w[j]), inv), __fmul_rn(ptx::bf16_hi_f(w[j]), inv));
+                b[j] = ptx::f32x2_to_e4m3x2(__fmul_rn(ptx::bf16_lo_f(w[j]), inv), __fmul_rn(ptx::bf16_hi_f(w[j]), inv));
             reinterpret_cast<uint2*>(dst)[k] = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
         }
         if (lane == 0) *reinterpret_cast<float2*>(dst + kD) = make_float2(scale, scale);

@@ -127,13 +127,6 @@ __host__ __device__ __forceinline__ int64_t head_warps(const RopeArgs& p) {
     return kRows == 0 ? ((int64_t)p.T * p.N + 7) / 8 : (int64_t)p.T * ((p.N + 8 * kRows - 1) / (kRows == 0 ? 1 : 8 * kRows));
 }
 
-// Two binary32 values -> two OCP E4M3 bytes (lo at the lower address), nearest even, saturating.
-__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // The cache rows of tokens [kTokens w, ...), by one warp. Each row is 72 chunks of 8 values: 64 of kv_c, two a
 // lane, and 8 of the turned k_pe, which lane 8 u + c holds for token u. A value is rounded once, to bf16 or, from
 // the fp32 of the rotation, to e4m3.
@@ -214,7 +207,7 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& p, const RopeRows& r, 
             auto store = [&](int c, const float* y) {
                 uint32_t b[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) b[j] = f32x2_to_e4m3x2(__fmul_rn(y[2 * j], inv), __fmul_rn(y[2 * j + 1], inv));
+                for (int j = 0; j < 4; ++j) b[j] = ptx::f32x2_to_e4m3x2(__fmul_rn(y[2 * j], inv), __fmul_rn(y[2 * j + 1], inv));
                 reinterpret_cast<uint2*>(dst)[c] = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
             };
             store(lane, z);

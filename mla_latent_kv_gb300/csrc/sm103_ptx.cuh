@@ -516,6 +516,13 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 __device__ __forceinline__ float bf16_lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// Two binary32 values -> two OCP E4M3 bytes (lo at the lower address), nearest even, saturating.
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // Two OCP E4M3 values (low byte first) -> two bf16 (low half first), exactly: every e4m3 value
 // is an f16 value and every f16 value of that range is a bf16 value.
 __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two_bytes) {
