@@ -153,7 +153,10 @@ constexpr int OFF_PROG = 520;     // CTA 2: pages of all units that its helper w
 constexpr int OFF_MX = 1024;      // scores: f32 [4][128] exchange between the column quarters
 constexpr int OFF_STAT_M = 2048;  // output: f32 [128] final running max (log2 units)
 constexpr int OFF_STAT_L = 2560;  // output: f32 [128] row sum
-constexpr int kMaxSorted = 240;   // requests whose lengths are kept and, for more units than clusters, sorted
+// Requests whose lengths are kept and, for more units than clusters, sorted: what the control block has room for. More are
+// taken in the caller's order and their lengths read from global memory: 7 to 8% slower (2 x 64 pairs over up to 2000 tokens,
+// us per million tokens: 240 requests 414, 241 446).
+constexpr int kMaxSorted = 240;
 constexpr int OFF_ORDER = 544;    // u16 [kMaxSorted] requests, longest first; or the cuts:
 constexpr int OFF_CUTS = OFF_ORDER;          // Place [2] where the cluster's part begins and ends
 constexpr int OFF_BEFORE = OFF_CUTS + 32;    // u32 [kTreeMaxCut] weights of the requests before
@@ -262,7 +265,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         return min(max(n, 0), p.max_seq_len);
     };
 
-    // Lengths, and the requests in their order (ties by number), every thread placing one.
+    // Lengths, and the requests in their order (ties by number), every thread placing one. The lengths are read ahead of the
+    // wait for the kernels in front, by the rule of the decode kernels: no kernel that writes lengths lets the next one start
+    // early (internal.h, launch_pdl). The roles of the cluster's CTAs, each of which reads them for itself, agree by that alone.
     const int clusters = (int)(gridDim.x >> 2), cluster = (int)(blockIdx.x >> 2);
     const bool kept = p.B <= kMaxSorted, sorted = kept && !kCut && p.units > (int64_t)clusters;
     int* lens = reinterpret_cast<int*>(smem + OFF_LENS);
@@ -312,7 +317,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     }
     cluster_sync();  // every CTA's barriers (and the order) exist before any remote arrive or copy
     const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM), 0);
-    griddep_wait();  // q, the masks, the cache and the lengths may be earlier kernels' outputs
+    // q, the masks, the cache, the table and, where they were not kept above, the lengths may be earlier kernels' outputs
+    griddep_wait();
     if (tid == 0) griddep_launch_dependents();
 
     // The cluster's unit number k (u: the one before). Whole units: in the order (request by length, tile), so that a
@@ -967,9 +973,9 @@ __global__ void __launch_bounds__(kWidenThreads) tree_widen_kernel(TreeArgs p, c
 
 // ------------------------------------------------------------------------------------------
 // The states of a cut unit's parts -> its rows:  o = sum_i w_i o_i / sum_i w_i,  lse = M + log sum_i w_i,  w_i =
-// exp(lse_i - M), M the largest lse. Half a row a warp, four rows a block and turn. Up to
-// 28 MB are read once, 6 to 9 us with the launch. No more blocks than run at once: with one for every cluster and four
-// rows (2304) 3 x 256 rows over up to 3000 tokens took 24.8 us a call, 23.5 so.
+// exp(lse_i - M), M the largest lse. Half a row a warp, four rows a block and turn. Up to two parts of 512 KB a cluster,
+// 37 MB, are read once, 6 to 9 us with the launch. Four blocks an SM, of which three run at once (76 registers): with one for
+// every cluster and four rows (2304) 3 x 256 rows over up to 3000 tokens took 24.8 us a call, 23.5 so.
 // ------------------------------------------------------------------------------------------
 constexpr int kMergeThreads = 256, kMergeRows = kMergeThreads / 64, kMergeBatch = 3, kMergeBlocks = 608;
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArgs p) {
@@ -1115,9 +1121,10 @@ int tree_shares(int B, int tiles, int slab_rows, int pages, int clusters, int* l
         const double shares = std::min(std::floor((double)clusters / n),
                                        std::max(requests, std::ceil((requests * (longest + kUnitGroups) - kUnitGroups) / part)));
         if (shares < 2) continue;
-        // beside a share of the groups: a start of its own, the merge's launch, and the partial rows written and read;
+        // beside a share of the groups: a start of its own, the merge's launch, and the partial rows written and read (12
+        // groups for 36 x 256 rows);
         // tiles that do not go through a share side by side find less of it in L2 (1 lane for 4 tiles: 10%)
-        const double merge = 2.0 + 12.0 / 36 / kTileRows * shares * n * slab_rows;
+        const double merge = 2.0 + 12.0 / (36 * kTileRows) * shares * n * slab_rows;
         const double cut = requests * (usual + kUnitGroups) / shares * (1.0 + 0.05 * std::log2((double)tiles / n)) + kUnitGroups + merge;
         if (cut < best) {
             best = cut;

@@ -81,7 +81,8 @@ mla_status rope_args(const char* who, const void* x, int64_t x_t, int64_t x_n, c
 // ------------------------------------------------------------------------------------ tree
 // How a tree call runs, and its workspace. At most 32 (draft, head) pairs, or 128 over an FP8 cache, are one row
 // of so many heads for the decode kernels (splits: theirs). More go through a kernel of their own, 256 at a time;
-// its workspace is the widened rows (FP8), then, if units are cut, their parts' states. Both sides of the border: 64 requests of up to
+// its workspace is the widened rows (FP8), then, if units are cut, their parts' states. The widened rows have room for the
+// bound on the lengths, not for the lengths, which the host does not know. Both sides of the border: 64 requests of up to
 // 8192 tokens, bf16, 32 pairs 131 us as a row and 147 by the tree kernel; 112 pairs 157 and 146, FP8 233 and 303;
 // 128 requests of up to 1000 tokens, 128 pairs, bf16 80 and 66, FP8 74 and 107.
 struct TreePlan {
@@ -98,9 +99,11 @@ bool plan_tree(mla_kv_dtype kv, int B, int Sq, int H, int max_seq_len, TreePlan*
         // Over an FP8 cache with more than 32 pairs: short requests one unit each where there are more of them than SM
         // pairs (128 of up to 1000 tokens 74 us, by the schedule built on the device 85); much work by the schedule
         // (64 of up to 8192 tokens 223 us, ranges of a fixed length 233; 30 of up to 6000 91 and 102; 40 of up to 20,000 288
-        // and 327), little by ranges, which need no plan (5 of up to 12,000 42 us, by the schedule 60).
+        // and 327), little by ranges, which need no plan (5 of up to 12,000 42 us, by the schedule 60). The borders lie
+        // where the two cost the same (112 pairs, us per 1000 pages: 3 and 4 requests of up to 60,000 tokens 45.6 and 46.1;
+        // 29 requests of up to 89 and 90 pages 48.7 and 45.2, 60 of them 40.4 both).
         const bool much = pages >= 90 && B >= 4 && (int64_t)B * pages > 2500;
-        const int splits = few ? -1 : pages <= 32 && B > 76 ? 1 : much ? -2 : -1;
+        const int splits = few ? -1 : pages <= 32 && B > mla::device_sm_count() / 2 ? 1 : much ? -2 : -1;
         w->splits = mla::resolve_splits(few, splits, B, (int)flat, max_seq_len);
         if (w->splits < 1 && w->splits != -2) return false;
         w->total = mla::workspace_layout(kv, B, B, (int)flat, w->splits, max_seq_len).total;

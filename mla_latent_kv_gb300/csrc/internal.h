@@ -160,7 +160,8 @@ __host__ __device__ inline void split_range(int n, int S, int s, int* j0, int* j
 // Launch with programmatic stream serialization: the kernel may start while the preceding
 // kernel of the stream finishes, once that kernel has signalled (griddepcontrol); every kernel
 // of this library calls ptx::griddep_wait() before it touches data another of its kernels writes. (The
-// decode kernels read cache pages before that: cache_write, which writes them, does not signal early.)
+// decode kernels read lengths, tables or cache pages before that: the kernels that write those (cache_write, rope, accept,
+// fork) do not signal early.)
 template <typename... Params, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                        Args... args) {
@@ -360,7 +361,7 @@ struct ForkArgs {
 };
 cudaError_t launch_fork_pages(const ForkArgs& a, bool fp8, cudaStream_t s);
 
-// ---- decode of drafted trees, more than 128 (draft, head) pairs a request ------------------------
+// ---- decode of drafted trees, more than 32 (draft, head) pairs a request, over an FP8 cache 128 ----
 constexpr int kTreeMaxDrafts = 64;  // bits of a mask
 constexpr int kTreeMaxCut = 112;    // requests whose units are cut
 constexpr int kTreeMaxClusters = 64;
