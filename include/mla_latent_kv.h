@@ -510,7 +510,9 @@ mla_status mla_rope_cache_write(const void* kv_c, int64_t kv_c_stride_t, const v
  * values. The drafts' rows have been written (they may
  * repeat positions: those are in the keys, by mla_rope).
  *   tree_mask  uint64 [B, Sq] in device memory; bits from Sq on are not read
- *   workspace  >= mla_decode_tree_workspace_bytes for the same arguments, 256-byte aligned, contents undefined
+ *   workspace  >= mla_decode_tree_workspace_bytes for the same arguments, 256-byte aligned, contents undefined. Over an
+ *              FP8 cache, with more than 128 pairs (Sq * H): the requests' rows as bf16 among it, 1160 bytes for
+ *              each of B * max_seq_len tokens, of the bound and not of the lengths (64 requests with a bound of 131,072: 9.8 GB)
  * 1 <= Sq <= 64. All other arguments, results, limits and errors as mla_decode; how a request's tokens are
  * divided over the device is the library's choice (from B, Sq, H, max_seq_len and the lengths).
  */

@@ -27,9 +27,9 @@
 // number of pages, which the host chose before: 20 requests x 256 rows over 8000 to 16,000 tokens 134 -> 101 us, 8 x 1024
 // over up to 32,768 325 -> 272, 5 x 320 over up to 100,000 307 -> 236, 1 x 1024 over 131,072 the same.
 //
-// Measured: 16 requests x 32 drafts x 128 heads over up to 8192 tokens 550 us, 1.59 PFLOP/s (FP8 553 with the
-// widening, 1.73), 32 x 8 over up to 4096 146 us, 1.47; 64 x 7 drafts of 16 heads over up
-// to 8192 tokens 140 us: less than half of the rows are in use there. A group takes 1.28 us, its 2304 cycles
+// Measured: 16 requests x 32 drafts x 128 heads over up to 8192 tokens 550 us, 1.59 PFLOP/s (FP8 551 with the
+// widening, 1.73), 29 x 8 over up to 4096 147 us, 1.38; 64 x 7 drafts of 16 heads over up
+// to 8192 tokens 137 to 145 us: less than half of the rows are in use there. A group takes 1.28 us, its 2304 cycles
 // of scores MMAs at the clock that the power leaves; a unit's change 6 us, the first scores 9 after the start.
 // What it took, on the 32 x 8 drafts: one launch a unit 174 us; clusters that stay, longest first 154; first keys
 // beside Q, lengths in shared memory 152; an arrival without a release, no 64-bit divisions 148; a later unit's Q loaded
