@@ -378,13 +378,20 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 tma_prefetch_desc(&k_map);
                 tma_prefetch_desc(&q_map);
                 bool ok = true;
-                // the K ring's slots and the staging buffers (of the last group too) as the groups before g0 left them
+                // The K ring's slots and the staging buffers (of the last group too) as the groups before g0 left them. A wait
+                // by parity needs the phase before the awaited one to be over. With the last MMAs done, the softmax warps have
+                // read the scores of group g0 - 3, so that g0 - 4 is staged but may not be sent (the output CTAs can be
+                // an epilogue behind): group g0 - 2 is awaited as staged first, which group g0 - 4's copies precede.
                 auto drained = [&](bool all) -> bool {
                     for (uint32_t m = 3 * g0 > kSlots ? 3 * g0 - kSlots : 0; m < 3 * g0; ++m)
                         if (!wait_bar<true>(bar(B_SLOTEMPTY + (int)(m % kSlots)), (m / kSlots) & 1, abort, ds)) return false;
                     for (uint32_t g = g0 > 2 ? g0 - 2 : 0; g + !all < g0; ++g)
-                        for (int q = 0; q < kPPG; ++q)
-                            if (!wait_bar<true>(bar(B_STAGEFREE + 2 * (int)(g & 1) + q), (g >> 1) & 1, abort, ds)) return false;
+                        for (int q = 0; q < kPPG; ++q) {
+                            const int sbi = 2 * (int)(g & 1) + q;
+                            if (!wait_bar(bar(B_STAGEFULL + sbi), (g >> 1) & 1, abort, ds) ||
+                                !wait_bar<true>(bar(B_STAGEFREE + sbi), (g >> 1) & 1, abort, ds))
+                                return false;
+                        }
                     return true;
                 };
                 for (int k = 0; ok && unit_of(k, u); ++k) {

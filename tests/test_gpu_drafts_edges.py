@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 import mla_inputs as mi
-from drafts_util import attend_tree, tree_masks
+from drafts_util import attend_tree, tree_case, tree_masks
 from longctx_util import PAGE, check_attention, dev, paged_case
 
 pytestmark = pytest.mark.gpu
@@ -133,3 +133,34 @@ def test_decode_tree_of_more_requests_than_a_grid_is_high(Sq, H, kv):
     some = [0, 1, 32767, 65534, 65535, 65536, 65537, B - 2, B - 1]
     part = dict(c, B=len(some), Sq=Sq, H=H, lens=lens[some], full_table=pages[some], q=q[some], masks_host=masks[some])
     check_attention(o[some], lse[some], attend_tree(part), bf16_out=True)
+
+
+@pytest.mark.parametrize("kv", [BF, F8])
+@pytest.mark.parametrize("Sq,H,pages", [
+    (27, 64, [10] * 9 + [9, 5, 4, 2, 0]),                        # seven tiles a request, 98 units for 36 clusters
+    (28, 64, [13] * 9 + [12, 8, 3, 3, 1, 0, 0, 0]),
+    (64, 128, [9, 9, 8, 0]),                                     # 32 tiles of four requests
+    (16, 71, [11] * 7 + [10] * 6 + [8, 7, 7, 4, 4, 3, 2, 2, 1]),
+    (12, 128, [20] * 8 + [19] * 8 + [18, 17, 16, 10, 8, 8, 5, 3, 2, 2, 1, 0]),
+    (48, 128, [9, 9, 9, 9, 9, 8, 7, 7, 2, 0, 0]),                # 24 tiles: six units a cluster
+    (24, 64, [31] * 3 + [30] * 6 + [29, 26, 26, 18, 14, 12, 9, 5, 2, 1, 0, 0]),
+    (3, 60, [2] * 40 + [1] * 80 + [4] * 60),                     # five short units a cluster
+])
+def test_decode_tree_of_short_units_in_a_row(Sq, H, pages, kv):
+    """Three and more short units a cluster: while the output CTAs finish one, the next one's weights wait to be sent and
+    the third one's queries are loaded beside them. The same call over and over gives the same bits, and the right ones."""
+    import torch
+
+    import mla_latent_kv_gb300 as mla
+    rng = np.random.default_rng(sum(pages))
+    lens = [max(0, 64 * n - int(rng.integers(0, 64))) for n in pages]
+    c = tree_case(lens, Sq, H, kv, 50 + len(pages), scale_v=1.7 if kv == F8 else None)
+    st = _status()
+    call = lambda: mla.decode_tree(c["q"], c["cache"], c["table"], c["seq_lens"], c["masks"], c["max_len"],  # noqa: E731
+                                   c["scale"], kv_dtype=kv, num_blocks=c["num_blocks"], dev_status=st)
+    o, lse = call()
+    check_attention(o, lse, attend_tree(c))
+    for _ in range(40):
+        again = call()
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    assert st.item() == 0
